@@ -314,6 +314,121 @@ int muonh_adamw_step(muonh_adamw_handle* h, const muonh_adamw_tensor* t, int32_t
 /* Release the handle (waits for its last upload).  NULL is a no-op. */
 int muonh_adamw_destroy(muonh_adamw_handle* h);
 
+/* ---- block-scaled FP8 operands and products ------------------------------
+ * The matrices MuonH steps are trained in block-scaled FP8 on the pages
+ * (arXiv HTML §3.2; App. C): E4M3 values whose scales are powers of two, one
+ * per group of 1 x 128 along the contraction for activations and gradients,
+ * one per block of 128 x 128 for weights.  These entry points quantise and
+ * multiply such operands; a layer's three products are
+ *   forward          Y  = X W^T    rows of X   by rows of W
+ *   data gradient    dX = dY W     rows of dY  by columns of W
+ *   weight gradient  dW = dY^T X   columns of dY by columns of X
+ * where "columns" is the column form below, so every product contracts two
+ * operands along their contiguous axis.  dW (fp32 or bf16) is the gradient
+ * muonh_step takes.  Conventions are those listed at the top of this file;
+ * these entry points keep nothing between calls, allocate nothing, and may be
+ * captured into a HIP graph.                                                */
+typedef struct muonh_fp8_matrix {
+  void*   data;        /* E4M3 (OCP, no infinities) [rows x ld], device, 16-byte aligned   */
+  void*   scale;       /* E8M0 bytes [ceil(rows / block_rows) x ld_scale], device, 4-byte
+                          aligned: value = data * 2^(byte - 127)                           */
+  int64_t rows, cols;  /* cols: the contraction; either may be 0                           */
+  int64_t ld;          /* bytes per row of data, a multiple of 128, >= cols; a product
+                          reads columns cols .. up to the next multiple of 128, which
+                          must be zero (the quantiser writes them)                         */
+  int64_t ld_scale;    /* bytes per row of scale, a multiple of 4, >= ceil(cols / 128);
+                          the quantiser zeroes the bytes up to the next multiple of 4      */
+  int32_t block_rows;  /* 1 or 128                                                         */
+  int32_t reserved;    /* must be 0                                                        */
+} muonh_fp8_matrix;
+
+/* Quantise x [rows x cols] (MUONH_F32 or MUONH_BF16, ldx elements between
+ * rows) into its row form q (rows x cols) and / or its column form qt, that of
+ * x transposed (cols x rows); either may be NULL.  Both take the same
+ * block_rows.  For a block with largest finite magnitude amax the scale is the
+ * least power of two 2^e with amax <= 448 2^e, e >= -127, and 1 for a block of
+ * zeros; elements round to nearest even, NaN and Inf become NaN.
+ * x needs element alignment only.  Errors: MUONH_EINVAL, MUONH_EHIP.        */
+int muonh_block_quantize(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t ldx,
+                         const muonh_fp8_matrix* q, const muonh_fp8_matrix* qt, void* stream);
+
+/* c [a.rows x b.rows] = a b^T, contracted over a.cols == b.cols in fp32 and
+ * rounded once to c_dtype (MUONH_F32 or MUONH_BF16, ldc elements between
+ * rows); accumulate = 1 adds the product to what c holds.  With a.cols = 0 the
+ * product is zero.  Results are the same in every call on the same operands.
+ * A bf16 c is computed by the FP8 matrix unit, whose sums are 2e-5 off (of the
+ * result's norm; bf16 rounds by 1.7e-3); an fp32 c by the bf16 matrix unit on
+ * widened operands, with fp32 sums, at half that rate.  There an operand's
+ * value of 2^128 or more (scale byte 247 and data of 256 or more) is infinite,
+ * and one below 2^-126 may lose bits.
+ * workspace: device memory of muonh_block_matmul_workspace bytes, 256-byte
+ * aligned, or NULL where that is 0; calls that may overlap in time need one
+ * each.  Errors: MUONH_EINVAL, MUONH_ENOMEM (workspace too small), MUONH_EHIP. */
+int muonh_block_matmul_workspace(const muonh_fp8_matrix* a, const muonh_fp8_matrix* b, size_t* bytes);
+int muonh_block_matmul(const muonh_fp8_matrix* a, const muonh_fp8_matrix* b, void* c, int32_t c_dtype,
+                       int64_t ldc, int32_t accumulate, void* workspace, size_t workspace_bytes,
+                       void* stream);
+
+/* ---- layer norm and RMS norm ----------------------------------------------
+ * The norms whose weights muonh_adamw_step trains, over the last axis of
+ * x [rows x cols]:
+ *   layer: mu = mean(x), r = 1/sqrt(mean((x - mu)^2) + eps), h = (x - mu) r
+ *   rms:   r = 1/sqrt(mean(x^2) + eps),                      h = x r
+ *   y = h weight (+ bias);  mean and rstd keep mu and r for the gradient
+ *   dx = r (g - [mean(g)] - h mean(g h)),  g = dy weight     ([]: layer only)
+ *   dweight = sum over rows of dy h,  dbias = sum over rows of dy
+ * Statistics and sums are fp32, sums in a fixed order.  x, y, dy and dx share
+ * one dtype (MUONH_F32 or MUONH_BF16) and need element alignment only; the
+ * vectors are fp32.  y may be x, and dx may be x or dy (same address and
+ * pitch); other overlaps are refused.                                       */
+#define MUONH_NORM_LAYER 0
+#define MUONH_NORM_RMS   1
+
+typedef struct muonh_norm_args {
+  const void*  x;
+  const float* weight;   /* [cols]                                            */
+  const float* bias;     /* [cols] or NULL                                    */
+  void*        y;
+  float*       mean;     /* [rows]; NULL for MUONH_NORM_RMS                   */
+  float*       rstd;     /* [rows]                                            */
+  int64_t      rows;     /* >= 0                                              */
+  int64_t      cols;     /* >= 1                                              */
+  int64_t      ldx, ldy; /* elements between rows                             */
+  int32_t      dtype;
+  int32_t      kind;     /* MUONH_NORM_*                                      */
+  float        eps;      /* >= 0                                              */
+  int32_t      reserved; /* must be 0                                         */
+} muonh_norm_args;
+
+/* Errors: MUONH_EINVAL, MUONH_EHIP. */
+int muonh_norm_forward(const muonh_norm_args* args, void* stream);
+
+typedef struct muonh_norm_grad_args {
+  const void*  dy;
+  const void*  x;
+  const float* weight;    /* [cols]                                           */
+  const float* mean;      /* [rows]; NULL for MUONH_NORM_RMS                  */
+  const float* rstd;      /* [rows]                                           */
+  void*        dx;
+  float*       dweight;   /* [cols]                                           */
+  float*       dbias;     /* [cols] or NULL                                   */
+  int64_t      rows;      /* >= 0; with 0 rows dweight and dbias are zero     */
+  int64_t      cols;      /* >= 1                                             */
+  int64_t      ld_dy, ldx, ld_dx;
+  int32_t      dtype;
+  int32_t      kind;
+  int32_t      accumulate; /* 1: add to dweight and dbias                     */
+  int32_t      reserved;   /* must be 0                                       */
+  void*        workspace;  /* muonh_norm_backward_workspace bytes, device,
+                              256-byte aligned; calls that may overlap in time
+                              need one each                                   */
+  size_t       workspace_bytes;
+} muonh_norm_grad_args;
+
+/* Errors: MUONH_EINVAL, MUONH_ENOMEM (workspace too small), MUONH_EHIP. */
+int muonh_norm_backward_workspace(int64_t rows, int64_t cols, size_t* bytes);
+int muonh_norm_backward(const muonh_norm_grad_args* args, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

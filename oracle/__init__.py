@@ -1,5 +1,5 @@
-"""CPU fp64 oracle for the MuonH optimizer step and the AdamW step of the
-parameters MuonH does not wrap.
+"""CPU fp64 oracle for the MuonH optimizer step, the AdamW step of the
+parameters MuonH does not wrap, the block-scaled FP8 operators and the norms.
 
 TEST INFRASTRUCTURE ONLY.  This package is the plain, slow, obviously-correct
 statement of what the GPU library computes.  Only the tests, the smoke check
@@ -55,3 +55,4 @@ from .adamw import (  # noqa: F401
     first_step_direction,
     constant_gradient_closed_form,
 )
+from . import block_fp8, norm  # noqa: F401

@@ -1,0 +1,326 @@
+// Host side of the block-scaled FP8 operators and of the norms: argument
+// checks, workspace sizes and the launches.  These entry points keep no state:
+// everything a call needs beyond its arguments is in the caller's workspace.
+
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <string>
+
+#include "operators.h"
+
+using namespace muonh;
+
+namespace {
+
+int fail(int code, const std::string& msg) { return set_last_error(code, msg.c_str()); }
+
+int launched(hipError_t e, const char* what) {
+  return e == hipSuccess ? MUONH_OK : fail(MUONH_EHIP, std::string(what) + ": " + hipGetErrorString(e));
+}
+
+constexpr int64_t kMaxRows = (int64_t)1 << 30;    // row and column counts: tile arithmetic is 32 bits
+constexpr int64_t kMaxGrid = (int64_t)1 << 22;    // workgroups of up to 1024 threads in one launch
+constexpr size_t kAlign = 256;
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+int64_t ceil_div(int64_t x, int64_t a) { return (x + a - 1) / a; }
+
+// Bytes from the first element to behind the last of `rows` rows.
+int64_t extent(int64_t rows, int64_t cols, int64_t ld, int64_t size) {
+  return rows < 1 || cols < 1 ? 0 : ((rows - 1) * ld + cols) * size;
+}
+
+bool overlap(const void* p, int64_t pn, const void* q, int64_t qn) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return pn > 0 && qn > 0 && a < b + (uintptr_t)qn && b < a + (uintptr_t)pn;
+}
+
+// Whether an output may share memory with an input of the same size: in place,
+// apart, or in other columns of the same rows.
+bool may_share(const void* out, int64_t ldo, const void* in, int64_t ldi, int64_t rows, int64_t cols,
+               int64_t size) {
+  if (!overlap(out, extent(rows, cols, ldo, size), in, extent(rows, cols, ldi, size))) return true;
+  if (ldo != ldi && rows > 1) return false;
+  if (out == in) return true;
+  if (rows == 1) return false;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(out), b = reinterpret_cast<uintptr_t>(in);
+  const int64_t d = (int64_t)(a > b ? a - b : b - a) % (ldo * size);
+  return d >= cols * size && ldo * size - d >= cols * size;
+}
+
+int check_dtype(int32_t t, const char* what) {
+  if (t != MUONH_F32 && t != MUONH_BF16) return fail(MUONH_EINVAL, std::string(what) + ": dtype must be F32 or BF16");
+  return MUONH_OK;
+}
+
+int check_size(int64_t v, int64_t least, const char* what) {
+  if (v < least || v > kMaxRows)
+    return fail(MUONH_EINVAL, std::string(what) + " must be in [" + std::to_string(least) + ", 2^30]");
+  return MUONH_OK;
+}
+
+int check_pitch(int64_t ld, int64_t cols, const char* what) {
+  if (ld < cols || ld > ((int64_t)1 << 40))
+    return fail(MUONH_EINVAL, std::string(what) + ": the pitch is less than a row, or beyond 2^40");
+  return MUONH_OK;
+}
+
+// One operand.  `whose` names it in the error text.
+int check_matrix(const muonh_fp8_matrix& m, const char* whose) {
+  const std::string who = std::string(whose) + ": ";
+  int rc;
+  if ((rc = check_size(m.rows, 0, (who + "rows").c_str()))) return rc;
+  if ((rc = check_size(m.cols, 0, (who + "cols").c_str()))) return rc;
+  if (m.block_rows != 1 && m.block_rows != 128) return fail(MUONH_EINVAL, who + "block_rows must be 1 or 128");
+  if (m.reserved != 0) return fail(MUONH_EINVAL, who + "reserved != 0");
+  if ((rc = check_pitch(m.ld, m.cols, (who + "ld").c_str()))) return rc;
+  if (m.ld % kFp8Block != 0) return fail(MUONH_EINVAL, who + "ld must be a multiple of 128");
+  if ((rc = check_pitch(m.ld_scale, ceil_div(m.cols, kFp8Block), (who + "ld_scale").c_str()))) return rc;
+  if (m.ld_scale % 4 != 0) return fail(MUONH_EINVAL, who + "ld_scale must be a multiple of 4");
+  if (m.rows > 0 && m.cols > 0) {
+    if (!m.data || !m.scale) return fail(MUONH_EINVAL, who + "null pointer");
+    if (!aligned(m.data, 16) || !aligned(m.scale, 4))
+      return fail(MUONH_EINVAL, who + "data must be 16-byte and scale 4-byte aligned");
+  }
+  return MUONH_OK;
+}
+
+int64_t data_bytes(const muonh_fp8_matrix& m) {
+  return m.rows > 0 && m.cols > 0 ? extent(m.rows, ceil_div(m.cols, kFp8Block) * kFp8Block, m.ld, 1) : 0;
+}
+int64_t scale_bytes(const muonh_fp8_matrix& m) {
+  return m.rows > 0 && m.cols > 0
+             ? extent(ceil_div(m.rows, m.block_rows), ceil_div(m.cols, kFp8Block), m.ld_scale, 1)
+             : 0;
+}
+
+int check_operands(const muonh_fp8_matrix* a, const muonh_fp8_matrix* b) {
+  if (!a || !b) return fail(MUONH_EINVAL, "null operand");
+  int rc;
+  if ((rc = check_matrix(*a, "a"))) return rc;
+  if ((rc = check_matrix(*b, "b"))) return rc;
+  if (a->cols != b->cols) return fail(MUONH_EINVAL, "a.cols differs from b.cols");
+  return MUONH_OK;
+}
+
+int check_vectors(bool ok, const char* what) {
+  return ok ? MUONH_OK : fail(MUONH_EINVAL, std::string("null pointer: ") + what);
+}
+
+}  // namespace
+
+extern "C" {
+
+int muonh_block_quantize(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t ldx,
+                         const muonh_fp8_matrix* q, const muonh_fp8_matrix* qt, void* stream) {
+  return guarded([&]() -> int {
+    int rc;
+    if (!q && !qt) return fail(MUONH_EINVAL, "neither form is asked for");
+    if ((rc = check_dtype(dtype, "x"))) return rc;
+    if ((rc = check_size(rows, 0, "rows")) || (rc = check_size(cols, 0, "cols"))) return rc;
+    if ((rc = check_pitch(ldx, cols, "ldx"))) return rc;
+    if (q) {
+      if ((rc = check_matrix(*q, "q"))) return rc;
+      if (q->rows != rows || q->cols != cols) return fail(MUONH_EINVAL, "q: shape differs from x");
+    }
+    if (qt) {
+      if ((rc = check_matrix(*qt, "qt"))) return rc;
+      if (qt->rows != cols || qt->cols != rows) return fail(MUONH_EINVAL, "qt: shape differs from x transposed");
+    }
+    if (q && qt && q->block_rows != qt->block_rows) return fail(MUONH_EINVAL, "q and qt: block_rows differ");
+    if (rows == 0 || cols == 0) return MUONH_OK;
+    const int64_t size = dtype == MUONH_BF16 ? 2 : 4, nx = extent(rows, cols, ldx, size);
+    if (!x) return fail(MUONH_EINVAL, "null x");
+    if (!aligned(x, (uintptr_t)size)) return fail(MUONH_EINVAL, "misaligned x");
+    for (const muonh_fp8_matrix* m : {q, qt})
+      if (m && (overlap(m->data, data_bytes(*m), x, nx) || overlap(m->scale, scale_bytes(*m), x, nx) ||
+                overlap(m->scale, scale_bytes(*m), m->data, data_bytes(*m))))
+        return fail(MUONH_EINVAL, "outputs overlap x or each other");
+    if (q && qt &&
+        (overlap(q->data, data_bytes(*q), qt->data, data_bytes(*qt)) ||
+         overlap(q->scale, scale_bytes(*q), qt->scale, scale_bytes(*qt)) ||
+         overlap(q->data, data_bytes(*q), qt->scale, scale_bytes(*qt)) ||
+         overlap(q->scale, scale_bytes(*q), qt->data, data_bytes(*qt))))
+      return fail(MUONH_EINVAL, "outputs overlap x or each other");
+    if (ceil_div(rows, kFp8Tile) * ceil_div(cols, kFp8Tile) > kMaxGrid)
+      return fail(MUONH_EINVAL, "x is too large for one launch");
+    QuantArgs a{};
+    a.x = x;
+    a.rows = rows;
+    a.cols = cols;
+    a.ldx = ldx;
+    int32_t block = 1;
+    if (q) {
+      a.q = static_cast<uint8_t*>(q->data);
+      a.s = static_cast<uint8_t*>(q->scale);
+      a.ldq = q->ld;
+      a.lds = q->ld_scale;
+      block = q->block_rows;
+    }
+    if (qt) {
+      a.qt = static_cast<uint8_t*>(qt->data);
+      a.st = static_cast<uint8_t*>(qt->scale);
+      a.ldqt = qt->ld;
+      a.ldst = qt->ld_scale;
+      block = qt->block_rows;
+    }
+    return launched(launch_block_quantize(dtype == MUONH_BF16, block == 128, a,
+                                          reinterpret_cast<hipStream_t>(stream)),
+                    "block_quantize");
+  });
+}
+
+int muonh_block_matmul_workspace(const muonh_fp8_matrix* a, const muonh_fp8_matrix* b, size_t* bytes) {
+  return guarded([&]() -> int {
+    if (!bytes) return fail(MUONH_EINVAL, "null argument");
+    const int rc = check_operands(a, b);
+    if (rc) return rc;
+    *bytes = 0;
+    return MUONH_OK;
+  });
+}
+
+int muonh_block_matmul(const muonh_fp8_matrix* a, const muonh_fp8_matrix* b, void* c, int32_t c_dtype,
+                       int64_t ldc, int32_t accumulate, void* workspace, size_t workspace_bytes,
+                       void* stream) {
+  return guarded([&]() -> int {
+    int rc;
+    if ((rc = check_operands(a, b)) || (rc = check_dtype(c_dtype, "c"))) return rc;
+    if ((rc = check_pitch(ldc, b->rows, "ldc"))) return rc;
+    if (accumulate != 0 && accumulate != 1) return fail(MUONH_EINVAL, "accumulate must be 0 or 1");
+    if (a->rows == 0 || b->rows == 0) return MUONH_OK;
+    const int64_t size = c_dtype == MUONH_BF16 ? 2 : 4, nc = extent(a->rows, b->rows, ldc, size);
+    if (!c) return fail(MUONH_EINVAL, "null c");
+    if (!aligned(c, (uintptr_t)size)) return fail(MUONH_EINVAL, "misaligned c");
+    for (const muonh_fp8_matrix* m : {a, b})
+      if (overlap(m->data, data_bytes(*m), c, nc) || overlap(m->scale, scale_bytes(*m), c, nc))
+        return fail(MUONH_EINVAL, "c overlaps an operand");
+    if (ceil_div(a->rows, 16) * ceil_div(b->rows, 16) > kMaxGrid * 4)
+      return fail(MUONH_EINVAL, "c is too large for one launch");
+    BlockMatmulArgs p{};
+    p.a = static_cast<const uint8_t*>(a->data);
+    p.b = static_cast<const uint8_t*>(b->data);
+    p.sa = static_cast<const uint8_t*>(a->scale);
+    p.sb = static_cast<const uint8_t*>(b->scale);
+    p.lda = a->ld;
+    p.ldb = b->ld;
+    p.ldsa = a->ld_scale;
+    p.ldsb = b->ld_scale;
+    p.c = c;
+    p.ldc = ldc;
+    p.m = (int32_t)a->rows;
+    p.n = (int32_t)b->rows;
+    p.kblocks = (int32_t)ceil_div(a->cols, kFp8Block);
+    p.a_shift = a->block_rows == 128 ? 7 : 0;
+    p.b_shift = b->block_rows == 128 ? 7 : 0;
+    return launched(launch_block_matmul(c_dtype == MUONH_BF16, accumulate, p,
+                                        reinterpret_cast<hipStream_t>(stream)),
+                    "block_matmul");
+  });
+}
+
+int muonh_norm_forward(const muonh_norm_args* g, void* stream) {
+  return guarded([&]() -> int {
+    int rc;
+    if (!g) return fail(MUONH_EINVAL, "null argument");
+    if ((rc = check_dtype(g->dtype, "x"))) return rc;
+    if (g->kind != MUONH_NORM_LAYER && g->kind != MUONH_NORM_RMS) return fail(MUONH_EINVAL, "unknown norm kind");
+    if (g->reserved != 0) return fail(MUONH_EINVAL, "reserved != 0");
+    if (!(g->eps >= 0.0f) || !std::isfinite(g->eps)) return fail(MUONH_EINVAL, "eps must be >= 0 and finite");
+    if ((rc = check_size(g->rows, 0, "rows")) || (rc = check_size(g->cols, 1, "cols"))) return rc;
+    if ((rc = check_pitch(g->ldx, g->cols, "ldx")) || (rc = check_pitch(g->ldy, g->cols, "ldy"))) return rc;
+    const int layer = g->kind == MUONH_NORM_LAYER;
+    if (!layer && g->mean) return fail(MUONH_EINVAL, "mean must be NULL for MUONH_NORM_RMS");
+    if (g->rows == 0) return MUONH_OK;
+    if ((rc = check_vectors(g->x && g->y && g->weight && g->rstd && (!layer || g->mean), "x, y, weight, rstd or mean")))
+      return rc;
+    const int64_t size = g->dtype == MUONH_BF16 ? 2 : 4;
+    if (!aligned(g->x, (uintptr_t)size) || !aligned(g->y, (uintptr_t)size) || !aligned(g->weight, 4) ||
+        !aligned(g->bias, 4) || !aligned(g->mean, 4) || !aligned(g->rstd, 4))
+      return fail(MUONH_EINVAL, "misaligned pointer");
+    if (!may_share(g->y, g->ldy, g->x, g->ldx, g->rows, g->cols, size))
+      return fail(MUONH_EINVAL, "y overlaps x");
+    NormArgs a{};
+    a.x = g->x;
+    a.weight = g->weight;
+    a.bias = g->bias;
+    a.y = g->y;
+    a.mean = g->mean;
+    a.rstd = g->rstd;
+    a.rows = g->rows;
+    a.cols = g->cols;
+    a.ldx = g->ldx;
+    a.ldy = g->ldy;
+    a.eps = g->eps;
+    return launched(launch_norm_forward(g->dtype == MUONH_BF16, layer, a, reinterpret_cast<hipStream_t>(stream)),
+                    "norm_forward");
+  });
+}
+
+int muonh_norm_backward_workspace(int64_t rows, int64_t cols, size_t* bytes) {
+  return guarded([&]() -> int {
+    if (!bytes) return fail(MUONH_EINVAL, "null argument");
+    int rc;
+    if ((rc = check_size(rows, 0, "rows")) || (rc = check_size(cols, 1, "cols"))) return rc;
+    *bytes = (size_t)(2 * norm_partial_rows(rows, cols) * cols) * sizeof(float);
+    return MUONH_OK;
+  });
+}
+
+int muonh_norm_backward(const muonh_norm_grad_args* g, void* stream) {
+  return guarded([&]() -> int {
+    int rc;
+    if (!g) return fail(MUONH_EINVAL, "null argument");
+    if ((rc = check_dtype(g->dtype, "x"))) return rc;
+    if (g->kind != MUONH_NORM_LAYER && g->kind != MUONH_NORM_RMS) return fail(MUONH_EINVAL, "unknown norm kind");
+    if (g->reserved != 0) return fail(MUONH_EINVAL, "reserved != 0");
+    if (g->accumulate != 0 && g->accumulate != 1) return fail(MUONH_EINVAL, "accumulate must be 0 or 1");
+    if ((rc = check_size(g->rows, 0, "rows")) || (rc = check_size(g->cols, 1, "cols"))) return rc;
+    if ((rc = check_pitch(g->ld_dy, g->cols, "ld_dy")) || (rc = check_pitch(g->ldx, g->cols, "ldx")) ||
+        (rc = check_pitch(g->ld_dx, g->cols, "ld_dx")))
+      return rc;
+    const int layer = g->kind == MUONH_NORM_LAYER;
+    if (!layer && g->mean) return fail(MUONH_EINVAL, "mean must be NULL for MUONH_NORM_RMS");
+    if ((rc = check_vectors(g->weight && g->dweight, "weight or dweight"))) return rc;
+    const int64_t size = g->dtype == MUONH_BF16 ? 2 : 4;
+    if (g->rows > 0) {
+      if ((rc = check_vectors(g->dy && g->x && g->dx && g->rstd && (!layer || g->mean), "dy, x, dx, rstd or mean")))
+        return rc;
+      if (!aligned(g->dy, (uintptr_t)size) || !aligned(g->x, (uintptr_t)size) || !aligned(g->dx, (uintptr_t)size))
+        return fail(MUONH_EINVAL, "misaligned pointer");
+      if (!may_share(g->dx, g->ld_dx, g->dy, g->ld_dy, g->rows, g->cols, size) ||
+          !may_share(g->dx, g->ld_dx, g->x, g->ldx, g->rows, g->cols, size))
+        return fail(MUONH_EINVAL, "dx overlaps dy or x");
+    }
+    if (!aligned(g->weight, 4) || !aligned(g->mean, 4) || !aligned(g->rstd, 4) || !aligned(g->dweight, 4) ||
+        !aligned(g->dbias, 4))
+      return fail(MUONH_EINVAL, "misaligned pointer");
+    size_t need = 0;
+    if ((rc = muonh_norm_backward_workspace(g->rows, g->cols, &need))) return rc;
+    if (need > 0 && (!g->workspace || g->workspace_bytes < need))
+      return fail(MUONH_ENOMEM, "workspace too small: need " + std::to_string(need) + " bytes");
+    if (!aligned(g->workspace, kAlign)) return fail(MUONH_EINVAL, "workspace must be 256-byte aligned");
+    NormGradArgs a{};
+    a.dy = g->dy;
+    a.x = g->x;
+    a.weight = g->weight;
+    a.mean = g->mean;
+    a.rstd = g->rstd;
+    a.dx = g->dx;
+    a.dweight = g->dweight;
+    a.dbias = g->dbias;
+    a.partials = static_cast<float*>(g->workspace);
+    a.rows = g->rows;
+    a.cols = g->cols;
+    a.lddy = g->ld_dy;
+    a.ldx = g->ldx;
+    a.lddx = g->ld_dx;
+    a.accumulate = g->accumulate;
+    return launched(launch_norm_backward(g->dtype == MUONH_BF16, layer, a, reinterpret_cast<hipStream_t>(stream)),
+                    "norm_backward");
+  });
+}
+
+}  // extern "C"

@@ -1,0 +1,91 @@
+// Launchers of the block-scaled FP8 operators (block_fp8.hip) and of the norms
+// (norm.hip), and the checks their C entry points share.  Not part of the
+// public ABI.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <exception>
+#include <string>
+
+#include "internal.h"
+
+namespace muonh {
+
+constexpr int kFp8Block = 128;   // elements of the contraction that share a scale
+constexpr int kFp8Tile = 128;    // the quantiser's tile: 128 x 128 elements per workgroup
+
+// The quantiser's view of one matrix: x [rows x cols], and the outputs of its
+// row form (q, s) and of its column form (qt, st); a null q or qt is not written.
+struct QuantArgs {
+  const void* x;
+  int64_t rows, cols, ldx;
+  uint8_t* q;
+  uint8_t* s;
+  int64_t ldq, lds;
+  uint8_t* qt;
+  uint8_t* st;
+  int64_t ldqt, ldst;
+};
+// bf16: x's type; square: blocks of 128 x 128 (else 1 x 128).
+hipError_t launch_block_quantize(int bf16, int square, const QuantArgs& a, hipStream_t st);
+
+// C[m][n] (+)= sum_k A[m][k] B[n][k].
+struct BlockMatmulArgs {
+  const uint8_t* a;
+  const uint8_t* b;
+  const uint8_t* sa;
+  const uint8_t* sb;
+  int64_t lda, ldb, ldsa, ldsb;   // bytes
+  void* c;
+  int64_t ldc;                    // elements
+  int32_t m, n, kblocks;          // kblocks: blocks of 128 along the contraction
+  int32_t a_shift, b_shift;       // scale row = row >> shift (0 or 7)
+};
+hipError_t launch_block_matmul(int c_bf16, int accumulate, const BlockMatmulArgs& a, hipStream_t st);
+
+struct NormArgs {
+  const void* x;
+  const float* weight;
+  const float* bias;    // nullable
+  void* y;
+  float* mean;          // layer norm only
+  float* rstd;
+  int64_t rows, cols, ldx, ldy;
+  float eps;
+};
+hipError_t launch_norm_forward(int bf16, int layer, const NormArgs& a, hipStream_t st);
+
+struct NormGradArgs {
+  const void* dy;
+  const void* x;
+  const float* weight;
+  const float* mean;    // layer norm only
+  const float* rstd;
+  void* dx;
+  float* dweight;
+  float* dbias;         // nullable
+  float* partials;      // norm_partial_rows() rows of cols floats (twice that with dbias)
+  int64_t rows, cols, lddy, ldx, lddx;
+  int32_t accumulate;
+};
+// Rows of per-workgroup partial sums of dweight that a backward pass writes.
+int64_t norm_partial_rows(int64_t rows, int64_t cols);
+hipError_t launch_norm_backward(int bf16, int layer, const NormGradArgs& a, hipStream_t st);
+
+// Runs the body of a C entry point; nothing is thrown across the ABI.
+template <typename F>
+int guarded(F&& body) {
+  try {
+    return body();
+  } catch (const std::exception& e) {
+    try {
+      return set_last_error(MUONH_ENOMEM, e.what());
+    } catch (...) {
+      return MUONH_ENOMEM;
+    }
+  }
+}
+
+}  // namespace muonh

@@ -85,6 +85,30 @@ class muonh_plan_info(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_size_t)]
 
 
+class muonh_fp8_matrix(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("ld", ctypes.c_int64), ("ld_scale", ctypes.c_int64),
+                ("block_rows", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class muonh_norm_args(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("y", ctypes.c_void_p), ("mean", ctypes.c_void_p), ("rstd", ctypes.c_void_p),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("ldx", ctypes.c_int64),
+                ("ldy", ctypes.c_int64), ("dtype", ctypes.c_int32), ("kind", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class muonh_norm_grad_args(ctypes.Structure):
+    _fields_ = [("dy", ctypes.c_void_p), ("x", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("mean", ctypes.c_void_p), ("rstd", ctypes.c_void_p), ("dx", ctypes.c_void_p),
+                ("dweight", ctypes.c_void_p), ("dbias", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("ld_dy", ctypes.c_int64), ("ldx", ctypes.c_int64),
+                ("ld_dx", ctypes.c_int64), ("dtype", ctypes.c_int32), ("kind", ctypes.c_int32),
+                ("accumulate", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
 _libs = {}
 
 # (name, restype, argtypes)
@@ -124,6 +148,19 @@ _SIGNATURES = [
     ("muonh_adamw_step", ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(muonh_adamw_tensor), ctypes.c_int32,
                                         ctypes.c_float, ctypes.c_int64, ctypes.c_void_p]),
     ("muonh_adamw_destroy", ctypes.c_int, [ctypes.c_void_p]),
+    ("muonh_block_quantize", ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64,
+                                            ctypes.c_int64, ctypes.POINTER(muonh_fp8_matrix),
+                                            ctypes.POINTER(muonh_fp8_matrix), ctypes.c_void_p]),
+    ("muonh_block_matmul_workspace", ctypes.c_int, [ctypes.POINTER(muonh_fp8_matrix),
+                                                    ctypes.POINTER(muonh_fp8_matrix),
+                                                    ctypes.POINTER(ctypes.c_size_t)]),
+    ("muonh_block_matmul", ctypes.c_int, [ctypes.POINTER(muonh_fp8_matrix), ctypes.POINTER(muonh_fp8_matrix),
+                                          ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32,
+                                          ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    ("muonh_norm_forward", ctypes.c_int, [ctypes.POINTER(muonh_norm_args), ctypes.c_void_p]),
+    ("muonh_norm_backward_workspace", ctypes.c_int, [ctypes.c_int64, ctypes.c_int64,
+                                                     ctypes.POINTER(ctypes.c_size_t)]),
+    ("muonh_norm_backward", ctypes.c_int, [ctypes.POINTER(muonh_norm_grad_args), ctypes.c_void_p]),
 ]
 
 
