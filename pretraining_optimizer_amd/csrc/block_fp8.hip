@@ -16,6 +16,8 @@
 // only rounding is the one to E4M3.  NaN and Inf become the E4M3 NaN, which
 // turns the outputs they take part in into NaN as the unquantised product does.
 
+#include <type_traits>
+
 #include "device_util.h"
 #include "operators.h"
 
@@ -346,14 +348,329 @@ __global__ __launch_bounds__(kThinThreads) void block_matmul_thin_kernel(BlockMa
   store_c<C, ACC>(reinterpret_cast<C*>(p.c), (int64_t)row * p.ldc + col, p.n - col, s);
 }
 
-template <typename C>
-hipError_t matmul_for(int accumulate, const BlockMatmulArgs& a, hipStream_t st) {
+#define MUONH_LDS __attribute__((address_space(3)))
+
+// Workgroup barrier without a memory fence (a fence would wait for every load
+// in flight); the empty asm statements keep LDS accesses on their side of it.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// s_waitcnt vmcnt(VM) lgkmcnt(0): all but the last VM global accesses, and all
+// LDS accesses, of this wavefront are done.
+template <int VM>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(VM >= 0 && VM < 64, "vmcnt is 6 bits");
+  __builtin_amdgcn_s_waitcnt((VM & 15) | ((VM >> 4) << 14) | (7 << 4) | (0 << 8));
+  asm volatile("" ::: "memory");
+}
+
+constexpr int kBufferConfig = 0x00020000;   // raw, unformatted buffer access
+constexpr int kSgValu = 0x002, kSgMfma = 0x008, kSgVmemRead = 0x020, kSgDsRead = 0x100;
+#define MUONH_SG(mask, n) __builtin_amdgcn_sched_group_barrier((mask), (n), 0)
+
+constexpr int kTileThreads = 256;
+constexpr int kStageK = 64;   // bytes of the contraction per stage and operand row
+
+// 16-byte chunk c of LDS row r (4 chunks) sits at c ^ swz64(r): the rows of a
+// fragment read then differ in banks whether 8 or 16 lanes are served at once.
+__device__ __forceinline__ int swz64(int r) { return ((r >> 1) & 3) ^ ((r >> 3) & 1); }
+
+// Tile of workgroup b: the hardware deals workgroups to the 8 XCDs in turn, so
+// XCD x gets a contiguous share of the tile list, and the list walks groups of
+// 4 tile rows column by column: the 32 tiles that run on an XCD at a time share
+// 4 panels of A and 8 of B in its L2.
+__device__ __forceinline__ void tile_of(uint32_t b, uint32_t mt, uint32_t nt, uint32_t& tm, uint32_t& tn) {
+  const uint32_t total = mt * nt, share = total / kMaxXcd, extra = total % kMaxXcd;
+  const uint32_t x = b % kMaxXcd;
+  const uint32_t idx = x * share + min(x, extra) + b / kMaxXcd;
+  const uint32_t g = idx / (4 * nt), rest = idx % (4 * nt), rows = min(4u, mt - 4 * g);
+  tm = 4 * g + rest % rows;
+  tn = rest / rows;
+}
+
+// C tile of (64 MB)^2 per workgroup of 4 wavefronts (2 x 2, each MB x MB MFMA
+// blocks of 32 x 32).  Stages of 64 bytes of K go straight from global memory
+// into a ring of 4 LDS slots; each slot is a variable of its own, so that the
+// compiler makes a fragment read wait for the loads into its own slot only.
+// In iteration t a wavefront multiplies stage t's fragments, reads those of
+// stage t + 1 and issues the loads of stage t + 4 into the slot that stage t
+// has left; one barrier per iteration, before these.
+template <typename C, bool ACC, int MB>
+__global__ __launch_bounds__(kTileThreads) void block_matmul_tile_kernel(BlockMatmulArgs p, uint32_t mt,
+                                                                         uint32_t nt) {
+  constexpr int kTile = 64 * MB;
+  constexpr int kOperand = kTile * kStageK;
+  constexpr int kSlot = 2 * kOperand;
+  constexpr int kLoads = 2 * MB;        // per wavefront and stage
+  constexpr bool kFp8 = sizeof(C) == 2;
+  __shared__ __attribute__((aligned(16))) uint8_t slot0[kSlot];
+  __shared__ __attribute__((aligned(16))) uint8_t slot1[kSlot];
+  __shared__ __attribute__((aligned(16))) uint8_t slot2[kSlot];
+  __shared__ __attribute__((aligned(16))) uint8_t slot3[kSlot];
+
+  uint32_t tm, tn;
+  tile_of(blockIdx.x, mt, nt, tm, tn);
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wr = wave >> 1, wc = wave & 1;
+  const int row0 = (int)tm * kTile, col0 = (int)tn * kTile;
+
+  f32x16_t acc[MB][MB];
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+#pragma unroll
+    for (int j = 0; j < MB; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+
+  // Loads: instruction i of a wavefront fills rows 16 (MB wave + i) .. + 15 of
+  // an operand; lane l lands in row l / 4, slot chunk l % 4.  Rows behind the
+  // matrix and stages behind the last are out of the descriptor's range: they
+  // make no memory access.  (The host keeps 256 rows below 2^31 bytes.)
+  const uint8_t* abase = p.a + (int64_t)row0 * p.lda;
+  const uint8_t* bbase = p.b + (int64_t)col0 * p.ldb;
+  const int arange = (int)(min(kTile, p.m - row0) * p.lda), brange = (int)(min(kTile, p.n - col0) * p.ldb);
+  const int lrow = lane >> 2, lchunk = (lane & 3) ^ swz64(lrow);
+  const int avoff = (int)((wave * MB * 16 + lrow) * p.lda) + lchunk * 16;
+  const int bvoff = (int)((wave * MB * 16 + lrow) * p.ldb) + lchunk * 16;
+  const int nh = 2 * p.kblocks;
+  auto load_stage = [&](uint8_t (&slot)[kSlot], int t) {
+    const __amdgpu_buffer_rsrc_t ra =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(abase), (short)0, t < nh ? arange : 0, kBufferConfig);
+    const __amdgpu_buffer_rsrc_t rb =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(bbase), (short)0, t < nh ? brange : 0, kBufferConfig);
+    MUONH_LDS uint8_t* d = (MUONH_LDS uint8_t*)slot + wave * MB * 16 * kStageK;
+#pragma unroll
+    for (int i = 0; i < MB; ++i) {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (MUONH_LDS void*)(d + i * 16 * kStageK), 16, avoff,
+                                               (int)(i * 16 * p.lda) + t * kStageK, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (MUONH_LDS void*)(d + kOperand + i * 16 * kStageK), 16, bvoff,
+                                               (int)(i * 16 * p.ldb) + t * kStageK, 0, 0);
+    }
+  };
+
+  // Fragments: block i of A is rows wr 32 MB + 32 i + l % 32; lane l holds the
+  // 32 bytes 32 (l / 32) .. of its stage.
+  const int fchunk = (2 * (lane >> 5)) ^ swz64(lane & 15);
+  const int aoff = (wr * MB * 32 + (lane & 31)) * kStageK, boff = kOperand + (wc * MB * 32 + (lane & 31)) * kStageK;
+  struct Frags {
+    u32x4_t a[MB][2], b[MB][2];
+  };
+  auto read_frags = [&](Frags& f, uint8_t (&slot)[kSlot]) {
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        f.a[i][h] = *reinterpret_cast<const u32x4_t*>(slot + aoff + i * 32 * kStageK + ((fchunk ^ h) << 4));
+        f.b[i][h] = *reinterpret_cast<const u32x4_t*>(slot + boff + i * 32 * kStageK + ((fchunk ^ h) << 4));
+      }
+  };
+
+  // Scales: 4 blocks' bytes per row at a time, the current one lowest.
+  const uint8_t* sa[MB];
+  const uint8_t* sb[MB];
+#pragma unroll
+  for (int i = 0; i < MB; ++i) {
+    sa[i] = p.sa + (int64_t)(min(row0 + (wr * MB + i) * 32 + (lane & 31), p.m - 1) >> p.a_shift) * p.ldsa;
+    sb[i] = p.sb + (int64_t)(min(col0 + (wc * MB + i) * 32 + (lane & 31), p.n - 1) >> p.b_shift) * p.ldsb;
+  }
+  uint32_t ea[MB], eb[MB], na[MB], nb[MB];
+  auto load_scales = [&](int kb) {
+    const int at = min(kb, p.kblocks - 1) & ~3;
+#pragma unroll
+    for (int i = 0; i < MB; ++i) {
+      na[i] = ld_global<uint32_t>(sa[i] + at);
+      nb[i] = ld_global<uint32_t>(sb[i] + at);
+    }
+  };
+
+  // Operands are swapped (B first), so a lane holds 4 consecutive columns of
+  // one row per group of 4 accumulators.
+  auto multiply = [&](const Frags& f) {
+    if constexpr (kFp8) {
+#pragma unroll
+      for (int i = 0; i < MB; ++i)
+#pragma unroll
+        for (int j = 0; j < MB; ++j) {
+          i32x8_t fa, fb;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            fa[e] = (int)f.a[i][0][e];
+            fa[4 + e] = (int)f.a[i][1][e];
+            fb[e] = (int)f.b[j][0][e];
+            fb[4 + e] = (int)f.b[j][1][e];
+          }
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb, fa, acc[i][j], 0, 0, 0, (int)eb[j], 0,
+                                                                      (int)ea[i]);
+        }
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        bf16x8_t wa[MB], wb[MB];
+#pragma unroll
+        for (int i = 0; i < MB; ++i) {
+          wa[i] = widen8(f.a[i][q >> 1][(q & 1) * 2], f.a[i][q >> 1][(q & 1) * 2 + 1], scale_value(ea[i] & 255u));
+          wb[i] = widen8(f.b[i][q >> 1][(q & 1) * 2], f.b[i][q >> 1][(q & 1) * 2 + 1], scale_value(eb[i] & 255u));
+        }
+#pragma unroll
+        for (int i = 0; i < MB; ++i)
+#pragma unroll
+          for (int j = 0; j < MB; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wb[j], wa[i], acc[i][j], 0, 0, 0);
+      }
+    }
+  };
+  // SC: scale loads that were issued after stage t + 1's loads.
+  auto iterate = [&](const Frags& cur, Frags& next, uint8_t (&mine)[kSlot], uint8_t (&after)[kSlot], int t,
+                     auto sc) {
+    wait_loads<2 * kLoads + decltype(sc)::value>();   // stage t + 1 is in LDS (t + 2 and t + 3 may be in flight)
+    lds_barrier();              // for every wavefront, and all are done with stage t's slot
+    load_stage(mine, t + 4);
+    read_frags(next, after);
+    multiply(cur);
+    if constexpr (kFp8) {
+#pragma unroll
+      for (int k = 0; k < MB * MB / 2; ++k) {
+        MUONH_SG(kSgMfma, 1);
+        MUONH_SG(kSgDsRead, MB == 4 ? 1 : 2);
+        MUONH_SG(kSgMfma, 1);
+        MUONH_SG(kSgDsRead, MB == 4 ? 1 : 2);
+        MUONH_SG(kSgVmemRead, MB == 4 ? 1 : 2);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  constexpr std::integral_constant<int, 2 * MB> with_scales{};
+  constexpr std::integral_constant<int, 0> without{};
+
+  load_scales(0);
+  asm volatile("" ::: "memory");   // ahead of the stages, so waiting for them waits for none
+  load_stage(slot0, 0);
+  load_stage(slot1, 1);
+  load_stage(slot2, 2);
+  load_stage(slot3, 3);
+  wait_loads<3 * kLoads>();
+  lds_barrier();
+  Frags f0, f1;
+  read_frags(f0, slot0);
+  // Two blocks of 128 per trip.  Behind an odd count the second one's data are
+  // out of range, which the loads turn into zeros; its scales are set to 1, as
+  // the bytes there are the caller's.
+  for (int kb = 0; kb < p.kblocks; kb += 2) {
+#pragma unroll
+    for (int i = 0; i < MB; ++i) {
+      ea[i] = na[i] >> (8 * (kb & 2));
+      eb[i] = nb[i] >> (8 * (kb & 2));
+    }
+    load_scales(kb + 2);
+    __builtin_amdgcn_sched_barrier(0);
+    iterate(f0, f1, slot0, slot1, 2 * kb, with_scales);
+    iterate(f1, f0, slot1, slot2, 2 * kb + 1, with_scales);
+    const bool last = kb + 1 >= p.kblocks;
+#pragma unroll
+    for (int i = 0; i < MB; ++i) {
+      ea[i] = last ? 127u : ea[i] >> 8;
+      eb[i] = last ? 127u : eb[i] >> 8;
+    }
+    iterate(f0, f1, slot2, slot3, 2 * kb + 2, with_scales);
+    iterate(f1, f0, slot3, slot0, 2 * kb + 3, without);
+  }
+  wait_loads<0>();   // no load into LDS is in flight past this point
+  lds_barrier();
+
+  // Epilogue: the wavefront's rows go through a slot of its own, in passes of
+  // as many rows as it holds, 16-byte chunk c of row r at c ^ (r & 15), and
+  // leave as whole rows.
+  uint8_t* reg = wave == 0 ? slot0 : wave == 1 ? slot1 : wave == 2 ? slot2 : slot3;
+  constexpr int kRowBytes = 32 * MB * (int)sizeof(C);
+  constexpr int kChunks = kRowBytes / 16;                  // 16-byte chunks per row
+  constexpr int kPass = kSlot / kRowBytes < 32 * MB ? kSlot / kRowBytes : 32 * MB;
+  static_assert(kPass % 32 == 0 && kChunks >= 8, "whole blocks per pass");
+  constexpr int kMask = kChunks < 16 ? kChunks - 1 : 15;
+  C* c = reinterpret_cast<C*>(p.c);
+#pragma unroll
+  for (int i0 = 0; i0 < MB; i0 += kPass / 32) {
+#pragma unroll
+    for (int i = 0; i < kPass / 32; ++i)
+#pragma unroll
+      for (int j = 0; j < MB; ++j)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int r = 32 * i + (lane & 31), col = 32 * j + 8 * g + 4 * (lane >> 5);
+          const f32x16_t& v = acc[i0 + i][j];
+          uint8_t* d = reg + r * kRowBytes + ((((col * (int)sizeof(C)) >> 4) ^ (r & kMask)) << 4);
+          if constexpr (kFp8 && !ACC) {
+            u32x2_t o;
+            o[0] = pack_bf16x2(v[4 * g], v[4 * g + 1]);
+            o[1] = pack_bf16x2(v[4 * g + 2], v[4 * g + 3]);
+            *reinterpret_cast<u32x2_t*>(d + (col & 4) * 2) = o;
+          } else if constexpr (kFp8) {
+            // added to c before the one rounding: straight to memory
+            const int row = row0 + wr * MB * 32 + i0 * 32 + r, cc = col0 + wc * MB * 32 + col;
+            if (row < p.m && cc < p.n)
+              store_c<C, ACC>(c, (int64_t)row * p.ldc + cc, p.n - cc, f32x4_t{v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]});
+          } else {
+            *reinterpret_cast<f32x4_t*>(d) = f32x4_t{v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]};
+          }
+        }
+    if constexpr (kFp8 && ACC) continue;
+#pragma unroll
+    for (int k = 0; k < kPass * kChunks / 64; ++k) {
+      const int idx = k * 64 + lane, r = idx / kChunks, ch = idx % kChunks;
+      const u32x4_t v = *reinterpret_cast<const u32x4_t*>(reg + r * kRowBytes + ((ch ^ (r & kMask)) << 4));
+      const int row = row0 + wr * MB * 32 + i0 * 32 + r;
+      const int col = col0 + wc * MB * 32 + ch * (16 / (int)sizeof(C));
+      if (row >= p.m || col >= p.n) continue;
+      C* d = c + (int64_t)row * p.ldc + col;
+      if constexpr (kFp8) {
+        typedef uint32_t vec __attribute__((ext_vector_type(4), aligned(2)));
+        if (col + 8 <= p.n) {
+          st_global<vec>(d, v);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (col + e < p.n) st_global<uint16_t>(d + e, (uint16_t)(v[e >> 1] >> (16 * (e & 1))));
+        }
+      } else {
+        typedef float vec __attribute__((ext_vector_type(4), aligned(4)));
+        vec o = __builtin_bit_cast(f32x4_t, v);
+        if (col + 4 <= p.n) {
+          if constexpr (ACC) o += ld_global<vec>(d);
+          st_global<vec>(d, o);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (col + e < p.n) st_global<float>(d + e, ACC ? ld_global<float>(d + e) + o[e] : o[e]);
+        }
+      }
+    }
+  }
+}
+
+// Tiles need panels of 256 rows below 2^31 bytes (buffer offsets).
+bool tiles_fit(const BlockMatmulArgs& a) {
+  return a.lda < ((int64_t)1 << 23) && a.ldb < ((int64_t)1 << 23);
+}
+
+template <typename C, bool ACC>
+hipError_t matmul_for(const BlockMatmulArgs& a, hipStream_t st) {
+  if (a.kblocks > 0 && tiles_fit(a) && a.m > 64 && a.n > 64) {
+    const int64_t big = (int64_t)((a.m + 255) / 256) * ((a.n + 255) / 256);
+    if (big >= 128) {
+      const uint32_t mt = (uint32_t)(a.m + 255) / 256, nt = (uint32_t)(a.n + 255) / 256;
+      hipLaunchKernelGGL((block_matmul_tile_kernel<C, ACC, 4>), dim3(mt * nt), dim3(kTileThreads), 0, st, a, mt, nt);
+    } else {
+      const uint32_t mt = (uint32_t)(a.m + 127) / 128, nt = (uint32_t)(a.n + 127) / 128;
+      hipLaunchKernelGGL((block_matmul_tile_kernel<C, ACC, 2>), dim3(mt * nt), dim3(kTileThreads), 0, st, a, mt, nt);
+    }
+    return hipGetLastError();
+  }
   const unsigned ntiles = (unsigned)((a.n + 15) / 16);
   const dim3 grid(ntiles * (unsigned)((a.m + 15) / 16));
-  if (accumulate)
-    hipLaunchKernelGGL((block_matmul_thin_kernel<C, true>), grid, dim3(kThinThreads), 0, st, a, ntiles);
-  else
-    hipLaunchKernelGGL((block_matmul_thin_kernel<C, false>), grid, dim3(kThinThreads), 0, st, a, ntiles);
+  hipLaunchKernelGGL((block_matmul_thin_kernel<C, ACC>), grid, dim3(kThinThreads), 0, st, a, ntiles);
   return hipGetLastError();
 }
 
@@ -378,7 +695,8 @@ hipError_t launch_block_quantize(int bf16, int square, const QuantArgs& a, hipSt
 }
 
 hipError_t launch_block_matmul(int c_bf16, int accumulate, const BlockMatmulArgs& a, hipStream_t st) {
-  return c_bf16 ? matmul_for<uint16_t>(accumulate, a, st) : matmul_for<float>(accumulate, a, st);
+  if (c_bf16) return accumulate ? matmul_for<uint16_t, true>(a, st) : matmul_for<uint16_t, false>(a, st);
+  return accumulate ? matmul_for<float, true>(a, st) : matmul_for<float, false>(a, st);
 }
 
 }  // namespace muonh
