@@ -19,60 +19,85 @@ from __future__ import annotations
 import ctypes
 from typing import Optional
 
-from .muonh import (MUONH_BF16, MUONH_F32, _check, _record, _stream_ptr, load_library, muonh_fp8_matrix,
-                    muonh_norm_args, muonh_norm_grad_args)
+from .muonh import (MUONH_BF16, MUONH_F32, _check, _record, load_library, muonh_fp8_matrix, muonh_norm_args,
+                    muonh_norm_grad_args)
 
+# The smallest calls are bound by this module: a launch takes about 3.5 us,
+# a tensor 1.5 us, torch.cuda.current_stream() 2.8 us.  So the library and
+# torch are looked up once, and the current stream is read as a raw pointer.
 NORM_KINDS = {"layer": 0, "rms": 1}
+_torch = None
+_lib = None
 _CODES = {}
 
 
-def _code(t, what: str) -> int:
-    if not _CODES:
-        import torch
-        _CODES.update({torch.float32: MUONH_F32, torch.bfloat16: MUONH_BF16})
-    try:
-        return _CODES[t.dtype]
-    except KeyError:
-        raise TypeError(f"{what}: dtype must be float32 or bfloat16, got {t.dtype}") from None
-
-
-def _here(*tensors):
-    """Every tensor is on the current device."""
+def _setup():
+    global _torch, _lib
     import torch
-    dev = torch.cuda.current_device()
+    _lib = load_library()
+    _CODES.update({torch.float32: MUONH_F32, torch.bfloat16: MUONH_BF16})
+    _torch = torch
+
+
+def _code(t, what: str) -> int:
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{what}: dtype must be float32 or bfloat16, got {t.dtype}")
+    return code
+
+
+def _here(*tensors) -> int:
+    """Every tensor is on the current device, whose index is returned."""
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.device.index != dev):
+        if t is not None and t.get_device() < 0:
             raise ValueError("all tensors must be CUDA tensors of the current device")
+    dev = _torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("all tensors must be CUDA tensors of the current device")
+    return dev
 
 
-def _rows2d(t, what: str) -> int:
+def _stream(stream, dev: int) -> int:
+    if stream is None:
+        return _torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device.index != dev:
+        raise ValueError("stream: of another device than the tensors")
+    return stream.cuda_stream
+
+
+def _pitch(t, rows: int, cols: int, what: str) -> int:
     """The row pitch of a matrix whose rows are contiguous."""
+    s0, s1 = t.stride()
+    if cols > 1 and s1 != 1:
+        raise ValueError(f"{what}: the elements of a row must be contiguous")
+    if rows <= 1:
+        return max(cols, s0)
+    if s0 < cols:
+        raise ValueError(f"{what}: rows overlap")
+    return s0
+
+
+def _matrix(t, what: str):
+    """(rows, cols, row pitch) of a 2-D tensor."""
     if t.dim() != 2:
         raise ValueError(f"{what}: a 2-D tensor is required")
     rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
-        raise ValueError(f"{what}: the elements of a row must be contiguous")
-    if rows <= 1:
-        return max(cols, t.stride(0))
-    if t.stride(0) < cols:
-        raise ValueError(f"{what}: rows overlap")
-    return t.stride(0)
+    return rows, cols, _pitch(t, rows, cols, what)
 
 
 def _vector(t, n: int, what: str):
-    import torch
-    if t.dtype != torch.float32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+    if t.dtype is not _torch.float32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
         raise ValueError(f"{what}: a contiguous float32 vector of {n} elements is required")
 
 
 def _empty(shape, dtype, device, stream):
     """A new tensor that work on `stream` may write at once: memory of that
     stream's pool, so no earlier work of another stream still uses it."""
-    import torch
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _torch.empty(shape, dtype=dtype, device=device)
+    with _torch.cuda.stream(stream):
+        return _torch.empty(shape, dtype=dtype, device=device)
 
 
 class Fp8Matrix:
@@ -88,7 +113,9 @@ class Fp8Matrix:
     __slots__ = ("data", "scale", "rows", "cols", "block_rows", "_desc")
 
     def __init__(self, data, scale, cols: int, block_rows: int = 1):
-        import torch
+        if _torch is None:
+            _setup()
+        torch = _torch
         if data.dtype != torch.float8_e4m3fn or scale.dtype != torch.uint8:
             raise TypeError("data must be float8_e4m3fn and scale uint8")
         if data.dim() != 2 or scale.dim() != 2 or not data.is_contiguous() or not scale.is_contiguous():
@@ -109,12 +136,19 @@ class Fp8Matrix:
     @classmethod
     def empty(cls, rows: int, cols: int, block_rows: int = 1, device=None, stream=None):
         """An operand of this shape to quantise into (uninitialised)."""
-        import torch
-        blocks = -(-cols // 128)
-        device = torch.device("cuda", torch.cuda.current_device()) if device is None else device
-        return cls(_empty((rows, blocks * 128), torch.float8_e4m3fn, device, stream),
-                   _empty((-(-rows // block_rows), -(-blocks // 4) * 4), torch.uint8, device, stream),
-                   cols, block_rows)
+        if _torch is None:
+            _setup()
+        if block_rows not in (1, 128):
+            raise ValueError("block_rows must be 1 or 128")
+        device = _torch.device("cuda", _torch.cuda.current_device()) if device is None else device
+        ld = (cols + 127) // 128 * 128
+        lds = (ld + 511) // 512 * 4
+        m = cls.__new__(cls)
+        m.rows, m.cols, m.block_rows = rows, cols, block_rows
+        m.data = _empty((rows, ld), _torch.float8_e4m3fn, device, stream)
+        m.scale = _empty(((rows + block_rows - 1) // block_rows, lds), _torch.uint8, device, stream)
+        m._desc = muonh_fp8_matrix(m.data.data_ptr(), m.scale.data_ptr(), rows, cols, ld, lds, block_rows, 0)
+        return m
 
 
 def fp8_quantize(x, form: str = "row", block_rows: int = 1, out: Optional[Fp8Matrix] = None,
@@ -128,10 +162,12 @@ def fp8_quantize(x, form: str = "row", block_rows: int = 1, out: Optional[Fp8Mat
     """
     if form not in ("row", "col", "both"):
         raise ValueError("form must be 'row', 'col' or 'both'")
-    code, ldx = _code(x, "x"), _rows2d(x, "x")
-    _here(x)
-    rows, cols = x.shape
+    if _torch is None:
+        _setup()
+    code = _code(x, "x")
+    rows, cols, ldx = _matrix(x, "x")
     q = qt = None
+    dev = _here(x, None if out is None else out.data, None if out_t is None else out_t.data)
     if form != "col":
         q = Fp8Matrix.empty(rows, cols, block_rows, x.device, stream) if out is None else out
         if (q.rows, q.cols, q.block_rows) != (rows, cols, block_rows):
@@ -146,9 +182,10 @@ def fp8_quantize(x, form: str = "row", block_rows: int = 1, out: Optional[Fp8Mat
         raise ValueError("out_t is the column form, which form='row' does not write")
     if stream is not None:
         _record(stream, [x] + [t for m in (q, qt) if m is not None for t in (m.data, m.scale)])
-    _check(load_library().muonh_block_quantize(
-        x.data_ptr(), code, rows, cols, ldx, None if q is None else ctypes.byref(q._desc),
-        None if qt is None else ctypes.byref(qt._desc), _stream_ptr(stream)), "muonh_block_quantize")
+    rc = _lib.muonh_block_quantize(x.data_ptr(), code, rows, cols, ldx, None if q is None else ctypes.byref(q._desc),
+                                   None if qt is None else ctypes.byref(qt._desc), _stream(stream, dev))
+    if rc:
+        _check(rc, "muonh_block_quantize")
     return (q, qt) if form == "both" else q if qt is None else qt
 
 
@@ -159,43 +196,50 @@ def fp8_matmul(a: Fp8Matrix, b: Fp8Matrix, out=None, out_dtype=None, accumulate:
                  pitch); a new one of out_dtype (bfloat16 if None) if not given
     accumulate : add the product to what out holds
     """
-    import torch
     if a.cols != b.cols:
         raise ValueError(f"the operands contract {a.cols} and {b.cols} columns")
+    m, n = a.rows, b.rows
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
-        out = _empty((a.rows, b.rows), out_dtype or torch.bfloat16, a.data.device, stream)
-    elif tuple(out.shape) != (a.rows, b.rows) or (out_dtype is not None and out.dtype != out_dtype):
-        raise ValueError(f"out: a matrix of shape {(a.rows, b.rows)} and the asked dtype is required")
-    code, ldc = _code(out, "out"), _rows2d(out, "out")
-    _here(a.data, b.data, out)
-    lib = load_library()
+        out = _empty((m, n), out_dtype or _torch.bfloat16, a.data.device, stream)
+        ldc = n
+    else:
+        if out.dim() != 2 or out.shape[0] != m or out.shape[1] != n or (out_dtype is not None and out.dtype != out_dtype):
+            raise ValueError(f"out: a matrix of shape {(m, n)} and the asked dtype is required")
+        ldc = _pitch(out, m, n, "out")
+    code = _code(out, "out")
+    dev = _here(a.data, b.data, out)
     ra, rb = ctypes.byref(a._desc), ctypes.byref(b._desc)
     need = ctypes.c_size_t()
-    _check(lib.muonh_block_matmul_workspace(ra, rb, ctypes.byref(need)), "muonh_block_matmul_workspace")
-    ws = _empty(need.value, torch.uint8, out.device, stream) if need.value else None
+    rc = _lib.muonh_block_matmul_workspace(ra, rb, ctypes.byref(need))
+    if rc:
+        _check(rc, "muonh_block_matmul_workspace")
+    need = need.value
+    ws = _empty(need, _torch.uint8, out.device, stream) if need else None
     if stream is not None:
         _record(stream, [a.data, a.scale, b.data, b.scale, out] + ([] if ws is None else [ws]))
-    _check(lib.muonh_block_matmul(ra, rb, out.data_ptr(), code, ldc, 1 if accumulate else 0,
-                                  None if ws is None else ws.data_ptr(), need.value, _stream_ptr(stream)),
-           "muonh_block_matmul")
+    rc = _lib.muonh_block_matmul(ra, rb, out.data_ptr(), code, ldc, 1 if accumulate else 0,
+                                 None if ws is None else ws.data_ptr(), need, _stream(stream, dev))
+    if rc:
+        _check(rc, "muonh_block_matmul")
     return out
 
 
 def _kind(kind: str) -> int:
-    try:
-        return NORM_KINDS[kind]
-    except KeyError:
-        raise ValueError("kind must be 'layer' or 'rms'") from None
+    code = NORM_KINDS.get(kind)
+    if code is None:
+        raise ValueError("kind must be 'layer' or 'rms'")
+    return code
 
 
-def _like(out, x, what: str, stream):
+def _like(out, x, rows: int, cols: int, what: str, stream):
+    """(out, its pitch): x's shape and dtype, new if out is None."""
     if out is None:
-        return _empty(x.shape, x.dtype, x.device, stream)
+        return _empty((rows, cols), x.dtype, x.device, stream), cols
     if out.shape != x.shape or out.dtype != x.dtype:
         raise ValueError(f"{what}: shape or dtype differs from x")
-    return out
+    return out, _pitch(out, rows, cols, what)
 
 
 def norm_forward(x, weight, bias=None, kind: str = "rms", eps: float = 1e-6, out=None, stream=None):
@@ -206,23 +250,25 @@ def norm_forward(x, weight, bias=None, kind: str = "rms", eps: float = 1e-6, out
     out          : y's memory; may be x itself
     mean is None for kind "rms".
     """
-    import torch
-    kind_code, code, ldx = _kind(kind), _code(x, "x"), _rows2d(x, "x")
-    rows, cols = x.shape
+    if _torch is None:
+        _setup()
+    kind_code, code = _kind(kind), _code(x, "x")
+    rows, cols, ldx = _matrix(x, "x")
     _vector(weight, cols, "weight")
     if bias is not None:
         _vector(bias, cols, "bias")
-    y = _like(out, x, "out", stream)
-    stats = _empty((2 if kind_code == 0 else 1, rows), torch.float32, x.device, stream)
-    rstd = stats[0]
-    mean = stats[1] if kind_code == 0 else None
-    _here(x, weight, bias, y)
+    dev = _here(x, weight, bias, out)
+    y, ldy = _like(out, x, rows, cols, "out", stream)
+    rstd = _empty(rows, _torch.float32, x.device, stream)
+    mean = None if kind_code else _empty(rows, _torch.float32, x.device, stream)
     args = muonh_norm_args(x.data_ptr(), weight.data_ptr(), None if bias is None else bias.data_ptr(),
                            y.data_ptr(), None if mean is None else mean.data_ptr(), rstd.data_ptr(), rows, cols,
-                           ldx, _rows2d(y, "out"), code, kind_code, eps, 0)
+                           ldx, ldy, code, kind_code, eps, 0)
     if stream is not None:
-        _record(stream, [x, weight, y, stats] + ([] if bias is None else [bias]))
-    _check(load_library().muonh_norm_forward(ctypes.byref(args), _stream_ptr(stream)), "muonh_norm_forward")
+        _record(stream, [t for t in (x, weight, bias, y, mean, rstd) if t is not None])
+    rc = _lib.muonh_norm_forward(ctypes.byref(args), _stream(stream, dev))
+    if rc:
+        _check(rc, "muonh_norm_forward")
     return y, mean, rstd
 
 
@@ -234,38 +280,44 @@ def norm_backward(dy, x, weight, mean, rstd, kind: str = "rms", bias: bool = Fal
     dx             : memory of dx; may be dy or x itself
     dweight, dbias : float32 [cols] to write, or with accumulate to add to
     """
-    import torch
-    kind_code, code, ldx = _kind(kind), _code(x, "x"), _rows2d(x, "x")
-    rows, cols = x.shape
+    if _torch is None:
+        _setup()
+    kind_code, code = _kind(kind), _code(x, "x")
+    rows, cols, ldx = _matrix(x, "x")
     if dy.shape != x.shape or dy.dtype != x.dtype:
         raise ValueError("dy: shape or dtype differs from x")
+    ld_dy = _pitch(dy, rows, cols, "dy")
     _vector(weight, cols, "weight")
     _vector(rstd, rows, "rstd")
     if (mean is None) != (kind_code == 1):
         raise ValueError("mean is the layer norm's, and None for kind 'rms'")
     if mean is not None:
         _vector(mean, rows, "mean")
-    dx = _like(dx, x, "dx", stream)
     if accumulate and (dweight is None or (bias and dbias is None)):
         raise ValueError("accumulate needs dweight (and dbias)")
-    if dweight is None:
-        dweight = _empty(cols, torch.float32, x.device, stream)
-    if bias and dbias is None:
-        dbias = _empty(cols, torch.float32, x.device, stream)
-    _vector(dweight, cols, "dweight")
+    if dweight is not None:
+        _vector(dweight, cols, "dweight")
     if dbias is not None:
         _vector(dbias, cols, "dbias")
-    _here(dy, x, weight, mean, rstd, dx, dweight, dbias)
-    lib = load_library()
+    dev = _here(dy, x, weight, mean, rstd, dx, dweight, dbias)
+    dx, ld_dx = _like(dx, x, rows, cols, "dx", stream)
+    if dweight is None:
+        dweight = _empty(cols, _torch.float32, x.device, stream)
+    if bias and dbias is None:
+        dbias = _empty(cols, _torch.float32, x.device, stream)
     need = ctypes.c_size_t()
-    _check(lib.muonh_norm_backward_workspace(rows, cols, ctypes.byref(need)), "muonh_norm_backward_workspace")
-    ws = _empty(max(need.value, 1), torch.uint8, x.device, stream)
+    rc = _lib.muonh_norm_backward_workspace(rows, cols, ctypes.byref(need))
+    if rc:
+        _check(rc, "muonh_norm_backward_workspace")
+    need = need.value
+    ws = _empty(need, _torch.uint8, x.device, stream) if need else None
     args = muonh_norm_grad_args(
         dy.data_ptr(), x.data_ptr(), weight.data_ptr(), None if mean is None else mean.data_ptr(), rstd.data_ptr(),
         dx.data_ptr(), dweight.data_ptr(), None if dbias is None else dbias.data_ptr(), rows, cols,
-        _rows2d(dy, "dy"), ldx, _rows2d(dx, "dx"), code, kind_code, 1 if accumulate else 0, 0, ws.data_ptr(),
-        need.value)
+        ld_dy, ldx, ld_dx, code, kind_code, 1 if accumulate else 0, 0, None if ws is None else ws.data_ptr(), need)
     if stream is not None:
         _record(stream, [t for t in (dy, x, weight, mean, rstd, dx, dweight, dbias, ws) if t is not None])
-    _check(lib.muonh_norm_backward(ctypes.byref(args), _stream_ptr(stream)), "muonh_norm_backward")
+    rc = _lib.muonh_norm_backward(ctypes.byref(args), _stream(stream, dev))
+    if rc:
+        _check(rc, "muonh_norm_backward")
     return dx, dweight, dbias
