@@ -29,155 +29,230 @@ typedef int i32x8_t __attribute__((ext_vector_type(8)));
 // ---------------------------------------------------------------------------
 // quantiser
 
-// Eight consecutive elements widened to fp32.  Rows may start at any element:
-// global loads of any width need no more than element alignment on gfx950.
-template <typename T> struct Load8;
-template <> struct Load8<uint16_t> {
+// Eight consecutive elements of a row in the type they are stored in.  Rows may
+// start at any element: global loads of any width need no more than element
+// alignment on gfx950.  kWords registers hold them; for bf16 a magnitude is 15
+// bits and two of them share a register.
+template <typename T> struct Row8;
+template <> struct Row8<uint16_t> {
+  static constexpr int kWords = 4;
+  static constexpr uint32_t kInf = 0x7f80u;      // magnitudes from here on are Inf or NaN
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
   typedef uint32_t vec __attribute__((ext_vector_type(4), aligned(2)));
-  static __device__ __forceinline__ void full(const uint16_t* p, float (&v)[8]) {
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const uint16_t* p) {
     const vec r = __builtin_nontemporal_load((const MUONH_GLOBAL vec*)p);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      v[2 * k] = __uint_as_float(r[k] << 16);
-      v[2 * k + 1] = __uint_as_float(r[k] & 0xffff0000u);
-    }
+    for (int k = 0; k < 4; ++k) w[k] = r[k];
   }
-  static __device__ __forceinline__ float one(const uint16_t* p) {
-    return bf16_to_f32(ld_global<uint16_t>(p));
+  __device__ __forceinline__ void set(int j, const uint16_t* p) {
+    w[j >> 1] |= (uint32_t)ld_global<uint16_t>(p) << (16 * (j & 1));
+  }
+  __device__ __forceinline__ float value(int j) const {
+    return __uint_as_float((j & 1) ? w[j >> 1] & 0xffff0000u : w[j >> 1] << 16);
+  }
+  __device__ __forceinline__ uint32_t magnitude(int k) const { return w[k] & 0x7fff7fffu; }
+  static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a),
+                                                                  __builtin_bit_cast(u16x2, b)));
+  }
+  // The larger half, and a magnitude as fp32 bits.
+  static __device__ __forceinline__ uint32_t fold(uint32_t m) { return max(m & 0xffffu, m >> 16); }
+  static __device__ __forceinline__ uint32_t bits(uint32_t m) { return m << 16; }
+  static __device__ __forceinline__ uint32_t column(const uint32_t (&m)[kWords], int j) {
+    return (j & 1) ? m[j >> 1] >> 16 : m[j >> 1] & 0xffffu;
+  }
+  // Magnitudes with Inf and NaN taken as zero.
+  static __device__ __forceinline__ uint32_t finite(uint32_t m) {
+    const uint32_t lo = m & 0xffffu, hi = m >> 16;
+    return (lo < kInf ? lo : 0u) | ((hi < kInf ? hi : 0u) << 16);
   }
 };
-template <> struct Load8<float> {
-  typedef float vec __attribute__((ext_vector_type(4), aligned(4)));
-  static __device__ __forceinline__ void full(const float* p, float (&v)[8]) {
+template <> struct Row8<float> {
+  static constexpr int kWords = 8;
+  static constexpr uint32_t kInf = 0x7f800000u;
+  typedef uint32_t vec __attribute__((ext_vector_type(4), aligned(4)));
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const float* p) {
     const vec lo = __builtin_nontemporal_load((const MUONH_GLOBAL vec*)p);
     const vec hi = __builtin_nontemporal_load((const MUONH_GLOBAL vec*)(p + 4));
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      v[k] = lo[k];
-      v[4 + k] = hi[k];
+      w[k] = lo[k];
+      w[4 + k] = hi[k];
     }
   }
-  static __device__ __forceinline__ float one(const float* p) { return ld_global<float>(p); }
+  __device__ __forceinline__ void set(int j, const float* p) { w[j] = __float_as_uint(ld_global<float>(p)); }
+  __device__ __forceinline__ float value(int j) const { return __uint_as_float(w[j]); }
+  __device__ __forceinline__ uint32_t magnitude(int k) const { return w[k] & 0x7fffffffu; }
+  static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return max(a, b); }
+  static __device__ __forceinline__ uint32_t fold(uint32_t m) { return m; }
+  static __device__ __forceinline__ uint32_t bits(uint32_t m) { return m; }
+  static __device__ __forceinline__ uint32_t column(const uint32_t (&m)[kWords], int j) { return m[j]; }
+  static __device__ __forceinline__ uint32_t finite(uint32_t m) { return m < kInf ? m : 0u; }
 };
-
-// |v| as an integer, 0 for NaN and Inf: the order of these integers is the
-// order of the magnitudes.
-__device__ __forceinline__ uint32_t finite_bits(float v) {
-  const uint32_t u = __float_as_uint(v) & 0x7fffffffu;
-  return u < 0x7f800000u ? u : 0u;
-}
 
 // The scale byte e + 127 of a block from its largest finite magnitude's bits:
 // with amax = (1 + f) 2^(E - 127) and 448 = 1.75 * 2^8, e = E - 135, one more
 // where 1 + f > 1.75.  Subnormal amax (E = 0) ends at the least byte.
 __device__ __forceinline__ uint32_t scale_byte(uint32_t amax) {
-  if (amax == 0) return 127;
   const int b = (int)(amax >> 23) - 8 + ((amax & 0x7fffffu) > 0x600000u);
-  return (uint32_t)max(b, 0);
+  return amax == 0 ? 127u : (uint32_t)max(b, 0);
 }
 
-// 2^-e from the scale byte (0 .. 247, so the result is a normal number).
-__device__ __forceinline__ float inverse_scale(uint32_t byte) {
-  return __uint_as_float((254u - byte) << 23);
-}
-
-__device__ __forceinline__ float scaled(float v, float inv) {
+// v * 2^-e as E4M3 where v may be Inf or NaN, which become NaN.
+__device__ __forceinline__ float scaled(float v, uint32_t byte) {
   const bool finite = (__float_as_uint(v) & 0x7f800000u) != 0x7f800000u;
-  return finite ? v * inv : __uint_as_float(0x7fc00000u);
+  // 2^-e; the byte is at most 247, so it is a normal number
+  return finite ? v * __uint_as_float((254u - byte) << 23) : __uint_as_float(0x7fc00000u);
 }
-
-// Four fp32 -> four E4M3 bytes (round to nearest even), lowest byte first.
 __device__ __forceinline__ uint32_t pack_fp8(float a, float b, float c, float d) {
   int r = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
   r = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
   return (uint32_t)r;
 }
 
-constexpr int kQuantThreads = 256;
-constexpr int kRowsPerThread = 8;
+typedef int16_t i16x2_t __attribute__((ext_vector_type(2)));
+
+// Four finite values divided by the scale's power of two and rounded to E4M3,
+// lowest byte first: two conversions that take the scale's exponent field.
+__device__ __forceinline__ uint32_t quantize4(float a, float b, float c, float d, float scale) {
+  i16x2_t r = {0, 0};
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, a, b, scale, false);
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, c, d, scale, true);
+  return __builtin_bit_cast(uint32_t, r);
+}
+__device__ __forceinline__ uint32_t quantize4(uint32_t ab, uint32_t cd, float scale) {
+  i16x2_t r = {0, 0};
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(bf16x2_t, ab), scale, false);
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(bf16x2_t, cd), scale, true);
+  return __builtin_bit_cast(uint32_t, r);
+}
+// Four consecutive elements of a row, and column j of four rows.
+__device__ __forceinline__ uint32_t quantize_row4(const Row8<uint16_t>& v, int h, float scale) {
+  return quantize4(v.w[2 * h], v.w[2 * h + 1], scale);
+}
+__device__ __forceinline__ uint32_t quantize_row4(const Row8<float>& v, int h, float scale) {
+  return quantize4(v.value(4 * h), v.value(4 * h + 1), v.value(4 * h + 2), v.value(4 * h + 3), scale);
+}
+__device__ __forceinline__ uint32_t quantize_col4(const Row8<uint16_t> (&v)[4], int j, float scale) {
+  const uint32_t sel = (j & 1) ? 0x07060302u : 0x05040100u;
+  return quantize4(__builtin_amdgcn_perm(v[1].w[j >> 1], v[0].w[j >> 1], sel),
+                   __builtin_amdgcn_perm(v[3].w[j >> 1], v[2].w[j >> 1], sel), scale);
+}
+__device__ __forceinline__ uint32_t quantize_col4(const Row8<float> (&v)[4], int j, float scale) {
+  return quantize4(v[0].value(j), v[1].value(j), v[2].value(j), v[3].value(j), scale);
+}
+
+// The largest value of each row of 16 lanes, in all of them (rotations).
+__device__ __forceinline__ uint32_t max16(uint32_t v) {
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xf, 0xf, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x124, 0xf, 0xf, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x122, 0xf, 0xf, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x121, 0xf, 0xf, false));
+  return v;
+}
+
+constexpr int kQuantThreads = 512;
+constexpr int kQuantWaves = kQuantThreads / 64;
+constexpr int kQuantRows = kFp8Tile * kFp8Tile / kQuantThreads / 8;   // rows per thread
+static_assert(kQuantRows == 4, "a thread's rows fill one 4-byte unit of the column form");
 
 // One 128 x 128 tile of x per workgroup.  Thread t holds columns 8 (t % 16) ..
-// + 7 of the eight rows 8 (t / 16) .. + 7, so a 16-lane group covers a row's
-// group of 128 and one thread holds 8 consecutive values of either axis: the
-// row form leaves as 8 bytes per row, the column form goes through LDS as one
-// 8-byte unit per column.  Elements behind the matrix count as zeros, and the
-// row form's padding up to a multiple of 128 is written as such.
+// + 7 of rows 4 (t / 16) .. + 3, so a 16-lane row covers a row's group of 128
+// and a thread holds 4 consecutive values of each of its columns: the row form
+// leaves as 8 bytes per row, the column form goes through LDS as one 4-byte
+// unit per column.  Elements behind the matrix count as zeros, and the padding
+// up to a multiple of 128 is written as such.
+//
+// Bound by HBM (one read, one write per form).  What a thread does per element
+// is kept to a mask, two packed maxima and a conversion per form that scales as
+// it converts; Inf and NaN take a path of their own, per thread.
 template <typename T, bool SQUARE>
 __global__ __launch_bounds__(kQuantThreads) void block_quantize_kernel(QuantArgs p, uint32_t ctiles) {
-  // Column form of the tile: row c is column c of x, 16 units of 8 rows; unit u
-  // of row c sits at u ^ ((c >> 3) & 15), which spreads one store's 16 columns
-  // (8 apart) over the banks.
+  typedef Row8<T> Row;
+  constexpr int W = Row::kWords;
+  // Column form of the tile: row c is column c of x, 32 units of 4 rows; unit u
+  // of row c sits at u ^ (2 ((c >> 3) & 15)), so that one store's 16 columns (8
+  // apart) and 4 units meet each bank twice, the least for 64 lanes.
   __shared__ __attribute__((aligned(16))) uint8_t tile[kFp8Tile * kFp8Tile];
-  __shared__ uint32_t colmax[4][kFp8Tile];
+  __shared__ __attribute__((aligned(16))) uint32_t colmax[kQuantWaves][16 * W];
 
   const uint32_t tr = blockIdx.x / ctiles, tc = blockIdx.x % ctiles;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int cg = tid & 15, rg = tid >> 4;
-  const int64_t r0 = (int64_t)tr * kFp8Tile + rg * 8, c0 = (int64_t)tc * kFp8Tile + cg * 8;
+  const int64_t r0 = (int64_t)tr * kFp8Tile + rg * 4, c0 = (int64_t)tc * kFp8Tile + cg * 8;
   const T* x = reinterpret_cast<const T*>(p.x);
 
-  float v[kRowsPerThread][8];
+  Row v[4];
 #pragma unroll
-  for (int i = 0; i < kRowsPerThread; ++i) {
+  for (int i = 0; i < 4; ++i) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+    for (int k = 0; k < W; ++k) v[i].w[k] = 0;
     if (r0 + i < p.rows) {
       const T* src = x + (r0 + i) * p.ldx + c0;
       if (c0 + 8 <= p.cols) {
-        Load8<T>::full(src, v[i]);
+        v[i].load(src);
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (c0 + j < p.cols) v[i][j] = Load8<T>::one(src + j);
+          if (c0 + j < p.cols) v[i].set(j, src + j);
       }
     }
   }
 
-  uint32_t rowmax[kRowsPerThread], cmax[8];
+  // Largest magnitudes of the thread's rows, and of its columns.
+  uint32_t rowmax[4], cmax[W];
+  auto maxima = [&](auto keep) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) cmax[j] = 0;
+    for (int k = 0; k < W; ++k) cmax[k] = 0;
 #pragma unroll
-  for (int i = 0; i < kRowsPerThread; ++i) {
-    rowmax[i] = 0;
+    for (int i = 0; i < 4; ++i) {
+      uint32_t m = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t u = finite_bits(v[i][j]);
-      rowmax[i] = max(rowmax[i], u);
-      cmax[j] = max(cmax[j], u);
+      for (int k = 0; k < W; ++k) {
+        const uint32_t a = keep(v[i].magnitude(k));
+        m = Row::larger(m, a);
+        cmax[k] = Row::larger(cmax[k], a);
+      }
+      rowmax[i] = Row::fold(m);
     }
-  }
+  };
+  maxima([](uint32_t m) { return m; });
+  const bool special = max(max(rowmax[0], rowmax[1]), max(rowmax[2], rowmax[3])) >= Row::kInf;
+  if (special) maxima([](uint32_t m) { return Row::finite(m); });
+
   uint32_t tile_byte = 0;
   if constexpr (SQUARE) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < kRowsPerThread; ++i) m = max(m, rowmax[i]);
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, off, 64));
-    if (lane == 0) colmax[0][wave] = m;
+    uint32_t m = max16(max(max(rowmax[0], rowmax[1]), max(rowmax[2], rowmax[3])));
+    m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
+    m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
+    if (lane == 0) colmax[wave][0] = m;
     __syncthreads();
-    m = max(max(colmax[0][0], colmax[0][1]), max(colmax[0][2], colmax[0][3]));
-    tile_byte = scale_byte(m);
+    m = 0;
+#pragma unroll
+    for (int w = 0; w < kQuantWaves; ++w) m = max(m, colmax[w][0]);
+    tile_byte = scale_byte(Row::bits(m));
   }
 
   if (p.q) {
-    if constexpr (!SQUARE) {
-#pragma unroll
-      for (int i = 0; i < kRowsPerThread; ++i)
-#pragma unroll
-        for (int off = 8; off > 0; off >>= 1)
-          rowmax[i] = max(rowmax[i], (uint32_t)__shfl_xor((int)rowmax[i], off, 64));
-    }
     // bytes of this tile's scale column, and zeros behind the last one
     const int64_t kb = (p.cols + kFp8Block - 1) / kFp8Block;
     const int nzero = (int64_t)tc == kb - 1 ? (int)((4 - (kb & 3)) & 3) : 0;
 #pragma unroll
-    for (int i = 0; i < kRowsPerThread; ++i) {
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t byte = SQUARE ? tile_byte : scale_byte(Row::bits(max16(rowmax[i])));
       if (r0 + i >= p.rows) continue;
-      const uint32_t byte = SQUARE ? tile_byte : scale_byte(rowmax[i]);
-      const float inv = inverse_scale(byte);
       u32x2_t o;
-      o[0] = pack_fp8(scaled(v[i][0], inv), scaled(v[i][1], inv), scaled(v[i][2], inv), scaled(v[i][3], inv));
-      o[1] = pack_fp8(scaled(v[i][4], inv), scaled(v[i][5], inv), scaled(v[i][6], inv), scaled(v[i][7], inv));
+      if (!special) {
+        const float scale = __uint_as_float(byte << 23);
+        o = u32x2_t{quantize_row4(v[i], 0, scale), quantize_row4(v[i], 1, scale)};
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          o[h] = pack_fp8(scaled(v[i].value(4 * h), byte), scaled(v[i].value(4 * h + 1), byte),
+                          scaled(v[i].value(4 * h + 2), byte), scaled(v[i].value(4 * h + 3), byte));
+      }
       st_global<u32x2_t>(p.q + (r0 + i) * p.ldq + c0, o);
       if (cg == 0 && (!SQUARE || (rg == 0 && i == 0))) {
         uint8_t* s = p.s + (SQUARE ? (int64_t)tr : r0 + i) * p.lds + tc;
@@ -188,57 +263,53 @@ __global__ __launch_bounds__(kQuantThreads) void block_quantize_kernel(QuantArgs
   }
 
   if (p.qt) {
-    float inv[8];
-    if constexpr (SQUARE) {
+    if constexpr (!SQUARE) {
+      // columns: over the wavefront's 4 groups of rows, then over the wavefronts
 #pragma unroll
-      for (int j = 0; j < 8; ++j) inv[j] = inverse_scale(tile_byte);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        cmax[j] = max(cmax[j], (uint32_t)__shfl_xor((int)cmax[j], 16, 64));
-        cmax[j] = max(cmax[j], (uint32_t)__shfl_xor((int)cmax[j], 32, 64));
+      for (int k = 0; k < W; ++k) {
+        cmax[k] = Row::larger(cmax[k], (uint32_t)__shfl_xor((int)cmax[k], 16, 64));
+        cmax[k] = Row::larger(cmax[k], (uint32_t)__shfl_xor((int)cmax[k], 32, 64));
       }
       if (lane < 16) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) colmax[wave][cg * 8 + j] = cmax[j];
+        for (int k = 0; k < W; ++k) colmax[wave][cg * W + k] = cmax[k];
       }
       __syncthreads();
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int c = cg * 8 + j;
-        inv[j] = inverse_scale(scale_byte(max(max(colmax[0][c], colmax[1][c]), max(colmax[2][c], colmax[3][c]))));
-      }
-    }
+      for (int w = 0; w < kQuantWaves; ++w)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      u32x2_t o;
-      o[0] = pack_fp8(scaled(v[0][j], inv[j]), scaled(v[1][j], inv[j]), scaled(v[2][j], inv[j]), scaled(v[3][j], inv[j]));
-      o[1] = pack_fp8(scaled(v[4][j], inv[j]), scaled(v[5][j], inv[j]), scaled(v[6][j], inv[j]), scaled(v[7][j], inv[j]));
-      const int c = cg * 8 + j;   // (c >> 3) & 15 == cg
-      *reinterpret_cast<u32x2_t*>(&tile[c * kFp8Tile + ((rg ^ cg) << 3)]) = o;
+        for (int k = 0; k < W; ++k) cmax[k] = Row::larger(cmax[k], colmax[w][cg * W + k]);
     }
     const int64_t kb = (p.rows + kFp8Block - 1) / kFp8Block;
     const int64_t cbase = (int64_t)tc * kFp8Tile;
-    if (tid < kFp8Tile && cbase + tid < p.cols && (!SQUARE || tid == 0)) {
-      const uint32_t byte = SQUARE ? tile_byte
-                                   : scale_byte(max(max(colmax[0][tid], colmax[1][tid]),
-                                                    max(colmax[2][tid], colmax[3][tid])));
-      uint8_t* s = p.st + (SQUARE ? (int64_t)tc : cbase + tid) * p.ldst + tr;
-      st_global<uint8_t>(s, (uint8_t)byte);
-      const int nzero = (int64_t)tr == kb - 1 ? (int)((4 - (kb & 3)) & 3) : 0;
-      for (int z = 1; z <= nzero; ++z) st_global<uint8_t>(s + z, (uint8_t)0);
+    const int nzero = (int64_t)tr == kb - 1 ? (int)((4 - (kb & 3)) & 3) : 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t byte = SQUARE ? tile_byte : scale_byte(Row::bits(Row::column(cmax, j)));
+      uint32_t o;
+      if (!special)
+        o = quantize_col4(v, j, __uint_as_float(byte << 23));
+      else
+        o = pack_fp8(scaled(v[0].value(j), byte), scaled(v[1].value(j), byte), scaled(v[2].value(j), byte),
+                     scaled(v[3].value(j), byte));
+      const int c = cg * 8 + j;   // (c >> 3) & 15 == cg
+      *reinterpret_cast<uint32_t*>(&tile[c * kFp8Tile + ((rg ^ (2 * cg)) << 2)]) = o;
+      if (rg == 0 && (SQUARE ? c == 0 : cbase + c < p.cols)) {
+        uint8_t* s = p.st + (SQUARE ? (int64_t)tc : cbase + c) * p.ldst + tr;
+        st_global<uint8_t>(s, (uint8_t)byte);
+        for (int z = 1; z <= nzero; ++z) st_global<uint8_t>(s + z, (uint8_t)0);
+      }
     }
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < kFp8Tile * kFp8Tile / 16 / kQuantThreads; ++k) {
       const int idx = k * kQuantThreads + tid;
-      const int c = idx >> 3, u = (idx & 7) * 2;
+      const int c = idx >> 3, ch = idx & 7, g = (c >> 3) & 15;
       if (cbase + c >= p.cols) continue;
-      const int sw = (c >> 3) & 15;
-      const u32x2_t lo = *reinterpret_cast<const u32x2_t*>(&tile[c * kFp8Tile + ((u ^ sw) << 3)]);
-      const u32x2_t hi = *reinterpret_cast<const u32x2_t*>(&tile[c * kFp8Tile + (((u + 1) ^ sw) << 3)]);
-      st_global<u32x4_t>(p.qt + (cbase + c) * p.ldqt + (int64_t)tr * kFp8Tile + u * 8,
-                         u32x4_t{lo[0], lo[1], hi[0], hi[1]});
+      // units 4 ch .. + 3: chunk ch ^ (g / 2), its halves swapped where g is odd
+      const u32x4_t r = *reinterpret_cast<const u32x4_t*>(&tile[c * kFp8Tile + ((ch ^ (g >> 1)) << 4)]);
+      st_global<u32x4_t>(p.qt + (cbase + c) * p.ldqt + (int64_t)tr * kFp8Tile + ch * 16,
+                         (g & 1) ? u32x4_t{r[2], r[3], r[0], r[1]} : r);
     }
   }
 }
@@ -294,17 +365,16 @@ __device__ __forceinline__ void store_c(C* c, int64_t off, int left, const f32x4
   }
 }
 
-constexpr int kThinThreads = 256;
-
-// 16 x 16 outputs per workgroup, its four wavefronts splitting the blocks of
-// the contraction.  One 16x16x128 scaled MFMA takes exactly one block of 128;
+// 16 x 16 outputs per workgroup, its WAVES wavefronts splitting the blocks of
+// the contraction (a column of one token reads 16 rows of B: only many loads
+// in flight per CU reach HBM's rate).  One 16x16x128 scaled MFMA takes exactly one block of 128;
 // every lane of a row carries the row's own scale byte and both operands are
 // laid out alike, so the K order inside an instruction does not matter.
 // The operands are swapped (B first): lane l then holds columns 4 (l / 16) ..
 // + 3 of row l % 16.  Rows behind the end read the last one and are dropped.
-template <typename C, bool ACC>
-__global__ __launch_bounds__(kThinThreads) void block_matmul_thin_kernel(BlockMatmulArgs p, uint32_t ntiles) {
-  __shared__ f32x4_t part[4][64];
+template <typename C, bool ACC, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void block_matmul_thin_kernel(BlockMatmulArgs p, uint32_t ntiles) {
+  __shared__ f32x4_t part[WAVES][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int m0 = (int)(blockIdx.x / ntiles) * 16, n0 = (int)(blockIdx.x % ntiles) * 16;
   const int m = min(m0 + (lane & 15), p.m - 1), n = min(n0 + (lane & 15), p.n - 1);
@@ -313,7 +383,8 @@ __global__ __launch_bounds__(kThinThreads) void block_matmul_thin_kernel(BlockMa
   const uint8_t* sa = p.sa + (int64_t)(m >> p.a_shift) * p.ldsa;
   const uint8_t* sb = p.sb + (int64_t)(n >> p.b_shift) * p.ldsb;
   f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int k = wave; k < p.kblocks; k += 4) {
+#pragma unroll 4
+  for (int k = wave; k < p.kblocks; k += WAVES) {
     const u32x4_t a0 = ld_global<u32x4_t>(a + (int64_t)k * 128), a1 = ld_global<u32x4_t>(a + (int64_t)k * 128 + 16);
     const u32x4_t b0 = ld_global<u32x4_t>(b + (int64_t)k * 128), b1 = ld_global<u32x4_t>(b + (int64_t)k * 128 + 16);
     const uint32_t ea = ld_global<uint8_t>(sa + k), eb = ld_global<uint8_t>(sb + k);
@@ -342,7 +413,9 @@ __global__ __launch_bounds__(kThinThreads) void block_matmul_thin_kernel(BlockMa
   part[wave][lane] = acc;
   __syncthreads();
   if (wave != 0) return;
-  const f32x4_t s = (part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]);
+  f32x4_t s = part[0][lane];
+#pragma unroll
+  for (int w = 1; w < WAVES; ++w) s += part[w][lane];
   const int row = m0 + (lane & 15), col = n0 + (lane >> 4) * 4;
   if (row >= p.m || col >= p.n) return;
   store_c<C, ACC>(reinterpret_cast<C*>(p.c), (int64_t)row * p.ldc + col, p.n - col, s);
@@ -670,7 +743,10 @@ hipError_t matmul_for(const BlockMatmulArgs& a, hipStream_t st) {
   }
   const unsigned ntiles = (unsigned)((a.n + 15) / 16);
   const dim3 grid(ntiles * (unsigned)((a.m + 15) / 16));
-  hipLaunchKernelGGL((block_matmul_thin_kernel<C, ACC>), grid, dim3(kThinThreads), 0, st, a, ntiles);
+  if (a.kblocks >= 16)
+    hipLaunchKernelGGL((block_matmul_thin_kernel<C, ACC, 16>), grid, dim3(1024), 0, st, a, ntiles);
+  else
+    hipLaunchKernelGGL((block_matmul_thin_kernel<C, ACC, 4>), grid, dim3(256), 0, st, a, ntiles);
   return hipGetLastError();
 }
 

@@ -22,20 +22,30 @@ namespace muonh {
 namespace {
 
 constexpr int kNormThreads = 256;
-// Workgroups of a backward pass: each adds its rows' dy h in registers and
-// leaves one row of partial sums, which a second launch adds in order.
-constexpr int kNormGroups = 512;
+// Workgroups of a backward pass, one per CU: each adds its rows' dy h in
+// registers and leaves one row of partial sums, which a second launch adds in
+// order.
+constexpr int kNormGroups = 256;
+constexpr int kBackThreads = 512;
 
-// Eight consecutive elements <-> fp32, from any element alignment.
-template <typename T> struct Vec8;
-template <> struct Vec8<uint16_t> {
+// Eight consecutive elements of a row as stored, from any element alignment
+// (global accesses of any width need no more on gfx950), and as fp32.
+template <typename T> struct Raw8;
+template <> struct Raw8<uint16_t> {
   typedef uint32_t vec __attribute__((ext_vector_type(4), aligned(2)));
-  static __device__ __forceinline__ void load(const uint16_t* p, float (&v)[8]) {
-    const vec r = __builtin_nontemporal_load((const MUONH_GLOBAL vec*)p);
+  vec w;
+  __device__ __forceinline__ void load(const uint16_t* p) {
+    w = __builtin_nontemporal_load((const MUONH_GLOBAL vec*)p);
+  }
+  __device__ __forceinline__ void zero() { w = vec{0, 0, 0, 0}; }
+  __device__ __forceinline__ void set(int j, const uint16_t* p) {
+    w[j >> 1] |= (uint32_t)ld_global<uint16_t>(p) << (16 * (j & 1));
+  }
+  __device__ __forceinline__ void widen(float (&v)[8]) const {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      v[2 * k] = __uint_as_float(r[k] << 16);
-      v[2 * k + 1] = __uint_as_float(r[k] & 0xffff0000u);
+      v[2 * k] = __uint_as_float(w[k] << 16);
+      v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
     }
   }
   static __device__ __forceinline__ float load1(const uint16_t* p) { return bf16_to_f32(ld_global<uint16_t>(p)); }
@@ -47,11 +57,20 @@ template <> struct Vec8<uint16_t> {
   }
   static __device__ __forceinline__ void store1(uint16_t* p, float v) { st_global<uint16_t>(p, f32_to_bf16(v)); }
 };
-template <> struct Vec8<float> {
+template <> struct Raw8<float> {
   typedef float vec __attribute__((ext_vector_type(4), aligned(4)));
-  static __device__ __forceinline__ void load(const float* p, float (&v)[8]) {
-    const vec lo = __builtin_nontemporal_load((const MUONH_GLOBAL vec*)p);
-    const vec hi = __builtin_nontemporal_load((const MUONH_GLOBAL vec*)(p + 4));
+  vec lo, hi;
+  __device__ __forceinline__ void load(const float* p) {
+    lo = __builtin_nontemporal_load((const MUONH_GLOBAL vec*)p);
+    hi = __builtin_nontemporal_load((const MUONH_GLOBAL vec*)(p + 4));
+  }
+  __device__ __forceinline__ void zero() { lo = hi = vec{0.0f, 0.0f, 0.0f, 0.0f}; }
+  __device__ __forceinline__ void set(int j, const float* p) {
+    const float v = ld_global<float>(p);
+    if (j < 4) lo[j] = v;
+    else hi[j - 4] = v;
+  }
+  __device__ __forceinline__ void widen(float (&v)[8]) const {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       v[k] = lo[k];
@@ -68,22 +87,26 @@ template <> struct Vec8<float> {
 
 // Elements [c, c + 8) of a row of n, zeros behind its end.
 template <typename T>
-__device__ __forceinline__ void load8(const T* row, int c, int n, float (&v)[8]) {
+__device__ __forceinline__ Raw8<T> load8(const T* row, int c, int n) {
+  Raw8<T> r;
   if (c + 8 <= n) {
-    Vec8<T>::load(row + c, v);
+    r.load(row + c);
   } else {
+    r.zero();
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = c + j < n ? Vec8<T>::load1(row + c + j) : 0.0f;
+    for (int j = 0; j < 8; ++j)
+      if (c + j < n) r.set(j, row + c + j);
   }
+  return r;
 }
 template <typename T>
 __device__ __forceinline__ void store8(T* row, int c, int n, const float (&v)[8]) {
   if (c + 8 <= n) {
-    Vec8<T>::store(row + c, v);
+    Raw8<T>::store(row + c, v);
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (c + j < n) Vec8<T>::store1(row + c + j, v[j]);
+      if (c + j < n) Raw8<T>::store1(row + c + j, v[j]);
   }
 }
 // A weight or bias vector: read by every row, so through the caches.
@@ -104,7 +127,7 @@ __device__ __forceinline__ void loadw(const float* w, int c, int n, float (&v)[8
 
 // Sums of NS values over the G threads of a row, the same in each of them: a
 // shuffle tree inside a wavefront, and the wavefronts' sums in order through
-// LDS for longer groups (which then are the whole workgroup).
+// LDS for longer groups (every thread of the workgroup then takes part).
 template <int G, int NS>
 __device__ __forceinline__ void group_sum(float (&s)[NS], float (*red)[16]) {
 #pragma unroll
@@ -118,11 +141,12 @@ __device__ __forceinline__ void group_sum(float (&s)[NS], float (*red)[16]) {
       for (int k = 0; k < NS; ++k) red[k][threadIdx.x >> 6] = s[k];
     }
     __syncthreads();
+    const int w0 = (threadIdx.x / G) * (G / 64);
 #pragma unroll
     for (int k = 0; k < NS; ++k) {
       s[k] = 0.0f;
 #pragma unroll
-      for (int w = 0; w < G / 64; ++w) s[k] += red[k][w];
+      for (int w = 0; w < G / 64; ++w) s[k] += red[k][w0 + w];
     }
   }
 }
@@ -144,7 +168,7 @@ __global__ __launch_bounds__(G > kNormThreads ? G : kNormThreads) void norm_forw
     const T* x = reinterpret_cast<const T*>(p.x) + (live ? row : p.rows - 1) * p.ldx;
     float v[NV][8];
 #pragma unroll
-    for (int k = 0; k < NV; ++k) load8<T>(x, 8 * (t + G * k), cols, v[k]);
+    for (int k = 0; k < NV; ++k) load8<T>(x, 8 * (t + G * k), cols).widen(v[k]);
     float mu = 0.0f;
     if constexpr (LAYER) {
       float s[1] = {0.0f};
@@ -203,13 +227,13 @@ __global__ __launch_bounds__(kLongThreads) void norm_forward_long_kernel(NormArg
     float mu = 0.0f;
     if constexpr (LAYER) {
       float s[1] = {0.0f};
-      for (int64_t c = threadIdx.x; c < p.cols; c += kLongThreads) s[0] += Vec8<T>::load1(x + c);
+      for (int64_t c = threadIdx.x; c < p.cols; c += kLongThreads) s[0] += Raw8<T>::load1(x + c);
       group_sum<kLongThreads, 1>(s, red);
       mu = (float)((double)s[0] * rn);
     }
     float ss[1] = {0.0f};
     for (int64_t c = threadIdx.x; c < p.cols; c += kLongThreads) {
-      const float d = Vec8<T>::load1(x + c) - mu;
+      const float d = Raw8<T>::load1(x + c) - mu;
       ss[0] += d * d;
     }
     group_sum<kLongThreads, 1>(ss, red);
@@ -219,9 +243,9 @@ __global__ __launch_bounds__(kLongThreads) void norm_forward_long_kernel(NormArg
       p.rstd[row] = r;
     }
     for (int64_t c = threadIdx.x; c < p.cols; c += kLongThreads) {
-      float v = (Vec8<T>::load1(x + c) - mu) * r * p.weight[c];
+      float v = (Raw8<T>::load1(x + c) - mu) * r * p.weight[c];
       if (p.bias) v += p.bias[c];
-      Vec8<T>::store1(y + c, v);
+      Raw8<T>::store1(y + c, v);
     }
   }
 }
@@ -231,37 +255,61 @@ __global__ __launch_bounds__(kLongThreads) void norm_forward_long_kernel(NormArg
 // (and dy) for them in registers.  At the end the groups of one workgroup are
 // added in order through LDS, and the workgroup writes one row of partials.
 template <typename T, bool LAYER, bool BIAS, int G, int NV>
-__global__ __launch_bounds__(G > kNormThreads ? G : kNormThreads) void norm_backward_kernel(NormGradArgs p) {
-  constexpr int kThreads = G > kNormThreads ? G : kNormThreads;
+__global__ __launch_bounds__(G > kBackThreads ? G : kBackThreads) void norm_backward_kernel(NormGradArgs p) {
+  constexpr int kThreads = G > kBackThreads ? G : kBackThreads;
   constexpr int kRows = kThreads / G;
   constexpr int kAcc = BIAS ? 2 : 1;
   __shared__ float red[2][16];
   __shared__ float fold[kRows > 1 ? kThreads * 8 : 1];
   const int t = threadIdx.x % G, grp = threadIdx.x / G, cols = (int)p.cols;
   const float rn = 1.0f / (float)cols;
+  const int64_t step = (int64_t)gridDim.x * kRows;
+  // The next trip's rows are on their way while this one's are used, and the
+  // weight stays in registers; 1024 threads have no room for either.
+  constexpr bool kAhead = kThreads < 1024;
+  Raw8<T> nx[NV], nd[NV];
+  float nr = 0.0f, nmu = 0.0f;
+  auto fetch = [&](int64_t r0) {
+    const int64_t at = min(r0 + grp, p.rows - 1);
+    const T* x = reinterpret_cast<const T*>(p.x) + at * p.ldx;
+    const T* dy = reinterpret_cast<const T*>(p.dy) + at * p.lddy;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      nx[k] = load8<T>(x, 8 * (t + G * k), cols);
+      nd[k] = load8<T>(dy, 8 * (t + G * k), cols);
+    }
+    nr = p.rstd[at];
+    if constexpr (LAYER) nmu = p.mean[at];
+  };
+  int64_t r0 = (int64_t)blockIdx.x * kRows;
+  if constexpr (kAhead) fetch(r0);
   float w[NV][8], acc[kAcc][NV][8];
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    loadw(p.weight, 8 * (t + G * k), cols, w[k]);
+    if constexpr (kAhead) loadw(p.weight, 8 * (t + G * k), cols, w[k]);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       acc[0][k][j] = 0.0f;
       if constexpr (BIAS) acc[1][k][j] = 0.0f;
     }
   }
-  for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < p.rows; r0 += (int64_t)gridDim.x * kRows) {
+  for (; r0 < p.rows; r0 += step) {
+    if constexpr (!kAhead) {
+      fetch(r0);
+#pragma unroll
+      for (int k = 0; k < NV; ++k) loadw(p.weight, 8 * (t + G * k), cols, w[k]);
+    }
     const int64_t row = r0 + grp;
     const bool live = row < p.rows;
-    const int64_t at = live ? row : p.rows - 1;
-    const T* x = reinterpret_cast<const T*>(p.x) + at * p.ldx;
-    const T* dy = reinterpret_cast<const T*>(p.dy) + at * p.lddy;
-    const float r = p.rstd[at];
-    const float mu = LAYER ? p.mean[at] : 0.0f;
+    const float r = nr, mu = nmu;
     float h[NV][8], g[NV][8];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      load8<T>(x, 8 * (t + G * k), cols, h[k]);
-      load8<T>(dy, 8 * (t + G * k), cols, g[k]);
+      nx[k].widen(h[k]);
+      nd[k].widen(g[k]);
+    }
+    if constexpr (kAhead) {
+      if (r0 + step < p.rows) fetch(r0 + step);
     }
     float s[2] = {0.0f, 0.0f};
 #pragma unroll
@@ -338,7 +386,7 @@ __global__ __launch_bounds__(kLongThreads) void norm_backward_long_kernel(NormGr
     const float r = p.rstd[row], mu = LAYER ? p.mean[row] : 0.0f;
     float s[2] = {0.0f, 0.0f};
     for (int64_t c = threadIdx.x; c < p.cols; c += kLongThreads) {
-      const float h = (Vec8<T>::load1(x + c) - mu) * r, d = Vec8<T>::load1(dy + c);
+      const float h = (Raw8<T>::load1(x + c) - mu) * r, d = Raw8<T>::load1(dy + c);
       pw[c] = (first ? 0.0f : pw[c]) + d * h;
       if constexpr (BIAS) pb[c] = (first ? 0.0f : pb[c]) + d;
       const float g = d * p.weight[c];
@@ -349,39 +397,47 @@ __global__ __launch_bounds__(kLongThreads) void norm_backward_long_kernel(NormGr
     group_sum<kLongThreads, 2>(s, red);
     const float c1 = (float)((double)s[0] * rn), c0 = LAYER ? (float)((double)s[1] * rn) : 0.0f;
     for (int64_t c = threadIdx.x; c < p.cols; c += kLongThreads) {
-      const float h = (Vec8<T>::load1(x + c) - mu) * r;
-      const float g = Vec8<T>::load1(dy + c) * p.weight[c];
-      Vec8<T>::store1(dx + c, r * (g - c0 - h * c1));
+      const float h = (Raw8<T>::load1(x + c) - mu) * r;
+      const float g = Raw8<T>::load1(dy + c) * p.weight[c];
+      Raw8<T>::store1(dx + c, r * (g - c0 - h * c1));
     }
   }
 }
 
-// dw (and db, blockIdx.y = 1) from the partial rows: 16 columns per workgroup,
-// 16 threads per column each adding every 16th row, then a tree in LDS.
-__global__ __launch_bounds__(256) void norm_fold_kernel(const float* __restrict__ partials, int64_t nrows,
-                                                        int64_t cols, float* dweight, float* dbias,
-                                                        int accumulate) {
-  __shared__ float red[16][17];
+// dw (and db, blockIdx.y = 1) from the partial rows: 16 columns per workgroup
+// and 32 threads per column, each adding every 32nd row, then in order in LDS.
+constexpr int kFoldThreads = 512;
+__global__ __launch_bounds__(kFoldThreads) void norm_fold_kernel(const float* __restrict__ partials, int64_t nrows,
+                                                                 int64_t cols, float* dweight, float* dbias,
+                                                                 int accumulate) {
+  __shared__ float red[32][17];
   const int lc = threadIdx.x & 15, lr = threadIdx.x >> 4;
   const int64_t c = (int64_t)blockIdx.x * 16 + lc;
   const float* p = partials + (blockIdx.y ? nrows * cols : 0);
   float s = 0.0f;
-  if (c < cols)
-    for (int64_t r = lr; r < nrows; r += 16) s += p[r * cols + c];
+  if (c < cols) {
+    float v[kNormGroups / 32];
+#pragma unroll
+    for (int k = 0; k < kNormGroups / 32; ++k) v[k] = lr + 32 * k < nrows ? p[(lr + 32 * k) * cols + c] : 0.0f;
+#pragma unroll
+    for (int k = 0; k < kNormGroups / 32; ++k) s += v[k];
+  }
   red[lr][lc] = s;
   __syncthreads();
   if (threadIdx.x >= 16 || c >= cols) return;
 #pragma unroll
-  for (int k = 1; k < 16; ++k) s += red[k][lc];
+  for (int k = 1; k < 32; ++k) s += red[k][lc];
   float* out = blockIdx.y ? dbias : dweight;
   out[c] = accumulate ? out[c] + s : s;
 }
 
 constexpr int64_t kRegisterCols = 16384;   // 1024 threads of 16 elements
 
-// Rows that a workgroup takes at a time (the kernels' kRows).
-int64_t rows_at_once(int64_t cols) {
-  return cols <= 128 ? 16 : cols <= 256 ? 8 : cols <= 2048 ? 4 : 1;
+// Rows that a workgroup of `threads` takes at a time (the kernels' kRows).
+int64_t rows_at_once(int64_t cols, int64_t threads) {
+  const int64_t group = cols <= 128 ? 16 : cols <= 256 ? 32 : cols <= 1024 ? 64 : cols <= 2048 ? 128
+                        : cols <= 4096 ? 256 : cols <= 8192 ? 512 : 1024;
+  return std::max<int64_t>(threads / group, 1);
 }
 
 template <typename T, bool LAYER>
@@ -392,7 +448,7 @@ hipError_t forward_for(const NormArgs& a, hipStream_t st) {
                        dim3(kLongThreads), 0, st, a);
     return hipGetLastError();
   }
-  const int64_t per = rows_at_once(cols);
+  const int64_t per = rows_at_once(cols, kNormThreads);
   const dim3 grid((unsigned)std::min<int64_t>((a.rows + per - 1) / per, 1 << 20));
 #define MUONH_NORM_FWD(G, NV)                                                                  \
   hipLaunchKernelGGL((norm_forward_kernel<T, LAYER, G, NV>), grid,                             \
@@ -401,9 +457,9 @@ hipError_t forward_for(const NormArgs& a, hipStream_t st) {
   else if (cols <= 256) MUONH_NORM_FWD(32, 1);
   else if (cols <= 512) MUONH_NORM_FWD(64, 1);
   else if (cols <= 1024) MUONH_NORM_FWD(64, 2);
-  else if (cols <= 2048) MUONH_NORM_FWD(64, 4);
+  else if (cols <= 2048) MUONH_NORM_FWD(128, 2);
   else if (cols <= 4096) MUONH_NORM_FWD(256, 2);
-  else if (cols <= 8192) MUONH_NORM_FWD(1024, 1);
+  else if (cols <= 8192) MUONH_NORM_FWD(512, 2);
   else MUONH_NORM_FWD(1024, 2);
 #undef MUONH_NORM_FWD
   return hipGetLastError();
@@ -416,22 +472,23 @@ hipError_t backward_for(const NormGradArgs& a, hipStream_t st) {
     const dim3 grid((unsigned)groups);
 #define MUONH_NORM_BWD(G, NV)                                                                  \
   hipLaunchKernelGGL((norm_backward_kernel<T, LAYER, BIAS, G, NV>), grid,                      \
-                     dim3(G > kNormThreads ? G : kNormThreads), 0, st, a)
+                     dim3(G > kBackThreads ? G : kBackThreads), 0, st, a)
     if (cols > kRegisterCols)
       hipLaunchKernelGGL((norm_backward_long_kernel<T, LAYER, BIAS>), grid, dim3(kLongThreads), 0, st, a);
     else if (cols <= 128) MUONH_NORM_BWD(16, 1);
     else if (cols <= 256) MUONH_NORM_BWD(32, 1);
     else if (cols <= 512) MUONH_NORM_BWD(64, 1);
     else if (cols <= 1024) MUONH_NORM_BWD(64, 2);
-    else if (cols <= 2048) MUONH_NORM_BWD(64, 4);
+    else if (cols <= 2048) MUONH_NORM_BWD(128, 2);
     else if (cols <= 4096) MUONH_NORM_BWD(256, 2);
-    else if (cols <= 8192) MUONH_NORM_BWD(1024, 1);
+    else if (cols <= 8192) MUONH_NORM_BWD(512, 2);
     else MUONH_NORM_BWD(1024, 2);
 #undef MUONH_NORM_BWD
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(norm_fold_kernel, dim3((unsigned)((cols + 15) / 16), BIAS ? 2 : 1), dim3(256), 0, st,
+  hipLaunchKernelGGL(norm_fold_kernel, dim3((unsigned)((cols + 15) / 16), BIAS ? 2 : 1), dim3(kFoldThreads), 0,
+                     st,
                      a.partials, groups, cols, a.dweight, a.dbias, a.accumulate);
   return hipGetLastError();
 }
@@ -439,7 +496,7 @@ hipError_t backward_for(const NormGradArgs& a, hipStream_t st) {
 }  // namespace
 
 int64_t norm_partial_rows(int64_t rows, int64_t cols) {
-  const int64_t per = cols > kRegisterCols ? 1 : rows_at_once(cols);
+  const int64_t per = cols > kRegisterCols ? 1 : rows_at_once(cols, kBackThreads);
   return std::min<int64_t>((rows + per - 1) / per, kNormGroups);
 }
 
