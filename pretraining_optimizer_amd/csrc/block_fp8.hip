@@ -436,20 +436,19 @@ __device__ __forceinline__ void lds_barrier() {
 template <int VM>
 __device__ __forceinline__ void wait_loads() {
   static_assert(VM >= 0 && VM < 64, "vmcnt is 6 bits");
+  asm volatile("" ::: "memory");
   __builtin_amdgcn_s_waitcnt((VM & 15) | ((VM >> 4) << 14) | (7 << 4) | (0 << 8));
   asm volatile("" ::: "memory");
 }
 
 constexpr int kBufferConfig = 0x00020000;   // raw, unformatted buffer access
-constexpr int kSgValu = 0x002, kSgMfma = 0x008, kSgVmemRead = 0x020, kSgDsRead = 0x100;
+constexpr int kSgMfma = 0x008, kSgVmemRead = 0x020, kSgDsRead = 0x100;
 #define MUONH_SG(mask, n) __builtin_amdgcn_sched_group_barrier((mask), (n), 0)
 
 constexpr int kTileThreads = 256;
-constexpr int kStageK = 64;   // bytes of the contraction per stage and operand row
-
-// 16-byte chunk c of LDS row r (4 chunks) sits at c ^ swz64(r): the rows of a
+// 16-byte chunk c of a 128-byte LDS row r sits at c ^ swz128(r): the rows of a
 // fragment read then differ in banks whether 8 or 16 lanes are served at once.
-__device__ __forceinline__ int swz64(int r) { return ((r >> 1) & 3) ^ ((r >> 3) & 1); }
+__device__ __forceinline__ int swz128(int r) { return (r & 7) ^ ((r >> 3) & 1); }
 
 // Tile of workgroup b: the hardware deals workgroups to the 8 XCDs in turn, so
 // XCD x gets a contiguous share of the tile list, and the list walks groups of
@@ -465,24 +464,23 @@ __device__ __forceinline__ void tile_of(uint32_t b, uint32_t mt, uint32_t nt, ui
 }
 
 // C tile of (64 MB)^2 per workgroup of 4 wavefronts (2 x 2, each MB x MB MFMA
-// blocks of 32 x 32).  Stages of 64 bytes of K go straight from global memory
-// into a ring of 4 LDS slots; each slot is a variable of its own, so that the
-// compiler makes a fragment read wait for the loads into its own slot only.
-// In iteration t a wavefront multiplies stage t's fragments, reads those of
-// stage t + 1 and issues the loads of stage t + 4 into the slot that stage t
-// has left; one barrier per iteration, before these.
+// blocks of 32 x 32).  Blocks of 128 bytes of K, whole 128-byte lines of every
+// row, go straight from global memory into one of two LDS slots; each slot is a
+// variable of its own, so that the compiler makes a fragment read wait for the
+// loads into its own slot only.  A block is multiplied in two halves.  During
+// the first the wavefront reads the second's fragments; then comes the block's
+// one barrier, after which its slot is free and the next block's data are in
+// the other; during the second half the next block's first fragments are read
+// and the block after it is loaded.
 template <typename C, bool ACC, int MB>
 __global__ __launch_bounds__(kTileThreads) void block_matmul_tile_kernel(BlockMatmulArgs p, uint32_t mt,
                                                                          uint32_t nt) {
   constexpr int kTile = 64 * MB;
-  constexpr int kOperand = kTile * kStageK;
+  constexpr int kOperand = kTile * kFp8Block;
   constexpr int kSlot = 2 * kOperand;
-  constexpr int kLoads = 2 * MB;        // per wavefront and stage
   constexpr bool kFp8 = sizeof(C) == 2;
   __shared__ __attribute__((aligned(16))) uint8_t slot0[kSlot];
   __shared__ __attribute__((aligned(16))) uint8_t slot1[kSlot];
-  __shared__ __attribute__((aligned(16))) uint8_t slot2[kSlot];
-  __shared__ __attribute__((aligned(16))) uint8_t slot3[kSlot];
 
   uint32_t tm, tn;
   tile_of(blockIdx.x, mt, nt, tm, tn);
@@ -499,50 +497,57 @@ __global__ __launch_bounds__(kTileThreads) void block_matmul_tile_kernel(BlockMa
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
 
-  // Loads: instruction i of a wavefront fills rows 16 (MB wave + i) .. + 15 of
-  // an operand; lane l lands in row l / 4, slot chunk l % 4.  Rows behind the
-  // matrix and stages behind the last are out of the descriptor's range: they
-  // make no memory access.  (The host keeps 256 rows below 2^31 bytes.)
+  // Loads: instruction i of a wavefront fills rows 16 MB wave + 8 i .. + 7 of an
+  // operand; lane l lands in row l / 8, slot chunk l % 8.  Rows behind the
+  // matrix and blocks behind the last are out of the descriptor's range: they
+  // make no memory access and leave zeros.  (The host keeps 256 rows below 2^31
+  // bytes.)
   const uint8_t* abase = p.a + (int64_t)row0 * p.lda;
   const uint8_t* bbase = p.b + (int64_t)col0 * p.ldb;
   const int arange = (int)(min(kTile, p.m - row0) * p.lda), brange = (int)(min(kTile, p.n - col0) * p.ldb);
-  const int lrow = lane >> 2, lchunk = (lane & 3) ^ swz64(lrow);
-  const int avoff = (int)((wave * MB * 16 + lrow) * p.lda) + lchunk * 16;
-  const int bvoff = (int)((wave * MB * 16 + lrow) * p.ldb) + lchunk * 16;
-  const int nh = 2 * p.kblocks;
-  auto load_stage = [&](uint8_t (&slot)[kSlot], int t) {
-    const __amdgpu_buffer_rsrc_t ra =
-        __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(abase), (short)0, t < nh ? arange : 0, kBufferConfig);
-    const __amdgpu_buffer_rsrc_t rb =
-        __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(bbase), (short)0, t < nh ? brange : 0, kBufferConfig);
-    MUONH_LDS uint8_t* d = (MUONH_LDS uint8_t*)slot + wave * MB * 16 * kStageK;
+  const int lrow = lane >> 3;
+  int avoff[2], bvoff[2];   // even and odd i
 #pragma unroll
-    for (int i = 0; i < MB; ++i) {
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (MUONH_LDS void*)(d + i * 16 * kStageK), 16, avoff,
-                                               (int)(i * 16 * p.lda) + t * kStageK, 0, 0);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (MUONH_LDS void*)(d + kOperand + i * 16 * kStageK), 16, bvoff,
-                                               (int)(i * 16 * p.ldb) + t * kStageK, 0, 0);
+  for (int o = 0; o < 2; ++o) {
+    const int chunk = (lane & 7) ^ swz128(lrow + 8 * o);
+    avoff[o] = (int)((wave * MB * 16 + lrow) * p.lda) + chunk * 16;
+    bvoff[o] = (int)((wave * MB * 16 + lrow) * p.ldb) + chunk * 16;
+  }
+  auto load_block = [&](uint8_t (&slot)[kSlot], int kb) {
+    const bool in = kb < p.kblocks;
+    const __amdgpu_buffer_rsrc_t ra =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(abase), (short)0, in ? arange : 0, kBufferConfig);
+    const __amdgpu_buffer_rsrc_t rb =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(bbase), (short)0, in ? brange : 0, kBufferConfig);
+    MUONH_LDS uint8_t* d = (MUONH_LDS uint8_t*)slot + wave * MB * 16 * kFp8Block;
+#pragma unroll
+    for (int i = 0; i < 2 * MB; ++i) {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (MUONH_LDS void*)(d + i * 8 * kFp8Block), 16, avoff[i & 1],
+                                               (int)(i * 8 * p.lda) + kb * kFp8Block, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (MUONH_LDS void*)(d + kOperand + i * 8 * kFp8Block), 16,
+                                               bvoff[i & 1], (int)(i * 8 * p.ldb) + kb * kFp8Block, 0, 0);
     }
   };
 
-  // Fragments: block i of A is rows wr 32 MB + 32 i + l % 32; lane l holds the
-  // 32 bytes 32 (l / 32) .. of its stage.
-  const int fchunk = (2 * (lane >> 5)) ^ swz64(lane & 15);
-  const int aoff = (wr * MB * 32 + (lane & 31)) * kStageK, boff = kOperand + (wc * MB * 32 + (lane & 31)) * kStageK;
+  // Fragments: block i of A is rows 32 (MB wr + i) + l % 32; lane l holds the 32
+  // bytes 32 (l / 32) .. of the half block.
+  const int fswz = swz128(lane & 15);
+  const int aoff = (wr * MB * 32 + (lane & 31)) * kFp8Block, boff = kOperand + (wc * MB * 32 + (lane & 31)) * kFp8Block;
   struct Frags {
     u32x4_t a[MB][2], b[MB][2];
   };
-  auto read_frags = [&](Frags& f, uint8_t (&slot)[kSlot]) {
+  auto read_frags = [&](Frags& f, uint8_t (&slot)[kSlot], int half) {
 #pragma unroll
     for (int i = 0; i < MB; ++i)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        f.a[i][h] = *reinterpret_cast<const u32x4_t*>(slot + aoff + i * 32 * kStageK + ((fchunk ^ h) << 4));
-        f.b[i][h] = *reinterpret_cast<const u32x4_t*>(slot + boff + i * 32 * kStageK + ((fchunk ^ h) << 4));
+        const int chunk = ((4 * half + 2 * (lane >> 5) + h) ^ fswz) << 4;
+        f.a[i][h] = *reinterpret_cast<const u32x4_t*>(slot + aoff + i * 32 * kFp8Block + chunk);
+        f.b[i][h] = *reinterpret_cast<const u32x4_t*>(slot + boff + i * 32 * kFp8Block + chunk);
       }
   };
 
-  // Scales: 4 blocks' bytes per row at a time, the current one lowest.
+  // Scale bytes of the lane's rows: the block's, and the next one's.
   const uint8_t* sa[MB];
   const uint8_t* sb[MB];
 #pragma unroll
@@ -552,11 +557,11 @@ __global__ __launch_bounds__(kTileThreads) void block_matmul_tile_kernel(BlockMa
   }
   uint32_t ea[MB], eb[MB], na[MB], nb[MB];
   auto load_scales = [&](int kb) {
-    const int at = min(kb, p.kblocks - 1) & ~3;
+    const int at = min(kb, p.kblocks - 1);
 #pragma unroll
     for (int i = 0; i < MB; ++i) {
-      na[i] = ld_global<uint32_t>(sa[i] + at);
-      nb[i] = ld_global<uint32_t>(sb[i] + at);
+      na[i] = ld_global<uint8_t>(sa[i] + at);
+      nb[i] = ld_global<uint8_t>(sb[i] + at);
     }
   };
 
@@ -585,8 +590,8 @@ __global__ __launch_bounds__(kTileThreads) void block_matmul_tile_kernel(BlockMa
         bf16x8_t wa[MB], wb[MB];
 #pragma unroll
         for (int i = 0; i < MB; ++i) {
-          wa[i] = widen8(f.a[i][q >> 1][(q & 1) * 2], f.a[i][q >> 1][(q & 1) * 2 + 1], scale_value(ea[i] & 255u));
-          wb[i] = widen8(f.b[i][q >> 1][(q & 1) * 2], f.b[i][q >> 1][(q & 1) * 2 + 1], scale_value(eb[i] & 255u));
+          wa[i] = widen8(f.a[i][q >> 1][(q & 1) * 2], f.a[i][q >> 1][(q & 1) * 2 + 1], scale_value(ea[i]));
+          wb[i] = widen8(f.b[i][q >> 1][(q & 1) * 2], f.b[i][q >> 1][(q & 1) * 2 + 1], scale_value(eb[i]));
         }
 #pragma unroll
         for (int i = 0; i < MB; ++i)
@@ -596,72 +601,65 @@ __global__ __launch_bounds__(kTileThreads) void block_matmul_tile_kernel(BlockMa
       }
     }
   };
-  // SC: scale loads that were issued after stage t + 1's loads.
-  auto iterate = [&](const Frags& cur, Frags& next, uint8_t (&mine)[kSlot], uint8_t (&after)[kSlot], int t,
-                     auto sc) {
-    wait_loads<2 * kLoads + decltype(sc)::value>();   // stage t + 1 is in LDS (t + 2 and t + 3 may be in flight)
-    lds_barrier();              // for every wavefront, and all are done with stage t's slot
-    load_stage(mine, t + 4);
-    read_frags(next, after);
-    multiply(cur);
+  Frags f0, f1;
+  auto block = [&](uint8_t (&mine)[kSlot], uint8_t (&other)[kSlot], int kb) {
+#pragma unroll
+    for (int i = 0; i < MB; ++i) {
+      ea[i] = na[i];
+      eb[i] = nb[i];
+    }
+    load_scales(kb + 1);
+    __builtin_amdgcn_sched_barrier(0);
+    read_frags(f1, mine, 1);
+    multiply(f0);
+    if constexpr (kFp8) {
+      // reads early, so that the last has landed by the barrier
+#pragma unroll
+      for (int k = 0; k < MB * MB; ++k) {
+        MUONH_SG(kSgMfma, 1);
+        MUONH_SG(kSgDsRead, MB == 4 ? 2 : 4);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    wait_loads<2 * MB>();   // all but the scale loads: the next block is in its slot
+    lds_barrier();          // for every wavefront, and all have read theirs
+    read_frags(f0, other, 0);
+    load_block(mine, kb + 2);
+    multiply(f1);
     if constexpr (kFp8) {
 #pragma unroll
-      for (int k = 0; k < MB * MB / 2; ++k) {
+      for (int k = 0; k < MB * MB; ++k) {
         MUONH_SG(kSgMfma, 1);
-        MUONH_SG(kSgDsRead, MB == 4 ? 1 : 2);
-        MUONH_SG(kSgMfma, 1);
-        MUONH_SG(kSgDsRead, MB == 4 ? 1 : 2);
-        MUONH_SG(kSgVmemRead, MB == 4 ? 1 : 2);
+        MUONH_SG(kSgDsRead, MB == 4 ? 2 : 4);
+        MUONH_SG(kSgVmemRead, MB == 4 ? 2 : 4);
       }
     }
     __builtin_amdgcn_sched_barrier(0);
   };
-  constexpr std::integral_constant<int, 2 * MB> with_scales{};
-  constexpr std::integral_constant<int, 0> without{};
 
   load_scales(0);
-  asm volatile("" ::: "memory");   // ahead of the stages, so waiting for them waits for none
-  load_stage(slot0, 0);
-  load_stage(slot1, 1);
-  load_stage(slot2, 2);
-  load_stage(slot3, 3);
-  wait_loads<3 * kLoads>();
+  asm volatile("" ::: "memory");   // ahead of the blocks, so waiting for them waits for none
+  load_block(slot0, 0);
+  load_block(slot1, 1);
+  wait_loads<4 * MB>();
   lds_barrier();
-  Frags f0, f1;
-  read_frags(f0, slot0);
-  // Two blocks of 128 per trip.  Behind an odd count the second one's data are
-  // out of range, which the loads turn into zeros; its scales are set to 1, as
-  // the bytes there are the caller's.
+  read_frags(f0, slot0, 0);
+  // Behind an odd count of blocks comes one of zeros (with the last scales).
   for (int kb = 0; kb < p.kblocks; kb += 2) {
-#pragma unroll
-    for (int i = 0; i < MB; ++i) {
-      ea[i] = na[i] >> (8 * (kb & 2));
-      eb[i] = nb[i] >> (8 * (kb & 2));
-    }
-    load_scales(kb + 2);
-    __builtin_amdgcn_sched_barrier(0);
-    iterate(f0, f1, slot0, slot1, 2 * kb, with_scales);
-    iterate(f1, f0, slot1, slot2, 2 * kb + 1, with_scales);
-    const bool last = kb + 1 >= p.kblocks;
-#pragma unroll
-    for (int i = 0; i < MB; ++i) {
-      ea[i] = last ? 127u : ea[i] >> 8;
-      eb[i] = last ? 127u : eb[i] >> 8;
-    }
-    iterate(f0, f1, slot2, slot3, 2 * kb + 2, with_scales);
-    iterate(f1, f0, slot3, slot0, 2 * kb + 3, without);
+    block(slot0, slot1, kb);
+    block(slot1, slot0, kb + 1);
   }
   wait_loads<0>();   // no load into LDS is in flight past this point
   lds_barrier();
 
-  // Epilogue: the wavefront's rows go through a slot of its own, in passes of
+  // Epilogue: the wavefront's rows go through half a slot of its own, in passes of
   // as many rows as it holds, 16-byte chunk c of row r at c ^ (r & 15), and
   // leave as whole rows.
-  uint8_t* reg = wave == 0 ? slot0 : wave == 1 ? slot1 : wave == 2 ? slot2 : slot3;
+  uint8_t* reg = ((wave & 2) ? slot1 : slot0) + (wave & 1) * kOperand;
   constexpr int kRowBytes = 32 * MB * (int)sizeof(C);
   constexpr int kChunks = kRowBytes / 16;                  // 16-byte chunks per row
-  constexpr int kPass = kSlot / kRowBytes < 32 * MB ? kSlot / kRowBytes : 32 * MB;
-  static_assert(kPass % 32 == 0 && kChunks >= 8, "whole blocks per pass");
+  constexpr int kPass = kOperand / kRowBytes < 32 * MB ? kOperand / kRowBytes : 32 * MB;
+  static_assert(kPass % 32 == 0, "whole blocks per pass");
   constexpr int kMask = kChunks < 16 ? kChunks - 1 : 15;
   C* c = reinterpret_cast<C*>(p.c);
 #pragma unroll
