@@ -446,6 +446,7 @@ constexpr int kSgMfma = 0x008, kSgVmemRead = 0x020, kSgDsRead = 0x100;
 #define MUONH_SG(mask, n) __builtin_amdgcn_sched_group_barrier((mask), (n), 0)
 
 constexpr int kTileThreads = 256;
+constexpr int kScaleBlocks = 16;   // scales staged at a time, per row
 // 16-byte chunk c of a 128-byte LDS row r sits at c ^ swz128(r): the rows of a
 // fragment read then differ in banks whether 8 or 16 lanes are served at once.
 __device__ __forceinline__ int swz128(int r) { return (r & 7) ^ ((r >> 3) & 1); }
@@ -481,6 +482,7 @@ __global__ __launch_bounds__(kTileThreads) void block_matmul_tile_kernel(BlockMa
   constexpr bool kFp8 = sizeof(C) == 2;
   __shared__ __attribute__((aligned(16))) uint8_t slot0[kSlot];
   __shared__ __attribute__((aligned(16))) uint8_t slot1[kSlot];
+  __shared__ __attribute__((aligned(16))) uint8_t scales[2][2 * kTile * kScaleBlocks];
 
   uint32_t tm, tn;
   tile_of(blockIdx.x, mt, nt, tm, tn);
@@ -547,21 +549,36 @@ __global__ __launch_bounds__(kTileThreads) void block_matmul_tile_kernel(BlockMa
       }
   };
 
-  // Scale bytes of the lane's rows: the block's, and the next one's.
-  const uint8_t* sa[MB];
-  const uint8_t* sb[MB];
+  // Scales: 16 blocks' bytes of every row of the tile at a time in LDS (A's
+  // rows, then B's), two such chunks in turn.  (Each lane reading its own rows'
+  // bytes from memory touches 32 lines per load, for every block more lines
+  // than the block's data: 454 against 401 us at 8192 x 8192 x 8192.)
+  auto load_scales = [&](int chunk) {
 #pragma unroll
-  for (int i = 0; i < MB; ++i) {
-    sa[i] = p.sa + (int64_t)(min(row0 + (wr * MB + i) * 32 + (lane & 31), p.m - 1) >> p.a_shift) * p.ldsa;
-    sb[i] = p.sb + (int64_t)(min(col0 + (wc * MB + i) * 32 + (lane & 31), p.n - 1) >> p.b_shift) * p.ldsb;
-  }
+    for (int q0 = 0; q0 < 2 * MB; q0 += 4) {
+      const int q = q0 + wave;
+      if (q >= 2 * MB) break;
+      const bool is_a = q < MB;
+      const uint8_t* base = is_a ? p.sa : p.sb;
+      const int64_t pitch = is_a ? p.ldsa : p.ldsb;
+      const int shift = is_a ? p.a_shift : p.b_shift, end = (is_a ? p.m : p.n) - 1, first = is_a ? row0 : col0;
+      const int s0 = first >> shift, rows = (min(first + kTile - 1, end) >> shift) - s0;
+      const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+          const_cast<uint8_t*>(base + s0 * pitch), (short)0, (int)(rows * pitch) + ((p.kblocks + 3) & ~3), kBufferConfig);
+      const int row = (min(first + (is_a ? q : q - MB) * 64 + lane, end) >> shift) - s0;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rs, (MUONH_LDS void*)((MUONH_LDS uint8_t*)scales[chunk & 1] + q * 64 * kScaleBlocks), 16,
+          (int)(row * pitch), chunk * kScaleBlocks, 0, 0);
+    }
+  };
   uint32_t ea[MB], eb[MB], na[MB], nb[MB];
-  auto load_scales = [&](int kb) {
+  auto read_scales = [&](int kb) {
     const int at = min(kb, p.kblocks - 1);
+    const uint8_t* s = scales[(at / kScaleBlocks) & 1] + (at % kScaleBlocks) + (lane & 31) * kScaleBlocks;
 #pragma unroll
     for (int i = 0; i < MB; ++i) {
-      na[i] = ld_global<uint8_t>(sa[i] + at);
-      nb[i] = ld_global<uint8_t>(sb[i] + at);
+      na[i] = s[((wr * MB + i) * 32) * kScaleBlocks];
+      nb[i] = s[(kTile + (wc * MB + i) * 32) * kScaleBlocks];
     }
   };
 
@@ -608,8 +625,6 @@ __global__ __launch_bounds__(kTileThreads) void block_matmul_tile_kernel(BlockMa
       ea[i] = na[i];
       eb[i] = nb[i];
     }
-    load_scales(kb + 1);
-    __builtin_amdgcn_sched_barrier(0);
     read_frags(f1, mine, 1);
     multiply(f0);
     if constexpr (kFp8) {
@@ -621,8 +636,9 @@ __global__ __launch_bounds__(kTileThreads) void block_matmul_tile_kernel(BlockMa
       }
     }
     __builtin_amdgcn_sched_barrier(0);
-    wait_loads<2 * MB>();   // all but the scale loads: the next block is in its slot
-    lds_barrier();          // for every wavefront, and all have read theirs
+    wait_loads<0>();   // the next block is in its slot
+    lds_barrier();     // for every wavefront, and all have read theirs
+    read_scales(kb + 1);
     read_frags(f0, other, 0);
     load_block(mine, kb + 2);
     multiply(f1);
@@ -638,16 +654,21 @@ __global__ __launch_bounds__(kTileThreads) void block_matmul_tile_kernel(BlockMa
   };
 
   load_scales(0);
-  asm volatile("" ::: "memory");   // ahead of the blocks, so waiting for them waits for none
   load_block(slot0, 0);
   load_block(slot1, 1);
   wait_loads<4 * MB>();
   lds_barrier();
+  read_scales(0);
   read_frags(f0, slot0, 0);
   // Behind an odd count of blocks comes one of zeros (with the last scales).
-  for (int kb = 0; kb < p.kblocks; kb += 2) {
-    block(slot0, slot1, kb);
-    block(slot1, slot0, kb + 1);
+  for (int k0 = 0; k0 < p.kblocks; k0 += kScaleBlocks) {
+    // the chunk before this one has been read by every wavefront
+    load_scales(k0 / kScaleBlocks + 1);
+    const int k1 = min(k0 + kScaleBlocks, p.kblocks);
+    for (int kb = k0; kb < k1; kb += 2) {
+      block(slot0, slot1, kb);
+      block(slot1, slot0, kb + 1);
+    }
   }
   wait_loads<0>();   // no load into LDS is in flight past this point
   lds_barrier();
