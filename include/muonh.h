@@ -364,7 +364,8 @@ int muonh_block_quantize(const void* x, int32_t dtype, int64_t rows, int64_t col
  * workspace: device memory of muonh_block_matmul_workspace bytes, 256-byte
  * aligned, or NULL where that is 0; calls that may overlap in time need one
  * each.  Errors: MUONH_EINVAL, MUONH_ENOMEM (workspace too small), MUONH_EHIP. */
-int muonh_block_matmul_workspace(const muonh_fp8_matrix* a, const muonh_fp8_matrix* b, size_t* bytes);
+int muonh_block_matmul_workspace(const muonh_fp8_matrix* a, const muonh_fp8_matrix* b, int32_t c_dtype,
+                                 size_t* bytes);
 int muonh_block_matmul(const muonh_fp8_matrix* a, const muonh_fp8_matrix* b, void* c, int32_t c_dtype,
                        int64_t ldc, int32_t accumulate, void* workspace, size_t workspace_bytes,
                        void* stream);

@@ -349,18 +349,18 @@ __device__ __forceinline__ bf16x8_t widen8(uint32_t lo, uint32_t hi, float scale
 }
 
 // Epilogue of 4 consecutive columns of one row.
-template <typename C, bool ACC>
-__device__ __forceinline__ void store_c(C* c, int64_t off, int left, const f32x4_t& v) {
+template <typename C>
+__device__ __forceinline__ void store_c(C* c, int left, int accumulate, const f32x4_t& v) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     if (e >= left) break;
     float r = v[e];
     if constexpr (sizeof(C) == 2) {
-      if constexpr (ACC) r += bf16_to_f32(c[off + e]);
-      c[off + e] = f32_to_bf16(r);
+      if (accumulate) r += bf16_to_f32(ld_global<uint16_t>(c + e));
+      st_global<uint16_t>(c + e, f32_to_bf16(r));
     } else {
-      if constexpr (ACC) r += c[off + e];
-      c[off + e] = r;
+      if (accumulate) r += ld_global<float>(c + e);
+      st_global<float>(c + e, r);
     }
   }
 }
@@ -372,7 +372,7 @@ __device__ __forceinline__ void store_c(C* c, int64_t off, int left, const f32x4
 // laid out alike, so the K order inside an instruction does not matter.
 // The operands are swapped (B first): lane l then holds columns 4 (l / 16) ..
 // + 3 of row l % 16.  Rows behind the end read the last one and are dropped.
-template <typename C, bool ACC, int WAVES>
+template <typename C, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void block_matmul_thin_kernel(BlockMatmulArgs p, uint32_t ntiles) {
   __shared__ f32x4_t part[WAVES][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -418,7 +418,7 @@ __global__ __launch_bounds__(64 * WAVES) void block_matmul_thin_kernel(BlockMatm
   for (int w = 1; w < WAVES; ++w) s += part[w][lane];
   const int row = m0 + (lane & 15), col = n0 + (lane >> 4) * 4;
   if (row >= p.m || col >= p.n) return;
-  store_c<C, ACC>(reinterpret_cast<C*>(p.c), (int64_t)row * p.ldc + col, p.n - col, s);
+  store_c<C>(reinterpret_cast<C*>(p.c) + (int64_t)row * p.ldc + col, p.n - col, p.accumulate, s);
 }
 
 #define MUONH_LDS __attribute__((address_space(3)))
@@ -464,56 +464,69 @@ __device__ __forceinline__ void tile_of(uint32_t b, uint32_t mt, uint32_t nt, ui
   tn = rest / rows;
 }
 
-// C tile of (64 MB)^2 per workgroup of 4 wavefronts (2 x 2, each MB x MB MFMA
-// blocks of 32 x 32).  Blocks of 128 bytes of K, whole 128-byte lines of every
-// row, go straight from global memory into one of two LDS slots; each slot is a
-// variable of its own, so that the compiler makes a fragment read wait for the
-// loads into its own slot only.  A block is multiplied in two halves.  During
-// the first the wavefront reads the second's fragments; then comes the block's
-// one barrier, after which its slot is free and the next block's data are in
-// the other; during the second half the next block's first fragments are read
-// and the block after it is loaded.
-template <typename C, bool ACC, int MB>
+// C tile of 64 MA x 64 NB per workgroup of 4 wavefronts (2 x 2, each MA x NB
+// MFMA blocks of 32 x 32).  Blocks of 128 bytes of K, whole 128-byte lines of
+// every row, go straight from global memory into one of two LDS slots; each
+// slot is a variable of its own, so that the compiler makes a fragment read wait
+// for the loads into its own slot only.  A block is multiplied in two halves.
+// During the first the wavefront reads the second's fragments; then comes the
+// block's one barrier, after which its slot is free and the next block's data
+// are in the other; during the second half the next block's first fragments are
+// read and the block after it is loaded.
+//
+// FP8: the arithmetic (see above); C: what is stored.  With a contraction split
+// over `splits` workgroups, C is float and each writes its own partial matrix.
+template <bool FP8, typename C, int MA, int NB>
 __global__ __launch_bounds__(kTileThreads) void block_matmul_tile_kernel(BlockMatmulArgs p, uint32_t mt,
                                                                          uint32_t nt) {
-  constexpr int kTile = 64 * MB;
-  constexpr int kOperand = kTile * kFp8Block;
-  constexpr int kSlot = 2 * kOperand;
-  constexpr bool kFp8 = sizeof(C) == 2;
+  constexpr int kTileA = 64 * MA, kTileB = 64 * NB;
+  constexpr int kOperandA = kTileA * kFp8Block;
+  constexpr int kSlot = kOperandA + kTileB * kFp8Block;
   __shared__ __attribute__((aligned(16))) uint8_t slot0[kSlot];
   __shared__ __attribute__((aligned(16))) uint8_t slot1[kSlot];
-  __shared__ __attribute__((aligned(16))) uint8_t scales[2][2 * kTile * kScaleBlocks];
+  __shared__ __attribute__((aligned(16))) uint8_t scales[2][(kTileA + kTileB) * kScaleBlocks];
 
   uint32_t tm, tn;
-  tile_of(blockIdx.x, mt, nt, tm, tn);
+  tile_of(blockIdx.x % (mt * nt), mt, nt, tm, tn);
+  if (p.splits > 1) {
+    const int k0 = (int)(blockIdx.x / (mt * nt)) * p.split_blocks;
+    p.a += (int64_t)k0 * kFp8Block;
+    p.b += (int64_t)k0 * kFp8Block;
+    p.sa += k0;
+    p.sb += k0;
+    p.c = reinterpret_cast<float*>(p.c) + (int64_t)(blockIdx.x / (mt * nt)) * p.m * p.ldc;
+    p.kblocks = min(p.kblocks - k0, p.split_blocks);
+  }
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wr = wave >> 1, wc = wave & 1;
-  const int row0 = (int)tm * kTile, col0 = (int)tn * kTile;
+  const int row0 = (int)tm * kTileA, col0 = (int)tn * kTileB;
 
-  f32x16_t acc[MB][MB];
+  f32x16_t acc[MA][NB];
 #pragma unroll
-  for (int i = 0; i < MB; ++i)
+  for (int i = 0; i < MA; ++i)
 #pragma unroll
-    for (int j = 0; j < MB; ++j)
+    for (int j = 0; j < NB; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
 
-  // Loads: instruction i of a wavefront fills rows 16 MB wave + 8 i .. + 7 of an
-  // operand; lane l lands in row l / 8, slot chunk l % 8.  Rows behind the
+  // Loads: instruction i of a wavefront fills rows 16 MA wave + 8 i .. + 7 of A
+  // (NB of B); lane l lands in row l / 8, slot chunk l % 8.  Rows behind the
   // matrix and blocks behind the last are out of the descriptor's range: they
   // make no memory access and leave zeros.  (The host keeps 256 rows below 2^31
   // bytes.)
   const uint8_t* abase = p.a + (int64_t)row0 * p.lda;
   const uint8_t* bbase = p.b + (int64_t)col0 * p.ldb;
-  const int arange = (int)(min(kTile, p.m - row0) * p.lda), brange = (int)(min(kTile, p.n - col0) * p.ldb);
+  // to the end of the last row's last block
+  const int arange = (int)((min(kTileA, p.m - row0) - 1) * p.lda) + p.kblocks * kFp8Block;
+  const int brange = (int)((min(kTileB, p.n - col0) - 1) * p.ldb) + p.kblocks * kFp8Block;
   const int lrow = lane >> 3;
   int avoff[2], bvoff[2];   // even and odd i
 #pragma unroll
   for (int o = 0; o < 2; ++o) {
     const int chunk = (lane & 7) ^ swz128(lrow + 8 * o);
-    avoff[o] = (int)((wave * MB * 16 + lrow) * p.lda) + chunk * 16;
-    bvoff[o] = (int)((wave * MB * 16 + lrow) * p.ldb) + chunk * 16;
+    avoff[o] = (int)((wave * MA * 16 + lrow) * p.lda) + chunk * 16;
+    bvoff[o] = (int)((wave * NB * 16 + lrow) * p.ldb) + chunk * 16;
   }
   auto load_block = [&](uint8_t (&slot)[kSlot], int kb) {
     const bool in = kb < p.kblocks;
@@ -521,31 +534,35 @@ __global__ __launch_bounds__(kTileThreads) void block_matmul_tile_kernel(BlockMa
         __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(abase), (short)0, in ? arange : 0, kBufferConfig);
     const __amdgpu_buffer_rsrc_t rb =
         __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(bbase), (short)0, in ? brange : 0, kBufferConfig);
-    MUONH_LDS uint8_t* d = (MUONH_LDS uint8_t*)slot + wave * MB * 16 * kFp8Block;
+    MUONH_LDS uint8_t* da = (MUONH_LDS uint8_t*)slot + wave * MA * 16 * kFp8Block;
+    MUONH_LDS uint8_t* db = (MUONH_LDS uint8_t*)slot + kOperandA + wave * NB * 16 * kFp8Block;
 #pragma unroll
-    for (int i = 0; i < 2 * MB; ++i) {
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (MUONH_LDS void*)(d + i * 8 * kFp8Block), 16, avoff[i & 1],
-                                               (int)(i * 8 * p.lda) + kb * kFp8Block, 0, 0);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (MUONH_LDS void*)(d + kOperand + i * 8 * kFp8Block), 16,
-                                               bvoff[i & 1], (int)(i * 8 * p.ldb) + kb * kFp8Block, 0, 0);
+    for (int i = 0; i < 2 * (MA > NB ? MA : NB); ++i) {
+      if (i < 2 * MA)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (MUONH_LDS void*)(da + i * 8 * kFp8Block), 16, avoff[i & 1],
+                                                 (int)(i * 8 * p.lda) + kb * kFp8Block, 0, 0);
+      if (i < 2 * NB)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (MUONH_LDS void*)(db + i * 8 * kFp8Block), 16, bvoff[i & 1],
+                                                 (int)(i * 8 * p.ldb) + kb * kFp8Block, 0, 0);
     }
   };
 
-  // Fragments: block i of A is rows 32 (MB wr + i) + l % 32; lane l holds the 32
+  // Fragments: block i of A is rows 32 (MA wr + i) + l % 32; lane l holds the 32
   // bytes 32 (l / 32) .. of the half block.
   const int fswz = swz128(lane & 15);
-  const int aoff = (wr * MB * 32 + (lane & 31)) * kFp8Block, boff = kOperand + (wc * MB * 32 + (lane & 31)) * kFp8Block;
+  const int aoff = (wr * MA * 32 + (lane & 31)) * kFp8Block;
+  const int boff = kOperandA + (wc * NB * 32 + (lane & 31)) * kFp8Block;
   struct Frags {
-    u32x4_t a[MB][2], b[MB][2];
+    u32x4_t a[MA][2], b[NB][2];
   };
   auto read_frags = [&](Frags& f, uint8_t (&slot)[kSlot], int half) {
 #pragma unroll
-    for (int i = 0; i < MB; ++i)
+    for (int i = 0; i < (MA > NB ? MA : NB); ++i)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int chunk = ((4 * half + 2 * (lane >> 5) + h) ^ fswz) << 4;
-        f.a[i][h] = *reinterpret_cast<const u32x4_t*>(slot + aoff + i * 32 * kFp8Block + chunk);
-        f.b[i][h] = *reinterpret_cast<const u32x4_t*>(slot + boff + i * 32 * kFp8Block + chunk);
+        if (i < MA) f.a[i][h] = *reinterpret_cast<const u32x4_t*>(slot + aoff + i * 32 * kFp8Block + chunk);
+        if (i < NB) f.b[i][h] = *reinterpret_cast<const u32x4_t*>(slot + boff + i * 32 * kFp8Block + chunk);
       }
   };
 
@@ -555,41 +572,40 @@ __global__ __launch_bounds__(kTileThreads) void block_matmul_tile_kernel(BlockMa
   // than the block's data: 454 against 401 us at 8192 x 8192 x 8192.)
   auto load_scales = [&](int chunk) {
 #pragma unroll
-    for (int q0 = 0; q0 < 2 * MB; q0 += 4) {
+    for (int q0 = 0; q0 < MA + NB; q0 += 4) {
       const int q = q0 + wave;
-      if (q >= 2 * MB) break;
-      const bool is_a = q < MB;
+      if (q >= MA + NB) break;
+      const bool is_a = q < MA;
       const uint8_t* base = is_a ? p.sa : p.sb;
       const int64_t pitch = is_a ? p.ldsa : p.ldsb;
       const int shift = is_a ? p.a_shift : p.b_shift, end = (is_a ? p.m : p.n) - 1, first = is_a ? row0 : col0;
-      const int s0 = first >> shift, rows = (min(first + kTile - 1, end) >> shift) - s0;
+      const int s0 = first >> shift, rows = (min(first + (is_a ? kTileA : kTileB) - 1, end) >> shift) - s0;
       const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
           const_cast<uint8_t*>(base + s0 * pitch), (short)0, (int)(rows * pitch) + ((p.kblocks + 3) & ~3), kBufferConfig);
-      const int row = (min(first + (is_a ? q : q - MB) * 64 + lane, end) >> shift) - s0;
+      const int row = (min(first + (is_a ? q : q - MA) * 64 + lane, end) >> shift) - s0;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
           rs, (MUONH_LDS void*)((MUONH_LDS uint8_t*)scales[chunk & 1] + q * 64 * kScaleBlocks), 16,
           (int)(row * pitch), chunk * kScaleBlocks, 0, 0);
     }
   };
-  uint32_t ea[MB], eb[MB], na[MB], nb[MB];
+  uint32_t ea[MA], eb[NB], na[MA], nb[NB];
   auto read_scales = [&](int kb) {
     const int at = min(kb, p.kblocks - 1);
     const uint8_t* s = scales[(at / kScaleBlocks) & 1] + (at % kScaleBlocks) + (lane & 31) * kScaleBlocks;
 #pragma unroll
-    for (int i = 0; i < MB; ++i) {
-      na[i] = s[((wr * MB + i) * 32) * kScaleBlocks];
-      nb[i] = s[(kTile + (wc * MB + i) * 32) * kScaleBlocks];
-    }
+    for (int i = 0; i < MA; ++i) na[i] = s[((wr * MA + i) * 32) * kScaleBlocks];
+#pragma unroll
+    for (int j = 0; j < NB; ++j) nb[j] = s[(kTileA + (wc * NB + j) * 32) * kScaleBlocks];
   };
 
   // Operands are swapped (B first), so a lane holds 4 consecutive columns of
   // one row per group of 4 accumulators.
   auto multiply = [&](const Frags& f) {
-    if constexpr (kFp8) {
+    if constexpr (FP8) {
 #pragma unroll
-      for (int i = 0; i < MB; ++i)
+      for (int i = 0; i < MA; ++i)
 #pragma unroll
-        for (int j = 0; j < MB; ++j) {
+        for (int j = 0; j < NB; ++j) {
           i32x8_t fa, fb;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -604,35 +620,37 @@ __global__ __launch_bounds__(kTileThreads) void block_matmul_tile_kernel(BlockMa
     } else {
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        bf16x8_t wa[MB], wb[MB];
+        bf16x8_t wa[MA], wb[NB];
 #pragma unroll
-        for (int i = 0; i < MB; ++i) {
+        for (int i = 0; i < MA; ++i)
           wa[i] = widen8(f.a[i][q >> 1][(q & 1) * 2], f.a[i][q >> 1][(q & 1) * 2 + 1], scale_value(ea[i]));
-          wb[i] = widen8(f.b[i][q >> 1][(q & 1) * 2], f.b[i][q >> 1][(q & 1) * 2 + 1], scale_value(eb[i]));
-        }
 #pragma unroll
-        for (int i = 0; i < MB; ++i)
+        for (int j = 0; j < NB; ++j)
+          wb[j] = widen8(f.b[j][q >> 1][(q & 1) * 2], f.b[j][q >> 1][(q & 1) * 2 + 1], scale_value(eb[j]));
 #pragma unroll
-          for (int j = 0; j < MB; ++j)
+        for (int i = 0; i < MA; ++i)
+#pragma unroll
+          for (int j = 0; j < NB; ++j)
             acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wb[j], wa[i], acc[i][j], 0, 0, 0);
       }
     }
   };
+  // Per MFMA so many fragment reads (and loads): all of a half's are then issued
+  // in its first half, and the last read has landed by the barrier.
+  constexpr int kPer = MA * NB >= 8 ? 2 : 4;
   Frags f0, f1;
   auto block = [&](uint8_t (&mine)[kSlot], uint8_t (&other)[kSlot], int kb) {
 #pragma unroll
-    for (int i = 0; i < MB; ++i) {
-      ea[i] = na[i];
-      eb[i] = nb[i];
-    }
+    for (int i = 0; i < MA; ++i) ea[i] = na[i];
+#pragma unroll
+    for (int j = 0; j < NB; ++j) eb[j] = nb[j];
     read_frags(f1, mine, 1);
     multiply(f0);
-    if constexpr (kFp8) {
-      // reads early, so that the last has landed by the barrier
+    if constexpr (FP8) {
 #pragma unroll
-      for (int k = 0; k < MB * MB; ++k) {
+      for (int k = 0; k < MA * NB; ++k) {
         MUONH_SG(kSgMfma, 1);
-        MUONH_SG(kSgDsRead, MB == 4 ? 2 : 4);
+        MUONH_SG(kSgDsRead, kPer);
       }
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -642,12 +660,12 @@ __global__ __launch_bounds__(kTileThreads) void block_matmul_tile_kernel(BlockMa
     read_frags(f0, other, 0);
     load_block(mine, kb + 2);
     multiply(f1);
-    if constexpr (kFp8) {
+    if constexpr (FP8) {
 #pragma unroll
-      for (int k = 0; k < MB * MB; ++k) {
+      for (int k = 0; k < MA * NB; ++k) {
         MUONH_SG(kSgMfma, 1);
-        MUONH_SG(kSgDsRead, MB == 4 ? 2 : 4);
-        MUONH_SG(kSgVmemRead, MB == 4 ? 2 : 4);
+        MUONH_SG(kSgDsRead, kPer);
+        MUONH_SG(kSgVmemRead, kPer);
       }
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -656,7 +674,7 @@ __global__ __launch_bounds__(kTileThreads) void block_matmul_tile_kernel(BlockMa
   load_scales(0);
   load_block(slot0, 0);
   load_block(slot1, 1);
-  wait_loads<4 * MB>();
+  wait_loads<2 * (MA + NB)>();
   lds_barrier();
   read_scales(0);
   read_frags(f0, slot0, 0);
@@ -673,99 +691,161 @@ __global__ __launch_bounds__(kTileThreads) void block_matmul_tile_kernel(BlockMa
   wait_loads<0>();   // no load into LDS is in flight past this point
   lds_barrier();
 
-  // Epilogue: the wavefront's rows go through half a slot of its own, in passes of
-  // as many rows as it holds, 16-byte chunk c of row r at c ^ (r & 15), and
+  // Epilogue: the wavefront's rows go through half a slot of its own, in passes
+  // of as many rows as it holds, 16-byte chunk c of row r at c ^ (r & kMask), and
   // leave as whole rows.
-  uint8_t* reg = ((wave & 2) ? slot1 : slot0) + (wave & 1) * kOperand;
-  constexpr int kRowBytes = 32 * MB * (int)sizeof(C);
-  constexpr int kChunks = kRowBytes / 16;                  // 16-byte chunks per row
-  constexpr int kPass = kOperand / kRowBytes < 32 * MB ? kOperand / kRowBytes : 32 * MB;
-  static_assert(kPass % 32 == 0, "whole blocks per pass");
-  constexpr int kMask = kChunks < 16 ? kChunks - 1 : 15;
-  C* c = reinterpret_cast<C*>(p.c);
+  uint8_t* reg = ((wave & 2) ? slot1 : slot0) + (wave & 1) * (kSlot / 2);
+  constexpr int kRowBytes = 32 * NB * (int)sizeof(C);
+  constexpr int kChunks = kRowBytes / 16;   // 16-byte chunks per row
+  constexpr int kBlocks = kSlot / 2 / kRowBytes / 32;
+  constexpr int kPass = kBlocks >= MA ? MA : kBlocks >= 2 ? 2 : 1;   // blocks of 32 rows per pass
+  constexpr int kMask = kChunks % 16 == 0 ? 15 : kChunks % 8 == 0 ? 7 : 3;
+  static_assert(kBlocks >= 1 && MA % kPass == 0 && kChunks % (kMask + 1) == 0, "whole blocks per pass");
+  C* c = reinterpret_cast<C*>(p.c) + (int64_t)(row0 + wr * MA * 32) * p.ldc + col0 + wc * NB * 32;
+  const int rows = p.m - (row0 + wr * MA * 32), cols = p.n - (col0 + wc * NB * 32);
+  if (sizeof(C) == 2 && p.accumulate) {
+    // added to c before the one rounding: straight to memory
 #pragma unroll
-  for (int i0 = 0; i0 < MB; i0 += kPass / 32) {
+    for (int i = 0; i < MA; ++i)
 #pragma unroll
-    for (int i = 0; i < kPass / 32; ++i)
+      for (int j = 0; j < NB; ++j)
 #pragma unroll
-      for (int j = 0; j < MB; ++j)
+        for (int g = 0; g < 4; ++g) {
+          const int r = 32 * i + (lane & 31), col = 32 * j + 8 * g + 4 * (lane >> 5);
+          const f32x16_t& v = acc[i][j];
+          if (r < rows && col < cols)
+            store_c<C>(c + (int64_t)r * p.ldc + col, cols - col, 1, f32x4_t{v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]});
+        }
+    return;
+  }
+#pragma unroll
+  for (int i0 = 0; i0 < MA; i0 += kPass) {
+#pragma unroll
+    for (int i = 0; i < kPass; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           const int r = 32 * i + (lane & 31), col = 32 * j + 8 * g + 4 * (lane >> 5);
           const f32x16_t& v = acc[i0 + i][j];
           uint8_t* d = reg + r * kRowBytes + ((((col * (int)sizeof(C)) >> 4) ^ (r & kMask)) << 4);
-          if constexpr (kFp8 && !ACC) {
-            u32x2_t o;
-            o[0] = pack_bf16x2(v[4 * g], v[4 * g + 1]);
-            o[1] = pack_bf16x2(v[4 * g + 2], v[4 * g + 3]);
-            *reinterpret_cast<u32x2_t*>(d + (col & 4) * 2) = o;
-          } else if constexpr (kFp8) {
-            // added to c before the one rounding: straight to memory
-            const int row = row0 + wr * MB * 32 + i0 * 32 + r, cc = col0 + wc * MB * 32 + col;
-            if (row < p.m && cc < p.n)
-              store_c<C, ACC>(c, (int64_t)row * p.ldc + cc, p.n - cc, f32x4_t{v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]});
-          } else {
+          if constexpr (sizeof(C) == 2)
+            *reinterpret_cast<u32x2_t*>(d + (col & 4) * 2) =
+                u32x2_t{pack_bf16x2(v[4 * g], v[4 * g + 1]), pack_bf16x2(v[4 * g + 2], v[4 * g + 3])};
+          else
             *reinterpret_cast<f32x4_t*>(d) = f32x4_t{v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]};
-          }
         }
-    if constexpr (kFp8 && ACC) continue;
 #pragma unroll
-    for (int k = 0; k < kPass * kChunks / 64; ++k) {
-      const int idx = k * 64 + lane, r = idx / kChunks, ch = idx % kChunks;
-      const u32x4_t v = *reinterpret_cast<const u32x4_t*>(reg + r * kRowBytes + ((ch ^ (r & kMask)) << 4));
-      const int row = row0 + wr * MB * 32 + i0 * 32 + r;
-      const int col = col0 + wc * MB * 32 + ch * (16 / (int)sizeof(C));
-      if (row >= p.m || col >= p.n) continue;
-      C* d = c + (int64_t)row * p.ldc + col;
-      if constexpr (kFp8) {
+    for (int k = 0; k < kPass * 32 * kChunks / 64; ++k) {
+      const int idx = k * 64 + lane, lr = idx / kChunks, ch = idx % kChunks;
+      const u32x4_t v = *reinterpret_cast<const u32x4_t*>(reg + lr * kRowBytes + ((ch ^ (lr & kMask)) << 4));
+      const int r = i0 * 32 + lr, col = ch * (16 / (int)sizeof(C));
+      if (r >= rows || col >= cols) continue;
+      C* d = c + (int64_t)r * p.ldc + col;
+      if constexpr (sizeof(C) == 2) {
         typedef uint32_t vec __attribute__((ext_vector_type(4), aligned(2)));
-        if (col + 8 <= p.n) {
-          st_global<vec>(d, v);
+        if (col + 8 <= cols) {
+          __builtin_nontemporal_store((vec)v, (MUONH_GLOBAL vec*)d);
         } else {
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            if (col + e < p.n) st_global<uint16_t>(d + e, (uint16_t)(v[e >> 1] >> (16 * (e & 1))));
+            if (col + e < cols) st_global<uint16_t>(d + e, (uint16_t)(v[e >> 1] >> (16 * (e & 1))));
         }
       } else {
         typedef float vec __attribute__((ext_vector_type(4), aligned(4)));
-        vec o = __builtin_bit_cast(f32x4_t, v);
-        if (col + 4 <= p.n) {
-          if constexpr (ACC) o += ld_global<vec>(d);
-          st_global<vec>(d, o);
+        const f32x4_t o = __builtin_bit_cast(f32x4_t, v);
+        if (col + 4 <= cols) {
+          vec x = o;
+          if (p.accumulate) x += ld_global<vec>(d);
+          __builtin_nontemporal_store(x, (MUONH_GLOBAL vec*)d);
         } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (col + e < p.n) st_global<float>(d + e, ACC ? ld_global<float>(d + e) + o[e] : o[e]);
+          store_c<float>(d, cols - col, p.accumulate, o);
         }
       }
     }
   }
 }
 
-// Tiles need panels of 256 rows below 2^31 bytes (buffer offsets).
-bool tiles_fit(const BlockMatmulArgs& a) {
-  return a.lda < ((int64_t)1 << 23) && a.ldb < ((int64_t)1 << 23);
+// Adds the partial matrices of a split contraction in order, 4 elements per
+// thread along the rows of the (dense) partials.
+template <typename C>
+__global__ __launch_bounds__(256) void block_matmul_fold_kernel(const float* __restrict__ part, int splits, int64_t m,
+                                                                int64_t n, C* c, int64_t ldc, int accumulate) {
+  const int64_t e0 = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, total = m * n;
+  if (e0 >= total) return;
+  typedef float vec __attribute__((ext_vector_type(4), aligned(4)));
+  if (e0 + 4 <= total) {
+    f32x4_t s = ld_global<vec>(part + e0);
+    for (int k = 1; k < splits; ++k) s += (f32x4_t)ld_global<vec>(part + k * total + e0);
+    int64_t row = e0 / n, col = e0 % n;
+    if (col + 4 <= n) {
+      store_c<C>(c + row * ldc + col, 4, accumulate, s);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        store_c<C>(c + row * ldc + col, 1, accumulate, f32x4_t{s[e], 0.0f, 0.0f, 0.0f});
+        if (++col == n) {
+          col = 0;
+          ++row;
+        }
+      }
+    }
+  } else {
+    for (int64_t e = e0; e < total; ++e) {
+      float s = part[e];
+      for (int k = 1; k < splits; ++k) s += part[k * total + e];
+      store_c<C>(c + (e / n) * ldc + e % n, 1, accumulate, f32x4_t{s, 0.0f, 0.0f, 0.0f});
+    }
+  }
 }
 
-template <typename C, bool ACC>
-hipError_t matmul_for(const BlockMatmulArgs& a, hipStream_t st) {
-  if (a.kblocks > 0 && tiles_fit(a) && a.m > 64 && a.n > 64) {
-    const int64_t big = (int64_t)((a.m + 255) / 256) * ((a.n + 255) / 256);
-    if (big >= 128) {
-      const uint32_t mt = (uint32_t)(a.m + 255) / 256, nt = (uint32_t)(a.n + 255) / 256;
-      hipLaunchKernelGGL((block_matmul_tile_kernel<C, ACC, 4>), dim3(mt * nt), dim3(kTileThreads), 0, st, a, mt, nt);
-    } else {
-      const uint32_t mt = (uint32_t)(a.m + 127) / 128, nt = (uint32_t)(a.n + 127) / 128;
-      hipLaunchKernelGGL((block_matmul_tile_kernel<C, ACC, 2>), dim3(mt * nt), dim3(kTileThreads), 0, st, a, mt, nt);
-    }
+template <bool FP8, typename C>
+hipError_t launch_tiles(const MatmulPlan& pl, const BlockMatmulArgs& a, hipStream_t st) {
+  const uint32_t mt = (uint32_t)((a.m + 64 * pl.ma - 1) / (64 * pl.ma));
+  const uint32_t nt = (uint32_t)((a.n + 64 * pl.nb - 1) / (64 * pl.nb));
+  const dim3 grid(mt * nt * (uint32_t)a.splits), block(kTileThreads);
+#define MUONH_TILE(MA, NB)                                                                            \
+  if (pl.ma == MA && pl.nb == NB) {                                                                   \
+    hipLaunchKernelGGL((block_matmul_tile_kernel<FP8, C, MA, NB>), grid, block, 0, st, a, mt, nt);    \
+    return hipGetLastError();                                                                         \
+  }
+  MUONH_TILE(4, 4)
+  MUONH_TILE(4, 3)
+  MUONH_TILE(3, 4)
+  MUONH_TILE(4, 2)
+  MUONH_TILE(2, 2)
+  MUONH_TILE(1, 1)
+#undef MUONH_TILE
+  return hipErrorInvalidValue;
+}
+
+template <typename C>
+hipError_t matmul_for(const MatmulPlan& pl, BlockMatmulArgs a, float* workspace, hipStream_t st) {
+  constexpr bool kFp8 = sizeof(C) == 2;
+  a.splits = 1;
+  a.split_blocks = a.kblocks;
+  if (pl.ma == 0) {
+    const unsigned ntiles = (unsigned)((a.n + 15) / 16);
+    const dim3 grid(ntiles * (unsigned)((a.m + 15) / 16));
+    // few tiles need more wavefronts each to have enough loads in flight
+    if (a.kblocks >= 16 && grid.x <= 512)
+      hipLaunchKernelGGL((block_matmul_thin_kernel<C, 16>), grid, dim3(1024), 0, st, a, ntiles);
+    else
+      hipLaunchKernelGGL((block_matmul_thin_kernel<C, 4>), grid, dim3(256), 0, st, a, ntiles);
     return hipGetLastError();
   }
-  const unsigned ntiles = (unsigned)((a.n + 15) / 16);
-  const dim3 grid(ntiles * (unsigned)((a.m + 15) / 16));
-  if (a.kblocks >= 16)
-    hipLaunchKernelGGL((block_matmul_thin_kernel<C, ACC, 16>), grid, dim3(1024), 0, st, a, ntiles);
-  else
-    hipLaunchKernelGGL((block_matmul_thin_kernel<C, ACC, 4>), grid, dim3(256), 0, st, a, ntiles);
+  if (pl.splits == 1) return launch_tiles<kFp8, C>(pl, a, st);
+  BlockMatmulArgs part = a;
+  part.splits = pl.splits;
+  part.split_blocks = pl.split_blocks;
+  part.c = workspace;
+  part.ldc = a.n;
+  part.accumulate = 0;
+  const hipError_t e = launch_tiles<kFp8, float>(pl, part, st);
+  if (e != hipSuccess) return e;
+  const int64_t groups = ((int64_t)a.m * a.n + 1023) / 1024;
+  hipLaunchKernelGGL((block_matmul_fold_kernel<C>), dim3((unsigned)groups), dim3(256), 0, st, workspace, pl.splits,
+                     (int64_t)a.m, (int64_t)a.n, reinterpret_cast<C*>(a.c), a.ldc, a.accumulate);
   return hipGetLastError();
 }
 
@@ -789,9 +869,9 @@ hipError_t launch_block_quantize(int bf16, int square, const QuantArgs& a, hipSt
   return hipGetLastError();
 }
 
-hipError_t launch_block_matmul(int c_bf16, int accumulate, const BlockMatmulArgs& a, hipStream_t st) {
-  if (c_bf16) return accumulate ? matmul_for<uint16_t, true>(a, st) : matmul_for<uint16_t, false>(a, st);
-  return accumulate ? matmul_for<float, true>(a, st) : matmul_for<float, false>(a, st);
+hipError_t launch_block_matmul(int c_bf16, const MatmulPlan& plan, const BlockMatmulArgs& a, float* workspace,
+                               hipStream_t st) {
+  return c_bf16 ? matmul_for<uint16_t>(plan, a, workspace, st) : matmul_for<float>(plan, a, workspace, st);
 }
 
 }  // namespace muonh

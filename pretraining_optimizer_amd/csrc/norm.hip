@@ -260,7 +260,7 @@ __global__ __launch_bounds__(G > kBackThreads ? G : kBackThreads) void norm_back
   constexpr int kRows = kThreads / G;
   constexpr int kAcc = BIAS ? 2 : 1;
   __shared__ float red[2][16];
-  __shared__ float fold[kRows > 1 ? kThreads * 8 : 1];
+  __shared__ __attribute__((aligned(16))) float fold[kRows > 1 ? kThreads * 8 : 1];
   const int t = threadIdx.x % G, grp = threadIdx.x / G, cols = (int)p.cols;
   const float rn = 1.0f / (float)cols;
   const int64_t step = (int64_t)gridDim.x * kRows;
@@ -342,28 +342,37 @@ __global__ __launch_bounds__(G > kBackThreads ? G : kBackThreads) void norm_back
       store8<T>(dx, c, cols, o);
     }
   }
+  // Vector k of the groups covers columns 8 G k .. 8 G (k + 1) - 1.
   float* out = p.partials + (int64_t)blockIdx.x * cols;
 #pragma unroll
   for (int a = 0; a < kAcc; ++a) {
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int c = 8 * (t + G * k);
       if constexpr (kRows > 1) {
         __syncthreads();
 #pragma unroll
-        for (int j = 0; j < 8; ++j) fold[j * kThreads + threadIdx.x] = acc[a][k][j];
+        for (int h = 0; h < 2; ++h)
+          *reinterpret_cast<f32x4_t*>(&fold[(grp * G + t) * 8 + 4 * h]) =
+              f32x4_t{acc[a][k][4 * h], acc[a][k][4 * h + 1], acc[a][k][4 * h + 2], acc[a][k][4 * h + 3]};
         __syncthreads();
-        // thread i adds element i / G of the 8 of lane i % G, over the groups in order
-        for (int e = grp; e < 8; e += kRows) {
+        for (int c = threadIdx.x; c < 8 * G; c += kThreads) {
           float v = 0.0f;
 #pragma unroll
-          for (int q = 0; q < kRows; ++q) v += fold[e * kThreads + q * G + t];
-          if (c + e < cols) out[c + e] = v;
+          for (int q = 0; q < kRows; ++q) v += fold[q * 8 * G + c];
+          if (8 * G * k + c < cols) out[8 * G * k + c] = v;
         }
       } else {
+        const int c = 8 * (t + G * k);
+        typedef float vec __attribute__((ext_vector_type(4), aligned(4)));
+        if (c + 8 <= cols) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (c + j < cols) out[c + j] = acc[a][k][j];
+          for (int h = 0; h < 2; ++h)
+            st_global<vec>(out + c + 4 * h, vec{acc[a][k][4 * h], acc[a][k][4 * h + 1], acc[a][k][4 * h + 2], acc[a][k][4 * h + 3]});
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (c + j < cols) out[c + j] = acc[a][k][j];
+        }
       }
     }
     out += (int64_t)gridDim.x * cols;
@@ -497,7 +506,10 @@ hipError_t backward_for(const NormGradArgs& a, hipStream_t st) {
 
 int64_t norm_partial_rows(int64_t rows, int64_t cols) {
   const int64_t per = cols > kRegisterCols ? 1 : rows_at_once(cols, kBackThreads);
-  return std::min<int64_t>((rows + per - 1) / per, kNormGroups);
+  const int64_t trips = (rows + per - 1) / per;
+  // every workgroup's row of partials is written and read again: at least 4
+  // trips each, unless that leaves fewer than 64 workgroups
+  return std::min<int64_t>(std::min<int64_t>(trips, std::max<int64_t>(64, (trips + 3) / 4)), kNormGroups);
 }
 
 hipError_t launch_norm_forward(int bf16, int layer, const NormArgs& a, hipStream_t st) {

@@ -105,11 +105,89 @@ int check_operands(const muonh_fp8_matrix* a, const muonh_fp8_matrix* b) {
   return MUONH_OK;
 }
 
+BlockMatmulArgs matmul_args(const muonh_fp8_matrix& a, const muonh_fp8_matrix& b) {
+  BlockMatmulArgs p{};
+  p.a = static_cast<const uint8_t*>(a.data);
+  p.b = static_cast<const uint8_t*>(b.data);
+  p.sa = static_cast<const uint8_t*>(a.scale);
+  p.sb = static_cast<const uint8_t*>(b.scale);
+  p.lda = a.ld;
+  p.ldb = b.ld;
+  p.ldsa = a.ld_scale;
+  p.ldsb = b.ld_scale;
+  p.m = (int32_t)a.rows;
+  p.n = (int32_t)b.rows;
+  p.kblocks = (int32_t)ceil_div(a.cols, kFp8Block);
+  p.a_shift = a.block_rows == 128 ? 7 : 0;
+  p.b_shift = b.block_rows == 128 ? 7 : 0;
+  return p;
+}
+
 int check_vectors(bool ok, const char* what) {
   return ok ? MUONH_OK : fail(MUONH_EINVAL, std::string("null pointer: ") + what);
 }
 
 }  // namespace
+
+namespace {
+
+// Measured times of the tile kernel on an MI355X, in us: one block of 128 of the
+// contraction with `per` workgroups on each CU (index per - 1), and what a round
+// costs besides its blocks.  [0]: FP8 arithmetic (bf16 results), [1]: bf16
+// arithmetic (fp32 results).
+struct TileRate {
+  int32_t ma, nb, per_cu;
+  double block[2][4], round[2];
+};
+constexpr TileRate kTileRates[] = {
+    {4, 4, 1, {{1.61, 0, 0, 0}, {2.88, 0, 0, 0}}, {8.8, 16.3}},
+    {4, 3, 1, {{1.20, 0, 0, 0}, {2.17, 0, 0, 0}}, {10.0, 13.1}},
+    {3, 4, 1, {{1.20, 0, 0, 0}, {2.17, 0, 0, 0}}, {10.0, 13.1}},
+    {4, 2, 1, {{0.88, 0, 0, 0}, {1.53, 0, 0, 0}}, {7.3, 8.4}},
+    {2, 2, 2, {{0.64, 0.88, 0, 0}, {0.90, 1.64, 0, 0}}, {4.0, 6.0}},
+    {1, 1, 4, {{0.28, 0.44, 0.62, 0.79}, {0.40, 0.58, 0.85, 1.12}}, {3.5, 4.0}},
+};
+constexpr int64_t kCus = 256;
+
+}  // namespace
+
+// The plan with the least time by the table: full rounds of workgroups over the
+// CUs, then the rest.  What decides is how the tiles fill the last round
+// (2048 x 6144 x 8192 to fp32: 192 tiles of 256 x 256 take 192 us, 256 of 256 x
+// 192 take 155), and for few tiles whether splitting a long contraction repays
+// its second launch and the partial sums' traffic (300 x 300 x 16384: 58 us
+// whole, 18 us split by 8; 1000 x 777 x 1500: 9.3 us whole, 14 us split by 2).
+MatmulPlan muonh::plan_block_matmul(int c_bf16, const BlockMatmulArgs& a) {
+  const int64_t m = a.m, n = a.n, nk = a.kblocks;
+  MatmulPlan best{0, 0, 1, a.kblocks, 0};
+  // Up to 32 rows (or columns) are bound by reading the other operand, which the
+  // thin kernel does with more loads in flight (32 x 2048 x 6144: 9.3 us, 15.2
+  // in tiles of 64; 64 x 2048 x 6144: 15.7 and 15.1).  Tiles need panels of 256
+  // rows below 2^31 bytes (buffer offsets).
+  if (nk == 0 || m <= 32 || n <= 32 || a.lda >= ((int64_t)1 << 23) || a.ldb >= ((int64_t)1 << 23)) return best;
+  const int arith = c_bf16 ? 0 : 1;
+  double best_us = 0.0;
+  for (const TileRate& r : kTileRates) {
+    const int64_t tiles = ceil_div(m, 64 * r.ma) * ceil_div(n, 64 * r.nb);
+    for (int64_t splits = 1; splits <= 16; splits *= 2) {
+      // whole scale words (4 blocks) per workgroup, at least 4 blocks
+      const int64_t blocks = splits == 1 ? nk : ceil_div(ceil_div(nk, splits), 4) * 4;
+      const int64_t used = ceil_div(nk, blocks), groups = tiles * used;
+      if (splits > 1 && (used < 2 || groups > 2 * kCus * r.per_cu)) break;
+      const int64_t full = groups / (kCus * r.per_cu), rest = groups - full * kCus * r.per_cu;
+      double us = full * (r.block[arith][r.per_cu - 1] * blocks + r.round[arith]);
+      if (rest > 0) us += r.block[arith][ceil_div(rest, kCus) - 1] * blocks + r.round[arith];
+      // a launch, a workspace, and partials written and read at about 4 TB/s
+      if (used > 1) us += 6.0 + (double)((2 * used + 1) * m * n) * 4.0 / 4e6;
+      if (best.ma == 0 || us < best_us) {
+        best_us = us;
+        best = MatmulPlan{r.ma, r.nb, (int32_t)used, (int32_t)blocks,
+                          used > 1 ? sizeof(float) * (size_t)(used * m * n) : 0};
+      }
+    }
+  }
+  return best;
+}
 
 extern "C" {
 
@@ -172,12 +250,13 @@ int muonh_block_quantize(const void* x, int32_t dtype, int64_t rows, int64_t col
   });
 }
 
-int muonh_block_matmul_workspace(const muonh_fp8_matrix* a, const muonh_fp8_matrix* b, size_t* bytes) {
+int muonh_block_matmul_workspace(const muonh_fp8_matrix* a, const muonh_fp8_matrix* b, int32_t c_dtype,
+                                 size_t* bytes) {
   return guarded([&]() -> int {
     if (!bytes) return fail(MUONH_EINVAL, "null argument");
-    const int rc = check_operands(a, b);
-    if (rc) return rc;
-    *bytes = 0;
+    int rc;
+    if ((rc = check_operands(a, b)) || (rc = check_dtype(c_dtype, "c"))) return rc;
+    *bytes = plan_block_matmul(c_dtype == MUONH_BF16, matmul_args(*a, *b)).workspace_bytes;
     return MUONH_OK;
   });
 }
@@ -199,23 +278,15 @@ int muonh_block_matmul(const muonh_fp8_matrix* a, const muonh_fp8_matrix* b, voi
         return fail(MUONH_EINVAL, "c overlaps an operand");
     if (ceil_div(a->rows, 16) * ceil_div(b->rows, 16) > kMaxGrid * 4)
       return fail(MUONH_EINVAL, "c is too large for one launch");
-    BlockMatmulArgs p{};
-    p.a = static_cast<const uint8_t*>(a->data);
-    p.b = static_cast<const uint8_t*>(b->data);
-    p.sa = static_cast<const uint8_t*>(a->scale);
-    p.sb = static_cast<const uint8_t*>(b->scale);
-    p.lda = a->ld;
-    p.ldb = b->ld;
-    p.ldsa = a->ld_scale;
-    p.ldsb = b->ld_scale;
+    BlockMatmulArgs p = matmul_args(*a, *b);
     p.c = c;
     p.ldc = ldc;
-    p.m = (int32_t)a->rows;
-    p.n = (int32_t)b->rows;
-    p.kblocks = (int32_t)ceil_div(a->cols, kFp8Block);
-    p.a_shift = a->block_rows == 128 ? 7 : 0;
-    p.b_shift = b->block_rows == 128 ? 7 : 0;
-    return launched(launch_block_matmul(c_dtype == MUONH_BF16, accumulate, p,
+    p.accumulate = accumulate;
+    const MatmulPlan plan = plan_block_matmul(c_dtype == MUONH_BF16, p);
+    if (plan.workspace_bytes > 0 && (!workspace || workspace_bytes < plan.workspace_bytes))
+      return fail(MUONH_ENOMEM, "workspace too small: need " + std::to_string(plan.workspace_bytes) + " bytes");
+    if (!aligned(workspace, kAlign)) return fail(MUONH_EINVAL, "workspace must be 256-byte aligned");
+    return launched(launch_block_matmul(c_dtype == MUONH_BF16, plan, p, static_cast<float*>(workspace),
                                         reinterpret_cast<hipStream_t>(stream)),
                     "block_matmul");
   });

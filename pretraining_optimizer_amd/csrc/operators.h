@@ -42,8 +42,20 @@ struct BlockMatmulArgs {
   int64_t ldc;                    // elements
   int32_t m, n, kblocks;          // kblocks: blocks of 128 along the contraction
   int32_t a_shift, b_shift;       // scale row = row >> shift (0 or 7)
+  int32_t accumulate;
+  int32_t splits, split_blocks;   // set by the launcher: workgroups along the contraction, blocks of each
 };
-hipError_t launch_block_matmul(int c_bf16, int accumulate, const BlockMatmulArgs& a, hipStream_t st);
+
+// How a product runs: 64 ma x 64 nb tiles (ma = 0: the thin kernel), the
+// contraction split over `splits` workgroups of split_blocks blocks each, whose
+// partial matrices then take workspace_bytes.
+struct MatmulPlan {
+  int32_t ma, nb, splits, split_blocks;
+  size_t workspace_bytes;
+};
+MatmulPlan plan_block_matmul(int c_bf16, const BlockMatmulArgs& a);
+hipError_t launch_block_matmul(int c_bf16, const MatmulPlan& plan, const BlockMatmulArgs& a, float* workspace,
+                               hipStream_t st);
 
 struct NormArgs {
   const void* x;

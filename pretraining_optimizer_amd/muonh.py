@@ -152,7 +152,7 @@ _SIGNATURES = [
                                             ctypes.c_int64, ctypes.POINTER(muonh_fp8_matrix),
                                             ctypes.POINTER(muonh_fp8_matrix), ctypes.c_void_p]),
     ("muonh_block_matmul_workspace", ctypes.c_int, [ctypes.POINTER(muonh_fp8_matrix),
-                                                    ctypes.POINTER(muonh_fp8_matrix),
+                                                    ctypes.POINTER(muonh_fp8_matrix), ctypes.c_int32,
                                                     ctypes.POINTER(ctypes.c_size_t)]),
     ("muonh_block_matmul", ctypes.c_int, [ctypes.POINTER(muonh_fp8_matrix), ctypes.POINTER(muonh_fp8_matrix),
                                           ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32,

@@ -46,15 +46,14 @@ def _code(t, what: str) -> int:
     return code
 
 
-def _here(*tensors) -> int:
+def _here(first, *rest) -> int:
     """Every tensor is on the current device, whose index is returned."""
-    for t in tensors:
-        if t is not None and t.get_device() < 0:
-            raise ValueError("all tensors must be CUDA tensors of the current device")
-    dev = _torch.cuda.current_device()
-    for t in tensors:
+    dev = first.get_device()
+    for t in rest:
         if t is not None and t.get_device() != dev:
             raise ValueError("all tensors must be CUDA tensors of the current device")
+    if dev < 0 or dev != _torch.cuda.current_device():
+        raise ValueError("all tensors must be CUDA tensors of the current device")
     return dev
 
 
@@ -87,7 +86,7 @@ def _matrix(t, what: str):
 
 
 def _vector(t, n: int, what: str):
-    if t.dtype is not _torch.float32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+    if t.dtype is not _torch.float32 or t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{what}: a contiguous float32 vector of {n} elements is required")
 
 
@@ -98,6 +97,14 @@ def _empty(shape, dtype, device, stream):
         return _torch.empty(shape, dtype=dtype, device=device)
     with _torch.cuda.stream(stream):
         return _torch.empty(shape, dtype=dtype, device=device)
+
+
+def _like(t, shape, stream):
+    """_empty of t's dtype and device (the quicker call)."""
+    if stream is None:
+        return t.new_empty(shape)
+    with _torch.cuda.stream(stream):
+        return t.new_empty(shape)
 
 
 class Fp8Matrix:
@@ -115,23 +122,23 @@ class Fp8Matrix:
     def __init__(self, data, scale, cols: int, block_rows: int = 1):
         if _torch is None:
             _setup()
-        torch = _torch
-        if data.dtype != torch.float8_e4m3fn or scale.dtype != torch.uint8:
+        if data.dtype is not _torch.float8_e4m3fn or scale.dtype is not _torch.uint8:
             raise TypeError("data must be float8_e4m3fn and scale uint8")
         if data.dim() != 2 or scale.dim() != 2 or not data.is_contiguous() or not scale.is_contiguous():
             raise ValueError("data and scale must be contiguous 2-D tensors")
-        if block_rows not in (1, 128):
+        if block_rows != 1 and block_rows != 128:
             raise ValueError("block_rows must be 1 or 128")
         _here(data, scale)
-        self.data, self.scale = data, scale
-        self.rows, self.cols, self.block_rows = data.shape[0], int(cols), block_rows
-        ld, lds = data.shape[1], scale.shape[1]
-        if not 0 <= self.cols <= ld or ld % 128:
+        rows, ld = data.shape
+        srows, lds = scale.shape
+        cols = int(cols)
+        if not 0 <= cols <= ld or ld % 128:
             raise ValueError("data: its columns must be a multiple of 128 that holds cols")
-        if lds % 4 or lds * 128 < self.cols or scale.shape[0] != -(-self.rows // block_rows):
+        if lds % 4 or lds * 128 < cols or srows != (rows + block_rows - 1) // block_rows:
             raise ValueError("scale: shape does not fit the data's blocks")
-        self._desc = muonh_fp8_matrix(data.data_ptr(), scale.data_ptr(), self.rows, self.cols, ld, lds,
-                                      block_rows, 0)
+        self.data, self.scale = data, scale
+        self.rows, self.cols, self.block_rows = rows, cols, block_rows
+        self._desc = muonh_fp8_matrix(data.data_ptr(), scale.data_ptr(), rows, cols, ld, lds, block_rows, 0)
 
     @classmethod
     def empty(cls, rows: int, cols: int, block_rows: int = 1, device=None, stream=None):
@@ -212,11 +219,11 @@ def fp8_matmul(a: Fp8Matrix, b: Fp8Matrix, out=None, out_dtype=None, accumulate:
     dev = _here(a.data, b.data, out)
     ra, rb = ctypes.byref(a._desc), ctypes.byref(b._desc)
     need = ctypes.c_size_t()
-    rc = _lib.muonh_block_matmul_workspace(ra, rb, ctypes.byref(need))
+    rc = _lib.muonh_block_matmul_workspace(ra, rb, code, ctypes.byref(need))
     if rc:
         _check(rc, "muonh_block_matmul_workspace")
     need = need.value
-    ws = _empty(need, _torch.uint8, out.device, stream) if need else None
+    ws = _like(a.scale, need, stream) if need else None
     if stream is not None:
         _record(stream, [a.data, a.scale, b.data, b.scale, out] + ([] if ws is None else [ws]))
     rc = _lib.muonh_block_matmul(ra, rb, out.data_ptr(), code, ldc, 1 if accumulate else 0,
@@ -233,10 +240,10 @@ def _kind(kind: str) -> int:
     return code
 
 
-def _like(out, x, rows: int, cols: int, what: str, stream):
+def _result(out, x, rows: int, cols: int, what: str, stream):
     """(out, its pitch): x's shape and dtype, new if out is None."""
     if out is None:
-        return _empty((rows, cols), x.dtype, x.device, stream), cols
+        return _like(x, (rows, cols), stream), cols
     if out.shape != x.shape or out.dtype != x.dtype:
         raise ValueError(f"{what}: shape or dtype differs from x")
     return out, _pitch(out, rows, cols, what)
@@ -258,9 +265,9 @@ def norm_forward(x, weight, bias=None, kind: str = "rms", eps: float = 1e-6, out
     if bias is not None:
         _vector(bias, cols, "bias")
     dev = _here(x, weight, bias, out)
-    y, ldy = _like(out, x, rows, cols, "out", stream)
-    rstd = _empty(rows, _torch.float32, x.device, stream)
-    mean = None if kind_code else _empty(rows, _torch.float32, x.device, stream)
+    y, ldy = _result(out, x, rows, cols, "out", stream)
+    rstd = _like(weight, rows, stream)
+    mean = None if kind_code else _like(weight, rows, stream)
     args = muonh_norm_args(x.data_ptr(), weight.data_ptr(), None if bias is None else bias.data_ptr(),
                            y.data_ptr(), None if mean is None else mean.data_ptr(), rstd.data_ptr(), rows, cols,
                            ldx, ldy, code, kind_code, eps, 0)
@@ -300,17 +307,17 @@ def norm_backward(dy, x, weight, mean, rstd, kind: str = "rms", bias: bool = Fal
     if dbias is not None:
         _vector(dbias, cols, "dbias")
     dev = _here(dy, x, weight, mean, rstd, dx, dweight, dbias)
-    dx, ld_dx = _like(dx, x, rows, cols, "dx", stream)
+    dx, ld_dx = _result(dx, x, rows, cols, "dx", stream)
     if dweight is None:
-        dweight = _empty(cols, _torch.float32, x.device, stream)
+        dweight = _like(weight, cols, stream)
     if bias and dbias is None:
-        dbias = _empty(cols, _torch.float32, x.device, stream)
+        dbias = _like(weight, cols, stream)
     need = ctypes.c_size_t()
     rc = _lib.muonh_norm_backward_workspace(rows, cols, ctypes.byref(need))
     if rc:
         _check(rc, "muonh_norm_backward_workspace")
     need = need.value
-    ws = _empty(need, _torch.uint8, x.device, stream) if need else None
+    ws = _like(weight, need // 4, stream) if need else None
     args = muonh_norm_grad_args(
         dy.data_ptr(), x.data_ptr(), weight.data_ptr(), None if mean is None else mean.data_ptr(), rstd.data_ptr(),
         dx.data_ptr(), dweight.data_ptr(), None if dbias is None else dbias.data_ptr(), rows, cols,

@@ -61,8 +61,8 @@ def test_matmul_refusals():
     empty = _mat(rows=0, data=None, scale=None)
     assert call(a=empty, c=None) == mb.MUONH_OK and call(b=empty, c=None, ldc=0) == mb.MUONH_OK
     need = ctypes.c_size_t(7)
-    assert lib.muonh_block_matmul_workspace(ctypes.byref(_mat()), ctypes.byref(_mat()), ctypes.byref(need)) == mb.MUONH_OK
-    _refused(lib.muonh_block_matmul_workspace(ctypes.byref(_mat()), ctypes.byref(_mat()), None), mb.MUONH_EINVAL, "null")
+    assert lib.muonh_block_matmul_workspace(ctypes.byref(_mat()), ctypes.byref(_mat()), pm.MUONH_BF16, ctypes.byref(need)) == mb.MUONH_OK
+    _refused(lib.muonh_block_matmul_workspace(ctypes.byref(_mat()), ctypes.byref(_mat()), pm.MUONH_BF16, None), mb.MUONH_EINVAL, "null")
 
 
 def test_quantize_refusals():
