@@ -370,6 +370,22 @@ int muonh_block_matmul(const muonh_fp8_matrix* a, const muonh_fp8_matrix* b, voi
                        int64_t ldc, int32_t accumulate, void* workspace, size_t workspace_bytes,
                        void* stream);
 
+/* muonh_step (same arguments, same arithmetic: W, M and the statistics come out
+ * bitwise equal) whose update also writes the forms of the updated weights that
+ * the next forward and backward passes multiply by: q[i], the row form of matrix
+ * i, and qt[i], its column form, both with block_rows 128 and the bytes that
+ * muonh_block_quantize gives for the updated W, without reading it again.  q or
+ * qt may be NULL, and an entry whose data is NULL is not written (its other
+ * members are not read).  The outputs must stay valid until the stream has
+ * passed the step, and may change between steps.  The first call on a handle
+ * allocates its tables on the device (12 bytes per 128 x 128 block), which
+ * muonh_destroy releases; not for use while `stream` is being captured.
+ * Errors: as muonh_step; MUONH_EINVAL for an output whose shape, block_rows or
+ * layout does not fit or that overlaps its own W, M or G; MUONH_ENOMEM.     */
+int muonh_step_quantized(muonh_handle* h, const muonh_matrix_desc* mats, int32_t n,
+                         const muonh_fp8_matrix* q, const muonh_fp8_matrix* qt,
+                         const muonh_step_args* args, void* stream);
+
 /* ---- layer norm and RMS norm ----------------------------------------------
  * The norms whose weights muonh_adamw_step trains, over the last axis of
  * x [rows x cols]:

@@ -18,8 +18,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmuonh.so")
-SOURCES = ("muonh.cpp", "adamw.cpp", "operators.cpp", "gemm.hip", "elementwise.hip", "noalloc.hip",
-           "block_fp8.hip", "norm.hip")
+SOURCES = ("muonh.cpp", "adamw.cpp", "operators.cpp", "step_fp8.cpp", "gemm.hip", "elementwise.hip",
+           "noalloc.hip", "block_fp8.hip", "norm.hip")
 ARCH = "gfx950"
 
 

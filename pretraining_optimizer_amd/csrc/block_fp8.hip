@@ -158,48 +158,35 @@ constexpr int kQuantWaves = kQuantThreads / 64;
 constexpr int kQuantRows = kFp8Tile * kFp8Tile / kQuantThreads / 8;   // rows per thread
 static_assert(kQuantRows == 4, "a thread's rows fill one 4-byte unit of the column form");
 
-// One 128 x 128 tile of x per workgroup.  Thread t holds columns 8 (t % 16) ..
-// + 7 of rows 4 (t / 16) .. + 3, so a 16-lane row covers a row's group of 128
-// and a thread holds 4 consecutive values of each of its columns: the row form
-// leaves as 8 bytes per row, the column form goes through LDS as one 4-byte
-// unit per column.  Elements behind the matrix count as zeros, and the padding
-// up to a multiple of 128 is written as such.
+// LDS of one tile.  Column form: row c is column c of x, 32 units of 4 rows;
+// unit u of row c sits at u ^ (2 ((c >> 3) & 15)), so that one store's 16 columns
+// (8 apart) and 4 units meet each bank twice, the least for 64 lanes.
+template <typename T>
+struct QuantLds {
+  __attribute__((aligned(16))) uint8_t tile[kFp8Tile * kFp8Tile];
+  __attribute__((aligned(16))) uint32_t colmax[kQuantWaves][16 * Row8<T>::kWords];
+};
+
+// Quantises and writes the tile (tr, tc) that a workgroup holds: thread t has
+// columns 8 (t % 16) .. + 7 of rows 4 (t / 16) .. + 3 in v, zeros behind the
+// matrix.  A 16-lane row thus covers a row's group of 128 and a thread holds 4
+// consecutive values of each of its columns: the row form leaves as 8 bytes per
+// row, the column form goes through LDS as one 4-byte unit per column.  The
+// padding up to a multiple of 128 is written as zeros.
 //
 // Bound by HBM (one read, one write per form).  What a thread does per element
 // is kept to a mask, two packed maxima and a conversion per form that scales as
 // it converts; Inf and NaN take a path of their own, per thread.
 template <typename T, bool SQUARE>
-__global__ __launch_bounds__(kQuantThreads) void block_quantize_kernel(QuantArgs p, uint32_t ctiles) {
+__device__ __forceinline__ void write_forms(const Row8<T> (&v)[4], const QuantArgs& p, uint32_t tr, uint32_t tc,
+                                            QuantLds<T>& lds) {
   typedef Row8<T> Row;
   constexpr int W = Row::kWords;
-  // Column form of the tile: row c is column c of x, 32 units of 4 rows; unit u
-  // of row c sits at u ^ (2 ((c >> 3) & 15)), so that one store's 16 columns (8
-  // apart) and 4 units meet each bank twice, the least for 64 lanes.
-  __shared__ __attribute__((aligned(16))) uint8_t tile[kFp8Tile * kFp8Tile];
-  __shared__ __attribute__((aligned(16))) uint32_t colmax[kQuantWaves][16 * W];
-
-  const uint32_t tr = blockIdx.x / ctiles, tc = blockIdx.x % ctiles;
+  auto& tile = lds.tile;
+  auto& colmax = lds.colmax;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int cg = tid & 15, rg = tid >> 4;
   const int64_t r0 = (int64_t)tr * kFp8Tile + rg * 4, c0 = (int64_t)tc * kFp8Tile + cg * 8;
-  const T* x = reinterpret_cast<const T*>(p.x);
-
-  Row v[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-#pragma unroll
-    for (int k = 0; k < W; ++k) v[i].w[k] = 0;
-    if (r0 + i < p.rows) {
-      const T* src = x + (r0 + i) * p.ldx + c0;
-      if (c0 + 8 <= p.cols) {
-        v[i].load(src);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (c0 + j < p.cols) v[i].set(j, src + j);
-      }
-    }
-  }
 
   // Largest magnitudes of the thread's rows, and of its columns.
   uint32_t rowmax[4], cmax[W];
@@ -312,6 +299,87 @@ __global__ __launch_bounds__(kQuantThreads) void block_quantize_kernel(QuantArgs
                          (g & 1) ? u32x4_t{r[2], r[3], r[0], r[1]} : r);
     }
   }
+}
+
+// Elements 4 rows x 8 columns of thread t's place in tile (tr, tc) of x.
+template <typename T>
+__device__ __forceinline__ void load_tile(Row8<T> (&v)[4], const T* x, int64_t rows, int64_t cols, int64_t ldx,
+                                          uint32_t tr, uint32_t tc) {
+  const int64_t r0 = (int64_t)tr * kFp8Tile + (threadIdx.x >> 4) * 4;
+  const int64_t c0 = (int64_t)tc * kFp8Tile + (threadIdx.x & 15) * 8;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+#pragma unroll
+    for (int k = 0; k < Row8<T>::kWords; ++k) v[i].w[k] = 0;
+    if (r0 + i < rows) {
+      const T* src = x + (r0 + i) * ldx + c0;
+      if (c0 + 8 <= cols) {
+        v[i].load(src);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (c0 + j < cols) v[i].set(j, src + j);
+      }
+    }
+  }
+}
+
+template <typename T, bool SQUARE>
+__global__ __launch_bounds__(kQuantThreads) void block_quantize_kernel(QuantArgs p, uint32_t ctiles) {
+  __shared__ QuantLds<T> lds;
+  const uint32_t tr = blockIdx.x / ctiles, tc = blockIdx.x % ctiles;
+  Row8<T> v[4];
+  load_tile<T>(v, reinterpret_cast<const T*>(p.x), p.rows, p.cols, p.ldx, tr, tc);
+  write_forms<T, SQUARE>(v, p, tr, tc, lds);
+}
+
+// The update of a MuonH step, W <- k1 W - k2 u, that also writes the block-scaled
+// forms of the updated W: one 128 x 128 tile of one matrix per workgroup, so W is
+// read and written once and never read again for its quantisation.  The update's
+// arithmetic is update_kernel's (the product k2 u rounded, then one fused
+// multiply-add), so W comes out bitwise the same.
+template <typename U>
+__global__ __launch_bounds__(kQuantThreads) void update_quantize_kernel(
+    const StepTile* __restrict__ tiles, const QuantArgs* __restrict__ outs, const MatGeom* __restrict__ geo,
+    const MatPtrs* __restrict__ ptrs, const MatScalars* __restrict__ scal) {
+  __shared__ QuantLds<float> lds;
+  const StepTile t = tiles[blockIdx.x];
+  const QuantArgs p = outs[t.mat];
+  const int64_t rows = p.rows, cols = p.cols;
+  float* w = ptrs[t.mat].w;
+  const float k1 = scal[t.mat].k1, k2 = scal[t.mat].k2;
+  Row8<float> v[4];
+  Row8<U> u[4];
+  load_tile<float>(v, w, rows, cols, cols, t.tr, t.tc);
+  load_tile<U>(u, reinterpret_cast<const U*>(geo[t.mat].U), rows, cols, cols, t.tr, t.tc);
+  const int64_t r0 = (int64_t)t.tr * kFp8Tile + (threadIdx.x >> 4) * 4;
+  const int64_t c0 = (int64_t)t.tc * kFp8Tile + (threadIdx.x & 15) * 8;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      v[i].w[j] = __float_as_uint(__builtin_fmaf(k1, v[i].value(j), -(k2 * u[i].value(j))));
+    if (r0 + i < rows) {
+      float* dst = w + (r0 + i) * cols + c0;
+      if (c0 + 8 <= cols) {
+        typedef uint32_t vec __attribute__((ext_vector_type(4), aligned(4)));
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          __builtin_nontemporal_store(vec{v[i].w[4 * h], v[i].w[4 * h + 1], v[i].w[4 * h + 2], v[i].w[4 * h + 3]},
+                                      (MUONH_GLOBAL vec*)(dst + 4 * h));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (c0 + j < cols) st_global<float>(dst + j, v[i].value(j));
+          else v[i].w[j] = 0;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i].w[j] = 0;   // k1 * 0 may be NaN where the step is
+    }
+  }
+  write_forms<float, true>(v, p, t.tr, t.tc, lds);
 }
 
 // ---------------------------------------------------------------------------
@@ -866,6 +934,17 @@ hipError_t launch_block_quantize(int bf16, int square, const QuantArgs& a, hipSt
     else
       hipLaunchKernelGGL((block_quantize_kernel<float, false>), grid, block, 0, st, a, c);
   }
+  return hipGetLastError();
+}
+
+hipError_t launch_update_quantize(int bf16, const StepTile* tiles, int64_t ntiles, const QuantArgs* outs,
+                                  const MatGeom* geo, const MatPtrs* ptrs, const MatScalars* scal, hipStream_t st) {
+  if (ntiles <= 0) return hipSuccess;
+  const dim3 grid((unsigned)ntiles), block(kQuantThreads);
+  if (bf16)
+    hipLaunchKernelGGL((update_quantize_kernel<uint16_t>), grid, block, 0, st, tiles, outs, geo, ptrs, scal);
+  else
+    hipLaunchKernelGGL((update_quantize_kernel<float>), grid, block, 0, st, tiles, outs, geo, ptrs, scal);
   return hipGetLastError();
 }
 

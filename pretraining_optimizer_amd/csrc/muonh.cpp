@@ -16,6 +16,7 @@
 #include <cstdlib>
 #include <cstring>
 #include <map>
+#include <memory>
 #include <string>
 #include <tuple>
 #include <vector>
@@ -517,6 +518,8 @@ struct muonh_handle {
   hipStream_t cap_stream = nullptr;
   hipGraph_t graph = nullptr;
   hipGraphExec_t graph_exec = nullptr;
+  // What a variant of the step keeps with the handle (see StepTail).
+  std::shared_ptr<void> extension;
 
   template <typename T> T* at(size_t off) { return reinterpret_cast<T*>(ws + off); }
 };
@@ -801,9 +804,10 @@ int prepare_step(muonh_handle* h, const muonh_matrix_desc* mats, int32_t n,
 }
 
 // Enqueues the launches of one step on `st`.  The step size is prm.elr times
-// scale_dev[i], or, when eta_dev is given, eta_dev[i] from device memory.
+// scale_dev[i], or, when eta_dev is given, eta_dev[i] from device memory.  A
+// `tail` takes the place of the update launch.
 int enqueue_step(muonh_handle* h, hipStream_t st, const ElemParams& prm, const float* scale_dev,
-                 const double* eta_dev) {
+                 const double* eta_dev, const StepTail* tail = nullptr) {
   const Plan& pl = h->plan;
   const int32_t n = pl.n;
   const int S = pl.opt.ns_steps;
@@ -865,8 +869,11 @@ int enqueue_step(muonh_handle* h, hipStream_t st, const ElemParams& prm, const f
   LAUNCH(launch_finalize_update(n, geo, part_upd, scal, h->at<muonh_stats>(pl.off_stats),
                                 scale_dev, eta_dev, prm, st));
   if ((rc = record(h, evi++, st))) return rc;
-  LAUNCH(launch_update(bf, h->at<Chunk>(pl.off_chunks), (int64_t)pl.chunks.size(), geo, dptrs,
-                       scal, st));
+  if (tail)
+    LAUNCH(tail->launch(tail->context, bf, geo, dptrs, scal, st));
+  else
+    LAUNCH(launch_update(bf, h->at<Chunk>(pl.off_chunks), (int64_t)pl.chunks.size(), geo, dptrs,
+                         scal, st));
   if ((rc = record(h, evi++, st))) return rc;
 #undef LAUNCH
   if (h->timing) h->ev_pending[h->ev_cur] = true;
@@ -945,6 +952,20 @@ int muonh_step_graph(muonh_handle* h, const muonh_matrix_desc* mats, int32_t n,
 }
 
 }  // extern "C"
+
+std::shared_ptr<void>& muonh::step_extension(muonh_handle* h) { return h->extension; }
+
+int muonh::step_with_tail(muonh_handle* h, const muonh_matrix_desc* mats, int32_t n,
+                          const muonh_step_args* args, hipStream_t st, const StepTail& tail) {
+  const float* scale_dev = nullptr;
+  int rc = prepare_step(h, mats, n, args, st, &scale_dev);
+  if (rc) return rc;
+  if ((rc = tail.prepare(tail.context, st))) return rc;
+  if ((rc = enqueue_step(h, st, step_params(h->plan, args->elr), scale_dev, nullptr, &tail))) return rc;
+  h->last_stream = st;
+  h->steps_done++;
+  return MUONH_OK;
+}
 
 int muonh::run_step_in_workspace(const muonh_matrix_desc* mats, int32_t n, const muonh_options& opt,
                                  const muonh_step_args& args, hipStream_t st, uint8_t* ws,

@@ -67,8 +67,18 @@ int check_pitch(int64_t ld, int64_t cols, const char* what) {
   return MUONH_OK;
 }
 
-// One operand.  `whose` names it in the error text.
-int check_matrix(const muonh_fp8_matrix& m, const char* whose) {
+int64_t data_bytes(const muonh_fp8_matrix& m) {
+  return m.rows > 0 && m.cols > 0 ? extent(m.rows, ceil_div(m.cols, kFp8Block) * kFp8Block, m.ld, 1) : 0;
+}
+int64_t scale_bytes(const muonh_fp8_matrix& m) {
+  return m.rows > 0 && m.cols > 0
+             ? extent(ceil_div(m.rows, m.block_rows), ceil_div(m.cols, kFp8Block), m.ld_scale, 1)
+             : 0;
+}
+
+}  // namespace
+
+int muonh::check_fp8_matrix(const muonh_fp8_matrix& m, const char* whose) {
   const std::string who = std::string(whose) + ": ";
   int rc;
   if ((rc = check_size(m.rows, 0, (who + "rows").c_str()))) return rc;
@@ -87,20 +97,31 @@ int check_matrix(const muonh_fp8_matrix& m, const char* whose) {
   return MUONH_OK;
 }
 
-int64_t data_bytes(const muonh_fp8_matrix& m) {
-  return m.rows > 0 && m.cols > 0 ? extent(m.rows, ceil_div(m.cols, kFp8Block) * kFp8Block, m.ld, 1) : 0;
+void muonh::set_row_form(QuantArgs& a, const muonh_fp8_matrix& m) {
+  a.q = static_cast<uint8_t*>(m.data);
+  a.s = static_cast<uint8_t*>(m.scale);
+  a.ldq = m.ld;
+  a.lds = m.ld_scale;
 }
-int64_t scale_bytes(const muonh_fp8_matrix& m) {
-  return m.rows > 0 && m.cols > 0
-             ? extent(ceil_div(m.rows, m.block_rows), ceil_div(m.cols, kFp8Block), m.ld_scale, 1)
-             : 0;
+
+void muonh::set_column_form(QuantArgs& a, const muonh_fp8_matrix& m) {
+  a.qt = static_cast<uint8_t*>(m.data);
+  a.st = static_cast<uint8_t*>(m.scale);
+  a.ldqt = m.ld;
+  a.ldst = m.ld_scale;
 }
+
+bool muonh::fp8_overlaps(const muonh_fp8_matrix& m, const void* p, int64_t bytes) {
+  return overlap(m.data, data_bytes(m), p, bytes) || overlap(m.scale, scale_bytes(m), p, bytes);
+}
+
+namespace {
 
 int check_operands(const muonh_fp8_matrix* a, const muonh_fp8_matrix* b) {
   if (!a || !b) return fail(MUONH_EINVAL, "null operand");
   int rc;
-  if ((rc = check_matrix(*a, "a"))) return rc;
-  if ((rc = check_matrix(*b, "b"))) return rc;
+  if ((rc = check_fp8_matrix(*a, "a"))) return rc;
+  if ((rc = check_fp8_matrix(*b, "b"))) return rc;
   if (a->cols != b->cols) return fail(MUONH_EINVAL, "a.cols differs from b.cols");
   return MUONH_OK;
 }
@@ -200,11 +221,11 @@ int muonh_block_quantize(const void* x, int32_t dtype, int64_t rows, int64_t col
     if ((rc = check_size(rows, 0, "rows")) || (rc = check_size(cols, 0, "cols"))) return rc;
     if ((rc = check_pitch(ldx, cols, "ldx"))) return rc;
     if (q) {
-      if ((rc = check_matrix(*q, "q"))) return rc;
+      if ((rc = check_fp8_matrix(*q, "q"))) return rc;
       if (q->rows != rows || q->cols != cols) return fail(MUONH_EINVAL, "q: shape differs from x");
     }
     if (qt) {
-      if ((rc = check_matrix(*qt, "qt"))) return rc;
+      if ((rc = check_fp8_matrix(*qt, "qt"))) return rc;
       if (qt->rows != cols || qt->cols != rows) return fail(MUONH_EINVAL, "qt: shape differs from x transposed");
     }
     if (q && qt && q->block_rows != qt->block_rows) return fail(MUONH_EINVAL, "q and qt: block_rows differ");
@@ -213,14 +234,9 @@ int muonh_block_quantize(const void* x, int32_t dtype, int64_t rows, int64_t col
     if (!x) return fail(MUONH_EINVAL, "null x");
     if (!aligned(x, (uintptr_t)size)) return fail(MUONH_EINVAL, "misaligned x");
     for (const muonh_fp8_matrix* m : {q, qt})
-      if (m && (overlap(m->data, data_bytes(*m), x, nx) || overlap(m->scale, scale_bytes(*m), x, nx) ||
-                overlap(m->scale, scale_bytes(*m), m->data, data_bytes(*m))))
+      if (m && (fp8_overlaps(*m, x, nx) || overlap(m->scale, scale_bytes(*m), m->data, data_bytes(*m))))
         return fail(MUONH_EINVAL, "outputs overlap x or each other");
-    if (q && qt &&
-        (overlap(q->data, data_bytes(*q), qt->data, data_bytes(*qt)) ||
-         overlap(q->scale, scale_bytes(*q), qt->scale, scale_bytes(*qt)) ||
-         overlap(q->data, data_bytes(*q), qt->scale, scale_bytes(*qt)) ||
-         overlap(q->scale, scale_bytes(*q), qt->data, data_bytes(*qt))))
+    if (q && qt && (fp8_overlaps(*q, qt->data, data_bytes(*qt)) || fp8_overlaps(*q, qt->scale, scale_bytes(*qt))))
       return fail(MUONH_EINVAL, "outputs overlap x or each other");
     if (ceil_div(rows, kFp8Tile) * ceil_div(cols, kFp8Tile) > kMaxGrid)
       return fail(MUONH_EINVAL, "x is too large for one launch");
@@ -229,21 +245,9 @@ int muonh_block_quantize(const void* x, int32_t dtype, int64_t rows, int64_t col
     a.rows = rows;
     a.cols = cols;
     a.ldx = ldx;
-    int32_t block = 1;
-    if (q) {
-      a.q = static_cast<uint8_t*>(q->data);
-      a.s = static_cast<uint8_t*>(q->scale);
-      a.ldq = q->ld;
-      a.lds = q->ld_scale;
-      block = q->block_rows;
-    }
-    if (qt) {
-      a.qt = static_cast<uint8_t*>(qt->data);
-      a.st = static_cast<uint8_t*>(qt->scale);
-      a.ldqt = qt->ld;
-      a.ldst = qt->ld_scale;
-      block = qt->block_rows;
-    }
+    if (q) set_row_form(a, *q);
+    if (qt) set_column_form(a, *qt);
+    const int32_t block = q ? q->block_rows : qt->block_rows;
     return launched(launch_block_quantize(dtype == MUONH_BF16, block == 128, a,
                                           reinterpret_cast<hipStream_t>(stream)),
                     "block_quantize");
@@ -274,7 +278,7 @@ int muonh_block_matmul(const muonh_fp8_matrix* a, const muonh_fp8_matrix* b, voi
     if (!c) return fail(MUONH_EINVAL, "null c");
     if (!aligned(c, (uintptr_t)size)) return fail(MUONH_EINVAL, "misaligned c");
     for (const muonh_fp8_matrix* m : {a, b})
-      if (overlap(m->data, data_bytes(*m), c, nc) || overlap(m->scale, scale_bytes(*m), c, nc))
+      if (fp8_overlaps(*m, c, nc))
         return fail(MUONH_EINVAL, "c overlaps an operand");
     if (ceil_div(a->rows, 16) * ceil_div(b->rows, 16) > kMaxGrid * 4)
       return fail(MUONH_EINVAL, "c is too large for one launch");

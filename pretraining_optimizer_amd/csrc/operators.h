@@ -31,6 +31,16 @@ struct QuantArgs {
 // bf16: x's type; square: blocks of 128 x 128 (else 1 x 128).
 hipError_t launch_block_quantize(int bf16, int square, const QuantArgs& a, hipStream_t st);
 
+// One workgroup of the step that also quantises: tile (tr, tc) of matrix mat.
+struct StepTile {
+  int32_t mat;
+  uint32_t tr, tc;
+};
+// The update W <- k1 W - k2 u of every tile, and the forms outs[mat] names (x and
+// ldx unused).  bf16: the type of u.
+hipError_t launch_update_quantize(int bf16, const StepTile* tiles, int64_t ntiles, const QuantArgs* outs,
+                                  const MatGeom* geo, const MatPtrs* ptrs, const MatScalars* scal, hipStream_t st);
+
 // C[m][n] (+)= sum_k A[m][k] B[n][k].
 struct BlockMatmulArgs {
   const uint8_t* a;
@@ -85,6 +95,14 @@ struct NormGradArgs {
 // Rows of per-workgroup partial sums of dweight that a backward pass writes.
 int64_t norm_partial_rows(int64_t rows, int64_t cols);
 hipError_t launch_norm_backward(int bf16, int layer, const NormGradArgs& a, hipStream_t st);
+
+// Checks one FP8 operand; `whose` names it in the error text.
+int check_fp8_matrix(const muonh_fp8_matrix& m, const char* whose);
+// Its forms' addresses in QuantArgs.
+void set_row_form(QuantArgs& a, const muonh_fp8_matrix& m);
+void set_column_form(QuantArgs& a, const muonh_fp8_matrix& m);
+// Whether an operand's values or scales share memory with [p, p + bytes).
+bool fp8_overlaps(const muonh_fp8_matrix& m, const void* p, int64_t bytes);
 
 // Runs the body of a C entry point; nothing is thrown across the ABI.
 template <typename F>

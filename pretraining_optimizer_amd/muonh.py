@@ -157,6 +157,9 @@ _SIGNATURES = [
     ("muonh_block_matmul", ctypes.c_int, [ctypes.POINTER(muonh_fp8_matrix), ctypes.POINTER(muonh_fp8_matrix),
                                           ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32,
                                           ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    ("muonh_step_quantized", ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(muonh_matrix_desc), ctypes.c_int32,
+                                            ctypes.POINTER(muonh_fp8_matrix), ctypes.POINTER(muonh_fp8_matrix),
+                                            ctypes.POINTER(muonh_step_args), ctypes.c_void_p]),
     ("muonh_norm_forward", ctypes.c_int, [ctypes.POINTER(muonh_norm_args), ctypes.c_void_p]),
     ("muonh_norm_backward_workspace", ctypes.c_int, [ctypes.c_int64, ctypes.c_int64,
                                                      ctypes.POINTER(ctypes.c_size_t)]),
@@ -301,8 +304,13 @@ class MuonH:
         self._descs = descs
 
     def step(self, grads: Sequence, elr: float, elr_scale: Optional[Sequence[float]] = None,
-             step: int = 0, stream=None, graph: bool = False):
-        """One step; graph=True goes through muonh_step_graph (a recorded HIP graph)."""
+             step: int = 0, stream=None, graph: bool = False, fp8: Optional[Sequence] = None):
+        """One step; graph=True goes through muonh_step_graph (a recorded HIP graph).
+
+        fp8: one pair (q, qt) per matrix, or None for a matrix: Fp8Matrix
+        operands with block_rows 128 (row form and column form, either may be
+        None) that receive the updated weight, as fp8_quantize(w,
+        form="both", block_rows=128) would write it."""
         if len(grads) != self.n:
             raise ValueError("one gradient per matrix is required")
         d = self._descs
@@ -322,9 +330,31 @@ class MuonH:
             scale_arr = (ctypes.c_float * self.n)(*[float(x) for x in elr_scale])
             args.elr_scale = ctypes.cast(scale_arr, ctypes.POINTER(ctypes.c_float))
         args.step = int(step)
+        if fp8 is not None:
+            if graph:
+                raise ValueError("a recorded step does not write FP8 weights")
+            self._step_quantized(fp8, args, stream)
+            return
         fn, name = ((self._lib.muonh_step_graph, "muonh_step_graph") if graph
                     else (self._lib.muonh_step, "muonh_step"))
         _check(fn(self._h, d, self.n, ctypes.byref(args), _stream_ptr(stream)), name)
+
+    def _step_quantized(self, fp8, args, stream):
+        if len(fp8) != self.n:
+            raise ValueError("one (q, qt) pair per matrix is required")
+        forms = [(muonh_fp8_matrix * self.n)(), (muonh_fp8_matrix * self.n)()]
+        used = []
+        for i, pair in enumerate(fp8):
+            for k, m in enumerate(pair or (None, None)):
+                if m is None:
+                    continue
+                if m.data.device != self.weights[i].device:
+                    raise ValueError(f"matrix {i}: the FP8 operand is on another device")
+                forms[k][i] = m._desc
+                used += [m.data, m.scale]
+        _record(stream, used)
+        _check(self._lib.muonh_step_quantized(self._h, self._descs, self.n, forms[0], forms[1], ctypes.byref(args),
+                                              _stream_ptr(stream)), "muonh_step_quantized")
 
     def radii(self) -> List[float]:
         out = (ctypes.c_float * self.n)()

@@ -151,3 +151,12 @@ def test_empty_norm_needs_no_rows():
     assert lib.muonh_norm_forward(ctypes.byref(_norm(rows=0, x=None, y=None, rstd=None)), None) == mb.MUONH_OK
     _refused(lib.muonh_norm_forward(None, None), mb.MUONH_EINVAL, "null")
     _refused(lib.muonh_norm_backward(None, None), mb.MUONH_EINVAL, "null")
+
+
+def test_quantized_step_refusals():
+    lib = pm.load_library()
+    mats = mb.shape_descs([(256, 128)])
+    args = mb.muonh_step_args()
+    q = _mat(256, 128, block=128)
+    for call in ((None, mats, 1, ctypes.byref(q), None, ctypes.byref(args)),):
+        _refused(lib.muonh_step_quantized(*call, None), mb.MUONH_EINVAL, "null")
