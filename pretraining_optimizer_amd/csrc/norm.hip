@@ -444,7 +444,7 @@ constexpr int64_t kRegisterCols = 16384;   // 1024 threads of 16 elements
 
 // Rows that a workgroup of `threads` takes at a time (the kernels' kRows).
 int64_t rows_at_once(int64_t cols, int64_t threads) {
-  const int64_t group = cols <= 128 ? 16 : cols <= 256 ? 32 : cols <= 1024 ? 64 : cols <= 2048 ? 128
+  const int64_t group = cols <= 64 ? 8 : cols <= 128 ? 16 : cols <= 256 ? 32 : cols <= 1024 ? 64 : cols <= 2048 ? 128
                         : cols <= 4096 ? 256 : cols <= 8192 ? 512 : 1024;
   return std::max<int64_t>(threads / group, 1);
 }
@@ -462,7 +462,8 @@ hipError_t forward_for(const NormArgs& a, hipStream_t st) {
 #define MUONH_NORM_FWD(G, NV)                                                                  \
   hipLaunchKernelGGL((norm_forward_kernel<T, LAYER, G, NV>), grid,                             \
                      dim3(G > kNormThreads ? G : kNormThreads), 0, st, a)
-  if (cols <= 128) MUONH_NORM_FWD(16, 1);
+  if (cols <= 64) MUONH_NORM_FWD(8, 1);
+  else if (cols <= 128) MUONH_NORM_FWD(16, 1);
   else if (cols <= 256) MUONH_NORM_FWD(32, 1);
   else if (cols <= 512) MUONH_NORM_FWD(64, 1);
   else if (cols <= 1024) MUONH_NORM_FWD(64, 2);
@@ -484,6 +485,7 @@ hipError_t backward_for(const NormGradArgs& a, hipStream_t st) {
                      dim3(G > kBackThreads ? G : kBackThreads), 0, st, a)
     if (cols > kRegisterCols)
       hipLaunchKernelGGL((norm_backward_long_kernel<T, LAYER, BIAS>), grid, dim3(kLongThreads), 0, st, a);
+    else if (cols <= 64) MUONH_NORM_BWD(8, 1);
     else if (cols <= 128) MUONH_NORM_BWD(16, 1);
     else if (cols <= 256) MUONH_NORM_BWD(32, 1);
     else if (cols <= 512) MUONH_NORM_BWD(64, 1);
@@ -507,9 +509,9 @@ hipError_t backward_for(const NormGradArgs& a, hipStream_t st) {
 int64_t norm_partial_rows(int64_t rows, int64_t cols) {
   const int64_t per = cols > kRegisterCols ? 1 : rows_at_once(cols, kBackThreads);
   const int64_t trips = (rows + per - 1) / per;
-  // every workgroup's row of partials is written and read again: at least 4
+  // every workgroup's row of partials is written and read again: at least 2
   // trips each, unless that leaves fewer than 64 workgroups
-  return std::min<int64_t>(std::min<int64_t>(trips, std::max<int64_t>(64, (trips + 3) / 4)), kNormGroups);
+  return std::min<int64_t>(std::min<int64_t>(trips, std::max<int64_t>(64, (trips + 1) / 2)), kNormGroups);
 }
 
 hipError_t launch_norm_forward(int bf16, int layer, const NormArgs& a, hipStream_t st) {
