@@ -29,6 +29,12 @@ typedef int i32x8_t __attribute__((ext_vector_type(8)));
 // ---------------------------------------------------------------------------
 // quantiser
 
+template <bool NT, typename V>
+__device__ __forceinline__ V load_vec(const void* p) {
+  if constexpr (NT) return __builtin_nontemporal_load((const MUONH_GLOBAL V*)p);
+  return ld_global<V>(p);
+}
+
 // Eight consecutive elements of a row in the type they are stored in.  Rows may
 // start at any element: global loads of any width need no more than element
 // alignment on gfx950.  kWords registers hold them; for bf16 a magnitude is 15
@@ -40,8 +46,9 @@ template <> struct Row8<uint16_t> {
   typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
   typedef uint32_t vec __attribute__((ext_vector_type(4), aligned(2)));
   uint32_t w[kWords];
+  template <bool NT>
   __device__ __forceinline__ void load(const uint16_t* p) {
-    const vec r = __builtin_nontemporal_load((const MUONH_GLOBAL vec*)p);
+    const vec r = load_vec<NT, vec>(p);
 #pragma unroll
     for (int k = 0; k < 4; ++k) w[k] = r[k];
   }
@@ -73,9 +80,9 @@ template <> struct Row8<float> {
   static constexpr uint32_t kInf = 0x7f800000u;
   typedef uint32_t vec __attribute__((ext_vector_type(4), aligned(4)));
   uint32_t w[kWords];
+  template <bool NT>
   __device__ __forceinline__ void load(const float* p) {
-    const vec lo = __builtin_nontemporal_load((const MUONH_GLOBAL vec*)p);
-    const vec hi = __builtin_nontemporal_load((const MUONH_GLOBAL vec*)(p + 4));
+    const vec lo = load_vec<NT, vec>(p), hi = load_vec<NT, vec>(p + 4);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       w[k] = lo[k];
@@ -302,7 +309,7 @@ __device__ __forceinline__ void write_forms(const Row8<T> (&v)[4], const QuantAr
 }
 
 // Elements 4 rows x 8 columns of thread t's place in tile (tr, tc) of x.
-template <typename T>
+template <bool NT, typename T>
 __device__ __forceinline__ void load_tile(Row8<T> (&v)[4], const T* x, int64_t rows, int64_t cols, int64_t ldx,
                                           uint32_t tr, uint32_t tc) {
   const int64_t r0 = (int64_t)tr * kFp8Tile + (threadIdx.x >> 4) * 4;
@@ -314,7 +321,7 @@ __device__ __forceinline__ void load_tile(Row8<T> (&v)[4], const T* x, int64_t r
     if (r0 + i < rows) {
       const T* src = x + (r0 + i) * ldx + c0;
       if (c0 + 8 <= cols) {
-        v[i].load(src);
+        v[i].template load<NT>(src);
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -324,12 +331,19 @@ __device__ __forceinline__ void load_tile(Row8<T> (&v)[4], const T* x, int64_t r
   }
 }
 
+// Activations and gradients have just been written and are read here for the
+// last time: non-temporal loads (a norm and the quantisation of its output,
+// 8192 x 2048 bf16: 27.0 us, 28.2 with ordinary loads).  Weights have not, and
+// are read again by the next step (6144 x 2048 fp32: 12.7 us with ordinary
+// loads, 17.5).  The forms are stored ordinarily, as a product reads them next
+// (quantisation and product, 8192 x 2048 x 6144: 116 us, 128 with non-temporal
+// stores).
 template <typename T, bool SQUARE>
 __global__ __launch_bounds__(kQuantThreads) void block_quantize_kernel(QuantArgs p, uint32_t ctiles) {
   __shared__ QuantLds<T> lds;
   const uint32_t tr = blockIdx.x / ctiles, tc = blockIdx.x % ctiles;
   Row8<T> v[4];
-  load_tile<T>(v, reinterpret_cast<const T*>(p.x), p.rows, p.cols, p.ldx, tr, tc);
+  load_tile<!SQUARE, T>(v, reinterpret_cast<const T*>(p.x), p.rows, p.cols, p.ldx, tr, tc);
   write_forms<T, SQUARE>(v, p, tr, tc, lds);
 }
 
@@ -350,8 +364,8 @@ __global__ __launch_bounds__(kQuantThreads) void update_quantize_kernel(
   const float k1 = scal[t.mat].k1, k2 = scal[t.mat].k2;
   Row8<float> v[4];
   Row8<U> u[4];
-  load_tile<float>(v, w, rows, cols, cols, t.tr, t.tc);
-  load_tile<U>(u, reinterpret_cast<const U*>(geo[t.mat].U), rows, cols, cols, t.tr, t.tc);
+  load_tile<true, float>(v, w, rows, cols, cols, t.tr, t.tc);
+  load_tile<true, U>(u, reinterpret_cast<const U*>(geo[t.mat].U), rows, cols, cols, t.tr, t.tc);
   const int64_t r0 = (int64_t)t.tr * kFp8Tile + (threadIdx.x >> 4) * 4;
   const int64_t c0 = (int64_t)t.tc * kFp8Tile + (threadIdx.x & 15) * 8;
 #pragma unroll
@@ -512,6 +526,16 @@ __device__ __forceinline__ void wait_loads() {
 constexpr int kBufferConfig = 0x00020000;   // raw, unformatted buffer access
 constexpr int kSgMfma = 0x008, kSgVmemRead = 0x020, kSgDsRead = 0x100;
 #define MUONH_SG(mask, n) __builtin_amdgcn_sched_group_barrier((mask), (n), 0)
+
+// A result larger than the caches keep goes past them (8192 x 12288 bf16, 201
+// MB: 180 us, 203 with ordinary stores; 8192 x 4096, 67 MB: 63.6 and 62.3, and
+// what reads it next finds it there).
+constexpr int64_t kStreamBytes = (int64_t)128 << 20;
+template <typename V>
+__device__ __forceinline__ void store_vec(void* p, V v, int stream) {
+  if (stream) __builtin_nontemporal_store(v, (MUONH_GLOBAL V*)p);
+  else st_global<V>(p, v);
+}
 
 constexpr int kTileThreads = 256;
 constexpr int kScaleBlocks = 16;   // scales staged at a time, per row
@@ -813,7 +837,7 @@ __global__ __launch_bounds__(kTileThreads) void block_matmul_tile_kernel(BlockMa
       if constexpr (sizeof(C) == 2) {
         typedef uint32_t vec __attribute__((ext_vector_type(4), aligned(2)));
         if (col + 8 <= cols) {
-          __builtin_nontemporal_store((vec)v, (MUONH_GLOBAL vec*)d);
+          store_vec<vec>(d, (vec)v, p.stream_c);
         } else {
 #pragma unroll
           for (int e = 0; e < 8; ++e)
@@ -825,7 +849,7 @@ __global__ __launch_bounds__(kTileThreads) void block_matmul_tile_kernel(BlockMa
         if (col + 4 <= cols) {
           vec x = o;
           if (p.accumulate) x += ld_global<vec>(d);
-          __builtin_nontemporal_store(x, (MUONH_GLOBAL vec*)d);
+          store_vec<vec>(d, x, p.stream_c);
         } else {
           store_c<float>(d, cols - col, p.accumulate, o);
         }
@@ -892,6 +916,7 @@ hipError_t matmul_for(const MatmulPlan& pl, BlockMatmulArgs a, float* workspace,
   constexpr bool kFp8 = sizeof(C) == 2;
   a.splits = 1;
   a.split_blocks = a.kblocks;
+  a.stream_c = (int64_t)a.m * a.n * (int64_t)sizeof(C) >= kStreamBytes;
   if (pl.ma == 0) {
     const unsigned ntiles = (unsigned)((a.n + 15) / 16);
     const dim3 grid(ntiles * (unsigned)((a.m + 15) / 16));
@@ -909,6 +934,7 @@ hipError_t matmul_for(const MatmulPlan& pl, BlockMatmulArgs a, float* workspace,
   part.c = workspace;
   part.ldc = a.n;
   part.accumulate = 0;
+  part.stream_c = 0;
   const hipError_t e = launch_tiles<kFp8, float>(pl, part, st);
   if (e != hipSuccess) return e;
   const int64_t groups = ((int64_t)a.m * a.n + 1023) / 1024;

@@ -35,7 +35,7 @@ template <> struct Raw8<uint16_t> {
   typedef uint32_t vec __attribute__((ext_vector_type(4), aligned(2)));
   vec w;
   __device__ __forceinline__ void load(const uint16_t* p) {
-    w = __builtin_nontemporal_load((const MUONH_GLOBAL vec*)p);
+    w = ld_global<vec>(p);
   }
   __device__ __forceinline__ void zero() { w = vec{0, 0, 0, 0}; }
   __device__ __forceinline__ void set(int j, const uint16_t* p) {
@@ -53,7 +53,7 @@ template <> struct Raw8<uint16_t> {
     vec r;
 #pragma unroll
     for (int k = 0; k < 4; ++k) r[k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
-    __builtin_nontemporal_store(r, (MUONH_GLOBAL vec*)p);
+    st_global<vec>(p, r);
   }
   static __device__ __forceinline__ void store1(uint16_t* p, float v) { st_global<uint16_t>(p, f32_to_bf16(v)); }
 };
@@ -61,8 +61,8 @@ template <> struct Raw8<float> {
   typedef float vec __attribute__((ext_vector_type(4), aligned(4)));
   vec lo, hi;
   __device__ __forceinline__ void load(const float* p) {
-    lo = __builtin_nontemporal_load((const MUONH_GLOBAL vec*)p);
-    hi = __builtin_nontemporal_load((const MUONH_GLOBAL vec*)(p + 4));
+    lo = ld_global<vec>(p);
+    hi = ld_global<vec>(p + 4);
   }
   __device__ __forceinline__ void zero() { lo = hi = vec{0.0f, 0.0f, 0.0f, 0.0f}; }
   __device__ __forceinline__ void set(int j, const float* p) {
@@ -79,8 +79,8 @@ template <> struct Raw8<float> {
   }
   static __device__ __forceinline__ float load1(const float* p) { return ld_global<float>(p); }
   static __device__ __forceinline__ void store(float* p, const float (&v)[8]) {
-    __builtin_nontemporal_store(vec{v[0], v[1], v[2], v[3]}, (MUONH_GLOBAL vec*)p);
-    __builtin_nontemporal_store(vec{v[4], v[5], v[6], v[7]}, (MUONH_GLOBAL vec*)(p + 4));
+    st_global<vec>(p, vec{v[0], v[1], v[2], v[3]});
+    st_global<vec>(p + 4, vec{v[4], v[5], v[6], v[7]});
   }
   static __device__ __forceinline__ void store1(float* p, float v) { st_global<float>(p, v); }
 };
