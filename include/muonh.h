@@ -381,7 +381,8 @@ int muonh_block_matmul(const muonh_fp8_matrix* a, const muonh_fp8_matrix* b, voi
  * allocates its tables on the device (12 bytes per 128 x 128 block), which
  * muonh_destroy releases; not for use while `stream` is being captured.
  * Errors: as muonh_step; MUONH_EINVAL for an output whose shape, block_rows or
- * layout does not fit or that overlaps its own W, M or G; MUONH_ENOMEM.     */
+ * layout does not fit, that overlaps its own W, M or G or that is named twice;
+ * MUONH_ENOMEM.                                                             */
 int muonh_step_quantized(muonh_handle* h, const muonh_matrix_desc* mats, int32_t n,
                          const muonh_fp8_matrix* q, const muonh_fp8_matrix* qt,
                          const muonh_step_args* args, void* stream);
@@ -409,7 +410,7 @@ typedef struct muonh_norm_args {
   float*       mean;     /* [rows]; NULL for MUONH_NORM_RMS                   */
   float*       rstd;     /* [rows]                                            */
   int64_t      rows;     /* >= 0                                              */
-  int64_t      cols;     /* >= 1                                              */
+  int64_t      cols;     /* 1 .. 2^26                                         */
   int64_t      ldx, ldy; /* elements between rows                             */
   int32_t      dtype;
   int32_t      kind;     /* MUONH_NORM_*                                      */
@@ -430,7 +431,7 @@ typedef struct muonh_norm_grad_args {
   float*       dweight;   /* [cols]                                           */
   float*       dbias;     /* [cols] or NULL                                   */
   int64_t      rows;      /* >= 0; with 0 rows dweight and dbias are zero     */
-  int64_t      cols;      /* >= 1                                             */
+  int64_t      cols;      /* 1 .. 2^26                                        */
   int64_t      ld_dy, ldx, ld_dx;
   int32_t      dtype;
   int32_t      kind;

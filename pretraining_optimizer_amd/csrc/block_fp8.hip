@@ -160,7 +160,7 @@ __device__ __forceinline__ uint32_t max16(uint32_t v) {
   return v;
 }
 
-constexpr int kQuantThreads = 512;
+constexpr int kQuantThreads = kQuantizeThreads;
 constexpr int kQuantWaves = kQuantThreads / 64;
 constexpr int kQuantRows = kFp8Tile * kFp8Tile / kQuantThreads / 8;   // rows per thread
 static_assert(kQuantRows == 4, "a thread's rows fill one 4-byte unit of the column form");
@@ -904,7 +904,6 @@ hipError_t launch_tiles(const MatmulPlan& pl, const BlockMatmulArgs& a, hipStrea
   MUONH_TILE(4, 4)
   MUONH_TILE(4, 3)
   MUONH_TILE(3, 4)
-  MUONH_TILE(4, 2)
   MUONH_TILE(2, 2)
   MUONH_TILE(1, 1)
 #undef MUONH_TILE

@@ -20,7 +20,8 @@ int launched(hipError_t e, const char* what) {
 }
 
 constexpr int64_t kMaxRows = (int64_t)1 << 30;    // row and column counts: tile arithmetic is 32 bits
-constexpr int64_t kMaxGrid = (int64_t)1 << 22;    // workgroups of up to 1024 threads in one launch
+constexpr int64_t kMaxNormCols = (int64_t)1 << 26;
+constexpr int64_t kMaxThreads = ((int64_t)1 << 32) - 1;   // of one launch
 constexpr size_t kAlign = 256;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -59,6 +60,11 @@ int check_size(int64_t v, int64_t least, const char* what) {
   if (v < least || v > kMaxRows)
     return fail(MUONH_EINVAL, std::string(what) + " must be in [" + std::to_string(least) + ", 2^30]");
   return MUONH_OK;
+}
+
+int check_norm_size(int64_t rows, int64_t cols) {
+  if (cols < 1 || cols > kMaxNormCols) return fail(MUONH_EINVAL, "cols must be in [1, 2^26]");
+  return check_size(rows, 0, "rows");
 }
 
 int check_pitch(int64_t ld, int64_t cols, const char* what) {
@@ -164,7 +170,6 @@ constexpr TileRate kTileRates[] = {
     {4, 4, 1, {{1.61, 0, 0, 0}, {2.88, 0, 0, 0}}, {8.8, 16.3}},
     {4, 3, 1, {{1.20, 0, 0, 0}, {2.17, 0, 0, 0}}, {10.0, 13.1}},
     {3, 4, 1, {{1.20, 0, 0, 0}, {2.17, 0, 0, 0}}, {10.0, 13.1}},
-    {4, 2, 1, {{0.88, 0, 0, 0}, {1.53, 0, 0, 0}}, {7.3, 8.4}},
     {2, 2, 2, {{0.64, 0.88, 0, 0}, {0.90, 1.64, 0, 0}}, {4.0, 6.0}},
     {1, 1, 4, {{0.28, 0.44, 0.62, 0.79}, {0.40, 0.58, 0.85, 1.12}}, {3.5, 4.0}},
 };
@@ -184,8 +189,10 @@ MatmulPlan muonh::plan_block_matmul(int c_bf16, const BlockMatmulArgs& a) {
   // Up to 32 rows (or columns) are bound by reading the other operand, which the
   // thin kernel does with more loads in flight (32 x 2048 x 6144: 9.3 us, 15.2
   // in tiles of 64; 64 x 2048 x 6144: 15.7 and 15.1).  Tiles need panels of 256
-  // rows below 2^31 bytes (buffer offsets).
-  if (nk == 0 || m <= 32 || n <= 32 || a.lda >= ((int64_t)1 << 23) || a.ldb >= ((int64_t)1 << 23)) return best;
+  // rows of values and of scales below 2^31 bytes (buffer offsets).
+  const int64_t most = (int64_t)1 << 23;
+  if (nk == 0 || m <= 32 || n <= 32 || a.lda >= most || a.ldb >= most || a.ldsa >= most || a.ldsb >= most)
+    return best;
   const int arith = c_bf16 ? 0 : 1;
   double best_us = 0.0;
   for (const TileRate& r : kTileRates) {
@@ -238,7 +245,7 @@ int muonh_block_quantize(const void* x, int32_t dtype, int64_t rows, int64_t col
         return fail(MUONH_EINVAL, "outputs overlap x or each other");
     if (q && qt && (fp8_overlaps(*q, qt->data, data_bytes(*qt)) || fp8_overlaps(*q, qt->scale, scale_bytes(*qt))))
       return fail(MUONH_EINVAL, "outputs overlap x or each other");
-    if (ceil_div(rows, kFp8Tile) * ceil_div(cols, kFp8Tile) > kMaxGrid)
+    if (ceil_div(rows, kFp8Tile) * ceil_div(cols, kFp8Tile) * kQuantizeThreads > kMaxThreads)
       return fail(MUONH_EINVAL, "x is too large for one launch");
     QuantArgs a{};
     a.x = x;
@@ -280,13 +287,14 @@ int muonh_block_matmul(const muonh_fp8_matrix* a, const muonh_fp8_matrix* b, voi
     for (const muonh_fp8_matrix* m : {a, b})
       if (fp8_overlaps(*m, c, nc))
         return fail(MUONH_EINVAL, "c overlaps an operand");
-    if (ceil_div(a->rows, 16) * ceil_div(b->rows, 16) > kMaxGrid * 4)
-      return fail(MUONH_EINVAL, "c is too large for one launch");
     BlockMatmulArgs p = matmul_args(*a, *b);
     p.c = c;
     p.ldc = ldc;
     p.accumulate = accumulate;
     const MatmulPlan plan = plan_block_matmul(c_dtype == MUONH_BF16, p);
+    const int64_t tile_a = plan.ma ? 64 * plan.ma : 16, tile_b = plan.ma ? 64 * plan.nb : 16;
+    if (ceil_div(p.m, tile_a) * ceil_div(p.n, tile_b) * plan.splits * 256 > kMaxThreads)
+      return fail(MUONH_EINVAL, "c is too large for one launch");
     if (plan.workspace_bytes > 0 && (!workspace || workspace_bytes < plan.workspace_bytes))
       return fail(MUONH_ENOMEM, "workspace too small: need " + std::to_string(plan.workspace_bytes) + " bytes");
     if (!aligned(workspace, kAlign)) return fail(MUONH_EINVAL, "workspace must be 256-byte aligned");
@@ -304,7 +312,7 @@ int muonh_norm_forward(const muonh_norm_args* g, void* stream) {
     if (g->kind != MUONH_NORM_LAYER && g->kind != MUONH_NORM_RMS) return fail(MUONH_EINVAL, "unknown norm kind");
     if (g->reserved != 0) return fail(MUONH_EINVAL, "reserved != 0");
     if (!(g->eps >= 0.0f) || !std::isfinite(g->eps)) return fail(MUONH_EINVAL, "eps must be >= 0 and finite");
-    if ((rc = check_size(g->rows, 0, "rows")) || (rc = check_size(g->cols, 1, "cols"))) return rc;
+    if ((rc = check_norm_size(g->rows, g->cols))) return rc;
     if ((rc = check_pitch(g->ldx, g->cols, "ldx")) || (rc = check_pitch(g->ldy, g->cols, "ldy"))) return rc;
     const int layer = g->kind == MUONH_NORM_LAYER;
     if (!layer && g->mean) return fail(MUONH_EINVAL, "mean must be NULL for MUONH_NORM_RMS");
@@ -338,7 +346,7 @@ int muonh_norm_backward_workspace(int64_t rows, int64_t cols, size_t* bytes) {
   return guarded([&]() -> int {
     if (!bytes) return fail(MUONH_EINVAL, "null argument");
     int rc;
-    if ((rc = check_size(rows, 0, "rows")) || (rc = check_size(cols, 1, "cols"))) return rc;
+    if ((rc = check_norm_size(rows, cols))) return rc;
     *bytes = (size_t)(2 * norm_partial_rows(rows, cols) * cols) * sizeof(float);
     return MUONH_OK;
   });
@@ -352,7 +360,7 @@ int muonh_norm_backward(const muonh_norm_grad_args* g, void* stream) {
     if (g->kind != MUONH_NORM_LAYER && g->kind != MUONH_NORM_RMS) return fail(MUONH_EINVAL, "unknown norm kind");
     if (g->reserved != 0) return fail(MUONH_EINVAL, "reserved != 0");
     if (g->accumulate != 0 && g->accumulate != 1) return fail(MUONH_EINVAL, "accumulate must be 0 or 1");
-    if ((rc = check_size(g->rows, 0, "rows")) || (rc = check_size(g->cols, 1, "cols"))) return rc;
+    if ((rc = check_norm_size(g->rows, g->cols))) return rc;
     if ((rc = check_pitch(g->ld_dy, g->cols, "ld_dy")) || (rc = check_pitch(g->ldx, g->cols, "ldx")) ||
         (rc = check_pitch(g->ld_dx, g->cols, "ld_dx")))
       return rc;

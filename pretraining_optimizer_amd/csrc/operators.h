@@ -15,6 +15,7 @@ namespace muonh {
 
 constexpr int kFp8Block = 128;   // elements of the contraction that share a scale
 constexpr int kFp8Tile = 128;    // the quantiser's tile: 128 x 128 elements per workgroup
+constexpr int kQuantizeThreads = 512;
 
 // The quantiser's view of one matrix: x [rows x cols], and the outputs of its
 // row form (q, s) and of its column form (qt, st); a null q or qt is not written.

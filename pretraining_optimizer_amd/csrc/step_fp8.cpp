@@ -5,6 +5,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cstring>
 #include <memory>
 #include <string>
@@ -144,6 +145,14 @@ extern "C" int muonh_step_quantized(muonh_handle* h, const muonh_matrix_desc* ma
         set_column_form(a, qt[i]);
       }
     }
+    // an output named twice would be written by two matrices at once
+    std::vector<const void*> named;
+    for (const QuantArgs& a : outs)
+      for (const void* p : {(const void*)a.q, (const void*)a.qt, (const void*)a.s, (const void*)a.st})
+        if (p) named.push_back(p);
+    std::sort(named.begin(), named.end());
+    if (std::adjacent_find(named.begin(), named.end()) != named.end())
+      return fail(MUONH_EINVAL, "an output is named twice");
     Context c{h, mats, n, &outs, nullptr};
     return step_with_tail(h, mats, n, args, reinterpret_cast<hipStream_t>(stream),
                           StepTail{prepare, launch, &c});

@@ -115,9 +115,18 @@ class Fp8Matrix:
     scale      : uint8 exponents [rows or ceil(rows / 128), ld_scale], ld_scale a
                  multiple of 4 >= ceil(cols / 128)
     block_rows : 1 (a scale per row and 128 columns) or 128 (per 128 x 128)
+
+    The tensors' contents may change, the tensors themselves not (they are
+    read-only attributes, and the library is given their addresses).
     """
 
-    __slots__ = ("data", "scale", "rows", "cols", "block_rows", "_desc")
+    __slots__ = ("_data", "_scale", "_rows", "_cols", "_block_rows", "_desc")
+
+    data = property(lambda self: self._data)
+    scale = property(lambda self: self._scale)
+    rows = property(lambda self: self._rows)
+    cols = property(lambda self: self._cols)
+    block_rows = property(lambda self: self._block_rows)
 
     def __init__(self, data, scale, cols: int, block_rows: int = 1):
         if _torch is None:
@@ -136,8 +145,8 @@ class Fp8Matrix:
             raise ValueError("data: its columns must be a multiple of 128 that holds cols")
         if lds % 4 or lds * 128 < cols or srows != (rows + block_rows - 1) // block_rows:
             raise ValueError("scale: shape does not fit the data's blocks")
-        self.data, self.scale = data, scale
-        self.rows, self.cols, self.block_rows = rows, cols, block_rows
+        self._data, self._scale = data, scale
+        self._rows, self._cols, self._block_rows = rows, cols, block_rows
         self._desc = muonh_fp8_matrix(data.data_ptr(), scale.data_ptr(), rows, cols, ld, lds, block_rows, 0)
 
     @classmethod
@@ -151,10 +160,10 @@ class Fp8Matrix:
         ld = (cols + 127) // 128 * 128
         lds = (ld + 511) // 512 * 4
         m = cls.__new__(cls)
-        m.rows, m.cols, m.block_rows = rows, cols, block_rows
-        m.data = _empty((rows, ld), _torch.float8_e4m3fn, device, stream)
-        m.scale = _empty(((rows + block_rows - 1) // block_rows, lds), _torch.uint8, device, stream)
-        m._desc = muonh_fp8_matrix(m.data.data_ptr(), m.scale.data_ptr(), rows, cols, ld, lds, block_rows, 0)
+        m._rows, m._cols, m._block_rows = rows, cols, block_rows
+        m._data = _empty((rows, ld), _torch.float8_e4m3fn, device, stream)
+        m._scale = _empty(((rows + block_rows - 1) // block_rows, lds), _torch.uint8, device, stream)
+        m._desc = muonh_fp8_matrix(m._data.data_ptr(), m._scale.data_ptr(), rows, cols, ld, lds, block_rows, 0)
         return m
 
 
@@ -203,9 +212,9 @@ def fp8_matmul(a: Fp8Matrix, b: Fp8Matrix, out=None, out_dtype=None, accumulate:
                  pitch); a new one of out_dtype (bfloat16 if None) if not given
     accumulate : add the product to what out holds
     """
-    if a.cols != b.cols:
+    if a._cols != b._cols:
         raise ValueError(f"the operands contract {a.cols} and {b.cols} columns")
-    m, n = a.rows, b.rows
+    m, n = a._rows, b._rows
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")

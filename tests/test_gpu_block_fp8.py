@@ -161,6 +161,43 @@ def test_matmul_shapes(m, n, k, blocks, dtype):
     assert torch.equal(c, again)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("m,n,k", [(2047, 6143, 1100), (6143, 2047, 1100), (4000, 4004, 2200), (8190, 8001, 640),
+                                   (2001, 1999, 640), (1501, 1300, 16200), (300, 301, 5000), (60, 2000, 9000)])
+def test_matmul_tiles_ragged(m, n, k, dtype):
+    """Sizes that take tiles of 256 x 192, 192 x 256, 256 x 256, 128 x 128 and
+    64 x 64, whole and with a split contraction, with odd counts of blocks (the
+    last trip's second block lies behind the operands), cut tiles on both axes
+    and scales behind the last block that are NaN; every output."""
+    announce(f"matmul ragged tiles {m}x{n}x{k} {dtype}")
+    gen = torch.Generator(device="cuda").manual_seed(m + n)
+    kb = -(-k // 128)
+    ops = []
+    for rows, br in ((m, 1), (n, 128)):
+        x = torch.randn((rows, k), generator=gen, device="cuda") * torch.exp(torch.randn((rows, 1), generator=gen, device="cuda"))
+        q = pm.fp8_quantize(x, block_rows=br)
+        scale = torch.full((q.scale.shape[0], q.scale.shape[1] + 4), 255, dtype=torch.uint8, device="cuda")
+        scale[:, :kb] = q.scale[:, :kb]
+        ops.append(pm.Fp8Matrix(q.data, scale, k, br))
+    c = pm.fp8_matmul(*ops, out_dtype=dtype)
+    a, b = (_dequant(o).double() for o in ops)
+    bt = b.t().contiguous()
+    ref, s = a @ bt, a.abs() @ bt.abs()
+    off = (k * 2.0 ** -23 + (7 * 2.0 ** -13 if dtype == torch.bfloat16 else 0.0)) * s
+    tol = off + HALF[dtype] * (ref.abs() + off)
+    err = (c.double() - ref).abs()
+    assert bool((err <= tol).all()), float((err - tol).max())
+    # far below the bound where it counts: the error's norm against the result's
+    rel = float(torch.linalg.vector_norm(c.double() - ref) / torch.linalg.vector_norm(ref))
+    assert rel <= (2.0 ** -8 if dtype == torch.bfloat16 else 2e-6), rel
+    acc = c.clone()
+    pm.fp8_matmul(*ops, out=acc, accumulate=True)
+    twice = c.double() + ref
+    tol = off + HALF[dtype] * (twice.abs() + off) + 2.0 ** -23 * (c.double().abs() + ref.abs())
+    assert bool(((acc.double() - twice).abs() <= tol).all())
+    assert torch.equal(c, pm.fp8_matmul(*ops, out_dtype=dtype))
+
+
 def test_matmul_large_sampled():
     """Sizes of a layer's products; rows and columns sampled, the four corners
     among them."""
@@ -257,8 +294,9 @@ def test_matmul_scales_and_nan():
         assert nan[1].all() and nan[:, 7].all() and int(nan.sum()) == m + n - 1
         a = pm.fp8_quantize(torch.ones((m, 384), device="cuda"))
         a.scale[2, 1] = 255
-        nan = torch.isnan(pm.fp8_matmul(a, pm.fp8_quantize(torch.ones((n, 384), device="cuda"))))
-        assert nan[2].all() and int(nan.sum()) == n
+        for dtype in DTYPES:
+            nan = torch.isnan(pm.fp8_matmul(a, pm.fp8_quantize(torch.ones((n, 384), device="cuda")), out_dtype=dtype))
+            assert nan[2].all() and int(nan.sum()) == n
 
 
 def test_matmul_streams_and_graph():
@@ -295,6 +333,37 @@ def test_matmul_streams_and_graph():
         assert torch.equal(out, again), k
 
 
+def test_two_products_at_once_and_two_graphs():
+    """Split contractions (a workspace each) on two streams at once, and in two
+    graphs replayed in turn on changed operands."""
+    announce("two products at once")
+    x, y = torch.randn((300, 5000), device="cuda"), torch.randn((400, 5000), device="cuda")
+    qx, qy = pm.fp8_quantize(x), pm.fp8_quantize(y)
+    want = [pm.fp8_matmul(qx, qy, out_dtype=torch.float32), pm.fp8_matmul(qy, qx, out_dtype=torch.float32)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(4):
+        for s, (p, q) in zip(streams, ((qx, qy), (qy, qx))):
+            got.append(pm.fp8_matmul(p, q, out_dtype=torch.float32, stream=s))
+    torch.cuda.synchronize()
+    for i, c in enumerate(got):
+        assert torch.equal(c, want[i % 2])
+    graphs, outs = [], []
+    for p, q in ((qx, qy), (qy, qx)):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(pm.fp8_matmul(p, q, out_dtype=torch.float32))
+        graphs.append(g)
+    for k in range(3):
+        pm.fp8_quantize(x.mul_(0.5 + k), out=qx)
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], pm.fp8_matmul(qx, qy, out_dtype=torch.float32)), k
+        assert torch.equal(outs[1], pm.fp8_matmul(qy, qx, out_dtype=torch.float32)), k
+
+
 def test_python_refusals():
     x = torch.zeros((4, 256), device="cuda")
     q = pm.fp8_quantize(x)
@@ -324,6 +393,10 @@ def test_python_refusals():
         pm.fp8_matmul(q, q, accumulate=True)
     with pytest.raises(TypeError):
         pm.fp8_matmul(q, q, out_dtype=torch.float16)
+    with pytest.raises(pm.MuonHError):
+        pm.fp8_matmul(q, q, out=q.data.view(torch.float32)[:, :4])
+    with pytest.raises(AttributeError):
+        q.data = q.data
     with pytest.raises(TypeError):
         pm.Fp8Matrix(q.scale, q.scale, 256)
     with pytest.raises(ValueError):

@@ -98,6 +98,11 @@ def test_step_refusals():
     for bad in ((good[1], None), (None, good[0]), (pm.fp8_quantize(w), None)):
         with pytest.raises(pm.MuonHError):
             opt.step([g], elr=0.01, fp8=[bad])
+    w2, m3 = torch.randn((200, 130), device="cuda"), torch.zeros((200, 130), device="cuda")
+    two = pm.MuonH([w, w2], [m, m3], grad_dtype=torch.float32)
+    with pytest.raises(pm.MuonHError, match="twice"):
+        two.step([g, g], elr=0.01, fp8=[good, good])
+    two.close()
     assert torch.equal(w, keep)
     opt.step([g], elr=0.01, fp8=[(None, None)])   # nothing to write: the plain update
     other = keep.clone()

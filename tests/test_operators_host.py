@@ -54,7 +54,7 @@ def test_matmul_refusals():
     _refused(call(acc=2), mb.MUONH_EINVAL, "accumulate")
     _refused(call(c=BASE + 1024), mb.MUONH_EINVAL, "overlaps")
     _refused(call(c=BASE + (1 << 32) - 256), mb.MUONH_EINVAL, "overlaps")
-    _refused(call(a=_mat(rows=1 << 26), b=_mat(rows=1 << 26, data=BASE * 4, scale=BASE * 5), c=BASE * 8, ldc=1 << 26),
+    _refused(call(a=_mat(rows=1 << 26), b=_mat(rows=1 << 26, data=BASE * 4, scale=BASE * 5), c=BASE << 12, ldc=1 << 26),
              mb.MUONH_EINVAL, "too large")
     _refused(lib.muonh_block_matmul(None, None, BASE, 0, 1, 0, None, 0, None), mb.MUONH_EINVAL, "null operand")
     # nothing to compute: no pointer is needed
@@ -100,6 +100,7 @@ def _norm(**kw):
 NORM_BAD = [
     (dict(dtype=3), "dtype"), (dict(kind=2), "kind"), (dict(reserved=1), "reserved"), (dict(eps=-1.0), "eps"),
     (dict(eps=float("nan")), "eps"), (dict(rows=-1), "rows"), (dict(cols=0), "cols"), (dict(ldx=95), "ldx"),
+    (dict(cols=(1 << 26) + 1, ldx=1 << 27, ldy=1 << 27), "cols"),
     (dict(ldy=95), "ldy"), (dict(mean=BASE * 5), "mean must be NULL"), (dict(kind=0), "null"), (dict(x=None), "null"),
     (dict(weight=None), "null"), (dict(y=None), "null"), (dict(rstd=None), "null"), (dict(x=BASE + 2), "misaligned"),
     (dict(weight=BASE * 2 + 2), "misaligned"), (dict(y=BASE + 4), "overlaps"), (dict(y=BASE, ldy=128), "overlaps"),
