@@ -4,6 +4,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <string>
 
@@ -165,13 +166,16 @@ namespace {
 struct TileRate {
   int32_t ma, nb, per_cu;
   double block[2][4], round[2];
+  // the least time of a block where operands beyond the caches (64 MB) are read
+  // by up to four tiles each, so from HBM
+  double cold[4];
 };
 constexpr TileRate kTileRates[] = {
-    {4, 4, 1, {{1.61, 0, 0, 0}, {2.88, 0, 0, 0}}, {8.8, 16.3}},
-    {4, 3, 1, {{1.20, 0, 0, 0}, {2.17, 0, 0, 0}}, {10.0, 13.1}},
-    {3, 4, 1, {{1.20, 0, 0, 0}, {2.17, 0, 0, 0}}, {10.0, 13.1}},
-    {2, 2, 2, {{0.64, 0.88, 0, 0}, {0.90, 1.64, 0, 0}}, {4.0, 6.0}},
-    {1, 1, 4, {{0.28, 0.44, 0.62, 0.79}, {0.40, 0.58, 0.85, 1.12}}, {3.5, 4.0}},
+    {4, 4, 1, {{1.61, 0, 0, 0}, {2.88, 0, 0, 0}}, {8.8, 16.3}, {1.7, 0, 0, 0}},
+    {4, 3, 1, {{1.20, 0, 0, 0}, {2.17, 0, 0, 0}}, {10.0, 13.1}, {1.4, 0, 0, 0}},
+    {3, 4, 1, {{1.20, 0, 0, 0}, {2.17, 0, 0, 0}}, {10.0, 13.1}, {1.4, 0, 0, 0}},
+    {2, 2, 2, {{0.64, 0.88, 0, 0}, {0.90, 1.64, 0, 0}}, {4.0, 6.0}, {1.10, 1.30, 0, 0}},
+    {1, 1, 4, {{0.28, 0.44, 0.62, 0.79}, {0.40, 0.58, 0.85, 1.12}}, {3.5, 4.0}, {0.72, 0.97, 1.2, 1.4}},
 };
 constexpr int64_t kCus = 256;
 
@@ -186,25 +190,28 @@ constexpr int64_t kCus = 256;
 MatmulPlan muonh::plan_block_matmul(int c_bf16, const BlockMatmulArgs& a) {
   const int64_t m = a.m, n = a.n, nk = a.kblocks;
   MatmulPlan best{0, 0, 1, a.kblocks, 0};
-  // Up to 32 rows (or columns) are bound by reading the other operand, which the
-  // thin kernel does with more loads in flight (32 x 2048 x 6144: 9.3 us, 15.2
-  // in tiles of 64; 64 x 2048 x 6144: 15.7 and 15.1).  Tiles need panels of 256
-  // rows of values and of scales below 2^31 bytes (buffer offsets).
+  // Up to 16 rows (or columns) are one row block of the thin kernel, which reads
+  // the other operand with more loads in flight and in one launch (1 x 16384 x
+  // 16384: 55 us, 68 in tiles; 1 x 2048 x 6144: 6.6 and 12.9; 17 x 16384 x 16384,
+  // where it would read it twice: 86 and 68).  Tiles need panels of 256 rows of
+  // values and of scales below 2^31 bytes (buffer offsets).
   const int64_t most = (int64_t)1 << 23;
-  if (nk == 0 || m <= 32 || n <= 32 || a.lda >= most || a.ldb >= most || a.ldsa >= most || a.ldsb >= most)
+  if (nk == 0 || m <= 16 || n <= 16 || a.lda >= most || a.ldb >= most || a.ldsa >= most || a.ldsb >= most)
     return best;
   const int arith = c_bf16 ? 0 : 1;
   double best_us = 0.0;
   for (const TileRate& r : kTileRates) {
-    const int64_t tiles = ceil_div(m, 64 * r.ma) * ceil_div(n, 64 * r.nb);
+    const int64_t mt = ceil_div(m, 64 * r.ma), nt = ceil_div(n, 64 * r.nb), tiles = mt * nt;
+    const bool cold = (m + n) * nk * kFp8Block >= ((int64_t)64 << 20) && std::min(mt, nt) <= 4;
+    auto block_us = [&](int64_t per) { return std::max(r.block[arith][per - 1], cold ? r.cold[per - 1] : 0.0); };
     for (int64_t splits = 1; splits <= 16; splits *= 2) {
       // whole scale words (4 blocks) per workgroup, at least 4 blocks
       const int64_t blocks = splits == 1 ? nk : ceil_div(ceil_div(nk, splits), 4) * 4;
       const int64_t used = ceil_div(nk, blocks), groups = tiles * used;
       if (splits > 1 && (used < 2 || groups > 2 * kCus * r.per_cu)) break;
       const int64_t full = groups / (kCus * r.per_cu), rest = groups - full * kCus * r.per_cu;
-      double us = full * (r.block[arith][r.per_cu - 1] * blocks + r.round[arith]);
-      if (rest > 0) us += r.block[arith][ceil_div(rest, kCus) - 1] * blocks + r.round[arith];
+      double us = full * (block_us(r.per_cu) * blocks + r.round[arith]);
+      if (rest > 0) us += block_us(ceil_div(rest, kCus)) * blocks + r.round[arith];
       // a launch, a workspace, and partials written and read at about 4 TB/s
       if (used > 1) us += 6.0 + (double)((2 * used + 1) * m * n) * 4.0 / 4e6;
       if (best.ma == 0 || us < best_us) {

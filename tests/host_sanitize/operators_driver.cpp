@@ -47,7 +47,7 @@ int64_t norm_partial_rows(int64_t rows, int64_t) { return rows < 256 ? rows : 25
   } while (0)
 
 static void plans() {
-  const int64_t sizes[] = {1, 31, 32, 33, 64, 65, 200, 256, 777, 1000, 2048, 4100, 8192, 12288, 100000};
+  const int64_t sizes[] = {1, 15, 16, 17, 33, 64, 65, 200, 256, 777, 1000, 2048, 4100, 8192, 12288, 100000};
   const int64_t lengths[] = {0, 1, 127, 128, 129, 1500, 2048, 8192, 16384, 100000};
   int seen[5][5] = {};
   int split = 0;
@@ -71,7 +71,8 @@ static void plans() {
           CHECK(p.splits == 1 || p.split_blocks % 4 == 0);
           CHECK(p.workspace_bytes == (p.splits > 1 ? sizeof(float) * (size_t)p.splits * (size_t)(m * n) : 0));
           split += p.splits > 1;
-          if (m <= 32 || n <= 32 || k == 0) CHECK(p.ma == 0 && p.splits == 1);
+          if (m <= 16 || n <= 16 || k == 0) CHECK(p.ma == 0 && p.splits == 1);
+          else CHECK(p.ma > 0);
           // panels beyond the tile kernel's 32-bit offsets go to the thin kernel
           a.ldb = (int64_t)1 << 23;
           CHECK(plan_block_matmul(bf16, a).ma == 0);
