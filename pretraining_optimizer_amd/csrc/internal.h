@@ -5,7 +5,6 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include <memory>
 #include <vector>
 
 #include "../../include/muonh.h"
@@ -202,21 +201,6 @@ hipError_t launch_adamw(const Chunk* chunks, int64_t nchunks, const AdamwPtrs* p
 
 // Records the text of a failure for muonh_last_error() and returns `code`.
 int set_last_error(int code, const char* msg);
-
-// A step whose last launch is another than launch_update: `prepare` runs after
-// the step's own checks and uploads, before its first launch; `launch` in place
-// of the update.  `context` is the caller's.
-struct StepTail {
-  int (*prepare)(void* context, hipStream_t st);
-  hipError_t (*launch)(void* context, int bf16, const MatGeom* geo, const MatPtrs* ptrs,
-                       const MatScalars* scal, hipStream_t st);
-  void* context;
-};
-int step_with_tail(muonh_handle* h, const muonh_matrix_desc* mats, int32_t n,
-                   const muonh_step_args* args, hipStream_t st, const StepTail& tail);
-// What such a variant keeps with the handle; released by muonh_destroy, after
-// the handle's last stream has passed its work.
-std::shared_ptr<void>& step_extension(muonh_handle* h);
 
 // Host state one device keeps for the allocation-free step: the host image
 // of the plan tables (reused, so an upload's source stays valid until the

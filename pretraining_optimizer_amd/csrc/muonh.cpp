@@ -22,6 +22,7 @@
 #include <vector>
 
 #include "internal.h"
+#include "step_tail.h"
 
 using namespace muonh;
 

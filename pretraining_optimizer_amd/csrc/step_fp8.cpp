@@ -12,6 +12,7 @@
 #include <vector>
 
 #include "operators.h"
+#include "step_tail.h"
 
 using namespace muonh;
 

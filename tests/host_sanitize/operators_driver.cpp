@@ -7,6 +7,7 @@
 #include <string>
 
 #include "../../pretraining_optimizer_amd/csrc/operators.h"
+#include "../../pretraining_optimizer_amd/csrc/step_tail.h"
 
 using namespace muonh;
 
