@@ -532,16 +532,6 @@ constexpr int kBufferConfig = 0x00020000;   // raw, unformatted buffer access
 constexpr int kSgMfma = 0x008, kSgVmemRead = 0x020, kSgDsRead = 0x100;
 #define MUONH_SG(mask, n) __builtin_amdgcn_sched_group_barrier((mask), (n), 0)
 
-// A result larger than the caches keep goes past them (8192 x 12288 bf16, 201
-// MB: 180 us, 203 with ordinary stores; 8192 x 4096, 67 MB: 63.6 and 62.3, and
-// what reads it next finds it there).
-constexpr int64_t kStreamBytes = (int64_t)128 << 20;
-template <typename V>
-__device__ __forceinline__ void store_vec(void* p, V v, int stream) {
-  if (stream) __builtin_nontemporal_store(v, (MUONH_GLOBAL V*)p);
-  else st_global<V>(p, v);
-}
-
 constexpr int kTileThreads = 256;
 constexpr int kScaleBlocks = 16;   // scales staged at a time, per row
 // 16-byte chunk c of a 128-byte LDS row r sits at c ^ swz128(r): the rows of a
@@ -847,7 +837,7 @@ __global__ __launch_bounds__(kTileThreads) void block_matmul_tile_kernel(BlockMa
       if constexpr (sizeof(C) == 2) {
         typedef uint32_t vec __attribute__((ext_vector_type(4), aligned(2)));
         if (col + 8 <= cols) {
-          store_vec<vec>(d, (vec)v, p.stream_c);
+          st_global<vec>(d, (vec)v);
         } else {
 #pragma unroll
           for (int e = 0; e < 8; ++e)
@@ -859,7 +849,7 @@ __global__ __launch_bounds__(kTileThreads) void block_matmul_tile_kernel(BlockMa
         if (col + 4 <= cols) {
           vec x = o;
           if (p.accumulate) x += ld_global<vec>(d);
-          store_vec<vec>(d, x, p.stream_c);
+          st_global<vec>(d, x);
         } else {
           store_c<float>(d, cols - col, p.accumulate, o);
         }
@@ -925,7 +915,6 @@ hipError_t matmul_for(const MatmulPlan& pl, BlockMatmulArgs a, float* workspace,
   constexpr bool kFp8 = sizeof(C) == 2;
   a.splits = 1;
   a.split_blocks = a.kblocks;
-  a.stream_c = (int64_t)a.m * a.n * (int64_t)sizeof(C) >= kStreamBytes;
   if (pl.ma == 0) {
     const unsigned ntiles = (unsigned)((a.n + 15) / 16);
     const dim3 grid(ntiles * (unsigned)((a.m + 15) / 16));
@@ -943,7 +932,6 @@ hipError_t matmul_for(const MatmulPlan& pl, BlockMatmulArgs a, float* workspace,
   part.c = workspace;
   part.ldc = a.n;
   part.accumulate = 0;
-  part.stream_c = 0;
   const hipError_t e = launch_tiles<kFp8, float>(pl, part, st);
   if (e != hipSuccess) return e;
   const int64_t groups = ((int64_t)a.m * a.n + 1023) / 1024;

@@ -54,8 +54,8 @@ struct BlockMatmulArgs {
   int32_t m, n, kblocks;          // kblocks: blocks of 128 along the contraction
   int32_t a_shift, b_shift;       // scale row = row >> shift (0 or 7)
   int32_t accumulate;
-  // Set by the launcher: workgroups along the contraction, blocks of each; non-temporal stores of C.
-  int32_t splits, split_blocks, stream_c;
+  // Set by the launcher: workgroups along the contraction, blocks of each.
+  int32_t splits, split_blocks;
 };
 
 // How a product runs: 64 ma x 64 nb tiles (ma = 0: the thin kernel), the
