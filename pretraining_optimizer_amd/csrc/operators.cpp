@@ -68,9 +68,10 @@ int check_norm_size(int64_t rows, int64_t cols) {
   return check_size(rows, 0, "rows");
 }
 
-int check_pitch(int64_t ld, int64_t cols, const char* what) {
-  if (ld < cols || ld > ((int64_t)1 << 40))
-    return fail(MUONH_EINVAL, std::string(what) + ": the pitch is less than a row, or beyond 2^40");
+// rows * ld stays at or below 2^60, so a matrix's bytes fit 64 bits.
+int check_pitch(int64_t ld, int64_t rows, int64_t cols, const char* what) {
+  if (ld < cols || ld > ((int64_t)1 << 40) || (rows > 0 && ld > ((int64_t)1 << 60) / rows))
+    return fail(MUONH_EINVAL, std::string(what) + ": the pitch is less than a row, or too large");
   return MUONH_OK;
 }
 
@@ -92,9 +93,9 @@ int muonh::check_fp8_matrix(const muonh_fp8_matrix& m, const char* whose) {
   if ((rc = check_size(m.cols, 0, (who + "cols").c_str()))) return rc;
   if (m.block_rows != 1 && m.block_rows != 128) return fail(MUONH_EINVAL, who + "block_rows must be 1 or 128");
   if (m.reserved != 0) return fail(MUONH_EINVAL, who + "reserved != 0");
-  if ((rc = check_pitch(m.ld, m.cols, (who + "ld").c_str()))) return rc;
+  if ((rc = check_pitch(m.ld, m.rows, m.cols, (who + "ld").c_str()))) return rc;
   if (m.ld % kFp8Block != 0) return fail(MUONH_EINVAL, who + "ld must be a multiple of 128");
-  if ((rc = check_pitch(m.ld_scale, ceil_div(m.cols, kFp8Block), (who + "ld_scale").c_str()))) return rc;
+  if ((rc = check_pitch(m.ld_scale, m.rows, ceil_div(m.cols, kFp8Block), (who + "ld_scale").c_str()))) return rc;
   if (m.ld_scale % 4 != 0) return fail(MUONH_EINVAL, who + "ld_scale must be a multiple of 4");
   if (m.rows > 0 && m.cols > 0) {
     if (!m.data || !m.scale) return fail(MUONH_EINVAL, who + "null pointer");
@@ -233,7 +234,7 @@ int muonh_block_quantize(const void* x, int32_t dtype, int64_t rows, int64_t col
     if (!q && !qt) return fail(MUONH_EINVAL, "neither form is asked for");
     if ((rc = check_dtype(dtype, "x"))) return rc;
     if ((rc = check_size(rows, 0, "rows")) || (rc = check_size(cols, 0, "cols"))) return rc;
-    if ((rc = check_pitch(ldx, cols, "ldx"))) return rc;
+    if ((rc = check_pitch(ldx, rows, cols, "ldx"))) return rc;
     if (q) {
       if ((rc = check_fp8_matrix(*q, "q"))) return rc;
       if (q->rows != rows || q->cols != cols) return fail(MUONH_EINVAL, "q: shape differs from x");
@@ -285,7 +286,7 @@ int muonh_block_matmul(const muonh_fp8_matrix* a, const muonh_fp8_matrix* b, voi
   return guarded([&]() -> int {
     int rc;
     if ((rc = check_operands(a, b)) || (rc = check_dtype(c_dtype, "c"))) return rc;
-    if ((rc = check_pitch(ldc, b->rows, "ldc"))) return rc;
+    if ((rc = check_pitch(ldc, a->rows, b->rows, "ldc"))) return rc;
     if (accumulate != 0 && accumulate != 1) return fail(MUONH_EINVAL, "accumulate must be 0 or 1");
     if (a->rows == 0 || b->rows == 0) return MUONH_OK;
     const int64_t size = c_dtype == MUONH_BF16 ? 2 : 4, nc = extent(a->rows, b->rows, ldc, size);
@@ -320,7 +321,7 @@ int muonh_norm_forward(const muonh_norm_args* g, void* stream) {
     if (g->reserved != 0) return fail(MUONH_EINVAL, "reserved != 0");
     if (!(g->eps >= 0.0f) || !std::isfinite(g->eps)) return fail(MUONH_EINVAL, "eps must be >= 0 and finite");
     if ((rc = check_norm_size(g->rows, g->cols))) return rc;
-    if ((rc = check_pitch(g->ldx, g->cols, "ldx")) || (rc = check_pitch(g->ldy, g->cols, "ldy"))) return rc;
+    if ((rc = check_pitch(g->ldx, g->rows, g->cols, "ldx")) || (rc = check_pitch(g->ldy, g->rows, g->cols, "ldy"))) return rc;
     const int layer = g->kind == MUONH_NORM_LAYER;
     if (!layer && g->mean) return fail(MUONH_EINVAL, "mean must be NULL for MUONH_NORM_RMS");
     if (g->rows == 0) return MUONH_OK;
@@ -368,8 +369,8 @@ int muonh_norm_backward(const muonh_norm_grad_args* g, void* stream) {
     if (g->reserved != 0) return fail(MUONH_EINVAL, "reserved != 0");
     if (g->accumulate != 0 && g->accumulate != 1) return fail(MUONH_EINVAL, "accumulate must be 0 or 1");
     if ((rc = check_norm_size(g->rows, g->cols))) return rc;
-    if ((rc = check_pitch(g->ld_dy, g->cols, "ld_dy")) || (rc = check_pitch(g->ldx, g->cols, "ldx")) ||
-        (rc = check_pitch(g->ld_dx, g->cols, "ld_dx")))
+    if ((rc = check_pitch(g->ld_dy, g->rows, g->cols, "ld_dy")) || (rc = check_pitch(g->ldx, g->rows, g->cols, "ldx")) ||
+        (rc = check_pitch(g->ld_dx, g->rows, g->cols, "ld_dx")))
       return rc;
     const int layer = g->kind == MUONH_NORM_LAYER;
     if (!layer && g->mean) return fail(MUONH_EINVAL, "mean must be NULL for MUONH_NORM_RMS");

@@ -161,3 +161,23 @@ def test_quantized_step_refusals():
     q = _mat(256, 128, block=128)
     for call in ((None, mats, 1, ctypes.byref(q), None, ctypes.byref(args)),):
         _refused(lib.muonh_step_quantized(*call, None), mb.MUONH_EINVAL, "null")
+
+
+def test_pitches_beyond_64_bits_are_refused():
+    """rows * pitch, in bytes, has to stay below 2^63."""
+    lib = pm.load_library()
+    rows, ld = 1 << 30, 1 << 40
+    text = "pitch"
+    _refused(lib.muonh_norm_forward(ctypes.byref(_norm(rows=rows, ldx=ld)), None), mb.MUONH_EINVAL, text)
+    _refused(lib.muonh_norm_forward(ctypes.byref(_norm(rows=rows, ldy=ld)), None), mb.MUONH_EINVAL, text)
+    for name in ("ld_dy", "ldx", "ld_dx"):
+        _refused(lib.muonh_norm_backward(ctypes.byref(_grad(rows=rows, **{name: ld})), None), mb.MUONH_EINVAL, text)
+    for m in (_mat(rows=rows, ld=ld), _mat(rows=rows, lds=ld)):
+        rc = lib.muonh_block_matmul(ctypes.byref(m), ctypes.byref(_mat()), BASE * 8, 0, 256, 0, None, 0, None)
+        _refused(rc, mb.MUONH_EINVAL, text)
+        rc = lib.muonh_block_quantize(BASE * 8, 0, rows, 256, 256, ctypes.byref(m), None, None)
+        _refused(rc, mb.MUONH_EINVAL, text)
+    rc = lib.muonh_block_matmul(ctypes.byref(_mat(rows=rows)), ctypes.byref(_mat()), BASE * 8, 0, ld, 0, None, 0, None)
+    _refused(rc, mb.MUONH_EINVAL, text)
+    rc = lib.muonh_block_quantize(BASE * 8, 0, rows, 256, ld, ctypes.byref(_mat(rows=rows)), None, None)
+    _refused(rc, mb.MUONH_EINVAL, text)
