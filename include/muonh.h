@@ -398,7 +398,7 @@ int muonh_step_quantized(muonh_handle* h, const muonh_matrix_desc* mats, int32_t
  * Statistics and sums are fp32, sums in a fixed order.  x, y, dy and dx share
  * one dtype (MUONH_F32 or MUONH_BF16) and need element alignment only; the
  * vectors are fp32.  y may be x, and dx may be x or dy (same address and
- * pitch); other overlaps are refused.                                       */
+ * pitch); an output or workspace that overlaps anything else is refused.     */
 #define MUONH_NORM_LAYER 0
 #define MUONH_NORM_RMS   1
 

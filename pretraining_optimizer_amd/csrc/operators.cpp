@@ -6,6 +6,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <initializer_list>
 #include <string>
 
 #include "operators.h"
@@ -38,6 +39,22 @@ bool overlap(const void* p, int64_t pn, const void* q, int64_t qn) {
   const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
   return pn > 0 && qn > 0 && a < b + (uintptr_t)qn && b < a + (uintptr_t)pn;
 }
+
+struct Span {
+  const void* p;
+  int64_t bytes;
+};
+// Whether an output shares memory with another or with an input.
+bool clash(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  for (const Span* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Span& i : ins)
+      if (overlap(o->p, o->bytes, i.p, i.bytes)) return true;
+    for (const Span* q = o + 1; q != outs.end(); ++q)
+      if (overlap(o->p, o->bytes, q->p, q->bytes)) return true;
+  }
+  return false;
+}
+Span vec(const float* p, int64_t n) { return Span{p, p ? n * 4 : 0}; }
 
 // Whether an output may share memory with an input of the same size: in place,
 // apart, or in other columns of the same rows.
@@ -306,6 +323,9 @@ int muonh_block_matmul(const muonh_fp8_matrix* a, const muonh_fp8_matrix* b, voi
     if (plan.workspace_bytes > 0 && (!workspace || workspace_bytes < plan.workspace_bytes))
       return fail(MUONH_ENOMEM, "workspace too small: need " + std::to_string(plan.workspace_bytes) + " bytes");
     if (!aligned(workspace, kAlign)) return fail(MUONH_EINVAL, "workspace must be 256-byte aligned");
+    const int64_t nws = (int64_t)plan.workspace_bytes;
+    if (overlap(workspace, nws, c, nc) || fp8_overlaps(*a, workspace, nws) || fp8_overlaps(*b, workspace, nws))
+      return fail(MUONH_EINVAL, "workspace overlaps c or an operand");
     return launched(launch_block_matmul(c_dtype == MUONH_BF16, plan, p, static_cast<float*>(workspace),
                                         reinterpret_cast<hipStream_t>(stream)),
                     "block_matmul");
@@ -333,6 +353,10 @@ int muonh_norm_forward(const muonh_norm_args* g, void* stream) {
       return fail(MUONH_EINVAL, "misaligned pointer");
     if (!may_share(g->y, g->ldy, g->x, g->ldx, g->rows, g->cols, size))
       return fail(MUONH_EINVAL, "y overlaps x");
+    const Span x{g->x, extent(g->rows, g->cols, g->ldx, size)}, y{g->y, extent(g->rows, g->cols, g->ldy, size)};
+    const Span mean = vec(g->mean, g->rows), rstd = vec(g->rstd, g->rows);
+    if (clash({y, mean, rstd}, {vec(g->weight, g->cols), vec(g->bias, g->cols)}) || clash({mean, rstd}, {x}))
+      return fail(MUONH_EINVAL, "an output overlaps an input or another output");
     NormArgs a{};
     a.x = g->x;
     a.weight = g->weight;
@@ -393,6 +417,12 @@ int muonh_norm_backward(const muonh_norm_grad_args* g, void* stream) {
     if (need > 0 && (!g->workspace || g->workspace_bytes < need))
       return fail(MUONH_ENOMEM, "workspace too small: need " + std::to_string(need) + " bytes");
     if (!aligned(g->workspace, kAlign)) return fail(MUONH_EINVAL, "workspace must be 256-byte aligned");
+    const Span dy{g->dy, extent(g->rows, g->cols, g->ld_dy, size)}, x{g->x, extent(g->rows, g->cols, g->ldx, size)};
+    const Span dx{g->dx, extent(g->rows, g->cols, g->ld_dx, size)}, ws{g->workspace, (int64_t)need};
+    const Span dweight = vec(g->dweight, g->cols), dbias = vec(g->dbias, g->cols);
+    if (clash({dx, dweight, dbias, ws}, {vec(g->weight, g->cols), vec(g->mean, g->rows), vec(g->rstd, g->rows)}) ||
+        clash({dweight, dbias, ws}, {dy, x}))
+      return fail(MUONH_EINVAL, "an output or the workspace overlaps an input or another output");
     NormGradArgs a{};
     a.dy = g->dy;
     a.x = g->x;

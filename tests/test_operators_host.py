@@ -163,6 +163,39 @@ def test_quantized_step_refusals():
         _refused(lib.muonh_step_quantized(*call, None), mb.MUONH_EINVAL, "null")
 
 
+VECTORS = dict(weight=BASE * 2, bias=BASE * 6, mean=BASE * 7, rstd=BASE * 4, kind=0)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(y=BASE * 2), dict(y=BASE * 6 - 96 * 4), dict(rstd=BASE + 32), dict(mean=BASE + 95 * 4), dict(rstd=BASE * 2),
+    dict(mean=BASE * 6), dict(mean=BASE * 4 + 28), dict(mean=BASE * 3 + 4),
+])
+def test_norm_forward_refuses_overlapping_vectors(kw):
+    a = _norm(**{**VECTORS, **kw})
+    _refused(pm.load_library().muonh_norm_forward(ctypes.byref(a), None), mb.MUONH_EINVAL, "overlap")
+
+
+@pytest.mark.parametrize("kw", [
+    dict(dweight=BASE * 3), dict(dbias=BASE * 6), dict(dbias=BASE * 6 + 95 * 4), dict(dbias=BASE * 5), dict(dweight=BASE),
+    dict(dweight=BASE * 2 + 64), dict(dx=BASE * 3), dict(dx=BASE * 4 - 64), dict(dweight=BASE * 8), dict(workspace=BASE * 3),
+    dict(workspace=BASE), dict(workspace=BASE * 5), dict(workspace=BASE * 6), dict(workspace=BASE * 8),
+])
+def test_norm_backward_refuses_overlapping_vectors(kw):
+    a = _grad(**{**dict(kind=0, mean=BASE * 8, dbias=BASE * 9), **kw})
+    _refused(pm.load_library().muonh_norm_backward(ctypes.byref(a), None), mb.MUONH_EINVAL, "overlap")
+
+
+def test_matmul_refuses_overlapping_workspace():
+    lib = pm.load_library()
+    a, b = _mat(cols=16384), _mat(cols=16384, data=BASE * 4, scale=BASE * 5)
+    need = ctypes.c_size_t()
+    assert lib.muonh_block_matmul_workspace(ctypes.byref(a), ctypes.byref(b), pm.MUONH_F32, ctypes.byref(need)) == mb.MUONH_OK
+    assert need.value > 0
+    for ws in (BASE, BASE + (1 << 32), BASE * 4 + 256, BASE * 5, BASE * 2):
+        rc = lib.muonh_block_matmul(ctypes.byref(a), ctypes.byref(b), BASE * 2, pm.MUONH_F32, 256, 0, ws, need.value, None)
+        _refused(rc, mb.MUONH_EINVAL, "workspace overlaps")
+
+
 def test_pitches_beyond_64_bits_are_refused():
     """rows * pitch, in bytes, has to stay below 2^63."""
     lib = pm.load_library()
