@@ -381,8 +381,8 @@ int muonh_block_matmul(const muonh_fp8_matrix* a, const muonh_fp8_matrix* b, voi
  * allocates its tables on the device (12 bytes per 128 x 128 block), which
  * muonh_destroy releases; not for use while `stream` is being captured.
  * Errors: as muonh_step; MUONH_EINVAL for an output whose shape, block_rows or
- * layout does not fit, that overlaps its own W, M or G or that is named twice;
- * MUONH_ENOMEM.                                                             */
+ * layout does not fit, that is named twice or that overlaps another (side by
+ * side in rows of one pitch is allowed) or a W, M or G of the step; MUONH_ENOMEM. */
 int muonh_step_quantized(muonh_handle* h, const muonh_matrix_desc* mats, int32_t n,
                          const muonh_fp8_matrix* q, const muonh_fp8_matrix* qt,
                          const muonh_step_args* args, void* stream);

@@ -92,16 +92,17 @@ int check_pitch(int64_t ld, int64_t rows, int64_t cols, const char* what) {
   return MUONH_OK;
 }
 
-int64_t data_bytes(const muonh_fp8_matrix& m) {
-  return m.rows > 0 && m.cols > 0 ? extent(m.rows, ceil_div(m.cols, kFp8Block) * kFp8Block, m.ld, 1) : 0;
-}
-int64_t scale_bytes(const muonh_fp8_matrix& m) {
-  return m.rows > 0 && m.cols > 0
-             ? extent(ceil_div(m.rows, m.block_rows), ceil_div(m.cols, kFp8Block), m.ld_scale, 1)
-             : 0;
-}
-
 }  // namespace
+
+// What a row of an operand takes: the quantiser writes zeros behind the columns.
+int64_t muonh::fp8_data_width(const muonh_fp8_matrix& m) { return ceil_div(m.cols, kFp8Block) * kFp8Block; }
+int64_t muonh::fp8_scale_width(const muonh_fp8_matrix& m) { return ceil_div(ceil_div(m.cols, kFp8Block), 4) * 4; }
+int64_t muonh::fp8_data_bytes(const muonh_fp8_matrix& m) {
+  return m.rows > 0 && m.cols > 0 ? extent(m.rows, fp8_data_width(m), m.ld, 1) : 0;
+}
+int64_t muonh::fp8_scale_bytes(const muonh_fp8_matrix& m) {
+  return m.rows > 0 && m.cols > 0 ? extent(ceil_div(m.rows, m.block_rows), fp8_scale_width(m), m.ld_scale, 1) : 0;
+}
 
 int muonh::check_fp8_matrix(const muonh_fp8_matrix& m, const char* whose) {
   const std::string who = std::string(whose) + ": ";
@@ -137,7 +138,7 @@ void muonh::set_column_form(QuantArgs& a, const muonh_fp8_matrix& m) {
 }
 
 bool muonh::fp8_overlaps(const muonh_fp8_matrix& m, const void* p, int64_t bytes) {
-  return overlap(m.data, data_bytes(m), p, bytes) || overlap(m.scale, scale_bytes(m), p, bytes);
+  return overlap(m.data, fp8_data_bytes(m), p, bytes) || overlap(m.scale, fp8_scale_bytes(m), p, bytes);
 }
 
 namespace {
@@ -266,9 +267,9 @@ int muonh_block_quantize(const void* x, int32_t dtype, int64_t rows, int64_t col
     if (!x) return fail(MUONH_EINVAL, "null x");
     if (!aligned(x, (uintptr_t)size)) return fail(MUONH_EINVAL, "misaligned x");
     for (const muonh_fp8_matrix* m : {q, qt})
-      if (m && (fp8_overlaps(*m, x, nx) || overlap(m->scale, scale_bytes(*m), m->data, data_bytes(*m))))
+      if (m && (fp8_overlaps(*m, x, nx) || overlap(m->scale, fp8_scale_bytes(*m), m->data, fp8_data_bytes(*m))))
         return fail(MUONH_EINVAL, "outputs overlap x or each other");
-    if (q && qt && (fp8_overlaps(*q, qt->data, data_bytes(*qt)) || fp8_overlaps(*q, qt->scale, scale_bytes(*qt))))
+    if (q && qt && (fp8_overlaps(*q, qt->data, fp8_data_bytes(*qt)) || fp8_overlaps(*q, qt->scale, fp8_scale_bytes(*qt))))
       return fail(MUONH_EINVAL, "outputs overlap x or each other");
     if (ceil_div(rows, kFp8Tile) * ceil_div(cols, kFp8Tile) * kQuantizeThreads > kMaxThreads)
       return fail(MUONH_EINVAL, "x is too large for one launch");

@@ -103,6 +103,12 @@ int check_fp8_matrix(const muonh_fp8_matrix& m, const char* whose);
 // Its forms' addresses in QuantArgs.
 void set_row_form(QuantArgs& a, const muonh_fp8_matrix& m);
 void set_column_form(QuantArgs& a, const muonh_fp8_matrix& m);
+// Bytes of a row's values and scales with their padding, and from the first to
+// behind the last of all rows.
+int64_t fp8_data_width(const muonh_fp8_matrix& m);
+int64_t fp8_scale_width(const muonh_fp8_matrix& m);
+int64_t fp8_data_bytes(const muonh_fp8_matrix& m);
+int64_t fp8_scale_bytes(const muonh_fp8_matrix& m);
 // Whether an operand's values or scales share memory with [p, p + bytes).
 bool fp8_overlaps(const muonh_fp8_matrix& m, const void* p, int64_t bytes);
 

@@ -106,18 +106,55 @@ hipError_t launch(void* context, int bf16, const MatGeom* geo, const MatPtrs* pt
   return launch_update_quantize(bf16, q->d_tiles, q->ntiles, q->d_outs, geo, ptrs, scal, st);
 }
 
-// Form f of matrix i (rows x cols): nothing if its data is NULL.
-int check_form(const muonh_fp8_matrix& f, const muonh_matrix_desc& d, int64_t rows, int64_t cols,
-               const std::string& who) {
+// The form f of a weight, rows x cols.
+int check_form(const muonh_fp8_matrix& f, int64_t rows, int64_t cols, const std::string& who) {
   if (f.rows != rows || f.cols != cols) return fail(MUONH_EINVAL, who + ": shape differs from the weight's");
   if (f.block_rows != 128) return fail(MUONH_EINVAL, who + ": block_rows must be 128");
-  const int rc = check_fp8_matrix(f, who.c_str());
-  if (rc) return rc;
-  const int64_t count = d.rows * d.cols;
-  if (fp8_overlaps(f, d.w, count * 4) || fp8_overlaps(f, d.m, count * 4) ||
-      fp8_overlaps(f, d.g, count * (d.g_dtype == MUONH_BF16 ? 2 : 4)))
-    return fail(MUONH_EINVAL, who + ": overlaps the weight, its gradient or its momentum");
-  return MUONH_OK;
+  return check_fp8_matrix(f, who.c_str());
+}
+
+// Memory of a step: rows of `width` bytes, `pitch` bytes apart.
+struct Span {
+  uintptr_t begin, end;
+  int64_t width, pitch;
+  bool out;
+};
+// Sizes that are out of range belong to no handle's matrices: such a step is
+// refused by its own checks.
+bool in_range(int64_t v) { return v >= 1 && v <= (int64_t)1 << 30; }
+
+// Whether an output shares memory with another, or with a weight, gradient or
+// momentum: two workgroups would write it, or one read what another writes.
+// Forms side by side in rows of one pitch do not.
+bool outputs_overlap(const muonh_matrix_desc* mats, int32_t n, const muonh_fp8_matrix* q, const muonh_fp8_matrix* qt) {
+  std::vector<Span> spans;
+  auto add = [&](const void* p, int64_t bytes, int64_t width, int64_t pitch, bool out) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    if (p && bytes > 0) spans.push_back(Span{at, at + (uintptr_t)bytes, width, pitch, out});
+  };
+  for (int32_t i = 0; i < n; ++i) {
+    if (in_range(mats[i].rows) && in_range(mats[i].cols)) {
+      const int64_t count = mats[i].rows * mats[i].cols;
+      const int64_t g_bytes = count * (mats[i].g_dtype == MUONH_BF16 ? 2 : 4);
+      add(mats[i].w, count * 4, count * 4, count * 4, false);
+      add(mats[i].m, count * 4, count * 4, count * 4, false);
+      add(mats[i].g, g_bytes, g_bytes, g_bytes, false);
+    }
+    for (const muonh_fp8_matrix* f : {q, qt})
+      if (f && f[i].data) {
+        add(f[i].data, fp8_data_bytes(f[i]), fp8_data_width(f[i]), f[i].ld, true);
+        add(f[i].scale, fp8_scale_bytes(f[i]), fp8_scale_width(f[i]), f[i].ld_scale, true);
+      }
+  }
+  std::sort(spans.begin(), spans.end(), [](const Span& x, const Span& y) { return x.begin < y.begin; });
+  for (size_t i = 0; i < spans.size(); ++i)
+    for (size_t j = i + 1; j < spans.size() && spans[j].begin < spans[i].end; ++j) {
+      const Span &x = spans[i], &y = spans[j];
+      if (!x.out && !y.out) continue;
+      const int64_t d = (int64_t)(y.begin - x.begin) % x.pitch;
+      if (x.pitch != y.pitch || d < x.width || x.pitch - d < y.width) return true;
+    }
+  return false;
 }
 
 }  // namespace
@@ -138,22 +175,16 @@ extern "C" int muonh_step_quantized(muonh_handle* h, const muonh_matrix_desc* ma
       a.cols = mats[i].cols;
       int rc;
       if (q && q[i].data) {
-        if ((rc = check_form(q[i], mats[i], a.rows, a.cols, name + " q"))) return rc;
+        if ((rc = check_form(q[i], a.rows, a.cols, name + " q"))) return rc;
         set_row_form(a, q[i]);
       }
       if (qt && qt[i].data) {
-        if ((rc = check_form(qt[i], mats[i], a.cols, a.rows, name + " qt"))) return rc;
+        if ((rc = check_form(qt[i], a.cols, a.rows, name + " qt"))) return rc;
         set_column_form(a, qt[i]);
       }
     }
-    // an output named twice would be written by two matrices at once
-    std::vector<const void*> named;
-    for (const QuantArgs& a : outs)
-      for (const void* p : {(const void*)a.q, (const void*)a.qt, (const void*)a.s, (const void*)a.st})
-        if (p) named.push_back(p);
-    std::sort(named.begin(), named.end());
-    if (std::adjacent_find(named.begin(), named.end()) != named.end())
-      return fail(MUONH_EINVAL, "an output is named twice");
+    if (outputs_overlap(mats, n, q, qt))
+      return fail(MUONH_EINVAL, "an output is named twice, or overlaps another, a weight, a gradient or a momentum");
     Context c{h, mats, n, &outs, nullptr};
     return step_with_tail(h, mats, n, args, reinterpret_cast<hipStream_t>(stream),
                           StepTail{prepare, launch, &c});

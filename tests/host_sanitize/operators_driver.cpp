@@ -121,6 +121,32 @@ static void refusals() {
   muonh_fp8_matrix same[2] = {q, q};
   CHECK(muonh_step_quantized(h, two, 2, same, nullptr, &args, nullptr) == MUONH_EINVAL);
   CHECK(g_error.find("twice") != std::string::npos);
+  // the second matrix's output on the first's rows, weight, gradient or momentum
+  two[1].w = c + ((uintptr_t)1 << 24);
+  two[1].g = c + ((uintptr_t)2 << 24);
+  two[1].m = c + ((uintptr_t)3 << 24);
+  two[0].g = c + ((uintptr_t)4 << 24);
+  two[0].m = c + ((uintptr_t)5 << 24);
+  muonh_fp8_matrix apart[2] = {q, mat(300, 500, 128, base + ((uintptr_t)1 << 30))};
+  CHECK(muonh_step_quantized(h, two, 2, apart, nullptr, &args, nullptr) == MUONH_ESTATE);
+  for (char* at : {base + 512 * 299, c + 256, c + ((uintptr_t)4 << 24), c + ((uintptr_t)5 << 24),
+                   c + ((uintptr_t)1 << 24) - 256}) {
+    muonh_fp8_matrix bad[2] = {q, mat(300, 500, 128, at)};
+    bad[1].scale = base + ((uintptr_t)1 << 31);
+    CHECK(muonh_step_quantized(h, two, 2, bad, nullptr, &args, nullptr) == MUONH_EINVAL);
+    CHECK(g_error.find("overlaps") != std::string::npos);
+  }
+  // forms side by side in rows of 1024 bytes, their scales in rows of 8
+  muonh_fp8_matrix side[2] = {q, q};
+  for (int i = 0; i < 2; ++i) {
+    side[i].ld = 1024;
+    side[i].ld_scale = 8;
+    side[i].data = base + 512 * i;
+    side[i].scale = base + ((uintptr_t)1 << 36) + 4 * i;
+  }
+  CHECK(muonh_step_quantized(h, two, 2, side, nullptr, &args, nullptr) == MUONH_ESTATE);
+  side[1].data = base + 384;
+  CHECK(muonh_step_quantized(h, two, 2, side, nullptr, &args, nullptr) == MUONH_EINVAL);
 }
 
 int main() {
