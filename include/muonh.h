@@ -331,7 +331,7 @@ int muonh_adamw_destroy(muonh_adamw_handle* h);
 typedef struct muonh_fp8_matrix {
   void*   data;        /* E4M3 (OCP, no infinities) [rows x ld], device, 16-byte aligned   */
   void*   scale;       /* E8M0 bytes [ceil(rows / block_rows) x ld_scale], device, 4-byte
-                          aligned: value = data * 2^(byte - 127)                           */
+                          aligned: value = data * 2^(byte - 127), byte <= 254              */
   int64_t rows, cols;  /* cols: the contraction; either may be 0                           */
   int64_t ld;          /* bytes per row of data, a multiple of 128, >= cols; a product
                           reads columns cols .. up to the next multiple of 128, which
@@ -379,7 +379,7 @@ int muonh_block_matmul(const muonh_fp8_matrix* a, const muonh_fp8_matrix* b, voi
  * members are not read).  The outputs must stay valid until the stream has
  * passed the step, and may change between steps.  The first call on a handle
  * allocates its tables on the device (12 bytes per 128 x 128 block), which
- * muonh_destroy releases; not for use while `stream` is being captured.
+ * muonh_destroy releases; MUONH_ESTATE while `stream` is being captured.
  * Errors: as muonh_step; MUONH_EINVAL for an output whose shape, block_rows or
  * layout does not fit, that is named twice or that overlaps another (side by
  * side in rows of one pitch is allowed) or a W, M or G of the step; MUONH_ENOMEM. */

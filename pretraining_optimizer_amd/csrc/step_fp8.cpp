@@ -166,6 +166,11 @@ extern "C" int muonh_step_quantized(muonh_handle* h, const muonh_matrix_desc* ma
     if (!h || !args || !mats) return fail(MUONH_EINVAL, "null argument");
     if (n < 1) return fail(MUONH_EINVAL, "matrix count must be >= 1");
     if (!q && !qt) return fail(MUONH_EINVAL, "neither form is asked for");
+    // the tables are allocated and uploaded from the host: not for a recording
+    hipStreamCaptureStatus capture = hipStreamCaptureStatusNone;
+    if (hipStreamIsCapturing(reinterpret_cast<hipStream_t>(stream), &capture) == hipSuccess &&
+        capture != hipStreamCaptureStatusNone)
+      return fail(MUONH_ESTATE, "the stream is being captured");
     std::vector<QuantArgs> outs(n);
     for (int32_t i = 0; i < n; ++i) {
       const std::string name = "matrix " + std::to_string(i);

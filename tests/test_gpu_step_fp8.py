@@ -114,6 +114,26 @@ def test_step_refusals():
     ref.close()
 
 
+def test_step_is_refused_while_the_stream_is_captured():
+    w, m = torch.randn((200, 130), device="cuda"), torch.zeros((200, 130), device="cuda")
+    g = torch.randn((200, 130), device="cuda")
+    opt = pm.MuonH([w], [m], grad_dtype=torch.float32)
+    forms = pm.fp8_quantize(w, form="both", block_rows=128)
+    keep, x = w.clone(), torch.zeros(4, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        x.add_(1.0)
+        with pytest.raises(pm.MuonHError, match="captured"):
+            opt.step([g], elr=0.01, fp8=[forms])
+    graph.replay()
+    assert torch.equal(w, keep) and x.sum().item() == 4.0
+    opt.step([g], elr=0.01, fp8=[forms])   # outside it is an ordinary step
+    q, qt = pm.fp8_quantize(w, form="both", block_rows=128)
+    assert not torch.equal(w, keep) and _same(forms[0], q) and _same(forms[1], qt)
+    opt.close()
+
+
 @pytest.mark.parametrize("kind", ["rms", "layer"])
 def test_layer_training_steps(kind):
     """h = norm(x) W^T trained for three steps on sum (h - target)^2 / 2: norm,
