@@ -182,8 +182,9 @@ struct QuantLds {
 // padding up to a multiple of 128 is written as zeros.
 //
 // Bound by HBM (one read, one write per form): 8192 x 2048 bf16 to both forms
-// takes 15 us (4.5 TB/s).  What a thread does per element is kept to a mask, two packed maxima and a conversion per form that scales as
-// it converts; Inf and NaN take a path of their own, per thread.
+// takes 15 us (4.5 TB/s).  What a thread does per element is kept to a mask, two
+// packed maxima and a conversion per form that scales as it converts; Inf and
+// NaN take a path of their own, per thread.
 template <typename T, bool SQUARE>
 __device__ __forceinline__ void write_forms(const Row8<T> (&v)[4], const QuantArgs& p, uint32_t tr, uint32_t tc,
                                             QuantLds<T>& lds) {
@@ -458,7 +459,8 @@ __device__ __forceinline__ void store_c(C* c, int left, int accumulate, const f3
 // instruction does not matter.  The operands are swapped (B first): lane l then
 // holds columns 4 (l / 16) .. + 3 of row l % 16.  Rows behind the end read the
 // last one and are dropped.  1 x 16384 x 16384 takes 55 us (4.9 TB/s), 1 x 2048 x
-// 6144 6.6 us, most of it latency.
+// 6144 6.6 us, most of it latency; 2 to 4 blocks' loads per wavefront at a time
+// change neither (55 to 56, 6.4 to 7.5), and cost up to twice at K = 2048.
 template <typename C, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void block_matmul_thin_kernel(BlockMatmulArgs p, uint32_t ntiles) {
   __shared__ f32x4_t part[WAVES][64];
@@ -470,7 +472,6 @@ __global__ __launch_bounds__(64 * WAVES) void block_matmul_thin_kernel(BlockMatm
   const uint8_t* sa = p.sa + (int64_t)(m >> p.a_shift) * p.ldsa;
   const uint8_t* sb = p.sb + (int64_t)(n >> p.b_shift) * p.ldsb;
   f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
   for (int k = wave; k < p.kblocks; k += WAVES) {
     const u32x4_t a0 = ld_global<u32x4_t>(a + (int64_t)k * 128), a1 = ld_global<u32x4_t>(a + (int64_t)k * 128 + 16);
     const u32x4_t b0 = ld_global<u32x4_t>(b + (int64_t)k * 128), b1 = ld_global<u32x4_t>(b + (int64_t)k * 128 + 16);
