@@ -331,7 +331,7 @@ int muonh_adamw_destroy(muonh_adamw_handle* h);
 typedef struct muonh_fp8_matrix {
   void*   data;        /* E4M3 (OCP, no infinities) [rows x ld], device, 16-byte aligned   */
   void*   scale;       /* E8M0 bytes [ceil(rows / block_rows) x ld_scale], device, 4-byte
-                          aligned: value = data * 2^(byte - 127), byte <= 254              */
+                          aligned: value = data * 2^(byte - 127); byte 255 is NaN          */
   int64_t rows, cols;  /* cols: the contraction; either may be 0                           */
   int64_t ld;          /* bytes per row of data, a multiple of 128, >= cols; a product
                           reads columns cols .. up to the next multiple of 128, which

@@ -16,6 +16,7 @@
 // only rounding is the one to E4M3.  NaN and Inf become the E4M3 NaN, which
 // turns the outputs they take part in into NaN as the unquantised product does.
 
+#include <algorithm>
 #include <type_traits>
 
 #include "device_util.h"
@@ -458,24 +459,45 @@ __device__ __forceinline__ void store_c(C* c, int left, int accumulate, const f3
 // scale byte and both operands are laid out alike, so the K order inside an
 // instruction does not matter.  The operands are swapped (B first): lane l then
 // holds columns 4 (l / 16) .. + 3 of row l % 16.  Rows behind the end read the
-// last one and are dropped.  1 x 16384 x 16384 takes 55 us (4.9 TB/s), 1 x 2048 x
-// 6144 6.6 us, most of it latency; 2 to 4 blocks' loads per wavefront at a time
-// change neither (55 to 56, 6.4 to 7.5), and cost up to twice at K = 2048.
-template <typename C, int WAVES>
+// last one and are dropped.
+//
+// PARTS = 2: 8 x 8 outputs, for up to 8 rows (or columns).  Row 8 h + i of an
+// instruction's operands is row i of every second block from the h-th on, so the
+// two diagonal 8 x 8 quarters of its result are the product's two parts (the
+// others are dropped) and twice as many workgroups read the other operand.
+//
+// 1 x 24576 x 16384 takes 74 us (5.4 TB/s), 1 x 2048 x 6144 5.0 us, most of it
+// latency.  Several blocks' loads per wavefront at a time gain nothing (1 x 16384 x
+// 16384 with 1 to 4 blocks: 56, 56, 54 and 55 us, and up to twice the time at K =
+// 2048).
+template <typename C, int WAVES, int PARTS>
 __global__ __launch_bounds__(64 * WAVES) void block_matmul_thin_kernel(BlockMatmulArgs p, uint32_t ntiles) {
+  constexpr int kTile = 16 / PARTS;
   __shared__ f32x4_t part[WAVES][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int m0 = (int)(blockIdx.x / ntiles) * 16, n0 = (int)(blockIdx.x % ntiles) * 16;
-  const int m = min(m0 + (lane & 15), p.m - 1), n = min(n0 + (lane & 15), p.n - 1);
+  const int m0 = (int)(blockIdx.x / ntiles) * kTile, n0 = (int)(blockIdx.x % ntiles) * kTile;
+  const int at = lane & (kTile - 1), part_k = (lane & 15) / kTile;
+  const int m = min(m0 + at, p.m - 1), n = min(n0 + at, p.n - 1);
   const uint8_t* a = p.a + (int64_t)m * p.lda + (lane >> 4) * 32;
   const uint8_t* b = p.b + (int64_t)n * p.ldb + (lane >> 4) * 32;
   const uint8_t* sa = p.sa + (int64_t)(m >> p.a_shift) * p.ldsa;
   const uint8_t* sb = p.sb + (int64_t)(n >> p.b_shift) * p.ldsb;
   f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int k = wave; k < p.kblocks; k += WAVES) {
-    const u32x4_t a0 = ld_global<u32x4_t>(a + (int64_t)k * 128), a1 = ld_global<u32x4_t>(a + (int64_t)k * 128 + 16);
-    const u32x4_t b0 = ld_global<u32x4_t>(b + (int64_t)k * 128), b1 = ld_global<u32x4_t>(b + (int64_t)k * 128 + 16);
+  for (int k0 = PARTS * wave; k0 < p.kblocks; k0 += PARTS * WAVES) {
+    const int k = PARTS == 1 ? k0 : min(k0 + part_k, p.kblocks - 1);
+    u32x4_t a0 = ld_global<u32x4_t>(a + (int64_t)k * 128), a1 = ld_global<u32x4_t>(a + (int64_t)k * 128 + 16);
+    u32x4_t b0 = ld_global<u32x4_t>(b + (int64_t)k * 128), b1 = ld_global<u32x4_t>(b + (int64_t)k * 128 + 16);
     const uint32_t ea = ld_global<uint8_t>(sa + k), eb = ld_global<uint8_t>(sb + k);
+    if constexpr (PARTS > 1) {   // behind the last block nothing is added
+      const uint32_t keep = k0 + part_k < p.kblocks ? 0xffffffffu : 0u;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        a0[e] &= keep;
+        a1[e] &= keep;
+        b0[e] &= keep;
+        b1[e] &= keep;
+      }
+    }
     if constexpr (sizeof(C) == 2) {
       i32x8_t fa, fb;
 #pragma unroll
@@ -501,11 +523,14 @@ __global__ __launch_bounds__(64 * WAVES) void block_matmul_thin_kernel(BlockMatm
   part[wave][lane] = acc;
   __syncthreads();
   if (wave != 0) return;
-  f32x4_t s = part[0][lane];
+  const int row = m0 + at, col = n0 + (lane >> 4) * 4;
+  if (part_k != 0 || (lane >> 4) * 4 >= kTile || row >= p.m || col >= p.n) return;
+  // part k's outputs are 16 / PARTS rows and columns on: k kTile lanes and k kTile / 4 groups of 16
+  f32x4_t s = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+  for (int w = 0; w < WAVES; ++w)
 #pragma unroll
-  for (int w = 1; w < WAVES; ++w) s += part[w][lane];
-  const int row = m0 + (lane & 15), col = n0 + (lane >> 4) * 4;
-  if (row >= p.m || col >= p.n) return;
+    for (int h = 0; h < PARTS; ++h) s += part[w][lane + h * 5 * kTile];
   store_c<C>(reinterpret_cast<C*>(p.c) + (int64_t)row * p.ldc + col, p.n - col, p.accumulate, s);
 }
 
@@ -917,13 +942,39 @@ hipError_t matmul_for(const MatmulPlan& pl, BlockMatmulArgs a, float* workspace,
   a.splits = 1;
   a.split_blocks = a.kblocks;
   if (pl.ma == 0) {
-    const unsigned ntiles = (unsigned)((a.n + 15) / 16);
-    const dim3 grid(ntiles * (unsigned)((a.m + 15) / 16));
-    // few tiles need more wavefronts each to have enough loads in flight
-    if (a.kblocks >= 16 && grid.x <= 512)
-      hipLaunchKernelGGL((block_matmul_thin_kernel<C, 16>), grid, dim3(1024), 0, st, a, ntiles);
-    else
-      hipLaunchKernelGGL((block_matmul_thin_kernel<C, 4>), grid, dim3(256), 0, st, a, ntiles);
+    // 8 x 8 tiles where they fill the CUs' rounds better by a fifth (1 x 2048 x
+    // 6144, 128 or 256 workgroups: 6.5 and 5.0 us; 1 x 6144 x 16384, 384 or 768:
+    // 27.4 and 20.1; but 8 x 8192 x 6144, 512 or 1024: 13.4 and 16.6), and for one
+    // or two rows, which are cheap to read twice as often, with a long contraction
+    // and more than a round (1 x 8192 x 6144: 16.0 and 11.9; 1 x 24576 x 16384: 84 and
+    // 74; x 2048 at 12288 columns: 6.7 and 7.1).  Short contractions leave nothing to
+    // split (1 x 2048 x 1024: 3.2 and 3.1; x 512: 2.5 and 2.6).
+    auto rounds = [](int64_t groups) { return (groups + kCus - 1) / kCus; };
+    const int64_t big = ((a.m + 15) / 16) * (int64_t)((a.n + 15) / 16);
+    const int64_t small = ((a.m + 7) / 8) * (int64_t)((a.n + 7) / 8);
+    const int32_t least = std::min(a.m, a.n);
+    const bool two = least <= 8 && a.kblocks >= 8 &&
+                     (10 * rounds(big) >= 6 * rounds(small) ||
+                      (least <= 2 && a.kblocks >= 32 && big > kCus && small < (1 << 20)));
+    const int tile = two ? 8 : 16;
+    const unsigned ntiles = (unsigned)((a.n + tile - 1) / tile);
+    const dim3 grid(ntiles * (unsigned)((a.m + tile - 1) / tile));
+    // With at most one workgroup per CU, more wavefronts each: from 2 blocks per
+    // wavefront on (1 x 4096 x 2048: 4 wavefronts 4.9 us, 8 4.2; x 1024 3.5 and
+    // 3.4), and 16 from 4 blocks on (1 x 3000 x 16384: 8 wavefronts 16.8 us, 16 13.7;
+    // x 6144 6.7 and 6.8).  With more workgroups 4 do (8 x 8192 x 2048: 6.0, 6.5, 7.0).
+    const int blocks = a.kblocks / (two ? 2 : 1);
+    const int waves = grid.x > kCus || blocks < 16 ? 4 : blocks < 64 ? 8 : 16;
+#define MUONH_THIN(W, P)                                                                       \
+  if (waves == W && two == (P == 2))                                                           \
+  hipLaunchKernelGGL((block_matmul_thin_kernel<C, W, P>), grid, dim3(64 * W), 0, st, a, ntiles)
+    MUONH_THIN(4, 1);
+    MUONH_THIN(8, 1);
+    MUONH_THIN(16, 1);
+    MUONH_THIN(4, 2);
+    MUONH_THIN(8, 2);
+    MUONH_THIN(16, 2);
+#undef MUONH_THIN
     return hipGetLastError();
   }
   if (pl.splits == 1) return launch_tiles<kFp8, C>(pl, a, st);

@@ -196,7 +196,6 @@ constexpr TileRate kTileRates[] = {
     {2, 2, 2, {{0.64, 0.88, 0, 0}, {0.90, 1.64, 0, 0}}, {4.0, 6.0}, {1.10, 1.30, 0, 0}},
     {1, 1, 4, {{0.28, 0.44, 0.62, 0.79}, {0.40, 0.58, 0.85, 1.12}}, {3.5, 4.0}, {0.72, 0.97, 1.2, 1.4}},
 };
-constexpr int64_t kCus = 256;
 
 }  // namespace
 
@@ -211,7 +210,7 @@ MatmulPlan muonh::plan_block_matmul(int c_bf16, const BlockMatmulArgs& a) {
   MatmulPlan best{0, 0, 1, a.kblocks, 0};
   // Up to 16 rows (or columns) are one row block of the thin kernel, which reads
   // the other operand with more loads in flight and in one launch (1 x 16384 x
-  // 16384: 55 us, 68 in tiles; 1 x 2048 x 6144: 6.6 and 12.9; 17 x 16384 x 16384,
+  // 16384: 55 us, 68 in tiles; 1 x 2048 x 6144: 5.0 and 12.9; 17 x 16384 x 16384,
   // where it would read it twice: 86 and 68).  Tiles need panels of 256 rows of
   // values and of scales below 2^31 bytes (buffer offsets).
   const int64_t most = (int64_t)1 << 23;

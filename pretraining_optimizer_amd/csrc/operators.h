@@ -42,6 +42,8 @@ struct StepTile {
 hipError_t launch_update_quantize(int bf16, const StepTile* tiles, int64_t ntiles, const QuantArgs* outs,
                                   const MatGeom* geo, const MatPtrs* ptrs, const MatScalars* scal, hipStream_t st);
 
+constexpr int64_t kCus = 256;   // of an MI355X
+
 // C[m][n] (+)= sum_k A[m][k] B[n][k].
 struct BlockMatmulArgs {
   const uint8_t* a;

@@ -269,6 +269,41 @@ def test_matmul_empty():
     assert pm.fp8_matmul(none, some).shape == (0, 3) and pm.fp8_matmul(some, none).shape == (3, 0)
 
 
+NARROW = [(1, 37, 900), (8, 64, 5000), (3, 100, 17000), (7, 2000, 2200), (2, 8200, 4200), (1, 4110, 4097), (5, 3001, 1100),
+          (8, 4000, 2200), (12, 300, 9000), (9, 4097, 1025), (16, 6000, 2100), (8, 8, 1024), (1, 1, 16500)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("swap", [False, True])
+@pytest.mark.parametrize("m,n,k", NARROW)
+def test_matmul_narrow(m, n, k, swap, dtype):
+    """Up to 16 rows or columns: 4, 8 and 16 wavefronts, 16 x 16 outputs and 8 x 8
+    with the contraction in two parts, odd counts of blocks (the last has no
+    second part); a row of NaN and one with an infinity in the last block reach
+    their own outputs only; added to what c holds in rows of a larger pitch."""
+    m, n = (n, m) if swap else (m, n)
+    announce(f"matmul narrow {m}x{n}x{k} {dtype}")
+    x, y = _input(m, k, torch.float32, seed=5, spread=1.0), _input(n, k, torch.float32, seed=6, spread=1.0)
+    a, b = pm.fp8_quantize(x.cuda()), pm.fp8_quantize(y.cuda(), block_rows=128)
+    ra, rb = block_fp8.quantize(_np(x)), block_fp8.quantize(_np(y), 128)
+    ref = block_fp8.matmul(ra, rb)
+    tol = _tolerance(ra, rb, k, dtype, ref)
+    c = pm.fp8_matmul(a, b, out_dtype=dtype)
+    assert np.all(np.abs(_np(c) - ref) <= tol)
+    assert torch.equal(c, pm.fp8_matmul(a, b, out_dtype=dtype))
+    wide = torch.full((m, n + 3), 7.0, dtype=dtype, device="cuda")
+    wide[:, :n] = c
+    pm.fp8_matmul(a, b, out=wide[:, :n], accumulate=True)
+    twice = _np(c) + ref
+    assert np.all(np.abs(_np(wide[:, :n]) - twice) <= tol + (HALF[dtype] + 2.0 ** -23) * (np.abs(twice) + tol))
+    assert bool((wide[:, n:] == 7.0).all())
+    bad = a.data.view(torch.uint8)
+    bad[m - 1, k // 2] = 0x7f
+    y[n // 2, k - 1] = float("inf")
+    nan = torch.isnan(pm.fp8_matmul(a, pm.fp8_quantize(y.cuda()), out_dtype=dtype))
+    assert nan[m - 1].all() and nan[:, n // 2].all() and int(nan.sum()) == m + n - 1
+
+
 def test_matmul_scales_and_nan():
     """The least and the largest scales, a NaN scale byte, and a NaN element that
     reaches its row (column) alone."""
