@@ -451,86 +451,70 @@ __device__ __forceinline__ void store_c(C* c, int left, int accumulate, const f3
   }
 }
 
-// 16 x 16 outputs per workgroup, its WAVES wavefronts splitting the blocks of
-// the contraction: for up to 16 rows (or columns), where reading the other
-// operand is all there is to do and only many loads in flight per CU reach HBM's
-// rate.  The operands go straight into registers.  One 16x16x128 scaled MFMA
-// takes exactly one block of 128; every lane of a row carries the row's own
-// scale byte and both operands are laid out alike, so the K order inside an
-// instruction does not matter.  The operands are swapped (B first): lane l then
-// holds columns 4 (l / 16) .. + 3 of row l % 16.  Rows behind the end read the
-// last one and are dropped.
-//
-// PARTS = 2: 8 x 8 outputs, for up to 8 rows (or columns).  Row 8 h + i of an
-// instruction's operands is row i of every second block from the h-th on, so the
-// two diagonal 8 x 8 quarters of its result are the product's two parts (the
-// others are dropped) and twice as many workgroups read the other operand.
-//
-// 1 x 24576 x 16384 takes 74 us (5.4 TB/s), 1 x 2048 x 6144 5.0 us, most of it
-// latency.  Several blocks' loads per wavefront at a time gain nothing (1 x 16384 x
-// 16384 with 1 to 4 blocks: 56, 56, 54 and 55 us, and up to twice the time at K =
-// 2048).
-template <typename C, int WAVES, int PARTS>
-__global__ __launch_bounds__(64 * WAVES) void block_matmul_thin_kernel(BlockMatmulArgs p, uint32_t ntiles) {
-  constexpr int kTile = 16 / PARTS;
-  __shared__ f32x4_t part[WAVES][64];
+// Narrow products: up to 16 rows (or columns), where reading the other operand is
+// all there is to do and only many loads in flight per CU reach HBM's rate.  16 x
+// 16 outputs per workgroup, its wavefronts splitting the blocks of the
+// contraction.  One 16x16x128 scaled MFMA takes exactly one block of 128; every
+// lane of a row carries the row's own scale byte and both operands are laid out
+// alike, so the K order inside an instruction does not matter.  The operands are
+// swapped (B first): lane l then holds columns 4 (l / 16) .. + 3 of row l % 16.
+
+// multiplies 32 bytes per lane of one block into acc
+template <typename C>
+__device__ __forceinline__ void multiply16(f32x4_t& acc, const u32x4_t& a0, const u32x4_t& a1, const u32x4_t& b0,
+                                           const u32x4_t& b1, uint32_t ea, uint32_t eb) {
+  if constexpr (sizeof(C) == 2) {
+    i32x8_t fa, fb;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      fa[e] = (int)a0[e];
+      fa[4 + e] = (int)a1[e];
+      fb[e] = (int)b0[e];
+      fb[4 + e] = (int)b1[e];
+    }
+    acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb, fa, acc, 0, 0, 0, (int)eb, 0, (int)ea);
+  } else {
+    const float va = scale_value(ea), vb = scale_value(eb);
+#pragma unroll
+    for (int e = 0; e < 4; e += 2)
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8(b0[e], b0[e + 1], vb), widen8(a0[e], a0[e + 1], va),
+                                                    acc, 0, 0, 0);
+#pragma unroll
+    for (int e = 0; e < 4; e += 2)
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8(b1[e], b1[e + 1], vb), widen8(a1[e], a1[e + 1], va),
+                                                    acc, 0, 0, 0);
+  }
+}
+
+// Short contractions (and pitches beyond the other kernel's offsets): operands
+// straight into registers, rows behind the end read the last one and are
+// dropped.  The 64 lanes of a load lie in 16 rows, which costs the address path
+// four times what whole lines do: 16 x 2048 x 16384 takes 21.7 us, 12.2 through LDS.
+constexpr int kDirectWaves = 4;
+template <typename C>
+__global__ __launch_bounds__(64 * kDirectWaves) void block_matmul_direct_kernel(BlockMatmulArgs p, uint32_t ntiles) {
+  __shared__ f32x4_t part[kDirectWaves][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int m0 = (int)(blockIdx.x / ntiles) * kTile, n0 = (int)(blockIdx.x % ntiles) * kTile;
-  const int at = lane & (kTile - 1), part_k = (lane & 15) / kTile;
-  const int m = min(m0 + at, p.m - 1), n = min(n0 + at, p.n - 1);
+  const int m0 = (int)(blockIdx.x / ntiles) * 16, n0 = (int)(blockIdx.x % ntiles) * 16;
+  const int m = min(m0 + (lane & 15), p.m - 1), n = min(n0 + (lane & 15), p.n - 1);
   const uint8_t* a = p.a + (int64_t)m * p.lda + (lane >> 4) * 32;
   const uint8_t* b = p.b + (int64_t)n * p.ldb + (lane >> 4) * 32;
   const uint8_t* sa = p.sa + (int64_t)(m >> p.a_shift) * p.ldsa;
   const uint8_t* sb = p.sb + (int64_t)(n >> p.b_shift) * p.ldsb;
   f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int k0 = PARTS * wave; k0 < p.kblocks; k0 += PARTS * WAVES) {
-    const int k = PARTS == 1 ? k0 : min(k0 + part_k, p.kblocks - 1);
-    u32x4_t a0 = ld_global<u32x4_t>(a + (int64_t)k * 128), a1 = ld_global<u32x4_t>(a + (int64_t)k * 128 + 16);
-    u32x4_t b0 = ld_global<u32x4_t>(b + (int64_t)k * 128), b1 = ld_global<u32x4_t>(b + (int64_t)k * 128 + 16);
-    const uint32_t ea = ld_global<uint8_t>(sa + k), eb = ld_global<uint8_t>(sb + k);
-    if constexpr (PARTS > 1) {   // behind the last block nothing is added
-      const uint32_t keep = k0 + part_k < p.kblocks ? 0xffffffffu : 0u;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        a0[e] &= keep;
-        a1[e] &= keep;
-        b0[e] &= keep;
-        b1[e] &= keep;
-      }
-    }
-    if constexpr (sizeof(C) == 2) {
-      i32x8_t fa, fb;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        fa[e] = (int)a0[e];
-        fa[4 + e] = (int)a1[e];
-        fb[e] = (int)b0[e];
-        fb[4 + e] = (int)b1[e];
-      }
-      acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb, fa, acc, 0, 0, 0, (int)eb, 0, (int)ea);
-    } else {
-      const float va = scale_value(ea), vb = scale_value(eb);
-#pragma unroll
-      for (int e = 0; e < 4; e += 2)
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8(b0[e], b0[e + 1], vb), widen8(a0[e], a0[e + 1], va),
-                                                      acc, 0, 0, 0);
-#pragma unroll
-      for (int e = 0; e < 4; e += 2)
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8(b1[e], b1[e + 1], vb), widen8(a1[e], a1[e + 1], va),
-                                                      acc, 0, 0, 0);
-    }
+  for (int k = wave; k < p.kblocks; k += kDirectWaves) {
+    const u32x4_t a0 = ld_global<u32x4_t>(a + (int64_t)k * 128), a1 = ld_global<u32x4_t>(a + (int64_t)k * 128 + 16);
+    const u32x4_t b0 = ld_global<u32x4_t>(b + (int64_t)k * 128), b1 = ld_global<u32x4_t>(b + (int64_t)k * 128 + 16);
+    multiply16<C>(acc, a0, a1, b0, b1, ld_global<uint8_t>(sa + k), ld_global<uint8_t>(sb + k));
   }
   part[wave][lane] = acc;
   __syncthreads();
   if (wave != 0) return;
-  const int row = m0 + at, col = n0 + (lane >> 4) * 4;
-  if (part_k != 0 || (lane >> 4) * 4 >= kTile || row >= p.m || col >= p.n) return;
-  // part k's outputs are 16 / PARTS rows and columns on: k kTile lanes and k kTile / 4 groups of 16
-  f32x4_t s = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 8
-  for (int w = 0; w < WAVES; ++w)
+  f32x4_t s = part[0][lane];
 #pragma unroll
-    for (int h = 0; h < PARTS; ++h) s += part[w][lane + h * 5 * kTile];
+  for (int w = 1; w < kDirectWaves; ++w) s += part[w][lane];
+  const int row = m0 + (lane & 15), col = n0 + (lane >> 4) * 4;
+  if (row >= p.m || col >= p.n) return;
   store_c<C>(reinterpret_cast<C*>(p.c) + (int64_t)row * p.ldc + col, p.n - col, p.accumulate, s);
 }
 
@@ -563,6 +547,144 @@ constexpr int kScaleBlocks = 16;   // scales staged at a time, per row
 // 16-byte chunk c of a 128-byte LDS row r sits at c ^ swz128(r): the rows of a
 // fragment read then differ in banks whether 8 or 16 lanes are served at once.
 __device__ __forceinline__ int swz128(int r) { return (r & 7) ^ ((r >> 3) & 1); }
+
+// The same through LDS, in whole 128-byte lines.  A step is one block of 128 of
+// the contraction: 16 rows of A and of B, loaded straight into a slot of LDS that
+// only its wavefront uses (no barrier), four steps ahead.  Each wavefront has a
+// contiguous share of the blocks, so the scale bytes of four steps are one load.
+//
+// PARTS = 2: 8 x 8 outputs, for up to 8 rows (or columns).  Row 8 h + i of a slot
+// is row i of the share's h-th half, so the two diagonal 8 x 8 quarters of an
+// MFMA's result are the product's two parts (the others are dropped), and twice
+// as many workgroups read the other operand.
+//
+// Bound by HBM where that operand is large: 8 x 12288 x 16384 takes 38 us (5.3
+// TB/s), 16 x 24576 x 16384 85 us (4.7); 1 x 2048 x 6144 4.8 us, most of it latency.
+constexpr int kNarrowSteps = 4;
+constexpr int kNarrowSlot = 2 * 16 * kFp8Block;   // 16 rows of A, 16 of B
+
+template <typename C, int WAVES, int PARTS>
+__global__ __launch_bounds__(64 * WAVES) void block_matmul_narrow_kernel(BlockMatmulArgs p, uint32_t mt,
+                                                                           uint32_t nt) {
+  constexpr int kTile = 16 / PARTS;
+  __shared__ __attribute__((aligned(16))) uint8_t slot0[WAVES * kNarrowSlot];
+  __shared__ __attribute__((aligned(16))) uint8_t slot1[WAVES * kNarrowSlot];
+  __shared__ __attribute__((aligned(16))) uint8_t slot2[WAVES * kNarrowSlot];
+  __shared__ __attribute__((aligned(16))) uint8_t slot3[WAVES * kNarrowSlot];
+  __shared__ f32x4_t part[WAVES][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // Tiles of the shorter side vary first, 8 workgroups apart: on the same XCD, so
+  // the longer side's panel is in its L2.
+  const uint32_t few = min(mt, nt), one = (blockIdx.x / kMaxXcd) % few;
+  const uint32_t other = blockIdx.x / (kMaxXcd * few) * kMaxXcd + blockIdx.x % kMaxXcd;
+  if (other >= max(mt, nt)) return;
+  const int m0 = (int)(mt < nt ? one : other) * kTile, n0 = (int)(mt < nt ? other : one) * kTile;
+  const int mrows = min(kTile, p.m - m0), nrows = min(kTile, p.n - n0);
+  const int per = (p.kblocks + WAVES * PARTS - 1) / (WAVES * PARTS);
+
+  // loads
+  const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint8_t*>(p.a + (int64_t)m0 * p.lda), (short)0, (int)((mrows - 1) * p.lda) + p.kblocks * kFp8Block,
+      kBufferConfig);
+  const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint8_t*>(p.b + (int64_t)n0 * p.ldb), (short)0, (int)((nrows - 1) * p.ldb) + p.kblocks * kFp8Block,
+      kBufferConfig);
+  constexpr int kNowhere = 0x7ffffff0;   // behind every range: no memory access, zeros
+  int aoff[2], boff[2], kfirst[2], kcount[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int lrow = (lane >> 3) + 8 * j;              // row of the slot
+    const int row = PARTS == 1 ? lrow : lane >> 3;
+    const int worker = PARTS == 1 ? wave : wave * PARTS + j;
+    kfirst[j] = worker * per;                          // its share of the blocks, maybe none
+    kcount[j] = min(per, p.kblocks - worker * per);
+    const int chunk = ((lane & 7) ^ swz128(lrow)) * 16;
+    aoff[j] = row < mrows ? (int)(row * p.lda) + chunk : kNowhere;
+    boff[j] = row < nrows ? (int)(row * p.ldb) + chunk : kNowhere;
+  }
+  auto load_step = [&](uint8_t (&slot)[WAVES * kNarrowSlot], int i) {
+    MUONH_LDS uint8_t* d = (MUONH_LDS uint8_t*)slot + wave * kNarrowSlot;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const bool in = i < kcount[j];
+      const int k = in ? (kfirst[j] + i) * kFp8Block : 0;
+      const int ao = in ? aoff[j] : kNowhere, bo = in ? boff[j] : kNowhere;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (MUONH_LDS void*)(d + j * 1024), 16, ao, k, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (MUONH_LDS void*)(d + 2048 + j * 1024), 16, bo, k, 0, 0);
+    }
+  };
+
+  // fragments and scales
+  const int at = lane & (kTile - 1), part_k = (lane & 15) / kTile;
+  const int m = min(m0 + at, p.m - 1), n = min(n0 + at, p.n - 1);
+  const int first = (wave * PARTS + part_k) * per, count = min(per, p.kblocks - first);
+  const uint8_t* sa = p.sa + (int64_t)(m >> p.a_shift) * p.ldsa;
+  const uint8_t* sb = p.sb + (int64_t)(n >> p.b_shift) * p.ldsb;
+  typedef uint32_t word __attribute__((aligned(1)));
+  // the bytes of 4 steps, from a start that keeps the 4 inside the row; 127 (times
+  // the zeros that were loaded) behind the last block
+  auto load_scales = [&](const uint8_t* s, int i) {
+    const int k = min(first + i, ((p.kblocks + 3) & ~3) - 4);
+    return ld_global<word>(s + max(k, 0)) >> (8 * min(first + i - max(k, 0), 3));
+  };
+  auto scale_at = [&](uint32_t w, int i, int u) { return i < count ? (w >> (8 * u)) & 0xffu : 127u; };
+  const int fswz = swz128(lane & 15);
+  const int c0 = ((2 * (lane >> 4)) ^ fswz) << 4, c1 = ((2 * (lane >> 4) + 1) ^ fswz) << 4;
+  f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  u32x4_t a0, a1, b0, b1;
+  auto read_step = [&](uint8_t (&slot)[WAVES * kNarrowSlot]) {
+    const uint8_t* d = slot + wave * kNarrowSlot + (lane & 15) * kFp8Block;
+    a0 = *reinterpret_cast<const u32x4_t*>(d + c0);
+    a1 = *reinterpret_cast<const u32x4_t*>(d + c1);
+    b0 = *reinterpret_cast<const u32x4_t*>(d + 2048 + c0);
+    b1 = *reinterpret_cast<const u32x4_t*>(d + 2048 + c1);
+  };
+  auto multiply = [&](uint32_t ea, uint32_t eb) { multiply16<C>(acc, a0, a1, b0, b1, ea, eb); };
+  load_step(slot0, 0);
+  load_step(slot1, 1);
+  load_step(slot2, 2);
+  load_step(slot3, 3);
+  uint32_t wa = load_scales(sa, 0), wb = load_scales(sb, 0);
+  int i = 0;
+  auto step = [&](uint8_t (&slot)[WAVES * kNarrowSlot], int u) {
+    wait_loads<4 * (kNarrowSteps - 1)>();   // this step's loads are done, the next three may not be
+    read_step(slot);
+    wait_loads<63>();                       // the slot has been read
+    load_step(slot, i + u + kNarrowSteps);
+    multiply(scale_at(wa, i + u, u), scale_at(wb, i + u, u));
+  };
+  for (; i + kNarrowSteps < per; i += kNarrowSteps) {
+    const uint32_t na = load_scales(sa, i + kNarrowSteps), nb = load_scales(sb, i + kNarrowSteps);
+    step(slot0, 0);
+    step(slot1, 1);
+    step(slot2, 2);
+    step(slot3, 3);
+    wa = na;
+    wb = nb;
+  }
+  wait_loads<0>();
+  read_step(slot0);
+  multiply(scale_at(wa, i, 0), scale_at(wb, i, 0));
+  read_step(slot1);
+  multiply(scale_at(wa, i + 1, 1), scale_at(wb, i + 1, 1));
+  read_step(slot2);
+  multiply(scale_at(wa, i + 2, 2), scale_at(wb, i + 2, 2));
+  read_step(slot3);
+  multiply(scale_at(wa, i + 3, 3), scale_at(wb, i + 3, 3));
+  part[wave][lane] = acc;
+  __syncthreads();
+  if (wave != 0) return;
+  const int row = m0 + at, col = n0 + (lane >> 4) * 4;
+  if (part_k != 0 || (lane >> 4) * 4 >= kTile || row >= p.m || col >= p.n) return;
+  // part k's outputs are 16 / PARTS rows and columns on: k kTile lanes and k kTile / 4 groups of 16
+  f32x4_t s = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+  for (int w = 0; w < WAVES; ++w)
+#pragma unroll
+    for (int h = 0; h < PARTS; ++h) s += part[w][lane + h * 5 * kTile];
+  store_c<C>(reinterpret_cast<C*>(p.c) + (int64_t)row * p.ldc + col, p.n - col, p.accumulate, s);
+}
 
 // Tile of workgroup b: the hardware deals workgroups to the 8 XCDs in turn, so
 // XCD x gets a contiguous share of the tile list, and the list walks groups of
@@ -942,39 +1064,29 @@ hipError_t matmul_for(const MatmulPlan& pl, BlockMatmulArgs a, float* workspace,
   a.splits = 1;
   a.split_blocks = a.kblocks;
   if (pl.ma == 0) {
-    // 8 x 8 tiles where they fill the CUs' rounds better by a fifth (1 x 2048 x
-    // 6144, 128 or 256 workgroups: 6.5 and 5.0 us; 1 x 6144 x 16384, 384 or 768:
-    // 27.4 and 20.1; but 8 x 8192 x 6144, 512 or 1024: 13.4 and 16.6), and for one
-    // or two rows, which are cheap to read twice as often, with a long contraction
-    // and more than a round (1 x 8192 x 6144: 16.0 and 11.9; 1 x 24576 x 16384: 84 and
-    // 74; x 2048 at 12288 columns: 6.7 and 7.1).  Short contractions leave nothing to
-    // split (1 x 2048 x 1024: 3.2 and 3.1; x 512: 2.5 and 2.6).
-    auto rounds = [](int64_t groups) { return (groups + kCus - 1) / kCus; };
     const int64_t big = ((a.m + 15) / 16) * (int64_t)((a.n + 15) / 16);
-    const int64_t small = ((a.m + 7) / 8) * (int64_t)((a.n + 7) / 8);
     const int32_t least = std::min(a.m, a.n);
-    const bool two = least <= 8 && a.kblocks >= 8 &&
-                     (10 * rounds(big) >= 6 * rounds(small) ||
-                      (least <= 2 && a.kblocks >= 32 && big > kCus && small < (1 << 20)));
+    if (narrow_direct(a)) {
+      hipLaunchKernelGGL((block_matmul_direct_kernel<C>), dim3((unsigned)big), dim3(64 * kDirectWaves), 0, st, a,
+                         (unsigned)((a.n + 15) / 16));
+      return hipGetLastError();
+    }
+    // Long contractions take more workgroups (8 x 8 outputs) or wavefronts each: 8 x
+    // 6144 x 16384: 4 wavefronts 25.4 us, 8 24.6, 8 x 8 outputs 21.2; 16 x 12288 x
+    // 16384: 44.2 and 41.9.  Others not (8 x 6144 x 8192: 12.7, 8 x 8 outputs 14.0; 16 x
+    // 6144 x 8192: 14.3, 8 wavefronts 16.3), unless most CUs are idle (8 x 64 x 8192: 4.4
+    // and 3.6).
+    const bool two = least <= 8 && a.kblocks >= (big <= 64 ? 64 : 128);
     const int tile = two ? 8 : 16;
-    const unsigned ntiles = (unsigned)((a.n + tile - 1) / tile);
-    const dim3 grid(ntiles * (unsigned)((a.m + tile - 1) / tile));
-    // With at most one workgroup per CU, more wavefronts each: from 2 blocks per
-    // wavefront on (1 x 4096 x 2048: 4 wavefronts 4.9 us, 8 4.2; x 1024 3.5 and
-    // 3.4), and 16 from 4 blocks on (1 x 3000 x 16384: 8 wavefronts 16.8 us, 16 13.7;
-    // x 6144 6.7 and 6.8).  With more workgroups 4 do (8 x 8192 x 2048: 6.0, 6.5, 7.0).
-    const int blocks = a.kblocks / (two ? 2 : 1);
-    const int waves = grid.x > kCus || blocks < 16 ? 4 : blocks < 64 ? 8 : 16;
-#define MUONH_THIN(W, P)                                                                       \
-  if (waves == W && two == (P == 2))                                                           \
-  hipLaunchKernelGGL((block_matmul_thin_kernel<C, W, P>), grid, dim3(64 * W), 0, st, a, ntiles)
-    MUONH_THIN(4, 1);
-    MUONH_THIN(8, 1);
-    MUONH_THIN(16, 1);
-    MUONH_THIN(4, 2);
-    MUONH_THIN(8, 2);
-    MUONH_THIN(16, 2);
-#undef MUONH_THIN
+    const unsigned mt = (unsigned)((a.m + tile - 1) / tile), nt = (unsigned)((a.n + tile - 1) / tile);
+    const unsigned few = std::min(mt, nt), many = (std::max(mt, nt) + kMaxXcd - 1) / kMaxXcd * kMaxXcd;
+    const dim3 grid(few * many);
+    if (two)
+      hipLaunchKernelGGL((block_matmul_narrow_kernel<C, 4, 2>), grid, dim3(256), 0, st, a, mt, nt);
+    else if (a.kblocks >= 128)
+      hipLaunchKernelGGL((block_matmul_narrow_kernel<C, 8, 1>), grid, dim3(512), 0, st, a, mt, nt);
+    else
+      hipLaunchKernelGGL((block_matmul_narrow_kernel<C, 4, 1>), grid, dim3(256), 0, st, a, mt, nt);
     return hipGetLastError();
   }
   if (pl.splits == 1) return launch_tiles<kFp8, C>(pl, a, st);

@@ -185,10 +185,11 @@ namespace {
 struct TileRate {
   int32_t ma, nb, per_cu;
   double block[2][4], round[2];
-  // the least time of a block where operands beyond the caches (64 MB) are read
-  // by up to four tiles each, so from HBM
+  // the least time of a block where operands beyond an XCD's L2 (kColdBytes) are
+  // read by up to four tiles each, so from further away
   double cold[4];
 };
+constexpr int64_t kColdBytes = (int64_t)4 << 20;
 constexpr TileRate kTileRates[] = {
     {4, 4, 1, {{1.61, 0, 0, 0}, {2.88, 0, 0, 0}}, {8.8, 16.3}, {1.7, 0, 0, 0}},
     {4, 3, 1, {{1.20, 0, 0, 0}, {2.17, 0, 0, 0}}, {10.0, 13.1}, {1.4, 0, 0, 0}},
@@ -202,25 +203,29 @@ constexpr TileRate kTileRates[] = {
 // The plan with the least time by the table: full rounds of workgroups over the
 // CUs, then the rest.  What decides is how the tiles fill the last round
 // (2048 x 6144 x 8192 to fp32: 192 tiles of 256 x 256 take 192 us, 256 of 256 x
-// 192 take 155), and for few tiles whether splitting a long contraction repays
-// its second launch and the partial sums' traffic (300 x 300 x 16384: 58 us
-// whole, 18 us split by 8; 1000 x 777 x 1500: 9.3 us whole, 14 us split by 2).
+// 192 take 155), for few tiles whether splitting a long contraction repays its
+// second launch and the partial sums' traffic (128 x 16384 x 8192: 40 us split by 4,
+// 56 whole; 1000 x 777 x 1500: 9.3 us whole, 14 us split by 2), and whether the
+// product is small enough for the narrow kernels.
 MatmulPlan muonh::plan_block_matmul(int c_bf16, const BlockMatmulArgs& a) {
   const int64_t m = a.m, n = a.n, nk = a.kblocks;
   MatmulPlan best{0, 0, 1, a.kblocks, 0};
-  // Up to 16 rows (or columns) are one row block of the thin kernel, which reads
-  // the other operand with more loads in flight and in one launch (1 x 16384 x
-  // 16384: 55 us, 68 in tiles; 1 x 2048 x 6144: 5.0 and 12.9; 17 x 16384 x 16384,
-  // where it would read it twice: 86 and 68).  Tiles need panels of 256 rows of
-  // values and of scales below 2^31 bytes (buffer offsets).
+  // Up to 16 rows (or columns) are narrow: the other operand is read once, at HBM's
+  // rate (16 x 12288 x 16384: 42 us, 50 in tiles).  Tiles need panels of 256 rows
+  // of values and of scales below 2^31 bytes (buffer offsets).
   const int64_t most = (int64_t)1 << 23;
   if (nk == 0 || m <= 16 || n <= 16 || a.lda >= most || a.ldb >= most || a.ldsa >= most || a.ldsb >= most)
     return best;
   const int arith = c_bf16 ? 0 : 1;
-  double best_us = 0.0;
+  // Narrow for more rows, in 16 x 16 outputs that each read their 32 rows: measured
+  // time of a block per workgroup on each CU (at least the latency of its share).
+  // 32 x 2048 x 2048: 4.0 us, 10.1 in tiles; 64 x 512 x 6144: 5.4 and 10.8; but 48 x
+  // 12288 x 2048: 13.5 and 10.9.
+  const double per_cu = (double)(ceil_div(m, 16) * ceil_div(n, 16)) / kCus;
+  double best_us = narrow_direct(a) ? 2.6 + 0.14 * nk * per_cu : 2.5 + nk * std::max(0.045, 0.066 * per_cu);
   for (const TileRate& r : kTileRates) {
     const int64_t mt = ceil_div(m, 64 * r.ma), nt = ceil_div(n, 64 * r.nb), tiles = mt * nt;
-    const bool cold = (m + n) * nk * kFp8Block >= ((int64_t)64 << 20) && std::min(mt, nt) <= 4;
+    const bool cold = (m + n) * nk * kFp8Block >= kColdBytes && std::min(mt, nt) <= 4;
     auto block_us = [&](int64_t per) { return std::max(r.block[arith][per - 1], cold ? r.cold[per - 1] : 0.0); };
     for (int64_t splits = 1; splits <= 16; splits *= 2) {
       // whole scale words (4 blocks) per workgroup, at least 4 blocks
@@ -232,7 +237,7 @@ MatmulPlan muonh::plan_block_matmul(int c_bf16, const BlockMatmulArgs& a) {
       if (rest > 0) us += block_us(ceil_div(rest, kCus)) * blocks + r.round[arith];
       // a launch, a workspace, and partials written and read at about 4 TB/s
       if (used > 1) us += 6.0 + (double)((2 * used + 1) * m * n) * 4.0 / 4e6;
-      if (best.ma == 0 || us < best_us) {
+      if (us < best_us) {
         best_us = us;
         best = MatmulPlan{r.ma, r.nb, (int32_t)used, (int32_t)blocks,
                           used > 1 ? sizeof(float) * (size_t)(used * m * n) : 0};

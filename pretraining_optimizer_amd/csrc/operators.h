@@ -60,7 +60,19 @@ struct BlockMatmulArgs {
   int32_t splits, split_blocks;
 };
 
-// How a product runs: 64 ma x 64 nb tiles (ma = 0: the thin kernel), the
+// Whether a narrow product's operands go straight into registers, not through
+// LDS.  There 16 rows' offsets have to fit 31 bits, and 2^22 workgroups a launch.
+// Short contractions are quicker without (1 x 12288 x 1024: 5.0 us, 5.7 through LDS;
+// 16 x 6144 x 1024: 4.8 and 4.2; 1 x 6144 x 512: 2.8 and 3.4; 1 x 37984 x 2048: 16.6
+// and 17.9, 16 rows of it 25 and 20).
+inline bool narrow_direct(const BlockMatmulArgs& a) {
+  const int64_t tiles = (((int64_t)a.m + 15) / 16) * (((int64_t)a.n + 15) / 16);
+  const int32_t least = a.m < a.n ? a.m : a.n;
+  return a.lda >= (1 << 27) || a.ldb >= (1 << 27) || tiles > (1 << 22) || a.kblocks < 8 ||
+         (a.kblocks < (least <= 2 ? 32 : 16) && tiles > 2 * kCus);
+}
+
+// How a product runs: 64 ma x 64 nb tiles (ma = 0: a narrow kernel), the
 // contraction split over `splits` workgroups of split_blocks blocks each, whose
 // partial matrices then take workspace_bytes.
 struct MatmulPlan {

@@ -73,8 +73,9 @@ static void plans() {
           CHECK(p.workspace_bytes == (p.splits > 1 ? sizeof(float) * (size_t)p.splits * (size_t)(m * n) : 0));
           split += p.splits > 1;
           if (m <= 16 || n <= 16 || k == 0) CHECK(p.ma == 0 && p.splits == 1);
-          else CHECK(p.ma > 0);
-          // panels beyond the tile kernel's 32-bit offsets go to the thin kernel
+          if (p.ma == 0) CHECK(p.splits == 1);
+          if (m >= 256 && n >= 2048 && k >= 8192) CHECK(p.ma > 0);
+          // panels beyond the tile kernel's 32-bit offsets go to the narrow kernels
           a.ldb = (int64_t)1 << 23;
           CHECK(plan_block_matmul(bf16, a).ma == 0);
         }
@@ -93,11 +94,11 @@ static void refusals() {
   CHECK(muonh_block_matmul_workspace(&a, &b, MUONH_F32, &need) == MUONH_OK);
   CHECK(muonh_block_matmul(&a, &b, c, MUONH_F32, 200, 0, nullptr, 0, nullptr) == MUONH_EHIP);
   CHECK(muonh_block_matmul(&a, &b, c, MUONH_F32, 199, 0, nullptr, 0, nullptr) == MUONH_EINVAL);
-  muonh_fp8_matrix la = mat(300, 16000, 1, base), lb = mat(300, 16000, 1, base + ((uintptr_t)1 << 38));
+  muonh_fp8_matrix la = mat(400, 9000, 1, base), lb = mat(700, 9000, 1, base + ((uintptr_t)1 << 38));
   CHECK(muonh_block_matmul_workspace(&la, &lb, MUONH_F32, &need) == MUONH_OK && need > 0);
-  CHECK(muonh_block_matmul(&la, &lb, c, MUONH_F32, 300, 0, nullptr, 0, nullptr) == MUONH_ENOMEM);
-  CHECK(muonh_block_matmul(&la, &lb, c, MUONH_F32, 300, 0, base, need - 1, nullptr) == MUONH_ENOMEM);
-  CHECK(muonh_block_matmul(&la, &lb, c, MUONH_F32, 300, 0, base + 64, need, nullptr) == MUONH_EINVAL);
+  CHECK(muonh_block_matmul(&la, &lb, c, MUONH_F32, 700, 0, nullptr, 0, nullptr) == MUONH_ENOMEM);
+  CHECK(muonh_block_matmul(&la, &lb, c, MUONH_F32, 700, 0, base, need - 1, nullptr) == MUONH_ENOMEM);
+  CHECK(muonh_block_matmul(&la, &lb, c, MUONH_F32, 700, 0, base + 64, need, nullptr) == MUONH_EINVAL);
   CHECK(muonh_block_quantize(c, MUONH_BF16, 300, 500, 500, &a, nullptr, nullptr) == MUONH_EHIP);
   CHECK(muonh_block_quantize(c, MUONH_BF16, 300, 500, 499, &a, nullptr, nullptr) == MUONH_EINVAL);
 

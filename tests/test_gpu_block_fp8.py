@@ -163,12 +163,14 @@ def test_matmul_shapes(m, n, k, blocks, dtype):
 
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("m,n,k", [(2047, 6143, 1100), (6143, 2047, 1100), (4000, 4004, 2200), (8190, 8001, 640),
-                                   (2001, 1999, 640), (1501, 1300, 16200), (300, 301, 5000), (60, 2000, 9000)])
+                                   (2001, 1999, 640), (1501, 1300, 16200), (300, 301, 5000), (60, 2000, 9000),
+                                   (401, 700, 9000), (65, 6143, 9000), (701, 1101, 300), (501, 1101, 2100), (1203, 901, 700)])
 def test_matmul_tiles_ragged(m, n, k, dtype):
     """Sizes that take tiles of 256 x 192, 192 x 256, 256 x 256, 128 x 128 and
-    64 x 64, whole and with a split contraction, with odd counts of blocks (the
-    last trip's second block lies behind the operands), cut tiles on both axes
-    and scales behind the last block that are NaN; every output."""
+    64 x 64, whole and with a split contraction, and many narrow outputs, with odd
+    counts of blocks (the last trip's second block lies behind the operands), cut
+    tiles on both axes and scales behind the last block that are NaN; every
+    output."""
     announce(f"matmul ragged tiles {m}x{n}x{k} {dtype}")
     gen = torch.Generator(device="cuda").manual_seed(m + n)
     kb = -(-k // 128)
@@ -270,17 +272,19 @@ def test_matmul_empty():
 
 
 NARROW = [(1, 37, 900), (8, 64, 5000), (3, 100, 17000), (7, 2000, 2200), (2, 8200, 4200), (1, 4110, 4097), (5, 3001, 1100),
-          (8, 4000, 2200), (12, 300, 9000), (9, 4097, 1025), (16, 6000, 2100), (8, 8, 1024), (1, 1, 16500)]
+          (8, 4000, 2200), (12, 300, 9000), (9, 4097, 1025), (16, 6000, 2100), (8, 8, 1024), (1, 1, 16500), (12, 300, 16500), (9, 1000, 20100),
+          (40, 300, 2100), (100, 33, 17000), (129, 70, 900)]
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("swap", [False, True])
 @pytest.mark.parametrize("m,n,k", NARROW)
 def test_matmul_narrow(m, n, k, swap, dtype):
-    """Up to 16 rows or columns: 4, 8 and 16 wavefronts, 16 x 16 outputs and 8 x 8
-    with the contraction in two parts, odd counts of blocks (the last has no
-    second part); a row of NaN and one with an infinity in the last block reach
-    their own outputs only; added to what c holds in rows of a larger pitch."""
+    """Up to 16 rows or columns, and small products: straight from memory and
+    through LDS, 4 and 8 wavefronts, 16 x 16 outputs and 8 x 8 with the contraction
+    in two parts, shares of the blocks that are cut short; a row of NaN and one with
+    an infinity in the last block reach their own outputs only; added to what c
+    holds in rows of a larger pitch."""
     m, n = (n, m) if swap else (m, n)
     announce(f"matmul narrow {m}x{n}x{k} {dtype}")
     x, y = _input(m, k, torch.float32, seed=5, spread=1.0), _input(n, k, torch.float32, seed=6, spread=1.0)
@@ -302,6 +306,22 @@ def test_matmul_narrow(m, n, k, swap, dtype):
     y[n // 2, k - 1] = float("inf")
     nan = torch.isnan(pm.fp8_matmul(a, pm.fp8_quantize(y.cuda()), out_dtype=dtype))
     assert nan[m - 1].all() and nan[:, n // 2].all() and int(nan.sum()) == m + n - 1
+
+
+@pytest.mark.parametrize("rows,ld", [(16, (1 << 27) - 128), (2, 1 << 27)])
+@pytest.mark.parametrize("swap", [False, True])
+def test_matmul_narrow_pitch(rows, ld, swap):
+    """The largest pitch whose 16 rows' offsets fit 31 bits, and the next."""
+    announce(f"matmul narrow pitch {rows} rows {ld} apart")
+    (a, ra), (b, rb) = _operand(rows, 2100, 1, 7), _operand(40, 2100, 128, 8)
+    data = torch.empty((rows, ld), dtype=torch.uint8, device="cuda")
+    data[:, :2176] = a.data.view(torch.uint8)
+    far = pm.Fp8Matrix(data.view(torch.float8_e4m3fn), a.scale, 2100)
+    want = pm.fp8_matmul(b, a, out_dtype=torch.float32) if swap else pm.fp8_matmul(a, b, out_dtype=torch.float32)
+    got = pm.fp8_matmul(b, far, out_dtype=torch.float32) if swap else pm.fp8_matmul(far, b, out_dtype=torch.float32)
+    ref = block_fp8.matmul(rb, ra) if swap else block_fp8.matmul(ra, rb)
+    tol = _tolerance(rb, ra, 2100, torch.float32, ref) if swap else _tolerance(ra, rb, 2100, torch.float32, ref)
+    assert np.all(np.abs(_np(got) - ref) <= tol) and np.all(np.abs(_np(want) - ref) <= tol)
 
 
 def test_matmul_scales_and_nan():
@@ -368,11 +388,12 @@ def test_matmul_streams_and_graph():
         assert torch.equal(out, again), k
 
 
-def test_two_products_at_once_and_two_graphs():
-    """Split contractions (a workspace each) on two streams at once, and in two
-    graphs replayed in turn on changed operands."""
-    announce("two products at once")
-    x, y = torch.randn((300, 5000), device="cuda"), torch.randn((400, 5000), device="cuda")
+@pytest.mark.parametrize("m,n,k", [(300, 400, 5000), (401, 700, 9000)])
+def test_two_products_at_once_and_two_graphs(m, n, k):
+    """Whole and split contractions (these with a workspace each) on two streams
+    at once, and in two graphs replayed in turn on changed operands."""
+    announce(f"two products at once {m}x{n}x{k}")
+    x, y = torch.randn((m, k), device="cuda"), torch.randn((n, k), device="cuda")
     qx, qy = pm.fp8_quantize(x), pm.fp8_quantize(y)
     want = [pm.fp8_matmul(qx, qy, out_dtype=torch.float32), pm.fp8_matmul(qy, qx, out_dtype=torch.float32)]
     streams = [torch.cuda.Stream(), torch.cuda.Stream()]
@@ -390,13 +411,13 @@ def test_two_products_at_once_and_two_graphs():
         with torch.cuda.graph(g):
             outs.append(pm.fp8_matmul(p, q, out_dtype=torch.float32))
         graphs.append(g)
-    for k in range(3):
-        pm.fp8_quantize(x.mul_(0.5 + k), out=qx)
+    for i in range(3):
+        pm.fp8_quantize(x.mul_(0.5 + i), out=qx)
         for g in graphs:
             g.replay()
         torch.cuda.synchronize()
-        assert torch.equal(outs[0], pm.fp8_matmul(qx, qy, out_dtype=torch.float32)), k
-        assert torch.equal(outs[1], pm.fp8_matmul(qy, qx, out_dtype=torch.float32)), k
+        assert torch.equal(outs[0], pm.fp8_matmul(qx, qy, out_dtype=torch.float32)), i
+        assert torch.equal(outs[1], pm.fp8_matmul(qy, qx, out_dtype=torch.float32)), i
 
 
 def test_python_refusals():

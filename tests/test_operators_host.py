@@ -187,12 +187,12 @@ def test_norm_backward_refuses_overlapping_vectors(kw):
 
 def test_matmul_refuses_overlapping_workspace():
     lib = pm.load_library()
-    a, b = _mat(cols=16384), _mat(cols=16384, data=BASE * 4, scale=BASE * 5)
+    a, b = _mat(rows=400, cols=9216), _mat(rows=700, cols=9216, data=BASE * 4, scale=BASE * 5)
     need = ctypes.c_size_t()
     assert lib.muonh_block_matmul_workspace(ctypes.byref(a), ctypes.byref(b), pm.MUONH_F32, ctypes.byref(need)) == mb.MUONH_OK
     assert need.value > 0
     for ws in (BASE, BASE + (1 << 32), BASE * 4 + 256, BASE * 5, BASE * 2):
-        rc = lib.muonh_block_matmul(ctypes.byref(a), ctypes.byref(b), BASE * 2, pm.MUONH_F32, 256, 0, ws, need.value, None)
+        rc = lib.muonh_block_matmul(ctypes.byref(a), ctypes.byref(b), BASE * 2, pm.MUONH_F32, 700, 0, ws, need.value, None)
         _refused(rc, mb.MUONH_EINVAL, "workspace overlaps")
 
 
