@@ -282,9 +282,9 @@ NARROW = [(1, 37, 900), (8, 64, 5000), (3, 100, 17000), (7, 2000, 2200), (2, 820
 def test_matmul_narrow(m, n, k, swap, dtype):
     """Up to 16 rows or columns, and small products: straight from memory and
     through LDS, 4 and 8 wavefronts, 16 x 16 outputs and 8 x 8 with the contraction
-    in two parts, shares of the blocks that are cut short; a row of NaN and one with
-    an infinity in the last block reach their own outputs only; added to what c
-    holds in rows of a larger pitch."""
+    in two parts, shares of the blocks that are cut short.  A NaN in one row, an
+    infinity or a NaN scale in the last block of another reach their own outputs
+    only.  Added to what c holds in rows of a larger pitch."""
     m, n = (n, m) if swap else (m, n)
     announce(f"matmul narrow {m}x{n}x{k} {dtype}")
     x, y = _input(m, k, torch.float32, seed=5, spread=1.0), _input(n, k, torch.float32, seed=6, spread=1.0)
@@ -306,6 +306,10 @@ def test_matmul_narrow(m, n, k, swap, dtype):
     y[n // 2, k - 1] = float("inf")
     nan = torch.isnan(pm.fp8_matmul(a, pm.fp8_quantize(y.cuda()), out_dtype=dtype))
     assert nan[m - 1].all() and nan[:, n // 2].all() and int(nan.sum()) == m + n - 1
+    bad[m - 1, k // 2] = 0
+    a.scale[0, (k - 1) // 128] = 255   # the last block of one row
+    nan = torch.isnan(pm.fp8_matmul(a, b, out_dtype=dtype))
+    assert nan[0].all() and int(nan.sum()) == n
 
 
 @pytest.mark.parametrize("rows,ld", [(16, (1 << 27) - 128), (2, 1 << 27)])
