@@ -321,10 +321,11 @@ __global__ __launch_bounds__(G > kBackThreads ? G : kBackThreads) void norm_back
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         h[k][j] = (h[k][j] - mu) * r;
+        // Columns behind the end have no weight gradient to write, and dy = w = 0;
+        // h is 0 there too, as (0 - mu) r may be infinite (rms: x = mu = 0).
+        if (LAYER && 8 * (t + G * k) + j >= cols) h[k][j] = 0.0f;
         // a group behind the last row adds nothing
         if (live) {
-          // columns behind the end have no weight gradient to write; their
-          // dy and w are zero, so they add nothing to the row's sums
           acc[0][k][j] += g[k][j] * h[k][j];
           if constexpr (BIAS) acc[1][k][j] += g[k][j];
         }

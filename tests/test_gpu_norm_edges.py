@@ -1,0 +1,56 @@
+"""Rows at which the norms' kernels can go wrong by their layout, on an MI355X
+against the fp64 oracle: columns behind a row's end."""
+
+import numpy as np
+import pytest
+import torch
+
+import pretraining_optimizer_amd as pm
+from oracle import norm
+from parity import announce
+from test_gpu_norm import DTYPES, HALF, U, _np
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("cols", [1, 3, 32, 100, 200, 300, 777, 1500, 2500, 5001, 9000, 17000])
+def test_columns_behind_a_row_add_nothing(cols, dtype, bias):
+    """Rows that are constant at 2^119 with a deviation of 2^-10: mean * rstd is
+    beyond fp32, and no column of the row has that product.
+
+    x - mean is zero, so h = 0, dw = 0 and dx = r (g - mean g): g off by u |g|, the
+    mean by 70 u mean|g| (64 additions, the terms and the division), the difference
+    and the product by u each; half a step of dx's type.  db: as dw of the other
+    tests (rows / 512 + 80 additions)."""
+    announce(f"norm far constant rows {cols} {dtype} bias {bias}")
+    rows = 5
+    gen = torch.Generator().manual_seed(cols)
+    dy = torch.randn((rows, cols), generator=gen).to(dtype).cuda()
+    w = (1.0 + 0.2 * torch.randn(cols, generator=gen)).cuda()
+    x = torch.full((rows, cols), 2.0 ** 119, dtype=dtype, device="cuda")
+    mean, rstd = torch.full((rows,), 2.0 ** 119, device="cuda"), torch.full((rows,), 2.0 ** 10, device="cuda")
+    dx, dw, db = pm.norm_backward(dy, x, w, mean, rstd, kind="layer", bias=bias)
+    ref, _, rdb = norm.norm_backward(_np(dy), _np(x), _np(w), _np(mean), _np(rstd), "layer")
+    g = np.abs(_np(dy) * _np(w))
+    off = 2.0 ** 10 * (4 * U * g + 72 * U * g.mean(1, keepdims=True))
+    assert np.all(np.abs(_np(dx) - ref) <= off + HALF[dtype] * (np.abs(ref) + off))
+    assert not dw.any()
+    if bias:
+        assert np.all(np.abs(_np(db) - rdb) <= (rows / 512 + 80) * U * np.abs(_np(dy)).sum(0))
+
+
+def test_constant_far_rows_through_both_passes():
+    """The same through the forward pass: 32 values of 2^119, whose sum is exact, and
+    eps = 1e-6, so rstd = 1000 and mean * rstd is 6.6e38."""
+    x = torch.full((3, 32), 2.0 ** 119, device="cuda")
+    w, b = torch.ones(32, device="cuda"), torch.full((32,), 0.25, device="cuda")
+    y, mean, rstd = pm.norm_forward(x, w, b, kind="layer", eps=1e-6)
+    assert torch.equal(y, b.expand(3, 32)) and torch.all(mean == 2.0 ** 119)
+    dy = torch.randn((3, 32), generator=torch.Generator().manual_seed(1)).cuda()
+    dx, dw, _ = pm.norm_backward(dy, x, w, mean, rstd, kind="layer")
+    g = _np(dy)
+    ref = _np(rstd)[:, None] * (g - g.mean(1, keepdims=True))
+    off = _np(rstd)[:, None] * (4 * U * np.abs(g) + 72 * U * np.abs(g).mean(1, keepdims=True))
+    assert np.all(np.abs(_np(dx) - ref) <= off + U * (np.abs(ref) + off)) and not dw.any()
