@@ -1,5 +1,5 @@
 """Rows at which the norms' kernels can go wrong by their layout, on an MI355X
-against the fp64 oracle: columns behind a row's end."""
+against the fp64 oracle: columns behind a row's end, very long rows."""
 
 import numpy as np
 import pytest
@@ -8,7 +8,7 @@ import torch
 import pretraining_optimizer_amd as pm
 from oracle import norm
 from parity import announce
-from test_gpu_norm import DTYPES, HALF, U, _np
+from test_gpu_norm import DTYPES, HALF, KINDS, U, _check_backward, _check_forward, _np
 
 pytestmark = pytest.mark.gpu
 
@@ -54,3 +54,25 @@ def test_constant_far_rows_through_both_passes():
     ref = _np(rstd)[:, None] * (g - g.mean(1, keepdims=True))
     off = _np(rstd)[:, None] * (4 * U * np.abs(g) + 72 * U * np.abs(g).mean(1, keepdims=True))
     assert np.all(np.abs(_np(dx) - ref) <= off + U * (np.abs(ref) + off)) and not dw.any()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_very_long_rows(dtype, kind):
+    """Rows of 2^22 + 3 columns, 4097 per thread, to the same 64 u: a sum of one
+    sign (a constant row, whose partial sums outgrow the terms) and a mixed one."""
+    announce(f"norm very long rows {dtype} {kind}")
+    cols = (1 << 22) + 3
+    gen = torch.Generator().manual_seed(11)
+    x = torch.randn((2, cols), generator=gen)
+    x[0] = 141 / 128
+    x[1] += 0.3
+    x = x.to(dtype).cuda()
+    dy = torch.randn((2, cols), generator=gen)
+    dy[0] = 0.1015625
+    dy = dy.to(dtype).cuda()
+    w = (1.0 + 0.2 * torch.randn(cols, generator=gen)).cuda()
+    got = pm.norm_forward(x, w, None, kind=kind, eps=1e-5)
+    _check_forward(got, x, w, None, kind, 1e-5, dtype, "forward")
+    _, mean, rstd = got
+    _check_backward(pm.norm_backward(dy, x, w, mean, rstd, kind=kind, bias=True), dy, x, w, mean, rstd, kind, dtype, "backward")
