@@ -382,7 +382,8 @@ int muonh_block_matmul(const muonh_fp8_matrix* a, const muonh_fp8_matrix* b, voi
  * muonh_destroy releases; MUONH_ESTATE while `stream` is being captured.
  * Errors: as muonh_step; MUONH_EINVAL for an output whose shape, block_rows or
  * layout does not fit, that is named twice or that overlaps another (side by
- * side in rows of one pitch is allowed) or a W, M or G of the step; MUONH_ENOMEM. */
+ * side in rows of one pitch is allowed), a W, M or G of the step or the handle's
+ * workspace (also the caller's, muonh_options.workspace); MUONH_ENOMEM.      */
 int muonh_step_quantized(muonh_handle* h, const muonh_matrix_desc* mats, int32_t n,
                          const muonh_fp8_matrix* q, const muonh_fp8_matrix* qt,
                          const muonh_step_args* args, void* stream);

@@ -959,8 +959,9 @@ std::shared_ptr<void>& muonh::step_extension(muonh_handle* h) { return h->extens
 int muonh::step_with_tail(muonh_handle* h, const muonh_matrix_desc* mats, int32_t n,
                           const muonh_step_args* args, hipStream_t st, const StepTail& tail) {
   const float* scale_dev = nullptr;
-  int rc = prepare_step(h, mats, n, args, st, &scale_dev);
+  int rc = tail.check(tail.context, h->ws, h->plan.total);
   if (rc) return rc;
+  if ((rc = prepare_step(h, mats, n, args, st, &scale_dev))) return rc;
   if ((rc = tail.prepare(tail.context, st))) return rc;
   if ((rc = enqueue_step(h, st, step_params(h->plan, args->elr), scale_dev, nullptr, &tail))) return rc;
   h->last_stream = st;

@@ -68,9 +68,22 @@ struct Context {
   muonh_handle* h;
   const muonh_matrix_desc* mats;
   int32_t n;
+  const muonh_fp8_matrix* q;
+  const muonh_fp8_matrix* qt;
   const std::vector<QuantArgs>* outs;
   QuantizedStep* step;
 };
+
+// No output lies in the handle's workspace, from which the launches read the
+// update, the coefficients and their tables while others write the outputs.
+int check(void* context, const void* workspace, size_t bytes) {
+  const auto* c = static_cast<const Context*>(context);
+  for (int32_t i = 0; i < c->n; ++i)
+    for (const muonh_fp8_matrix* f : {c->q, c->qt})
+      if (f && f[i].data && fp8_overlaps(f[i], workspace, (int64_t)bytes))
+        return fail(MUONH_EINVAL, "matrix " + std::to_string(i) + ": an output overlaps the handle's workspace");
+  return MUONH_OK;
+}
 
 int prepare(void* context, hipStream_t st) {
   auto* c = static_cast<Context*>(context);
@@ -190,8 +203,8 @@ extern "C" int muonh_step_quantized(muonh_handle* h, const muonh_matrix_desc* ma
     }
     if (outputs_overlap(mats, n, q, qt))
       return fail(MUONH_EINVAL, "an output is named twice, or overlaps another, a weight, a gradient or a momentum");
-    Context c{h, mats, n, &outs, nullptr};
+    Context c{h, mats, n, q, qt, &outs, nullptr};
     return step_with_tail(h, mats, n, args, reinterpret_cast<hipStream_t>(stream),
-                          StepTail{prepare, launch, &c});
+                          StepTail{check, prepare, launch, &c});
   });
 }

@@ -8,10 +8,12 @@
 
 namespace muonh {
 
-// A step whose last launch is another than launch_update: `prepare` runs after
-// the step's own checks and uploads, before its first launch; `launch` in place
-// of the update.  `context` is the caller's.
+// A step whose last launch is another than launch_update: `check` runs before
+// anything is enqueued, with the handle's workspace (the caller's, where the
+// options gave one); `prepare` after the step's own checks and uploads, before its
+// first launch; `launch` in place of the update.  `context` is the caller's.
 struct StepTail {
+  int (*check)(void* context, const void* workspace, size_t bytes);
   int (*prepare)(void* context, hipStream_t st);
   hipError_t (*launch)(void* context, int bf16, const MatGeom* geo, const MatPtrs* ptrs,
                        const MatScalars* scal, hipStream_t st);
