@@ -1,5 +1,6 @@
 """Rows at which the norms' kernels can go wrong by their layout, on an MI355X
-against the fp64 oracle: columns behind a row's end, very long rows."""
+against the fp64 oracle: columns behind a row's end, very long rows,
+several long rows per workgroup, more rows than a launch takes at once."""
 
 import numpy as np
 import pytest
@@ -8,7 +9,7 @@ import torch
 import pretraining_optimizer_amd as pm
 from oracle import norm
 from parity import announce
-from test_gpu_norm import DTYPES, HALF, KINDS, U, _check_backward, _check_forward, _np
+from test_gpu_norm import DTYPES, HALF, KINDS, U, _check_backward, _check_forward, _inputs, _np
 
 pytestmark = pytest.mark.gpu
 
@@ -76,3 +77,45 @@ def test_very_long_rows(dtype, kind):
     _check_forward(got, x, w, None, kind, 1e-5, dtype, "forward")
     _, mean, rstd = got
     _check_backward(pm.norm_backward(dy, x, w, mean, rstd, kind=kind, bias=True), dy, x, w, mean, rstd, kind, dtype, "backward")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rows,cols,dtype", [(133, 5001, torch.float32), (133, 9000, torch.bfloat16), (133, 17000, torch.float32),
+                                             (600, 9000, torch.float32), (600, 5001, torch.bfloat16), (600, 17000, torch.bfloat16),
+                                             (1100, 3001, torch.float32)])
+def test_several_long_rows_per_workgroup(rows, cols, dtype, kind):
+    """Two and three rows per workgroup of the backward pass for the row lengths of
+    512 and 1024 threads and for those beyond the registers, into new and into given
+    gradients."""
+    announce(f"norm {rows}x{cols} {dtype} {kind}")
+    x, dy, w, b = (t.cuda() for t in _inputs(rows, cols, dtype))
+    for bias in (None, b):
+        got = pm.norm_forward(x, w, bias, kind=kind, eps=1e-5)
+        _check_forward(got, x, w, bias, kind, 1e-5, dtype, "forward")
+        _, mean, rstd = got
+        got = pm.norm_backward(dy, x, w, mean, rstd, kind=kind, bias=bias is not None)
+        _check_backward(got, dy, x, w, mean, rstd, kind, dtype, "backward")
+        given = [torch.randn(cols, generator=torch.Generator().manual_seed(5 + i)).cuda() for i in range(2)]
+        before = {"dw": _np(given[0]), "db": _np(given[1])}
+        got = pm.norm_backward(dy, x, w, mean, rstd, kind=kind, dweight=given[0], dbias=given[1] if bias is not None else None, accumulate=True)
+        _check_backward(got, dy, x, w, mean, rstd, kind, dtype, "accumulate", before)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rows,cols,dtype", [((1 << 25) + 5, 1, torch.float32), ((1 << 21) + 5, 1025, torch.bfloat16)])
+def test_more_rows_than_one_trip_of_a_forward_launch(rows, cols, dtype, kind):
+    """2^20 workgroups take 2^25 rows of one column or 2^21 of 1025 (whose groups of
+    two wavefronts add through LDS); the rows of the next trip, and windows around
+    its start, equal the same rows alone."""
+    announce(f"norm forward {rows}x{cols} {kind}")
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.empty((rows, cols), dtype=dtype, device="cuda").normal_(generator=gen)
+    w = torch.randn(cols, generator=gen, device="cuda")
+    b = torch.randn(cols, generator=gen, device="cuda")
+    y, mean, rstd = pm.norm_forward(x, w, b, kind=kind, eps=1e-5)
+    for r0, r1 in ((0, 100), (rows // 2, rows // 2 + 77), (rows - 45, rows)):
+        alone = pm.norm_forward(x[r0:r1], w, b, kind=kind, eps=1e-5)
+        _check_forward(alone, x[r0:r1], w, b, kind, 1e-5, dtype, "window")
+        assert torch.equal(y[r0:r1], alone[0]) and torch.equal(rstd[r0:r1], alone[2])
+        assert mean is None or torch.equal(mean[r0:r1], alone[1])
+    assert bool(torch.isfinite(y).all()) and bool(torch.isfinite(rstd).all())
