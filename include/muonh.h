@@ -356,11 +356,17 @@ int muonh_block_quantize(const void* x, int32_t dtype, int64_t rows, int64_t col
  * rounded once to c_dtype (MUONH_F32 or MUONH_BF16, ldc elements between
  * rows); accumulate = 1 adds the product to what c holds.  With a.cols = 0 the
  * product is zero.  Results are the same in every call on the same operands.
- * A bf16 c is computed by the FP8 matrix unit, whose sums are 2e-5 off (of the
- * result's norm; bf16 rounds by 1.7e-3); an fp32 c by the bf16 matrix unit on
- * widened operands, with fp32 sums, at half that rate.  There an operand's
- * value of 2^128 or more (scale byte 247 and data of 256 or more) is infinite,
- * and one below 2^-126 may lose bits.
+ * c_dtype chooses the arithmetic, too:
+ *   bf16  the FP8 matrix unit, which of every 8 products drops what lies 2^-13
+ *         below the largest.  With S the sum of |a_k b_k|, a sum is off by at most
+ *         7 2^-13 S; 3e-7 S on normal operands, 4e-6 S on values over all of E4M3
+ *         (measured, norms).  Where signs are random that is 2e-5 of the result,
+ *         which bf16 hides (it rounds by 1.7e-3); where products cancel, not.
+ *   fp32  the bf16 matrix unit on widened operands, with fp32 sums (at most
+ *         K 2^-23 S; 1e-9 S), at half that rate.  For a bf16 result with such
+ *         sums, round this one.  Here an operand's value of 2^128 or more (scale
+ *         byte 247 and data of 256 or more) is infinite, and one below 2^-126 may
+ *         lose bits.
  * workspace: device memory of muonh_block_matmul_workspace bytes, 256-byte
  * aligned, or NULL where that is 0; calls that may overlap in time need one
  * each.  Errors: MUONH_EINVAL, MUONH_ENOMEM (workspace too small), MUONH_EHIP. */

@@ -1,6 +1,6 @@
 """Every tile kernel of the block-scaled FP8 product, whole and with a split
-contraction (the sizes whose plans tests/test_matmul_plans_host.py pins), on an
-MI355X against the product in 64 bits of the same FP8 values.
+contraction (the sizes whose plans tests/test_matmul_plans_host.py pins), and sums
+that cancel, on an MI355X against the product in 64 bits of the same FP8 values.
 
 Bounds per element, with S = sum |a_k b_k|: products of E4M3 values and powers of
 two are exact in fp32.  A chain of fewer than K additions, each off by at most one
@@ -122,3 +122,48 @@ def test_least_and_largest_scales(m, n, k, result):
             want = float("inf")   # the operands' own values are formed: 256 2^(247 - 127) = 2^128
         c = pm.fp8_matmul(qa, qb, out_dtype=dtype)
         assert torch.all(c.double() == want), (ea, eb, c[0, 0].item(), want)
+
+
+CANCELLING = [(1, 300, 4096), (16, 700, 16384), (300, 300, 4096), (1300, 1500, 2304), (401, 700, 9216), (2047, 6143, 2304)]
+
+
+def _grid(rows, k, gen):
+    """E4M3 bytes spread over the whole type, NaN apart."""
+    code = torch.randint(0, 127, (rows, k), generator=gen, device="cuda", dtype=torch.int32)
+    sign = torch.randint(0, 2, (rows, k), generator=gen, device="cuda", dtype=torch.int32) << 7
+    return (code | sign).to(torch.uint8)
+
+
+@pytest.mark.parametrize("order", ["halves", "shuffled", "pairs"])
+@pytest.mark.parametrize("m,n,k", CANCELLING)
+def test_sums_that_cancel(m, n, k, order):
+    """Operands [u, u] and [v, -v], apart, shuffled and element by element, of values
+    spread over all of E4M3: every product sum is zero, and what is left is at most
+    the bound in S = 2 sum |u v|, which no share of the result's norm could state.
+    An fp32 result, rounded to bf16 afterwards, keeps to K 2^-23 S."""
+    announce(f"matmul cancelling {m}x{n}x{k} {order}")
+    gen = torch.Generator(device="cuda").manual_seed(m + n + k)
+    u, v = _grid(m, k // 2, gen), _grid(n, k // 2, gen)
+    a, b = torch.cat([u, u], 1), torch.cat([v, v ^ 0x80], 1)
+    if order != "halves":
+        at = torch.arange(k, device="cuda").view(2, k // 2).t().reshape(-1) if order == "pairs" else \
+            torch.randperm(k, generator=gen, device="cuda")
+        a, b = a[:, at].contiguous(), b[:, at].contiguous()
+    qa, qb = (pm.Fp8Matrix(d.view(torch.float8_e4m3fn), torch.full((d.shape[0], -(-k // 512) * 4), 127, dtype=torch.uint8, device="cuda"), k)
+              for d in (a, b))
+    x, y = _value(qa), _value(qb)
+    s = x.abs() @ y.abs().t().contiguous()
+    for dtype in TYPES.values():
+        c = pm.fp8_matmul(qa, qb, out_dtype=dtype).double().abs()
+        off = _off(k, dtype, s)
+        assert bool((c <= off + HALF[dtype] * off).all()), (dtype, float((c / s).max()))
+    c = pm.fp8_matmul(qa, qb, out_dtype=torch.float32).bfloat16().double().abs()
+    assert bool((c <= (1 + 2.0 ** -8) * _off(k, torch.float32, s)).all())
+    # one part more in u: the sum is u v' exactly, small against S
+    qb.data.view(torch.uint8)[:, 0] = 0x38   # 1.0
+    y = _value(qb)
+    ref = x @ y.t().contiguous()
+    for dtype in TYPES.values():
+        off = _off(k, dtype, s + x[:, :1].abs())
+        c = pm.fp8_matmul(qa, qb, out_dtype=dtype).double()
+        assert bool(((c - ref).abs() <= off + HALF[dtype] * (ref.abs() + off)).all())
