@@ -354,8 +354,8 @@ __global__ __launch_bounds__(kQuantThreads) void block_quantize_kernel(QuantArgs
 // read and written once and never read again for its quantisation.  The update's
 // arithmetic is update_kernel's (the product k2 u rounded, then one fused
 // multiply-add), so W comes out bitwise the same.  Bound by HBM: 12 bytes per
-// parameter at 5.5 TB/s over 1.41 G parameters (3.09 ms; the plain update takes
-// 2.17 ms and a separate quantisation 2.7 more).
+// parameter at 5.5 TB/s over 1.41 G parameters (3.08 ms; the plain update takes
+// 2.16 ms and a separate quantisation 2.4 more).
 template <typename U>
 __global__ __launch_bounds__(kQuantThreads) void update_quantize_kernel(
     const StepTile* __restrict__ tiles, const QuantArgs* __restrict__ outs, const MatGeom* __restrict__ geo,

@@ -11,8 +11,8 @@
 // and its output, so each of these streams passes once; the variance is taken
 // about the mean of the values in hand, not from a difference of moments.
 // Statistics, sums and the weight gradient are fp32; each output element is
-// rounded once.  8192 x 2048 bf16: forward 12.5 us (5.4 TB/s, part of it from the
-// 256 MB cache), backward 18.4 us and 3.5 us for the partial rows' sum (4.6 TB/s).
+// rounded once.  8192 x 2048 bf16, calls in a row: forward 12.8 us (5.2 TB/s, part of
+// it from the 256 MB cache), backward with the partial rows' sum 21.8 us (4.6 TB/s).
 // Loads and stores are ordinary ones: the input was just written by another
 // operator and the output is read by the next (8192 x 2048 fp32 forward: 27.4 us,
 // 32.3 with non-temporal accesses).

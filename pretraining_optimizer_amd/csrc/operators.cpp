@@ -219,8 +219,10 @@ MatmulPlan muonh::plan_block_matmul(int c_bf16, const BlockMatmulArgs& a) {
   const int arith = c_bf16 ? 0 : 1;
   // Narrow for more rows, in 16 x 16 outputs that each read their 32 rows: measured
   // time of a block per workgroup on each CU (at least the latency of its share).
-  // 32 x 2048 x 2048: 4.0 us, 10.1 in tiles; 64 x 512 x 6144: 5.4 and 10.8; but 48 x
-  // 12288 x 2048: 13.5 and 10.9.
+  // 32 x 2048 x 2048: 3.6 us, 7.1 in tiles; 64 x 512 x 6144: 4.4 and 9.8.  One price
+  // of operands beyond L2 per tile shape (`cold`) is too high for some long operands
+  // of few tile rows, which go narrow where tiles are quicker: 48 x 12288 x 2048 13.5
+  // us (11.0), 32 x 6144 x 16384 34.1 (26.6), 64 x 6144 x 6144 17.2 (15.3).
   const double per_cu = (double)(ceil_div(m, 16) * ceil_div(n, 16)) / kCus;
   double best_us = narrow_direct(a) ? 2.6 + 0.14 * nk * per_cu : 2.5 + nk * std::max(0.045, 0.066 * per_cu);
   for (const TileRate& r : kTileRates) {
