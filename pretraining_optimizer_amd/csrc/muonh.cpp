@@ -771,6 +771,9 @@ int prepare_step(muonh_handle* h, const muonh_matrix_desc* mats, int32_t n,
   int dev = 0;
   HIP_TRY(hipGetDevice(&dev));
   if (dev != h->device) return fail(MUONH_EINVAL, "current device differs from the one at init");
+  // The launches read their status from hipGetLastError: an error that the thread
+  // left behind earlier is not theirs.
+  (void)hipGetLastError();
   // The workspace was last used (or initialised) on h->last_stream.
   if ((rc = order_after_last(h, st))) return rc;
 

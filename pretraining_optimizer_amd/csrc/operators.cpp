@@ -287,6 +287,7 @@ int muonh_block_quantize(const void* x, int32_t dtype, int64_t rows, int64_t col
     if (q) set_row_form(a, *q);
     if (qt) set_column_form(a, *qt);
     const int32_t block = q ? q->block_rows : qt->block_rows;
+    forget_older_errors();
     return launched(launch_block_quantize(dtype == MUONH_BF16, block == 128, a,
                                           reinterpret_cast<hipStream_t>(stream)),
                     "block_quantize");
@@ -333,6 +334,7 @@ int muonh_block_matmul(const muonh_fp8_matrix* a, const muonh_fp8_matrix* b, voi
     const int64_t nws = (int64_t)plan.workspace_bytes;
     if (overlap(workspace, nws, c, nc) || fp8_overlaps(*a, workspace, nws) || fp8_overlaps(*b, workspace, nws))
       return fail(MUONH_EINVAL, "workspace overlaps c or an operand");
+    forget_older_errors();
     return launched(launch_block_matmul(c_dtype == MUONH_BF16, plan, p, static_cast<float*>(workspace),
                                         reinterpret_cast<hipStream_t>(stream)),
                     "block_matmul");
@@ -376,6 +378,7 @@ int muonh_norm_forward(const muonh_norm_args* g, void* stream) {
     a.ldx = g->ldx;
     a.ldy = g->ldy;
     a.eps = g->eps;
+    forget_older_errors();
     return launched(launch_norm_forward(g->dtype == MUONH_BF16, layer, a, reinterpret_cast<hipStream_t>(stream)),
                     "norm_forward");
   });
@@ -446,6 +449,7 @@ int muonh_norm_backward(const muonh_norm_grad_args* g, void* stream) {
     a.ldx = g->ldx;
     a.lddx = g->ld_dx;
     a.accumulate = g->accumulate;
+    forget_older_errors();
     return launched(launch_norm_backward(g->dtype == MUONH_BF16, layer, a, reinterpret_cast<hipStream_t>(stream)),
                     "norm_backward");
   });

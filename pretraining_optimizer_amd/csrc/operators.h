@@ -126,6 +126,11 @@ int64_t fp8_scale_bytes(const muonh_fp8_matrix& m);
 // Whether an operand's values or scales share memory with [p, p + bytes).
 bool fp8_overlaps(const muonh_fp8_matrix& m, const void* p, int64_t bytes);
 
+// HIP keeps a failed call's error until it is read, and a launch's own is read the
+// same way: one that the thread left behind earlier (an allocation that it gave up
+// on) would be taken for the launch's.
+inline void forget_older_errors() { (void)hipGetLastError(); }
+
 // Runs the body of a C entry point; nothing is thrown across the ABI.
 template <typename F>
 int guarded(F&& body) {

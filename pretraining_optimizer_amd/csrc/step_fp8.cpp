@@ -41,8 +41,10 @@ struct QuantizedStep {
 #define QSTEP_HIP(expr)                                                                 \
   do {                                                                                  \
     hipError_t e_ = (expr);                                                             \
-    if (e_ != hipSuccess)                                                               \
+    if (e_ != hipSuccess) {                                                             \
+      forget_older_errors(); /* reported here */                                        \
       return fail(MUONH_EHIP, std::string(#expr) + ": " + hipGetErrorString(e_));       \
+    }                                                                                   \
   } while (0)
 
 // The tables of a handle's first quantised step.
@@ -56,8 +58,10 @@ int make_tables(const muonh_matrix_desc* mats, int32_t n, std::shared_ptr<Quanti
   q->ntiles = (int64_t)tiles.size();
   if (hipMalloc(reinterpret_cast<void**>(&q->d_tiles), sizeof(StepTile) * tiles.size()) != hipSuccess ||
       hipMalloc(reinterpret_cast<void**>(&q->d_outs), sizeof(QuantArgs) * n) != hipSuccess ||
-      hipHostMalloc(reinterpret_cast<void**>(&q->staging), sizeof(QuantArgs) * n, hipHostMallocDefault) != hipSuccess)
+      hipHostMalloc(reinterpret_cast<void**>(&q->staging), sizeof(QuantArgs) * n, hipHostMallocDefault) != hipSuccess) {
+    forget_older_errors();
     return fail(MUONH_ENOMEM, "allocation of the quantised step's tables failed");
+  }
   QSTEP_HIP(hipEventCreateWithFlags(&q->uploaded, hipEventDisableTiming));
   QSTEP_HIP(hipMemcpy(q->d_tiles, tiles.data(), sizeof(StepTile) * tiles.size(), hipMemcpyHostToDevice));
   out = std::move(q);
