@@ -90,21 +90,31 @@ def _vector(t, n: int, what: str):
         raise ValueError(f"{what}: a contiguous float32 vector of {n} elements is required")
 
 
-def _empty(shape, dtype, device, stream):
+def _on(stream, make, result=True):
     """A new tensor that work on `stream` may write at once: memory of that
-    stream's pool, so no earlier work of another stream still uses it."""
+    stream's pool, so no earlier work of another stream still uses it.  A result is
+    used on torch's current stream afterwards (behind a wait), so its memory returns
+    to the pool only behind that stream's work."""
+    user = _torch.cuda.current_stream()
+    with _torch.cuda.stream(stream):
+        t = make()
+    if result and user != stream:
+        t.record_stream(user)
+    return t
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor for work on `stream`, or on torch's current stream."""
     if stream is None:
         return _torch.empty(shape, dtype=dtype, device=device)
-    with _torch.cuda.stream(stream):
-        return _torch.empty(shape, dtype=dtype, device=device)
+    return _on(stream, lambda: _torch.empty(shape, dtype=dtype, device=device))
 
 
-def _like(t, shape, stream):
+def _like(t, shape, stream, result=True):
     """_empty of t's dtype and device (the quicker call)."""
     if stream is None:
         return t.new_empty(shape)
-    with _torch.cuda.stream(stream):
-        return t.new_empty(shape)
+    return _on(stream, lambda: t.new_empty(shape), result)
 
 
 class Fp8Matrix:
@@ -238,7 +248,7 @@ def fp8_matmul(a: Fp8Matrix, b: Fp8Matrix, out=None, out_dtype=None, accumulate:
     if rc:
         _check(rc, "muonh_block_matmul_workspace")
     need = need.value
-    ws = _like(a.scale, need, stream) if need else None
+    ws = _like(a.scale, need, stream, result=False) if need else None
     if stream is not None:
         _record(stream, [a.data, a.scale, b.data, b.scale, out] + ([] if ws is None else [ws]))
     rc = _lib.muonh_block_matmul(ra, rb, out.data_ptr(), code, ldc, 1 if accumulate else 0,
@@ -332,7 +342,7 @@ def norm_backward(dy, x, weight, mean, rstd, kind: str = "rms", bias: bool = Fal
     if rc:
         _check(rc, "muonh_norm_backward_workspace")
     need = need.value
-    ws = _like(weight, need // 4, stream) if need else None
+    ws = _like(weight, need // 4, stream, result=False) if need else None
     args = muonh_norm_grad_args(
         dy.data_ptr(), x.data_ptr(), weight.data_ptr(), None if mean is None else mean.data_ptr(), rstd.data_ptr(),
         dx.data_ptr(), dweight.data_ptr(), None if dbias is None else dbias.data_ptr(), rows, cols,
