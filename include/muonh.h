@@ -363,10 +363,10 @@ int muonh_block_quantize(const void* x, int32_t dtype, int64_t rows, int64_t col
  *         (measured, norms).  Where signs are random that is 2e-5 of the result,
  *         which bf16 hides (it rounds by 1.7e-3); where products cancel, not.
  *   fp32  the bf16 matrix unit on widened operands, with fp32 sums (at most
- *         K 2^-23 S; 1e-9 S), at half that rate.  For a bf16 result with such
- *         sums, round this one.  Here an operand's value of 2^128 or more (scale
- *         byte 247 and data of 256 or more) is infinite, and one below 2^-126 may
- *         lose bits.
+ *         K 2^-23 S; 1e-9 and 2e-8 S measured as above), at half that rate.  For a
+ *         bf16 result with such sums, round this one.  Here an operand's value of
+ *         2^128 or more (scale byte 247 and data of 256 or more) is infinite, and
+ *         one below 2^-126 may lose bits.
  * workspace: device memory of muonh_block_matmul_workspace bytes, 256-byte
  * aligned, or NULL where that is 0; calls that may overlap in time need one
  * each.  Errors: MUONH_EINVAL, MUONH_ENOMEM (workspace too small), MUONH_EHIP. */

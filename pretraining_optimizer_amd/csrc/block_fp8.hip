@@ -413,7 +413,7 @@ __global__ __launch_bounds__(kQuantThreads) void update_quantize_kernel(
 // E4M3.  So a bf16 C is computed by the scaled FP8 instructions, which also apply
 // both E8M0 scales; an fp32 C by the bf16 instructions on operands widened in
 // registers with their scales (exact above 2^-126), which keep full fp32 sums
-// (1e-9 S) at half the rate, also for callers who round them to bf16.
+// (1e-9 and 2e-8 S) at half the rate, also for callers who round them to bf16.
 
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
@@ -757,8 +757,9 @@ __global__ __launch_bounds__(kTileThreads) void block_matmul_tile_kernel(BlockMa
   // Loads: instruction i of a wavefront fills rows 16 MA wave + 8 i .. + 7 of A
   // (NB of B); lane l lands in row l / 8, slot chunk l % 8.  Rows behind the
   // matrix and blocks behind the last are out of the descriptor's range: they
-  // make no memory access and leave zeros.  (The host keeps 256 rows below 2^31
-  // bytes.)
+  // make no memory access and leave zeros.  The range check counts the scalar
+  // offset, word by word, and does not wrap where that alone is behind the range
+  // (checked on the device).  The host keeps 256 rows below 2^31 bytes.
   const uint8_t* abase = p.a + (int64_t)row0 * p.lda;
   const uint8_t* bbase = p.b + (int64_t)col0 * p.ldb;
   // to the end of the last row's last block
