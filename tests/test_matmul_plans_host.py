@@ -7,7 +7,8 @@ import subprocess
 
 import pytest
 
-from matmul_plans import OTHERS, TILES
+import test_gpu_block_fp8
+from matmul_plans import KERNELS, TILES
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -41,8 +42,21 @@ def plans(tmp_path_factory):
 def test_plans_of_the_tested_sizes(plans, blocks):
     got = plans([(m, n, k, *blocks, t) for m, n, k, t, _ in TILES])
     assert [g[:4] for g in got] == [want for *_, want in TILES]
-    got = plans([(m, n, k, *blocks, t) for m, n, k, t, _ in OTHERS])
-    assert [(g[0], g[1], g[2] > 1, g[4] == 1) for g in got] == [want for *_, want in OTHERS]
+    for (bf16, f32), sizes in KERNELS.items():
+        for result, want in (("bf16", bf16), ("f32", f32)):
+            for size, p in zip(sizes, plans([(*s, *blocks, result) for s in sizes])):
+                tile = f"{64 * p[0]}x{64 * p[1]}" + (" split" if p[2] > 1 else "")
+                kernel = tile if p[0] else "direct" if p[4] else "narrow"
+                assert kernel == want, (size, result)
+
+
+def test_every_size_of_the_gpu_tests_is_pinned():
+    pinned = {size for sizes in KERNELS.values() for size in sizes}
+    tested = test_gpu_block_fp8.SHAPES + test_gpu_block_fp8.NARROW + [(n, m, k) for m, n, k in test_gpu_block_fp8.NARROW]
+    for name in ("test_matmul_tiles_ragged", "test_matmul_accumulate_and_pitch", "test_two_products_at_once_and_two_graphs"):
+        marks = getattr(test_gpu_block_fp8, name).pytestmark
+        tested += [size for m in marks if m.name == "parametrize" and m.args[0] == "m,n,k" for size in m.args[1]]
+    assert set(tested) <= pinned
 
 
 def test_every_tile_that_a_product_takes_is_tested(plans):
