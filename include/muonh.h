@@ -402,10 +402,11 @@ int muonh_step_quantized(muonh_handle* h, const muonh_matrix_desc* mats, int32_t
  *   y = h weight (+ bias);  mean and rstd keep mu and r for the gradient
  *   dx = r (g - [mean(g)] - h mean(g h)),  g = dy weight     ([]: layer only)
  *   dweight = sum over rows of dy h,  dbias = sum over rows of dy
- * Statistics and sums are fp32, sums in a fixed order.  x, y, dy and dx share
- * one dtype (MUONH_F32 or MUONH_BF16) and need element alignment only; the
- * vectors are fp32.  y may be x, and dx may be x or dy (same address and
- * pitch); an output or workspace that overlaps anything else is refused.     */
+ * Statistics and sums are fp32, sums in a fixed order (those of squares too: a
+ * row whose sum is beyond 3.4e38 gets rstd 0).  x, y, dy and dx share one dtype
+ * (MUONH_F32 or MUONH_BF16) and need element alignment only; the vectors are
+ * fp32.  y may be x, and dx may be x or dy (same address and pitch); an output or
+ * workspace that overlaps anything else is refused.                          */
 #define MUONH_NORM_LAYER 0
 #define MUONH_NORM_RMS   1
 

@@ -119,3 +119,17 @@ def test_more_rows_than_one_trip_of_a_forward_launch(rows, cols, dtype, kind):
         assert torch.equal(y[r0:r1], alone[0]) and torch.equal(rstd[r0:r1], alone[2])
         assert mean is None or torch.equal(mean[r0:r1], alone[1])
     assert bool(torch.isfinite(y).all()) and bool(torch.isfinite(rstd).all())
+
+
+@pytest.mark.parametrize("cols", [700, 20000])
+def test_squares_beyond_fp32(cols):
+    """A row whose sum of squares is beyond fp32 gets rstd 0 and y = 0, and its
+    neighbours are as without it."""
+    announce(f"norm squares beyond fp32 {cols}")
+    x, _, w, _ = (t.cuda() for t in _inputs(3, cols, torch.float32))
+    want = pm.norm_forward(x, w, kind="rms")
+    x[1] = 1e20
+    y, _, rstd = pm.norm_forward(x, w, kind="rms")
+    assert rstd[1] == 0 and not y[1].any()
+    for i in (0, 2):
+        assert torch.equal(y[i], want[0][i]) and rstd[i] == want[2][i]
