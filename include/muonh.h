@@ -455,6 +455,65 @@ typedef struct muonh_norm_grad_args {
 int muonh_norm_backward_workspace(int64_t rows, int64_t cols, size_t* bytes);
 int muonh_norm_backward(const muonh_norm_grad_args* args, void* stream);
 
+/* ---- causal attention over packed sequences ---------------------------------
+ * The attention between a layer's qkv and output products, and its gradients.
+ * Sequence b of `sequences` is rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 of the
+ * tokens (an empty one is allowed); row i of it sees rows j <= i of the same
+ * sequence.  Head h of q reads head h / (heads / kv_heads) of k and v:
+ *   S_ij = scale q_i.k_j,  lse_i = log sum_j exp S_ij,  P_ij = exp(S_ij - lse_i)
+ *   out_i = sum_j P_ij v_j
+ *   dS_ij = scale P_ij (dout_i.v_j - dout_i.out_i)
+ *   dq_i = sum_j dS_ij k_j,  dk_j = sum dS_ij q_i,  dv_j = sum P_ij dout_i
+ * dk and dv over the rows i >= j and the heads that read them.
+ *
+ * q, out, dout, dq are bf16 [tokens x heads x dim], k, v, dk, dv [tokens x kv_heads x
+ * dim], with contiguous heads and ld elements between tokens (slices of one fused
+ * matrix are allowed), 16-byte aligned; ld a multiple of 8 below 2^23.  Scores,
+ * softmax statistics and all sums are fp32; P and dS are rounded to bf16 where they
+ * are multiplied, results once.  Sums run in a fixed order.
+ *
+ * Rows that no sequence holds are neither read nor written.  The device reads
+ * cu_seqlens: ends are taken into [0, tokens] and a sequence that would end before
+ * it starts is empty, but sequences that overlap give undefined results.  An
+ * infinity or a NaN in a token of k or v reaches out and lse of later rows of its
+ * sequence (and its own), of no earlier one; one in any operand of the backward pass may reach
+ * every gradient of its sequence.  Other sequences' results do not change.
+ * An output or workspace that overlaps an input or another output is refused, unless
+ * they lie side by side in rows of one pitch.                                */
+typedef struct muonh_attention_args {
+  const void*    q;
+  const void*    k;
+  const void*    v;
+  void*          out;         /* read by muonh_attention_backward                 */
+  float*         lse;         /* [heads x tokens]; read by the backward pass      */
+  const int32_t* cu_seqlens;  /* [sequences + 1], device, not decreasing          */
+  int64_t        tokens;      /* 0 .. 2^30                                        */
+  int64_t        sequences;   /* >= 0                                             */
+  int64_t        ld_q, ld_k, ld_v, ld_out;
+  int32_t        heads;       /* a multiple of kv_heads                           */
+  int32_t        kv_heads;    /* >= 1                                             */
+  int32_t        dim;         /* 8, 16, .. 128                                    */
+  float          scale;       /* > 0, usually dim^-1/2                            */
+} muonh_attention_args;
+
+typedef struct muonh_attention_grad_args {
+  muonh_attention_args a;     /* the forward pass's arguments and results         */
+  const void*    dout;
+  void*          dq;
+  void*          dk;
+  void*          dv;
+  int64_t        ld_dout, ld_dq, ld_dk, ld_dv;
+  void*          workspace;   /* muonh_attention_backward_workspace bytes, device,
+                                 256-byte aligned; calls that may overlap in time
+                                 need one each                                    */
+  size_t         workspace_bytes;
+} muonh_attention_grad_args;
+
+/* Errors: MUONH_EINVAL, MUONH_ENOMEM (workspace too small), MUONH_EHIP. */
+int muonh_attention_forward(const muonh_attention_args* args, void* stream);
+int muonh_attention_backward_workspace(const muonh_attention_args* args, size_t* bytes);
+int muonh_attention_backward(const muonh_attention_grad_args* args, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -28,6 +28,8 @@ from .muonh import (  # noqa: F401
 )
 from .operators import (  # noqa: F401
     Fp8Matrix,
+    attention_backward,
+    attention_forward,
     fp8_matmul,
     fp8_quantize,
     norm_backward,

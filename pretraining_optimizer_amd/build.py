@@ -19,7 +19,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmuonh.so")
 SOURCES = ("muonh.cpp", "adamw.cpp", "operators.cpp", "step_fp8.cpp", "gemm.hip", "elementwise.hip",
-           "noalloc.hip", "block_fp8.hip", "norm.hip")
+           "noalloc.hip", "block_fp8.hip", "norm.hip", "attention.cpp", "attention.hip")
 ARCH = "gfx950"
 
 

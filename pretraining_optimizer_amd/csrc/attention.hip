@@ -1,0 +1,581 @@
+// Causal attention over packed sequences with grouped heads, and its gradients
+// (gfx950, bf16 operands, fp32 scores, softmax statistics and sums).
+//
+// For row i of a sequence and a head, with S_ij = c q_i.k_j over its rows j <= i:
+//   lse_i = log sum_j exp S_ij,  P_ij = exp(S_ij - lse_i),  o_i = sum_j P_ij v_j
+//   dP_ij = do_i.v_j,  delta_i = do_i.o_i,  dS_ij = c P_ij (dP_ij - delta_i)
+//   dq_i = sum_j dS_ij k_j,  dk_j = sum_i dS_ij q_i,  dv_j = sum_i P_ij do_i
+// dk and dv are sums over the heads of a group, too.
+//
+// All kernels work in 32 x 32 blocks of scores on v_mfma_f32_32x32x16_bf16, whose
+// result has one column per lane (l % 32) and rows 8 (r / 4) + 4 (l / 32) + r % 4 in
+// its 16 registers.  The scores are computed so that the axis which the next product
+// contracts lies in the registers: rounded to bf16 in pairs, registers 8 s .. 8 s + 7
+// are then the B operand of step s of that product as they are, if its A operand
+// takes its 16 rows in the same order.  A comes out of LDS through the transposing
+// read (ds_read_b64_tr_b16: 4 consecutive rows of one column per lane), two reads
+// for rows 16 s + 4 (l / 32) .. + 3 and 8 further.  So neither scores nor
+// probabilities pass through LDS.
+//
+// Rounding to bf16: P and dS where they become matrix operands (2^-9 of a term, random),
+// and the results, once.
+//
+// Tiles of 64 rows go straight from memory to LDS, the next while one is used, a
+// barrier per tile.  Rows behind a sequence's end and columns behind the head's width
+// are out of the buffer descriptor's range and arrive as zeros, so nothing of another
+// sequence or head is read.
+
+#include "attention.h"
+
+#include <type_traits>
+
+#include "device_util.h"
+
+namespace muonh {
+namespace {
+
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+typedef short i16x4_t __attribute__((ext_vector_type(4)));
+
+#define MUONH_LDS __attribute__((address_space(3)))
+
+constexpr int kThreads = kAttentionThreads;
+constexpr int kBlock = kAttentionRows;   // rows of a workgroup: 32 per wavefront
+constexpr int kTile = 64;                // rows of a tile in LDS
+constexpr int kBufferConfig = 0x00020000;
+constexpr int kBehind = (int)0x80000000;  // an offset behind every descriptor's range
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Row r's 16-byte chunk c sits at c ^ swizzle(r).  A row is 256 (128) bytes; 16 (8)
+// rows of one chunk, as an operand read has them, and 8 rows of 4 chunks, as a
+// transposing read has them, then lie in different banks.
+template <int DP>
+__device__ __forceinline__ int swizzle(int r) {
+  return DP == 128 ? ((r & 3) << 2) | ((r >> 2) & 3) : (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
+}
+
+__device__ __forceinline__ f32x16_t mfma(u32x4_t a, u32x4_t b, f32x16_t c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c,
+                                                 0, 0, 0);
+}
+
+__device__ __forceinline__ f32x16_t splat(float v) {
+  f32x16_t r;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) r[i] = v;
+  return r;
+}
+
+// Barrier without a memory fence, and the wait for this wavefront's loads.
+__device__ __forceinline__ void arrive() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((0 << 0) | (7 << 4) | (0 << 8));   // vmcnt(0) lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// Score register r's row within its block of 32.
+__device__ __forceinline__ constexpr int block_row(int r) { return 8 * (r / 4) + r % 4; }
+
+// Registers 8 s .. 8 s + 7 of a block as a B operand.
+__device__ __forceinline__ u32x4_t operand(const f32x16_t& v, int s) {
+  u32x4_t r;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) r[w] = pack_bf16x2(v[8 * s + 2 * w], v[8 * s + 2 * w + 1]);
+  return r;
+}
+
+// The larger (the sum) of lane l's and lane l ^ 32's values.
+__device__ __forceinline__ float pair_max(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float pair_sum(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// The rows of a tensor [tokens, heads, dim] that a workgroup reads, from one row on.
+struct Rows {
+  const uint16_t* base;   // of the sequence's first row, at the head
+  int64_t ld;
+  int len, dim;
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t at(int row, int rows) const {
+    const int n = min(rows, len - row);
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base + row * ld), (short)0,
+                                             n > 0 ? (int)(((n - 1) * ld + dim) * 2) : 0, kBufferConfig);
+  }
+};
+
+// A tile's loads: instruction i of wavefront w fills 1024 bytes of LDS.
+template <int DP>
+struct TileLoad {
+  static constexpr int kRow = DP * 2, kChunks = DP / 8, kStep = 4096 / kRow;   // rows per round of the wavefronts
+  int voff, step;
+  __device__ __forceinline__ TileLoad(const Rows& t, int wave, int lane) {
+    const int row = wave * (kStep / 4) + lane / kChunks, chunk = (lane % kChunks) ^ swizzle<DP>(row);
+    voff = chunk * 8 < t.dim ? (int)(row * t.ld * 2) + chunk * 16 : kBehind;
+    step = (int)(kStep * t.ld * 2);
+  }
+  __device__ __forceinline__ void operator()(const Rows& t, int row, uint8_t* slot, int wave) const {
+    const __amdgpu_buffer_rsrc_t r = t.at(row, kTile);
+#pragma unroll
+    for (int i = 0; i < kTile / kStep; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (MUONH_LDS void*)((MUONH_LDS uint8_t*)slot + (i * 4 + wave) * 1024),
+                                               16, voff, i * step, 0, 0);
+  }
+};
+
+// Operands out of a tile in LDS.
+template <int DP>
+struct TileRead {
+  static constexpr int kRow = DP * 2;
+  int row, tr;    // byte offsets of the lane's row and of its transposing reads
+  int chunk, trc; // swizzled chunk of step 0, and of the first reads
+  __device__ __forceinline__ explicit TileRead(int lane) {
+    row = (lane & 31) * kRow;
+    chunk = (lane >> 5) ^ swizzle<DP>(lane & 15);
+    const int r = 4 * (lane >> 5) + ((lane & 15) >> 2);
+    tr = r * kRow + (lane & 1) * 8;
+    trc = (2 * ((lane >> 4) & 1) + ((lane >> 1) & 1)) ^ swizzle<DP>(r);
+  }
+  // Rows of block `sub`, columns 16 step + 8 (l / 32) .. + 7.
+  __device__ __forceinline__ u32x4_t rows(const uint8_t* tile, int sub, int step) const {
+    return *reinterpret_cast<const u32x4_t*>(tile + sub * 32 * kRow + row + ((chunk ^ (2 * step)) << 4));
+  }
+  // Column 32 dt + l % 32 of block `sub`, rows 16 s + 4 (l / 32) .. + 3 and 8 further.
+  __device__ __forceinline__ u32x4_t columns(uint8_t* tile, int sub, int s, int dt) const {
+    MUONH_LDS uint8_t* t = (MUONH_LDS uint8_t*)tile + (sub * 32 + 16 * s) * kRow + tr;
+    const u32x2_t lo = __builtin_bit_cast(
+        u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((MUONH_LDS i16x4_t*)(t + ((trc ^ (4 * dt)) << 4))));
+    // 8 rows further the swizzle differs in one bit
+    const u32x2_t hi = __builtin_bit_cast(
+        u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                     (MUONH_LDS i16x4_t*)(t + 8 * kRow + ((trc ^ (4 * dt) ^ 2) << 4))));
+    return u32x4_t{lo[0], lo[1], hi[0], hi[1]};
+  }
+};
+
+// The wavefront's 32 rows from `row` on as an operand held in registers: lane l has
+// row l % 32, columns 16 s + 8 (l / 32) .. + 7 of step s.
+template <int DP>
+__device__ __forceinline__ void load_operand(u32x4_t (&f)[DP / 16], const Rows& t, int row, int lane) {
+  const __amdgpu_buffer_rsrc_t r = t.at(row, 32);
+  const int base = (int)((lane & 31) * t.ld * 2);
+#pragma unroll
+  for (int s = 0; s < DP / 16; ++s) {
+    const int chunk = 2 * s + (lane >> 5);
+    f[s] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                                           r, chunk * 8 < t.dim ? base + chunk * 16 : kBehind, 0, 0));
+  }
+}
+
+// The sequence and the place in it of a workgroup's rows.  Sequence b's blocks are
+// numbered from first_block(b) = cu[b] / 128 + b on, which leaves room for the last,
+// cut one; a number between two sequences has no rows.  Ends are taken into
+// [0, tokens], so no cu_seqlens reads or writes outside the tensors.
+struct Place {
+  int64_t start;   // the sequence's first row
+  int len, row;    // its rows, and the workgroup's first
+};
+__device__ __forceinline__ int sequence_end(const AttentionArgs& p, int b) { return min(max(p.cu[b], 0), p.tokens); }
+__device__ __forceinline__ Place find_place(const AttentionArgs& p, int block) {
+  int lo = 0, hi = p.sequences - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (sequence_end(p, mid) / kBlock + mid <= block) lo = mid;
+    else hi = mid - 1;
+  }
+  const int s = sequence_end(p, lo), e = max(sequence_end(p, lo + 1), s);
+  const int64_t row = ((int64_t)block - s / kBlock - lo) * kBlock;
+  return Place{s, e - s, row < 0 || row >= e - s ? -1 : (int)row};
+}
+
+// The work of workgroup i.  Workgroups i, i + 8, .. run on one XCD: it gets a run of
+// consecutive items, so that one key head's rows stay in its L2.
+__device__ __forceinline__ int64_t item_of(int64_t i, int64_t n) {
+  const int64_t xcd = i & 7, per = n >> 3, more = n & 7;
+  return xcd * per + min(xcd, more) + (i >> 3);
+}
+
+// Where the lane's results lie: column l % 32 is a row of the tensor, registers 4 j ..
+// of block dt are 4 consecutive columns of it.
+template <int DP>
+__device__ __forceinline__ void store_rows(uint16_t* base, int64_t ld, int dim, const f32x16_t (&acc)[DP / 32],
+                                           float factor, int lane) {
+  uint16_t* out = base + (lane & 31) * ld + 4 * (lane >> 5);
+#pragma unroll
+  for (int dt = 0; dt < DP / 32; ++dt)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (32 * dt + 8 * j < dim) {
+        u32x2_t w;
+        w[0] = pack_bf16x2(acc[dt][4 * j] * factor, acc[dt][4 * j + 1] * factor);
+        w[1] = pack_bf16x2(acc[dt][4 * j + 2] * factor, acc[dt][4 * j + 3] * factor);
+        st_global<u32x2_t>(out + 32 * dt + 8 * j, w);
+      }
+}
+
+// Whether any of the wavefront's values is an infinity or a NaN.
+__device__ __forceinline__ bool has_special(u32x4_t v) {
+  bool any = false;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) any |= (v[w] & 0x7f80u) == 0x7f80u || (v[w] & 0x7f800000u) == 0x7f800000u;
+  return any;
+}
+
+// Forward.  A wavefront holds 32 rows of q and their output transposed (a row per
+// lane), and passes over the keys once with a running maximum and sum.  The output is
+// rescaled only where a maximum has grown by more than 2^8 since the last time: until
+// then the probabilities are up to 2^8 too large, which neither bf16 nor fp32 minds.
+template <int DP>
+__global__ __launch_bounds__(kThreads, 2) void attention_forward_kernel(AttentionArgs p) {
+  constexpr int kBytes = kTile * DP * 2;
+  __shared__ __attribute__((aligned(1024))) uint8_t slot0[2 * kBytes], slot1[2 * kBytes];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int group = p.heads / p.kv_heads;
+  const int64_t item = item_of(blockIdx.x, gridDim.x), per = (int64_t)p.blocks * group;
+  const int kv = (int)(item / per), head = kv * group + (int)(item % per % group);
+  const Place at = find_place(p, p.blocks - 1 - (int)(item % per / group));   // long rows first
+  if (at.row < 0) return;
+
+  const Rows q{p.q + at.start * p.ldq + head * p.dim, p.ldq, at.len, p.dim};
+  const Rows k{p.k + at.start * p.ldk + kv * p.dim, p.ldk, at.len, p.dim};
+  const Rows v{p.v + at.start * p.ldv + kv * p.dim, p.ldv, at.len, p.dim};
+  const int row = at.row + 32 * wave;   // the wavefront's first
+  const int tiles = (min(at.len, at.row + kBlock) + kTile - 1) / kTile;
+  const TileLoad<DP> load_k(k, wave, lane), load_v(v, wave, lane);
+  const TileRead<DP> read(lane);
+  load_k(k, 0, slot0, wave);
+  load_v(v, 0, slot0 + kBytes, wave);
+  u32x4_t fq[DP / 16];
+  load_operand<DP>(fq, q, row, lane);
+
+  f32x16_t acc[DP / 32];
+#pragma unroll
+  for (int dt = 0; dt < DP / 32; ++dt) acc[dt] = splat(0.0f);
+  float top = -INFINITY, sum = 0.0f;   // both times c log2 e; the sum is of this lane's keys
+  const float c = p.scale * kLog2e;
+
+  // N blocks of 32 keys; DIAG: the last is the rows' own.
+  auto step = [&](uint8_t* tile, auto n, auto diag) {
+    constexpr int N = decltype(n)::value;
+    constexpr bool DIAG = decltype(diag)::value;
+    f32x16_t s[N];
+#pragma unroll
+    for (int b = 0; b < N; ++b) {
+      s[b] = splat(0.0f);
+#pragma unroll
+      for (int d = 0; d < DP / 16; ++d) s[b] = mfma(read.rows(tile, b, d), fq[d], s[b]);
+    }
+    if constexpr (DIAG) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        if (block_row(r) + 4 * (lane >> 5) > (lane & 31)) s[N - 1][r] = -INFINITY;
+    }
+    float m = s[0][0];
+#pragma unroll
+    for (int b = 0; b < N; ++b)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) m = fmaxf(m, s[b][r]);
+    m = pair_max(m) * c;
+    if (__any(m > top + 8.0f)) {
+      const float grown = fmaxf(top, m), f = __builtin_amdgcn_exp2f(top - grown);
+      top = grown;
+      sum *= f;
+#pragma unroll
+      for (int dt = 0; dt < DP / 32; ++dt)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[dt][r] *= f;
+    }
+#pragma unroll
+    for (int b = 0; b < N; ++b)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        s[b][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][r], c, -top));
+        sum += s[b][r];
+      }
+#pragma unroll
+    for (int b = 0; b < N; ++b)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const u32x4_t pr = operand(s[b], h);
+        u32x4_t fv[DP / 32];
+        bool special = false;
+#pragma unroll
+        for (int dt = 0; dt < DP / 32; ++dt) {
+          fv[dt] = read.columns(tile + kBytes, b, h, dt);
+          if (DIAG && b == N - 1) special |= has_special(fv[dt]);
+        }
+        if (DIAG && b == N - 1 && __any(special)) {
+          // A later row's infinity or NaN times its probability 0 would be a NaN: one
+          // key at a time, and only the rows that see it keep the result.
+#pragma unroll 1
+          for (int e = 0; e < 16; ++e) {
+            // key 16 h + e: half (e / 4) % 2 of the lanes, word and half word
+            const int word = (e >> 3) * 2 + ((e >> 1) & 1);
+            const uint32_t keep = ((e >> 2) & 1) != (lane >> 5) ? 0u : (e & 1) ? 0xffff0000u : 0xffffu;
+            u32x4_t mask;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) mask[w] = w == word ? keep : 0u;
+#pragma unroll
+            for (int dt = 0; dt < DP / 32; ++dt) {
+              const f32x16_t more = mfma(fv[dt] & mask, pr & mask, acc[dt]);
+#pragma unroll
+              for (int r = 0; r < 16; ++r) acc[dt][r] = (lane & 31) >= 16 * h + e ? more[r] : acc[dt][r];
+            }
+          }
+        } else {
+#pragma unroll
+          for (int dt = 0; dt < DP / 32; ++dt) acc[dt] = mfma(fv[dt], pr, acc[dt]);
+        }
+      }
+  };
+  auto use = [&](uint8_t* tile, int j) {
+    const int first = j * kTile;
+    if (row >= at.len || first > row) return;
+    if (first == row) step(tile, std::integral_constant<int, 1>{}, std::true_type{});
+    else if (first + 32 == row) step(tile, std::integral_constant<int, 2>{}, std::true_type{});
+    else step(tile, std::integral_constant<int, 2>{}, std::false_type{});
+  };
+  auto trip = [&](uint8_t* tile, uint8_t* next, int j) {
+    arrive();   // the tile is there, and every wavefront has read the other
+    if (j + 1 < tiles) {
+      load_k(k, (j + 1) * kTile, next, wave);
+      load_v(v, (j + 1) * kTile, next + kBytes, wave);
+    }
+    use(tile, j);
+  };
+  for (int j = 0; j < tiles; j += 2) {
+    trip(slot0, slot1, j);
+    if (j + 1 < tiles) trip(slot1, slot0, j + 1);
+  }
+
+  sum = pair_sum(sum);
+  if (row + (lane & 31) >= at.len) return;
+  const int64_t t = at.start + row;
+  store_rows<DP>(p.out + t * p.ldo + head * p.dim, p.ldo, p.dim, acc, 1.0f / sum, lane);
+  if (lane < 32) p.lse[head * (int64_t)p.tokens + t + lane] = (top + __builtin_amdgcn_logf(sum)) * (1.0f / kLog2e);
+}
+
+// Gradient of q, row by row as in the forward pass: S and dP from k and v, dq from dS and k.
+// It also leaves what the other kernel needs of each row: -lse log2 e and -delta.
+template <int DP>
+__global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttentionGradArgs g) {
+  const AttentionArgs& p = g.a;
+  constexpr int kBytes = kTile * DP * 2;
+  __shared__ __attribute__((aligned(1024))) uint8_t slot0[2 * kBytes], slot1[2 * kBytes];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int group = p.heads / p.kv_heads;
+  const int64_t item = item_of(blockIdx.x, gridDim.x), per = (int64_t)p.blocks * group;
+  const int kv = (int)(item / per), head = kv * group + (int)(item % per % group);
+  const Place at = find_place(p, p.blocks - 1 - (int)(item % per / group));
+  if (at.row < 0) return;
+
+  const Rows q{p.q + at.start * p.ldq + head * p.dim, p.ldq, at.len, p.dim};
+  const Rows k{p.k + at.start * p.ldk + kv * p.dim, p.ldk, at.len, p.dim};
+  const Rows v{p.v + at.start * p.ldv + kv * p.dim, p.ldv, at.len, p.dim};
+  const Rows o{p.out + at.start * p.ldo + head * p.dim, p.ldo, at.len, p.dim};
+  const Rows d{g.dout + at.start * g.lddo + head * p.dim, g.lddo, at.len, p.dim};
+  const int row = at.row + 32 * wave;
+  const int tiles = (min(at.len, at.row + kBlock) + kTile - 1) / kTile;
+  const TileLoad<DP> load_k(k, wave, lane), load_v(v, wave, lane);
+  const TileRead<DP> read(lane);
+  load_k(k, 0, slot0, wave);
+  load_v(v, 0, slot0 + kBytes, wave);
+  u32x4_t fq[DP / 16], fd[DP / 16];
+  load_operand<DP>(fq, q, row, lane);
+  load_operand<DP>(fd, d, row, lane);
+
+  const int64_t t = head * (int64_t)p.tokens + at.start + row + (lane & 31);
+  const bool live = row + (lane & 31) < at.len;
+  float delta = 0.0f, lse = 0.0f;
+  {
+    u32x4_t fo[DP / 16];
+    load_operand<DP>(fo, o, row, lane);
+    if (live) lse = -p.lse[t] * kLog2e;
+#pragma unroll
+    for (int s = 0; s < DP / 16; ++s)
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        delta = __builtin_fmaf(__uint_as_float(fo[s][w] << 16), __uint_as_float(fd[s][w] << 16), delta);
+        delta = __builtin_fmaf(__uint_as_float(fo[s][w] & 0xffff0000u), __uint_as_float(fd[s][w] & 0xffff0000u), delta);
+      }
+    delta = -pair_sum(delta);
+    if (live && lane < 32) {
+      g.row_lse[t] = lse;
+      g.row_delta[t] = delta;
+    }
+  }
+
+  f32x16_t acc[DP / 32];
+#pragma unroll
+  for (int dt = 0; dt < DP / 32; ++dt) acc[dt] = splat(0.0f);
+  const float c = p.scale * kLog2e;
+
+  auto block = [&](uint8_t* tile, int b, auto diag) {
+    f32x16_t s = splat(0.0f), ds = splat(delta);
+#pragma unroll
+    for (int e = 0; e < DP / 16; ++e) s = mfma(read.rows(tile, b, e), fq[e], s);
+#pragma unroll
+    for (int e = 0; e < DP / 16; ++e) ds = mfma(read.rows(tile + kBytes, b, e), fd[e], ds);
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      ds[r] *= __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], c, lse));
+      if (decltype(diag)::value && block_row(r) + 4 * (lane >> 5) > (lane & 31)) ds[r] = 0.0f;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const u32x4_t f = operand(ds, h);
+#pragma unroll
+      for (int dt = 0; dt < DP / 32; ++dt) acc[dt] = mfma(read.columns(tile, b, h, dt), f, acc[dt]);
+    }
+  };
+  auto trip = [&](uint8_t* tile, uint8_t* next, int j) {
+    arrive();
+    if (j + 1 < tiles) {
+      load_k(k, (j + 1) * kTile, next, wave);
+      load_v(v, (j + 1) * kTile, next + kBytes, wave);
+    }
+    if (row >= at.len) return;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int first = j * kTile + 32 * b;
+      if (first < row) block(tile, b, std::false_type{});
+      else if (first == row) block(tile, b, std::true_type{});
+    }
+  };
+  for (int j = 0; j < tiles; j += 2) {
+    trip(slot0, slot1, j);
+    if (j + 1 < tiles) trip(slot1, slot0, j + 1);
+  }
+  if (!live) return;
+  store_rows<DP>(g.dq + (at.start + row) * g.lddq + head * p.dim, g.lddq, p.dim, acc, p.scale, lane);
+}
+
+// Gradients of k and v: a wavefront holds 32 rows of both and passes over the rows of
+// q and dout that see them, head by head of the group.
+template <int DP>
+__global__ __launch_bounds__(kThreads, 2) void attention_dkv_kernel(AttentionGradArgs g) {
+  const AttentionArgs& p = g.a;
+  constexpr int kBytes = kTile * DP * 2;
+  __shared__ __attribute__((aligned(1024))) uint8_t slot0[2 * kBytes], slot1[2 * kBytes];
+  __shared__ __attribute__((aligned(16))) float rows0[2][kTile], rows1[2][kTile];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int group = p.heads / p.kv_heads;
+  const int64_t item = item_of(blockIdx.x, gridDim.x);
+  const int kv = (int)(item / p.blocks);
+  const Place at = find_place(p, (int)(item % p.blocks));
+  if (at.row < 0) return;
+
+  const Rows k{p.k + at.start * p.ldk + kv * p.dim, p.ldk, at.len, p.dim};
+  const Rows v{p.v + at.start * p.ldv + kv * p.dim, p.ldv, at.len, p.dim};
+  Rows q{p.q + at.start * p.ldq + kv * group * p.dim, p.ldq, at.len, p.dim};
+  Rows d{g.dout + at.start * g.lddo + kv * group * p.dim, g.lddo, at.len, p.dim};
+  const int row = at.row + 32 * wave;
+  const TileLoad<DP> load_q(q, wave, lane), load_d(d, wave, lane);
+  const TileRead<DP> read(lane);
+  const int first_tile = at.row / kTile, end_tile = (at.len + kTile - 1) / kTile;
+  // Rows behind the end arrive as zeros: P = exp 0, but dout, delta and q are 0.
+  int lh = 0, lt = first_tile;   // the next tile to load
+  auto load = [&](uint8_t* tile, float (&rows)[2][kTile]) {
+    load_q(q, lt * kTile, tile, wave);
+    load_d(d, lt * kTile, tile + kBytes, wave);
+    if (wave < 2) {
+      const float* src = (wave ? g.row_delta : g.row_lse) + (kv * group + lh) * (int64_t)p.tokens + at.start + lt * kTile;
+      const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+          const_cast<float*>(src), (short)0, min(kTile, at.len - lt * kTile) * 4, kBufferConfig);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (MUONH_LDS void*)((MUONH_LDS float*)rows[wave]), 4, lane * 4, 0, 0, 0);
+    }
+    if (++lt == end_tile) {
+      lt = first_tile;
+      ++lh;
+      q.base += p.dim;
+      d.base += p.dim;
+    }
+  };
+  load(slot0, rows0);
+  u32x4_t fk[DP / 16], fv[DP / 16];
+  load_operand<DP>(fk, k, row, lane);
+  load_operand<DP>(fv, v, row, lane);
+  f32x16_t dk[DP / 32], dv[DP / 32];
+#pragma unroll
+  for (int dt = 0; dt < DP / 32; ++dt) dk[dt] = dv[dt] = splat(0.0f);
+  const float c = p.scale * kLog2e;
+
+  auto block = [&](uint8_t* tile, const float (&rows)[2][kTile], int b, auto diag) {
+    f32x16_t s = splat(0.0f), ds;
+    f32x4_t lse[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      lse[j] = *reinterpret_cast<const f32x4_t*>(&rows[0][32 * b + 8 * j + 4 * (lane >> 5)]);
+      const f32x4_t del = *reinterpret_cast<const f32x4_t*>(&rows[1][32 * b + 8 * j + 4 * (lane >> 5)]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) ds[4 * j + e] = del[e];
+    }
+#pragma unroll
+    for (int e = 0; e < DP / 16; ++e) s = mfma(read.rows(tile, b, e), fk[e], s);
+#pragma unroll
+    for (int e = 0; e < DP / 16; ++e) ds = mfma(read.rows(tile + kBytes, b, e), fv[e], ds);
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      s[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], c, lse[r / 4][r % 4]));
+      ds[r] *= s[r];
+      if (decltype(diag)::value && block_row(r) + 4 * (lane >> 5) < (lane & 31)) s[r] = ds[r] = 0.0f;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const u32x4_t fp = operand(s, h), fs = operand(ds, h);
+#pragma unroll
+      for (int dt = 0; dt < DP / 32; ++dt) dv[dt] = mfma(read.columns(tile + kBytes, b, h, dt), fp, dv[dt]);
+#pragma unroll
+      for (int dt = 0; dt < DP / 32; ++dt) dk[dt] = mfma(read.columns(tile, b, h, dt), fs, dk[dt]);
+    }
+  };
+  const int per_head = end_tile - first_tile, trips = per_head * group;
+  int tile_row = first_tile * kTile;
+  auto trip = [&](uint8_t* tile, const float (&rows)[2][kTile], uint8_t* next, float (&next_rows)[2][kTile], int j) {
+    arrive();
+    if (j + 1 < trips) load(next, next_rows);
+    if (row < at.len) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int first = tile_row + 32 * b;
+        if (first > row) block(tile, rows, b, std::false_type{});
+        else if (first == row) block(tile, rows, b, std::true_type{});
+      }
+    }
+    tile_row = tile_row + kTile < at.len ? tile_row + kTile : first_tile * kTile;
+  };
+  for (int j = 0; j < trips; j += 2) {
+    trip(slot0, rows0, slot1, rows1, j);
+    if (j + 1 < trips) trip(slot1, rows1, slot0, rows0, j + 1);
+  }
+  if (row + (lane & 31) >= at.len) return;
+  const int64_t t = at.start + row;
+  store_rows<DP>(g.dk + t * g.lddk + kv * p.dim, g.lddk, p.dim, dk, p.scale, lane);
+  store_rows<DP>(g.dv + t * g.lddv + kv * p.dim, g.lddv, p.dim, dv, 1.0f, lane);
+}
+
+}  // namespace
+
+hipError_t launch_attention_forward(const AttentionArgs& a, hipStream_t st) {
+  const dim3 grid((unsigned)((int64_t)a.blocks * a.heads));
+  if (a.dim <= 64) hipLaunchKernelGGL(attention_forward_kernel<64>, grid, dim3(kThreads), 0, st, a);
+  else hipLaunchKernelGGL(attention_forward_kernel<128>, grid, dim3(kThreads), 0, st, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_attention_backward(const AttentionGradArgs& g, hipStream_t st) {
+  const dim3 rows((unsigned)((int64_t)g.a.blocks * g.a.heads)), keys((unsigned)((int64_t)g.a.blocks * g.a.kv_heads));
+  if (g.a.dim <= 64) hipLaunchKernelGGL(attention_dq_kernel<64>, rows, dim3(kThreads), 0, st, g);
+  else hipLaunchKernelGGL(attention_dq_kernel<128>, rows, dim3(kThreads), 0, st, g);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  if (g.a.dim <= 64) hipLaunchKernelGGL(attention_dkv_kernel<64>, keys, dim3(kThreads), 0, st, g);
+  else hipLaunchKernelGGL(attention_dkv_kernel<128>, keys, dim3(kThreads), 0, st, g);
+  return hipGetLastError();
+}
+
+}  // namespace muonh

@@ -109,6 +109,22 @@ class muonh_norm_grad_args(ctypes.Structure):
                 ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
 
 
+class muonh_attention_args(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("cu_seqlens", ctypes.c_void_p),
+                ("tokens", ctypes.c_int64), ("sequences", ctypes.c_int64), ("ld_q", ctypes.c_int64),
+                ("ld_k", ctypes.c_int64), ("ld_v", ctypes.c_int64), ("ld_out", ctypes.c_int64),
+                ("heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
+class muonh_attention_grad_args(ctypes.Structure):
+    _fields_ = [("a", muonh_attention_args), ("dout", ctypes.c_void_p), ("dq", ctypes.c_void_p),
+                ("dk", ctypes.c_void_p), ("dv", ctypes.c_void_p), ("ld_dout", ctypes.c_int64),
+                ("ld_dq", ctypes.c_int64), ("ld_dk", ctypes.c_int64), ("ld_dv", ctypes.c_int64),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
 _libs = {}
 
 # (name, restype, argtypes)
@@ -164,6 +180,10 @@ _SIGNATURES = [
     ("muonh_norm_backward_workspace", ctypes.c_int, [ctypes.c_int64, ctypes.c_int64,
                                                      ctypes.POINTER(ctypes.c_size_t)]),
     ("muonh_norm_backward", ctypes.c_int, [ctypes.POINTER(muonh_norm_grad_args), ctypes.c_void_p]),
+    ("muonh_attention_forward", ctypes.c_int, [ctypes.POINTER(muonh_attention_args), ctypes.c_void_p]),
+    ("muonh_attention_backward_workspace", ctypes.c_int, [ctypes.POINTER(muonh_attention_args),
+                                                          ctypes.POINTER(ctypes.c_size_t)]),
+    ("muonh_attention_backward", ctypes.c_int, [ctypes.POINTER(muonh_attention_grad_args), ctypes.c_void_p]),
 ]
 
 

@@ -1,5 +1,5 @@
-"""ctypes binding of the block-scaled FP8 operators and the norms (argument
-marshalling only; the work runs in the library's HIP kernels).
+"""ctypes binding of the block-scaled FP8 operators, the norms and the attention
+(argument marshalling only; the work runs in the library's HIP kernels).
 
 One linear layer y = x W^T, its gradients and the step of its weight:
 
@@ -19,8 +19,8 @@ from __future__ import annotations
 import ctypes
 from typing import Optional
 
-from .muonh import (MUONH_BF16, MUONH_F32, _check, _record, load_library, muonh_fp8_matrix, muonh_norm_args,
-                    muonh_norm_grad_args)
+from .muonh import (MUONH_BF16, MUONH_F32, _check, _record, load_library, muonh_attention_args,
+                    muonh_attention_grad_args, muonh_fp8_matrix, muonh_norm_args, muonh_norm_grad_args)
 
 # The smallest calls are bound by this module: a launch takes about 3.5 us,
 # a tensor 1.5 us, torch.cuda.current_stream() 2.8 us.  So the library and
@@ -353,3 +353,98 @@ def norm_backward(dy, x, weight, mean, rstd, kind: str = "rms", bias: bool = Fal
     if rc:
         _check(rc, "muonh_norm_backward")
     return dx, dweight, dbias
+
+
+def _heads(t, tokens: int, heads: int, dim: int, what: str) -> int:
+    """The token pitch of a bfloat16 tensor [tokens, heads, dim] with contiguous heads."""
+    if t.dtype is not _torch.bfloat16:
+        raise TypeError(f"{what}: dtype must be bfloat16, got {t.dtype}")
+    if t.shape != (tokens, heads, dim):
+        raise ValueError(f"{what}: shape {(tokens, heads, dim)} is required")
+    s0, s1, s2 = t.stride()
+    if (dim > 1 and s2 != 1) or (heads > 1 and s1 != dim):
+        raise ValueError(f"{what}: the heads of a token must be contiguous")
+    return heads * dim if tokens <= 1 else s0
+
+
+def _attention(q, k, v, cu_seqlens, scale, out, lse, stream):
+    """muonh_attention_args, with new results where none are given: (args, out, lse, device)."""
+    if _torch is None:
+        _setup()
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q and k: tensors [tokens, heads, dim] are required")
+    tokens, heads, dim = q.shape
+    kv_heads = k.shape[1]
+    ld_q, ld_k = _heads(q, tokens, heads, dim, "q"), _heads(k, tokens, kv_heads, dim, "k")
+    ld_v = _heads(v, tokens, kv_heads, dim, "v")
+    if cu_seqlens.dtype is not _torch.int32 or cu_seqlens.dim() != 1 or not cu_seqlens.is_contiguous() or not len(cu_seqlens):
+        raise ValueError("cu_seqlens: a contiguous int32 vector of sequences + 1 elements is required")
+    dev = _here(q, k, v, cu_seqlens, out, lse)
+    if out is None:
+        out = _like(q, (tokens, heads, dim), stream)
+    ld_out = _heads(out, tokens, heads, dim, "out")
+    if lse is None:
+        lse = _empty((heads, tokens), _torch.float32, q.device, stream)
+    elif lse.dtype is not _torch.float32 or lse.shape != (heads, tokens) or not lse.is_contiguous():
+        raise ValueError(f"lse: a contiguous float32 tensor of shape {(heads, tokens)} is required")
+    args = muonh_attention_args(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
+                                cu_seqlens.data_ptr(), tokens, len(cu_seqlens) - 1, ld_q, ld_k, ld_v, ld_out, heads,
+                                kv_heads, dim, dim ** -0.5 if scale is None else scale)
+    return args, out, lse, dev
+
+
+def attention_forward(q, k, v, cu_seqlens, scale: Optional[float] = None, out=None, lse=None, stream=None):
+    """(out, lse) of causal attention over packed sequences with grouped heads.
+
+    q          : bfloat16 [tokens, heads, dim], dim 8, 16, .. 128, heads contiguous
+                 (so a slice of a fused projection's output will do)
+    k, v       : [tokens, kv_heads, dim]; heads is a multiple of kv_heads
+    cu_seqlens : int32 [sequences + 1]; sequence b is tokens cu_seqlens[b] ..
+                 cu_seqlens[b + 1] - 1, each of which sees those up to itself
+    scale      : of the scores, > 0; dim^-1/2 if None
+    out, lse   : memory of the results; lse is float32 [heads, tokens], the log of
+                 each row's sum of exponentials, which the backward pass reads
+    Tokens behind the last sequence are left as they were.
+    """
+    args, out, lse, dev = _attention(q, k, v, cu_seqlens, scale, out, lse, stream)
+    if stream is not None:
+        _record(stream, [q, k, v, cu_seqlens, out, lse])
+    rc = _lib.muonh_attention_forward(ctypes.byref(args), _stream(stream, dev))
+    if rc:
+        _check(rc, "muonh_attention_forward")
+    return out, lse
+
+
+def attention_backward(dout, q, k, v, out, lse, cu_seqlens, scale: Optional[float] = None, dq=None, dk=None, dv=None,
+                       stream=None):
+    """(dq, dk, dv) from the output's gradient and the forward pass's arguments and
+    results.
+
+    dq, dk, dv : their memory (slices of one fused gradient will do)
+    Tokens behind the last sequence are left as they were.
+    """
+    if out is None or lse is None:
+        raise ValueError("out and lse are the forward pass's results")
+    args, out, lse, dev = _attention(q, k, v, cu_seqlens, scale, out, lse, stream)
+    tokens, heads, dim = q.shape
+    kv_heads = k.shape[1]
+    ld_dout = _heads(dout, tokens, heads, dim, "dout")
+    _here(q, dout, dq, dk, dv)
+    dq = _like(q, (tokens, heads, dim), stream) if dq is None else dq
+    dk = _like(k, (tokens, kv_heads, dim), stream) if dk is None else dk
+    dv = _like(v, (tokens, kv_heads, dim), stream) if dv is None else dv
+    lds = _heads(dq, tokens, heads, dim, "dq"), _heads(dk, tokens, kv_heads, dim, "dk"), _heads(dv, tokens, kv_heads, dim, "dv")
+    need = ctypes.c_size_t()
+    rc = _lib.muonh_attention_backward_workspace(ctypes.byref(args), ctypes.byref(need))
+    if rc:
+        _check(rc, "muonh_attention_backward_workspace")
+    need = need.value
+    ws = _like(lse, need // 4, stream, result=False) if need else None
+    grad = muonh_attention_grad_args(args, dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ld_dout, *lds,
+                                     None if ws is None else ws.data_ptr(), need)
+    if stream is not None:
+        _record(stream, [t for t in (dout, q, k, v, out, lse, cu_seqlens, dq, dk, dv, ws) if t is not None])
+    rc = _lib.muonh_attention_backward(ctypes.byref(grad), _stream(stream, dev))
+    if rc:
+        _check(rc, "muonh_attention_backward")
+    return dq, dk, dv

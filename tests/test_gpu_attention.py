@@ -1,0 +1,366 @@
+"""Causal attention over packed sequences and its gradients, on an MI355X against
+the fp64 oracle.
+
+Tolerances, element by element (u = 2^-23: fp32 sums whose additions may truncate;
+b = 2^-8: half a step of bf16).  With n rows seen and D columns:
+  S:    es_ij = c D u sum|q k|
+  P:    the exponent's product, difference and 2^x: ep_ij = es_ij + 8 u (|S_ij| + |lse_i| + 1),
+        and b for the matrix operand
+  out:  sum_j P |v| (b + 2 max_j ep_ij + 2 n u), and b (the maximum over j: numerator
+        and denominator)
+  lse:  max_j ep_ij + n u
+  dP:   D u sum|do v|;  delta: D u sum|do o|;  together ed_ij
+  dS:   eds_ij = |dS| (b + 2 ep_ij) + c P (ed_ij + 2 u |dP - delta|)
+  dq:   sum_j (eds |k| + 2 n u |dS k|), and b;  dk likewise over the rows and heads
+  dv:   sum_i P |do| (b + 2 ep + 2 n u), and b
+In the backward pass out and lse are inputs, the same for both sides.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import pretraining_optimizer_amd as pm
+from oracle import attention
+from parity import announce
+
+pytestmark = pytest.mark.gpu
+
+U, B = 2.0 ** -23, 2.0 ** -8
+
+
+def _np(t):
+    return t.detach().double().cpu().numpy()
+
+
+def _inputs(lens, heads, kv, dim, seed=0, tail=0, spread=1.5):
+    gen = torch.Generator().manual_seed(seed + 7 * sum(lens) + dim)
+    n = sum(lens) + tail
+    q = (spread * torch.randn((n, heads, dim), generator=gen)).bfloat16()
+    k, v, do = (torch.randn((n, h, dim), generator=gen).bfloat16() for h in (kv, kv, heads))
+    cu = torch.tensor([0] + list(np.cumsum(lens)), dtype=torch.int32)
+    return q.cuda(), k.cuda(), v.cuda(), (0.1 * do).bfloat16().cuda(), cu.cuda()
+
+
+def _each(q, k, v, cu, scale):
+    """Per sequence and head: rows, head, key head, |S|, lse, P and the error of S."""
+    Q, K, V = _np(q), _np(k), _np(v)
+    tokens, heads, dim = Q.shape
+    group = heads // K.shape[1]
+    ends = [min(max(int(c), 0), tokens) for c in cu.tolist()]
+    for s, e in zip(ends[:-1], ends[1:]):
+        for h in range(heads if e > s else 0):
+            rows, g = slice(s, e), h // group
+            a, b = Q[rows, h], K[rows, g]
+            S, lse, P = attention.probabilities(a, b, scale)
+            low = P > 0
+            S = np.where(low, np.abs(np.where(low, S, 0.0)), 0.0)
+            es = np.where(low, scale * dim * U * (np.abs(a) @ np.abs(b).T), 0.0)
+            ep = np.where(low, es + 8 * U * (S + np.abs(lse)[:, None] + 1), 0.0)
+            yield rows, h, g, a, b, V[rows, g], lse, P, ep
+
+
+def _check_forward(out, lse, q, k, v, cu, scale, what):
+    O, L = _np(out), _np(lse)
+    for rows, h, g, a, b, vh, rl, P, ep in _each(q, k, v, cu, scale):
+        n, worst = len(a), ep.max(axis=1)
+        want = P @ vh
+        tol = (P @ np.abs(vh)) * (B + 2 * worst + 2 * n * U)[:, None]
+        tol += B * (np.abs(want) + tol)
+        err = np.abs(O[rows, h] - want)
+        assert np.all(err <= tol), (what, "out", rows, h, float((err - tol).max()))
+        err = np.abs(L[h, rows] - rl)
+        assert np.all(err <= worst + n * U), (what, "lse", rows, h, float(err.max()))
+
+
+def _check_backward(grads, do, q, k, v, out, lse, cu, scale, what):
+    dQ, dK, dV = (_np(t) for t in grads)
+    DO, O, L = _np(do), _np(out), _np(lse)
+    rdq, rdk, rdv = attention.attention_backward(DO, _np(q), _np(k), _np(v), O, L, cu.tolist(), scale)
+    tq, tk, tv = (np.zeros(t.shape) for t in (rdq, rdk, rdv))
+    dim, group = q.shape[2], q.shape[1] // k.shape[1]
+    for rows, h, g, a, b, vh, rl, P, ep in _each(q, k, v, cu, scale):
+        n, d = len(a), DO[rows, h]
+        # the given lse is the formula's: P's error from it is the reference's, too
+        P = P * np.exp(rl - L[h, rows])[:, None]
+        dP = d @ vh.T
+        delta = (d * O[rows, h]).sum(axis=1, keepdims=True)
+        ed = dim * U * (np.abs(d) @ np.abs(vh).T + np.abs(d * O[rows, h]).sum(axis=1, keepdims=True))
+        ds = scale * P * (dP - delta)
+        eds = np.abs(ds) * (B + 2 * ep) + scale * P * (ed + 2 * U * np.abs(dP - delta))
+        m = group * n
+        tq[rows, h] = eds @ np.abs(b) + 2 * n * U * (np.abs(ds) @ np.abs(b))
+        tk[rows, g] += eds.T @ np.abs(a) + 2 * m * U * (np.abs(ds).T @ np.abs(a))
+        tv[rows, g] += (P * (B + 2 * ep + 2 * m * U)).T @ np.abs(d)
+    for name, got, want, tol in (("dq", dQ, rdq, tq), ("dk", dK, rdk, tk), ("dv", dV, rdv, tv)):
+        live = np.isfinite(want)
+        tol = tol + B * (np.abs(want) + tol)
+        err = np.abs(got - want)
+        assert np.all(err[live] <= tol[live]), (what, name, float((err - tol)[live].max()))
+
+
+def _both(q, k, v, do, cu, scale, what):
+    out, lse = pm.attention_forward(q, k, v, cu, scale=scale)
+    real = q.shape[2] ** -0.5 if scale is None else scale
+    _check_forward(out, lse, q, k, v, cu, real, what)
+    grads = pm.attention_backward(do, q, k, v, out, lse, cu, scale=scale)
+    _check_backward(grads, do, q, k, v, out, lse, cu, real, what)
+    again = pm.attention_backward(do, q, k, v, out, lse, cu, scale=scale)
+    assert all(torch.equal(a, b) for a, b in zip(grads, again))
+    out2, lse2 = pm.attention_forward(q, k, v, cu, scale=scale)
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+    return out, lse, grads
+
+
+LENS = [[1], [2], [31], [32], [33], [63, 65], [64], [77], [127], [128], [129], [1, 1, 1], [200, 1, 0, 300], [0, 5, 0],
+        [257, 63], [500]]
+
+
+@pytest.mark.parametrize("lens", LENS, ids=lambda v: "+".join(map(str, v)))
+@pytest.mark.parametrize("heads,kv,dim", [(4, 2, 128), (3, 1, 64)])
+def test_lengths(lens, heads, kv, dim):
+    announce(f"attention {lens} {heads}/{kv} heads of {dim}")
+    _both(*_inputs(lens, heads, kv, dim), None, f"{lens}")
+
+
+@pytest.mark.parametrize("dim", [8, 16, 24, 32, 40, 56, 64, 72, 80, 96, 104, 120, 128])
+def test_head_widths(dim):
+    announce(f"attention width {dim}")
+    _both(*_inputs([150, 70], 4, 2, dim), 0.2, f"dim {dim}")
+
+
+@pytest.mark.parametrize("heads,kv", [(1, 1), (8, 8), (8, 1), (6, 3), (5, 5), (16, 2)])
+def test_groups(heads, kv):
+    announce(f"attention {heads}/{kv} heads")
+    _both(*_inputs([170, 90], heads, kv, 64), None, f"{heads}/{kv}")
+
+
+def test_longer_sequences():
+    """Many tiles per row, more workgroups than one per XCD."""
+    announce("attention 1500+700, 64 sequences")
+    _both(*_inputs([1500, 700], 2, 1, 128), None, "1500+700")
+    _both(*_inputs([13 * i % 97 for i in range(64)], 2, 2, 64), None, "64 sequences")
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_peaked_and_growing_scores(dim):
+    """Scores far apart, and maxima that grow along a row by more and by less than the
+    factor from which the output is rescaled."""
+    announce(f"attention peaked {dim}")
+    q, k, v, do, cu = _inputs([300, 40], 2, 1, dim, seed=3)
+    _both(q * 8, k, v, do, cu, None, "peaked")
+    ramp = torch.linspace(0.1, 6.0, len(k), device="cuda")[:, None, None]
+    _both(q.abs(), (k.abs() * ramp).bfloat16(), v, do, cu, None, "growing")
+    _both(q.abs(), (k.abs() * ramp.flip(0)).bfloat16(), v, do, cu, None, "falling")
+    _both(q.abs(), (-k.abs() * 20).bfloat16(), v, do, cu, None, "far below zero")
+    zero = torch.zeros_like(q)
+    _both(zero, k, v, do, cu, 3.0, "equal scores")
+
+
+def _windows(tokens, heads, kv, dim, pad=8):
+    """q, k, v as slices of one fused matrix with other columns behind."""
+    wide = torch.full((tokens, (heads + 2 * kv) * dim + pad), 7.0, dtype=torch.bfloat16, device="cuda")
+    parts = wide[:, :heads * dim], wide[:, heads * dim:(heads + kv) * dim], wide[:, (heads + kv) * dim:(heads + 2 * kv) * dim]
+    return wide, [p.unflatten(1, (-1, dim)) for p in parts]
+
+
+@pytest.mark.parametrize("dim", [40, 64, 128])
+def test_fused_buffers_and_tokens_behind_the_last_sequence(dim):
+    """Slices of a fused projection and of a fused gradient; rows that no sequence
+    holds are NaN in the inputs and stay as they were in the results."""
+    announce(f"attention windows {dim}")
+    heads, kv, lens, tail = 4, 2, [130, 35], 70
+    q, k, v, do, cu = _inputs(lens, heads, kv, dim, tail=tail)
+    n, live = len(q), sum(lens)
+    want_out, want_lse = pm.attention_forward(q[:live], k[:live], v[:live], cu)
+    want = pm.attention_backward(do[:live], q[:live], k[:live], v[:live], want_out, want_lse, cu)
+    fused, (fq, fk, fv) = _windows(n, heads, kv, dim)
+    for a, b in ((fq, q), (fk, k), (fv, v)):
+        a.copy_(b)
+        a[live:] = float("nan")
+    out = torch.full((n, heads * dim + 16), 3.0, dtype=torch.bfloat16, device="cuda")
+    o = out[:, 8:8 + heads * dim].unflatten(1, (heads, dim))
+    lse = torch.full((heads, n), 3.0, device="cuda")
+    got = pm.attention_forward(fq, fk, fv, cu, out=o, lse=lse)
+    assert got[0] is o and got[1] is lse
+    assert torch.equal(o[:live], want_out) and torch.equal(lse[:, :live], want_lse)
+    assert (out[live:] == 3).all() and (out[:, :8] == 3).all() and (out[:, 8 + heads * dim:] == 3).all()
+    assert (lse[:, live:] == 3).all()
+    do = do.clone()
+    do[live:] = float("nan")
+    lse[:, live:] = float("nan")
+    o[live:] = float("nan")
+    grads, (gq, gk, gv) = _windows(n, heads, kv, dim)
+    pm.attention_backward(do, fq, fk, fv, o, lse, cu, dq=gq, dk=gk, dv=gv)
+    for a, b in zip((gq, gk, gv), want):
+        assert torch.equal(a[:live], b)
+    assert (grads[live:] == 7).all() and (grads[:, -8:] == 7).all()
+    assert (fused[:, -8:] == 7).all()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("where", [0, 5, 31, 32, 40, 63, 64, 100, 149])
+def test_special_values_reach_later_rows_only(where, value, dim):
+    """An Inf or NaN in a token's key or value: other sequences keep their results bit
+    for bit, earlier rows and other columns theirs (within the tolerances: a block
+    with such a value adds its keys one at a time), and the rest is what the formula
+    gives."""
+    announce(f"attention {value} at {where}, width {dim}")
+    q, k, v, do, cu = _inputs([20, 150, 30], 2, 1, dim)
+    want, wl = pm.attention_forward(q, k, v, cu)
+    later = slice(20 + where, 170)
+    for t in (k, v):
+        bad = t.clone()
+        bad[20 + where, 0, 3] = value
+        out, lse = pm.attention_forward(q, bad if t is k else k, bad if t is v else v, cu)
+        for s in (slice(0, 20), slice(170, 200)):
+            assert torch.equal(out[s], want[s]) and torch.equal(lse[:, s], wl[:, s])
+        hit, hit_lse = out[later].clone(), lse[:, later].clone()
+        if t is v:
+            # every row that sees it has P > 0
+            assert torch.equal(lse, wl)
+            assert (torch.isnan(hit[:, :, 3]).all() if value != value else (hit[:, :, 3] == value).all())
+            out[later, :, 3] = want[later, :, 3]
+        else:
+            if value != value:
+                assert torch.isnan(hit).all() and torch.isnan(hit_lse).all()
+            out[later], lse[:, later] = want[later], wl[:, later]
+        _check_forward(out, lse, q, k, v, cu, dim ** -0.5, f"{value} at {where}")
+
+
+def test_gradients_of_other_sequences_are_kept():
+    announce("attention backward NaN in one sequence")
+    q, k, v, do, cu = _inputs([70, 90, 50], 2, 1, 64)
+    out, lse = pm.attention_forward(q, k, v, cu)
+    want = pm.attention_backward(do, q, k, v, out, lse, cu)
+    for i in range(6):
+        args = [t.clone() for t in (do, q, k, v, out, lse)]
+        if i == 5:
+            args[5][:, 70:160] = float("nan")
+        else:
+            args[i][70:160] = float("nan")
+        got = pm.attention_backward(*args, cu)
+        for a, b in zip(got, want):
+            assert torch.equal(a[:70], b[:70]) and torch.equal(a[160:], b[160:])
+
+
+def test_ends_outside_the_tokens():
+    """The device's cu_seqlens is taken into the tokens; a sequence that would end before
+    it starts is empty."""
+    announce("attention ends outside")
+    q, k, v, do, _ = _inputs([200], 2, 1, 64)
+    for raw, clean in (([-5, 70, 1 << 30], [0, 70, 200]), ([10, 60, 60, 150], [10, 60, 150]),
+                       ([300, 400], None), ([90, 40], None)):
+        cu = torch.tensor(raw, dtype=torch.int32, device="cuda")
+        out, lse = torch.full_like(q, 3.0), torch.full((2, 200), 3.0, device="cuda")
+        pm.attention_forward(q, k, v, cu, out=out, lse=lse)
+        grads = [torch.full_like(t, 3.0) for t in (q, k, v)]
+        pm.attention_backward(do, q, k, v, out, lse, cu, dq=grads[0], dk=grads[1], dv=grads[2])
+        if clean is None:
+            assert all((t == 3).all() for t in [out, lse] + grads)
+            continue
+        _check_forward(out, lse, q, k, v, torch.tensor(clean), 64 ** -0.5, raw)
+        _check_backward(grads, do, q, k, v, out, lse, torch.tensor(clean), 64 ** -0.5, raw)
+        for s in (slice(0, clean[0]), slice(clean[-1], 200)):
+            assert (out[s] == 3).all() and all((t[s] == 3).all() for t in grads)
+
+
+def test_empty():
+    announce("attention empty")
+    q = torch.empty((0, 4, 64), dtype=torch.bfloat16, device="cuda")
+    cu = torch.zeros(3, dtype=torch.int32, device="cuda")
+    out, lse = pm.attention_forward(q, q, q, cu)
+    assert out.shape == (0, 4, 64) and lse.shape == (4, 0)
+    assert [t.shape for t in pm.attention_backward(q, q, q, q, out, lse, cu)] == [(0, 4, 64)] * 3
+    # no sequences at all: nothing is written
+    x = torch.ones((5, 2, 8), dtype=torch.bfloat16, device="cuda")
+    one = cu[:1].clone()
+    out, lse = pm.attention_forward(x, x, x, one, out=torch.full_like(x, 2.0))
+    assert (out == 2).all()
+    grads = pm.attention_backward(x, x, x, x, out, lse, one, dq=torch.full_like(x, 5.0))
+    assert (grads[0] == 5).all()
+
+
+def test_streams_two_at_once_and_graphs():
+    """Two calls on streams of their own, and two graphs of the whole pass replayed in
+    turn with eager work between, each against the eager result."""
+    announce("attention streams and graphs")
+    sets = [_inputs([300, 57], 4, 2, 64, seed=s) for s in (1, 2)]
+    want = []
+    for q, k, v, do, cu in sets:
+        out, lse = pm.attention_forward(q, k, v, cu)
+        want.append((out, lse) + pm.attention_backward(do, q, k, v, out, lse, cu))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for (q, k, v, do, cu), st in zip(sets, streams):
+            out, lse = pm.attention_forward(q, k, v, cu, stream=st)
+            got.append((out, lse) + pm.attention_backward(do, q, k, v, out, lse, cu, stream=st))
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert all(torch.equal(a, b) for a, b in zip(g, w))
+    graphs, results = [], []
+    for q, k, v, do, cu in sets:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out, lse = pm.attention_forward(q, k, v, cu)
+            results.append((out, lse) + pm.attention_backward(do, q, k, v, out, lse, cu))
+        graphs.append(graph)
+    for _ in range(4):
+        for t in results[0] + results[1]:
+            t.fill_(9.0)
+        graphs[0].replay()
+        with torch.cuda.stream(streams[0]):
+            pm.attention_forward(*sets[1][:3], sets[1][4])
+        graphs[1].replay()
+        torch.cuda.synchronize()
+        for g, w in zip(results, want):
+            assert all(torch.equal(a, b) for a, b in zip(g, w))
+
+
+def test_python_refusals():
+    announce("attention refusals")
+    q, k, v, do, cu = _inputs([40], 4, 2, 64)
+    out, lse = pm.attention_forward(q, k, v, cu)
+    with pytest.raises(TypeError):
+        pm.attention_forward(q.float(), k, v, cu)
+    with pytest.raises(TypeError):
+        pm.attention_forward(q, k.half(), v, cu)
+    with pytest.raises(ValueError):
+        pm.attention_forward(q, k, v[:, :1], cu)
+    with pytest.raises(ValueError):
+        pm.attention_forward(q, k, v[:30], cu)
+    with pytest.raises(ValueError):
+        pm.attention_forward(q[0], k, v, cu)
+    with pytest.raises(ValueError):
+        pm.attention_forward(q, k, v, cu.long())
+    with pytest.raises(ValueError):
+        pm.attention_forward(q, k, v, cu[:0])
+    with pytest.raises(ValueError):
+        pm.attention_forward(q, k, v, cu.cpu())
+    with pytest.raises(ValueError):
+        pm.attention_forward(q[:, ::2], k, v, cu)
+    with pytest.raises(ValueError):
+        pm.attention_forward(q, k, v, cu, lse=lse[:2])
+    with pytest.raises(pm.MuonHError):
+        pm.attention_forward(q, k, v, cu, scale=0.0)
+    with pytest.raises(pm.MuonHError):
+        pm.attention_forward(q, k, v, cu, scale=float("nan"))
+    with pytest.raises(pm.MuonHError):
+        pm.attention_forward(q, k, v, cu, out=q)
+    with pytest.raises(pm.MuonHError):
+        pm.attention_forward(q[:, :3].contiguous(), k, v, cu)
+    odd = torch.zeros((40, 4 * 64 + 1), dtype=torch.bfloat16, device="cuda")[:, 1:].unflatten(1, (4, 64))
+    with pytest.raises(pm.MuonHError):
+        pm.attention_forward(odd, k, v, cu)
+    with pytest.raises(ValueError):
+        pm.attention_backward(do, q, k, v, None, lse, cu)
+    with pytest.raises(ValueError):
+        pm.attention_backward(do[:, :2], q, k, v, out, lse, cu)
+    with pytest.raises(pm.MuonHError):
+        pm.attention_backward(do, q, k, v, out, lse, cu, dq=do)
+    wide = torch.empty((1, 4, 136), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(pm.MuonHError):
+        pm.attention_forward(wide, wide, wide, cu)
