@@ -514,6 +514,91 @@ int muonh_attention_forward(const muonh_attention_args* args, void* stream);
 int muonh_attention_backward_workspace(const muonh_attention_args* args, size_t* bytes);
 int muonh_attention_backward(const muonh_attention_grad_args* args, void* stream);
 
+/* ---- residual addition, RMS norm and FP8 output ------------------------------
+ * What stands between two linear layers of a block:
+ *   h = x + residual, rounded to x's type        (residual NULL: h is x)
+ *   rstd = 1/sqrt(mean(h^2) + eps),  y = h rstd weight
+ * and y in block-scaled FP8 (blocks of 1 x 128, as muonh_block_quantize gives them): q,
+ * its row form, and / or qt, its column form; either may be NULL.  y itself is
+ * not stored: it is formed in fp32 from the h that is kept and rounded once, to
+ * E4M3.  x, residual and h share one dtype and need element alignment only.  h may
+ * be x or residual (same address and pitch); any other output that overlaps an
+ * input or another output is refused.                                         */
+typedef struct muonh_add_norm_args {
+  const void*  x;
+  const void*  residual;  /* or NULL                                          */
+  const float* weight;    /* [cols]                                           */
+  void*        h;         /* NULL if residual is                              */
+  float*       rstd;      /* [rows]                                           */
+  int64_t      rows;      /* >= 0                                             */
+  int64_t      cols;      /* 1 .. 2^26                                        */
+  int64_t      ldx, ld_residual, ldh;
+  int32_t      dtype;     /* MUONH_F32 or MUONH_BF16                          */
+  float        eps;       /* >= 0                                             */
+} muonh_add_norm_args;
+
+/* Errors: MUONH_EINVAL, MUONH_EHIP. */
+int muonh_add_norm_quantize(const muonh_add_norm_args* args, const muonh_fp8_matrix* q, const muonh_fp8_matrix* qt,
+                            void* stream);
+
+/* The gradient of x (and of residual, which is the same) and of weight:
+ *   dx = dh + rstd (g - n mean(g n)),  n = h rstd, g = dy weight;  dweight = sum dy n
+ * dh, the gradient that reaches h by the residual stream, shares dy's dtype; dx may be dh, dy
+ * or h.  args.x is h, args.kind MUONH_NORM_RMS, args.mean and args.dbias NULL; the
+ * workspace is muonh_norm_backward_workspace's.                               */
+typedef struct muonh_add_norm_grad_args {
+  muonh_norm_grad_args g;
+  const void*  dh;
+  int64_t      ld_dh;
+} muonh_add_norm_grad_args;
+
+/* Errors: MUONH_EINVAL, MUONH_ENOMEM (workspace too small), MUONH_EHIP. */
+int muonh_add_norm_backward(const muonh_add_norm_grad_args* args, void* stream);
+
+/* ---- embedding ---------------------------------------------------------------
+ * The table that muonh_adamw_step trains, [rows x cols]:
+ *   out[t] = scale table[tokens[t]],  dtable[v] = scale sum over tokens[t] = v of dout[t]
+ * A token outside 0 .. rows - 1 (padding) gives a row of zeros and adds nothing.
+ * Each result is rounded once; sums are fp32, in a fixed order.  Matrices need element
+ * alignment only; an output or workspace that overlaps anything else is refused.   */
+typedef struct muonh_embedding_args {
+  const void* tokens;       /* [count] int32 or int64, device                  */
+  const void* table;        /* table_dtype                                     */
+  void*       out;          /* [count x cols], out_dtype                       */
+  int64_t     count;        /* >= 0; times cols (rounded up to 256) below 2^32 */
+  int64_t     rows;         /* 0 .. 2^30                                       */
+  int64_t     cols;         /* 1 .. 2^20                                       */
+  int64_t     ld_table, ld_out;
+  int32_t     token_bytes;  /* 4 or 8                                          */
+  int32_t     table_dtype;  /* MUONH_F32 or MUONH_BF16                         */
+  int32_t     out_dtype;    /* MUONH_F32 or MUONH_BF16                         */
+  float       scale;        /* finite                                          */
+} muonh_embedding_args;
+
+typedef struct muonh_embedding_grad_args {
+  const void* tokens;
+  const void* dout;         /* [count x cols], dout_dtype                      */
+  void*       dtable;       /* [rows x cols], table_dtype; all of it is written */
+  int64_t     count, rows, cols;
+  int64_t     ld_dout, ld_table;
+  int32_t     token_bytes;
+  int32_t     dout_dtype;
+  int32_t     table_dtype;
+  int32_t     accumulate;   /* 1: add to what dtable holds; rows that no token names
+                               are then not touched                            */
+  float       scale;
+  int32_t     reserved;     /* must be 0                                       */
+  void*       workspace;    /* muonh_embedding_backward_workspace bytes, device,
+                               256-byte aligned; calls that may overlap in time
+                               need one each                                   */
+  size_t      workspace_bytes;
+} muonh_embedding_grad_args;
+
+/* Errors: MUONH_EINVAL, MUONH_ENOMEM (workspace too small), MUONH_EHIP. */
+int muonh_embedding_forward(const muonh_embedding_args* args, void* stream);
+int muonh_embedding_backward_workspace(int64_t count, int64_t rows, int64_t cols, size_t* bytes);
+int muonh_embedding_backward(const muonh_embedding_grad_args* args, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,6 +1,6 @@
 """CPU fp64 oracle for the MuonH optimizer step, the AdamW step of the
-parameters MuonH does not wrap, the block-scaled FP8 operators, the norms and
-the attention.
+parameters MuonH does not wrap, the block-scaled FP8 operators, the norms, the
+attention and the embedding.
 
 TEST INFRASTRUCTURE ONLY.  This package is the plain, slow, obviously-correct
 statement of what the GPU library computes.  Only the tests, the smoke check
@@ -56,4 +56,4 @@ from .adamw import (  # noqa: F401
     first_step_direction,
     constant_gradient_closed_form,
 )
-from . import attention, block_fp8, norm  # noqa: F401
+from . import attention, block_fp8, embedding, norm  # noqa: F401

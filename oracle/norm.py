@@ -26,3 +26,9 @@ def norm_backward(dy, x, weight, mean, rstd, kind: str):
     if kind == "layer":
         dx = dx - g.mean(axis=1, keepdims=True)
     return dx * rstd[:, None], (dy * h).sum(axis=0), dy.sum(axis=0)
+
+
+def add_norm_backward(dy, dh, h, weight, rstd):
+    """(dx, dweight) of an RMS norm of h whose residual stream has the gradient dh."""
+    dx, dweight, _ = norm_backward(dy, h, weight, None, rstd, "rms")
+    return np.asarray(dh, dtype=np.float64) + dx, dweight

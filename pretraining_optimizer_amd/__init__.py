@@ -28,8 +28,12 @@ from .muonh import (  # noqa: F401
 )
 from .operators import (  # noqa: F401
     Fp8Matrix,
+    add_norm_backward,
+    add_norm_quantize,
     attention_backward,
     attention_forward,
+    embedding_backward,
+    embedding_forward,
     fp8_matmul,
     fp8_quantize,
     norm_backward,

@@ -19,7 +19,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmuonh.so")
 SOURCES = ("muonh.cpp", "adamw.cpp", "operators.cpp", "step_fp8.cpp", "gemm.hip", "elementwise.hip",
-           "noalloc.hip", "block_fp8.hip", "norm.hip", "attention.cpp", "attention.hip")
+           "noalloc.hip", "block_fp8.hip", "norm.hip", "attention.cpp", "attention.hip",
+           "add_norm.cpp", "embedding.cpp", "embedding.hip")
 ARCH = "gfx950"
 
 

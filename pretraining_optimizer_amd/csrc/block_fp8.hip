@@ -349,6 +349,33 @@ __global__ __launch_bounds__(kQuantThreads) void block_quantize_kernel(QuantArgs
   write_forms<T, SQUARE>(v, p, tr, tc, lds);
 }
 
+// The forms of y = (h r) w, an RMS norm whose rows' r = 1 / rms are given: y is
+// formed in fp32 as the tile is read, so it is rounded once, to E4M3, and never
+// stored.  The order of the two products is norm_forward's.
+template <typename T>
+__global__ __launch_bounds__(kQuantThreads) void norm_quantize_kernel(QuantArgs p, const float* __restrict__ weight,
+                                                                      const float* __restrict__ rstd, uint32_t ctiles) {
+  __shared__ QuantLds<float> lds;
+  const uint32_t tr = blockIdx.x / ctiles, tc = blockIdx.x % ctiles;
+  Row8<T> h[4];
+  load_tile<false, T>(h, reinterpret_cast<const T*>(p.x), p.rows, p.cols, p.ldx, tr, tc);
+  const int64_t r0 = (int64_t)tr * kFp8Tile + (threadIdx.x >> 4) * 4;
+  const int64_t c0 = (int64_t)tc * kFp8Tile + (threadIdx.x & 15) * 8;
+  float w[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) w[j] = c0 + j < p.cols ? weight[c0 + j] : 0.0f;
+  Row8<float> v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bool live = r0 + i < p.rows;
+    const float r = live ? rstd[r0 + i] : 0.0f;
+    // behind the matrix 0 r w is no zero where r or w is infinite
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[i].w[j] = live && c0 + j < p.cols ? __float_as_uint(h[i].value(j) * r * w[j]) : 0u;
+  }
+  write_forms<float, false>(v, p, tr, tc, lds);
+}
+
 // The update of a MuonH step, W <- k1 W - k2 u, that also writes the block-scaled
 // forms of the updated W: one 128 x 128 tile of one matrix per workgroup, so W is
 // read and written once and never read again for its quantisation.  The update's
@@ -1126,6 +1153,15 @@ hipError_t launch_block_quantize(int bf16, int square, const QuantArgs& a, hipSt
     else
       hipLaunchKernelGGL((block_quantize_kernel<float, false>), grid, block, 0, st, a, c);
   }
+  return hipGetLastError();
+}
+
+hipError_t launch_norm_quantize(int bf16, const QuantArgs& a, const float* weight, const float* rstd, hipStream_t st) {
+  if (a.rows <= 0 || a.cols <= 0) return hipSuccess;
+  const uint32_t c = (uint32_t)((a.cols + kFp8Tile - 1) / kFp8Tile);
+  const dim3 grid((unsigned)((a.rows + kFp8Tile - 1) / kFp8Tile) * c), block(kQuantThreads);
+  if (bf16) hipLaunchKernelGGL((norm_quantize_kernel<uint16_t>), grid, block, 0, st, a, weight, rstd, c);
+  else hipLaunchKernelGGL((norm_quantize_kernel<float>), grid, block, 0, st, a, weight, rstd, c);
   return hipGetLastError();
 }
 

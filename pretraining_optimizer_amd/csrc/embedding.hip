@@ -1,0 +1,455 @@
+// Embedding lookup with scaling, and its gradient by sorted tokens (gfx950).
+//
+//   out[t] = scale table[token t],  dtable[v] = scale (sum over t with token v of dout[t])
+//
+// A token outside the table (padding) gives zeros and adds nothing.
+//
+// Backward: the tokens are sorted by a stable radix sort, so each row's tokens stand
+// together in their order of appearance; runs of 16 (or 64) sorted tokens are added by
+// one group of threads each, and rows whose tokens go over a run's end are joined from
+// the runs' partial sums in order.  No atomics: results are the same in every call.
+// Sums are fp32, each result is rounded once.
+
+#include "embedding.h"
+
+#include <algorithm>
+
+#include "row_vectors.h"
+
+namespace muonh {
+namespace {
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ int64_t token_at(const void* tokens, int wide, int64_t i) {
+  return wide ? ld_global<int64_t>(reinterpret_cast<const int64_t*>(tokens) + i)
+              : (int64_t)ld_global<int32_t>(reinterpret_cast<const int32_t*>(tokens) + i);
+}
+
+// Groups of G threads take a token each, 8 columns per thread at a time.  Bound by HBM:
+// a row is read and written once.
+template <typename T, typename O>
+__global__ __launch_bounds__(kThreads) void embedding_forward_kernel(EmbeddingArgs p, int log_group) {
+  const int group = 1 << log_group, t = threadIdx.x & (group - 1);
+  const int64_t i = (int64_t)blockIdx.x * (kThreads >> log_group) + (threadIdx.x >> log_group);
+  if (i >= p.count) return;
+  const int64_t v = token_at(p.tokens, p.wide, i);
+  const bool known = v >= 0 && v < p.rows;
+  const T* src = reinterpret_cast<const T*>(p.table) + (known ? v : 0) * p.ldt;
+  O* dst = reinterpret_cast<O*>(p.out) + i * p.ldo;
+  const int cols = (int)p.cols;
+  for (int c = 8 * t; c < cols; c += 8 * group) {
+    float a[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) a[j] = 0.0f;
+    if (known) {
+      load8<T>(src, c, cols).widen(a);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) a[j] *= p.scale;
+    }
+    store8<O>(dst, c, cols, a);
+  }
+}
+
+// One pass of the sort by one workgroup's keys: the stable rank of each among them.
+// Thread t of wavefront w holds items 512 w + 64 k + t % 64.  Each wavefront counts its
+// digits in order (equal digits of one load by a ballot per bit), and the wavefronts'
+// counts are added up over the digits and, for each, over the wavefronts.
+constexpr int kWaves = kSortThreads / 64;
+constexpr int kWaveItems = 64 * kSortItems;
+struct SortLds {
+  uint32_t count[kWaves][kSortDigits + 1];   // + 1: a digit's counters lie in different banks
+  uint32_t wave[kWaves];
+};
+
+template <bool HELD>
+__device__ __forceinline__ void count_digits(SortLds& lds, const uint32_t (&key)[kSortItems], uint32_t (&rank)[kSortItems],
+                                             int64_t left, int shift, int bits) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint32_t mask = (1u << bits) - 1;
+  for (int i = threadIdx.x; i < kWaves * (kSortDigits + 1); i += kSortThreads) (&lds.count[0][0])[i] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kSortItems; ++k) {
+    const bool live = wave * kWaveItems + k * 64 + lane < left;
+    const uint32_t d = (key[k] >> shift) & mask;
+    uint64_t same = __ballot(live);
+    for (int b = 0; b < bits; ++b) {
+      const uint64_t m = __ballot((d >> b) & 1);
+      same &= (d >> b) & 1 ? m : ~m;
+    }
+    if (live) {
+      const uint32_t before = lds.count[wave][d], at = __popcll(same & ((1ull << lane) - 1));
+      if (HELD) rank[k] = before + at;
+      // the wavefront's LDS accesses are in order: all have read before one writes
+      __builtin_amdgcn_wave_barrier();
+      if (at == 0) lds.count[wave][d] = before + (uint32_t)__popcll(same);
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+  __syncthreads();
+}
+
+// counts[digit][wave] -> where the first key of each begins among the workgroup's, and
+// in total[] the digit's count.
+__device__ __forceinline__ uint32_t begin_digits(SortLds& lds, int digits) {
+  const int d = threadIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  uint32_t total = 0;
+  if (d < digits)
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      const uint32_t c = lds.count[w][d];
+      lds.count[w][d] = total;
+      total += c;
+    }
+  uint32_t sum = total;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const uint32_t up = __shfl_up(sum, off, 64);
+    if (lane >= off) sum += up;
+  }
+  if (lane == 63) lds.wave[wave] = sum;
+  __syncthreads();
+  for (int w = 0; w < wave; ++w) sum += lds.wave[w];
+  if (d < digits)
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) lds.count[w][d] += sum - total;
+  __syncthreads();
+  return total;
+}
+static_assert(kSortDigits <= kSortThreads, "a thread per digit");
+
+__device__ __forceinline__ uint32_t key_of(const EmbeddingGradArgs& p, int64_t i) {
+  const int64_t v = token_at(p.tokens, p.wide, i);
+  return v >= 0 && v < p.rows ? (uint32_t)v : (uint32_t)p.rows;
+}
+
+// Zeros in rows [0, rows) of the table, 16 bytes at a time, by the workgroups from
+// `first` on.
+template <typename O>
+__device__ __forceinline__ void fill_zeros(const EmbeddingGradArgs& p, int64_t first) {
+  const int64_t per = (p.cols + 7) / 8, n = p.rows * per;
+  const float zeros[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  for (int64_t i = ((int64_t)blockIdx.x - first) * kSortThreads + threadIdx.x; i < n;
+       i += ((int64_t)gridDim.x - first) * kSortThreads) {
+    const int64_t row = i / per;
+    store8<O>(reinterpret_cast<O*>(p.dtable) + row * p.ldt, (int)(i - row * per) * 8, (int)p.cols, zeros);
+  }
+}
+
+// Up to kSortBlock tokens: one workgroup sorts them, in registers and LDS, while the
+// others clear the table.
+template <typename O>
+__global__ __launch_bounds__(kSortThreads) void sort_and_clear_kernel(EmbeddingGradArgs p, SortPlan plan) {
+  __shared__ SortLds lds;
+  __shared__ uint32_t keys[kSortBlock];
+  __shared__ uint16_t places[kSortBlock];
+  if (blockIdx.x > 0) {
+    fill_zeros<O>(p, 1);
+    return;
+  }
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  uint32_t key[kSortItems], place[kSortItems], rank[kSortItems];
+#pragma unroll
+  for (int k = 0; k < kSortItems; ++k) {
+    const int i = wave * kWaveItems + k * 64 + lane;
+    key[k] = i < p.count ? key_of(p, i) : 0;
+    place[k] = i;
+  }
+  for (int pass = 0; pass < plan.passes; ++pass) {
+    const int shift = pass * plan.bits;
+    count_digits<true>(lds, key, rank, p.count, shift, plan.bits);
+    begin_digits(lds, 1 << plan.bits);
+#pragma unroll
+    for (int k = 0; k < kSortItems; ++k) {
+      const int i = wave * kWaveItems + k * 64 + lane;
+      if (i < p.count) {
+        const uint32_t to = lds.count[wave][(key[k] >> shift) & ((1u << plan.bits) - 1)] + rank[k];
+        keys[to] = key[k];
+        places[to] = (uint16_t)place[k];
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kSortItems; ++k) {
+      const int i = wave * kWaveItems + k * 64 + lane;
+      if (i < p.count) {
+        key[k] = keys[i];
+        place[k] = places[i];
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kSortItems; ++k) {
+    const int i = wave * kWaveItems + k * 64 + lane;
+    if (i < p.count) {
+      p.keys[0][i] = key[k];
+      p.places[0][i] = place[k];
+    }
+  }
+}
+static_assert(kSortBlock <= 65536, "places of one workgroup's tokens are 16 bits");
+
+template <typename O>
+__global__ __launch_bounds__(kSortThreads) void clear_kernel(EmbeddingGradArgs p) {
+  fill_zeros<O>(p, 0);
+}
+
+// More tokens: per pass the digits' counts of every workgroup, where each begins, and
+// the keys put there.  `from` is the buffer read (pass 0: the tokens).
+__device__ __forceinline__ void read_keys(const EmbeddingGradArgs& p, int pass, int from, int64_t first,
+                                          uint32_t (&key)[kSortItems], uint32_t (&place)[kSortItems]) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int k = 0; k < kSortItems; ++k) {
+    const int64_t i = first + wave * kWaveItems + k * 64 + lane;
+    key[k] = place[k] = 0;
+    if (i < p.count) {
+      key[k] = pass == 0 ? key_of(p, i) : p.keys[from][i];
+      place[k] = pass == 0 ? (uint32_t)i : p.places[from][i];
+    }
+  }
+}
+
+__global__ __launch_bounds__(kSortThreads) void sort_count_kernel(EmbeddingGradArgs p, SortPlan plan, int pass, int from) {
+  __shared__ SortLds lds;
+  const int64_t first = (int64_t)blockIdx.x * kSortBlock;
+  uint32_t key[kSortItems], place[kSortItems], rank[kSortItems];
+  read_keys(p, pass, from, first, key, place);
+  count_digits<false>(lds, key, rank, p.count - first, pass * plan.bits, plan.bits);
+  const uint32_t total = begin_digits(lds, 1 << plan.bits);
+  if ((int)threadIdx.x < 1 << plan.bits) p.digits[(int64_t)blockIdx.x * kSortDigits + threadIdx.x] = total;
+}
+
+// digits[block][d] -> where block's keys of digit d begin.
+__global__ __launch_bounds__(kSortThreads) void sort_begin_kernel(EmbeddingGradArgs p, SortPlan plan) {
+  __shared__ uint32_t sums[kWaves];
+  const int d = threadIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const bool live = d < 1 << plan.bits;
+  uint32_t total = 0;
+  if (live)
+    for (int64_t b = 0; b < plan.blocks; ++b) total += p.digits[b * kSortDigits + d];
+  uint32_t sum = total;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const uint32_t up = __shfl_up(sum, off, 64);
+    if (lane >= off) sum += up;
+  }
+  if (lane == 63) sums[wave] = sum;
+  __syncthreads();
+  for (int w = 0; w < wave; ++w) sum += sums[w];
+  uint32_t at = sum - total;
+  if (live)
+    for (int64_t b = 0; b < plan.blocks; ++b) {
+      const uint32_t c = p.digits[b * kSortDigits + d];
+      p.digits[b * kSortDigits + d] = at;
+      at += c;
+    }
+}
+
+__global__ __launch_bounds__(kSortThreads) void sort_place_kernel(EmbeddingGradArgs p, SortPlan plan, int pass, int from, int to) {
+  __shared__ SortLds lds;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t first = (int64_t)blockIdx.x * kSortBlock;
+  uint32_t key[kSortItems], place[kSortItems], rank[kSortItems];
+  read_keys(p, pass, from, first, key, place);
+  const int shift = pass * plan.bits;
+  const uint32_t mask = (1u << plan.bits) - 1;
+  count_digits<true>(lds, key, rank, p.count - first, shift, plan.bits);
+  // before this wavefront's keys of a digit: the other workgroups' and wavefronts'
+  const int d = threadIdx.x;
+  if (d <= (int)mask) {
+    uint32_t at = p.digits[(int64_t)blockIdx.x * kSortDigits + d];
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      const uint32_t c = lds.count[w][d];
+      lds.count[w][d] = at;
+      at += c;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kSortItems; ++k)
+    if (first + wave * kWaveItems + k * 64 + lane < p.count) {
+      const uint32_t at = lds.count[wave][(key[k] >> shift) & mask] + rank[k];
+      p.keys[to][at] = key[k];
+      p.places[to][at] = place[k];
+    }
+}
+
+// A row of the table's gradient: 8 columns of it, rounded once.
+template <typename O>
+__device__ __forceinline__ void store_sum(const EmbeddingGradArgs& p, uint32_t key, int c, const float (&sum)[8]) {
+  if (key >= (uint32_t)p.rows) return;
+  O* dst = reinterpret_cast<O*>(p.dtable) + (int64_t)key * p.ldt;
+  float a[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) a[j] = sum[j] * p.scale;
+  if (p.accumulate) {
+    float old[8];
+    load8<O>(dst, c, (int)p.cols).widen(old);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) a[j] += old[j];
+  }
+  store8<O>(dst, c, (int)p.cols, a);
+}
+__device__ __forceinline__ void store_partial(float* row, int c, int cols, const float (&sum)[8]) {
+  store8<float>(row, c, cols, sum);
+}
+
+// Sums of a run of sorted tokens: rows whose tokens all lie in the run are written,
+// the sums of the row that began before it and of the one that goes on behind it are
+// left in partials[run][0] and [1] (one that does both: in [0]).
+template <typename T, typename O>
+__global__ __launch_bounds__(kThreads) void embedding_sum_kernel(EmbeddingGradArgs p, int which, int log_group, int64_t run) {
+  const int group = 1 << log_group, t = threadIdx.x & (group - 1);
+  const int64_t r = (int64_t)blockIdx.x * (kThreads >> log_group) + (threadIdx.x >> log_group);
+  const int64_t first = r * run, end = min(first + run, p.count);
+  const int c = 8 * ((int)blockIdx.y * group + t), cols = (int)p.cols;
+  if (first >= p.count || c >= cols) return;
+  const uint32_t* keys = p.keys[which];
+  const uint32_t* places = p.places[which];
+  float* part = p.partials + r * 2 * p.cols;
+  const T* dout = reinterpret_cast<const T*>(p.dout);
+  const uint32_t before = first > 0 ? keys[first - 1] : 0xffffffffu, behind = end < p.count ? keys[end] : 0xffffffffu;
+  float sum[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
+  uint32_t current = keys[first];
+  bool opened = current == before;   // the current row's tokens began in an earlier run
+  constexpr int kAhead = 8;
+  for (int64_t i = first; i < end; i += kAhead) {
+    Raw8<T> v[kAhead];
+    uint32_t key[kAhead];
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      const int64_t at = min(i + a, end - 1);
+      key[a] = keys[at];
+      v[a] = load8<T>(dout + (int64_t)places[at] * p.ldd, c, cols);
+    }
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      if (i + a >= end) break;
+      if (key[a] != current) {
+        if (opened) store_partial(part, c, cols, sum);
+        else store_sum<O>(p, current, c, sum);
+        opened = false;
+        current = key[a];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
+      }
+      float x[8];
+      v[a].widen(x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[j] += x[j];
+    }
+  }
+  if (opened) store_partial(part, c, cols, sum);
+  else if (current == behind) store_partial(part + p.cols, c, cols, sum);
+  else store_sum<O>(p, current, c, sum);
+}
+
+// Joins the partial sums of a row whose tokens begin in run r and go on: 8 groups of 32
+// threads add every eighth run's, then those sums in order.
+constexpr int kJoin = 8;
+template <typename O>
+__global__ __launch_bounds__(kThreads) void embedding_join_kernel(EmbeddingGradArgs p, int which, int64_t run) {
+  __shared__ float sums[kJoin][32][9];
+  const int64_t r = blockIdx.x, first = r * run, end = first + run;
+  if (end >= p.count) return;
+  const uint32_t* keys = p.keys[which];
+  const uint32_t key = keys[end - 1];
+  // a row of several runs that began before this one is joined by the run it began in
+  if (keys[end] != key || key >= (uint32_t)p.rows || (first > 0 && keys[first - 1] == key)) return;
+  const int t = threadIdx.x & 31, g = threadIdx.x >> 5;
+  const int c = 8 * ((int)blockIdx.y * 32 + t), cols = (int)p.cols;
+  float sum[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
+  // the runs behind r that begin with the key
+  for (int64_t q = r + g; q == r || (q * run < p.count && keys[q * run] == key); q += kJoin) {
+    if (c >= cols) break;
+    float x[8];
+    load8<float>(p.partials + (q * 2 + (q == r)) * p.cols, c, cols).widen(x);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum[j] += x[j];
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sums[g][t][j] = sum[j];
+  __syncthreads();
+  if (g != 0 || c >= cols) return;
+#pragma unroll
+  for (int q = 1; q < kJoin; ++q)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum[j] += sums[q][t][j];
+  store_sum<O>(p, key, c, sum);
+}
+
+// Threads per row, as a power of two's exponent: as many as it has vectors, at most 256.
+int log_group_of(int64_t cols) {
+  int g = 0;
+  while (g < 8 && ((int64_t)8 << g) < cols) ++g;
+  return g;
+}
+
+template <typename T, typename O>
+hipError_t backward_for(const EmbeddingGradArgs& a, hipStream_t st) {
+  const SortPlan plan = plan_sort(a.count, a.rows);
+  // the table is cleared by 1024 workgroups (4 per CU) at most, 16 KiB each at least
+  const int64_t bytes = a.rows * a.cols * (int64_t)sizeof(O);
+  const unsigned clear = a.accumulate ? 0u : (unsigned)std::min<int64_t>((bytes + 16383) / 16384, 1024);
+  hipError_t e = hipSuccess;
+  int which = 0;
+  if (a.count == 0 || plan.blocks > 1) {
+    if (clear) hipLaunchKernelGGL(clear_kernel<O>, dim3(clear), dim3(kSortThreads), 0, st, a);
+    e = hipGetLastError();
+    if (e != hipSuccess || a.count == 0) return e;
+    const dim3 grid((unsigned)plan.blocks), block(kSortThreads);
+    for (int pass = 0; pass < plan.passes; ++pass) {
+      const int from = which;
+      which = pass == 0 ? 0 : 1 - which;
+      hipLaunchKernelGGL(sort_count_kernel, grid, block, 0, st, a, plan, pass, from);
+      hipLaunchKernelGGL(sort_begin_kernel, dim3(1), block, 0, st, a, plan);
+      hipLaunchKernelGGL(sort_place_kernel, grid, block, 0, st, a, plan, pass, from, which);
+      e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+  } else {
+    hipLaunchKernelGGL(sort_and_clear_kernel<O>, dim3(1 + clear), dim3(kSortThreads), 0, st, a, plan);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  const int lg = log_group_of(a.cols);
+  const int64_t run = sum_run(a.count), runs = (a.count + run - 1) / run, per = kThreads >> lg;
+  const unsigned wide = (unsigned)((a.cols + (8 << lg) - 1) / (8 << lg));
+  hipLaunchKernelGGL((embedding_sum_kernel<T, O>), dim3((unsigned)((runs + per - 1) / per), wide), dim3(kThreads), 0, st,
+                     a, which, lg, run);
+  e = hipGetLastError();
+  if (e != hipSuccess || runs < 2) return e;
+  hipLaunchKernelGGL(embedding_join_kernel<O>, dim3((unsigned)(runs - 1), (unsigned)((a.cols + 255) / 256)), dim3(kThreads),
+                     0, st, a, which, run);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_embedding_forward(int table_bf16, int out_bf16, const EmbeddingArgs& a, hipStream_t st) {
+  const int lg = log_group_of(a.cols);
+  const int64_t per = kThreads >> lg;
+  const dim3 grid((unsigned)((a.count + per - 1) / per)), block(kThreads);
+  if (table_bf16) {
+    if (out_bf16) hipLaunchKernelGGL((embedding_forward_kernel<uint16_t, uint16_t>), grid, block, 0, st, a, lg);
+    else hipLaunchKernelGGL((embedding_forward_kernel<uint16_t, float>), grid, block, 0, st, a, lg);
+  } else {
+    if (out_bf16) hipLaunchKernelGGL((embedding_forward_kernel<float, uint16_t>), grid, block, 0, st, a, lg);
+    else hipLaunchKernelGGL((embedding_forward_kernel<float, float>), grid, block, 0, st, a, lg);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_embedding_backward(int dout_bf16, int table_bf16, const EmbeddingGradArgs& a, hipStream_t st) {
+  if (dout_bf16) return table_bf16 ? backward_for<uint16_t, uint16_t>(a, st) : backward_for<uint16_t, float>(a, st);
+  return table_bf16 ? backward_for<float, uint16_t>(a, st) : backward_for<float, float>(a, st);
+}
+
+}  // namespace muonh

@@ -19,8 +19,8 @@
 
 #include <algorithm>
 
-#include "device_util.h"
 #include "operators.h"
+#include "row_vectors.h"
 
 namespace muonh {
 namespace {
@@ -32,87 +32,6 @@ constexpr int kNormThreads = 256;
 constexpr int kNormGroups = 256;
 constexpr int kBackThreads = 512;
 
-// Eight consecutive elements of a row as stored, from any element alignment
-// (global accesses of any width need no more on gfx950), and as fp32.
-template <typename T> struct Raw8;
-template <> struct Raw8<uint16_t> {
-  typedef uint32_t vec __attribute__((ext_vector_type(4), aligned(2)));
-  vec w;
-  __device__ __forceinline__ void load(const uint16_t* p) {
-    w = ld_global<vec>(p);
-  }
-  __device__ __forceinline__ void zero() { w = vec{0, 0, 0, 0}; }
-  __device__ __forceinline__ void set(int j, const uint16_t* p) {
-    w[j >> 1] |= (uint32_t)ld_global<uint16_t>(p) << (16 * (j & 1));
-  }
-  __device__ __forceinline__ void widen(float (&v)[8]) const {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      v[2 * k] = __uint_as_float(w[k] << 16);
-      v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-    }
-  }
-  static __device__ __forceinline__ float load1(const uint16_t* p) { return bf16_to_f32(ld_global<uint16_t>(p)); }
-  static __device__ __forceinline__ void store(uint16_t* p, const float (&v)[8]) {
-    vec r;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) r[k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
-    st_global<vec>(p, r);
-  }
-  static __device__ __forceinline__ void store1(uint16_t* p, float v) { st_global<uint16_t>(p, f32_to_bf16(v)); }
-};
-template <> struct Raw8<float> {
-  typedef float vec __attribute__((ext_vector_type(4), aligned(4)));
-  vec lo, hi;
-  __device__ __forceinline__ void load(const float* p) {
-    lo = ld_global<vec>(p);
-    hi = ld_global<vec>(p + 4);
-  }
-  __device__ __forceinline__ void zero() { lo = hi = vec{0.0f, 0.0f, 0.0f, 0.0f}; }
-  __device__ __forceinline__ void set(int j, const float* p) {
-    const float v = ld_global<float>(p);
-    if (j < 4) lo[j] = v;
-    else hi[j - 4] = v;
-  }
-  __device__ __forceinline__ void widen(float (&v)[8]) const {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      v[k] = lo[k];
-      v[4 + k] = hi[k];
-    }
-  }
-  static __device__ __forceinline__ float load1(const float* p) { return ld_global<float>(p); }
-  static __device__ __forceinline__ void store(float* p, const float (&v)[8]) {
-    st_global<vec>(p, vec{v[0], v[1], v[2], v[3]});
-    st_global<vec>(p + 4, vec{v[4], v[5], v[6], v[7]});
-  }
-  static __device__ __forceinline__ void store1(float* p, float v) { st_global<float>(p, v); }
-};
-
-// Elements [c, c + 8) of a row of n, zeros behind its end.
-template <typename T>
-__device__ __forceinline__ Raw8<T> load8(const T* row, int c, int n) {
-  Raw8<T> r;
-  if (c + 8 <= n) {
-    r.load(row + c);
-  } else {
-    r.zero();
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (c + j < n) r.set(j, row + c + j);
-  }
-  return r;
-}
-template <typename T>
-__device__ __forceinline__ void store8(T* row, int c, int n, const float (&v)[8]) {
-  if (c + 8 <= n) {
-    Raw8<T>::store(row + c, v);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (c + j < n) Raw8<T>::store1(row + c + j, v[j]);
-  }
-}
 // A weight or bias vector: read by every row, so through the caches.
 __device__ __forceinline__ void loadw(const float* w, int c, int n, float (&v)[8]) {
   typedef float vec __attribute__((ext_vector_type(4), aligned(4)));
@@ -127,6 +46,13 @@ __device__ __forceinline__ void loadw(const float* w, int c, int n, float (&v)[8
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = c + j < n ? ld_global<float>(w + c + j) : 0.0f;
   }
+}
+
+// v rounded to T, as fp32.
+template <typename T>
+__device__ __forceinline__ float round_to(float v) {
+  if constexpr (sizeof(T) == 2) return bf16_to_f32(f32_to_bf16(v));
+  else return v;
 }
 
 // Sums of NS values over the G threads of a row, the same in each of them: a
@@ -218,6 +144,46 @@ __global__ __launch_bounds__(G > kNormThreads ? G : kNormThreads) void norm_forw
   }
 }
 
+// h = x + residual, kept in x's type, and 1 / sqrt(mean(h^2) + eps) of the kept
+// values: what the tile kernel that normalises and quantises h (block_fp8.hip) needs
+// of its rows.  Without a residual h is x, which is only read.
+template <typename T, int G, int NV>
+__global__ __launch_bounds__(G > kNormThreads ? G : kNormThreads) void add_norm_rows_kernel(AddNormArgs p) {
+  constexpr int kThreads = G > kNormThreads ? G : kNormThreads;
+  constexpr int kRows = kThreads / G;
+  __shared__ float red[1][16];
+  const int t = threadIdx.x % G, cols = (int)p.cols;
+  const float rn = 1.0f / (float)cols;
+  for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < p.rows; r0 += (int64_t)gridDim.x * kRows) {
+    const int64_t row = r0 + threadIdx.x / G, at = min(row, p.rows - 1);
+    const T* x = reinterpret_cast<const T*>(p.x) + at * p.ldx;
+    const T* r = reinterpret_cast<const T*>(p.residual) + at * p.ldr;
+    Raw8<T> v[NV], w[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      v[k] = load8<T>(x, 8 * (t + G * k), cols);
+      if (p.residual) w[k] = load8<T>(r, 8 * (t + G * k), cols);
+    }
+    float ss[1] = {0.0f};
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      float a[8], b[8];
+      v[k].widen(a);
+      if (p.residual) {
+        w[k].widen(b);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) a[j] = round_to<T>(a[j] + b[j]);
+        const int c = 8 * (t + G * k);
+        if (row < p.rows && c < cols) store8<T>(reinterpret_cast<T*>(p.h) + row * p.ldh, c, cols, a);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss[0] += a[j] * a[j];
+    }
+    group_sum<G, 1>(ss, red);
+    if (row < p.rows && t == 0) p.rstd[row] = 1.0f / sqrtf(ss[0] * rn + p.eps);
+  }
+}
+
 // Rows too long for registers: one workgroup per row reads it once per
 // reduction and once for the output, from the caches after the first.
 //
@@ -271,11 +237,33 @@ __global__ __launch_bounds__(kLongThreads) void norm_forward_long_kernel(NormArg
   }
 }
 
+template <typename T>
+__global__ __launch_bounds__(kLongThreads) void add_norm_rows_long_kernel(AddNormArgs p) {
+  __shared__ float red[1][16];
+  const double rn = 1.0 / (double)p.cols;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    const T* x = reinterpret_cast<const T*>(p.x) + row * p.ldx;
+    const T* r = reinterpret_cast<const T*>(p.residual) + row * p.ldr;
+    T* h = reinterpret_cast<T*>(p.h) + row * p.ldh;
+    float ss[1] = {long_sum(p.cols, [&](int64_t c) {
+      float v = Raw8<T>::load1(x + c);
+      if (p.residual) {
+        v = round_to<T>(v + Raw8<T>::load1(r + c));
+        Raw8<T>::store1(h + c, v);
+      }
+      return v * v;
+    })};
+    group_sum<kLongThreads, 1>(ss, red);
+    if (threadIdx.x == 0) p.rstd[row] = 1.0f / sqrtf((float)((double)ss[0] * rn) + p.eps);
+  }
+}
+
 // Backward.  Workgroup b takes rows kRows b .. , kRows (b + gridDim.x) .. and
 // so on; a thread keeps the same columns for all of its rows and adds dy h
 // (and dy) for them in registers.  At the end the groups of one workgroup are
 // added in order through LDS, and the workgroup writes one row of partials.
-template <typename T, bool LAYER, bool BIAS, int G, int NV>
+// RES: dx also takes the residual stream's gradient dh, rounded once.
+template <typename T, bool LAYER, bool BIAS, bool RES, int G, int NV>
 __global__ __launch_bounds__(G > kBackThreads ? G : kBackThreads) void norm_backward_kernel(NormGradArgs p) {
   constexpr int kThreads = G > kBackThreads ? G : kBackThreads;
   constexpr int kRows = kThreads / G;
@@ -288,7 +276,7 @@ __global__ __launch_bounds__(G > kBackThreads ? G : kBackThreads) void norm_back
   // The next trip's rows are on their way while this one's are used, and the
   // weight stays in registers; 1024 threads have no room for either.
   constexpr bool kAhead = kThreads < 1024;
-  Raw8<T> nx[NV], nd[NV];
+  Raw8<T> nx[NV], nd[NV], nh[RES ? NV : 1];
   float nr = 0.0f, nmu = 0.0f;
   auto fetch = [&](int64_t r0) {
     const int64_t at = min(r0 + grp, p.rows - 1);
@@ -298,6 +286,8 @@ __global__ __launch_bounds__(G > kBackThreads ? G : kBackThreads) void norm_back
     for (int k = 0; k < NV; ++k) {
       nx[k] = load8<T>(x, 8 * (t + G * k), cols);
       nd[k] = load8<T>(dy, 8 * (t + G * k), cols);
+      if constexpr (RES)
+        nh[k] = load8<T>(reinterpret_cast<const T*>(p.dh) + at * p.lddh, 8 * (t + G * k), cols);
     }
     nr = p.rstd[at];
     if constexpr (LAYER) nmu = p.mean[at];
@@ -324,10 +314,12 @@ __global__ __launch_bounds__(G > kBackThreads ? G : kBackThreads) void norm_back
     const bool live = row < p.rows;
     const float r = nr, mu = nmu;
     float h[NV][8], g[NV][8];
+    Raw8<T> dh[RES ? NV : 1];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       nx[k].widen(h[k]);
       nd[k].widen(g[k]);
+      if constexpr (RES) dh[k] = nh[k];
     }
     if constexpr (kAhead) {
       if (r0 + step < p.rows) fetch(r0 + step);
@@ -361,6 +353,12 @@ __global__ __launch_bounds__(G > kBackThreads ? G : kBackThreads) void norm_back
       float o[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) o[j] = r * (g[k][j] - c0 - h[k][j] * c1);
+      if constexpr (RES) {
+        float a[8];
+        dh[k].widen(a);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] += a[j];
+      }
       store8<T>(dx, c, cols, o);
     }
   }
@@ -403,7 +401,7 @@ __global__ __launch_bounds__(G > kBackThreads ? G : kBackThreads) void norm_back
 
 // Rows too long for registers: a workgroup adds each of its rows to its own
 // row of partials in memory (each column always by the same thread).
-template <typename T, bool LAYER, bool BIAS>
+template <typename T, bool LAYER, bool BIAS, bool RES>
 __global__ __launch_bounds__(kLongThreads) void norm_backward_long_kernel(NormGradArgs p) {
   __shared__ float red[2][16];
   const double rn = 1.0 / (double)p.cols;
@@ -437,7 +435,9 @@ __global__ __launch_bounds__(kLongThreads) void norm_backward_long_kernel(NormGr
     for (int64_t c = threadIdx.x; c < p.cols; c += kLongThreads) {
       const float h = (Raw8<T>::load1(x + c) - mu) * r;
       const float g = Raw8<T>::load1(dy + c) * p.weight[c];
-      Raw8<T>::store1(dx + c, r * (g - c0 - h * c1));
+      float o = r * (g - c0 - h * c1);
+      if constexpr (RES) o += Raw8<T>::load1(reinterpret_cast<const T*>(p.dh) + row * p.lddh + c);
+      Raw8<T>::store1(dx + c, o);
     }
   }
 }
@@ -504,16 +504,16 @@ hipError_t forward_for(const NormArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <typename T, bool LAYER, bool BIAS>
+template <typename T, bool LAYER, bool BIAS, bool RES = false>
 hipError_t backward_for(const NormGradArgs& a, hipStream_t st) {
   const int64_t cols = a.cols, groups = norm_partial_rows(a.rows, cols);
   if (groups > 0) {
     const dim3 grid((unsigned)groups);
 #define MUONH_NORM_BWD(G, NV)                                                                  \
-  hipLaunchKernelGGL((norm_backward_kernel<T, LAYER, BIAS, G, NV>), grid,                      \
+  hipLaunchKernelGGL((norm_backward_kernel<T, LAYER, BIAS, RES, G, NV>), grid,                      \
                      dim3(G > kBackThreads ? G : kBackThreads), 0, st, a)
     if (cols > kRegisterCols)
-      hipLaunchKernelGGL((norm_backward_long_kernel<T, LAYER, BIAS>), grid, dim3(kLongThreads), 0, st, a);
+      hipLaunchKernelGGL((norm_backward_long_kernel<T, LAYER, BIAS, RES>), grid, dim3(kLongThreads), 0, st, a);
     else if (cols <= 64) MUONH_NORM_BWD(8, 1);
     else if (cols <= 128) MUONH_NORM_BWD(16, 1);
     else if (cols <= 256) MUONH_NORM_BWD(32, 1);
@@ -533,7 +533,40 @@ hipError_t backward_for(const NormGradArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
+template <typename T>
+hipError_t add_norm_rows_for(const AddNormArgs& a, hipStream_t st) {
+  const int64_t cols = a.cols;
+  if (cols > kRegisterCols) {
+    hipLaunchKernelGGL(add_norm_rows_long_kernel<T>, dim3((unsigned)std::min<int64_t>(a.rows, 1 << 20)),
+                       dim3(kLongThreads), 0, st, a);
+    return hipGetLastError();
+  }
+  const int64_t per = rows_at_once(cols, kNormThreads);
+  const dim3 grid((unsigned)std::min<int64_t>((a.rows + per - 1) / per, 1 << 20));
+#define MUONH_ADD_NORM(G, NV)                                                                  \
+  hipLaunchKernelGGL((add_norm_rows_kernel<T, G, NV>), grid, dim3(G > kNormThreads ? G : kNormThreads), 0, st, a)
+  if (cols <= 64) MUONH_ADD_NORM(8, 1);
+  else if (cols <= 128) MUONH_ADD_NORM(16, 1);
+  else if (cols <= 256) MUONH_ADD_NORM(32, 1);
+  else if (cols <= 512) MUONH_ADD_NORM(64, 1);
+  else if (cols <= 1024) MUONH_ADD_NORM(64, 2);
+  else if (cols <= 2048) MUONH_ADD_NORM(128, 2);
+  else if (cols <= 4096) MUONH_ADD_NORM(256, 2);
+  else if (cols <= 8192) MUONH_ADD_NORM(512, 2);
+  else MUONH_ADD_NORM(1024, 2);
+#undef MUONH_ADD_NORM
+  return hipGetLastError();
+}
+
 }  // namespace
+
+hipError_t launch_add_norm_rows(int bf16, const AddNormArgs& a, hipStream_t st) {
+  return bf16 ? add_norm_rows_for<uint16_t>(a, st) : add_norm_rows_for<float>(a, st);
+}
+
+hipError_t launch_add_norm_backward(int bf16, const NormGradArgs& a, hipStream_t st) {
+  return bf16 ? backward_for<uint16_t, false, false, true>(a, st) : backward_for<float, false, false, true>(a, st);
+}
 
 int64_t norm_partial_rows(int64_t rows, int64_t cols) {
   const int64_t per = cols > kRegisterCols ? 1 : rows_at_once(cols, kBackThreads);

@@ -107,10 +107,29 @@ struct NormGradArgs {
   float* partials;      // norm_partial_rows() rows of cols floats (twice that with dbias)
   int64_t rows, cols, lddy, ldx, lddx;
   int32_t accumulate;
+  const void* dh;       // launch_add_norm_backward only: added to dx
+  int64_t lddh;
 };
 // Rows of per-workgroup partial sums of dweight that a backward pass writes.
 int64_t norm_partial_rows(int64_t rows, int64_t cols);
 hipError_t launch_norm_backward(int bf16, int layer, const NormGradArgs& a, hipStream_t st);
+
+// The residual's addition, the RMS norm of the sum and its FP8 forms: first h and
+// rstd of every row, then the forms of h rstd weight, tile by tile.
+struct AddNormArgs {
+  const void* x;
+  const void* residual;   // nullable: h is x, and not written
+  const float* weight;
+  void* h;
+  float* rstd;
+  int64_t rows, cols, ldx, ldr, ldh;
+  float eps;
+};
+hipError_t launch_add_norm_rows(int bf16, const AddNormArgs& a, hipStream_t st);
+// out.x, out.ldx: h.
+hipError_t launch_norm_quantize(int bf16, const QuantArgs& out, const float* weight, const float* rstd, hipStream_t st);
+// norm_backward of an RMS norm without bias, whose dx also takes dh.
+hipError_t launch_add_norm_backward(int bf16, const NormGradArgs& a, hipStream_t st);
 
 // Checks one FP8 operand; `whose` names it in the error text.
 int check_fp8_matrix(const muonh_fp8_matrix& m, const char* whose);

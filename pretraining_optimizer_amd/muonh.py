@@ -125,6 +125,33 @@ class muonh_attention_grad_args(ctypes.Structure):
                 ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
 
 
+class muonh_add_norm_args(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("h", ctypes.c_void_p), ("rstd", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("ldx", ctypes.c_int64), ("ld_residual", ctypes.c_int64),
+                ("ldh", ctypes.c_int64), ("dtype", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class muonh_add_norm_grad_args(ctypes.Structure):
+    _fields_ = [("g", muonh_norm_grad_args), ("dh", ctypes.c_void_p), ("ld_dh", ctypes.c_int64)]
+
+
+class muonh_embedding_args(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_void_p), ("table", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("count", ctypes.c_int64), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("ld_table", ctypes.c_int64), ("ld_out", ctypes.c_int64), ("token_bytes", ctypes.c_int32),
+                ("table_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class muonh_embedding_grad_args(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_void_p), ("dout", ctypes.c_void_p), ("dtable", ctypes.c_void_p),
+                ("count", ctypes.c_int64), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("ld_dout", ctypes.c_int64), ("ld_table", ctypes.c_int64), ("token_bytes", ctypes.c_int32),
+                ("dout_dtype", ctypes.c_int32), ("table_dtype", ctypes.c_int32), ("accumulate", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("reserved", ctypes.c_int32), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t)]
+
+
 _libs = {}
 
 # (name, restype, argtypes)
@@ -180,6 +207,13 @@ _SIGNATURES = [
     ("muonh_norm_backward_workspace", ctypes.c_int, [ctypes.c_int64, ctypes.c_int64,
                                                      ctypes.POINTER(ctypes.c_size_t)]),
     ("muonh_norm_backward", ctypes.c_int, [ctypes.POINTER(muonh_norm_grad_args), ctypes.c_void_p]),
+    ("muonh_add_norm_quantize", ctypes.c_int, [ctypes.POINTER(muonh_add_norm_args), ctypes.POINTER(muonh_fp8_matrix),
+                                               ctypes.POINTER(muonh_fp8_matrix), ctypes.c_void_p]),
+    ("muonh_add_norm_backward", ctypes.c_int, [ctypes.POINTER(muonh_add_norm_grad_args), ctypes.c_void_p]),
+    ("muonh_embedding_forward", ctypes.c_int, [ctypes.POINTER(muonh_embedding_args), ctypes.c_void_p]),
+    ("muonh_embedding_backward_workspace", ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
+                                                          ctypes.POINTER(ctypes.c_size_t)]),
+    ("muonh_embedding_backward", ctypes.c_int, [ctypes.POINTER(muonh_embedding_grad_args), ctypes.c_void_p]),
     ("muonh_attention_forward", ctypes.c_int, [ctypes.POINTER(muonh_attention_args), ctypes.c_void_p]),
     ("muonh_attention_backward_workspace", ctypes.c_int, [ctypes.POINTER(muonh_attention_args),
                                                           ctypes.POINTER(ctypes.c_size_t)]),

@@ -1,5 +1,5 @@
-"""ctypes binding of the block-scaled FP8 operators, the norms and the attention
-(argument marshalling only; the work runs in the library's HIP kernels).
+"""ctypes binding of the block-scaled FP8 operators, the norms, the attention and
+the embedding (argument marshalling only; the work runs in the library's HIP kernels).
 
 One linear layer y = x W^T, its gradients and the step of its weight:
 
@@ -19,8 +19,9 @@ from __future__ import annotations
 import ctypes
 from typing import Optional
 
-from .muonh import (MUONH_BF16, MUONH_F32, _check, _record, load_library, muonh_attention_args,
-                    muonh_attention_grad_args, muonh_fp8_matrix, muonh_norm_args, muonh_norm_grad_args)
+from .muonh import (MUONH_BF16, MUONH_F32, _check, _record, load_library, muonh_add_norm_args,
+                    muonh_add_norm_grad_args, muonh_attention_args, muonh_attention_grad_args, muonh_embedding_args,
+                    muonh_embedding_grad_args, muonh_fp8_matrix, muonh_norm_args, muonh_norm_grad_args)
 
 # The smallest calls are bound by this module: a launch takes about 3.5 us,
 # a tensor 1.5 us, torch.cuda.current_stream() 2.8 us.  So the library and
@@ -353,6 +354,197 @@ def norm_backward(dy, x, weight, mean, rstd, kind: str = "rms", bias: bool = Fal
     if rc:
         _check(rc, "muonh_norm_backward")
     return dx, dweight, dbias
+
+
+def add_norm_quantize(x, residual, weight, eps: float = 1e-6, form: str = "row", h=None, out: Optional[Fp8Matrix] = None,
+                      out_t: Optional[Fp8Matrix] = None, stream=None):
+    """(h, rstd, q): h = x + residual, and the RMS norm of h in block-scaled FP8.
+
+    x, residual : float32 or bfloat16 [rows, cols], contiguous rows of any pitch;
+                  residual may be None, h is then x itself
+    weight      : float32 [cols]
+    form        : "row", "col" or "both", as fp8_quantize takes it; q is what that returns
+    h           : memory of the sum (x's type); may be x or residual
+    out, out_t  : operands to write instead of new ones (row form, column form)
+    The norm is not rounded before it is quantised, and h is (to x's type) before it is
+    normalised.  h and rstd are what add_norm_backward needs.
+    """
+    if form not in ("row", "col", "both"):
+        raise ValueError("form must be 'row', 'col' or 'both'")
+    if _torch is None:
+        _setup()
+    code = _code(x, "x")
+    rows, cols, ldx = _matrix(x, "x")
+    ldr = ldh = cols
+    if residual is not None:
+        if residual.shape != x.shape or residual.dtype != x.dtype:
+            raise ValueError("residual: shape or dtype differs from x")
+        ldr = _pitch(residual, rows, cols, "residual")
+    elif h is not None:
+        raise ValueError("h is x where there is no residual")
+    _vector(weight, cols, "weight")
+    if (out is not None and form == "col") or (out_t is not None and form == "row"):
+        raise ValueError("out is the row form and out_t the column form")
+    dev = _here(x, residual, weight, h, None if out is None else out.data, None if out_t is None else out_t.data)
+    q = qt = None
+    if form != "col":
+        q = Fp8Matrix.empty(rows, cols, 1, x.device, stream) if out is None else out
+        if (q.rows, q.cols, q.block_rows) != (rows, cols, 1):
+            raise ValueError("out: shape or block_rows differs")
+    if form != "row":
+        qt = Fp8Matrix.empty(cols, rows, 1, x.device, stream) if out_t is None else out_t
+        if (qt.rows, qt.cols, qt.block_rows) != (cols, rows, 1):
+            raise ValueError("out_t: shape or block_rows differs")
+    if residual is not None:
+        h, ldh = _result(h, x, rows, cols, "h", stream)
+    rstd = _like(weight, rows, stream)
+    args = muonh_add_norm_args(x.data_ptr(), None if residual is None else residual.data_ptr(), weight.data_ptr(),
+                               None if residual is None else h.data_ptr(), rstd.data_ptr(), rows, cols, ldx, ldr, ldh,
+                               code, eps)
+    if stream is not None:
+        _record(stream, [t for t in (x, residual, weight, h, rstd) if t is not None] +
+                [t for m in (q, qt) if m is not None for t in (m.data, m.scale)])
+    rc = _lib.muonh_add_norm_quantize(ctypes.byref(args), None if q is None else ctypes.byref(q._desc),
+                                      None if qt is None else ctypes.byref(qt._desc), _stream(stream, dev))
+    if rc:
+        _check(rc, "muonh_add_norm_quantize")
+    return x if residual is None else h, rstd, (q, qt) if form == "both" else q if qt is None else qt
+
+
+def add_norm_backward(dy, dh, h, weight, rstd, dx=None, dweight=None, accumulate: bool = False, stream=None):
+    """(dx, dweight) of add_norm_quantize: dx, the gradient of x and of residual, is
+    that of the norm plus dh, the gradient which reaches h by the residual stream.
+
+    dy      : the gradient of the norm's output, in h's type
+    h, rstd : the forward pass's results
+    dx      : memory of dx; may be dh, dy or h itself
+    dweight : float32 [cols] to write, or with accumulate to add to
+    """
+    if _torch is None:
+        _setup()
+    code = _code(h, "h")
+    rows, cols, ldh = _matrix(h, "h")
+    for t, what in ((dy, "dy"), (dh, "dh")):
+        if t.shape != h.shape or t.dtype != h.dtype:
+            raise ValueError(f"{what}: shape or dtype differs from h")
+    ld_dy, ld_dh = _pitch(dy, rows, cols, "dy"), _pitch(dh, rows, cols, "dh")
+    _vector(weight, cols, "weight")
+    _vector(rstd, rows, "rstd")
+    if accumulate and dweight is None:
+        raise ValueError("accumulate needs dweight")
+    if dweight is not None:
+        _vector(dweight, cols, "dweight")
+    dev = _here(dy, dh, h, weight, rstd, dx, dweight)
+    dx, ld_dx = _result(dx, h, rows, cols, "dx", stream)
+    if dweight is None:
+        dweight = _like(weight, cols, stream)
+    need = ctypes.c_size_t()
+    rc = _lib.muonh_norm_backward_workspace(rows, cols, ctypes.byref(need))
+    if rc:
+        _check(rc, "muonh_norm_backward_workspace")
+    need = need.value
+    ws = _like(weight, need // 4, stream, result=False) if need else None
+    args = muonh_add_norm_grad_args(muonh_norm_grad_args(
+        dy.data_ptr(), h.data_ptr(), weight.data_ptr(), None, rstd.data_ptr(), dx.data_ptr(), dweight.data_ptr(), None,
+        rows, cols, ld_dy, ldh, ld_dx, code, NORM_KINDS["rms"], 1 if accumulate else 0, 0,
+        None if ws is None else ws.data_ptr(), need), dh.data_ptr(), ld_dh)
+    if stream is not None:
+        _record(stream, [t for t in (dy, dh, h, weight, rstd, dx, dweight, ws) if t is not None])
+    rc = _lib.muonh_add_norm_backward(ctypes.byref(args), _stream(stream, dev))
+    if rc:
+        _check(rc, "muonh_add_norm_backward")
+    return dx, dweight
+
+
+def _tokens(tokens) -> int:
+    """Bytes of a token."""
+    if tokens.dtype is not _torch.int64 and tokens.dtype is not _torch.int32:
+        raise TypeError(f"tokens: dtype must be int32 or int64, got {tokens.dtype}")
+    if tokens.dim() != 1 or not tokens.is_contiguous():
+        raise ValueError("tokens: a contiguous vector is required")
+    return tokens.element_size()
+
+
+def embedding_forward(tokens, table, scale: float = 1.0, out=None, out_dtype=None, stream=None):
+    """scale * table[tokens]: [tokens, cols].
+
+    tokens : int32 or int64 vector; one outside the table (padding, such as -1) gives zeros
+    table  : float32 or bfloat16 [rows, cols], contiguous rows of any pitch
+    out    : memory of the result (float32 or bfloat16); a new one of out_dtype (bfloat16
+             if None) if not given
+    """
+    if _torch is None:
+        _setup()
+    size = _tokens(tokens)
+    code = _code(table, "table")
+    rows, cols, ld = _matrix(table, "table")
+    n = len(tokens)
+    if out is None:
+        out = _empty((n, cols), out_dtype or _torch.bfloat16, table.device, stream)
+        ld_out = cols
+    else:
+        if out.shape != (n, cols) or (out_dtype is not None and out.dtype != out_dtype):
+            raise ValueError(f"out: a matrix of shape {(n, cols)} and the asked dtype is required")
+        ld_out = _pitch(out, n, cols, "out")
+    out_code = _code(out, "out")
+    dev = _here(tokens, table, out)
+    args = muonh_embedding_args(tokens.data_ptr(), table.data_ptr(), out.data_ptr(), n, rows, cols, ld, ld_out, size,
+                                code, out_code, scale)
+    if stream is not None:
+        _record(stream, [tokens, table, out])
+    rc = _lib.muonh_embedding_forward(ctypes.byref(args), _stream(stream, dev))
+    if rc:
+        _check(rc, "muonh_embedding_forward")
+    return out
+
+
+def embedding_backward(tokens, dout, rows: int, scale: float = 1.0, dtable=None, out_dtype=None, accumulate: bool = False,
+                       stream=None):
+    """The table's gradient [rows, cols] from that of the lookup's output, dense:
+    scale times the sum of dout's rows over each token's places.
+
+    rows       : of the table; a token outside it (padding) adds nothing
+    dout       : float32 or bfloat16 [tokens, cols], contiguous rows of any pitch
+    dtable     : memory of the gradient (float32 or bfloat16), which AdamW.step takes;
+                 a new one of out_dtype (float32 if None) if not given
+    accumulate : add to what dtable holds
+    """
+    if _torch is None:
+        _setup()
+    size = _tokens(tokens)
+    code = _code(dout, "dout")
+    n, cols, ld = _matrix(dout, "dout")
+    if n != len(tokens):
+        raise ValueError(f"dout: {len(tokens)} rows are required")
+    if dtable is None:
+        if accumulate:
+            raise ValueError("accumulate needs dtable")
+        dtable = _empty((rows, cols), out_dtype or _torch.float32, dout.device, stream)
+        ld_table = cols
+    else:
+        if dtable.shape != (rows, cols) or (out_dtype is not None and dtable.dtype != out_dtype):
+            raise ValueError(f"dtable: a matrix of shape {(rows, cols)} and the asked dtype is required")
+        ld_table = _pitch(dtable, rows, cols, "dtable")
+    table_code = _code(dtable, "dtable")
+    dev = _here(tokens, dout, dtable)
+    need = ctypes.c_size_t()
+    rc = _lib.muonh_embedding_backward_workspace(n, rows, cols, ctypes.byref(need))
+    if rc:
+        _check(rc, "muonh_embedding_backward_workspace")
+    need = need.value
+    ws = None
+    if need:
+        make = lambda: _torch.empty(need, dtype=_torch.uint8, device=dout.device)  # noqa: E731
+        ws = make() if stream is None else _on(stream, make, False)
+    args = muonh_embedding_grad_args(tokens.data_ptr(), dout.data_ptr(), dtable.data_ptr(), n, rows, cols, ld, ld_table,
+                                     size, code, table_code, 1 if accumulate else 0, scale, 0,
+                                     None if ws is None else ws.data_ptr(), need)
+    if stream is not None:
+        _record(stream, [t for t in (tokens, dout, dtable, ws) if t is not None])
+    rc = _lib.muonh_embedding_backward(ctypes.byref(args), _stream(stream, dev))
+    if rc:
+        _check(rc, "muonh_embedding_backward")
+    return dtable
 
 
 def _heads(t, tokens: int, heads: int, dim: int, what: str) -> int:
