@@ -259,7 +259,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_forward_kernel(Attentio
   const float c = p.scale * kLog2e;
 
   // N blocks of 32 keys; DIAG: the last is the rows' own.
-  auto step = [&](uint8_t* tile, auto n, auto diag) {
+  auto step = [&](uint8_t* tile, auto n, auto diag) __attribute__((always_inline)) {
     constexpr int N = decltype(n)::value;
     constexpr bool DIAG = decltype(diag)::value;
     f32x16_t s[N];
@@ -332,24 +332,33 @@ __global__ __launch_bounds__(kThreads, 2) void attention_forward_kernel(Attentio
         }
       }
   };
-  auto use = [&](uint8_t* tile, int j) {
-    const int first = j * kTile;
-    if (row >= at.len || first > row) return;
-    if (first == row) step(tile, std::integral_constant<int, 1>{}, std::true_type{});
-    else if (first + 32 == row) step(tile, std::integral_constant<int, 2>{}, std::true_type{});
-    else step(tile, std::integral_constant<int, 2>{}, std::false_type{});
-  };
-  auto trip = [&](uint8_t* tile, uint8_t* next, int j) {
-    arrive();   // the tile is there, and every wavefront has read the other
-    if (j + 1 < tiles) {
-      load_k(k, (j + 1) * kTile, next, wave);
-      load_v(v, (j + 1) * kTile, next + kBytes, wave);
+  auto fetch = [&](uint8_t* tile, int j) __attribute__((always_inline)) {
+    if (j < tiles) {
+      load_k(k, j * kTile, tile, wave);
+      load_v(v, j * kTile, tile + kBytes, wave);
     }
-    use(tile, j);
   };
-  for (int j = 0; j < tiles; j += 2) {
-    trip(slot0, slot1, j);
-    if (j + 1 < tiles) trip(slot1, slot0, j + 1);
+  // The tiles before the workgroup's rows are seen whole by all of them, an even number.
+  constexpr std::integral_constant<int, 1> one{};
+  constexpr std::integral_constant<int, 2> two{};
+  const int whole = at.row / kTile;
+  for (int j = 0; j < whole; j += 2) {
+    arrive();   // the tile is there, and every wavefront has read the other
+    fetch(slot1, j + 1);
+    step(slot0, two, std::false_type{});
+    arrive();
+    fetch(slot0, j + 2);
+    step(slot1, two, std::false_type{});
+  }
+  arrive();
+  fetch(slot1, whole + 1);
+  if (wave == 0) step(slot0, one, std::true_type{});
+  else if (wave == 1) step(slot0, two, std::true_type{});
+  else step(slot0, two, std::false_type{});
+  if (whole + 1 < tiles) {
+    arrive();
+    if (wave == 2) step(slot1, one, std::true_type{});
+    else if (wave == 3) step(slot1, two, std::true_type{});
   }
 
   sum = pair_sum(sum);
@@ -414,7 +423,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttentionGrad
   for (int dt = 0; dt < DP / 32; ++dt) acc[dt] = splat(0.0f);
   const float c = p.scale * kLog2e;
 
-  auto block = [&](uint8_t* tile, int b, auto diag) {
+  auto block = [&](uint8_t* tile, int b, auto diag) __attribute__((always_inline)) {
     f32x16_t s = splat(0.0f), ds = splat(delta);
 #pragma unroll
     for (int e = 0; e < DP / 16; ++e) s = mfma(read.rows(tile, b, e), fq[e], s);
@@ -432,23 +441,38 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttentionGrad
       for (int dt = 0; dt < DP / 32; ++dt) acc[dt] = mfma(read.columns(tile, b, h, dt), f, acc[dt]);
     }
   };
-  auto trip = [&](uint8_t* tile, uint8_t* next, int j) {
-    arrive();
-    if (j + 1 < tiles) {
-      load_k(k, (j + 1) * kTile, next, wave);
-      load_v(v, (j + 1) * kTile, next + kBytes, wave);
-    }
-    if (row >= at.len) return;
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const int first = j * kTile + 32 * b;
-      if (first < row) block(tile, b, std::false_type{});
-      else if (first == row) block(tile, b, std::true_type{});
+  auto fetch = [&](uint8_t* tile, int j) __attribute__((always_inline)) {
+    if (j < tiles) {
+      load_k(k, j * kTile, tile, wave);
+      load_v(v, j * kTile, tile + kBytes, wave);
     }
   };
-  for (int j = 0; j < tiles; j += 2) {
-    trip(slot0, slot1, j);
-    if (j + 1 < tiles) trip(slot1, slot0, j + 1);
+  auto full = [&](uint8_t* tile) __attribute__((always_inline)) {
+    block(tile, 0, std::false_type{});
+    block(tile, 1, std::false_type{});
+  };
+  // as in the forward pass
+  const int whole = at.row / kTile;
+  for (int j = 0; j < whole; j += 2) {
+    arrive();
+    fetch(slot1, j + 1);
+    full(slot0);
+    arrive();
+    fetch(slot0, j + 2);
+    full(slot1);
+  }
+  arrive();
+  fetch(slot1, whole + 1);
+  if (wave >= 2) {
+    full(slot0);
+  } else {
+    if (wave == 1) block(slot0, 0, std::false_type{});
+    block(slot0, wave, std::true_type{});
+  }
+  if (whole + 1 < tiles) {
+    arrive();
+    if (wave == 3) block(slot1, 0, std::false_type{});
+    if (wave >= 2) block(slot1, wave - 2, std::true_type{});
   }
   if (!live) return;
   store_rows<DP>(g.dq + (at.start + row) * g.lddq + head * p.dim, g.lddq, p.dim, acc, p.scale, lane);
@@ -457,7 +481,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttentionGrad
 // Gradients of k and v: a wavefront holds 32 rows of both and passes over the rows of
 // q and dout that see them, head by head of the group.
 template <int DP>
-__global__ __launch_bounds__(kThreads, 2) void attention_dkv_kernel(AttentionGradArgs g) {
+__global__ __launch_bounds__(kThreads, DP > 64 ? 1 : 2) void attention_dkv_kernel(AttentionGradArgs g) {
   const AttentionArgs& p = g.a;
   constexpr int kBytes = kTile * DP * 2;
   __shared__ __attribute__((aligned(1024))) uint8_t slot0[2 * kBytes], slot1[2 * kBytes];
@@ -479,7 +503,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dkv_kernel(AttentionGra
   const int first_tile = at.row / kTile, end_tile = (at.len + kTile - 1) / kTile;
   // Rows behind the end arrive as zeros: P = exp 0, but dout, delta and q are 0.
   int lh = 0, lt = first_tile;   // the next tile to load
-  auto load = [&](uint8_t* tile, float (&rows)[2][kTile]) {
+  auto load = [&](uint8_t* tile, float (&rows)[2][kTile]) __attribute__((always_inline)) {
     load_q(q, lt * kTile, tile, wave);
     load_d(d, lt * kTile, tile + kBytes, wave);
     if (wave < 2) {
@@ -504,7 +528,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dkv_kernel(AttentionGra
   for (int dt = 0; dt < DP / 32; ++dt) dk[dt] = dv[dt] = splat(0.0f);
   const float c = p.scale * kLog2e;
 
-  auto block = [&](uint8_t* tile, const float (&rows)[2][kTile], int b, auto diag) {
+  auto block = [&](uint8_t* tile, const float (&rows)[2][kTile], int b, auto diag) __attribute__((always_inline)) {
     f32x16_t s = splat(0.0f), ds;
     f32x4_t lse[4];
 #pragma unroll
@@ -533,24 +557,42 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dkv_kernel(AttentionGra
       for (int dt = 0; dt < DP / 32; ++dt) dk[dt] = mfma(read.columns(tile, b, h, dt), fs, dk[dt]);
     }
   };
-  const int per_head = end_tile - first_tile, trips = per_head * group;
-  int tile_row = first_tile * kTile;
-  auto trip = [&](uint8_t* tile, const float (&rows)[2][kTile], uint8_t* next, float (&next_rows)[2][kTile], int j) {
-    arrive();
-    if (j + 1 < trips) load(next, next_rows);
-    if (row < at.len) {
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const int first = tile_row + 32 * b;
-        if (first > row) block(tile, rows, b, std::false_type{});
-        else if (first == row) block(tile, rows, b, std::true_type{});
-      }
-    }
-    tile_row = tile_row + kTile < at.len ? tile_row + kTile : first_tile * kTile;
+  auto fetch = [&](uint8_t* tile, float (&rows)[2][kTile]) __attribute__((always_inline)) {
+    if (lh < group) load(tile, rows);
   };
-  for (int j = 0; j < trips; j += 2) {
-    trip(slot0, rows0, slot1, rows1, j);
-    if (j + 1 < trips) trip(slot1, rows1, slot0, rows0, j + 1);
+  auto full = [&](uint8_t* tile, const float (&rows)[2][kTile]) __attribute__((always_inline)) {
+    block(tile, rows, 0, std::false_type{});
+    block(tile, rows, 1, std::false_type{});
+  };
+  // Head by head: the two tiles of the workgroup's own rows, then the tiles behind
+  // them, which all of its rows are seen by.  The heads' tiles take the slots in turn.
+  const int tiles = end_tile - first_tile;
+  auto own = [&](uint8_t* tile, const float (&rows)[2][kTile], int j) __attribute__((always_inline)) {
+    if (j == 0) {
+      if (wave >= 2) return;
+      block(tile, rows, wave, std::true_type{});
+      if (wave == 0) block(tile, rows, 1, std::false_type{});
+    } else {
+      if (wave < 2) return full(tile, rows);
+      block(tile, rows, wave - 2, std::true_type{});
+      if (wave == 2) block(tile, rows, 1, std::false_type{});
+    }
+  };
+  auto use = [&](uint8_t* tile, const float (&rows)[2][kTile], int j) __attribute__((always_inline)) {
+    if (j < 2) own(tile, rows, j);
+    else full(tile, rows);
+  };
+  const int trips = tiles * group;
+  for (int j = 0, at_tile = 0; j < trips; j += 2) {
+    arrive();
+    fetch(slot1, rows1);
+    use(slot0, rows0, at_tile);
+    at_tile = at_tile + 1 < tiles ? at_tile + 1 : 0;
+    if (j + 1 == trips) break;
+    arrive();
+    fetch(slot0, rows0);
+    use(slot1, rows1, at_tile);
+    at_tile = at_tile + 1 < tiles ? at_tile + 1 : 0;
   }
   if (row + (lane & 31) >= at.len) return;
   const int64_t t = at.start + row;
