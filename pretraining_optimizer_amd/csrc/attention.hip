@@ -28,6 +28,7 @@
 #include "attention.h"
 
 #include <type_traits>
+#include <utility>
 
 #include "device_util.h"
 
@@ -113,49 +114,70 @@ template <int DP>
 struct TileLoad {
   static constexpr int kRow = DP * 2, kChunks = DP / 8, kStep = 4096 / kRow;   // rows per round of the wavefronts
   int voff, step;
-  __device__ __forceinline__ TileLoad(const Rows& t, int wave, int lane) {
+  __device__ __forceinline__ TileLoad(int64_t ld, int dim, int wave, int lane) {
     const int row = wave * (kStep / 4) + lane / kChunks, chunk = (lane % kChunks) ^ swizzle<DP>(row);
-    voff = chunk * 8 < t.dim ? (int)(row * t.ld * 2) + chunk * 16 : kBehind;
-    step = (int)(kStep * t.ld * 2);
+    voff = chunk * 8 < dim ? (int)(row * ld * 2) + chunk * 16 : kBehind;
+    step = (int)(kStep * ld * 2);
   }
-  __device__ __forceinline__ void operator()(const Rows& t, int row, uint8_t* slot, int wave) const {
+  __device__ __forceinline__ void operator()(const Rows& t, int row, MUONH_LDS uint8_t* slot, int wave) const {
     const __amdgpu_buffer_rsrc_t r = t.at(row, kTile);
 #pragma unroll
     for (int i = 0; i < kTile / kStep; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (MUONH_LDS void*)((MUONH_LDS uint8_t*)slot + (i * 4 + wave) * 1024),
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (MUONH_LDS void*)(slot + (i * 4 + wave) * 1024),
                                                16, voff, i * step, 0, 0);
   }
 };
 
-// Operands out of a tile in LDS.
+// Operands out of a tile in LDS.  Within a row a step or a block of columns only changes
+// bits of the chunk's number, so an address is one exclusive or from the lane's first.
 template <int DP>
 struct TileRead {
   static constexpr int kRow = DP * 2;
-  int row, tr;    // byte offsets of the lane's row and of its transposing reads
-  int chunk, trc; // swizzled chunk of step 0, and of the first reads
+  int row, tr;    // byte offsets of the lane's first operand and transposing reads
   __device__ __forceinline__ explicit TileRead(int lane) {
-    row = (lane & 31) * kRow;
-    chunk = (lane >> 5) ^ swizzle<DP>(lane & 15);
+    row = (lane & 31) * kRow + (((lane >> 5) ^ swizzle<DP>(lane & 15)) << 4);
     const int r = 4 * (lane >> 5) + ((lane & 15) >> 2);
-    tr = r * kRow + (lane & 1) * 8;
-    trc = (2 * ((lane >> 4) & 1) + ((lane >> 1) & 1)) ^ swizzle<DP>(r);
+    tr = r * kRow + (((2 * ((lane >> 4) & 1) + ((lane >> 1) & 1)) ^ swizzle<DP>(r)) << 4) + (lane & 1) * 8;
   }
   // Rows of block `sub`, columns 16 step + 8 (l / 32) .. + 7.
-  __device__ __forceinline__ u32x4_t rows(const uint8_t* tile, int sub, int step) const {
-    return *reinterpret_cast<const u32x4_t*>(tile + sub * 32 * kRow + row + ((chunk ^ (2 * step)) << 4));
+  __device__ __forceinline__ u32x4_t rows(MUONH_LDS uint8_t* tile, int sub, int step) const {
+    return *reinterpret_cast<MUONH_LDS u32x4_t*>(tile + sub * 32 * kRow + (row ^ (step << 5)));
   }
   // Column 32 dt + l % 32 of block `sub`, rows 16 s + 4 (l / 32) .. + 3 and 8 further.
-  __device__ __forceinline__ u32x4_t columns(uint8_t* tile, int sub, int s, int dt) const {
-    MUONH_LDS uint8_t* t = (MUONH_LDS uint8_t*)tile + (sub * 32 + 16 * s) * kRow + tr;
+  __device__ __forceinline__ u32x4_t columns(MUONH_LDS uint8_t* tile, int sub, int s, int dt) const {
+    MUONH_LDS uint8_t* t = tile + (sub * 32 + 16 * s) * kRow;
     const u32x2_t lo = __builtin_bit_cast(
-        u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((MUONH_LDS i16x4_t*)(t + ((trc ^ (4 * dt)) << 4))));
+        u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((MUONH_LDS i16x4_t*)(t + (tr ^ (dt << 6)))));
     // 8 rows further the swizzle differs in one bit
     const u32x2_t hi = __builtin_bit_cast(
-        u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                     (MUONH_LDS i16x4_t*)(t + 8 * kRow + ((trc ^ (4 * dt) ^ 2) << 4))));
+        u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((MUONH_LDS i16x4_t*)(t + 8 * kRow + (tr ^ (dt << 6) ^ 32))));
     return u32x4_t{lo[0], lo[1], hi[0], hi[1]};
   }
 };
+
+// Instruction order of N pairs of a product's steps whose operands come out of LDS: reads
+// stay two pairs ahead.
+constexpr int kSgMfma = 0x008, kSgDsRead = 0x100;
+template <int N>
+__device__ __forceinline__ void order_pairs() {
+  __builtin_amdgcn_sched_group_barrier(kSgDsRead, 4, 0);
+#pragma unroll
+  for (int i = 0; i < N - 2; ++i) {
+    __builtin_amdgcn_sched_group_barrier(kSgMfma, 2, 0);
+    __builtin_amdgcn_sched_group_barrier(kSgDsRead, 2, 0);
+  }
+  __builtin_amdgcn_sched_group_barrier(kSgMfma, 4, 0);
+}
+
+// f(0), .. f(N - 1) with constants.
+template <typename F, int... I>
+__device__ __forceinline__ void each_of(F&& f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void each(F&& f) {
+  each_of(f, std::make_integer_sequence<int, N>{});
+}
 
 // The wavefront's 32 rows from `row` on as an operand held in registers: lane l has
 // row l % 32, columns 16 s + 8 (l / 32) .. + 7 of step s.
@@ -232,7 +254,8 @@ __device__ __forceinline__ bool has_special(u32x4_t v) {
 template <int DP>
 __global__ __launch_bounds__(kThreads, 2) void attention_forward_kernel(AttentionArgs p) {
   constexpr int kBytes = kTile * DP * 2;
-  __shared__ __attribute__((aligned(1024))) uint8_t slot0[2 * kBytes], slot1[2 * kBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds0[2 * kBytes], lds1[2 * kBytes];
+  MUONH_LDS uint8_t *const slot0 = (MUONH_LDS uint8_t*)lds0, *const slot1 = (MUONH_LDS uint8_t*)lds1;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int group = p.heads / p.kv_heads;
   const int64_t item = item_of(blockIdx.x, gridDim.x), per = (int64_t)p.blocks * group;
@@ -245,7 +268,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_forward_kernel(Attentio
   const Rows v{p.v + at.start * p.ldv + kv * p.dim, p.ldv, at.len, p.dim};
   const int row = at.row + 32 * wave;   // the wavefront's first
   const int tiles = (min(at.len, at.row + kBlock) + kTile - 1) / kTile;
-  const TileLoad<DP> load_k(k, wave, lane), load_v(v, wave, lane);
+  const TileLoad<DP> load_k(p.ldk, p.dim, wave, lane), load_v(p.ldv, p.dim, wave, lane);
   const TileRead<DP> read(lane);
   load_k(k, 0, slot0, wave);
   load_v(v, 0, slot0 + kBytes, wave);
@@ -259,16 +282,17 @@ __global__ __launch_bounds__(kThreads, 2) void attention_forward_kernel(Attentio
   const float c = p.scale * kLog2e;
 
   // N blocks of 32 keys; DIAG: the last is the rows' own.
-  auto step = [&](uint8_t* tile, auto n, auto diag) __attribute__((always_inline)) {
+  auto step = [&](MUONH_LDS uint8_t* tile, auto n, auto diag) __attribute__((always_inline)) {
     constexpr int N = decltype(n)::value;
     constexpr bool DIAG = decltype(diag)::value;
     f32x16_t s[N];
 #pragma unroll
-    for (int b = 0; b < N; ++b) {
-      s[b] = splat(0.0f);
+    for (int b = 0; b < N; ++b) s[b] = splat(0.0f);
 #pragma unroll
-      for (int d = 0; d < DP / 16; ++d) s[b] = mfma(read.rows(tile, b, d), fq[d], s[b]);
-    }
+    for (int d = 0; d < DP / 16; ++d)
+#pragma unroll
+      for (int b = 0; b < N; ++b) s[b] = mfma(read.rows(tile, b, d), fq[d], s[b]);
+    if constexpr (N == 2) order_pairs<DP / 16>();
     if constexpr (DIAG) {
 #pragma unroll
       for (int r = 0; r < 16; ++r)
@@ -332,7 +356,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_forward_kernel(Attentio
         }
       }
   };
-  auto fetch = [&](uint8_t* tile, int j) __attribute__((always_inline)) {
+  auto fetch = [&](MUONH_LDS uint8_t* tile, int j) __attribute__((always_inline)) {
     if (j < tiles) {
       load_k(k, j * kTile, tile, wave);
       load_v(v, j * kTile, tile + kBytes, wave);
@@ -374,7 +398,8 @@ template <int DP>
 __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttentionGradArgs g) {
   const AttentionArgs& p = g.a;
   constexpr int kBytes = kTile * DP * 2;
-  __shared__ __attribute__((aligned(1024))) uint8_t slot0[2 * kBytes], slot1[2 * kBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds0[2 * kBytes], lds1[2 * kBytes];
+  MUONH_LDS uint8_t *const slot0 = (MUONH_LDS uint8_t*)lds0, *const slot1 = (MUONH_LDS uint8_t*)lds1;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int group = p.heads / p.kv_heads;
   const int64_t item = item_of(blockIdx.x, gridDim.x), per = (int64_t)p.blocks * group;
@@ -389,7 +414,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttentionGrad
   const Rows d{g.dout + at.start * g.lddo + head * p.dim, g.lddo, at.len, p.dim};
   const int row = at.row + 32 * wave;
   const int tiles = (min(at.len, at.row + kBlock) + kTile - 1) / kTile;
-  const TileLoad<DP> load_k(k, wave, lane), load_v(v, wave, lane);
+  const TileLoad<DP> load_k(p.ldk, p.dim, wave, lane), load_v(p.ldv, p.dim, wave, lane);
   const TileRead<DP> read(lane);
   load_k(k, 0, slot0, wave);
   load_v(v, 0, slot0 + kBytes, wave);
@@ -423,12 +448,14 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttentionGrad
   for (int dt = 0; dt < DP / 32; ++dt) acc[dt] = splat(0.0f);
   const float c = p.scale * kLog2e;
 
-  auto block = [&](uint8_t* tile, int b, auto diag) __attribute__((always_inline)) {
+  auto block = [&](MUONH_LDS uint8_t* tile, int b, auto diag) __attribute__((always_inline)) {
     f32x16_t s = splat(0.0f), ds = splat(delta);
 #pragma unroll
-    for (int e = 0; e < DP / 16; ++e) s = mfma(read.rows(tile, b, e), fq[e], s);
-#pragma unroll
-    for (int e = 0; e < DP / 16; ++e) ds = mfma(read.rows(tile + kBytes, b, e), fd[e], ds);
+    for (int e = 0; e < DP / 16; ++e) {
+      s = mfma(read.rows(tile, b, e), fq[e], s);
+      ds = mfma(read.rows(tile + kBytes, b, e), fd[e], ds);
+    }
+    order_pairs<DP / 16>();
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
       ds[r] *= __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], c, lse));
@@ -441,13 +468,13 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttentionGrad
       for (int dt = 0; dt < DP / 32; ++dt) acc[dt] = mfma(read.columns(tile, b, h, dt), f, acc[dt]);
     }
   };
-  auto fetch = [&](uint8_t* tile, int j) __attribute__((always_inline)) {
+  auto fetch = [&](MUONH_LDS uint8_t* tile, int j) __attribute__((always_inline)) {
     if (j < tiles) {
       load_k(k, j * kTile, tile, wave);
       load_v(v, j * kTile, tile + kBytes, wave);
     }
   };
-  auto full = [&](uint8_t* tile) __attribute__((always_inline)) {
+  auto full = [&](MUONH_LDS uint8_t* tile) __attribute__((always_inline)) {
     block(tile, 0, std::false_type{});
     block(tile, 1, std::false_type{});
   };
@@ -480,12 +507,24 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttentionGrad
 
 // Gradients of k and v: a wavefront holds 32 rows of both and passes over the rows of
 // q and dout that see them, head by head of the group.
+//
+// One wavefront per SIMD has the registers for both sums (128), both operands (64) and
+// two blocks of scores, so a tile's two blocks are pipelined by hand: the 16 products of
+// block 1's S and dP run beside block 0's exponentials, those of block 0's sums beside
+// block 1's, a product (32 cycles) with one value's VALU work (24) at a time; operands
+// come out of LDS four products ahead, also over the tiles' border: three slots, the
+// barrier in the middle of a tile.
 template <int DP>
-__global__ __launch_bounds__(kThreads, DP > 64 ? 1 : 2) void attention_dkv_kernel(AttentionGradArgs g) {
+__global__ __launch_bounds__(kThreads, 1) void attention_dkv_kernel(AttentionGradArgs g) {
   const AttentionArgs& p = g.a;
-  constexpr int kBytes = kTile * DP * 2;
-  __shared__ __attribute__((aligned(1024))) uint8_t slot0[2 * kBytes], slot1[2 * kBytes];
-  __shared__ __attribute__((aligned(16))) float rows0[2][kTile], rows1[2][kTile];
+  constexpr int kBytes = kTile * DP * 2, kSteps = DP / 16, kCols = DP / 32;
+  constexpr int kPhase = 2 * kSteps;   // products of a block's scores, and of its sums
+  __shared__ __attribute__((aligned(1024))) uint8_t lds0[2 * kBytes], lds1[2 * kBytes], lds2[2 * kBytes];
+  __shared__ __attribute__((aligned(16))) float ldsr0[4 * kTile], ldsr1[4 * kTile], ldsr2[4 * kTile];
+  MUONH_LDS uint8_t *const slot0 = (MUONH_LDS uint8_t*)lds0, *const slot1 = (MUONH_LDS uint8_t*)lds1,
+                           *const slot2 = (MUONH_LDS uint8_t*)lds2;
+  MUONH_LDS float *const rows0 = (MUONH_LDS float*)ldsr0, *const rows1 = (MUONH_LDS float*)ldsr1,
+                         *const rows2 = (MUONH_LDS float*)ldsr2;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int group = p.heads / p.kv_heads;
   const int64_t item = item_of(blockIdx.x, gridDim.x);
@@ -495,105 +534,169 @@ __global__ __launch_bounds__(kThreads, DP > 64 ? 1 : 2) void attention_dkv_kerne
 
   const Rows k{p.k + at.start * p.ldk + kv * p.dim, p.ldk, at.len, p.dim};
   const Rows v{p.v + at.start * p.ldv + kv * p.dim, p.ldv, at.len, p.dim};
-  Rows q{p.q + at.start * p.ldq + kv * group * p.dim, p.ldq, at.len, p.dim};
-  Rows d{g.dout + at.start * g.lddo + kv * group * p.dim, g.lddo, at.len, p.dim};
   const int row = at.row + 32 * wave;
-  const TileLoad<DP> load_q(q, wave, lane), load_d(d, wave, lane);
+  const TileLoad<DP> load_q(p.ldq, p.dim, wave, lane), load_d(g.lddo, p.dim, wave, lane);
   const TileRead<DP> read(lane);
-  const int first_tile = at.row / kTile, end_tile = (at.len + kTile - 1) / kTile;
-  // Rows behind the end arrive as zeros: P = exp 0, but dout, delta and q are 0.
-  int lh = 0, lt = first_tile;   // the next tile to load
-  auto load = [&](uint8_t* tile, float (&rows)[2][kTile]) __attribute__((always_inline)) {
-    load_q(q, lt * kTile, tile, wave);
-    load_d(d, lt * kTile, tile + kBytes, wave);
-    if (wave < 2) {
-      const float* src = (wave ? g.row_delta : g.row_lse) + (kv * group + lh) * (int64_t)p.tokens + at.start + lt * kTile;
-      const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-          const_cast<float*>(src), (short)0, min(kTile, at.len - lt * kTile) * 4, kBufferConfig);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (MUONH_LDS void*)((MUONH_LDS float*)rows[wave]), 4, lane * 4, 0, 0, 0);
-    }
-    if (++lt == end_tile) {
-      lt = first_tile;
-      ++lh;
-      q.base += p.dim;
-      d.base += p.dim;
-    }
+  // The tiles of q and dout: first those of the workgroup's own rows, head by head, then
+  // the whole ones behind them, head by head.  Rows behind the end arrive as zeros: P =
+  // exp 0, but dout, delta and q are 0.  Behind the last tile zeros are loaded, from nowhere.
+  const int first_tile = at.row / kTile, tiles = (at.len + kTile - 1) / kTile - first_tile, owns = min(tiles, 2);
+  int lh = 0, lt = 0, lo = 0, hi = owns;   // the next to load: its head and tile, the stage's tiles
+  auto fetch = [&](MUONH_LDS uint8_t* tile, MUONH_LDS float* rows) __attribute__((always_inline)) {
+    const int first = (first_tile + lt) * kTile, h = min(lh, group - 1);
+    Rows q{p.q + at.start * p.ldq + (kv * group + h) * p.dim, p.ldq, lh < group ? at.len : 0, p.dim};
+    Rows d{g.dout + at.start * g.lddo + (kv * group + h) * p.dim, g.lddo, lh < group ? at.len : 0, p.dim};
+    load_q(q, first, tile, wave);
+    load_d(d, first, tile + kBytes, wave);
+    // wavefront 0: -lse, 1: -delta (2 and 3 to where nobody reads)
+    const float* src = (wave & 1 ? g.row_delta : g.row_lse) + (kv * group + h) * (int64_t)p.tokens + at.start + first;
+    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<float*>(src), (short)0, lh < group && wave < 2 ? min(kTile, at.len - first) * 4 : 0, kBufferConfig);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (MUONH_LDS void*)(rows + wave * kTile), 4, lane * 4, 0, 0, 0);
+    const bool turn = lt + 1 == hi, last = turn && lh + 1 == group, second = last && lo == 0 && tiles > 2;
+    lo = second ? 2 : lo;
+    hi = second ? tiles : hi;
+    lh = second ? 0 : turn ? lh + 1 : lh;
+    lt = turn ? lo : lt + 1;
   };
-  load(slot0, rows0);
-  u32x4_t fk[DP / 16], fv[DP / 16];
+  const int own_trips = owns * group, trips = (tiles - owns) * group;
+  // slot 0 is the first whole tile's
+  auto slot_of = [&](int j) __attribute__((always_inline)) {
+    const int i = (j + 3 - own_trips % 3) % 3;
+    return i == 0 ? slot0 : i == 1 ? slot1 : slot2;
+  };
+  auto rows_of = [&](int j) __attribute__((always_inline)) {
+    const int i = (j + 3 - own_trips % 3) % 3;
+    return i == 0 ? rows0 : i == 1 ? rows1 : rows2;
+  };
+  fetch(slot_of(0), rows_of(0));
+  u32x4_t fk[kSteps], fv[kSteps];
   load_operand<DP>(fk, k, row, lane);
   load_operand<DP>(fv, v, row, lane);
-  f32x16_t dk[DP / 32], dv[DP / 32];
+  f32x16_t dk[kCols], dv[kCols];
 #pragma unroll
-  for (int dt = 0; dt < DP / 32; ++dt) dk[dt] = dv[dt] = splat(0.0f);
+  for (int dt = 0; dt < kCols; ++dt) dk[dt] = dv[dt] = splat(0.0f);
   const float c = p.scale * kLog2e;
 
-  auto block = [&](uint8_t* tile, const float (&rows)[2][kTile], int b, auto diag) __attribute__((always_inline)) {
-    f32x16_t s = splat(0.0f), ds;
-    f32x4_t lse[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      lse[j] = *reinterpret_cast<const f32x4_t*>(&rows[0][32 * b + 8 * j + 4 * (lane >> 5)]);
-      const f32x4_t del = *reinterpret_cast<const f32x4_t*>(&rows[1][32 * b + 8 * j + 4 * (lane >> 5)]);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) ds[4 * j + e] = del[e];
-    }
-#pragma unroll
-    for (int e = 0; e < DP / 16; ++e) s = mfma(read.rows(tile, b, e), fk[e], s);
-#pragma unroll
-    for (int e = 0; e < DP / 16; ++e) ds = mfma(read.rows(tile + kBytes, b, e), fv[e], ds);
-#pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      s[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], c, lse[r / 4][r % 4]));
-      ds[r] *= s[r];
-      if (decltype(diag)::value && block_row(r) + 4 * (lane >> 5) < (lane & 31)) s[r] = ds[r] = 0.0f;
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const u32x4_t fp = operand(s, h), fs = operand(ds, h);
-#pragma unroll
-      for (int dt = 0; dt < DP / 32; ++dt) dv[dt] = mfma(read.columns(tile + kBytes, b, h, dt), fp, dv[dt]);
-#pragma unroll
-      for (int dt = 0; dt < DP / 32; ++dt) dk[dt] = mfma(read.columns(tile, b, h, dt), fs, dk[dt]);
-    }
+  // -lse (w = 0) or -delta (1) of rows 8 j + 4 (l / 32) .. + 3 of block b: the lane's of
+  // registers 4 j .. + 3.
+  auto row_values = [&](MUONH_LDS float* rows, int w, int b, int j) __attribute__((always_inline)) {
+    return *reinterpret_cast<MUONH_LDS f32x4_t*>(rows + w * kTile + 32 * b + 8 * j + 4 * (lane >> 5));
   };
-  auto fetch = [&](uint8_t* tile, float (&rows)[2][kTile]) __attribute__((always_inline)) {
-    if (lh < group) load(tile, rows);
-  };
-  auto full = [&](uint8_t* tile, const float (&rows)[2][kTile]) __attribute__((always_inline)) {
-    block(tile, rows, 0, std::false_type{});
-    block(tile, rows, 1, std::false_type{});
-  };
-  // Head by head: the two tiles of the workgroup's own rows, then the tiles behind
-  // them, which all of its rows are seen by.  The heads' tiles take the slots in turn.
-  const int tiles = end_tile - first_tile;
-  auto own = [&](uint8_t* tile, const float (&rows)[2][kTile], int j) __attribute__((always_inline)) {
-    if (j == 0) {
-      if (wave >= 2) return;
-      block(tile, rows, wave, std::true_type{});
-      if (wave == 0) block(tile, rows, 1, std::false_type{});
-    } else {
-      if (wave < 2) return full(tile, rows);
-      block(tile, rows, wave - 2, std::true_type{});
-      if (wave == 2) block(tile, rows, 1, std::false_type{});
+
+  // A tile of the workgroup's own rows, block by block: those before the wavefront's do
+  // not see its keys.
+  auto own = [&](MUONH_LDS uint8_t* tile, MUONH_LDS float* rows, int j) __attribute__((always_inline)) {
+#pragma unroll 1
+    for (int b = 0; b < 2; ++b) {
+      const int ahead = 2 * j + b - wave;   // blocks between the rows' and the keys'
+      if (ahead < 0) continue;
+      MUONH_LDS uint8_t* blk = tile + b * 32 * DP * 2;
+      f32x16_t s = splat(0.0f), ds = splat(0.0f);
+#pragma unroll
+      for (int e = 0; e < kSteps; ++e) {
+        s = mfma(read.rows(blk, 0, e), fk[e], s);
+        ds = mfma(read.rows(blk + kBytes, 0, e), fv[e], ds);
+      }
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        s[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], c, row_values(rows, 0, b, r / 4)[r % 4]));
+        ds[r] = (ds[r] + row_values(rows, 1, b, r / 4)[r % 4]) * s[r];
+        if (ahead == 0 && block_row(r) + 4 * (lane >> 5) < (lane & 31)) s[r] = ds[r] = 0.0f;
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const u32x4_t fp = operand(s, h), fs = operand(ds, h);
+#pragma unroll
+        for (int dt = 0; dt < kCols; ++dt) dv[dt] = mfma(read.columns(blk + kBytes, 0, h, dt), fp, dv[dt]);
+#pragma unroll
+        for (int dt = 0; dt < kCols; ++dt) dk[dt] = mfma(read.columns(blk, 0, h, dt), fs, dk[dt]);
+      }
     }
   };
-  auto use = [&](uint8_t* tile, const float (&rows)[2][kTile], int j) __attribute__((always_inline)) {
-    if (j < 2) own(tile, rows, j);
-    else full(tile, rows);
+
+  // A whole tile: products n = 0 .. 4 kPhase - 1 in the order S and dP of block 0, of
+  // block 1, sums of block 0, of block 1.
+  constexpr int kAhead = 4;
+  u32x4_t ring[kAhead];
+  auto fragment = [&](MUONH_LDS uint8_t* tile, auto number) __attribute__((always_inline)) {
+    constexpr int n = decltype(number)::value, phase = n / kPhase, i = n % kPhase;
+    MUONH_LDS uint8_t* t = tile + ((phase < 2) == (i & 1) ? kBytes : 0);
+    if constexpr (phase < 2) return read.rows(t, phase & 1, i / 2);
+    else return read.columns(t, phase & 1, i / (2 * kCols), i / 2 % kCols);
   };
-  const int trips = tiles * group;
-  for (int j = 0, at_tile = 0; j < trips; j += 2) {
+  auto full = [&](MUONH_LDS uint8_t* tile, MUONH_LDS float* rows, MUONH_LDS uint8_t* next) __attribute__((always_inline)) {
+    f32x16_t s[2], ds[2];
+    u32x4_t fp[2][2], fs[2][2];
+    f32x4_t lse[2], del[2];   // of two groups of four rows in turn
+    auto load_values = [&](int b, int j) __attribute__((always_inline)) {
+      lse[j & 1] = row_values(rows, 0, b, j);
+      del[j & 1] = row_values(rows, 1, b, j);
+    };
+    each<4 * kPhase>([&](auto number) __attribute__((always_inline)) {
+      constexpr int n = decltype(number)::value, phase = n / kPhase, i = n % kPhase;
+      const u32x4_t f = ring[n % kAhead];
+      if constexpr (phase < 2) {
+        if constexpr (i < 2) (i & 1 ? ds : s)[phase] = splat(0.0f);
+        if constexpr (i & 1) ds[phase] = mfma(f, fv[i / 2], ds[phase]);
+        else s[phase] = mfma(f, fk[i / 2], s[phase]);
+      } else {
+        constexpr int h = i / (2 * kCols), dt = i / 2 % kCols;
+        if constexpr (i & 1) dk[dt] = mfma(f, fs[phase - 2][h], dk[dt]);
+        else dv[dt] = mfma(f, fp[phase - 2][h], dv[dt]);
+      }
+      constexpr int ahead = (n + kAhead) % (4 * kPhase);
+      ring[n % kAhead] = fragment(ahead == n + kAhead ? tile : next, std::integral_constant<int, ahead>{});
+      // Values of block b beside the products of phase b + 1: none beside the first two,
+      // whose operands the products before have just left.
+      if constexpr ((phase == 1 || phase == 2) && i >= 2) {
+        constexpr int b = phase - 1;
+        each<16>([&](auto reg) __attribute__((always_inline)) {
+          constexpr int r = decltype(reg)::value;
+          if constexpr (r >= 16 * (i - 2) / (kPhase - 2) && r < 16 * (i - 1) / (kPhase - 2)) {
+            s[b][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][r], c, lse[r / 4 & 1][r % 4]));
+            ds[b][r] = (ds[b][r] + del[r / 4 & 1][r % 4]) * s[b][r];
+            if constexpr (r % 4 == 3 && r < 8) load_values(b, r / 4 + 2);
+            if constexpr (r & 1) {
+              fp[b][r / 8][r % 8 / 2] = pack_bf16x2(s[b][r - 1], s[b][r]);
+              fs[b][r / 8][r % 8 / 2] = pack_bf16x2(ds[b][r - 1], ds[b][r]);
+            }
+          }
+        });
+      }
+      if constexpr (n == kPhase - 2 || n == 2 * kPhase - 1) {
+        load_values(phase, 0);
+        load_values(phase, 1);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  };
+
+  // Before tile j: tile j + 1 is there for all, and all are done with tile j - 1, whose
+  // slot takes tile j + 2.
+  arrive();
+  fetch(slot_of(1), rows_of(1));
+#pragma unroll 1
+  for (int j = 0; j < own_trips; ++j) {
     arrive();
-    fetch(slot1, rows1);
-    use(slot0, rows0, at_tile);
-    at_tile = at_tile + 1 < tiles ? at_tile + 1 : 0;
-    if (j + 1 == trips) break;
+    fetch(slot_of(j + 2), rows_of(j + 2));
+    own(slot_of(j), rows_of(j), owns == 2 ? j & 1 : 0);
+  }
+  each<kAhead>([&](auto n) __attribute__((always_inline)) { ring[decltype(n)::value] = fragment(slot0, n); });
+  for (int j = 0; j < trips; j += 3) {
+    arrive();
+    fetch(slot2, rows2);
+    full(slot0, rows0, slot1);
+    if (j + 1 >= trips) break;
     arrive();
     fetch(slot0, rows0);
-    use(slot1, rows1, at_tile);
-    at_tile = at_tile + 1 < tiles ? at_tile + 1 : 0;
+    full(slot1, rows1, slot2);
+    if (j + 2 >= trips) break;
+    arrive();
+    fetch(slot1, rows1);
+    full(slot2, rows2, slot0);
   }
+  arrive();   // no load into LDS outlives the workgroup
   if (row + (lane & 31) >= at.len) return;
   const int64_t t = at.start + row;
   store_rows<DP>(g.dk + t * g.lddk + kv * p.dim, g.lddk, p.dim, dk, p.scale, lane);
