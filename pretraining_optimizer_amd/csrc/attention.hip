@@ -193,32 +193,83 @@ __device__ __forceinline__ void load_operand(u32x4_t (&f)[DP / 16], const Rows& 
   }
 }
 
-// The sequence and the place in it of a workgroup's rows.  Sequence b's blocks are
-// numbered from first_block(b) = cu[b] / 128 + b on, which leaves room for the last,
-// cut one; a number between two sequences has no rows.  Ends are taken into
-// [0, tokens], so no cu_seqlens reads or writes outside the tensors.
+// The sequence and the place in it of a workgroup's rows: the block of the rank-th most
+// work, counted in blocks seen (KEYS = false: up to its own; true: from its own on).
+// Long ones first, the short ones fill the gaps at the end (documents of 8192 tokens, gradients:
+// 349 us in the sequences' order).  With n_b blocks in sequence b, count(h) = sum_b
+// max(0, n_b - h + 1) blocks see h or more, so the rank's h is the largest with count(h) >
+// rank; a lane per sequence evaluates it.  More than 64 sequences keep their order:
+// blocks are numbered from cu[b] / 128 + b on, which leaves room for the last, cut one.
+//
+// Ends are taken into [0, tokens], so no cu_seqlens reads or writes outside the tensors.
 struct Place {
   int64_t start;   // the sequence's first row
-  int len, row;    // its rows, and the workgroup's first
+  int len, row;    // its rows, and the workgroup's first (-1: none)
 };
 __device__ __forceinline__ int sequence_end(const AttentionArgs& p, int b) { return min(max(p.cu[b], 0), p.tokens); }
-__device__ __forceinline__ Place find_place(const AttentionArgs& p, int block) {
-  int lo = 0, hi = p.sequences - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (sequence_end(p, mid) / kBlock + mid <= block) lo = mid;
-    else hi = mid - 1;
-  }
-  const int s = sequence_end(p, lo), e = max(sequence_end(p, lo + 1), s);
-  const int64_t row = ((int64_t)block - s / kBlock - lo) * kBlock;
-  return Place{s, e - s, row < 0 || row >= e - s ? -1 : (int)row};
+
+// The sum over the wavefront.
+__device__ __forceinline__ int wave_sum(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);   // from lanes 1, 2, 4, 8 below in the row of 16
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);   // rows 1 and 3 from lanes 15 and 47
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);   // rows 2 and 3 from lane 31
+  return __builtin_amdgcn_readlane(v, 63);
 }
 
-// The work of workgroup i.  Workgroups i, i + 8, .. run on one XCD: it gets a run of
-// consecutive items, so that one key head's rows stay in its L2.
-__device__ __forceinline__ int64_t item_of(int64_t i, int64_t n) {
-  const int64_t xcd = i & 7, per = n >> 3, more = n & 7;
-  return xcd * per + min(xcd, more) + (i >> 3);
+template <bool KEYS>
+__device__ __forceinline__ Place find_place(const AttentionArgs& p, int rank) {
+  const int lane = threadIdx.x & 63;
+  if (p.sequences > 64) {
+    const int block = KEYS ? rank : p.blocks - 1 - rank;
+    int lo = 0, hi = p.sequences - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (sequence_end(p, mid) / kBlock + mid <= block) lo = mid;
+      else hi = mid - 1;
+    }
+    const int s = sequence_end(p, lo), e = max(sequence_end(p, lo + 1), s);
+    const int64_t row = ((int64_t)block - s / kBlock - lo) * kBlock;
+    return Place{s, e - s, row < 0 || row >= e - s ? -1 : (int)row};
+  }
+  int s = 0, e = 0;
+  if (lane < p.sequences) {
+    s = sequence_end(p, lane);
+    e = max(sequence_end(p, lane + 1), s);
+  }
+  const int n = (e - s + kBlock - 1) / kBlock;
+  int h = __builtin_amdgcn_readlane(n, 0) - rank, b = 0;   // of one sequence
+  if (p.sequences > 1) {
+    int top = p.blocks;
+    h = 0;
+    while (h < top) {   // count(h) > rank, or h = 0; count(top + 1) <= rank
+      const int mid = (h + top + 1) >> 1;
+      if (wave_sum(max(n - mid + 1, 0)) > rank) h = mid;
+      else top = mid - 1;
+    }
+    // the sequences with such a block, in their order
+    const uint64_t have = __ballot(n >= h);
+    const int skip = rank - wave_sum(max(n - h, 0));
+    const uint64_t hit = __ballot(n >= h && __popcll(have & ((1ull << lane) - 1)) == skip);
+    b = hit ? __builtin_ctzll(hit) : 0;
+  }
+  if (h < 1) return Place{0, 0, -1};
+  s = __builtin_amdgcn_readlane(s, b);
+  e = __builtin_amdgcn_readlane(e, b);
+  return Place{s, e - s, (KEYS ? __builtin_amdgcn_readlane(n, b) - h : h - 1) * kBlock};
+}
+
+// Workgroup i's key head, head of its group and rank.  Workgroups i, i + 8, .. run on one
+// XCD: with the key head first, an XCD's have few different ones, whose rows stay in its
+// L2, and all ranks.
+struct Item {
+  int kv, member, rank;
+};
+__device__ __forceinline__ Item item_of(int kv_heads, int group) {
+  const int i = blockIdx.x, rest = i / kv_heads;
+  return Item{i % kv_heads, rest % group, rest / group};
 }
 
 // Where the lane's results lie: column l % 32 is a row of the tensor, registers 4 j ..
@@ -258,9 +309,9 @@ __global__ __launch_bounds__(kThreads, 2) void attention_forward_kernel(Attentio
   MUONH_LDS uint8_t *const slot0 = (MUONH_LDS uint8_t*)lds0, *const slot1 = (MUONH_LDS uint8_t*)lds1;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int group = p.heads / p.kv_heads;
-  const int64_t item = item_of(blockIdx.x, gridDim.x), per = (int64_t)p.blocks * group;
-  const int kv = (int)(item / per), head = kv * group + (int)(item % per % group);
-  const Place at = find_place(p, p.blocks - 1 - (int)(item % per / group));   // long rows first
+  const Item item = item_of(p.kv_heads, group);
+  const int kv = item.kv, head = kv * group + item.member;
+  const Place at = find_place<false>(p, item.rank);
   if (at.row < 0) return;
 
   const Rows q{p.q + at.start * p.ldq + head * p.dim, p.ldq, at.len, p.dim};
@@ -402,9 +453,9 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttentionGrad
   MUONH_LDS uint8_t *const slot0 = (MUONH_LDS uint8_t*)lds0, *const slot1 = (MUONH_LDS uint8_t*)lds1;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int group = p.heads / p.kv_heads;
-  const int64_t item = item_of(blockIdx.x, gridDim.x), per = (int64_t)p.blocks * group;
-  const int kv = (int)(item / per), head = kv * group + (int)(item % per % group);
-  const Place at = find_place(p, p.blocks - 1 - (int)(item % per / group));
+  const Item item = item_of(p.kv_heads, group);
+  const int kv = item.kv, head = kv * group + item.member;
+  const Place at = find_place<false>(p, item.rank);
   if (at.row < 0) return;
 
   const Rows q{p.q + at.start * p.ldq + head * p.dim, p.ldq, at.len, p.dim};
@@ -527,9 +578,9 @@ __global__ __launch_bounds__(kThreads, 1) void attention_dkv_kernel(AttentionGra
                          *const rows2 = (MUONH_LDS float*)ldsr2;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int group = p.heads / p.kv_heads;
-  const int64_t item = item_of(blockIdx.x, gridDim.x);
-  const int kv = (int)(item / p.blocks);
-  const Place at = find_place(p, (int)(item % p.blocks));
+  const Item item = item_of(p.kv_heads, 1);
+  const int kv = item.kv;
+  const Place at = find_place<true>(p, item.rank);
   if (at.row < 0) return;
 
   const Rows k{p.k + at.start * p.ldk + kv * p.dim, p.ldk, at.len, p.dim};
