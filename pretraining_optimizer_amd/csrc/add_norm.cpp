@@ -90,11 +90,18 @@ int muonh_add_norm_quantize(const muonh_add_norm_args* g, const muonh_fp8_matrix
     out.cols = g->cols;
     if (q) set_row_form(out, *q);
     if (qt) set_column_form(out, *qt);
+    if (q && add_norm_rows_quantize(g->cols)) {
+      a.q = out.q;
+      a.s = out.s;
+      a.ldq = out.ldq;
+      a.lds = out.lds;
+      out.q = out.s = nullptr;
+    }
     const int bf16 = g->dtype == MUONH_BF16;
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
     forget_older_errors();
     hipError_t e = launch_add_norm_rows(bf16, a, st);
-    if (e == hipSuccess) e = launch_norm_quantize(bf16, out, g->weight, g->rstd, st);
+    if (e == hipSuccess && (out.q || out.qt)) e = launch_norm_quantize(bf16, out, g->weight, g->rstd, st);
     return launched(e, "add_norm_quantize");
   });
 }

@@ -19,21 +19,23 @@ struct EmbeddingArgs {
 hipError_t launch_embedding_forward(int table_bf16, int out_bf16, const EmbeddingArgs& a, hipStream_t st);
 
 constexpr int kSortThreads = 1024;
-constexpr int kSortItems = 8;                               // per thread
-constexpr int64_t kSortBlock = kSortThreads * kSortItems;   // tokens that one workgroup sorts
+// Tokens that one workgroup sorts: up to 8192 alone, 4096 beside others.
+constexpr int kSortAlone = 8, kSortBeside = 4;              // per thread
+constexpr int64_t kSortBlock = kSortThreads * kSortBeside;
 constexpr int kSortDigits = 1024;                           // at most, of one pass
 
 // A token's key is its row, or `rows` if it has none.  Keys are sorted in passes of
 // equally many bits, at most 10.
 struct SortPlan {
   int32_t passes, bits;
-  int64_t blocks;
+  int64_t blocks;   // workgroups
 };
 inline SortPlan plan_sort(int64_t count, int64_t rows) {
   int bits = 1;
   while (((int64_t)1 << bits) <= rows) ++bits;
   const int passes = (bits + 9) / 10;
-  return SortPlan{passes, (bits + passes - 1) / passes, (count + kSortBlock - 1) / kSortBlock};
+  return SortPlan{passes, (bits + passes - 1) / passes,
+                  count <= kSortThreads * kSortAlone ? 1 : (count + kSortBlock - 1) / kSortBlock};
 }
 // Sorted tokens that one workgroup adds up.
 inline int64_t sum_run(int64_t count) { return count <= 65536 ? 16 : 64; }

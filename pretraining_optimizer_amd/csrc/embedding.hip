@@ -52,35 +52,39 @@ __global__ __launch_bounds__(kThreads) void embedding_forward_kernel(EmbeddingAr
 }
 
 // One pass of the sort by one workgroup's keys: the stable rank of each among them.
-// Thread t of wavefront w holds items 512 w + 64 k + t % 64.  Each wavefront counts its
+// Thread t of wavefront w holds items 64 (N w + k) + t % 64, k < N.  Each wavefront counts its
 // digits in order (equal digits of one load by a ballot per bit), and the wavefronts'
 // counts are added up over the digits and, for each, over the wavefronts.
 constexpr int kWaves = kSortThreads / 64;
-constexpr int kWaveItems = 64 * kSortItems;
 struct SortLds {
   uint32_t count[kWaves][kSortDigits + 1];   // + 1: a digit's counters lie in different banks
   uint32_t wave[kWaves];
 };
 
-template <bool HELD>
-__device__ __forceinline__ void count_digits(SortLds& lds, const uint32_t (&key)[kSortItems], uint32_t (&rank)[kSortItems],
+template <int N>
+__device__ __forceinline__ void count_digits(SortLds& lds, const uint32_t (&key)[N], uint32_t (&rank)[N],
                                              int64_t left, int shift, int bits) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const uint32_t mask = (1u << bits) - 1;
   for (int i = threadIdx.x; i < kWaves * (kSortDigits + 1); i += kSortThreads) (&lds.count[0][0])[i] = 0;
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < kSortItems; ++k) {
-    const bool live = wave * kWaveItems + k * 64 + lane < left;
+  for (int k = 0; k < N; ++k) {
+    const bool live = (wave * N + k) * 64 + lane < left;
     const uint32_t d = (key[k] >> shift) & mask;
-    uint64_t same = __ballot(live);
+    // the lanes with this one's digit: a bit's are its ballot's or the others
+    const uint64_t all = __ballot(live);
+    uint32_t lo = (uint32_t)all, hi = (uint32_t)(all >> 32);
     for (int b = 0; b < bits; ++b) {
-      const uint64_t m = __ballot((d >> b) & 1);
-      same &= (d >> b) & 1 ? m : ~m;
+      const uint32_t bit = (uint32_t)__builtin_amdgcn_sbfe((int)d, b, 1);   // 0 or ~0
+      const uint64_t m = __ballot(bit != 0);
+      lo &= ~((uint32_t)m ^ bit);
+      hi &= ~((uint32_t)(m >> 32) ^ bit);
     }
+    const uint64_t same = (uint64_t)hi << 32 | lo;
     if (live) {
       const uint32_t before = lds.count[wave][d], at = __popcll(same & ((1ull << lane) - 1));
-      if (HELD) rank[k] = before + at;
+      rank[k] = before + at;
       // the wavefront's LDS accesses are in order: all have read before one writes
       __builtin_amdgcn_wave_barrier();
       if (at == 0) lds.count[wave][d] = before + (uint32_t)__popcll(same);
@@ -90,9 +94,8 @@ __device__ __forceinline__ void count_digits(SortLds& lds, const uint32_t (&key)
   __syncthreads();
 }
 
-// counts[digit][wave] -> where the first key of each begins among the workgroup's, and
-// in total[] the digit's count.
-__device__ __forceinline__ uint32_t begin_digits(SortLds& lds, int digits) {
+// counts[digit][wave] -> where the first key of each begins among the workgroup's.
+__device__ __forceinline__ void begin_digits(SortLds& lds, int digits) {
   const int d = threadIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   uint32_t total = 0;
   if (d < digits)
@@ -115,94 +118,89 @@ __device__ __forceinline__ uint32_t begin_digits(SortLds& lds, int digits) {
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) lds.count[w][d] += sum - total;
   __syncthreads();
-  return total;
 }
-static_assert(kSortDigits <= kSortThreads, "a thread per digit");
 
 __device__ __forceinline__ uint32_t key_of(const EmbeddingGradArgs& p, int64_t i) {
   const int64_t v = token_at(p.tokens, p.wide, i);
   return v >= 0 && v < p.rows ? (uint32_t)v : (uint32_t)p.rows;
 }
 
-// Zeros in rows [0, rows) of the table, 16 bytes at a time, by the workgroups from
-// `first` on.
+// Zeros in all of the table: 16 bytes per thread where the rows follow each other (one
+// store each: 151936 x 2048 fp32 183 us, 6.8 TB/s; 281 us in a loop over the grid), else
+// a workgroup per row.
+constexpr int64_t kClearGroups = (int64_t)1 << 23;   // of one launch
 template <typename O>
-__device__ __forceinline__ void fill_zeros(const EmbeddingGradArgs& p, int64_t first) {
-  const int64_t per = (p.cols + 7) / 8, n = p.rows * per;
-  const float zeros[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  for (int64_t i = ((int64_t)blockIdx.x - first) * kSortThreads + threadIdx.x; i < n;
-       i += ((int64_t)gridDim.x - first) * kSortThreads) {
-    const int64_t row = i / per;
-    store8<O>(reinterpret_cast<O*>(p.dtable) + row * p.ldt, (int)(i - row * per) * 8, (int)p.cols, zeros);
+__global__ __launch_bounds__(kThreads) void clear_kernel(EmbeddingGradArgs p) {
+  O* const table = reinterpret_cast<O*>(p.dtable);
+  const int64_t n = p.rows * p.cols;
+  const int64_t head = min((int64_t)((16 - (reinterpret_cast<uintptr_t>(table) & 15)) & 15) / (int64_t)sizeof(O), n);
+  const int64_t whole = (n - head) * (int64_t)sizeof(O) / 16, tail = head + whole * 16 / (int64_t)sizeof(O);
+  u32x4_t* const span = reinterpret_cast<u32x4_t*>(table + head);
+  const u32x4_t zero = {0, 0, 0, 0};
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < whole; i += (int64_t)gridDim.x * kThreads)
+    st_global<u32x4_t>(span + i, zero);
+  if (blockIdx.x == 0) {
+    if ((int64_t)threadIdx.x < head) table[threadIdx.x] = 0;
+    if (tail + (int64_t)threadIdx.x < n) table[tail + threadIdx.x] = 0;
   }
 }
-
-// Up to kSortBlock tokens: one workgroup sorts them, in registers and LDS, while the
-// others clear the table.
 template <typename O>
-__global__ __launch_bounds__(kSortThreads) void sort_and_clear_kernel(EmbeddingGradArgs p, SortPlan plan) {
+__global__ __launch_bounds__(kThreads) void clear_rows_kernel(EmbeddingGradArgs p) {
+  const float zeros[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x)
+    for (int c = 8 * (int)threadIdx.x; c < (int)p.cols; c += 8 * kThreads)
+      store8<O>(reinterpret_cast<O*>(p.dtable) + row * p.ldt, c, (int)p.cols, zeros);
+}
+
+// Up to 8192 tokens: one workgroup sorts them, in registers and LDS.
+__global__ __launch_bounds__(kSortThreads) void sort_alone_kernel(EmbeddingGradArgs p, SortPlan plan) {
+  constexpr int N = kSortAlone;
   __shared__ SortLds lds;
-  __shared__ uint32_t keys[kSortBlock];
-  __shared__ uint16_t places[kSortBlock];
-  if (blockIdx.x > 0) {
-    fill_zeros<O>(p, 1);
-    return;
-  }
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  uint32_t key[kSortItems], place[kSortItems], rank[kSortItems];
+  __shared__ uint32_t keys[kSortThreads * N];
+  __shared__ uint16_t places[kSortThreads * N];
+  const int first = (threadIdx.x >> 6) * 64 * N + (threadIdx.x & 63), wave = threadIdx.x >> 6;
+  uint32_t key[N], place[N], rank[N];
 #pragma unroll
-  for (int k = 0; k < kSortItems; ++k) {
-    const int i = wave * kWaveItems + k * 64 + lane;
-    key[k] = i < p.count ? key_of(p, i) : 0;
-    place[k] = i;
+  for (int k = 0; k < N; ++k) {
+    place[k] = first + k * 64;
+    key[k] = place[k] < p.count ? key_of(p, place[k]) : 0;
   }
   for (int pass = 0; pass < plan.passes; ++pass) {
     const int shift = pass * plan.bits;
-    count_digits<true>(lds, key, rank, p.count, shift, plan.bits);
+    count_digits<N>(lds, key, rank, p.count, shift, plan.bits);
     begin_digits(lds, 1 << plan.bits);
 #pragma unroll
-    for (int k = 0; k < kSortItems; ++k) {
-      const int i = wave * kWaveItems + k * 64 + lane;
-      if (i < p.count) {
+    for (int k = 0; k < N; ++k)
+      if (first + k * 64 < p.count) {
         const uint32_t to = lds.count[wave][(key[k] >> shift) & ((1u << plan.bits) - 1)] + rank[k];
         keys[to] = key[k];
         places[to] = (uint16_t)place[k];
       }
-    }
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < kSortItems; ++k) {
-      const int i = wave * kWaveItems + k * 64 + lane;
-      if (i < p.count) {
-        key[k] = keys[i];
-        place[k] = places[i];
+    for (int k = 0; k < N; ++k)
+      if (first + k * 64 < p.count) {
+        key[k] = keys[first + k * 64];
+        place[k] = places[first + k * 64];
       }
-    }
   }
 #pragma unroll
-  for (int k = 0; k < kSortItems; ++k) {
-    const int i = wave * kWaveItems + k * 64 + lane;
-    if (i < p.count) {
-      p.keys[0][i] = key[k];
-      p.places[0][i] = place[k];
+  for (int k = 0; k < N; ++k)
+    if (first + k * 64 < p.count) {
+      p.keys[0][first + k * 64] = key[k];
+      p.places[0][first + k * 64] = place[k];
     }
-  }
 }
-static_assert(kSortBlock <= 65536, "places of one workgroup's tokens are 16 bits");
-
-template <typename O>
-__global__ __launch_bounds__(kSortThreads) void clear_kernel(EmbeddingGradArgs p) {
-  fill_zeros<O>(p, 0);
-}
+static_assert(kSortThreads * kSortAlone <= 65536, "places of one workgroup's tokens are 16 bits");
 
 // More tokens: per pass the digits' counts of every workgroup, where each begins, and
 // the keys put there.  `from` is the buffer read (pass 0: the tokens).
 __device__ __forceinline__ void read_keys(const EmbeddingGradArgs& p, int pass, int from, int64_t first,
-                                          uint32_t (&key)[kSortItems], uint32_t (&place)[kSortItems]) {
+                                          uint32_t (&key)[kSortBeside], uint32_t (&place)[kSortBeside]) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
-  for (int k = 0; k < kSortItems; ++k) {
-    const int64_t i = first + wave * kWaveItems + k * 64 + lane;
+  for (int k = 0; k < kSortBeside; ++k) {
+    const int64_t i = first + wave * 64 * kSortBeside + k * 64 + lane;
     key[k] = place[k] = 0;
     if (i < p.count) {
       key[k] = pass == 0 ? key_of(p, i) : p.keys[from][i];
@@ -212,14 +210,21 @@ __device__ __forceinline__ void read_keys(const EmbeddingGradArgs& p, int pass, 
 }
 
 __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(EmbeddingGradArgs p, SortPlan plan, int pass, int from) {
-  __shared__ SortLds lds;
+  __shared__ uint32_t count[kSortDigits];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t first = (int64_t)blockIdx.x * kSortBlock;
-  uint32_t key[kSortItems], place[kSortItems], rank[kSortItems];
+  uint32_t key[kSortBeside], place[kSortBeside];
   read_keys(p, pass, from, first, key, place);
-  count_digits<false>(lds, key, rank, p.count - first, pass * plan.bits, plan.bits);
-  const uint32_t total = begin_digits(lds, 1 << plan.bits);
-  if ((int)threadIdx.x < 1 << plan.bits) p.digits[(int64_t)blockIdx.x * kSortDigits + threadIdx.x] = total;
+  count[threadIdx.x] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kSortBeside; ++k)   // whole numbers: their order does not matter
+    if (first + wave * 64 * kSortBeside + k * 64 + lane < p.count)
+      atomicAdd(&count[(key[k] >> (pass * plan.bits)) & ((1u << plan.bits) - 1)], 1u);
+  __syncthreads();
+  p.digits[(int64_t)blockIdx.x * kSortDigits + threadIdx.x] = count[threadIdx.x];
 }
+static_assert(kSortDigits == kSortThreads, "a thread per digit");
 
 // digits[block][d] -> where block's keys of digit d begin.
 __global__ __launch_bounds__(kSortThreads) void sort_begin_kernel(EmbeddingGradArgs p, SortPlan plan) {
@@ -227,8 +232,9 @@ __global__ __launch_bounds__(kSortThreads) void sort_begin_kernel(EmbeddingGradA
   const int d = threadIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const bool live = d < 1 << plan.bits;
   uint32_t total = 0;
-  if (live)
+  if (live) {
     for (int64_t b = 0; b < plan.blocks; ++b) total += p.digits[b * kSortDigits + d];
+  }
   uint32_t sum = total;
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) {
@@ -239,23 +245,29 @@ __global__ __launch_bounds__(kSortThreads) void sort_begin_kernel(EmbeddingGradA
   __syncthreads();
   for (int w = 0; w < wave; ++w) sum += sums[w];
   uint32_t at = sum - total;
-  if (live)
-    for (int64_t b = 0; b < plan.blocks; ++b) {
-      const uint32_t c = p.digits[b * kSortDigits + d];
-      p.digits[b * kSortDigits + d] = at;
-      at += c;
+  if (!live) return;
+  constexpr int kAhead = 8;
+  for (int64_t b0 = 0; b0 < plan.blocks; b0 += kAhead) {
+    uint32_t c[kAhead];
+#pragma unroll
+    for (int b = 0; b < kAhead; ++b) c[b] = b0 + b < plan.blocks ? p.digits[(b0 + b) * kSortDigits + d] : 0;
+#pragma unroll
+    for (int b = 0; b < kAhead; ++b) {
+      if (b0 + b < plan.blocks) p.digits[(b0 + b) * kSortDigits + d] = at;
+      at += c[b];
     }
+  }
 }
 
 __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(EmbeddingGradArgs p, SortPlan plan, int pass, int from, int to) {
   __shared__ SortLds lds;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t first = (int64_t)blockIdx.x * kSortBlock;
-  uint32_t key[kSortItems], place[kSortItems], rank[kSortItems];
+  uint32_t key[kSortBeside], place[kSortBeside], rank[kSortBeside];
   read_keys(p, pass, from, first, key, place);
   const int shift = pass * plan.bits;
   const uint32_t mask = (1u << plan.bits) - 1;
-  count_digits<true>(lds, key, rank, p.count - first, shift, plan.bits);
+  count_digits<kSortBeside>(lds, key, rank, p.count - first, shift, plan.bits);
   // before this wavefront's keys of a digit: the other workgroups' and wavefronts'
   const int d = threadIdx.x;
   if (d <= (int)mask) {
@@ -269,8 +281,8 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(EmbeddingGradA
   }
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < kSortItems; ++k)
-    if (first + wave * kWaveItems + k * 64 + lane < p.count) {
+  for (int k = 0; k < kSortBeside; ++k)
+    if (first + wave * 64 * kSortBeside + k * 64 + lane < p.count) {
       const uint32_t at = lds.count[wave][(key[k] >> shift) & mask] + rank[k];
       p.keys[to][at] = key[k];
       p.places[to][at] = place[k];
@@ -317,16 +329,18 @@ __global__ __launch_bounds__(kThreads) void embedding_sum_kernel(EmbeddingGradAr
   for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
   uint32_t current = keys[first];
   bool opened = current == before;   // the current row's tokens began in an earlier run
-  constexpr int kAhead = 8;
+  constexpr int kAhead = sizeof(T) == 2 ? 16 : 8;   // bf16: all rows of a short run are on their way at once
   for (int64_t i = first; i < end; i += kAhead) {
     Raw8<T> v[kAhead];
-    uint32_t key[kAhead];
+    uint32_t key[kAhead], place[kAhead];
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
       const int64_t at = min(i + a, end - 1);
       key[a] = keys[at];
-      v[a] = load8<T>(dout + (int64_t)places[at] * p.ldd, c, cols);
+      place[a] = places[at];
     }
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) v[a] = load8<T>(dout + (int64_t)place[a] * p.ldd, c, cols);
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
       if (i + a >= end) break;
@@ -349,8 +363,9 @@ __global__ __launch_bounds__(kThreads) void embedding_sum_kernel(EmbeddingGradAr
   else store_sum<O>(p, current, c, sum);
 }
 
-// Joins the partial sums of a row whose tokens begin in run r and go on: 8 groups of 32
-// threads add every eighth run's, then those sums in order.
+// Joins the partial sums of a row whose tokens begin in run r and go on: its runs are
+// counted by the workgroup's threads side by side, then 8 groups of 32 threads add every
+// eighth run's sums, four at a time, and those are added in order.
 constexpr int kJoin = 8;
 template <typename O>
 __global__ __launch_bounds__(kThreads) void embedding_join_kernel(EmbeddingGradArgs p, int which, int64_t run) {
@@ -358,22 +373,40 @@ __global__ __launch_bounds__(kThreads) void embedding_join_kernel(EmbeddingGradA
   const int64_t r = blockIdx.x, first = r * run, end = first + run;
   if (end >= p.count) return;
   const uint32_t* keys = p.keys[which];
-  const uint32_t key = keys[end - 1];
+  const uint32_t key = keys[end - 1], behind = keys[end], before = first > 0 ? keys[first - 1] : 0xffffffffu;
   // a row of several runs that began before this one is joined by the run it began in
-  if (keys[end] != key || key >= (uint32_t)p.rows || (first > 0 && keys[first - 1] == key)) return;
+  if (behind != key || key >= (uint32_t)p.rows || before == key) return;
+  const int64_t runs = (p.count + run - 1) / run;
+  int64_t last = r + 1;   // the last run that begins with the key
+  for (;;) {
+    const int64_t q = last + 1 + threadIdx.x;
+    const int more = __syncthreads_count(q < runs && keys[min(q, runs - 1) * run] == key);
+    last += more;
+    if (more < kThreads) break;
+  }
   const int t = threadIdx.x & 31, g = threadIdx.x >> 5;
   const int c = 8 * ((int)blockIdx.y * 32 + t), cols = (int)p.cols;
   float sum[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
-  // the runs behind r that begin with the key
-  for (int64_t q = r + g; q == r || (q * run < p.count && keys[q * run] == key); q += kJoin) {
-    if (c >= cols) break;
-    float x[8];
-    load8<float>(p.partials + (q * 2 + (q == r)) * p.cols, c, cols).widen(x);
+  constexpr int kAhead = 4;
+  if (c < cols)
+    for (int64_t q = r + g; q <= last; q += kAhead * kJoin) {
+      Raw8<float> v[kAhead];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sum[j] += x[j];
-  }
+      for (int a = 0; a < kAhead; ++a) {
+        const int64_t at = q + a * kJoin;
+        v[a].zero();
+        if (at <= last) v[a] = load8<float>(p.partials + (at * 2 + (at == r)) * p.cols, c, cols);
+      }
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) {
+        float x[8];
+        v[a].widen(x);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[j] += x[j];
+      }
+    }
 #pragma unroll
   for (int j = 0; j < 8; ++j) sums[g][t][j] = sum[j];
   __syncthreads();
@@ -395,15 +428,21 @@ int log_group_of(int64_t cols) {
 template <typename T, typename O>
 hipError_t backward_for(const EmbeddingGradArgs& a, hipStream_t st) {
   const SortPlan plan = plan_sort(a.count, a.rows);
-  // the table is cleared by 1024 workgroups (4 per CU) at most, 16 KiB each at least
-  const int64_t bytes = a.rows * a.cols * (int64_t)sizeof(O);
-  const unsigned clear = a.accumulate ? 0u : (unsigned)std::min<int64_t>((bytes + 16383) / 16384, 1024);
   hipError_t e = hipSuccess;
-  int which = 0;
-  if (a.count == 0 || plan.blocks > 1) {
-    if (clear) hipLaunchKernelGGL(clear_kernel<O>, dim3(clear), dim3(kSortThreads), 0, st, a);
+  if (!a.accumulate) {
+    if (a.ldt == a.cols || a.rows == 1) {
+      const int64_t groups = (a.rows * a.cols * (int64_t)sizeof(O) / 16 + kThreads - 1) / kThreads;
+      hipLaunchKernelGGL(clear_kernel<O>, dim3((unsigned)std::min(std::max<int64_t>(groups, 1), kClearGroups)), dim3(kThreads), 0, st, a);
+    } else {
+      hipLaunchKernelGGL(clear_rows_kernel<O>, dim3((unsigned)std::min(a.rows, kClearGroups)), dim3(kThreads), 0, st, a);
+    }
     e = hipGetLastError();
-    if (e != hipSuccess || a.count == 0) return e;
+  }
+  if (e != hipSuccess || a.count == 0) return e;
+  int which = 0;
+  if (plan.blocks == 1) {
+    hipLaunchKernelGGL(sort_alone_kernel, dim3(1), dim3(kSortThreads), 0, st, a, plan);
+  } else {
     const dim3 grid((unsigned)plan.blocks), block(kSortThreads);
     for (int pass = 0; pass < plan.passes; ++pass) {
       const int from = which;
@@ -414,11 +453,9 @@ hipError_t backward_for(const EmbeddingGradArgs& a, hipStream_t st) {
       e = hipGetLastError();
       if (e != hipSuccess) return e;
     }
-  } else {
-    hipLaunchKernelGGL(sort_and_clear_kernel<O>, dim3(1 + clear), dim3(kSortThreads), 0, st, a, plan);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
   }
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
   const int lg = log_group_of(a.cols);
   const int64_t run = sum_run(a.count), runs = (a.count + run - 1) / run, per = kThreads >> lg;
   const unsigned wide = (unsigned)((a.cols + (8 << lg) - 1) / (8 << lg));

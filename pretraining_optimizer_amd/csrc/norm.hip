@@ -19,6 +19,7 @@
 
 #include <algorithm>
 
+#include "fp8_convert.h"
 #include "operators.h"
 #include "row_vectors.h"
 
@@ -144,43 +145,93 @@ __global__ __launch_bounds__(G > kNormThreads ? G : kNormThreads) void norm_forw
   }
 }
 
-// h = x + residual, kept in x's type, and 1 / sqrt(mean(h^2) + eps) of the kept
-// values: what the tile kernel that normalises and quantises h (block_fp8.hip) needs
-// of its rows.  Without a residual h is x, which is only read.
+// h = x + residual, kept in x's type, 1 / sqrt(mean(h^2) + eps) of the kept values, and
+// the row form of y = (h r) w in block-scaled FP8, all from the registers that hold the
+// row: 16 threads have a group of 128 columns.  y is rounded once, to E4M3.  Without a
+// residual h is x, which is only read.
 template <typename T, int G, int NV>
 __global__ __launch_bounds__(G > kNormThreads ? G : kNormThreads) void add_norm_rows_kernel(AddNormArgs p) {
+  static_assert(G >= 16, "16 threads share a scale");
   constexpr int kThreads = G > kNormThreads ? G : kNormThreads;
   constexpr int kRows = kThreads / G;
   __shared__ float red[1][16];
   const int t = threadIdx.x % G, cols = (int)p.cols;
+  const int groups = (cols + kFp8Block - 1) / kFp8Block;
   const float rn = 1.0f / (float)cols;
   for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < p.rows; r0 += (int64_t)gridDim.x * kRows) {
     const int64_t row = r0 + threadIdx.x / G, at = min(row, p.rows - 1);
+    const bool live = row < p.rows;
     const T* x = reinterpret_cast<const T*>(p.x) + at * p.ldx;
     const T* r = reinterpret_cast<const T*>(p.residual) + at * p.ldr;
-    Raw8<T> v[NV], w[NV];
+    float v[NV][8];
+    {
+      Raw8<T> a[NV], b[NV];
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      v[k] = load8<T>(x, 8 * (t + G * k), cols);
-      if (p.residual) w[k] = load8<T>(r, 8 * (t + G * k), cols);
+      for (int k = 0; k < NV; ++k) {
+        a[k] = load8<T>(x, 8 * (t + G * k), cols);
+        if (p.residual) b[k] = load8<T>(r, 8 * (t + G * k), cols);
+      }
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        a[k].widen(v[k]);
+        if (p.residual) {
+          float w[8];
+          b[k].widen(w);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[k][j] = round_to<T>(v[k][j] + w[j]);
+          const int c = 8 * (t + G * k);
+          if (live && c < cols) store8<T>(reinterpret_cast<T*>(p.h) + row * p.ldh, c, cols, v[k]);
+        }
+      }
     }
     float ss[1] = {0.0f};
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      float a[8], b[8];
-      v[k].widen(a);
-      if (p.residual) {
-        w[k].widen(b);
+    for (int k = 0; k < NV; ++k)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) a[j] = round_to<T>(a[j] + b[j]);
-        const int c = 8 * (t + G * k);
-        if (row < p.rows && c < cols) store8<T>(reinterpret_cast<T*>(p.h) + row * p.ldh, c, cols, a);
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) ss[0] += a[j] * a[j];
-    }
+      for (int j = 0; j < 8; ++j) ss[0] += v[k][j] * v[k][j];
     group_sum<G, 1>(ss, red);
-    if (row < p.rows && t == 0) p.rstd[row] = 1.0f / sqrtf(ss[0] * rn + p.eps);
+    const float rstd = 1.0f / sqrtf(ss[0] * rn + p.eps);
+    if (live && t == 0) p.rstd[row] = rstd;
+    if (!p.q) continue;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int c = 8 * (t + G * k), group = c / kFp8Block;
+      float w[8];
+      loadw(p.weight, c, cols, w);
+      // behind the end 0 r w is no zero where r or w is infinite
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[k][j] = c + j < cols ? v[k][j] * rstd * w[j] : 0.0f;
+      uint32_t most = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) most = max(most, __float_as_uint(v[k][j]) & 0x7fffffffu);
+      const bool special = most >= 0x7f800000u;
+      if (special) {
+        most = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t m = __float_as_uint(v[k][j]) & 0x7fffffffu;
+          most = max(most, m < 0x7f800000u ? m : 0u);
+        }
+      }
+      const uint32_t byte = scale_byte(max16(most));
+      u32x2_t q;
+      if (special) {
+        q[0] = pack_fp8(scaled(v[k][0], byte), scaled(v[k][1], byte), scaled(v[k][2], byte), scaled(v[k][3], byte));
+        q[1] = pack_fp8(scaled(v[k][4], byte), scaled(v[k][5], byte), scaled(v[k][6], byte), scaled(v[k][7], byte));
+      } else {
+        const float scale = __uint_as_float(byte << 23);
+        q[0] = quantize4(v[k][0], v[k][1], v[k][2], v[k][3], scale);
+        q[1] = quantize4(v[k][4], v[k][5], v[k][6], v[k][7], scale);
+      }
+      if (!live || group >= groups) continue;
+      st_global<u32x2_t>(p.q + row * p.ldq + c, q);   // zeros up to the group's end
+      if ((t & 15) == 0) {
+        uint8_t* s = p.s + row * p.lds + group;
+        *s = (uint8_t)byte;
+        if (group == groups - 1)   // zero bytes up to a multiple of 4
+          for (int z = groups; z & 3; ++z) p.s[row * p.lds + z] = 0;
+      }
+    }
   }
 }
 
@@ -541,12 +592,11 @@ hipError_t add_norm_rows_for(const AddNormArgs& a, hipStream_t st) {
                        dim3(kLongThreads), 0, st, a);
     return hipGetLastError();
   }
-  const int64_t per = rows_at_once(cols, kNormThreads);
+  const int64_t per = rows_at_once(std::max<int64_t>(cols, 65), kNormThreads);   // groups of 16 threads at least
   const dim3 grid((unsigned)std::min<int64_t>((a.rows + per - 1) / per, 1 << 20));
 #define MUONH_ADD_NORM(G, NV)                                                                  \
   hipLaunchKernelGGL((add_norm_rows_kernel<T, G, NV>), grid, dim3(G > kNormThreads ? G : kNormThreads), 0, st, a)
-  if (cols <= 64) MUONH_ADD_NORM(8, 1);
-  else if (cols <= 128) MUONH_ADD_NORM(16, 1);
+  if (cols <= 128) MUONH_ADD_NORM(16, 1);
   else if (cols <= 256) MUONH_ADD_NORM(32, 1);
   else if (cols <= 512) MUONH_ADD_NORM(64, 1);
   else if (cols <= 1024) MUONH_ADD_NORM(64, 2);
@@ -559,6 +609,8 @@ hipError_t add_norm_rows_for(const AddNormArgs& a, hipStream_t st) {
 }
 
 }  // namespace
+
+bool add_norm_rows_quantize(int64_t cols) { return cols <= kRegisterCols; }
 
 hipError_t launch_add_norm_rows(int bf16, const AddNormArgs& a, hipStream_t st) {
   return bf16 ? add_norm_rows_for<uint16_t>(a, st) : add_norm_rows_for<float>(a, st);

@@ -114,8 +114,9 @@ struct NormGradArgs {
 int64_t norm_partial_rows(int64_t rows, int64_t cols);
 hipError_t launch_norm_backward(int bf16, int layer, const NormGradArgs& a, hipStream_t st);
 
-// The residual's addition, the RMS norm of the sum and its FP8 forms: first h and
-// rstd of every row, then the forms of h rstd weight, tile by tile.
+// The residual's addition, the RMS norm of the sum and its FP8 forms: first h, rstd
+// and, of rows that registers hold (add_norm_rows_quantize), the row form, then the
+// other forms of h rstd weight, tile by tile.
 struct AddNormArgs {
   const void* x;
   const void* residual;   // nullable: h is x, and not written
@@ -124,7 +125,11 @@ struct AddNormArgs {
   float* rstd;
   int64_t rows, cols, ldx, ldr, ldh;
   float eps;
+  uint8_t* q;             // nullable: the row form is not written here
+  uint8_t* s;
+  int64_t ldq, lds;
 };
+bool add_norm_rows_quantize(int64_t cols);
 hipError_t launch_add_norm_rows(int bf16, const AddNormArgs& a, hipStream_t st);
 // out.x, out.ldx: h.
 hipError_t launch_norm_quantize(int bf16, const QuantArgs& out, const float* weight, const float* rstd, hipStream_t st);
