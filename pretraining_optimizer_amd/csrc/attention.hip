@@ -109,22 +109,22 @@ struct Rows {
   }
 };
 
-// A tile's loads: instruction i of wavefront w fills 1024 bytes of LDS.
-template <int DP>
+// A tile's loads by WAVES wavefronts: instruction i of wavefront w fills 1024 bytes of LDS.
+template <int DP, int ROWS = kTile, int WAVES = 4>
 struct TileLoad {
-  static constexpr int kRow = DP * 2, kChunks = DP / 8, kStep = 4096 / kRow;   // rows per round of the wavefronts
+  static constexpr int kRow = DP * 2, kChunks = DP / 8, kStep = 1024 * WAVES / kRow;   // rows per round
+  static_assert(ROWS % kStep == 0 && kStep % 16 == 0, "whole rounds, the swizzle the same in each");
   int voff, step;
   __device__ __forceinline__ TileLoad(int64_t ld, int dim, int wave, int lane) {
-    const int row = wave * (kStep / 4) + lane / kChunks, chunk = (lane % kChunks) ^ swizzle<DP>(row);
+    const int row = wave * (kStep / WAVES) + lane / kChunks, chunk = (lane % kChunks) ^ swizzle<DP>(row);
     voff = chunk * 8 < dim ? (int)(row * ld * 2) + chunk * 16 : kBehind;
     step = (int)(kStep * ld * 2);
   }
   __device__ __forceinline__ void operator()(const Rows& t, int row, MUONH_LDS uint8_t* slot, int wave) const {
-    const __amdgpu_buffer_rsrc_t r = t.at(row, kTile);
+    const __amdgpu_buffer_rsrc_t r = t.at(row, ROWS);
 #pragma unroll
-    for (int i = 0; i < kTile / kStep; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (MUONH_LDS void*)(slot + (i * 4 + wave) * 1024),
-                                               16, voff, i * step, 0, 0);
+    for (int i = 0; i < ROWS / kStep; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (MUONH_LDS void*)(slot + (i * WAVES + wave) * 1024), 16, voff, i * step, 0, 0);
   }
 };
 
@@ -557,26 +557,28 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttentionGrad
 }
 
 // Gradients of k and v: a wavefront holds 32 rows of both and passes over the rows of
-// q and dout that see them, head by head of the group.
+// q and dout that see them, head by head of the group.  Eight wavefronts have 128 rows
+// of keys: w and w + 4 the same 32, for the even and the odd blocks of 32 rows, and their sums
+// are added at the end, the odd blocks' to the even ones'.  That halves the longest
+// workgroup, which sequences of different lengths wait for (documents of 8192 tokens,
+// 16/8 heads of 128: 175 us with four wavefronts on all blocks).
 //
-// One wavefront per SIMD has the registers for both sums (128), both operands (64) and
-// two blocks of scores, so a tile's two blocks are pipelined by hand: the 16 products of
-// block 1's S and dP run beside block 0's exponentials, those of block 0's sums beside
-// block 1's, a product (32 cycles) with one value's VALU work (24) at a time; operands
-// come out of LDS four products ahead, also over the tiles' border: three slots, the
-// barrier in the middle of a tile.
+// Two wavefronts per SIMD, so one's products overlap the other's exponentials: a product
+// takes 32 cycles and about 9 other instructions of 4 each go with it.  Of at most 256
+// registers both sums take 128 and the keys 32 (D = 128), so the values' operand stays
+// in LDS beside the two slots.  Operands come out of LDS two steps, or four products,
+// ahead.
+constexpr int kKeyThreads = 512;
 template <int DP>
-__global__ __launch_bounds__(kThreads, 1) void attention_dkv_kernel(AttentionGradArgs g) {
+__global__ __launch_bounds__(kKeyThreads, 2) void attention_dkv_kernel(AttentionGradArgs g) {
   const AttentionArgs& p = g.a;
-  constexpr int kBytes = kTile * DP * 2, kSteps = DP / 16, kCols = DP / 32;
-  constexpr int kPhase = 2 * kSteps;   // products of a block's scores, and of its sums
-  __shared__ __attribute__((aligned(1024))) uint8_t lds0[2 * kBytes], lds1[2 * kBytes], lds2[2 * kBytes];
-  __shared__ __attribute__((aligned(16))) float ldsr0[4 * kTile], ldsr1[4 * kTile], ldsr2[4 * kTile];
-  MUONH_LDS uint8_t *const slot0 = (MUONH_LDS uint8_t*)lds0, *const slot1 = (MUONH_LDS uint8_t*)lds1,
-                           *const slot2 = (MUONH_LDS uint8_t*)lds2;
-  MUONH_LDS float *const rows0 = (MUONH_LDS float*)ldsr0, *const rows1 = (MUONH_LDS float*)ldsr1,
-                         *const rows2 = (MUONH_LDS float*)ldsr2;
+  constexpr int kBytes = kTile * DP * 2, kSteps = DP / 16, kCols = DP / 32, kWaves = kKeyThreads / 64;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds0[2 * kBytes], lds1[2 * kBytes], ldsv[kBlock * DP * 2];
+  __shared__ __attribute__((aligned(16))) float ldsr0[kWaves * kTile], ldsr1[kWaves * kTile];
+  MUONH_LDS uint8_t *const slot0 = (MUONH_LDS uint8_t*)lds0, *const slot1 = (MUONH_LDS uint8_t*)lds1;
+  MUONH_LDS float *const rows0 = (MUONH_LDS float*)ldsr0, *const rows1 = (MUONH_LDS float*)ldsr1;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int key_block = wave & 3, odd = wave >> 2;
   const int group = p.heads / p.kv_heads;
   const Item item = item_of(p.kv_heads, 1);
   const int kv = item.kv;
@@ -585,173 +587,166 @@ __global__ __launch_bounds__(kThreads, 1) void attention_dkv_kernel(AttentionGra
 
   const Rows k{p.k + at.start * p.ldk + kv * p.dim, p.ldk, at.len, p.dim};
   const Rows v{p.v + at.start * p.ldv + kv * p.dim, p.ldv, at.len, p.dim};
-  const int row = at.row + 32 * wave;
-  const TileLoad<DP> load_q(p.ldq, p.dim, wave, lane), load_d(g.lddo, p.dim, wave, lane);
-  const TileRead<DP> read(lane);
+  const int row = at.row + 32 * key_block;
+  const TileLoad<DP, kTile, kWaves> load_q(p.ldq, p.dim, wave, lane), load_d(g.lddo, p.dim, wave, lane);
+  const TileLoad<DP, kBlock, kWaves> load_v(p.ldv, p.dim, wave, lane);
+  TileRead<DP> read(lane);
   // The tiles of q and dout: first those of the workgroup's own rows, head by head, then
-  // the whole ones behind them, head by head.  Rows behind the end arrive as zeros: P =
-  // exp 0, but dout, delta and q are 0.  Behind the last tile zeros are loaded, from nowhere.
+  // the ones behind them, which see all of its keys, head by head.  Rows behind the end
+  // arrive as zeros: P = exp 0, but dout, delta and q are 0.  Behind the last tile zeros are
+  // loaded, from nowhere.
   const int first_tile = at.row / kTile, tiles = (at.len + kTile - 1) / kTile - first_tile, owns = min(tiles, 2);
+  const int own_trips = owns * group, trips = tiles * group;
   int lh = 0, lt = 0, lo = 0, hi = owns;   // the next to load: its head and tile, the stage's tiles
   auto fetch = [&](MUONH_LDS uint8_t* tile, MUONH_LDS float* rows) __attribute__((always_inline)) {
     const int first = (first_tile + lt) * kTile, h = min(lh, group - 1);
-    Rows q{p.q + at.start * p.ldq + (kv * group + h) * p.dim, p.ldq, lh < group ? at.len : 0, p.dim};
-    Rows d{g.dout + at.start * g.lddo + (kv * group + h) * p.dim, g.lddo, lh < group ? at.len : 0, p.dim};
+    const Rows q{p.q + at.start * p.ldq + (kv * group + h) * p.dim, p.ldq, lh < group ? at.len : 0, p.dim};
+    const Rows d{g.dout + at.start * g.lddo + (kv * group + h) * p.dim, g.lddo, lh < group ? at.len : 0, p.dim};
     load_q(q, first, tile, wave);
     load_d(d, first, tile + kBytes, wave);
-    // wavefront 0: -lse, 1: -delta (2 and 3 to where nobody reads)
+    // wavefront 0: -lse, 1: -delta (the others to where nobody reads)
     const float* src = (wave & 1 ? g.row_delta : g.row_lse) + (kv * group + h) * (int64_t)p.tokens + at.start + first;
     const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
         const_cast<float*>(src), (short)0, lh < group && wave < 2 ? min(kTile, at.len - first) * 4 : 0, kBufferConfig);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (MUONH_LDS void*)(rows + wave * kTile), 4, lane * 4, 0, 0, 0);
-    const bool turn = lt + 1 == hi, last = turn && lh + 1 == group, second = last && lo == 0 && tiles > 2;
-    lo = second ? 2 : lo;
+    const bool turn = lt + 1 == hi, second = turn && lh + 1 == group && lo == 0 && tiles > owns;
+    lo = second ? owns : lo;
     hi = second ? tiles : hi;
     lh = second ? 0 : turn ? lh + 1 : lh;
     lt = turn ? lo : lt + 1;
   };
-  const int own_trips = owns * group, trips = (tiles - owns) * group;
-  // slot 0 is the first whole tile's
-  auto slot_of = [&](int j) __attribute__((always_inline)) {
-    const int i = (j + 3 - own_trips % 3) % 3;
-    return i == 0 ? slot0 : i == 1 ? slot1 : slot2;
-  };
-  auto rows_of = [&](int j) __attribute__((always_inline)) {
-    const int i = (j + 3 - own_trips % 3) % 3;
-    return i == 0 ? rows0 : i == 1 ? rows1 : rows2;
-  };
-  fetch(slot_of(0), rows_of(0));
-  u32x4_t fk[kSteps], fv[kSteps];
+  load_v(v, at.row, (MUONH_LDS uint8_t*)ldsv, wave);
+  fetch(own_trips & 1 ? slot1 : slot0, own_trips & 1 ? rows1 : rows0);
+  u32x4_t fk[kSteps];
   load_operand<DP>(fk, k, row, lane);
-  load_operand<DP>(fv, v, row, lane);
   f32x16_t dk[kCols], dv[kCols];
 #pragma unroll
   for (int dt = 0; dt < kCols; ++dt) dk[dt] = dv[dt] = splat(0.0f);
   const float c = p.scale * kLog2e;
+  MUONH_LDS uint8_t* const values = (MUONH_LDS uint8_t*)ldsv + key_block * 32 * DP * 2;
 
-  // -lse (w = 0) or -delta (1) of rows 8 j + 4 (l / 32) .. + 3 of block b: the lane's of
-  // registers 4 j .. + 3.
-  auto row_values = [&](MUONH_LDS float* rows, int w, int b, int j) __attribute__((always_inline)) {
-    return *reinterpret_cast<MUONH_LDS f32x4_t*>(rows + w * kTile + 32 * b + 8 * j + 4 * (lane >> 5));
-  };
-
-  // A tile of the workgroup's own rows, block by block: those before the wavefront's do
-  // not see its keys.
-  auto own = [&](MUONH_LDS uint8_t* tile, MUONH_LDS float* rows, int j) __attribute__((always_inline)) {
-#pragma unroll 1
-    for (int b = 0; b < 2; ++b) {
-      const int ahead = 2 * j + b - wave;   // blocks between the rows' and the keys'
-      if (ahead < 0) continue;
-      MUONH_LDS uint8_t* blk = tile + b * 32 * DP * 2;
-      f32x16_t s = splat(0.0f), ds = splat(0.0f);
-#pragma unroll
-      for (int e = 0; e < kSteps; ++e) {
-        s = mfma(read.rows(blk, 0, e), fk[e], s);
-        ds = mfma(read.rows(blk + kBytes, 0, e), fv[e], ds);
-      }
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        s[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], c, row_values(rows, 0, b, r / 4)[r % 4]));
-        ds[r] = (ds[r] + row_values(rows, 1, b, r / 4)[r % 4]) * s[r];
-        if (ahead == 0 && block_row(r) + 4 * (lane >> 5) < (lane & 31)) s[r] = ds[r] = 0.0f;
-      }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const u32x4_t fp = operand(s, h), fs = operand(ds, h);
-#pragma unroll
-        for (int dt = 0; dt < kCols; ++dt) dv[dt] = mfma(read.columns(blk + kBytes, 0, h, dt), fp, dv[dt]);
-#pragma unroll
-        for (int dt = 0; dt < kCols; ++dt) dk[dt] = mfma(read.columns(blk, 0, h, dt), fs, dk[dt]);
-      }
-    }
-  };
-
-  // A whole tile: products n = 0 .. 4 kPhase - 1 in the order S and dP of block 0, of
-  // block 1, sums of block 0, of block 1.
-  constexpr int kAhead = 4;
-  u32x4_t ring[kAhead];
-  auto fragment = [&](MUONH_LDS uint8_t* tile, auto number) __attribute__((always_inline)) {
-    constexpr int n = decltype(number)::value, phase = n / kPhase, i = n % kPhase;
-    MUONH_LDS uint8_t* t = tile + ((phase < 2) == (i & 1) ? kBytes : 0);
-    if constexpr (phase < 2) return read.rows(t, phase & 1, i / 2);
-    else return read.columns(t, phase & 1, i / (2 * kCols), i / 2 % kCols);
-  };
-  auto full = [&](MUONH_LDS uint8_t* tile, MUONH_LDS float* rows, MUONH_LDS uint8_t* next) __attribute__((always_inline)) {
-    f32x16_t s[2], ds[2];
-    u32x4_t fp[2][2], fs[2][2];
+  u32x4_t fp[2], fs[2];   // P and dS of a block
+  // The wavefront's block of a tile: S and dP and their values.
+  auto scores = [&](MUONH_LDS uint8_t* slot, MUONH_LDS float* slot_rows, bool diag) __attribute__((always_inline)) {
+    MUONH_LDS uint8_t* const tile = slot + odd * 32 * DP * 2;
+    MUONH_LDS float* const rows = slot_rows + odd * 32;
+    f32x16_t s = splat(0.0f), ds = splat(0.0f);
+    u32x4_t fq[2], fd[2], fv[2];
+    // the addresses made from this are not worth registers over all blocks
+    asm volatile("" : "+v"(read.row));
     f32x4_t lse[2], del[2];   // of two groups of four rows in turn
-    auto load_values = [&](int b, int j) __attribute__((always_inline)) {
-      lse[j & 1] = row_values(rows, 0, b, j);
-      del[j & 1] = row_values(rows, 1, b, j);
+    auto load_values = [&](int j) __attribute__((always_inline)) {
+      lse[j & 1] = *reinterpret_cast<MUONH_LDS f32x4_t*>(rows + 8 * j + 4 * (lane >> 5));
+      del[j & 1] = *reinterpret_cast<MUONH_LDS f32x4_t*>(rows + kTile + 8 * j + 4 * (lane >> 5));
     };
-    each<4 * kPhase>([&](auto number) __attribute__((always_inline)) {
-      constexpr int n = decltype(number)::value, phase = n / kPhase, i = n % kPhase;
-      const u32x4_t f = ring[n % kAhead];
-      if constexpr (phase < 2) {
-        if constexpr (i < 2) (i & 1 ? ds : s)[phase] = splat(0.0f);
-        if constexpr (i & 1) ds[phase] = mfma(f, fv[i / 2], ds[phase]);
-        else s[phase] = mfma(f, fk[i / 2], s[phase]);
-      } else {
-        constexpr int h = i / (2 * kCols), dt = i / 2 % kCols;
-        if constexpr (i & 1) dk[dt] = mfma(f, fs[phase - 2][h], dk[dt]);
-        else dv[dt] = mfma(f, fp[phase - 2][h], dv[dt]);
-      }
-      constexpr int ahead = (n + kAhead) % (4 * kPhase);
-      ring[n % kAhead] = fragment(ahead == n + kAhead ? tile : next, std::integral_constant<int, ahead>{});
-      // Values of block b beside the products of phase b + 1: none beside the first two,
-      // whose operands the products before have just left.
-      if constexpr ((phase == 1 || phase == 2) && i >= 2) {
-        constexpr int b = phase - 1;
-        each<16>([&](auto reg) __attribute__((always_inline)) {
-          constexpr int r = decltype(reg)::value;
-          if constexpr (r >= 16 * (i - 2) / (kPhase - 2) && r < 16 * (i - 1) / (kPhase - 2)) {
-            s[b][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][r], c, lse[r / 4 & 1][r % 4]));
-            ds[b][r] = (ds[b][r] + del[r / 4 & 1][r % 4]) * s[b][r];
-            if constexpr (r % 4 == 3 && r < 8) load_values(b, r / 4 + 2);
-            if constexpr (r & 1) {
-              fp[b][r / 8][r % 8 / 2] = pack_bf16x2(s[b][r - 1], s[b][r]);
-              fs[b][r / 8][r % 8 / 2] = pack_bf16x2(ds[b][r - 1], ds[b][r]);
-            }
-          }
-        });
-      }
-      if constexpr (n == kPhase - 2 || n == 2 * kPhase - 1) {
-        load_values(phase, 0);
-        load_values(phase, 1);
-      }
+    auto load_step = [&](auto step) __attribute__((always_inline)) {
+      constexpr int e = decltype(step)::value;
+      fq[e & 1] = read.rows(tile, 0, e);
+      fd[e & 1] = read.rows(tile + kBytes, 0, e);
+      fv[e & 1] = read.rows(values, 0, e);
+    };
+    load_step(std::integral_constant<int, 0>{});
+    load_step(std::integral_constant<int, 1>{});
+    __builtin_amdgcn_sched_barrier(0);
+    each<kSteps>([&](auto step) __attribute__((always_inline)) {
+      constexpr int e = decltype(step)::value;
+      s = mfma(fq[e & 1], fk[e], s);
+      ds = mfma(fd[e & 1], fv[e & 1], ds);
+      if constexpr (e + 2 < kSteps) load_step(std::integral_constant<int, e + 2>{});
+      if constexpr (e >= kSteps - 2) load_values(e - (kSteps - 2));
       __builtin_amdgcn_sched_barrier(0);
     });
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      s[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], c, lse[r / 4 & 1][r % 4]));
+      ds[r] = (ds[r] + del[r / 4 & 1][r % 4]) * s[r];
+      if (r == 3 || r == 7) load_values(r / 4 + 2);
+      if (diag && block_row(r) + 4 * (lane >> 5) < (lane & 31)) s[r] = ds[r] = 0.0f;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      fp[h] = operand(s, h);
+      fs[h] = operand(ds, h);
+    }
+    __builtin_amdgcn_sched_barrier(0);
   };
-
-  // Before tile j: tile j + 1 is there for all, and all are done with tile j - 1, whose
-  // slot takes tile j + 2.
-  arrive();
-  fetch(slot_of(1), rows_of(1));
+  // Its sums.
+  auto sums = [&](MUONH_LDS uint8_t* slot) __attribute__((always_inline)) {
+    MUONH_LDS uint8_t* const tile = slot + odd * 32 * DP * 2;
+    asm volatile("" : "+v"(read.tr));
+    u32x4_t ring[4];
+    auto load_sum = [&](auto number) __attribute__((always_inline)) {
+      constexpr int n = decltype(number)::value;
+      ring[n & 3] = read.columns(n & 1 ? tile : tile + kBytes, 0, n / (2 * kCols), n / 2 % kCols);
+    };
+    each<4>(load_sum);
+    each<4 * kCols>([&](auto number) __attribute__((always_inline)) {
+      constexpr int n = decltype(number)::value, h = n / (2 * kCols), dt = n / 2 % kCols;
+      if constexpr (n & 1) dk[dt] = mfma(ring[n & 3], fs[h], dk[dt]);
+      else dv[dt] = mfma(ring[n & 3], fp[h], dv[dt]);
+      if constexpr (n + 4 < 4 * kCols) load_sum(std::integral_constant<int, n + 4>{});
+      if constexpr (n & 1) __builtin_amdgcn_sched_barrier(0);
+    });
+  };
+  // The two wavefronts of a SIMD leave the barriers together, and would come to their
+  // exponentials together: with the even ones first, the odd ones' products run beside
+  // their exponentials and the other way round.
+  if (!odd) __builtin_amdgcn_s_setprio(1);
+  // Own blocks before the keys' do not see them.  Tile t lies in slot t & 1, counted from
+  // the first whole one.
 #pragma unroll 1
-  for (int j = 0; j < own_trips; ++j) {
-    arrive();
-    fetch(slot_of(j + 2), rows_of(j + 2));
-    own(slot_of(j), rows_of(j), owns == 2 ? j & 1 : 0);
+  for (int t = -own_trips, j = 0; t < 0; ++t) {
+    arrive();   // tile t is there, and all are done with the one before
+    MUONH_LDS uint8_t* const slot = t & 1 ? slot1 : slot0;
+    fetch(t & 1 ? slot0 : slot1, t & 1 ? rows0 : rows1);
+    const int ahead = 2 * j + odd - key_block;
+    if (ahead >= 0) {
+      scores(slot, t & 1 ? rows1 : rows0, ahead == 0);
+      sums(slot);
+    }
+    j = j + 1 == owns ? 0 : j + 1;
   }
-  each<kAhead>([&](auto n) __attribute__((always_inline)) { ring[decltype(n)::value] = fragment(slot0, n); });
-  for (int j = 0; j < trips; j += 3) {
-    arrive();
-    fetch(slot2, rows2);
-    full(slot0, rows0, slot1);
-    if (j + 1 >= trips) break;
-    arrive();
-    fetch(slot0, rows0);
-    full(slot1, rows1, slot2);
-    if (j + 2 >= trips) break;
+  for (int t = own_trips; t < trips; t += 2) {
     arrive();
     fetch(slot1, rows1);
-    full(slot2, rows2, slot0);
+    scores(slot0, rows0, false);
+    sums(slot0);
+    if (t + 1 >= trips) break;
+    arrive();
+    fetch(slot0, rows0);
+    scores(slot1, rows1, false);
+    sums(slot1);
   }
-  arrive();   // no load into LDS outlives the workgroup
-  if (row + (lane & 31) >= at.len) return;
-  const int64_t t = at.start + row;
-  store_rows<DP>(g.dk + t * g.lddk + kv * p.dim, g.lddk, p.dim, dk, p.scale, lane);
-  store_rows<DP>(g.dv + t * g.lddv + kv * p.dim, g.lddv, p.dim, dv, 1.0f, lane);
+  // The odd blocks' sums through the slots: dk, then dv.
+  MUONH_LDS f32x4_t* const part = (MUONH_LDS f32x4_t*)(key_block & 1 ? slot1 : slot0) + (key_block >> 1) * kCols * 4 * 64 + lane;
+  static_assert(2 * kCols * 4 * 64 * 16 <= 2 * kBytes, "two wavefronts' sums fill a slot");
+  auto join = [&](f32x16_t (&sum)[kCols]) __attribute__((always_inline)) {
+    arrive();   // all are done with what the slots held; no load into them is on its way
+    if (odd) {
+#pragma unroll
+      for (int dt = 0; dt < kCols; ++dt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          part[(dt * 4 + j) * 64] = f32x4_t{sum[dt][4 * j], sum[dt][4 * j + 1], sum[dt][4 * j + 2], sum[dt][4 * j + 3]};
+    }
+    arrive();
+    if (!odd) {
+#pragma unroll
+      for (int dt = 0; dt < kCols; ++dt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const f32x4_t o = part[(dt * 4 + j) * 64];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sum[dt][4 * j + e] += o[e];
+        }
+    }
+  };
+  join(dk);
+  join(dv);
+  if (odd || row + (lane & 31) >= at.len) return;
+  const int64_t first = at.start + row;
+  store_rows<DP>(g.dk + first * g.lddk + kv * p.dim, g.lddk, p.dim, dk, p.scale, lane);
+  store_rows<DP>(g.dv + first * g.lddv + kv * p.dim, g.lddv, p.dim, dv, 1.0f, lane);
 }
 
 }  // namespace
@@ -769,8 +764,8 @@ hipError_t launch_attention_backward(const AttentionGradArgs& g, hipStream_t st)
   else hipLaunchKernelGGL(attention_dq_kernel<128>, rows, dim3(kThreads), 0, st, g);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (g.a.dim <= 64) hipLaunchKernelGGL(attention_dkv_kernel<64>, keys, dim3(kThreads), 0, st, g);
-  else hipLaunchKernelGGL(attention_dkv_kernel<128>, keys, dim3(kThreads), 0, st, g);
+  if (g.a.dim <= 64) hipLaunchKernelGGL(attention_dkv_kernel<64>, keys, dim3(kKeyThreads), 0, st, g);
+  else hipLaunchKernelGGL(attention_dkv_kernel<128>, keys, dim3(kKeyThreads), 0, st, g);
   return hipGetLastError();
 }
 
