@@ -52,7 +52,7 @@ int check_shape(const muonh_attention_args& g) {
     return fail(MUONH_EINVAL, "heads must be a multiple of kv_heads, both at least 1");
   if (g.dim < 8 || g.dim > 128 || g.dim % 8 != 0) return fail(MUONH_EINVAL, "dim must be 8, 16, .. 128");
   if (!(g.scale > 0.0f) || !std::isfinite(g.scale)) return fail(MUONH_EINVAL, "scale must be > 0 and finite");
-  if (attention_blocks(g.tokens, g.sequences) * kAttentionThreads > kMaxThreads / g.heads)
+  if (attention_blocks(g.tokens, g.sequences, kAttentionRows) * 2 * kAttentionThreads > kMaxThreads / g.heads)
     return fail(MUONH_EINVAL, "tokens, sequences and heads are too many for one launch");
   return MUONH_OK;
 }
@@ -80,7 +80,6 @@ AttentionArgs device_args(const muonh_attention_args& g) {
   a.heads = g.heads;
   a.kv_heads = g.kv_heads;
   a.dim = g.dim;
-  a.blocks = (int32_t)attention_blocks(g.tokens, g.sequences);
   a.scale = g.scale;
   return a;
 }

@@ -7,7 +7,8 @@
 namespace muonh {
 
 constexpr int kAttentionThreads = 256;
-constexpr int kAttentionRows = 128;   // rows of a workgroup
+constexpr int kAttentionRows = 128;   // rows of a workgroup, where there are enough of them
+constexpr int64_t kAttentionCus = 256;
 
 struct AttentionArgs {
   const uint16_t* q;
@@ -18,7 +19,7 @@ struct AttentionArgs {
   const int32_t* cu;              // [sequences + 1]
   int64_t ldq, ldk, ldv, ldo;     // elements between tokens
   int32_t tokens, sequences, heads, kv_heads, dim;
-  int32_t blocks;                 // attention_blocks()
+  int32_t blocks;                 // set by the launchers: attention_blocks() of the kernel's rows
   float scale;
 };
 struct AttentionGradArgs {
@@ -31,8 +32,8 @@ struct AttentionGradArgs {
   float* row_lse;                 // [heads][tokens]: -lse log2 e
   float* row_delta;               // [heads][tokens]: -delta
 };
-// Blocks of 128 rows of any sequences in so many tokens, each sequence's last one cut.
-inline int64_t attention_blocks(int64_t tokens, int64_t sequences) { return tokens / kAttentionRows + sequences; }
+// Blocks of `rows` rows of any sequences in so many tokens, each sequence's last one cut.
+inline int64_t attention_blocks(int64_t tokens, int64_t sequences, int64_t rows) { return tokens / rows + sequences; }
 
 hipError_t launch_attention_forward(const AttentionArgs& a, hipStream_t st);
 hipError_t launch_attention_backward(const AttentionGradArgs& g, hipStream_t st);

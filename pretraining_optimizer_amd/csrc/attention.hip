@@ -42,7 +42,6 @@ typedef short i16x4_t __attribute__((ext_vector_type(4)));
 #define MUONH_LDS __attribute__((address_space(3)))
 
 constexpr int kThreads = kAttentionThreads;
-constexpr int kBlock = kAttentionRows;   // rows of a workgroup: 32 per wavefront
 constexpr int kTile = 64;                // rows of a tile in LDS
 constexpr int kBufferConfig = 0x00020000;
 constexpr int kBehind = (int)0x80000000;  // an offset behind every descriptor's range
@@ -193,13 +192,13 @@ __device__ __forceinline__ void load_operand(u32x4_t (&f)[DP / 16], const Rows& 
   }
 }
 
-// The sequence and the place in it of a workgroup's rows: the block of the rank-th most
-// work, counted in blocks seen (KEYS = false: up to its own; true: from its own on).
+// The sequence and the place in it of a workgroup's ROWS rows: the block of the rank-th
+// most work, counted in blocks seen (KEYS = false: up to its own; true: from its own on).
 // Long ones first, the short ones fill the gaps at the end (documents of 8192 tokens, gradients:
 // 349 us in the sequences' order).  With n_b blocks in sequence b, count(h) = sum_b
 // max(0, n_b - h + 1) blocks see h or more, so the rank's h is the largest with count(h) >
 // rank; a lane per sequence evaluates it.  More than 64 sequences keep their order:
-// blocks are numbered from cu[b] / 128 + b on, which leaves room for the last, cut one.
+// blocks are numbered from cu[b] / ROWS + b on, which leaves room for the last, cut one.
 //
 // Ends are taken into [0, tokens], so no cu_seqlens reads or writes outside the tensors.
 struct Place {
@@ -219,7 +218,7 @@ __device__ __forceinline__ int wave_sum(int v) {
   return __builtin_amdgcn_readlane(v, 63);
 }
 
-template <bool KEYS>
+template <bool KEYS, int ROWS>
 __device__ __forceinline__ Place find_place(const AttentionArgs& p, int rank) {
   const int lane = threadIdx.x & 63;
   if (p.sequences > 64) {
@@ -227,11 +226,11 @@ __device__ __forceinline__ Place find_place(const AttentionArgs& p, int rank) {
     int lo = 0, hi = p.sequences - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (sequence_end(p, mid) / kBlock + mid <= block) lo = mid;
+      if (sequence_end(p, mid) / ROWS + mid <= block) lo = mid;
       else hi = mid - 1;
     }
     const int s = sequence_end(p, lo), e = max(sequence_end(p, lo + 1), s);
-    const int64_t row = ((int64_t)block - s / kBlock - lo) * kBlock;
+    const int64_t row = ((int64_t)block - s / ROWS - lo) * ROWS;
     return Place{s, e - s, row < 0 || row >= e - s ? -1 : (int)row};
   }
   int s = 0, e = 0;
@@ -239,7 +238,7 @@ __device__ __forceinline__ Place find_place(const AttentionArgs& p, int rank) {
     s = sequence_end(p, lane);
     e = max(sequence_end(p, lane + 1), s);
   }
-  const int n = (e - s + kBlock - 1) / kBlock;
+  const int n = (e - s + ROWS - 1) / ROWS;
   int h = __builtin_amdgcn_readlane(n, 0) - rank, b = 0;   // of one sequence
   if (p.sequences > 1) {
     int top = p.blocks;
@@ -258,7 +257,7 @@ __device__ __forceinline__ Place find_place(const AttentionArgs& p, int rank) {
   if (h < 1) return Place{0, 0, -1};
   s = __builtin_amdgcn_readlane(s, b);
   e = __builtin_amdgcn_readlane(e, b);
-  return Place{s, e - s, (KEYS ? __builtin_amdgcn_readlane(n, b) - h : h - 1) * kBlock};
+  return Place{s, e - s, (KEYS ? __builtin_amdgcn_readlane(n, b) - h : h - 1) * ROWS};
 }
 
 // Workgroup i's key head, head of its group and rank.  Workgroups i, i + 8, .. run on one
@@ -274,20 +273,44 @@ __device__ __forceinline__ Item item_of(int kv_heads, int group) {
 
 // Where the lane's results lie: column l % 32 is a row of the tensor, registers 4 j ..
 // of block dt are 4 consecutive columns of it.
+__device__ __forceinline__ void store_columns(uint16_t* base, int64_t ld, int dim, int dt, const f32x16_t& acc,
+                                              float factor, int lane) {
+  uint16_t* out = base + (lane & 31) * ld + 4 * (lane >> 5) + 32 * dt;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (32 * dt + 8 * j < dim) {
+      u32x2_t w;
+      w[0] = pack_bf16x2(acc[4 * j] * factor, acc[4 * j + 1] * factor);
+      w[1] = pack_bf16x2(acc[4 * j + 2] * factor, acc[4 * j + 3] * factor);
+      st_global<u32x2_t>(out + 8 * j, w);
+    }
+}
 template <int DP>
 __device__ __forceinline__ void store_rows(uint16_t* base, int64_t ld, int dim, const f32x16_t (&acc)[DP / 32],
                                            float factor, int lane) {
-  uint16_t* out = base + (lane & 31) * ld + 4 * (lane >> 5);
+#pragma unroll
+  for (int dt = 0; dt < DP / 32; ++dt) store_columns(base, ld, dim, dt, acc[dt], factor, lane);
+}
+
+// One wavefront's sums in LDS: block dt, registers 4 j .. + 3 of lane l at (4 dt + j) 64 + l.
+typedef MUONH_LDS f32x4_t* SumsInLds;
+template <int DP>
+__device__ __forceinline__ void put_sums(SumsInLds at, const f32x16_t (&sum)[DP / 32], int lane) {
 #pragma unroll
   for (int dt = 0; dt < DP / 32; ++dt)
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (32 * dt + 8 * j < dim) {
-        u32x2_t w;
-        w[0] = pack_bf16x2(acc[dt][4 * j] * factor, acc[dt][4 * j + 1] * factor);
-        w[1] = pack_bf16x2(acc[dt][4 * j + 2] * factor, acc[dt][4 * j + 3] * factor);
-        st_global<u32x2_t>(out + 32 * dt + 8 * j, w);
-      }
+      at[(4 * dt + j) * 64 + lane] = f32x4_t{sum[dt][4 * j], sum[dt][4 * j + 1], sum[dt][4 * j + 2], sum[dt][4 * j + 3]};
+}
+__device__ __forceinline__ f32x16_t take_sums(SumsInLds at, int dt, int lane) {
+  f32x16_t v;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const f32x4_t q = at[(4 * dt + j) * 64 + lane];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[4 * j + e] = q[e];
+  }
+  return v;
 }
 
 // Whether any of the wavefront's values is an infinity or a NaN.
@@ -302,24 +325,28 @@ __device__ __forceinline__ bool has_special(u32x4_t v) {
 // lane), and passes over the keys once with a running maximum and sum.  The output is
 // rescaled only where a maximum has grown by more than 2^8 since the last time: until
 // then the probabilities are up to 2^8 too large, which neither bf16 nor fp32 minds.
-template <int DP>
-__global__ __launch_bounds__(kThreads, 2) void attention_forward_kernel(AttentionArgs p) {
-  constexpr int kBytes = kTile * DP * 2;
+//
+// SPLIT: a workgroup has 32 rows and its wavefronts every fourth block of 32 keys each,
+// whose sums are joined in LDS.  The chain of one wavefront is a quarter as long, for
+// four times the loads: for problems of few workgroups (rows_split()).
+template <int DP, bool SPLIT>
+__global__ __launch_bounds__(kThreads, SPLIT ? 1 : 2) void attention_forward_kernel(AttentionArgs p) {
+  constexpr int kKeys = SPLIT ? 4 * 32 : kTile, kBytes = kKeys * DP * 2, kCols = DP / 32;
   __shared__ __attribute__((aligned(1024))) uint8_t lds0[2 * kBytes], lds1[2 * kBytes];
   MUONH_LDS uint8_t *const slot0 = (MUONH_LDS uint8_t*)lds0, *const slot1 = (MUONH_LDS uint8_t*)lds1;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int group = p.heads / p.kv_heads;
   const Item item = item_of(p.kv_heads, group);
   const int kv = item.kv, head = kv * group + item.member;
-  const Place at = find_place<false>(p, item.rank);
+  const Place at = find_place<false, SPLIT ? 32 : kAttentionRows>(p, item.rank);
   if (at.row < 0) return;
 
   const Rows q{p.q + at.start * p.ldq + head * p.dim, p.ldq, at.len, p.dim};
   const Rows k{p.k + at.start * p.ldk + kv * p.dim, p.ldk, at.len, p.dim};
   const Rows v{p.v + at.start * p.ldv + kv * p.dim, p.ldv, at.len, p.dim};
-  const int row = at.row + 32 * wave;   // the wavefront's first
-  const int tiles = (min(at.len, at.row + kBlock) + kTile - 1) / kTile;
-  const TileLoad<DP> load_k(p.ldk, p.dim, wave, lane), load_v(p.ldv, p.dim, wave, lane);
+  const int row = SPLIT ? at.row : at.row + 32 * wave;   // the wavefront's first
+  const int tiles = (min(at.len, at.row + (SPLIT ? 32 : kAttentionRows)) + kKeys - 1) / kKeys;
+  const TileLoad<DP, kKeys> load_k(p.ldk, p.dim, wave, lane), load_v(p.ldv, p.dim, wave, lane);
   const TileRead<DP> read(lane);
   load_k(k, 0, slot0, wave);
   load_v(v, 0, slot0 + kBytes, wave);
@@ -364,11 +391,13 @@ __global__ __launch_bounds__(kThreads, 2) void attention_forward_kernel(Attentio
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[dt][r] *= f;
     }
+    // where all scores so far are -inf the maximum is no number to subtract
+    const float base = fmaxf(top, -3.4028235e38f);
 #pragma unroll
     for (int b = 0; b < N; ++b)
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        s[b][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][r], c, -top));
+        s[b][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][r], c, -base));
         sum += s[b][r];
       }
 #pragma unroll
@@ -409,13 +438,61 @@ __global__ __launch_bounds__(kThreads, 2) void attention_forward_kernel(Attentio
   };
   auto fetch = [&](MUONH_LDS uint8_t* tile, int j) __attribute__((always_inline)) {
     if (j < tiles) {
-      load_k(k, j * kTile, tile, wave);
-      load_v(v, j * kTile, tile + kBytes, wave);
+      load_k(k, j * kKeys, tile, wave);
+      load_v(v, j * kKeys, tile + kBytes, wave);
     }
   };
-  // The tiles before the workgroup's rows are seen whole by all of them, an even number.
   constexpr std::integral_constant<int, 1> one{};
   constexpr std::integral_constant<int, 2> two{};
+  if constexpr (SPLIT) {
+    __shared__ float stats[2][4][64];
+    auto use = [&](MUONH_LDS uint8_t* tile, int j) __attribute__((always_inline)) {
+      const int block = 4 * j + wave, own = at.row / 32;
+      MUONH_LDS uint8_t* const mine = tile + wave * 32 * DP * 2;
+      if (block < own) step(mine, one, std::false_type{});
+      else if (block == own) step(mine, one, std::true_type{});
+    };
+    for (int j = 0; j < tiles; j += 2) {
+      arrive();   // the tile is there, and every wavefront has read the other
+      fetch(slot1, j + 1);
+      use(slot0, j);
+      if (j + 1 >= tiles) break;
+      arrive();
+      fetch(slot0, j + 2);
+      use(slot1, j + 1);
+    }
+    stats[0][wave][lane] = top;
+    stats[1][wave][lane] = pair_sum(sum);
+    arrive();   // all are done with the slots, which take the sums
+    auto part = [&](int w) { return (SumsInLds)(w & 1 ? slot1 : slot0) + (w >> 1) * kCols * 4 * 64; };
+    static_assert(2 * kCols * 4 * 64 * 16 <= 2 * kBytes, "two wavefronts' sums fill a slot");
+    put_sums<DP>(part(wave), acc, lane);
+    arrive();
+    float most = stats[0][0][lane], total = 0.0f, factor[4];
+#pragma unroll
+    for (int w = 1; w < 4; ++w) most = fmaxf(most, stats[0][w][lane]);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      factor[w] = __builtin_amdgcn_exp2f(stats[0][w][lane] - most);   // 0 of a wavefront without keys
+      total += factor[w] * stats[1][w][lane];
+    }
+    if (row + (lane & 31) >= at.len) return;
+    const int64_t t = at.start + row;
+    for (int dt = wave; dt < kCols; dt += 4) {   // the columns over the wavefronts
+      f32x16_t v = splat(0.0f);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const f32x16_t o = take_sums(part(w), dt, lane);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) v[r] += factor[w] * o[r];
+      }
+      store_columns(p.out + t * p.ldo + head * p.dim, p.ldo, p.dim, dt, v, 1.0f / total, lane);
+    }
+    if (wave == 0 && lane < 32)
+      p.lse[head * (int64_t)p.tokens + t + lane] = (most + __builtin_amdgcn_logf(total)) * (1.0f / kLog2e);
+    return;
+  }
+  // The tiles before the workgroup's rows are seen whole by all of them, an even number.
   const int whole = at.row / kTile;
   for (int j = 0; j < whole; j += 2) {
     arrive();   // the tile is there, and every wavefront has read the other
@@ -445,17 +522,17 @@ __global__ __launch_bounds__(kThreads, 2) void attention_forward_kernel(Attentio
 
 // Gradient of q, row by row as in the forward pass: S and dP from k and v, dq from dS and k.
 // It also leaves what the other kernel needs of each row: -lse log2 e and -delta.
-template <int DP>
-__global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttentionGradArgs g) {
+template <int DP, bool SPLIT>
+__global__ __launch_bounds__(kThreads, SPLIT ? 1 : 2) void attention_dq_kernel(AttentionGradArgs g) {
   const AttentionArgs& p = g.a;
-  constexpr int kBytes = kTile * DP * 2;
+  constexpr int kKeys = SPLIT ? 4 * 32 : kTile, kBytes = kKeys * DP * 2, kCols = DP / 32;
   __shared__ __attribute__((aligned(1024))) uint8_t lds0[2 * kBytes], lds1[2 * kBytes];
   MUONH_LDS uint8_t *const slot0 = (MUONH_LDS uint8_t*)lds0, *const slot1 = (MUONH_LDS uint8_t*)lds1;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int group = p.heads / p.kv_heads;
   const Item item = item_of(p.kv_heads, group);
   const int kv = item.kv, head = kv * group + item.member;
-  const Place at = find_place<false>(p, item.rank);
+  const Place at = find_place<false, SPLIT ? 32 : kAttentionRows>(p, item.rank);
   if (at.row < 0) return;
 
   const Rows q{p.q + at.start * p.ldq + head * p.dim, p.ldq, at.len, p.dim};
@@ -463,9 +540,9 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttentionGrad
   const Rows v{p.v + at.start * p.ldv + kv * p.dim, p.ldv, at.len, p.dim};
   const Rows o{p.out + at.start * p.ldo + head * p.dim, p.ldo, at.len, p.dim};
   const Rows d{g.dout + at.start * g.lddo + head * p.dim, g.lddo, at.len, p.dim};
-  const int row = at.row + 32 * wave;
-  const int tiles = (min(at.len, at.row + kBlock) + kTile - 1) / kTile;
-  const TileLoad<DP> load_k(p.ldk, p.dim, wave, lane), load_v(p.ldv, p.dim, wave, lane);
+  const int row = SPLIT ? at.row : at.row + 32 * wave;
+  const int tiles = (min(at.len, at.row + (SPLIT ? 32 : kAttentionRows)) + kKeys - 1) / kKeys;
+  const TileLoad<DP, kKeys> load_k(p.ldk, p.dim, wave, lane), load_v(p.ldv, p.dim, wave, lane);
   const TileRead<DP> read(lane);
   load_k(k, 0, slot0, wave);
   load_v(v, 0, slot0 + kBytes, wave);
@@ -488,7 +565,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttentionGrad
         delta = __builtin_fmaf(__uint_as_float(fo[s][w] & 0xffff0000u), __uint_as_float(fd[s][w] & 0xffff0000u), delta);
       }
     delta = -pair_sum(delta);
-    if (live && lane < 32) {
+    if (live && lane < 32 && (!SPLIT || wave == 0)) {
       g.row_lse[t] = lse;
       g.row_delta[t] = delta;
     }
@@ -521,10 +598,43 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttentionGrad
   };
   auto fetch = [&](MUONH_LDS uint8_t* tile, int j) __attribute__((always_inline)) {
     if (j < tiles) {
-      load_k(k, j * kTile, tile, wave);
-      load_v(v, j * kTile, tile + kBytes, wave);
+      load_k(k, j * kKeys, tile, wave);
+      load_v(v, j * kKeys, tile + kBytes, wave);
     }
   };
+  if constexpr (SPLIT) {
+    auto use = [&](MUONH_LDS uint8_t* tile, int j) __attribute__((always_inline)) {
+      const int own = at.row / 32 - 4 * j;
+      if (wave < own) block(tile, wave, std::false_type{});
+      else if (wave == own) block(tile, wave, std::true_type{});
+    };
+    for (int j = 0; j < tiles; j += 2) {
+      arrive();
+      fetch(slot1, j + 1);
+      use(slot0, j);
+      if (j + 1 >= tiles) break;
+      arrive();
+      fetch(slot0, j + 2);
+      use(slot1, j + 1);
+    }
+    arrive();   // all are done with the slots, which take the sums
+    auto part = [&](int w) { return (SumsInLds)(w & 1 ? slot1 : slot0) + (w >> 1) * kCols * 4 * 64; };
+    static_assert(2 * kCols * 4 * 64 * 16 <= 2 * kBytes, "two wavefronts' sums fill a slot");
+    put_sums<DP>(part(wave), acc, lane);
+    arrive();
+    if (!live) return;
+    for (int dt = wave; dt < kCols; dt += 4) {   // the columns over the wavefronts
+      f32x16_t v = take_sums(part(0), dt, lane);
+#pragma unroll
+      for (int w = 1; w < 4; ++w) {
+        const f32x16_t o = take_sums(part(w), dt, lane);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) v[r] += o[r];
+      }
+      store_columns(g.dq + (at.start + row) * g.lddq + head * p.dim, g.lddq, p.dim, dt, v, p.scale, lane);
+    }
+    return;
+  }
   auto full = [&](MUONH_LDS uint8_t* tile) __attribute__((always_inline)) {
     block(tile, 0, std::false_type{});
     block(tile, 1, std::false_type{});
@@ -557,11 +667,12 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttentionGrad
 }
 
 // Gradients of k and v: a wavefront holds 32 rows of both and passes over the rows of
-// q and dout that see them, head by head of the group.  Eight wavefronts have 128 rows
-// of keys: w and w + 4 the same 32, for the even and the odd blocks of 32 rows, and their sums
-// are added at the end, the odd blocks' to the even ones'.  That halves the longest
-// workgroup, which sequences of different lengths wait for (documents of 8192 tokens,
-// 16/8 heads of 128: 175 us with four wavefronts on all blocks).
+// q and dout that see them, head by head of the group.  Eight wavefronts have BLOCKS blocks
+// of 32 keys: w, w + BLOCKS, .. the same, each for every PARTS-th block of rows, and their
+// sums are added at the end in order.  That shortens the longest workgroup, which
+// sequences of different lengths wait for (documents of 8192 tokens, 16/8 heads of 128: 4
+// blocks in two parts 164 us, four wavefronts on all rows 175); problems of few
+// workgroups take 2 blocks in four parts (keys_split()).
 //
 // Two wavefronts per SIMD, so one's products overlap the other's exponentials: a product
 // takes 32 cycles and about 9 other instructions of 4 each go with it.  Of at most 256
@@ -569,46 +680,50 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttentionGrad
 // in LDS beside the two slots.  Operands come out of LDS two steps, or four products,
 // ahead.
 constexpr int kKeyThreads = 512;
-template <int DP>
+template <int DP, int BLOCKS>
 __global__ __launch_bounds__(kKeyThreads, 2) void attention_dkv_kernel(AttentionGradArgs g) {
   const AttentionArgs& p = g.a;
-  constexpr int kBytes = kTile * DP * 2, kSteps = DP / 16, kCols = DP / 32, kWaves = kKeyThreads / 64;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds0[2 * kBytes], lds1[2 * kBytes], ldsv[kBlock * DP * 2];
-  __shared__ __attribute__((aligned(16))) float ldsr0[kWaves * kTile], ldsr1[kWaves * kTile];
+  constexpr int kWaves = kKeyThreads / 64, kParts = kWaves / BLOCKS, kKeys = 32 * BLOCKS, kRows = 32 * kParts;
+  constexpr int kBytes = kRows * DP * 2, kSteps = DP / 16, kCols = DP / 32;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds0[2 * kBytes], lds1[2 * kBytes], ldsv[kKeys * DP * 2];
+  // -lse and -delta of a tile's rows, 64 at a time, and a place for loads of nothing
+  constexpr int kRowLoads = kRows / 64, kRowValues = (kWaves > 2 * kRowLoads ? kWaves : 2 * kRowLoads) * 64;
+  __shared__ __attribute__((aligned(16))) float ldsr0[kRowValues], ldsr1[kRowValues];
   MUONH_LDS uint8_t *const slot0 = (MUONH_LDS uint8_t*)lds0, *const slot1 = (MUONH_LDS uint8_t*)lds1;
   MUONH_LDS float *const rows0 = (MUONH_LDS float*)ldsr0, *const rows1 = (MUONH_LDS float*)ldsr1;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int key_block = wave & 3, odd = wave >> 2;
+  const int key_block = wave % BLOCKS, part = wave / BLOCKS;
   const int group = p.heads / p.kv_heads;
   const Item item = item_of(p.kv_heads, 1);
   const int kv = item.kv;
-  const Place at = find_place<true>(p, item.rank);
+  const Place at = find_place<true, kKeys>(p, item.rank);
   if (at.row < 0) return;
 
   const Rows k{p.k + at.start * p.ldk + kv * p.dim, p.ldk, at.len, p.dim};
   const Rows v{p.v + at.start * p.ldv + kv * p.dim, p.ldv, at.len, p.dim};
   const int row = at.row + 32 * key_block;
-  const TileLoad<DP, kTile, kWaves> load_q(p.ldq, p.dim, wave, lane), load_d(g.lddo, p.dim, wave, lane);
-  const TileLoad<DP, kBlock, kWaves> load_v(p.ldv, p.dim, wave, lane);
+  const TileLoad<DP, kRows, kWaves> load_q(p.ldq, p.dim, wave, lane), load_d(g.lddo, p.dim, wave, lane);
+  const TileLoad<DP, kKeys, kWaves> load_v(p.ldv, p.dim, wave, lane);
   TileRead<DP> read(lane);
   // The tiles of q and dout: first those of the workgroup's own rows, head by head, then
   // the ones behind them, which see all of its keys, head by head.  Rows behind the end
   // arrive as zeros: P = exp 0, but dout, delta and q are 0.  Behind the last tile zeros are
   // loaded, from nowhere.
-  const int first_tile = at.row / kTile, tiles = (at.len + kTile - 1) / kTile - first_tile, owns = min(tiles, 2);
+  const int tiles = (at.len - at.row + kRows - 1) / kRows, owns = min(tiles, (kKeys + kRows - 1) / kRows);
   const int own_trips = owns * group, trips = tiles * group;
   int lh = 0, lt = 0, lo = 0, hi = owns;   // the next to load: its head and tile, the stage's tiles
   auto fetch = [&](MUONH_LDS uint8_t* tile, MUONH_LDS float* rows) __attribute__((always_inline)) {
-    const int first = (first_tile + lt) * kTile, h = min(lh, group - 1);
+    const int first = at.row + lt * kRows, h = min(lh, group - 1);
     const Rows q{p.q + at.start * p.ldq + (kv * group + h) * p.dim, p.ldq, lh < group ? at.len : 0, p.dim};
     const Rows d{g.dout + at.start * g.lddo + (kv * group + h) * p.dim, g.lddo, lh < group ? at.len : 0, p.dim};
     load_q(q, first, tile, wave);
     load_d(d, first, tile + kBytes, wave);
-    // wavefront 0: -lse, 1: -delta (the others to where nobody reads)
-    const float* src = (wave & 1 ? g.row_delta : g.row_lse) + (kv * group + h) * (int64_t)p.tokens + at.start + first;
-    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<float*>(src), (short)0, lh < group && wave < 2 ? min(kTile, at.len - first) * 4 : 0, kBufferConfig);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (MUONH_LDS void*)(rows + wave * kTile), 4, lane * 4, 0, 0, 0);
+    // wavefronts 0 .. : -lse, then as many: -delta (the others load nothing to where nobody reads)
+    const int at_row = first + wave % kRowLoads * 64, rest = lh < group && wave < 2 * kRowLoads ? at.len - at_row : 0;
+    const float* src = (wave < kRowLoads ? g.row_lse : g.row_delta) + (kv * group + h) * (int64_t)p.tokens + at.start + at_row;
+    const __amdgpu_buffer_rsrc_t r =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(src), (short)0, max(min(64, rest), 0) * 4, kBufferConfig);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (MUONH_LDS void*)(rows + wave * 64), 4, lane * 4, 0, 0, 0);
     const bool turn = lt + 1 == hi, second = turn && lh + 1 == group && lo == 0 && tiles > owns;
     lo = second ? owns : lo;
     hi = second ? tiles : hi;
@@ -628,8 +743,8 @@ __global__ __launch_bounds__(kKeyThreads, 2) void attention_dkv_kernel(Attention
   u32x4_t fp[2], fs[2];   // P and dS of a block
   // The wavefront's block of a tile: S and dP and their values.
   auto scores = [&](MUONH_LDS uint8_t* slot, MUONH_LDS float* slot_rows, bool diag) __attribute__((always_inline)) {
-    MUONH_LDS uint8_t* const tile = slot + odd * 32 * DP * 2;
-    MUONH_LDS float* const rows = slot_rows + odd * 32;
+    MUONH_LDS uint8_t* const tile = slot + part * 32 * DP * 2;
+    MUONH_LDS float* const rows = slot_rows + part * 32;
     f32x16_t s = splat(0.0f), ds = splat(0.0f);
     u32x4_t fq[2], fd[2], fv[2];
     // the addresses made from this are not worth registers over all blocks
@@ -637,7 +752,7 @@ __global__ __launch_bounds__(kKeyThreads, 2) void attention_dkv_kernel(Attention
     f32x4_t lse[2], del[2];   // of two groups of four rows in turn
     auto load_values = [&](int j) __attribute__((always_inline)) {
       lse[j & 1] = *reinterpret_cast<MUONH_LDS f32x4_t*>(rows + 8 * j + 4 * (lane >> 5));
-      del[j & 1] = *reinterpret_cast<MUONH_LDS f32x4_t*>(rows + kTile + 8 * j + 4 * (lane >> 5));
+      del[j & 1] = *reinterpret_cast<MUONH_LDS f32x4_t*>(rows + kRows + 8 * j + 4 * (lane >> 5));
     };
     auto load_step = [&](auto step) __attribute__((always_inline)) {
       constexpr int e = decltype(step)::value;
@@ -672,7 +787,7 @@ __global__ __launch_bounds__(kKeyThreads, 2) void attention_dkv_kernel(Attention
   };
   // Its sums.
   auto sums = [&](MUONH_LDS uint8_t* slot) __attribute__((always_inline)) {
-    MUONH_LDS uint8_t* const tile = slot + odd * 32 * DP * 2;
+    MUONH_LDS uint8_t* const tile = slot + part * 32 * DP * 2;
     asm volatile("" : "+v"(read.tr));
     u32x4_t ring[4];
     auto load_sum = [&](auto number) __attribute__((always_inline)) {
@@ -689,9 +804,9 @@ __global__ __launch_bounds__(kKeyThreads, 2) void attention_dkv_kernel(Attention
     });
   };
   // The two wavefronts of a SIMD leave the barriers together, and would come to their
-  // exponentials together: with the even ones first, the odd ones' products run beside
-  // their exponentials and the other way round.
-  if (!odd) __builtin_amdgcn_s_setprio(1);
+  // exponentials together: with the first half of them first, the others' products run
+  // beside their exponentials and the other way round (172 -> 168 us as above).
+  if (wave < 4) __builtin_amdgcn_s_setprio(1);
   // Own blocks before the keys' do not see them.  Tile t lies in slot t & 1, counted from
   // the first whole one.
 #pragma unroll 1
@@ -699,7 +814,7 @@ __global__ __launch_bounds__(kKeyThreads, 2) void attention_dkv_kernel(Attention
     arrive();   // tile t is there, and all are done with the one before
     MUONH_LDS uint8_t* const slot = t & 1 ? slot1 : slot0;
     fetch(t & 1 ? slot0 : slot1, t & 1 ? rows0 : rows1);
-    const int ahead = 2 * j + odd - key_block;
+    const int ahead = kParts * j + part - key_block;
     if (ahead >= 0) {
       scores(slot, t & 1 ? rows1 : rows0, ahead == 0);
       sums(slot);
@@ -717,33 +832,28 @@ __global__ __launch_bounds__(kKeyThreads, 2) void attention_dkv_kernel(Attention
     scores(slot1, rows1, false);
     sums(slot1);
   }
-  // The odd blocks' sums through the slots: dk, then dv.
-  MUONH_LDS f32x4_t* const part = (MUONH_LDS f32x4_t*)(key_block & 1 ? slot1 : slot0) + (key_block >> 1) * kCols * 4 * 64 + lane;
-  static_assert(2 * kCols * 4 * 64 * 16 <= 2 * kBytes, "two wavefronts' sums fill a slot");
+  // The parts' sums through the slots: dk, then dv.
+  constexpr int kSums = kCols * 4 * 64;   // of one wavefront
+  static_assert((kParts - 1) * BLOCKS * kSums * 16 <= 2 * 2 * kBytes, "all but the first part's fit the slots");
+  constexpr int kInSlot = 2 * kBytes / (kSums * 16);
+  auto place = [&](int i) { return (SumsInLds)(i < kInSlot ? slot0 : slot1) + i % kInSlot * kSums; };
   auto join = [&](f32x16_t (&sum)[kCols]) __attribute__((always_inline)) {
     arrive();   // all are done with what the slots held; no load into them is on its way
-    if (odd) {
-#pragma unroll
-      for (int dt = 0; dt < kCols; ++dt)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          part[(dt * 4 + j) * 64] = f32x4_t{sum[dt][4 * j], sum[dt][4 * j + 1], sum[dt][4 * j + 2], sum[dt][4 * j + 3]};
-    }
+    if (part > 0) put_sums<DP>(place((part - 1) * BLOCKS + key_block), sum, lane);
     arrive();
-    if (!odd) {
+    if (part == 0)
 #pragma unroll
       for (int dt = 0; dt < kCols; ++dt)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const f32x4_t o = part[(dt * 4 + j) * 64];
+        for (int o = 0; o < kParts - 1; ++o) {
+          const f32x16_t more = take_sums(place(o * BLOCKS + key_block), dt, lane);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sum[dt][4 * j + e] += o[e];
+          for (int r = 0; r < 16; ++r) sum[dt][r] += more[r];
         }
-    }
   };
   join(dk);
   join(dv);
-  if (odd || row + (lane & 31) >= at.len) return;
+  if (part > 0 || row + (lane & 31) >= at.len) return;
   const int64_t first = at.start + row;
   store_rows<DP>(g.dk + first * g.lddk + kv * p.dim, g.lddk, p.dim, dk, p.scale, lane);
   store_rows<DP>(g.dv + first * g.lddv + kv * p.dim, g.lddv, p.dim, dv, 1.0f, lane);
@@ -751,22 +861,49 @@ __global__ __launch_bounds__(kKeyThreads, 2) void attention_dkv_kernel(Attention
 
 }  // namespace
 
-hipError_t launch_attention_forward(const AttentionArgs& a, hipStream_t st) {
-  const dim3 grid((unsigned)((int64_t)a.blocks * a.heads));
-  if (a.dim <= 64) hipLaunchKernelGGL(attention_forward_kernel<64>, grid, dim3(kThreads), 0, st, a);
-  else hipLaunchKernelGGL(attention_forward_kernel<128>, grid, dim3(kThreads), 0, st, a);
+// Whether the kernels are to have smaller blocks.  Measured, forward / both gradients in us
+// (blocks of 128 x heads, then smaller and large ones):
+//   rows: 1000 tokens, 8 heads of 128 (64): 17.6 and 23.1; 2000 tokens, 8 heads (128): 38.8 and
+//   39.3; 1777 tokens in two sequences, 12 heads of 64 (180): 22.7 and 17.7.  Worth it
+//   while the smaller workgroups are one per CU at most.
+//   keys: 1000 tokens, 8 heads of 128 (64): 42.7 and 63.7; 4000 tokens, 4 heads (128): 134 and 200;
+//   1777 tokens, 12 heads of 64 (180): 38.6 and 43.2; 1777 tokens, 16/8 heads of 128 (120):
+//   88.6 and 91.5.  Worth it while the large ones are less than one per CU.
+static bool rows_split(const AttentionArgs& a) {
+  return 4 * attention_blocks(a.tokens, a.sequences, kAttentionRows) * a.heads <= kAttentionCus;
+}
+static bool keys_split(const AttentionArgs& a) {
+  return attention_blocks(a.tokens, a.sequences, kAttentionRows) * a.kv_heads < kAttentionCus;
+}
+
+// A kernel over blocks of `rows` rows of so many heads.
+template <typename K, typename A>
+static hipError_t launch_blocks(K kernel, A args, AttentionArgs& a, int rows, int heads, int threads, hipStream_t st) {
+  a.blocks = (int32_t)attention_blocks(a.tokens, a.sequences, rows);
+  hipLaunchKernelGGL(kernel, dim3((unsigned)((int64_t)a.blocks * heads)), dim3((unsigned)threads), 0, st, args());
   return hipGetLastError();
 }
 
-hipError_t launch_attention_backward(const AttentionGradArgs& g, hipStream_t st) {
-  const dim3 rows((unsigned)((int64_t)g.a.blocks * g.a.heads)), keys((unsigned)((int64_t)g.a.blocks * g.a.kv_heads));
-  if (g.a.dim <= 64) hipLaunchKernelGGL(attention_dq_kernel<64>, rows, dim3(kThreads), 0, st, g);
-  else hipLaunchKernelGGL(attention_dq_kernel<128>, rows, dim3(kThreads), 0, st, g);
-  const hipError_t e = hipGetLastError();
+hipError_t launch_attention_forward(const AttentionArgs& given, hipStream_t st) {
+  AttentionArgs a = given;
+  auto args = [&] { return a; };
+  const bool split = rows_split(a);
+  const auto kernel = a.dim <= 64 ? (split ? attention_forward_kernel<64, true> : attention_forward_kernel<64, false>)
+                                  : (split ? attention_forward_kernel<128, true> : attention_forward_kernel<128, false>);
+  return launch_blocks(kernel, args, a, split ? 32 : kAttentionRows, a.heads, kThreads, st);
+}
+
+hipError_t launch_attention_backward(const AttentionGradArgs& given, hipStream_t st) {
+  AttentionGradArgs g = given;
+  auto args = [&] { return g; };
+  const bool wide = g.a.dim > 64, rows = rows_split(g.a), keys = keys_split(g.a);
+  const auto dq = wide ? (rows ? attention_dq_kernel<128, true> : attention_dq_kernel<128, false>)
+                       : (rows ? attention_dq_kernel<64, true> : attention_dq_kernel<64, false>);
+  const hipError_t e = launch_blocks(dq, args, g.a, rows ? 32 : kAttentionRows, g.a.heads, kThreads, st);
   if (e != hipSuccess) return e;
-  if (g.a.dim <= 64) hipLaunchKernelGGL(attention_dkv_kernel<64>, keys, dim3(kKeyThreads), 0, st, g);
-  else hipLaunchKernelGGL(attention_dkv_kernel<128>, keys, dim3(kKeyThreads), 0, st, g);
-  return hipGetLastError();
+  const auto dkv = wide ? (keys ? attention_dkv_kernel<128, 2> : attention_dkv_kernel<128, 4>)
+                        : (keys ? attention_dkv_kernel<64, 2> : attention_dkv_kernel<64, 4>);
+  return launch_blocks(dkv, args, g.a, keys ? 64 : kAttentionRows, g.a.kv_heads, kKeyThreads, st);
 }
 
 }  // namespace muonh

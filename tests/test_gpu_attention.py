@@ -123,6 +123,64 @@ def test_lengths(lens, heads, kv, dim):
     _both(*_inputs(lens, heads, kv, dim), None, f"{lens}")
 
 
+def _heads_for_large_blocks(lens):
+    """The least heads whose blocks of 128 rows are a workgroup per CU, so that neither
+    the rows' nor the keys' kernels take smaller ones."""
+    return -(-256 // (sum(lens) // 128 + len(lens)))
+
+
+@pytest.mark.parametrize("lens", LENS, ids=lambda v: "+".join(map(str, v)))
+@pytest.mark.parametrize("group,dim", [(1, 128), (2, 64)])
+def test_lengths_in_large_blocks(lens, group, dim):
+    kv = _heads_for_large_blocks(lens)
+    announce(f"attention {lens} {group * kv}/{kv} heads of {dim}")
+    _both(*_inputs(lens, group * kv, kv, dim), None, f"{lens}")
+
+
+@pytest.mark.parametrize("dim", [8, 40, 72, 104])
+def test_head_widths_in_large_blocks(dim):
+    announce(f"attention width {dim}, large blocks")
+    _both(*_inputs([150, 70], 86, 86, dim), 0.2, f"dim {dim}")
+
+
+def test_rows_in_large_blocks_and_keys_in_small_ones():
+    """Many heads that read few key heads."""
+    announce("attention 64/2 heads")
+    _both(*_inputs([530, 260], 64, 2, 64), None, "64/2")
+
+
+def test_more_than_64_sequences():
+    """Their blocks keep the sequences' order; empty ones and single tokens among them."""
+    announce("attention 65 and 200 sequences")
+    _both(*_inputs([37 * i % 131 for i in range(65)], 2, 1, 64), None, "65 sequences")
+    _both(*_inputs([i * i % 17 for i in range(200)], 4, 2, 64), None, "200 sequences")
+    _both(*_inputs([0] * 70 + [300] + [0] * 70 + [1], 4, 4, 128), None, "142 sequences")
+
+
+def test_offsets_beyond_32_bits():
+    """Tokens 2^22 elements apart: the last lie beyond 2^31 elements, and 2^32 bytes."""
+    announce("attention large pitch")
+    lens, heads, kv, dim = [300, 250], 2, 1, 64
+    q, k, v, do, cu = _inputs(lens, heads, kv, dim)
+    want = pm.attention_forward(q, k, v, cu)
+    wantg = pm.attention_backward(do, q, k, v, *want, cu)
+    wide = torch.empty((sum(lens), 1 << 22), dtype=torch.bfloat16, device="cuda")
+    at = 0
+    views = []
+    for t in (q, k, v, do, want[0], q, k, v):
+        n = t.shape[1] * dim
+        views.append(wide[:, at:at + n].unflatten(1, (-1, dim)))
+        views[-1].copy_(t)
+        at += n
+    fq, fk, fv, fdo, fo, gq, gk, gv = views
+    out, lse = pm.attention_forward(fq, fk, fv, cu, out=fo)
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    pm.attention_backward(fdo, fq, fk, fv, out, lse, cu, dq=gq, dk=gk, dv=gv)
+    assert all(torch.equal(a, b) for a, b in zip((gq, gk, gv), wantg))
+    del wide, views
+    torch.cuda.empty_cache()
+
+
 @pytest.mark.parametrize("dim", [8, 16, 24, 32, 40, 56, 64, 72, 80, 96, 104, 120, 128])
 def test_head_widths(dim):
     announce(f"attention width {dim}")
@@ -136,9 +194,10 @@ def test_groups(heads, kv):
 
 
 def test_longer_sequences():
-    """Many tiles per row, more workgroups than one per XCD."""
+    """Many tiles per row, in small and in large blocks."""
     announce("attention 1500+700, 64 sequences")
     _both(*_inputs([1500, 700], 2, 1, 128), None, "1500+700")
+    _both(*_inputs([1100, 700], 16, 16, 128), None, "1100+700")
     _both(*_inputs([13 * i % 97 for i in range(64)], 2, 2, 64), None, "64 sequences")
 
 
@@ -198,21 +257,21 @@ def test_fused_buffers_and_tokens_behind_the_last_sequence(dim):
     assert (fused[:, -8:] == 7).all()
 
 
-@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("dim,kv", [(64, 1), (128, 1), (64, 64)])
 @pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
 @pytest.mark.parametrize("where", [0, 5, 31, 32, 40, 63, 64, 100, 149])
-def test_special_values_reach_later_rows_only(where, value, dim):
+def test_special_values_reach_later_rows_only(where, value, dim, kv):
     """An Inf or NaN in a token's key or value: other sequences keep their results bit
     for bit, earlier rows and other columns theirs (within the tolerances: a block
     with such a value adds its keys one at a time), and the rest is what the formula
     gives."""
-    announce(f"attention {value} at {where}, width {dim}")
-    q, k, v, do, cu = _inputs([20, 150, 30], 2, 1, dim)
+    announce(f"attention {value} at {where}, width {dim}, {kv} key heads")
+    q, k, v, do, cu = _inputs([20, 150, 30], 2 * kv, kv, dim)
     want, wl = pm.attention_forward(q, k, v, cu)
     later = slice(20 + where, 170)
     for t in (k, v):
         bad = t.clone()
-        bad[20 + where, 0, 3] = value
+        bad[20 + where, :, 3] = value
         out, lse = pm.attention_forward(q, bad if t is k else k, bad if t is v else v, cu)
         for s in (slice(0, 20), slice(170, 200)):
             assert torch.equal(out[s], want[s]) and torch.equal(lse[:, s], wl[:, s])
@@ -227,6 +286,21 @@ def test_special_values_reach_later_rows_only(where, value, dim):
                 assert torch.isnan(hit).all() and torch.isnan(hit_lse).all()
             out[later], lse[:, later] = want[later], wl[:, later]
         _check_forward(out, lse, q, k, v, cu, dim ** -0.5, f"{value} at {where}")
+
+
+@pytest.mark.parametrize("kv", [1, 32])
+def test_scores_of_minus_infinity(kv):
+    """Keys whose scores are -inf for every row: rows that see others as well have what
+    the formula gives, in a wavefront that sees only such keys, too."""
+    announce(f"attention minus infinity, {kv} key heads")
+    q, k, v, do, cu = _inputs([200, 90], 2 * kv, kv, 64)
+    q = q.abs() + 0.5
+    k[:96, :, 5] = -float("inf")
+    out, lse = pm.attention_forward(q, k, v, cu)
+    # a row without a finite score is no number
+    assert torch.isnan(out[:96]).all()
+    kept, at = torch.cat([k[96:200], k[200:]]), torch.tensor([0, 104, 194], dtype=torch.int32, device="cuda")
+    _check_forward(out[96:], lse[:, 96:], q[96:], kept, v[96:], at, 64 ** -0.5, "minus infinity")
 
 
 def test_gradients_of_other_sequences_are_kept():
