@@ -861,16 +861,18 @@ __global__ __launch_bounds__(kKeyThreads, 2) void attention_dkv_kernel(Attention
 
 }  // namespace
 
-// Whether the kernels are to have smaller blocks.  Measured, forward / both gradients in us
-// (blocks of 128 x heads, then smaller and large ones):
-//   rows: 1000 tokens, 8 heads of 128 (64): 17.6 and 23.1; 2000 tokens, 8 heads (128): 38.8 and
-//   39.3; 1777 tokens in two sequences, 12 heads of 64 (180): 22.7 and 17.7.  Worth it
-//   while the smaller workgroups are one per CU at most.
-//   keys: 1000 tokens, 8 heads of 128 (64): 42.7 and 63.7; 4000 tokens, 4 heads (128): 134 and 200;
-//   1777 tokens, 12 heads of 64 (180): 38.6 and 43.2; 1777 tokens, 16/8 heads of 128 (120):
-//   88.6 and 91.5.  Worth it while the large ones are less than one per CU.
+// Whether the kernels are to have smaller blocks.  Measured, in us with smaller and with
+// large ones (in brackets: blocks of 128 rows x heads):
+//   rows, forward: 1000 tokens, 8 heads of 128 (64) 17.6 and 23.1; 8000 tokens, 2 heads of 64 (126)
+//   59 and 95; 4 x 300 tokens, 8 heads of 128 (104) 14.5 and 11.9; 1777 tokens in two
+//   sequences, 12 heads of 64 (180) 22.7 and 17.6.  Gradients: 4000 tokens, 4 heads of 128 (128)
+//   134 and 157; (104) 32.8 and 28.7; 1777 tokens, 16 heads of 128 (240) 88.6 and 68.1.
+//   Long sequences win more than short ones lose up to half a workgroup per CU.
+//   keys, gradients: 1000 tokens, 8 heads of 128 (64) 42.7 and 63.7; 4000 tokens, 4 heads (128) 134
+//   and 200; 1777 tokens, 12 heads of 64 (180) 38.6 and 43.2.  Worth it while the large
+//   ones are less than one per CU.
 static bool rows_split(const AttentionArgs& a) {
-  return 4 * attention_blocks(a.tokens, a.sequences, kAttentionRows) * a.heads <= kAttentionCus;
+  return 2 * attention_blocks(a.tokens, a.sequences, kAttentionRows) * a.heads <= kAttentionCus;
 }
 static bool keys_split(const AttentionArgs& a) {
   return attention_blocks(a.tokens, a.sequences, kAttentionRows) * a.kv_heads < kAttentionCus;
