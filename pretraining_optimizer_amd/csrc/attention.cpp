@@ -14,7 +14,7 @@ using namespace muonh;
 
 namespace {
 
-constexpr int64_t kMaxPitch = ((int64_t)1 << 23) - 1;   // 64 rows stay below 2^31 bytes
+constexpr int64_t kMaxPitch = ((int64_t)1 << 23) - 1;   // 128 rows stay below 2^31 bytes
 
 // A tensor [tokens, cols] of bf16 with ld elements between tokens.
 struct Tensor {

@@ -305,6 +305,21 @@ __device__ __forceinline__ void store_sum(const EmbeddingGradArgs& p, uint32_t k
   }
   store8<O>(dst, c, (int)p.cols, a);
 }
+// load8 of one chunk of many rows: first all loads, then what belongs to a row's end.
+struct Chunk {
+  int c, cols, skip;   // skip: elements before c that the load of a row's last eight has
+  __device__ __forceinline__ Chunk(int c, int cols) : c(c), cols(cols), skip(cols >= 8 ? max(c + 8 - cols, 0) : 0) {}
+  template <typename T>
+  __device__ __forceinline__ void load(Raw8<T>& r, const T* row) const {
+    if (cols >= 8) r.load(row + c - skip);
+    else r = load8<T>(row, c, cols);
+  }
+  template <typename T>
+  __device__ __forceinline__ void widen(Raw8<T>& r, float (&v)[8]) const {
+    if (skip > 0) r.drop(skip);
+    r.widen(v);
+  }
+};
 __device__ __forceinline__ void store_partial(float* row, int c, int cols, const float (&sum)[8]) {
   store8<float>(row, c, cols, sum);
 }
@@ -327,6 +342,7 @@ __global__ __launch_bounds__(kThreads) void embedding_sum_kernel(EmbeddingGradAr
   float sum[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
+  const Chunk chunk(c, cols);
   uint32_t current = keys[first];
   bool opened = current == before;   // the current row's tokens began in an earlier run
   constexpr int kAhead = sizeof(T) == 2 ? 16 : 8;   // bf16: all rows of a short run are on their way at once
@@ -340,7 +356,7 @@ __global__ __launch_bounds__(kThreads) void embedding_sum_kernel(EmbeddingGradAr
       place[a] = places[at];
     }
 #pragma unroll
-    for (int a = 0; a < kAhead; ++a) v[a] = load8<T>(dout + (int64_t)place[a] * p.ldd, c, cols);
+    for (int a = 0; a < kAhead; ++a) chunk.load(v[a], dout + (int64_t)place[a] * p.ldd);
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
       if (i + a >= end) break;
@@ -353,7 +369,7 @@ __global__ __launch_bounds__(kThreads) void embedding_sum_kernel(EmbeddingGradAr
         for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
       }
       float x[8];
-      v[a].widen(x);
+      chunk.widen(v[a], x);
 #pragma unroll
       for (int j = 0; j < 8; ++j) sum[j] += x[j];
     }
@@ -390,6 +406,7 @@ __global__ __launch_bounds__(kThreads) void embedding_join_kernel(EmbeddingGradA
 #pragma unroll
   for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
   constexpr int kAhead = 4;
+  const Chunk chunk(c, cols);
   if (c < cols)
     for (int64_t q = r + g; q <= last; q += kAhead * kJoin) {
       Raw8<float> v[kAhead];
@@ -397,12 +414,12 @@ __global__ __launch_bounds__(kThreads) void embedding_join_kernel(EmbeddingGradA
       for (int a = 0; a < kAhead; ++a) {
         const int64_t at = q + a * kJoin;
         v[a].zero();
-        if (at <= last) v[a] = load8<float>(p.partials + (at * 2 + (at == r)) * p.cols, c, cols);
+        if (at <= last) chunk.load(v[a], p.partials + (at * 2 + (at == r)) * p.cols);
       }
 #pragma unroll
       for (int a = 0; a < kAhead; ++a) {
         float x[8];
-        v[a].widen(x);
+        chunk.widen(v[a], x);
 #pragma unroll
         for (int j = 0; j < 8; ++j) sum[j] += x[j];
       }

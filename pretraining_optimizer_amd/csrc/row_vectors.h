@@ -19,6 +19,12 @@ template <> struct Raw8<uint16_t> {
   __device__ __forceinline__ void set(int j, const uint16_t* p) {
     w[j >> 1] |= (uint32_t)ld_global<uint16_t>(p) << (16 * (j & 1));
   }
+  // Elements n .. 7 to the front, zeros behind them; 0 < n < 8.
+  __device__ __forceinline__ void drop(int n) {
+    if (n & 4) w = vec{w[2], w[3], 0, 0};
+    if (n & 2) w = vec{w[1], w[2], w[3], 0};
+    if (n & 1) w = vec{w[0] >> 16 | w[1] << 16, w[1] >> 16 | w[2] << 16, w[2] >> 16 | w[3] << 16, w[3] >> 16};
+  }
   __device__ __forceinline__ void widen(float (&v)[8]) const {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -48,6 +54,20 @@ template <> struct Raw8<float> {
     if (j < 4) lo[j] = v;
     else hi[j - 4] = v;
   }
+  __device__ __forceinline__ void drop(int n) {
+    if (n & 4) {
+      lo = hi;
+      hi = vec{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    if (n & 2) {
+      lo = vec{lo[2], lo[3], hi[0], hi[1]};
+      hi = vec{hi[2], hi[3], 0.0f, 0.0f};
+    }
+    if (n & 1) {
+      lo = vec{lo[1], lo[2], lo[3], hi[0]};
+      hi = vec{hi[1], hi[2], hi[3], 0.0f};
+    }
+  }
   __device__ __forceinline__ void widen(float (&v)[8]) const {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -63,12 +83,16 @@ template <> struct Raw8<float> {
   static __device__ __forceinline__ void store1(float* p, float v) { st_global<float>(p, v); }
 };
 
-// Elements [c, c + 8) of a row of n, zeros behind its end.
+// Elements [c, c + 8) of a row of n, zeros behind its end.  At the end the row's last
+// eight are loaded: one by one each load would wait for the one before.
 template <typename T>
 __device__ __forceinline__ Raw8<T> load8(const T* row, int c, int n) {
   Raw8<T> r;
   if (c + 8 <= n) {
     r.load(row + c);
+  } else if (c < n && n >= 8) {
+    r.load(row + n - 8);
+    r.drop(c + 8 - n);
   } else {
     r.zero();
 #pragma unroll
