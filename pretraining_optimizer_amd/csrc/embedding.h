@@ -19,7 +19,9 @@ struct EmbeddingArgs {
 hipError_t launch_embedding_forward(int table_bf16, int out_bf16, const EmbeddingArgs& a, hipStream_t st);
 
 constexpr int kSortThreads = 1024;
-// Tokens that one workgroup sorts: up to 8192 alone, 4096 beside others.
+// Up to 8192 tokens are ranked among each other; of more, a workgroup sorts 4096.  Whole
+// gradient of so many tokens into rows of 64 columns, in us, ranked and sorted: 12288 into
+// 151936 rows 35.3 and 44.7, 16384 into 300 rows (a single pass) 38.0 and 26.5.
 constexpr int kSortAlone = 8, kSortBeside = 4;              // per thread
 constexpr int64_t kSortBlock = kSortThreads * kSortBeside;
 constexpr int kSortDigits = 1024;                           // at most, of one pass

@@ -4,8 +4,8 @@
 //
 // A token outside the table (padding) gives zeros and adds nothing.
 //
-// Backward: the tokens are sorted by a stable radix sort, so each row's tokens stand
-// together in their order of appearance; runs of 16 (or 64) sorted tokens are added by
+// Backward: the tokens are sorted, in a stable way, so each row's tokens stand together
+// in their order of appearance; runs of 16 (or 64) sorted tokens are added by
 // one group of threads each, and rows whose tokens go over a run's end are joined from
 // the runs' partial sums in order.  No atomics: results are the same in every call.
 // Sums are fp32, each result is rounded once.
@@ -58,7 +58,6 @@ __global__ __launch_bounds__(kThreads) void embedding_forward_kernel(EmbeddingAr
 constexpr int kWaves = kSortThreads / 64;
 struct SortLds {
   uint32_t count[kWaves][kSortDigits + 1];   // + 1: a digit's counters lie in different banks
-  uint32_t wave[kWaves];
 };
 
 template <int N>
@@ -94,34 +93,7 @@ __device__ __forceinline__ void count_digits(SortLds& lds, const uint32_t (&key)
   __syncthreads();
 }
 
-// counts[digit][wave] -> where the first key of each begins among the workgroup's.
-__device__ __forceinline__ void begin_digits(SortLds& lds, int digits) {
-  const int d = threadIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  uint32_t total = 0;
-  if (d < digits)
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      const uint32_t c = lds.count[w][d];
-      lds.count[w][d] = total;
-      total += c;
-    }
-  uint32_t sum = total;
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const uint32_t up = __shfl_up(sum, off, 64);
-    if (lane >= off) sum += up;
-  }
-  if (lane == 63) lds.wave[wave] = sum;
-  __syncthreads();
-  for (int w = 0; w < wave; ++w) sum += lds.wave[w];
-  if (d < digits)
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) lds.count[w][d] += sum - total;
-  __syncthreads();
-}
-
-__device__ __forceinline__ uint32_t key_of(const EmbeddingGradArgs& p, int64_t i) {
-  const int64_t v = token_at(p.tokens, p.wide, i);
+__device__ __forceinline__ uint32_t key_of(const EmbeddingGradArgs& p, int64_t v) {
   return v >= 0 && v < p.rows ? (uint32_t)v : (uint32_t)p.rows;
 }
 
@@ -152,46 +124,55 @@ __global__ __launch_bounds__(kThreads) void clear_rows_kernel(EmbeddingGradArgs 
       store8<O>(reinterpret_cast<O*>(p.dtable) + row * p.ldt, c, (int)p.cols, zeros);
 }
 
-// Up to 8192 tokens: one workgroup sorts them, in registers and LDS.
-__global__ __launch_bounds__(kSortThreads) void sort_alone_kernel(EmbeddingGradArgs p, SortPlan plan) {
-  constexpr int N = kSortAlone;
-  __shared__ SortLds lds;
-  __shared__ uint32_t keys[kSortThreads * N];
-  __shared__ uint16_t places[kSortThreads * N];
-  const int first = (threadIdx.x >> 6) * 64 * N + (threadIdx.x & 63), wave = threadIdx.x >> 6;
-  uint32_t key[N], place[N], rank[N];
+// Up to 8192 tokens: a token's place is the number of smaller keys, and of equal ones
+// before it.  A workgroup ranks 32 tokens against all keys, 32 slices of them side by side.
+// n^2 comparisons of about three instructions, but on all CUs, in one launch and without
+// a pass per digit: 8192 tokens 10.3 us, bound by issue (a sort of 18 bits by one workgroup:
+// 20.4).
+template <typename I>
+__global__ __launch_bounds__(kSortThreads) void sort_ranks_kernel(EmbeddingGradArgs p) {
+  constexpr int kTokens = 32, kSlices = kSortThreads / kTokens;
+  __shared__ __attribute__((aligned(16))) uint32_t keys[kSortThreads * kSortAlone];
+  __shared__ uint32_t ranks[kTokens];
+  const int n = (int)p.count, t = threadIdx.x % kTokens, slice = threadIdx.x / kTokens;
+  const int size = (n + 4 * kSlices - 1) / (4 * kSlices) * 4, all = size * kSlices;
+  constexpr int kAhead = 8;
+  const I* tokens = reinterpret_cast<const I*>(p.tokens);
+  for (int i0 = threadIdx.x; i0 < all; i0 += kAhead * kSortThreads) {
+    I token[kAhead];
 #pragma unroll
-  for (int k = 0; k < N; ++k) {
-    place[k] = first + k * 64;
-    key[k] = place[k] < p.count ? key_of(p, place[k]) : 0;
-  }
-  for (int pass = 0; pass < plan.passes; ++pass) {
-    const int shift = pass * plan.bits;
-    count_digits<N>(lds, key, rank, p.count, shift, plan.bits);
-    begin_digits(lds, 1 << plan.bits);
+    for (int a = 0; a < kAhead; ++a) token[a] = ld_global<I>(tokens + min(i0 + a * kSortThreads, n - 1));
 #pragma unroll
-    for (int k = 0; k < N; ++k)
-      if (first + k * 64 < p.count) {
-        const uint32_t to = lds.count[wave][(key[k] >> shift) & ((1u << plan.bits) - 1)] + rank[k];
-        keys[to] = key[k];
-        places[to] = (uint16_t)place[k];
-      }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < N; ++k)
-      if (first + k * 64 < p.count) {
-        key[k] = keys[first + k * 64];
-        place[k] = places[first + k * 64];
-      }
-  }
-#pragma unroll
-  for (int k = 0; k < N; ++k)
-    if (first + k * 64 < p.count) {
-      p.keys[0][first + k * 64] = key[k];
-      p.places[0][first + k * 64] = place[k];
+    for (int a = 0; a < kAhead; ++a) {
+      const int i = i0 + a * kSortThreads;
+      if (i < all) keys[i] = i < n ? key_of(p, token[a]) : 0xffffffffu;
     }
+  }
+  if (threadIdx.x < kTokens) ranks[threadIdx.x] = 0;
+  __syncthreads();
+  const int i = blockIdx.x * kTokens + t, first = slice * size;
+  const uint32_t key = keys[min(i, n - 1)];
+  const int before = min(max(i - first, 0), size);   // keys of the slice that stand before the token
+  uint32_t rank = 0;
+#pragma unroll 8
+  for (int j = 0; j < size; j += 4) {
+    const u32x4_t v = *reinterpret_cast<const u32x4_t*>(keys + first + j);
+    const uint32_t behind = key + (j + 4 <= before ? 1 : 0);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) rank += v[e] < behind ? 1 : 0;
+  }
+#pragma unroll
+  for (int e = 0; e < 3; ++e) {   // the four that the token stands among
+    const int j = (before & ~3) + e;
+    if (j < before) rank += keys[first + j] == key ? 1 : 0;
+  }
+  atomicAdd(&ranks[t], rank);   // whole numbers: their order does not matter
+  __syncthreads();
+  if (slice == 0 && i < n) {
+    p.keys[0][ranks[t]] = key;
+    p.places[0][ranks[t]] = (uint32_t)i;
+  }
 }
-static_assert(kSortThreads * kSortAlone <= 65536, "places of one workgroup's tokens are 16 bits");
 
 // More tokens: per pass the digits' counts of every workgroup, where each begins, and
 // the keys put there.  `from` is the buffer read (pass 0: the tokens).
@@ -203,7 +184,7 @@ __device__ __forceinline__ void read_keys(const EmbeddingGradArgs& p, int pass, 
     const int64_t i = first + wave * 64 * kSortBeside + k * 64 + lane;
     key[k] = place[k] = 0;
     if (i < p.count) {
-      key[k] = pass == 0 ? key_of(p, i) : p.keys[from][i];
+      key[k] = pass == 0 ? key_of(p, token_at(p.tokens, p.wide, i)) : p.keys[from][i];
       place[k] = pass == 0 ? (uint32_t)i : p.places[from][i];
     }
   }
@@ -458,7 +439,9 @@ hipError_t backward_for(const EmbeddingGradArgs& a, hipStream_t st) {
   if (e != hipSuccess || a.count == 0) return e;
   int which = 0;
   if (plan.blocks == 1) {
-    hipLaunchKernelGGL(sort_alone_kernel, dim3(1), dim3(kSortThreads), 0, st, a, plan);
+    const dim3 grid((unsigned)((a.count + 31) / 32)), block(kSortThreads);
+    if (a.wide) hipLaunchKernelGGL(sort_ranks_kernel<int64_t>, grid, block, 0, st, a);
+    else hipLaunchKernelGGL(sort_ranks_kernel<int32_t>, grid, block, 0, st, a);
   } else {
     const dim3 grid((unsigned)plan.blocks), block(kSortThreads);
     for (int pass = 0; pass < plan.passes; ++pass) {
