@@ -5,8 +5,9 @@ quintic Newton-Schulz on a grouped bf16/fp32 MFMA GEMM engine and the
 Hyperball update of Eq. (1) of "Puro-2B: Poor Lab's Qwen2-1.5B Trained on
 RTX 5090 within $5090" (arXiv HTML §3.3), plus the AdamW step of the
 parameters MuonH does not wrap, and the operators whose gradients these steps
-take: block-scaled FP8 products (§3.2) and the norms.  ``muonh`` and
-``operators`` are its ctypes binding.
+take: block-scaled FP8 products (§3.2), the norms, the residual's with FP8
+output, attention over packed sequences and the embedding, each with its
+gradient.  ``muonh`` and ``operators`` are its ctypes binding.
 """
 
 from .muonh import (  # noqa: F401

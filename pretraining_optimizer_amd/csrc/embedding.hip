@@ -27,7 +27,8 @@ __device__ __forceinline__ int64_t token_at(const void* tokens, int wide, int64_
 }
 
 // Groups of G threads take a token each, 8 columns per thread at a time.  Bound by HBM:
-// a row is read and written once.
+// a row is read and written once (8192 of 151936 x 2048 fp32 to bf16: 14 us, 7 TB/s, as
+// frequent rows come from the cache).
 template <typename T, typename O>
 __global__ __launch_bounds__(kThreads) void embedding_forward_kernel(EmbeddingArgs p, int log_group) {
   const int group = 1 << log_group, t = threadIdx.x & (group - 1);
@@ -98,7 +99,7 @@ __device__ __forceinline__ uint32_t key_of(const EmbeddingGradArgs& p, int64_t v
 }
 
 // Zeros in all of the table: 16 bytes per thread where the rows follow each other (one
-// store each: 151936 x 2048 fp32 183 us, 6.8 TB/s; 281 us in a loop over the grid), else
+// store each: 151936 x 2048 fp32 181 us, 6.9 TB/s; 281 us in a loop over the grid), else
 // a workgroup per row.
 constexpr int64_t kClearGroups = (int64_t)1 << 23;   // of one launch
 template <typename O>
@@ -175,7 +176,8 @@ __global__ __launch_bounds__(kSortThreads) void sort_ranks_kernel(EmbeddingGradA
 }
 
 // More tokens: per pass the digits' counts of every workgroup, where each begins, and
-// the keys put there.  `from` is the buffer read (pass 0: the tokens).
+// the keys put there.  `from` is the buffer read (pass 0: the tokens).  20000 tokens, a pass:
+// 6.0 + 3.3 + 8.7 us, latencies of 5 workgroups.
 __device__ __forceinline__ void read_keys(const EmbeddingGradArgs& p, int pass, int from, int64_t first,
                                           uint32_t (&key)[kSortBeside], uint32_t (&place)[kSortBeside]) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -307,7 +309,9 @@ __device__ __forceinline__ void store_partial(float* row, int c, int cols, const
 
 // Sums of a run of sorted tokens: rows whose tokens all lie in the run are written,
 // the sums of the row that began before it and of the one that goes on behind it are
-// left in partials[run][0] and [1] (one that does both: in [0]).
+// left in partials[run][0] and [1] (one that does both: in [0]).  Runs are short, so that
+// there are enough workgroups, and their rows are all on their way at once: 8192 x 2048 bf16
+// 24 us, 20000 x 769 bf16 11.
 template <typename T, typename O>
 __global__ __launch_bounds__(kThreads) void embedding_sum_kernel(EmbeddingGradArgs p, int which, int log_group, int64_t run) {
   const int group = 1 << log_group, t = threadIdx.x & (group - 1);
@@ -362,7 +366,9 @@ __global__ __launch_bounds__(kThreads) void embedding_sum_kernel(EmbeddingGradAr
 
 // Joins the partial sums of a row whose tokens begin in run r and go on: its runs are
 // counted by the workgroup's threads side by side, then 8 groups of 32 threads add every
-// eighth run's sums, four at a time, and those are added in order.
+// eighth run's sums, four at a time, and those are added in order (eight at a time are 0.5 to
+// 1.5 us slower).  20000 tokens of 300 rows: 9 us, the latency of about five loads that wait for
+// each other in the most frequent row's.
 constexpr int kJoin = 8;
 template <typename O>
 __global__ __launch_bounds__(kThreads) void embedding_join_kernel(EmbeddingGradArgs p, int which, int64_t run) {

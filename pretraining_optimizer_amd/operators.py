@@ -10,6 +10,12 @@ One linear layer y = x W^T, its gradients and the step of its weight:
     dx = fp8_matmul(gr, wc)                                # [tokens, in]
     dw = fp8_matmul(gc, xc, out_dtype=torch.float32)       # [out, in], the gradient MuonH.step takes (or .bfloat16())
 
+Between such layers, each with its gradient:
+
+    x = embedding_forward(tokens, table)                   # the residual stream
+    h, rstd, (nr, nc) = add_norm_quantize(y, x, gamma, form="both")   # h = y + x, its norm in FP8
+    out, lse = attention_forward(q, k, v, cu_seqlens)      # heads of a product's output
+
 All tensors are on the current device.  Work is enqueued on `stream`, or on
 torch's current stream.
 """
