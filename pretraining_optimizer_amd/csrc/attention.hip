@@ -327,6 +327,9 @@ __device__ __forceinline__ bool has_special(u32x4_t v) {
 // then the probabilities are up to 2^8 too large, which neither bf16 nor fp32 minds.
 //
 // A workgroup's tiles before its own rows are seen whole, in a loop without branches.
+// Heads up to 64 columns leave room for tiles of 128 keys, whose products cover more of the
+// next one's latency: 1000 + 777 tokens, 12 heads of 64, 17.8 -> 15.7 us (the gradients do
+// not gain by it: dq 19.7, key gradients 17.9 -> 19.5).
 // 2 x 4096 tokens, 16/8 heads of 128: 146 to 175 us as the card's clock allows (940 to 785
 // TFLOP/s; a large library product 1209).  Matrix unit and exponentials bind alike: a tile's
 // 32 products take 1030 cycles of a SIMD, its exponentials, maxima and packing about
@@ -338,7 +341,7 @@ __device__ __forceinline__ bool has_special(u32x4_t v) {
 // four times the loads: for problems of few workgroups (rows_split()).
 template <int DP, bool SPLIT>
 __global__ __launch_bounds__(kThreads, SPLIT ? 1 : 2) void attention_forward_kernel(AttentionArgs p) {
-  constexpr int kKeys = SPLIT ? 4 * 32 : kTile, kBytes = kKeys * DP * 2, kCols = DP / 32;
+  constexpr int kKeys = SPLIT || DP == 64 ? 2 * kTile : kTile, kBytes = kKeys * DP * 2, kCols = DP / 32;
   __shared__ __attribute__((aligned(1024))) uint8_t lds0[2 * kBytes], lds1[2 * kBytes];
   MUONH_LDS uint8_t *const slot0 = (MUONH_LDS uint8_t*)lds0, *const slot1 = (MUONH_LDS uint8_t*)lds1;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -499,25 +502,43 @@ __global__ __launch_bounds__(kThreads, SPLIT ? 1 : 2) void attention_forward_ker
       p.lse[head * (int64_t)p.tokens + t + lane] = (most + __builtin_amdgcn_logf(total)) * (1.0f / kLog2e);
     return;
   }
-  // The tiles before the workgroup's rows are seen whole by all of them, an even number.
-  const int whole = at.row / kTile;
-  for (int j = 0; j < whole; j += 2) {
+  // The tiles before the workgroup's rows are seen whole by all of them.
+  auto full = [&](MUONH_LDS uint8_t* tile) __attribute__((always_inline)) {
+    step(tile, two, std::false_type{});
+    if constexpr (kKeys > kTile) step(tile + kTile * DP * 2, two, std::false_type{});
+  };
+  // 64 of the workgroup's own keys, the first or the second.
+  auto own = [&](MUONH_LDS uint8_t* tile, int half) __attribute__((always_inline)) {
+    if (wave == 2 * half) step(tile, one, std::true_type{});
+    else if (wave == 2 * half + 1) step(tile, two, std::true_type{});
+    else if (half == 0) step(tile, two, std::false_type{});
+  };
+  const int whole = at.row / kKeys;
+  for (int j = 0; j + 1 < whole; j += 2) {
     arrive();   // the tile is there, and every wavefront has read the other
     fetch(slot1, j + 1);
-    step(slot0, two, std::false_type{});
+    full(slot0);
     arrive();
     fetch(slot0, j + 2);
-    step(slot1, two, std::false_type{});
+    full(slot1);
   }
   arrive();
-  fetch(slot1, whole + 1);
-  if (wave == 0) step(slot0, one, std::true_type{});
-  else if (wave == 1) step(slot0, two, std::true_type{});
-  else step(slot0, two, std::false_type{});
-  if (whole + 1 < tiles) {
-    arrive();
-    if (wave == 2) step(slot1, one, std::true_type{});
-    else if (wave == 3) step(slot1, two, std::true_type{});
+  if constexpr (kKeys == kTile) {   // an even number of whole ones
+    fetch(slot1, whole + 1);
+    own(slot0, 0);
+    if (whole + 1 < tiles) {
+      arrive();
+      own(slot1, 1);
+    }
+  } else {
+    if (whole & 1) {
+      fetch(slot1, whole);
+      full(slot0);
+      arrive();
+    }
+    MUONH_LDS uint8_t* const last = whole & 1 ? slot1 : slot0;
+    own(last, 0);
+    own(last + kTile * DP * 2, 1);
   }
 
   sum = pair_sum(sum);
@@ -649,7 +670,7 @@ __global__ __launch_bounds__(kThreads, SPLIT ? 1 : 2) void attention_dq_kernel(A
     block(tile, 0, std::false_type{});
     block(tile, 1, std::false_type{});
   };
-  // as in the forward pass
+  // as in the forward pass, an even number of whole tiles
   const int whole = at.row / kTile;
   for (int j = 0; j < whole; j += 2) {
     arrive();
