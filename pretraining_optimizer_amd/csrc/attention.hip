@@ -894,10 +894,10 @@ __global__ __launch_bounds__(kKeyThreads, 2) void attention_dkv_kernel(Attention
 
 // Whether the kernels are to have smaller blocks.  Measured, in us with smaller and with
 // large ones (in brackets: blocks of 128 rows x heads):
-//   rows, forward: 1000 tokens, 8 heads of 128 (64) 17.6 and 23.1; 8000 tokens, 2 heads of 64 (126)
-//   59 and 95; 4 x 300 tokens, 8 heads of 128 (104) 14.5 and 11.9; 1777 tokens in two
-//   sequences, 12 heads of 64 (180) 22.7 and 17.6.  Gradients: 4000 tokens, 4 heads of 128 (128)
-//   134 and 157; (104) 32.8 and 28.7; 1777 tokens, 16 heads of 128 (240) 88.6 and 68.1.
+//   rows, forward: 1000 tokens, 8 heads of 128 (64) 17.6 and 23.0; 8000 tokens, 2 heads of 64 (126)
+//   59 and 83; 4 x 300 tokens, 8 heads of 128 (104) 14.5 and 11.8; 1777 tokens in two
+//   sequences, 12 heads of 64 (180) 22.7 and 15.6.  Gradients: 4000 tokens, 4 heads of 128 (128)
+//   134 and 158; (104) 32.9 and 28.7; 1777 tokens, 16 heads of 128 (240) 88.6 and 68.4.
 //   Long sequences win more than short ones lose up to half a workgroup per CU.
 //   keys, gradients: 1000 tokens, 8 heads of 128 (64) 42.7 and 63.7; 4000 tokens, 4 heads (128) 134
 //   and 200; 1777 tokens, 12 heads of 64 (180) 38.6 and 43.2.  Worth it while the large

@@ -214,10 +214,19 @@ __global__ __launch_bounds__(kSortThreads) void sort_begin_kernel(EmbeddingGradA
   __shared__ uint32_t sums[kWaves];
   const int d = threadIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const bool live = d < 1 << plan.bits;
+  constexpr int kAhead = 16;
+  uint32_t c[kAhead];
+  auto load = [&](int64_t b0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int b = 0; b < kAhead; ++b) c[b] = p.digits[min(b0 + b, plan.blocks - 1) * kSortDigits + d];
+  };
   uint32_t total = 0;
-  if (live) {
-    for (int64_t b = 0; b < plan.blocks; ++b) total += p.digits[b * kSortDigits + d];
-  }
+  if (live)
+    for (int64_t b0 = 0; b0 < plan.blocks; b0 += kAhead) {
+      load(b0);
+#pragma unroll
+      for (int b = 0; b < kAhead; ++b) total += b0 + b < plan.blocks ? c[b] : 0;
+    }
   uint32_t sum = total;
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) {
@@ -229,11 +238,8 @@ __global__ __launch_bounds__(kSortThreads) void sort_begin_kernel(EmbeddingGradA
   for (int w = 0; w < wave; ++w) sum += sums[w];
   uint32_t at = sum - total;
   if (!live) return;
-  constexpr int kAhead = 8;
   for (int64_t b0 = 0; b0 < plan.blocks; b0 += kAhead) {
-    uint32_t c[kAhead];
-#pragma unroll
-    for (int b = 0; b < kAhead; ++b) c[b] = b0 + b < plan.blocks ? p.digits[(b0 + b) * kSortDigits + d] : 0;
+    load(b0);
 #pragma unroll
     for (int b = 0; b < kAhead; ++b) {
       if (b0 + b < plan.blocks) p.digits[(b0 + b) * kSortDigits + d] = at;
