@@ -116,6 +116,19 @@ def test_shapes(rows, cols, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("base", [8, 1016])
+def test_every_row_end(base, dtype):
+    """Rows that end after each number of elements of a vector."""
+    for cols in range(base, base + 9):
+        announce(f"add norm 9x{cols} {dtype}")
+        x, r, w, dy, dh = _inputs(9, cols, dtype)
+        for res in (r, None):
+            _check_forward(x, res, w, 1e-5, pm.add_norm_quantize(x, res, w, eps=1e-5, form="both"), "both", cols)
+        h, rstd, _ = pm.add_norm_quantize(x, r, w, eps=1e-5)
+        _check_backward(pm.add_norm_backward(dy, dh, h, w, rstd), dy, dh, h, w, rstd, dtype, cols)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_forms_are_the_quantisers(dtype):
     """Bit for bit what quantising the fp32 norm gives, also where values are special,
     zero or far apart."""

@@ -201,6 +201,61 @@ def test_longer_sequences():
     _both(*_inputs([13 * i % 97 for i in range(64)], 2, 2, 64), None, "64 sequences")
 
 
+@pytest.mark.parametrize("dim,kv", [(64, 1), (128, 2), (40, 2)])
+def test_a_long_sequence(dim, kv):
+    """One sequence of 20011 tokens: some of its rows and keys, to the module's
+    tolerances; keys are summed over the heads of a group."""
+    n, heads = 20011, 2
+    announce(f"attention {n} tokens, 2/{kv} heads of {dim}")
+    q, k, v, do, cu = _inputs([n], heads, kv, dim)
+    out, lse = pm.attention_forward(q, k, v, cu)
+    grads = pm.attention_backward(do, q, k, v, out, lse, cu)
+    Q, K, V, DO, O, L = (_np(t) for t in (q, k, v, do, out, lse))
+    dQ, dK, dV = (_np(t) for t in grads)
+    c, group = dim ** -0.5, heads // kv
+    at = [0, 1, 31, 32, 127, 128, 8191, 10000, n - 129, n - 2, n - 1]
+
+    def close(got, want, tol, what):
+        tol = tol + B * (np.abs(want) + tol)
+        assert np.all(np.abs(got - want) <= tol), (what, float((np.abs(got - want) - tol).max()))
+
+    delta = (DO * O).sum(axis=2)          # [tokens, heads]
+    size = np.abs(DO * O).sum(axis=2)
+    for i in at:
+        for h in range(heads):
+            g, m = h // group, i + 1
+            S = c * (K[:m, g] @ Q[i, h])
+            ep = c * dim * U * (np.abs(K[:m, g]) @ np.abs(Q[i, h])) + 8 * U * (np.abs(S) + abs(L[h, i]) + 1)
+            top = S.max()
+            rl = top + np.log(np.exp(S - top).sum())
+            P = np.exp(S - rl)
+            assert abs(L[h, i] - rl) <= ep.max() + m * U, ("lse", i, h)
+            close(O[i, h], P @ V[:m, g], (P @ np.abs(V[:m, g])) * (B + 2 * ep.max() + 2 * m * U), ("out", i, h))
+            P = np.exp(S - L[h, i])
+            dP = V[:m, g] @ DO[i, h]
+            ed = dim * U * (np.abs(V[:m, g]) @ np.abs(DO[i, h]) + size[i, h])
+            ds = c * P * (dP - delta[i, h])
+            eds = np.abs(ds) * (B + 2 * ep) + c * P * (ed + 2 * U * np.abs(dP - delta[i, h]))
+            close(dQ[i, h], ds @ K[:m, g], eds @ np.abs(K[:m, g]) + 2 * m * U * (np.abs(ds) @ np.abs(K[:m, g])), ("dq", i, h))
+    for j in at:
+        for g in range(kv):
+            wk = wv = tk = tv = 0.0
+            for h in range(g * group, (g + 1) * group):
+                a, d, m = Q[j:, h], DO[j:, h], group * (n - j)
+                S = c * (a @ K[j, g])
+                ep = c * dim * U * (np.abs(a) @ np.abs(K[j, g])) + 8 * U * (np.abs(S) + np.abs(L[h, j:]) + 1)
+                P = np.exp(S - L[h, j:])
+                dP = d @ V[j, g]
+                ed = dim * U * (np.abs(d) @ np.abs(V[j, g]) + size[j:, h])
+                ds = c * P * (dP - delta[j:, h])
+                eds = np.abs(ds) * (B + 2 * ep) + c * P * (ed + 2 * U * np.abs(dP - delta[j:, h]))
+                wk, wv = wk + ds @ a, wv + P @ d
+                tk = tk + eds @ np.abs(a) + 2 * m * U * (np.abs(ds) @ np.abs(a))
+                tv = tv + (P * (B + 2 * ep + 2 * m * U)) @ np.abs(d)
+            close(dK[j, g], wk, tk, ("dk", j, g))
+            close(dV[j, g], wv, tv, ("dv", j, g))
+
+
 @pytest.mark.parametrize("dim", [64, 128])
 def test_peaked_and_growing_scores(dim):
     """Scores far apart, and maxima that grow along a row by more and by less than the

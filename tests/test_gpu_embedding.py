@@ -104,6 +104,24 @@ def test_sort_of_many_tokens(n, rows, cols, kind):
     assert torch.equal(got, pm.embedding_backward(t, d, rows))
 
 
+@pytest.mark.parametrize("dout,table", [(BF16, F32), (F32, BF16)])
+@pytest.mark.parametrize("base", [1, 9, 2041])
+def test_every_row_end(base, dout, table):
+    """Rows that end after each number of elements of a vector; tokens of few rows, whose
+    sums go over several runs."""
+    for cols in range(base, base + 8):
+        announce(f"embedding gradient 90 of 4x{cols} {dout} {table}")
+        t = _tokens(90, 4, "words").cuda()
+        d = torch.randn((90, cols), generator=torch.Generator().manual_seed(cols)).to(dout).cuda()
+        got = pm.embedding_backward(t, d, 4, out_dtype=table)
+        _check_backward(got, t, d, 4, 1.0, cols)
+        before = _np(got)
+        pm.embedding_backward(t, d, 4, scale=-0.5, dtable=got, accumulate=True)
+        _check_backward(got, t, d, 4, -0.5, cols, before)
+        out = pm.embedding_forward(t, got, scale=3.0, out_dtype=dout)
+        assert torch.equal(out, (got[t].float() * 3.0).to(dout))
+
+
 def test_three_passes():
     """Keys of more than 20 bits."""
     announce("embedding gradient three passes")
