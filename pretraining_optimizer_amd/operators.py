@@ -484,7 +484,7 @@ def embedding_forward(tokens, table, scale: float = 1.0, out=None, out_dtype=Non
     size = _tokens(tokens)
     code = _code(table, "table")
     rows, cols, ld = _matrix(table, "table")
-    n = len(tokens)
+    n = tokens.numel()
     if out is None:
         out = _empty((n, cols), out_dtype or _torch.bfloat16, table.device, stream)
         ld_out = cols
@@ -520,8 +520,8 @@ def embedding_backward(tokens, dout, rows: int, scale: float = 1.0, dtable=None,
     size = _tokens(tokens)
     code = _code(dout, "dout")
     n, cols, ld = _matrix(dout, "dout")
-    if n != len(tokens):
-        raise ValueError(f"dout: {len(tokens)} rows are required")
+    if n != tokens.numel():
+        raise ValueError(f"dout: {tokens.numel()} rows are required")
     if dtable is None:
         if accumulate:
             raise ValueError("accumulate needs dtable")
@@ -575,18 +575,20 @@ def _attention(q, k, v, cu_seqlens, scale, out, lse, stream):
     kv_heads = k.shape[1]
     ld_q, ld_k = _heads(q, tokens, heads, dim, "q"), _heads(k, tokens, kv_heads, dim, "k")
     ld_v = _heads(v, tokens, kv_heads, dim, "v")
-    if cu_seqlens.dtype is not _torch.int32 or cu_seqlens.dim() != 1 or not cu_seqlens.is_contiguous() or not len(cu_seqlens):
+    ends = cu_seqlens.numel()
+    if cu_seqlens.dtype is not _torch.int32 or cu_seqlens.dim() != 1 or ends < 1 or not cu_seqlens.is_contiguous():
         raise ValueError("cu_seqlens: a contiguous int32 vector of sequences + 1 elements is required")
     dev = _here(q, k, v, cu_seqlens, out, lse)
     if out is None:
-        out = _like(q, (tokens, heads, dim), stream)
-    ld_out = _heads(out, tokens, heads, dim, "out")
+        out, ld_out = _like(q, (tokens, heads, dim), stream), heads * dim
+    else:
+        ld_out = _heads(out, tokens, heads, dim, "out")
     if lse is None:
         lse = _empty((heads, tokens), _torch.float32, q.device, stream)
     elif lse.dtype is not _torch.float32 or lse.shape != (heads, tokens) or not lse.is_contiguous():
         raise ValueError(f"lse: a contiguous float32 tensor of shape {(heads, tokens)} is required")
     args = muonh_attention_args(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
-                                cu_seqlens.data_ptr(), tokens, len(cu_seqlens) - 1, ld_q, ld_k, ld_v, ld_out, heads,
+                                cu_seqlens.data_ptr(), tokens, ends - 1, ld_q, ld_k, ld_v, ld_out, heads,
                                 kv_heads, dim, dim ** -0.5 if scale is None else scale)
     return args, out, lse, dev
 
@@ -628,10 +630,12 @@ def attention_backward(dout, q, k, v, out, lse, cu_seqlens, scale: Optional[floa
     kv_heads = k.shape[1]
     ld_dout = _heads(dout, tokens, heads, dim, "dout")
     _here(q, dout, dq, dk, dv)
-    dq = _like(q, (tokens, heads, dim), stream) if dq is None else dq
-    dk = _like(k, (tokens, kv_heads, dim), stream) if dk is None else dk
-    dv = _like(v, (tokens, kv_heads, dim), stream) if dv is None else dv
-    lds = _heads(dq, tokens, heads, dim, "dq"), _heads(dk, tokens, kv_heads, dim, "dk"), _heads(dv, tokens, kv_heads, dim, "dv")
+    lds = []
+    grads = []
+    for t, like, n, what in ((dq, q, heads, "dq"), (dk, k, kv_heads, "dk"), (dv, v, kv_heads, "dv")):
+        lds.append(n * dim if t is None else _heads(t, tokens, n, dim, what))
+        grads.append(_like(like, (tokens, n, dim), stream) if t is None else t)
+    dq, dk, dv = grads
     need = ctypes.c_size_t()
     rc = _lib.muonh_attention_backward_workspace(ctypes.byref(args), ctypes.byref(need))
     if rc:
