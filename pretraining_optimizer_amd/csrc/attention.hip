@@ -336,26 +336,28 @@ __device__ __forceinline__ bool has_special(u32x4_t v) {
 // 900 issue cycles of each of its two wavefronts, which overlap them only in part.  Without
 // loads from memory 135 us of 154, without exponentials 135.
 //
-// SPLIT: a workgroup has 32 rows and its wavefronts every fourth block of 32 keys each,
-// whose sums are joined in LDS.  The chain of one wavefront is a quarter as long, for
-// four times the loads: for problems of few workgroups (rows_split()).
-template <int DP, bool SPLIT>
-__global__ __launch_bounds__(kThreads, SPLIT ? 1 : 2) void attention_forward_kernel(AttentionArgs p) {
-  constexpr int kKeys = SPLIT || DP == 64 ? 2 * kTile : kTile, kBytes = kKeys * DP * 2, kCols = DP / 32;
+// PARTS > 1: a workgroup has 128 / PARTS rows, and PARTS wavefronts share 32 of them and
+// take every PARTS-th block of 32 keys each; their sums are joined in LDS.  The chain of one
+// wavefront is that much shorter, for as many times the loads: for problems of few
+// workgroups (row_parts()).
+template <int DP, int PARTS>
+__global__ __launch_bounds__(kThreads, PARTS == 4 ? 1 : 2) void attention_forward_kernel(AttentionArgs p) {
+  constexpr bool SPLIT = PARTS > 1;
+  constexpr int kRows = kAttentionRows / PARTS, kKeys = SPLIT || DP == 64 ? 2 * kTile : kTile, kBytes = kKeys * DP * 2, kCols = DP / 32;
   __shared__ __attribute__((aligned(1024))) uint8_t lds0[2 * kBytes], lds1[2 * kBytes];
   MUONH_LDS uint8_t *const slot0 = (MUONH_LDS uint8_t*)lds0, *const slot1 = (MUONH_LDS uint8_t*)lds1;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int group = p.heads / p.kv_heads;
   const Item item = item_of(p.kv_heads, group);
   const int kv = item.kv, head = kv * group + item.member;
-  const Place at = find_place<false, SPLIT ? 32 : kAttentionRows>(p, item.rank);
+  const Place at = find_place<false, kRows>(p, item.rank);
   if (at.row < 0) return;
 
   const Rows q{p.q + at.start * p.ldq + head * p.dim, p.ldq, at.len, p.dim};
   const Rows k{p.k + at.start * p.ldk + kv * p.dim, p.ldk, at.len, p.dim};
   const Rows v{p.v + at.start * p.ldv + kv * p.dim, p.ldv, at.len, p.dim};
-  const int row = SPLIT ? at.row : at.row + 32 * wave;   // the wavefront's first
-  const int tiles = (min(at.len, at.row + (SPLIT ? 32 : kAttentionRows)) + kKeys - 1) / kKeys;
+  const int part = wave % PARTS, row = at.row + 32 * (wave / PARTS);   // the wavefront's share of the keys, its first row
+  const int tiles = (min(at.len, at.row + kRows) + kKeys - 1) / kKeys;
   const TileLoad<DP, kKeys> load_k(p.ldk, p.dim, wave, lane), load_v(p.ldv, p.dim, wave, lane);
   const TileRead<DP> read(lane);
   load_k(k, 0, slot0, wave);
@@ -457,10 +459,13 @@ __global__ __launch_bounds__(kThreads, SPLIT ? 1 : 2) void attention_forward_ker
   if constexpr (SPLIT) {
     __shared__ float stats[2][4][64];
     auto use = [&](MUONH_LDS uint8_t* tile, int j) __attribute__((always_inline)) {
-      const int block = 4 * j + wave, own = at.row / 32;
-      MUONH_LDS uint8_t* const mine = tile + wave * 32 * DP * 2;
-      if (block < own) step(mine, one, std::false_type{});
-      else if (block == own) step(mine, one, std::true_type{});
+#pragma unroll
+      for (int b = 0; b < 4 / PARTS; ++b) {
+        const int block = PARTS * b + part, own = row / 32 - 4 * j;
+        MUONH_LDS uint8_t* const mine = tile + block * 32 * DP * 2;
+        if (block < own) step(mine, one, std::false_type{});
+        else if (block == own) step(mine, one, std::true_type{});
+      }
     };
     for (int j = 0; j < tiles; j += 2) {
       arrive();   // the tile is there, and every wavefront has read the other
@@ -474,31 +479,32 @@ __global__ __launch_bounds__(kThreads, SPLIT ? 1 : 2) void attention_forward_ker
     stats[0][wave][lane] = top;
     stats[1][wave][lane] = pair_sum(sum);
     arrive();   // all are done with the slots, which take the sums
-    auto part = [&](int w) { return (SumsInLds)(w & 1 ? slot1 : slot0) + (w >> 1) * kCols * 4 * 64; };
+    auto place = [&](int w) { return (SumsInLds)(w & 1 ? slot1 : slot0) + (w >> 1) * kCols * 4 * 64; };
     static_assert(2 * kCols * 4 * 64 * 16 <= 2 * kBytes, "two wavefronts' sums fill a slot");
-    put_sums<DP>(part(wave), acc, lane);
+    put_sums<DP>(place(wave), acc, lane);
     arrive();
-    float most = stats[0][0][lane], total = 0.0f, factor[4];
+    const int first = wave - part;   // of the wavefronts that share the rows
+    float most = stats[0][first][lane], total = 0.0f, factor[PARTS];
 #pragma unroll
-    for (int w = 1; w < 4; ++w) most = fmaxf(most, stats[0][w][lane]);
+    for (int w = 1; w < PARTS; ++w) most = fmaxf(most, stats[0][first + w][lane]);
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      factor[w] = __builtin_amdgcn_exp2f(stats[0][w][lane] - most);   // 0 of a wavefront without keys
-      total += factor[w] * stats[1][w][lane];
+    for (int w = 0; w < PARTS; ++w) {
+      factor[w] = __builtin_amdgcn_exp2f(stats[0][first + w][lane] - most);   // 0 of a wavefront without keys
+      total += factor[w] * stats[1][first + w][lane];
     }
     if (row + (lane & 31) >= at.len) return;
     const int64_t t = at.start + row;
-    for (int dt = wave; dt < kCols; dt += 4) {   // the columns over the wavefronts
+    for (int dt = part; dt < kCols; dt += PARTS) {   // the columns over the wavefronts
       f32x16_t v = splat(0.0f);
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const f32x16_t o = take_sums(part(w), dt, lane);
+      for (int w = 0; w < PARTS; ++w) {
+        const f32x16_t o = take_sums(place(first + w), dt, lane);
 #pragma unroll
         for (int r = 0; r < 16; ++r) v[r] += factor[w] * o[r];
       }
       store_columns(p.out + t * p.ldo + head * p.dim, p.ldo, p.dim, dt, v, 1.0f / total, lane);
     }
-    if (wave == 0 && lane < 32)
+    if (part == 0 && lane < 32)
       p.lse[head * (int64_t)p.tokens + t + lane] = (most + __builtin_amdgcn_logf(total)) * (1.0f / kLog2e);
     return;
   }
@@ -551,19 +557,20 @@ __global__ __launch_bounds__(kThreads, SPLIT ? 1 : 2) void attention_forward_ker
 // Gradient of q, row by row as in the forward pass: S and dP from k and v, dq from dS and k.
 // It also leaves what the other kernel needs of each row: -lse log2 e and -delta.
 // Packed documents of 8192 tokens, 16/8 heads of 128: 115 us, three products of five (870
-// TFLOP/s); 1000 + 777 tokens, 12 heads of 64: 19 us, 180 workgroups whose longest waits for 16
-// tiles one after another.
-template <int DP, bool SPLIT>
-__global__ __launch_bounds__(kThreads, SPLIT ? 1 : 2) void attention_dq_kernel(AttentionGradArgs g) {
+// TFLOP/s); 1000 + 777 tokens, 12 heads of 64: 16 us in two parts, 19 in one, bound by the longest
+// workgroup's chain of tiles.
+template <int DP, int PARTS>
+__global__ __launch_bounds__(kThreads, PARTS == 4 ? 1 : 2) void attention_dq_kernel(AttentionGradArgs g) {
   const AttentionArgs& p = g.a;
-  constexpr int kKeys = SPLIT ? 4 * 32 : kTile, kBytes = kKeys * DP * 2, kCols = DP / 32;
+  constexpr bool SPLIT = PARTS > 1;
+  constexpr int kRows = kAttentionRows / PARTS, kKeys = SPLIT ? 2 * kTile : kTile, kBytes = kKeys * DP * 2, kCols = DP / 32;
   __shared__ __attribute__((aligned(1024))) uint8_t lds0[2 * kBytes], lds1[2 * kBytes];
   MUONH_LDS uint8_t *const slot0 = (MUONH_LDS uint8_t*)lds0, *const slot1 = (MUONH_LDS uint8_t*)lds1;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int group = p.heads / p.kv_heads;
   const Item item = item_of(p.kv_heads, group);
   const int kv = item.kv, head = kv * group + item.member;
-  const Place at = find_place<false, SPLIT ? 32 : kAttentionRows>(p, item.rank);
+  const Place at = find_place<false, kRows>(p, item.rank);
   if (at.row < 0) return;
 
   const Rows q{p.q + at.start * p.ldq + head * p.dim, p.ldq, at.len, p.dim};
@@ -571,8 +578,8 @@ __global__ __launch_bounds__(kThreads, SPLIT ? 1 : 2) void attention_dq_kernel(A
   const Rows v{p.v + at.start * p.ldv + kv * p.dim, p.ldv, at.len, p.dim};
   const Rows o{p.out + at.start * p.ldo + head * p.dim, p.ldo, at.len, p.dim};
   const Rows d{g.dout + at.start * g.lddo + head * p.dim, g.lddo, at.len, p.dim};
-  const int row = SPLIT ? at.row : at.row + 32 * wave;
-  const int tiles = (min(at.len, at.row + (SPLIT ? 32 : kAttentionRows)) + kKeys - 1) / kKeys;
+  const int part = wave % PARTS, row = at.row + 32 * (wave / PARTS);
+  const int tiles = (min(at.len, at.row + kRows) + kKeys - 1) / kKeys;
   const TileLoad<DP, kKeys> load_k(p.ldk, p.dim, wave, lane), load_v(p.ldv, p.dim, wave, lane);
   const TileRead<DP> read(lane);
   load_k(k, 0, slot0, wave);
@@ -596,7 +603,7 @@ __global__ __launch_bounds__(kThreads, SPLIT ? 1 : 2) void attention_dq_kernel(A
         delta = __builtin_fmaf(__uint_as_float(fo[s][w] & 0xffff0000u), __uint_as_float(fd[s][w] & 0xffff0000u), delta);
       }
     delta = -pair_sum(delta);
-    if (live && lane < 32 && (!SPLIT || wave == 0)) {
+    if (live && lane < 32 && part == 0) {
       g.row_lse[t] = lse;
       g.row_delta[t] = delta;
     }
@@ -635,9 +642,12 @@ __global__ __launch_bounds__(kThreads, SPLIT ? 1 : 2) void attention_dq_kernel(A
   };
   if constexpr (SPLIT) {
     auto use = [&](MUONH_LDS uint8_t* tile, int j) __attribute__((always_inline)) {
-      const int own = at.row / 32 - 4 * j;
-      if (wave < own) block(tile, wave, std::false_type{});
-      else if (wave == own) block(tile, wave, std::true_type{});
+#pragma unroll
+      for (int b = 0; b < 4 / PARTS; ++b) {
+        const int mine = PARTS * b + part, own = row / 32 - 4 * j;
+        if (mine < own) block(tile, mine, std::false_type{});
+        else if (mine == own) block(tile, mine, std::true_type{});
+      }
     };
     for (int j = 0; j < tiles; j += 2) {
       arrive();
@@ -649,16 +659,17 @@ __global__ __launch_bounds__(kThreads, SPLIT ? 1 : 2) void attention_dq_kernel(A
       use(slot1, j + 1);
     }
     arrive();   // all are done with the slots, which take the sums
-    auto part = [&](int w) { return (SumsInLds)(w & 1 ? slot1 : slot0) + (w >> 1) * kCols * 4 * 64; };
+    auto place = [&](int w) { return (SumsInLds)(w & 1 ? slot1 : slot0) + (w >> 1) * kCols * 4 * 64; };
     static_assert(2 * kCols * 4 * 64 * 16 <= 2 * kBytes, "two wavefronts' sums fill a slot");
-    put_sums<DP>(part(wave), acc, lane);
+    put_sums<DP>(place(wave), acc, lane);
     arrive();
     if (!live) return;
-    for (int dt = wave; dt < kCols; dt += 4) {   // the columns over the wavefronts
-      f32x16_t v = take_sums(part(0), dt, lane);
+    const int first = wave - part;   // of the wavefronts that share the rows
+    for (int dt = part; dt < kCols; dt += PARTS) {   // the columns over the wavefronts
+      f32x16_t v = take_sums(place(first), dt, lane);
 #pragma unroll
-      for (int w = 1; w < 4; ++w) {
-        const f32x16_t o = take_sums(part(w), dt, lane);
+      for (int w = 1; w < PARTS; ++w) {
+        const f32x16_t o = take_sums(place(first + w), dt, lane);
 #pragma unroll
         for (int r = 0; r < 16; ++r) v[r] += o[r];
       }
@@ -892,18 +903,26 @@ __global__ __launch_bounds__(kKeyThreads, 2) void attention_dkv_kernel(Attention
 
 }  // namespace
 
-// Whether the kernels are to have smaller blocks.  Measured, in us with smaller and with
-// large ones (in brackets: blocks of 128 rows x heads):
-//   rows, forward: 1000 tokens, 8 heads of 128 (64) 17.6 and 23.0; 8000 tokens, 2 heads of 64 (126)
-//   59 and 83; 4 x 300 tokens, 8 heads of 128 (104) 14.5 and 11.8; 1777 tokens in two
-//   sequences, 12 heads of 64 (180) 22.7 and 15.6.  Gradients: 4000 tokens, 4 heads of 128 (128)
-//   134 and 158; (104) 32.9 and 28.7; 1777 tokens, 16 heads of 128 (240) 88.6 and 68.4.
-//   Long sequences win more than short ones lose up to half a workgroup per CU.
-//   keys, gradients: 1000 tokens, 8 heads of 128 (64) 42.7 and 63.7; 4000 tokens, 4 heads (128) 134
-//   and 200; 1777 tokens, 12 heads of 64 (180) 38.6 and 43.2.  Worth it while the large
-//   ones are less than one per CU.
-static bool rows_split(const AttentionArgs& a) {
-  return 2 * attention_blocks(a.tokens, a.sequences, kAttentionRows) * a.heads <= kAttentionCus;
+// Whether the kernels are to have smaller blocks, by n, the blocks of 128 rows x heads.
+// Measured, in us of the forward pass / of the gradients:
+//                                                  n    4 parts        2 parts        1 part
+//   1000 tokens, 8 heads of 128                    64   17.6 / 42.7                   23.0 / 51.9
+//   4000 tokens, 4 heads of 128                   128   71.2 / 134     79.7 / 153     69.1 / 158
+//   8000 tokens, 2 heads of 64                    126   60.8 / 191     67.7 / 207     82.6 / 242
+//   4 x 300 tokens, 8 heads of 128                104   14.5 / 32.8    12.2 / 29.5    11.8 / 28.7
+//   6 x 500 tokens, 4 heads of 64                 116   11.8 / 21.0     8.7 / 20.8     9.3 / 23.0
+//   1000 + 777 tokens, 12 heads of 64             180                  14.8 / 34.5    15.5 / 37.3
+//   1000 + 777 tokens, 16 heads of 128            240                  31.0 / 72.1    25.4 / 68.1
+// Four parts up to a quarter of a workgroup of 128 rows per CU, long sequences up to half of
+// one; two up to one of heads up to 64 columns, whose tiles of 128 keys fit a CU twice.
+//   Keys, gradients, smaller and large blocks: 1000 tokens, 8 heads of 128 (64) 42.7 and 63.7;
+//   4000 tokens, 4 heads (128) 134 and 200; 1777 tokens, 12 heads of 64 (180) 38.6 and 43.2.  Worth
+//   it while the large ones are less than one per CU.
+static int row_parts(const AttentionArgs& a) {
+  const int64_t n = attention_blocks(a.tokens, a.sequences, kAttentionRows) * a.heads;
+  const bool long_ones = a.tokens >= 1024 * (int64_t)a.sequences;
+  if (4 * n <= kAttentionCus || (2 * n <= kAttentionCus && long_ones)) return 4;
+  return a.dim <= 64 && n < kAttentionCus ? 2 : 1;
 }
 static bool keys_split(const AttentionArgs& a) {
   return attention_blocks(a.tokens, a.sequences, kAttentionRows) * a.kv_heads < kAttentionCus;
@@ -917,26 +936,36 @@ static hipError_t launch_blocks(K kernel, A args, AttentionArgs& a, int rows, in
   return hipGetLastError();
 }
 
+template <int DP>
+static hipError_t forward_for(AttentionArgs& a, hipStream_t st) {
+  auto args = [&] { return a; };
+  const int parts = row_parts(a);
+  auto kernel = parts == 4 ? attention_forward_kernel<DP, 4> : attention_forward_kernel<DP, 1>;
+  if constexpr (DP == 64)
+    if (parts == 2) kernel = attention_forward_kernel<DP, 2>;
+  return launch_blocks(kernel, args, a, kAttentionRows / parts, a.heads, kThreads, st);
+}
 hipError_t launch_attention_forward(const AttentionArgs& given, hipStream_t st) {
   AttentionArgs a = given;
-  auto args = [&] { return a; };
-  const bool split = rows_split(a);
-  const auto kernel = a.dim <= 64 ? (split ? attention_forward_kernel<64, true> : attention_forward_kernel<64, false>)
-                                  : (split ? attention_forward_kernel<128, true> : attention_forward_kernel<128, false>);
-  return launch_blocks(kernel, args, a, split ? 32 : kAttentionRows, a.heads, kThreads, st);
+  return a.dim <= 64 ? forward_for<64>(a, st) : forward_for<128>(a, st);
 }
 
+template <int DP>
+static hipError_t backward_for(AttentionGradArgs& g, hipStream_t st) {
+  auto args = [&] { return g; };
+  const int parts = row_parts(g.a);
+  const bool split = keys_split(g.a);
+  auto dq = parts == 4 ? attention_dq_kernel<DP, 4> : attention_dq_kernel<DP, 1>;
+  if constexpr (DP == 64)
+    if (parts == 2) dq = attention_dq_kernel<DP, 2>;
+  const hipError_t e = launch_blocks(dq, args, g.a, kAttentionRows / parts, g.a.heads, kThreads, st);
+  if (e != hipSuccess) return e;
+  const auto dkv = split ? attention_dkv_kernel<DP, 2> : attention_dkv_kernel<DP, 4>;
+  return launch_blocks(dkv, args, g.a, split ? 64 : kAttentionRows, g.a.kv_heads, kKeyThreads, st);
+}
 hipError_t launch_attention_backward(const AttentionGradArgs& given, hipStream_t st) {
   AttentionGradArgs g = given;
-  auto args = [&] { return g; };
-  const bool wide = g.a.dim > 64, rows = rows_split(g.a), keys = keys_split(g.a);
-  const auto dq = wide ? (rows ? attention_dq_kernel<128, true> : attention_dq_kernel<128, false>)
-                       : (rows ? attention_dq_kernel<64, true> : attention_dq_kernel<64, false>);
-  const hipError_t e = launch_blocks(dq, args, g.a, rows ? 32 : kAttentionRows, g.a.heads, kThreads, st);
-  if (e != hipSuccess) return e;
-  const auto dkv = wide ? (keys ? attention_dkv_kernel<128, 2> : attention_dkv_kernel<128, 4>)
-                        : (keys ? attention_dkv_kernel<64, 2> : attention_dkv_kernel<64, 4>);
-  return launch_blocks(dkv, args, g.a, keys ? 64 : kAttentionRows, g.a.kv_heads, kKeyThreads, st);
+  return g.a.dim <= 64 ? backward_for<64>(g, st) : backward_for<128>(g, st);
 }
 
 }  // namespace muonh

@@ -137,6 +137,15 @@ def test_lengths_in_large_blocks(lens, group, dim):
     _both(*_inputs(lens, group * kv, kv, dim), None, f"{lens}")
 
 
+@pytest.mark.parametrize("lens", LENS, ids=lambda v: "+".join(map(str, v)))
+@pytest.mark.parametrize("group,dim", [(1, 128), (2, 64)])
+def test_lengths_in_blocks_between(lens, group, dim):
+    """More workgroups of 128 rows than half the CUs, and fewer than all of them."""
+    kv = -(-140 // (group * (sum(lens) // 128 + len(lens))))
+    announce(f"attention {lens} {group * kv}/{kv} heads of {dim}")
+    _both(*_inputs(lens, group * kv, kv, dim), None, f"{lens}")
+
+
 @pytest.mark.parametrize("dim", [8, 40, 72, 104])
 def test_head_widths_in_large_blocks(dim):
     announce(f"attention width {dim}, large blocks")
@@ -197,6 +206,7 @@ def test_longer_sequences():
     """Many tiles per row, in small and in large blocks."""
     announce("attention 1500+700, 64 sequences")
     _both(*_inputs([1500, 700], 2, 1, 128), None, "1500+700")
+    _both(*_inputs([1000, 777], 12, 12, 64), None, "1000+777")
     _both(*_inputs([1100, 700], 16, 16, 128), None, "1100+700")
     _both(*_inputs([13 * i % 97 for i in range(64)], 2, 2, 64), None, "64 sequences")
 
@@ -312,7 +322,7 @@ def test_fused_buffers_and_tokens_behind_the_last_sequence(dim):
     assert (fused[:, -8:] == 7).all()
 
 
-@pytest.mark.parametrize("dim,kv", [(64, 1), (128, 1), (64, 64)])
+@pytest.mark.parametrize("dim,kv", [(64, 1), (128, 1), (64, 64), (64, 20)])
 @pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
 @pytest.mark.parametrize("where", [0, 5, 31, 32, 40, 63, 64, 100, 149])
 def test_special_values_reach_later_rows_only(where, value, dim, kv):
@@ -343,7 +353,7 @@ def test_special_values_reach_later_rows_only(where, value, dim, kv):
         _check_forward(out, lse, q, k, v, cu, dim ** -0.5, f"{value} at {where}")
 
 
-@pytest.mark.parametrize("kv", [1, 32])
+@pytest.mark.parametrize("kv", [1, 20, 32])
 def test_scores_of_minus_infinity(kv):
     """Keys whose scores are -inf for every row: rows that see others as well have what
     the formula gives, in a wavefront that sees only such keys, too."""
