@@ -19,10 +19,11 @@ struct EmbeddingArgs {
 hipError_t launch_embedding_forward(int table_bf16, int out_bf16, const EmbeddingArgs& a, hipStream_t st);
 
 constexpr int kSortThreads = 1024;
-// Up to 8192 tokens are ranked among each other; of more, a workgroup sorts 4096.  Whole
-// gradient of so many tokens into rows of 64 columns, in us, ranked and sorted: 12288 into
-// 151936 rows 35.3 and 44.7, 16384 into 300 rows (a single pass) 38.0 and 26.5.
-constexpr int kSortAlone = 8, kSortBeside = 4;              // per thread
+// Up to 8192 tokens, and up to 16384 whose keys would take several passes, are ranked
+// among each other; of others, a workgroup sorts 4096.  Whole gradient into rows of 64
+// columns, in us, ranked and sorted: 8192 tokens of 300 rows (a pass) 24 and 25.5, 16384 of them
+// 38.0 and 24.7; of 151936 rows (two passes) 12288 tokens 35.1 and 41, 16384 40.4 and 41.4.
+constexpr int kSortAlone = 16, kSortBeside = 4;             // per thread
 constexpr int64_t kSortBlock = kSortThreads * kSortBeside;
 constexpr int kSortDigits = 1024;                           // at most, of one pass
 
@@ -36,8 +37,8 @@ inline SortPlan plan_sort(int64_t count, int64_t rows) {
   int bits = 1;
   while (((int64_t)1 << bits) <= rows) ++bits;
   const int passes = (bits + 9) / 10;
-  return SortPlan{passes, (bits + passes - 1) / passes,
-                  count <= kSortThreads * kSortAlone ? 1 : (count + kSortBlock - 1) / kSortBlock};
+  const bool alone = count <= kSortThreads * (passes > 1 ? kSortAlone : kSortAlone / 2);
+  return SortPlan{passes, (bits + passes - 1) / passes, alone ? 1 : (count + kSortBlock - 1) / kSortBlock};
 }
 // Sorted tokens that one workgroup adds up.
 inline int64_t sum_run(int64_t count) { return count <= 65536 ? 16 : 64; }

@@ -125,7 +125,7 @@ __global__ __launch_bounds__(kThreads) void clear_rows_kernel(EmbeddingGradArgs 
       store8<O>(reinterpret_cast<O*>(p.dtable) + row * p.ldt, c, (int)p.cols, zeros);
 }
 
-// Up to 8192 tokens: a token's place is the number of smaller keys, and of equal ones
+// Up to 8192 or 16384 tokens: a token's place is the number of smaller keys, and of equal ones
 // before it.  A workgroup ranks 32 tokens against all keys, 32 slices of them side by side.
 // n^2 comparisons of about three instructions, but on all CUs, in one launch and without
 // a pass per digit: 8192 tokens 10.3 us, bound by issue (a sort of 18 bits by one workgroup:
@@ -177,7 +177,8 @@ __global__ __launch_bounds__(kSortThreads) void sort_ranks_kernel(EmbeddingGradA
 
 // More tokens: per pass the digits' counts of every workgroup, where each begins, and
 // the keys put there.  `from` is the buffer read (pass 0: the tokens).  20000 tokens, a pass:
-// 6.0 + 3.3 + 8.7 us, latencies of 5 workgroups.
+// 6.0 + 10.0 us, latencies of 5 workgroups (18 us with a launch between for the beginnings,
+// which more than 32 workgroups have).
 __device__ __forceinline__ void read_keys(const EmbeddingGradArgs& p, int pass, int from, int64_t first,
                                           uint32_t (&key)[kSortBeside], uint32_t (&place)[kSortBeside]) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -209,10 +210,25 @@ __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(EmbeddingGradA
 }
 static_assert(kSortDigits == kSortThreads, "a thread per digit");
 
+// The sum of the threads' values before this one's.
+__device__ __forceinline__ uint32_t sum_before(uint32_t value, uint32_t (&sums)[kWaves]) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  uint32_t sum = value;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const uint32_t up = __shfl_up(sum, off, 64);
+    if (lane >= off) sum += up;
+  }
+  if (lane == 63) sums[wave] = sum;
+  __syncthreads();
+  for (int w = 0; w < wave; ++w) sum += sums[w];
+  return sum - value;
+}
+
 // digits[block][d] -> where block's keys of digit d begin.
 __global__ __launch_bounds__(kSortThreads) void sort_begin_kernel(EmbeddingGradArgs p, SortPlan plan) {
   __shared__ uint32_t sums[kWaves];
-  const int d = threadIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int d = threadIdx.x;
   const bool live = d < 1 << plan.bits;
   constexpr int kAhead = 16;
   uint32_t c[kAhead];
@@ -227,16 +243,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_begin_kernel(EmbeddingGradA
 #pragma unroll
       for (int b = 0; b < kAhead; ++b) total += b0 + b < plan.blocks ? c[b] : 0;
     }
-  uint32_t sum = total;
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const uint32_t up = __shfl_up(sum, off, 64);
-    if (lane >= off) sum += up;
-  }
-  if (lane == 63) sums[wave] = sum;
-  __syncthreads();
-  for (int w = 0; w < wave; ++w) sum += sums[w];
-  uint32_t at = sum - total;
+  uint32_t at = sum_before(total, sums);
   if (!live) return;
   for (int64_t b0 = 0; b0 < plan.blocks; b0 += kAhead) {
     load(b0);
@@ -248,8 +255,12 @@ __global__ __launch_bounds__(kSortThreads) void sort_begin_kernel(EmbeddingGradA
   }
 }
 
+// OWN: of few workgroups each finds by itself where its keys begin, from the counts.
+constexpr int64_t kOwnBegin = 32;
+template <bool OWN>
 __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(EmbeddingGradArgs p, SortPlan plan, int pass, int from, int to) {
   __shared__ SortLds lds;
+  __shared__ uint32_t sums[kWaves];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t first = (int64_t)blockIdx.x * kSortBlock;
   uint32_t key[kSortBeside], place[kSortBeside], rank[kSortBeside];
@@ -259,8 +270,25 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(EmbeddingGradA
   count_digits<kSortBeside>(lds, key, rank, p.count - first, shift, plan.bits);
   // before this wavefront's keys of a digit: the other workgroups' and wavefronts'
   const int d = threadIdx.x;
+  uint32_t at = 0;
+  if constexpr (OWN) {
+    uint32_t all = 0;
+    constexpr int kAhead = 8;
+    for (int b0 = 0; b0 < (int)plan.blocks; b0 += kAhead) {
+      uint32_t c[kAhead];
+#pragma unroll
+      for (int b = 0; b < kAhead; ++b) c[b] = p.digits[min(b0 + b, (int)plan.blocks - 1) * kSortDigits + d];
+#pragma unroll
+      for (int b = 0; b < kAhead; ++b) {
+        all += b0 + b < (int)plan.blocks ? c[b] : 0;
+        at += b0 + b < (int)blockIdx.x ? c[b] : 0;
+      }
+    }
+    at += sum_before(all, sums);
+  } else if (d <= (int)mask) {
+    at = p.digits[(int64_t)blockIdx.x * kSortDigits + d];
+  }
   if (d <= (int)mask) {
-    uint32_t at = p.digits[(int64_t)blockIdx.x * kSortDigits + d];
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
       const uint32_t c = lds.count[w][d];
@@ -460,8 +488,12 @@ hipError_t backward_for(const EmbeddingGradArgs& a, hipStream_t st) {
       const int from = which;
       which = pass == 0 ? 0 : 1 - which;
       hipLaunchKernelGGL(sort_count_kernel, grid, block, 0, st, a, plan, pass, from);
-      hipLaunchKernelGGL(sort_begin_kernel, dim3(1), block, 0, st, a, plan);
-      hipLaunchKernelGGL(sort_place_kernel, grid, block, 0, st, a, plan, pass, from, which);
+      if (plan.blocks <= kOwnBegin) {
+        hipLaunchKernelGGL(sort_place_kernel<true>, grid, block, 0, st, a, plan, pass, from, which);
+      } else {
+        hipLaunchKernelGGL(sort_begin_kernel, dim3(1), block, 0, st, a, plan);
+        hipLaunchKernelGGL(sort_place_kernel<false>, grid, block, 0, st, a, plan, pass, from, which);
+      }
       e = hipGetLastError();
       if (e != hipSuccess) return e;
     }

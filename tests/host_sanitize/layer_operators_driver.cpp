@@ -334,7 +334,7 @@ static void embedding() {
         const SortPlan p = plan_sort(n, r);
         CHECK(p.bits >= 1 && p.bits <= 10 && ((int64_t)1 << p.bits) <= kSortDigits);
         CHECK(((int64_t)1 << (p.bits * p.passes)) > r);
-        CHECK(p.blocks == 1 ? n <= kSortThreads * kSortAlone : p.blocks * kSortBlock >= n && (p.blocks - 1) * kSortBlock < n);
+        CHECK(p.blocks == 1 ? n <= kSortThreads * kSortAlone && (p.passes > 1 || n <= 8192) : n > 8192 && p.blocks * kSortBlock >= n && (p.blocks - 1) * kSortBlock < n);
         const int64_t runs = (n + sum_run(n) - 1) / sum_run(n);
         CHECK((int64_t)need >= 16 * n + (runs > 1 ? runs * 2 * cols * 4 : 0));
         if (r == 0 || r * cols * 4 > ((int64_t)1 << 38) || n * cols * 2 > ((int64_t)1 << 38)) continue;
