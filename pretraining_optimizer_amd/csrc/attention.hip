@@ -46,6 +46,9 @@ constexpr int kTile = 64;                // rows of a tile in LDS
 constexpr int kBufferConfig = 0x00020000;
 constexpr int kBehind = (int)0x80000000;  // an offset behind every descriptor's range
 constexpr float kLog2e = 1.4426950408889634f;
+// Running maxima begin here and not at -inf: where all scores so far are -inf, so would the
+// maximum be, and -inf minus itself is a NaN where 2^x of the difference has to be 0.
+constexpr float kLowest = -3.4028235e38f;
 
 // Row r's 16-byte chunk c sits at c ^ swizzle(r).  A row is 256 (128) bytes; 16 (8)
 // rows of one chunk, as an operand read has them, and 8 rows of 4 chunks, as a
@@ -368,7 +371,7 @@ __global__ __launch_bounds__(kThreads, PARTS == 4 ? 1 : 2) void attention_forwar
   f32x16_t acc[DP / 32];
 #pragma unroll
   for (int dt = 0; dt < DP / 32; ++dt) acc[dt] = splat(0.0f);
-  float top = -INFINITY, sum = 0.0f;   // both times c log2 e; the sum is of this lane's keys
+  float top = kLowest, sum = 0.0f;   // both times c log2 e; the sum is of this lane's keys
   const float c = p.scale * kLog2e;
 
   // N blocks of 32 keys; DIAG: the last is the rows' own.
@@ -403,13 +406,11 @@ __global__ __launch_bounds__(kThreads, PARTS == 4 ? 1 : 2) void attention_forwar
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[dt][r] *= f;
     }
-    // where all scores so far are -inf the maximum is no number to subtract
-    const float base = fmaxf(top, -3.4028235e38f);
 #pragma unroll
     for (int b = 0; b < N; ++b)
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        s[b][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][r], c, -base));
+        s[b][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][r], c, -top));
         sum += s[b][r];
       }
 #pragma unroll

@@ -503,3 +503,92 @@ def test_python_refusals():
     wide = torch.empty((1, 4, 136), dtype=torch.bfloat16, device="cuda")
     with pytest.raises(pm.MuonHError):
         pm.attention_forward(wide, wide, wide, cu)
+
+
+def _seen_softmax(q, k, v, scale, seen):
+    """out, lse and their tolerances of one head, for rows that see the keys of `seen`
+    [rows, keys]; NaN for a row that sees none."""
+    n, dim = q.shape
+    S = np.where(seen, scale * (q @ k.T), -np.inf)
+    top = S.max(axis=1)
+    some = np.isfinite(top)
+    top = np.where(some, top, 0.0)
+    lse = np.where(some, top + np.log(np.maximum(np.exp(S - top[:, None]).sum(axis=1), 1e-300)), np.nan)
+    P = np.exp(S - np.where(some, lse, 0.0)[:, None])
+    size = np.where(seen, np.abs(np.where(seen, S, 0.0)) + np.abs(lse)[:, None] + 1, 0.0)
+    worst = np.where(seen, scale * dim * U * (np.abs(q) @ np.abs(k).T) + 8 * U * size, 0.0).max(axis=1)
+    out = np.where(some[:, None], P @ v, np.nan)
+    tol = (P @ np.abs(v)) * (B + 2 * worst + 2 * n * U)[:, None]
+    return out, lse, tol + B * (np.abs(out) + tol), worst + n * U
+
+
+# heads of one sequence of 300 tokens: rows in four parts, in two, in one; of 64 columns and of 128
+SPLITS = [(2, 64), (2, 128), (30, 64), (30, 128), (90, 64)]
+
+
+@pytest.mark.parametrize("heads,dim", SPLITS)
+@pytest.mark.parametrize("masked", [32, 64, 70, 128, 200])
+def test_keys_that_only_some_rows_of_a_wavefront_see(masked, heads, dim):
+    """The first keys hold bf16's lowest value in a spare column, where some rows' q has 8
+    and the others' 0: those rows' scores are -inf there, beside rows whose scores are finite.
+    A row has what the formula gives without its masked keys; where it sees no other, lse
+    is -inf, the logarithm of an empty sum, and out NaN."""
+    announce(f"attention {masked} keys masked for some rows, {heads} heads of {dim}")
+    n = 300
+    q, k, v, do, cu = _inputs([n], heads, heads, dim)
+    flagged = torch.arange(n, device="cuda") * 7 % 16 < 9
+    q[:, :, -1] = torch.where(flagged, 8.0, 0.0).bfloat16()[:, None]
+    k[:, :, -1] = 0.0
+    k[:masked, :, -1] = torch.finfo(torch.bfloat16).min
+    out, lse = pm.attention_forward(q, k, v, cu)
+    i, j = np.arange(n)[:, None], np.arange(n)[None]
+    seen = (j <= i) & ~(_np(flagged.float())[:, None].astype(bool) & (j < masked))
+    clean = _np(k)
+    clean[:, :, -1] = 0.0   # masked keys are left out by `seen`, elsewhere q or k is 0 there
+    O, L, Q, V = _np(out), _np(lse), _np(q), _np(v)
+    assert np.array_equal(L == -np.inf, np.broadcast_to(~seen.any(axis=1), L.shape)) and not np.isnan(L).any()
+    for h in {0, heads // 2, heads - 1}:
+        want, wl, tol, ltol = _seen_softmax(Q[:, h], clean[:, h], V[:, h], dim ** -0.5, seen)
+        some = seen.any(axis=1)
+        assert np.all(np.abs(O[some, h] - want[some]) <= tol[some]), (h, "out")
+        assert np.isnan(O[~some, h]).all()
+        assert np.all(np.abs(L[h, some] - wl[some]) <= ltol[some]), (h, "lse")
+
+
+@pytest.mark.parametrize("heads,dim", SPLITS)
+def test_gradients_of_keys_that_only_some_rows_see(heads, dim):
+    """As above, with rows masked only where they see other keys, so that all have a
+    result: masked keys add nothing to the gradients of those rows, nor these to theirs."""
+    announce(f"attention gradients of masked keys, {heads} heads of {dim}")
+    n, masked = 300, 100
+    q, k, v, do, cu = _inputs([n], heads, heads, dim)
+    at = torch.arange(n, device="cuda")
+    flagged = (at * 7 % 16 < 9) & (at >= masked)
+    q[:, :, -1] = torch.where(flagged, 8.0, 0.0).bfloat16()[:, None]
+    k[:, :, -1] = 0.0
+    clean = k.clone()
+    k[:masked, :, -1] = torch.finfo(torch.bfloat16).min
+    out, lse = pm.attention_forward(q, k, v, cu)
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+    dq, dk, dv = (_np(t) for t in pm.attention_backward(do, q, k, v, out, lse, cu))
+    i, j = np.arange(n)[:, None], np.arange(n)[None]
+    seen = (j <= i) & ~(_np(flagged.float())[:, None].astype(bool) & (j < masked))
+    Q, K, V, DO, O, L = (_np(t) for t in (q, clean, v, do, out, lse))
+    c = dim ** -0.5
+    for h in {0, heads // 2, heads - 1}:
+        a, b, vh, d = Q[:, h], K[:, h], V[:, h], DO[:, h]
+        S = c * (a @ b.T)
+        P = np.where(seen, np.exp(np.where(seen, S, 0.0) - L[h][:, None]), 0.0)
+        ep = c * dim * U * (np.abs(a) @ np.abs(b).T) + 8 * U * (np.abs(S) + np.abs(L[h])[:, None] + 1)
+        delta = (d * O[:, h]).sum(axis=1, keepdims=True)
+        ed = dim * U * (np.abs(d) @ np.abs(vh).T + np.abs(d * O[:, h]).sum(axis=1, keepdims=True))
+        dP = d @ vh.T
+        ds = c * P * (dP - delta)
+        eds = np.abs(ds) * (B + 2 * ep) + c * P * (ed + 2 * U * np.abs(dP - delta))
+        for name, got, want, tol in (
+                # the spare column of dq is a sum of products with the lowest value
+                ("dq", dq[:, h, :-1], (ds @ b)[:, :-1], (eds @ np.abs(b) + 2 * n * U * (np.abs(ds) @ np.abs(b)))[:, :-1]),
+                ("dk", dk[:, h], ds.T @ a, eds.T @ np.abs(a) + 2 * n * U * (np.abs(ds).T @ np.abs(a))),
+                ("dv", dv[:, h], P.T @ d, (P * (B + 2 * ep + 2 * n * U)).T @ np.abs(d))):
+            tol = tol + B * (np.abs(want) + tol)
+            assert np.all(np.abs(got - want) <= tol), (name, h, float((np.abs(got - want) - tol).max()))
