@@ -472,7 +472,8 @@ int muonh_norm_backward(const muonh_norm_grad_args* args, void* stream);
  * softmax statistics and all sums are fp32; P and dS are rounded to bf16 where they
  * are multiplied, results once.  Sums run in a fixed order.
  *
- * Rows that no sequence holds are neither read nor written.  The device reads
+ * Rows that no sequence holds, before the first and behind the last, are not read; in the
+ * results that zero_rest names they become zeros, in others they stay as they were.  The device reads
  * cu_seqlens: ends are taken into [0, tokens] and a sequence that would end before
  * it starts is empty, but sequences that overlap give undefined results.  An
  * infinity or a NaN in a token of k or v reaches out and lse of later rows of its
@@ -480,6 +481,12 @@ int muonh_norm_backward(const muonh_norm_grad_args* args, void* stream);
  * every gradient of its sequence.  Other sequences' results do not change.
  * An output or workspace that overlaps an input or another output is refused, unless
  * they lie side by side in rows of one pitch.                                */
+#define MUONH_ZERO_OUT 1
+#define MUONH_ZERO_LSE 2
+#define MUONH_ZERO_DQ 4
+#define MUONH_ZERO_DK 8
+#define MUONH_ZERO_DV 16
+
 typedef struct muonh_attention_args {
   const void*    q;
   const void*    k;
@@ -494,6 +501,8 @@ typedef struct muonh_attention_args {
   int32_t        kv_heads;    /* >= 1                                             */
   int32_t        dim;         /* 8, 16, .. 128                                    */
   float          scale;       /* > 0, usually dim^-1/2                            */
+  int32_t        zero_rest;   /* a sum of MUONH_ZERO_*                            */
+  int32_t        reserved;    /* must be 0                                        */
 } muonh_attention_args;
 
 typedef struct muonh_attention_grad_args {

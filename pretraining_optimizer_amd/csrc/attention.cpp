@@ -16,6 +16,8 @@ namespace {
 
 constexpr int64_t kMaxPitch = ((int64_t)1 << 23) - 1;   // 128 rows stay below 2^31 bytes
 
+constexpr int32_t kZeroResults = MUONH_ZERO_OUT | MUONH_ZERO_LSE, kZeroGradients = MUONH_ZERO_DQ | MUONH_ZERO_DK | MUONH_ZERO_DV;
+
 // A tensor [tokens, cols] of bf16 with ld elements between tokens.
 struct Tensor {
   const void* p;
@@ -52,18 +54,24 @@ int check_shape(const muonh_attention_args& g) {
     return fail(MUONH_EINVAL, "heads must be a multiple of kv_heads, both at least 1");
   if (g.dim < 8 || g.dim > 128 || g.dim % 8 != 0) return fail(MUONH_EINVAL, "dim must be 8, 16, .. 128");
   if (!(g.scale > 0.0f) || !std::isfinite(g.scale)) return fail(MUONH_EINVAL, "scale must be > 0 and finite");
-  if (attention_blocks(g.tokens, g.sequences, kAttentionRows) * 2 * kAttentionThreads > kMaxThreads / g.heads)
+  if (g.zero_rest & ~(kZeroResults | kZeroGradients)) return fail(MUONH_EINVAL, "zero_rest must be a sum of MUONH_ZERO_*");
+  if (g.reserved != 0) return fail(MUONH_EINVAL, "reserved != 0");
+  if (attention_blocks(g.tokens, g.sequences + (g.zero_rest != 0), kAttentionRows) * 2 * kAttentionThreads > kMaxThreads / g.heads)
     return fail(MUONH_EINVAL, "tokens, sequences and heads are too many for one launch");
   return MUONH_OK;
 }
 
 size_t row_bytes(const muonh_attention_args& g) { return (size_t)(g.heads * g.tokens) * sizeof(float); }
+// Whether a call writes nothing; `zeros` are its results' bits of zero_rest.
+bool nothing_to_do(const muonh_attention_args& g, int32_t zeros) {
+  return g.tokens == 0 || (g.sequences == 0 && !(g.zero_rest & zeros));
+}
 // Two rows of floats per head, each from a multiple of 256 bytes on.
 size_t workspace_of(const muonh_attention_args& g) {
   return g.sequences == 0 ? 0 : 2 * (size_t)ceil_div((int64_t)row_bytes(g), kAlign) * kAlign;
 }
 
-AttentionArgs device_args(const muonh_attention_args& g) {
+AttentionArgs device_args(const muonh_attention_args& g, int32_t zeros) {
   AttentionArgs a{};
   a.q = static_cast<const uint16_t*>(g.q);
   a.k = static_cast<const uint16_t*>(g.k);
@@ -81,6 +89,7 @@ AttentionArgs device_args(const muonh_attention_args& g) {
   a.kv_heads = g.kv_heads;
   a.dim = g.dim;
   a.scale = g.scale;
+  a.zero_rest = g.zero_rest & zeros;
   return a;
 }
 
@@ -119,7 +128,7 @@ int muonh_attention_forward(const muonh_attention_args* g, void* stream) {
     const Tensor out{g->out, g->ld_out, cols, "out"};
     for (const Tensor* t : {&ins[0], &ins[1], &ins[2], &out})
       if ((rc = check_tensor(*t))) return rc;
-    if (g->tokens == 0 || g->sequences == 0) return MUONH_OK;
+    if (nothing_to_do(*g, kZeroResults)) return MUONH_OK;
     for (const Tensor* t : {&ins[0], &ins[1], &ins[2], &out})
       if ((rc = check_address(*t))) return rc;
     if (!g->lse || !g->cu_seqlens) return fail(MUONH_EINVAL, "null pointer: lse or cu_seqlens");
@@ -127,7 +136,7 @@ int muonh_attention_forward(const muonh_attention_args* g, void* stream) {
     const Span lse{g->lse, (int64_t)row_bytes(*g)}, cu{g->cu_seqlens, (g->sequences + 1) * 4};
     if ((rc = check_sharing(&out, 1, ins, 3, g->tokens, {lse}, {cu}))) return rc;
     forget_older_errors();
-    return launched(launch_attention_forward(device_args(*g), reinterpret_cast<hipStream_t>(stream)), "attention_forward");
+    return launched(launch_attention_forward(device_args(*g, kZeroResults), reinterpret_cast<hipStream_t>(stream)), "attention_forward");
   });
 }
 
@@ -155,7 +164,7 @@ int muonh_attention_backward(const muonh_attention_grad_args* b, void* stream) {
       if ((rc = check_tensor(t))) return rc;
     for (const Tensor& t : outs)
       if ((rc = check_tensor(t))) return rc;
-    if (g->tokens == 0 || g->sequences == 0) return MUONH_OK;
+    if (nothing_to_do(*g, kZeroGradients)) return MUONH_OK;
     for (const Tensor& t : ins)
       if ((rc = check_address(t))) return rc;
     for (const Tensor& t : outs)
@@ -163,14 +172,14 @@ int muonh_attention_backward(const muonh_attention_grad_args* b, void* stream) {
     if (!g->lse || !g->cu_seqlens) return fail(MUONH_EINVAL, "null pointer: lse or cu_seqlens");
     if (!aligned(g->lse, 4) || !aligned(g->cu_seqlens, 4)) return fail(MUONH_EINVAL, "misaligned lse or cu_seqlens");
     const size_t need = workspace_of(*g);
-    if (!b->workspace || b->workspace_bytes < need)
+    if (need > 0 && (!b->workspace || b->workspace_bytes < need))
       return fail(MUONH_ENOMEM, "workspace too small: need " + std::to_string(need) + " bytes");
     if (!aligned(b->workspace, kAlign)) return fail(MUONH_EINVAL, "workspace must be 256-byte aligned");
     const Span lse{g->lse, (int64_t)row_bytes(*g)}, cu{g->cu_seqlens, (g->sequences + 1) * 4};
     const Span ws{b->workspace, (int64_t)need};
     if ((rc = check_sharing(outs, 3, ins, 5, g->tokens, {ws}, {lse, cu}))) return rc;
     AttentionGradArgs a{};
-    a.a = device_args(*g);
+    a.a = device_args(*g, kZeroGradients);
     a.dout = static_cast<const uint16_t*>(b->dout);
     a.dq = static_cast<uint16_t*>(b->dq);
     a.dk = static_cast<uint16_t*>(b->dk);

@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "../../include/muonh.h"
+
 namespace muonh {
 
 constexpr int kAttentionThreads = 256;
@@ -21,6 +23,7 @@ struct AttentionArgs {
   int32_t tokens, sequences, heads, kv_heads, dim;
   int32_t blocks;                 // set by the launchers: attention_blocks() of the kernel's rows
   float scale;
+  int32_t zero_rest;              // MUONH_ZERO_*: results whose rows that no sequence holds become zeros
 };
 struct AttentionGradArgs {
   AttentionArgs a;

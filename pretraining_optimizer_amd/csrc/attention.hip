@@ -263,6 +263,47 @@ __device__ __forceinline__ Place find_place(const AttentionArgs& p, int rank) {
   return Place{s, e - s, (KEYS ? __builtin_amdgcn_readlane(n, b) - h : h - 1) * ROWS};
 }
 
+// The rows that no sequence holds, before the first and behind the last, shared out among
+// the workgroups that have no rows of a sequence: zero(row, columns' first) for every 8
+// columns, 16 threads a row.  With zero_rest a launch has room for one more sequence, so there
+// is such a workgroup for every head.
+template <bool KEYS, int ROWS, int THREADS, typename F>
+__device__ __forceinline__ void each_rest(const AttentionArgs& p, int rank, F zero) {
+  int first, last, share, shares;
+  if (p.sequences > 64) {
+    first = sequence_end(p, 0);
+    last = max(sequence_end(p, p.sequences), first);
+    const int used = last / ROWS + p.sequences;
+    share = (KEYS ? rank : p.blocks - 1 - rank) - used;
+    shares = p.blocks - used;
+    if (share < 0) return;   // a number that a sequence's cut block left over
+  } else {
+    const int lane = threadIdx.x & 63;
+    int n = 0;
+    first = p.tokens;
+    last = 0;
+    if (lane < p.sequences) {
+      first = sequence_end(p, lane);
+      last = max(sequence_end(p, lane + 1), first);
+      n = (last - first + ROWS - 1) / ROWS;
+    }
+    const int used = wave_sum(n);
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) {
+      first = min(first, __shfl_xor(first, off, 64));
+      last = max(last, __shfl_xor(last, off, 64));
+    }
+    last = max(last, first);
+    share = rank - used;
+    shares = p.blocks - used;
+  }
+  constexpr int kRowsAtOnce = THREADS / 16;
+  const int64_t rest = (int64_t)first + p.tokens - last;
+  for (int64_t i = (int64_t)share * kRowsAtOnce + threadIdx.x / 16; i < rest; i += (int64_t)shares * kRowsAtOnce)
+    zero(i < first ? i : last - first + i, 8 * (int)(threadIdx.x % 16));
+}
+__device__ __forceinline__ void zero8(uint16_t* p) { st_global<u32x4_t>(p, u32x4_t{0, 0, 0, 0}); }
+
 // Workgroup i's key head, head of its group and rank.  Workgroups i, i + 8, .. run on one
 // XCD: with the key head first, an XCD's have few different ones, whose rows stay in its
 // L2, and all ranks.
@@ -354,7 +395,14 @@ __global__ __launch_bounds__(kThreads, PARTS == 4 ? 1 : 2) void attention_forwar
   const Item item = item_of(p.kv_heads, group);
   const int kv = item.kv, head = kv * group + item.member;
   const Place at = find_place<false, kRows>(p, item.rank);
-  if (at.row < 0) return;
+  if (at.row < 0) {
+    if (p.zero_rest)
+      each_rest<false, kRows, kThreads>(p, item.rank, [&](int64_t t, int c) {
+        if ((p.zero_rest & MUONH_ZERO_OUT) && c < p.dim) zero8(p.out + t * p.ldo + head * p.dim + c);
+        if ((p.zero_rest & MUONH_ZERO_LSE) && c == 0) p.lse[head * (int64_t)p.tokens + t] = 0.0f;
+      });
+    return;
+  }
 
   const Rows q{p.q + at.start * p.ldq + head * p.dim, p.ldq, at.len, p.dim};
   const Rows k{p.k + at.start * p.ldk + kv * p.dim, p.ldk, at.len, p.dim};
@@ -572,7 +620,7 @@ __global__ __launch_bounds__(kThreads, PARTS == 4 ? 1 : 2) void attention_dq_ker
   const Item item = item_of(p.kv_heads, group);
   const int kv = item.kv, head = kv * group + item.member;
   const Place at = find_place<false, kRows>(p, item.rank);
-  if (at.row < 0) return;
+  if (at.row < 0) return;   // the other kernel clears dq's rows that no sequence holds, too
 
   const Rows q{p.q + at.start * p.ldq + head * p.dim, p.ldq, at.len, p.dim};
   const Rows k{p.k + at.start * p.ldk + kv * p.dim, p.ldk, at.len, p.dim};
@@ -740,7 +788,17 @@ __global__ __launch_bounds__(kKeyThreads, 2) void attention_dkv_kernel(Attention
   const Item item = item_of(p.kv_heads, 1);
   const int kv = item.kv;
   const Place at = find_place<true, kKeys>(p, item.rank);
-  if (at.row < 0) return;
+  if (at.row < 0) {
+    if (p.zero_rest)
+      each_rest<true, kKeys, kKeyThreads>(p, item.rank, [&](int64_t t, int c) {
+        if (c >= p.dim) return;
+        if (p.zero_rest & MUONH_ZERO_DQ)
+          for (int h = 0; h < group; ++h) zero8(g.dq + t * g.lddq + (kv * group + h) * p.dim + c);
+        if (p.zero_rest & MUONH_ZERO_DK) zero8(g.dk + t * g.lddk + kv * p.dim + c);
+        if (p.zero_rest & MUONH_ZERO_DV) zero8(g.dv + t * g.lddv + kv * p.dim + c);
+      });
+    return;
+  }
 
   const Rows k{p.k + at.start * p.ldk + kv * p.dim, p.ldk, at.len, p.dim};
   const Rows v{p.v + at.start * p.ldv + kv * p.dim, p.ldv, at.len, p.dim};
@@ -932,7 +990,7 @@ static bool keys_split(const AttentionArgs& a) {
 // A kernel over blocks of `rows` rows of so many heads.
 template <typename K, typename A>
 static hipError_t launch_blocks(K kernel, A args, AttentionArgs& a, int rows, int heads, int threads, hipStream_t st) {
-  a.blocks = (int32_t)attention_blocks(a.tokens, a.sequences, rows);
+  a.blocks = (int32_t)attention_blocks(a.tokens, (int64_t)a.sequences + (a.zero_rest != 0), rows);
   hipLaunchKernelGGL(kernel, dim3((unsigned)((int64_t)a.blocks * heads)), dim3((unsigned)threads), 0, st, args());
   return hipGetLastError();
 }

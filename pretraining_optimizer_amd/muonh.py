@@ -31,6 +31,12 @@ MUONH_MODE_HYPERBALL = 0
 MUONH_MODE_MUON_WD = 1
 MUONH_MODE_ELR_ALIGNED = 2
 
+MUONH_ZERO_OUT = 1
+MUONH_ZERO_LSE = 2
+MUONH_ZERO_DQ = 4
+MUONH_ZERO_DK = 8
+MUONH_ZERO_DV = 16
+
 PHASES = ("momentum", "ns_gram", "ns_poly", "ns_apply", "ns_apply_last", "finalize", "update")
 
 
@@ -115,7 +121,7 @@ class muonh_attention_args(ctypes.Structure):
                 ("tokens", ctypes.c_int64), ("sequences", ctypes.c_int64), ("ld_q", ctypes.c_int64),
                 ("ld_k", ctypes.c_int64), ("ld_v", ctypes.c_int64), ("ld_out", ctypes.c_int64),
                 ("heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("dim", ctypes.c_int32),
-                ("scale", ctypes.c_float)]
+                ("scale", ctypes.c_float), ("zero_rest", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 class muonh_attention_grad_args(ctypes.Structure):

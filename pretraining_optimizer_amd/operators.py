@@ -25,9 +25,10 @@ from __future__ import annotations
 import ctypes
 from typing import Optional
 
-from .muonh import (MUONH_BF16, MUONH_F32, _check, _record, load_library, muonh_add_norm_args,
-                    muonh_add_norm_grad_args, muonh_attention_args, muonh_attention_grad_args, muonh_embedding_args,
-                    muonh_embedding_grad_args, muonh_fp8_matrix, muonh_norm_args, muonh_norm_grad_args)
+from .muonh import (MUONH_BF16, MUONH_F32, MUONH_ZERO_DK, MUONH_ZERO_DQ, MUONH_ZERO_DV, MUONH_ZERO_LSE,
+                    MUONH_ZERO_OUT, _check, _record, load_library, muonh_add_norm_args, muonh_add_norm_grad_args,
+                    muonh_attention_args, muonh_attention_grad_args, muonh_embedding_args, muonh_embedding_grad_args,
+                    muonh_fp8_matrix, muonh_norm_args, muonh_norm_grad_args)
 
 # The smallest calls are bound by this module: a launch takes about 3.5 us,
 # a tensor 1.5 us, torch.cuda.current_stream() 2.8 us.  So the library and
@@ -579,17 +580,20 @@ def _attention(q, k, v, cu_seqlens, scale, out, lse, stream):
     if cu_seqlens.dtype is not _torch.int32 or cu_seqlens.dim() != 1 or ends < 1 or not cu_seqlens.is_contiguous():
         raise ValueError("cu_seqlens: a contiguous int32 vector of sequences + 1 elements is required")
     dev = _here(q, k, v, cu_seqlens, out, lse)
+    zero = 0
     if out is None:
         out, ld_out = _like(q, (tokens, heads, dim), stream), heads * dim
+        zero |= MUONH_ZERO_OUT
     else:
         ld_out = _heads(out, tokens, heads, dim, "out")
     if lse is None:
         lse = _empty((heads, tokens), _torch.float32, q.device, stream)
+        zero |= MUONH_ZERO_LSE
     elif lse.dtype is not _torch.float32 or lse.shape != (heads, tokens) or not lse.is_contiguous():
         raise ValueError(f"lse: a contiguous float32 tensor of shape {(heads, tokens)} is required")
     args = muonh_attention_args(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
                                 cu_seqlens.data_ptr(), tokens, ends - 1, ld_q, ld_k, ld_v, ld_out, heads,
-                                kv_heads, dim, dim ** -0.5 if scale is None else scale)
+                                kv_heads, dim, dim ** -0.5 if scale is None else scale, zero)
     return args, out, lse, dev
 
 
@@ -604,7 +608,8 @@ def attention_forward(q, k, v, cu_seqlens, scale: Optional[float] = None, out=No
     scale      : of the scores, > 0; dim^-1/2 if None
     out, lse   : memory of the results; lse is float32 [heads, tokens], the log of
                  each row's sum of exponentials, which the backward pass reads
-    Tokens behind the last sequence are left as they were.
+    Rows of tokens that no sequence holds (padding behind the last one) are zeros in new
+    results and stay as they were in memory that is passed in.
     """
     args, out, lse, dev = _attention(q, k, v, cu_seqlens, scale, out, lse, stream)
     if stream is not None:
@@ -621,7 +626,7 @@ def attention_backward(dout, q, k, v, out, lse, cu_seqlens, scale: Optional[floa
     results.
 
     dq, dk, dv : their memory (slices of one fused gradient will do)
-    Tokens behind the last sequence are left as they were.
+    Rows of tokens that no sequence holds: as attention_forward has them.
     """
     if out is None or lse is None:
         raise ValueError("out and lse are the forward pass's results")
@@ -632,9 +637,13 @@ def attention_backward(dout, q, k, v, out, lse, cu_seqlens, scale: Optional[floa
     _here(q, dout, dq, dk, dv)
     lds = []
     grads = []
-    for t, like, n, what in ((dq, q, heads, "dq"), (dk, k, kv_heads, "dk"), (dv, v, kv_heads, "dv")):
+    for t, like, n, what, zero in ((dq, q, heads, "dq", MUONH_ZERO_DQ), (dk, k, kv_heads, "dk", MUONH_ZERO_DK),
+                                   (dv, v, kv_heads, "dv", MUONH_ZERO_DV)):
         lds.append(n * dim if t is None else _heads(t, tokens, n, dim, what))
-        grads.append(_like(like, (tokens, n, dim), stream) if t is None else t)
+        if t is None:
+            t = _like(like, (tokens, n, dim), stream)
+            args.zero_rest |= zero
+        grads.append(t)
     dq, dk, dv = grads
     need = ctypes.c_size_t()
     rc = _lib.muonh_attention_backward_workspace(ctypes.byref(args), ctypes.byref(need))

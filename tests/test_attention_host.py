@@ -2,6 +2,7 @@
 returns its status before any device work."""
 
 import ctypes
+import os
 
 import pytest
 
@@ -95,3 +96,29 @@ def test_nothing_to_do_needs_no_pointer():
         need = ctypes.c_size_t(7)
         assert lib.muonh_attention_backward_workspace(ctypes.byref(_args(**kw)), ctypes.byref(need)) == mb.MUONH_OK
         assert need.value == 0
+
+
+def test_zero_rest_is_checked():
+    """Unknown bits are refused; with a bit of the call's own results there is something to do
+    without sequences, too, so pointers are required."""
+    lib = pm.load_library()
+    forward = lambda **kw: lib.muonh_attention_forward(ctypes.byref(_args(**kw)), None)  # noqa: E731
+    backward = lambda **kw: lib.muonh_attention_backward(ctypes.byref(_grad(**kw)), None)  # noqa: E731
+    own = {forward: mb.MUONH_ZERO_OUT | mb.MUONH_ZERO_LSE, backward: mb.MUONH_ZERO_DQ | mb.MUONH_ZERO_DK | mb.MUONH_ZERO_DV}
+    for call in (forward, backward):
+        for bad in (32, -1, 64 + 1):
+            _refused(call(zero_rest=bad), mb.MUONH_EINVAL, "zero_rest")
+        _refused(call(reserved=1), mb.MUONH_EINVAL, "reserved")
+        for bit in (1, 2, 4, 8, 16):
+            rc = call(sequences=0, zero_rest=bit, q=None)
+            if bit & own[call]:
+                _refused(rc, mb.MUONH_EINVAL, "null pointer: q")
+            else:
+                assert rc == mb.MUONH_OK
+        assert call(tokens=0, zero_rest=31, q=None) == mb.MUONH_OK
+
+
+def test_zero_bits_are_the_headers():
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "muonh.h")).read()
+    for name in ("OUT", "LSE", "DQ", "DK", "DV"):
+        assert f"#define MUONH_ZERO_{name} {getattr(mb, 'MUONH_ZERO_' + name)}\n" in text

@@ -592,3 +592,78 @@ def test_gradients_of_keys_that_only_some_rows_see(heads, dim):
                 ("dv", dv[:, h], P.T @ d, (P * (B + 2 * ep + 2 * n * U)).T @ np.abs(d))):
             tol = tol + B * (np.abs(want) + tol)
             assert np.all(np.abs(got - want) <= tol), (name, h, float((np.abs(got - want) - tol).max()))
+
+
+def _fill_free_memory(*shapes):
+    """Leaves NaN in memory that the next tensors of these shapes and types are given."""
+    held = [torch.full(shape, float("nan"), dtype=dtype, device="cuda") for shape, dtype in shapes]
+    torch.cuda.synchronize()
+    del held
+
+
+@pytest.mark.parametrize("lens,front,tail", [
+    ([130, 35], 0, 70), ([130, 35], 9, 0), ([77], 0, 1), ([77], 300, 500), ([0], 0, 5), ([], 3, 4), ([128], 0, 128),
+    ([3] * 64, 1, 100), ([3] * 65, 1, 100), ([40, 0] * 40 + [0] * 20, 200, 300)], ids=str)
+@pytest.mark.parametrize("heads,kv,dim", [(2, 1, 64), (4, 2, 40), (2, 2, 128), (90, 90, 64), (32, 16, 128)])
+def test_new_results_are_zero_where_no_sequence_is(lens, front, tail, heads, kv, dim):
+    """Padded batches: results that the call makes are zeros in the rows before the first
+    sequence and behind the last one; the others' are those of the sequences alone."""
+    announce(f"attention {len(lens)} sequences of {sum(lens)}, {front} rows before and {tail} behind, {heads}/{kv} heads of {dim}")
+    bf16 = torch.bfloat16
+    n, live = front + sum(lens) + tail, slice(front, front + sum(lens))
+    q, k, v, do, _ = _inputs([n], heads, kv, dim)
+    cu = torch.tensor([front] + list(front + np.cumsum(lens)), dtype=torch.int32, device="cuda")
+    rest = torch.ones(n, dtype=torch.bool, device="cuda")
+    rest[live] = False
+    for t in (q, k, v, do):
+        t[rest] = float("nan")
+    qs, ks, rows = ((n, heads, dim), bf16), ((n, kv, dim), bf16), ((heads, n), torch.float32)
+    held = [torch.full(s, 3.0, dtype=t, device="cuda") for s, t in (qs, rows, qs, ks, ks)]
+    pm.attention_forward(q, k, v, cu, out=held[0], lse=held[1])
+    pm.attention_backward(do, q, k, v, held[0], held[1], cu, dq=held[2], dk=held[3], dv=held[4])
+    assert all((t[rest] == 3).all() for t in (held[0], *held[2:])) and (held[1][:, rest] == 3).all()
+    _fill_free_memory(qs, rows)
+    out, lse = pm.attention_forward(q, k, v, cu)
+    _fill_free_memory(qs, ks, ks)
+    grads = pm.attention_backward(do, q, k, v, out, lse, cu)
+    for got, kept in zip((out, lse.T, *grads), (held[0], held[1].T, *held[2:])):
+        assert torch.equal(got[live], kept[live])
+        assert (got[rest] == 0).all()
+    # a part of the results given
+    _fill_free_memory(qs, rows)
+    mine = torch.full_like(q, 3.0)
+    _, lse = pm.attention_forward(q, k, v, cu, out=mine)
+    assert torch.equal(mine, held[0]) and (lse[:, rest] == 0).all()
+    _fill_free_memory(qs, ks)
+    mine = torch.full_like(k, 3.0)
+    dq, dk, dv = pm.attention_backward(do, q, k, v, out, lse, cu, dv=mine)
+    assert torch.equal(mine, held[4]) and (dq[rest] == 0).all() and (dk[rest] == 0).all()
+
+
+def test_a_captured_call_whose_sequences_change():
+    """cu_seqlens is read by the device, so a graph's sequences may become shorter: rows
+    that they leave are zeros in the graph's results, on a stream of its own, too."""
+    announce("attention graph with changing sequences")
+    q, k, v, do, _ = _inputs([300], 4, 2, 64)
+    cu = torch.tensor([0, 180, 300], dtype=torch.int32, device="cuda")
+    both = lambda st=None: (lambda r: r + pm.attention_backward(do, q, k, v, *r, cu, stream=st))(  # noqa: E731
+        pm.attention_forward(q, k, v, cu, stream=st))
+    both()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        results = both()
+    stream = torch.cuda.Stream()
+    for ends in ([0, 180, 300], [0, 100, 250], [7, 7, 40], [0, 0, 0], [0, 150, 300]):
+        cu.copy_(torch.tensor(ends, dtype=torch.int32))
+        for t in results:
+            t.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        held = [torch.zeros_like(t) for t in results]
+        pm.attention_forward(q, k, v, cu, out=held[0], lse=held[1])
+        pm.attention_backward(do, q, k, v, held[0], held[1], cu, dq=held[2], dk=held[3], dv=held[4])
+        torch.cuda.synchronize()
+        apart = both(stream)
+        torch.cuda.synchronize()
+        for got, other, want in zip(results, apart, held):
+            assert torch.equal(got, want) and torch.equal(other, want)
