@@ -574,7 +574,7 @@ typedef struct muonh_embedding_args {
   const void* tokens;       /* [count] int32 or int64, device                  */
   const void* table;        /* table_dtype                                     */
   void*       out;          /* [count x cols], out_dtype                       */
-  int64_t     count;        /* >= 0; times cols (rounded up to 256) below 2^32 */
+  int64_t     count;        /* 0 .. 2^24 - 1                                   */
   int64_t     rows;         /* 0 .. 2^30                                       */
   int64_t     cols;         /* 1 .. 2^20                                       */
   int64_t     ld_table, ld_out;
@@ -588,7 +588,7 @@ typedef struct muonh_embedding_grad_args {
   const void* tokens;
   const void* dout;         /* [count x cols], dout_dtype                      */
   void*       dtable;       /* [rows x cols], table_dtype; all of it is written */
-  int64_t     count, rows, cols;
+  int64_t     count, rows, cols;   /* as above                                 */
   int64_t     ld_dout, ld_table;
   int32_t     token_bytes;
   int32_t     dout_dtype;

@@ -20,8 +20,8 @@ int check_sizes(int64_t count, int64_t rows, int64_t cols) {
   int rc;
   if ((rc = check_size(count, 0, "count")) || (rc = check_size(rows, 0, "rows"))) return rc;
   if (cols < 1 || cols > kMaxCols) return fail(MUONH_EINVAL, "cols must be in [1, 2^20]");
-  // a launch's threads: at most one per token and column
-  if (count > kMaxThreads / (ceil_div(cols, 256) * 256)) return fail(MUONH_EINVAL, "count and cols are too large for one launch");
+  // of no launch are there more than 256 threads along x per token
+  if (count > kMaxThreads / 256) return fail(MUONH_EINVAL, "count is too large for one launch");
   return MUONH_OK;
 }
 

@@ -258,3 +258,25 @@ def test_python_refusals():
         pm.embedding_forward(t, w, out=w[:3])
     with pytest.raises(pm.MuonHError):
         pm.embedding_backward(t, w[:3], 5, dtable=w)
+
+
+def test_more_than_2_32_elements():
+    """2^20 + 1 tokens of 4096 columns; the gradients are small whole numbers, whose sums
+    are exact in any order."""
+    n, rows, cols = (1 << 20) + 1, 300, 4096
+    announce(f"embedding {n} of {rows}x{cols}")
+    t = _tokens(n, rows, "padding").cuda()
+    weight = torch.randn((rows, cols), generator=torch.Generator().manual_seed(5)).bfloat16().cuda()
+    known = (t >= 0) & (t < rows)
+    at = t.clamp(0, rows - 1)
+    out = pm.embedding_forward(t, weight)
+    for s in range(0, n, 1 << 17):
+        part = slice(s, s + (1 << 17))
+        assert torch.equal(out[part], torch.where(known[part, None], weight[at[part]], torch.zeros_like(weight[:1])))
+    out.random_(-2, 3)
+    got = pm.embedding_backward(t, out, rows)
+    for s in range(0, cols, 512):
+        d = torch.where(known[:, None], out[:, s:s + 512], torch.zeros_like(out[:1, :1])).float()
+        assert torch.equal(got[:, s:s + 512], torch.zeros((rows, 512), device="cuda").index_add_(0, at, d))
+    del out, d
+    torch.cuda.empty_cache()

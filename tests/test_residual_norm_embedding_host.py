@@ -154,3 +154,17 @@ def test_embedding_workspace_and_empty():
     assert _embed_grad(rows=0, **none) == mb.MUONH_OK
     _refused(lib.muonh_embedding_forward(None, None), mb.MUONH_EINVAL, "null")
     _refused(lib.muonh_embedding_backward(None, None), mb.MUONH_EINVAL, "null")
+
+
+def test_embedding_counts():
+    """The most tokens do not depend on the columns."""
+    lib = pm.load_library()
+    need = ctypes.c_size_t()
+    most = (1 << 24) - 1
+    for cols in (1, 64, 4096, 1 << 20):
+        assert lib.muonh_embedding_backward_workspace(most, 300, cols, ctypes.byref(need)) == mb.MUONH_OK
+        _refused(lib.muonh_embedding_backward_workspace(most + 1, 300, cols, ctypes.byref(need)), mb.MUONH_EINVAL, "count")
+        wide = dict(cols=cols, ld_table=cols, count=most)
+        # past the sizes, to the next check
+        _refused(_embed(**wide, ld_out=cols, tokens=None), mb.MUONH_EINVAL, "null")
+        _refused(_embed_grad(**wide, ld_dout=cols, tokens=None), mb.MUONH_EINVAL, "null")
