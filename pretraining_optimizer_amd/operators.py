@@ -593,7 +593,7 @@ def _attention(q, k, v, cu_seqlens, scale, out, lse, stream):
         raise ValueError(f"lse: a contiguous float32 tensor of shape {(heads, tokens)} is required")
     args = muonh_attention_args(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
                                 cu_seqlens.data_ptr(), tokens, ends - 1, ld_q, ld_k, ld_v, ld_out, heads,
-                                kv_heads, dim, dim ** -0.5 if scale is None else scale, zero)
+                                kv_heads, dim, max(dim, 1) ** -0.5 if scale is None else scale, zero)
     return args, out, lse, dev
 
 

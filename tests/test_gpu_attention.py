@@ -667,3 +667,11 @@ def test_a_captured_call_whose_sequences_change():
         torch.cuda.synchronize()
         for got, other, want in zip(results, apart, held):
             assert torch.equal(got, want) and torch.equal(other, want)
+
+
+def test_heads_without_columns_are_refused():
+    announce("attention heads of no columns")
+    none = torch.empty((40, 1, 0), dtype=torch.bfloat16, device="cuda")
+    cu = torch.tensor([0, 40], dtype=torch.int32, device="cuda")
+    with pytest.raises(pm.MuonHError, match="dim"):
+        pm.attention_forward(none, none, none, cu)
