@@ -675,3 +675,29 @@ def test_heads_without_columns_are_refused():
     cu = torch.tensor([0, 40], dtype=torch.int32, device="cuda")
     with pytest.raises(pm.MuonHError, match="dim"):
         pm.attention_forward(none, none, none, cu)
+
+
+@pytest.mark.parametrize("heads,dim", SPLITS[:4])
+def test_infinite_keys_by_the_sign_of_their_scores(heads, dim):
+    """A key with an infinity: a later row whose score it makes -inf has what the formula
+    gives without that key (NaN and lse -inf if it sees no other), one whose score it makes
+    +inf is NaN, and earlier rows stay within the tolerances."""
+    n = 150
+    q, k, v, do, cu = _inputs([n], heads, heads, dim)
+    assert (q != 0).all()
+    i, j = np.arange(n)[:, None], np.arange(n)[None]
+    for where in (0, 5, 31, 32, 40, 64, 100, 149):
+        for value in (float("inf"), -float("inf")):
+            announce(f"attention key {value} at {where}, {heads} heads of {dim}")
+            bad = k.clone()
+            bad[where, :, 3] = value
+            out, lse = pm.attention_forward(q, bad, v, cu)
+            O, L, Q, K, V = (_np(t) for t in (out, lse, q, k, v))
+            for h in {0, heads // 2, heads - 1}:
+                seen = (j <= i) & (j != where)
+                up = (np.arange(n) >= where) & (Q[:, h, 3] * value > 0)
+                some = seen.any(axis=1) & ~up
+                assert np.isnan(O[~some, h]).all() and np.isnan(L[h, up]).all() and (L[h, ~some & ~up] == -np.inf).all()
+                want, wl, tol, ltol = _seen_softmax(Q[:, h], K[:, h], V[:, h], dim ** -0.5, seen)
+                assert np.all(np.abs(O[some, h] - want[some]) <= tol[some]), (h, "out")
+                assert np.all(np.abs(L[h, some] - wl[some]) <= ltol[some]), (h, "lse")
