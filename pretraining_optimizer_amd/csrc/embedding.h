@@ -26,6 +26,9 @@ constexpr int kSortThreads = 1024;
 constexpr int kSortAlone = 16, kSortBeside = 4;             // per thread
 constexpr int64_t kSortBlock = kSortThreads * kSortBeside;
 constexpr int kSortDigits = 1024;                           // at most, of one pass
+// Of up to so many workgroups each finds by itself where its keys of a digit begin, more
+// have a launch for it.
+constexpr int64_t kOwnBegin = 32;
 
 // A token's key is its row, or `rows` if it has none.  Keys are sorted in passes of
 // equally many bits, at most 10.
@@ -40,7 +43,7 @@ inline SortPlan plan_sort(int64_t count, int64_t rows) {
   const bool alone = count <= kSortThreads * (passes > 1 ? kSortAlone : kSortAlone / 2);
   return SortPlan{passes, (bits + passes - 1) / passes, alone ? 1 : (count + kSortBlock - 1) / kSortBlock};
 }
-// Sorted tokens that one workgroup adds up.
+// Sorted tokens that one group of threads adds up.
 inline int64_t sum_run(int64_t count) { return count <= 65536 ? 16 : 64; }
 
 struct EmbeddingGradArgs {

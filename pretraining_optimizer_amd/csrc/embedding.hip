@@ -255,8 +255,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_begin_kernel(EmbeddingGradA
   }
 }
 
-// OWN: of few workgroups each finds by itself where its keys begin, from the counts.
-constexpr int64_t kOwnBegin = 32;
+// OWN: each workgroup finds by itself where its keys begin, from the counts.
 template <bool OWN>
 __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(EmbeddingGradArgs p, SortPlan plan, int pass, int from, int to) {
   __shared__ SortLds lds;

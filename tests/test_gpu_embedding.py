@@ -13,6 +13,7 @@ import torch
 import pretraining_optimizer_amd as pm
 from oracle import embedding
 from parity import announce
+from sort_plans import SORTS
 
 pytestmark = pytest.mark.gpu
 
@@ -279,4 +280,36 @@ def test_more_than_2_32_elements():
         d = torch.where(known[:, None], out[:, s:s + 512], torch.zeros_like(out[:1, :1])).float()
         assert torch.equal(got[:, s:s + 512], torch.zeros((rows, 512), device="cuda").index_add_(0, at, d))
     del out, d
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("n,rows", [(n, r) for n, r, _, _, path in SORTS if path != "ranked" and r < 1 << 30])
+def test_sorts_of_every_plan(n, rows):
+    """One, two and three passes over few and over more than 32 workgroups, skewed tokens
+    and padding; the sizes' plans are pinned on the host."""
+    for kind, cols in (("words", 2), ("padding", 3), ("one", 1)):
+        announce(f"embedding gradient {n} of {rows}x{cols} {kind}")
+        t = _tokens(n, rows, kind).cuda()
+        t[:5] = torch.tensor([rows - 1, 0, rows, -1, rows // 2])
+        d = torch.randn((n, cols), generator=torch.Generator().manual_seed(n)).cuda()
+        got = pm.embedding_backward(t, d, rows)
+        _check_backward(got, t, d, rows, 1.0, kind)
+        assert torch.equal(got, pm.embedding_backward(t, d, rows))
+
+
+@pytest.mark.parametrize("n,rows", [(n, r) for n, r, _, _, path in SORTS if r == 1 << 30])
+def test_four_passes(n, rows):
+    """The most rows: keys of 31 bits.  Small whole numbers, whose sums are exact."""
+    announce(f"embedding gradient {n} of {rows}x1")
+    gen = torch.Generator("cuda").manual_seed(n)
+    t = torch.randint(0, rows, (n,), device="cuda", generator=gen)
+    t[::5] = t[3::5][torch.randint(0, 50, (len(t[::5]),), device="cuda", generator=gen)]
+    t[:5] = torch.tensor([rows - 1, 0, rows, -1, 1 << 20])
+    d = torch.randint(1, 3, (n, 1), device="cuda", generator=gen).float()
+    got = pm.embedding_backward(t, d, rows)
+    known = (t >= 0) & (t < rows)
+    row, where = torch.unique(t[known], return_inverse=True)
+    want = torch.zeros(len(row), device="cuda").index_add_(0, where, d[known, 0])
+    assert torch.equal(got[row, 0], want) and int((got != 0).sum()) == len(row)
+    del got
     torch.cuda.empty_cache()
