@@ -472,13 +472,17 @@ int muonh_norm_backward(const muonh_norm_grad_args* args, void* stream);
  * softmax statistics and all sums are fp32; P and dS are rounded to bf16 where they
  * are multiplied, results once.  Sums run in a fixed order.
  *
- * Rows that no sequence holds, before the first and behind the last, are not read; in the
- * results that zero_rest names they become zeros, in others they stay as they were.  The device reads
- * cu_seqlens: ends are taken into [0, tokens] and a sequence that would end before
- * it starts is empty, but sequences that overlap give undefined results.  An
- * infinity or a NaN in a token of k or v reaches out and lse of later rows of its
- * sequence (and its own), of no earlier one; one in any operand of the backward pass may reach
- * every gradient of its sequence.  Other sequences' results do not change.
+ * The device reads cu_seqlens.  Its ends are taken into [0, tokens] and must not
+ * decrease (repeat the last one to pad it to a fixed length): ends that do give undefined
+ * results, but no access outside the tensors.  Rows that no sequence holds, before the
+ * first and behind the last, are not read; in the results that zero_rest names they
+ * become zeros, in others they stay as they were.
+ *
+ * A row all of whose scores are -inf has lse -inf and out NaN, one with a score of +inf NaN in
+ * both.  An infinity or a NaN in a token of k or v reaches out and lse of later rows of its
+ * sequence (and its own), of no earlier one; one in any operand of the backward pass (lse
+ * -inf is one) may reach every gradient of its sequence.  Other sequences' results do not
+ * change.
  * An output or workspace that overlaps an input or another output is refused, unless
  * they lie side by side in rows of one pitch.                                */
 #define MUONH_ZERO_OUT 1

@@ -17,8 +17,9 @@
 // for rows 16 s + 4 (l / 32) .. + 3 and 8 further.  So neither scores nor
 // probabilities pass through LDS.
 //
-// Rounding to bf16: P and dS where they become matrix operands (2^-9 of a term, random),
-// and the results, once.
+// Rounding to bf16: P and dS where they become matrix operands, which the matrix unit takes
+// in 16 bits at the rate that this work needs (at most 2^-8 of a term, of either sign), and the
+// results, once.
 //
 // Tiles of 64 rows go straight from memory to LDS, the next while one is used, a
 // barrier per tile.  Rows behind a sequence's end and columns behind the head's width
@@ -203,7 +204,8 @@ __device__ __forceinline__ void load_operand(u32x4_t (&f)[DP / 16], const Rows& 
 // rank; a lane per sequence evaluates it.  More than 64 sequences keep their order:
 // blocks are numbered from cu[b] / ROWS + b on, which leaves room for the last, cut one.
 //
-// Ends are taken into [0, tokens], so no cu_seqlens reads or writes outside the tensors.
+// Ends are taken into [0, tokens], so no cu_seqlens reads or writes outside the tensors; the
+// search among more than 64 needs them not to decrease.
 struct Place {
   int64_t start;   // the sequence's first row
   int len, row;    // its rows, and the workgroup's first (-1: none)

@@ -604,7 +604,8 @@ def attention_forward(q, k, v, cu_seqlens, scale: Optional[float] = None, out=No
                  (so a slice of a fused projection's output will do)
     k, v       : [tokens, kv_heads, dim]; heads is a multiple of kv_heads
     cu_seqlens : int32 [sequences + 1]; sequence b is tokens cu_seqlens[b] ..
-                 cu_seqlens[b + 1] - 1, each of which sees those up to itself
+                 cu_seqlens[b + 1] - 1, each of which sees those up to itself.  It must not
+                 decrease; repeat its last element to pad it
     scale      : of the scores, > 0; dim^-1/2 if None
     out, lse   : memory of the results; lse is float32 [heads, tokens], the log of
                  each row's sum of exponentials, which the backward pass reads
