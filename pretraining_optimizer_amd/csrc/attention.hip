@@ -47,9 +47,6 @@ constexpr int kTile = 64;                // rows of a tile in LDS
 constexpr int kBufferConfig = 0x00020000;
 constexpr int kBehind = (int)0x80000000;  // an offset behind every descriptor's range
 constexpr float kLog2e = 1.4426950408889634f;
-// Running maxima begin here and not at -inf: where all scores so far are -inf, so would the
-// maximum be, and -inf minus itself is a NaN where 2^x of the difference has to be 0.
-constexpr float kLowest = -3.4028235e38f;
 
 // Row r's 16-byte chunk c sits at c ^ swizzle(r).  A row is 256 (128) bytes; 16 (8)
 // rows of one chunk, as an operand read has them, and 8 rows of 4 chunks, as a
@@ -367,6 +364,109 @@ __device__ __forceinline__ bool has_special(u32x4_t v) {
   return any;
 }
 
+// Products of the probabilities of keys 16 h .. + 15 of the rows' own block where a value is
+// an infinity or a NaN: a later row's, times its probability 0, would be a NaN.  One key at a
+// time, and only the rows that see it keep the result.
+template <int COLS>
+__device__ __forceinline__ void add_key_by_key(f32x16_t (&acc)[COLS], const u32x4_t (&fv)[COLS], u32x4_t pr, int h, int lane) {
+#pragma unroll 1
+  for (int e = 0; e < 16; ++e) {
+    // key 16 h + e: half (e / 4) % 2 of the lanes, word and half word
+    const int word = (e >> 3) * 2 + ((e >> 1) & 1);
+    const uint32_t keep = ((e >> 2) & 1) != (lane >> 5) ? 0u : (e & 1) ? 0xffff0000u : 0xffffu;
+    u32x4_t mask;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) mask[w] = w == word ? keep : 0u;
+#pragma unroll
+    for (int dt = 0; dt < COLS; ++dt) {
+      const f32x16_t more = mfma(fv[dt] & mask, pr & mask, acc[dt]);
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[dt][r] = (lane & 31) >= 16 * h + e ? more[r] : acc[dt][r];
+    }
+  }
+}
+
+// The exponents of a row count from a rounded product, c times its largest score.  The
+// rounding is an error of them all alike, which falls out of the result while it is small:
+// at most 1 up to kFar, but 2^100 where the lowest number, as a mask, is the largest score.
+// So maxima begin at -kFar, which leaves out whatever lies far below (and -inf, which minus
+// itself would be a NaN), and rows whose largest score is not in between are computed again.
+constexpr float kFar = 16777216.0f, kLowest = -3.4028235e38f;
+__device__ __forceinline__ bool is_far(float top, float sum) {
+  return top > kFar || (top <= -kFar && sum == sum);   // a NaN is the row's result already
+}
+
+// The wavefront's 32 rows again, keys and values straight from memory: the largest score is
+// subtracted before the product with c, an instruction more per score, which would cost the
+// main loop 4 to 6%.  Only far rows keep the result.  2 x 4096 tokens, 16/8 heads of 128, all
+// rows far: 608 us; 1000 + 777 tokens, 12 heads of 64, the first 64 keys masked: 18.7 (16.3 without).
+template <int DP>
+__device__ __forceinline__ void far_rows(const AttentionArgs& p, const Rows& q, const Rows& k, const Rows& v, const Place& at,
+                                         int row, bool far, int head, int lane) {
+  constexpr int kCols = DP / 32;
+  if (!__any(far)) return;
+  const float c = p.scale * kLog2e;
+  u32x4_t fq[DP / 16], fk[DP / 16];
+  load_operand<DP>(fq, q, row, lane);
+  f32x16_t acc[kCols];
+#pragma unroll
+  for (int dt = 0; dt < kCols; ++dt) acc[dt] = splat(0.0f);
+  float top = kLowest, sum = 0.0f;
+#pragma unroll 1
+  for (int first = 0; first <= row; first += 32) {
+    load_operand<DP>(fk, k, first, lane);
+    f32x16_t s = splat(0.0f);
+#pragma unroll
+    for (int d = 0; d < DP / 16; ++d) s = mfma(fk[d], fq[d], s);
+    float m = top;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      if (first == row && block_row(r) + 4 * (lane >> 5) > (lane & 31)) s[r] = -INFINITY;
+      m = fmaxf(m, s[r]);
+    }
+    m = pair_max(m);
+    const float f = __builtin_amdgcn_exp2f((top - m) * c);
+    top = m;
+    sum *= f;
+#pragma unroll
+    for (int dt = 0; dt < kCols; ++dt)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[dt][r] *= f;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      s[r] = __builtin_amdgcn_exp2f((s[r] - top) * c);
+      sum += s[r];
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      // as TileRead::columns; rows behind the end and columns behind the width are never kept
+      u32x4_t fv[kCols];
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        const int key = min(first + 16 * h + 4 * (lane >> 5) + w % 4 + 8 * (w / 4), at.len - 1);
+#pragma unroll
+        for (int dt = 0; dt < kCols; ++dt) {
+          const uint32_t one = ld_global<uint16_t>(v.base + key * v.ld + min(32 * dt + (lane & 31), p.dim - 1));
+          fv[dt][w / 2] = w % 2 ? fv[dt][w / 2] | one << 16 : one;
+        }
+      }
+      const u32x4_t pr = operand(s, h);
+      if (first == row) {
+        add_key_by_key(acc, fv, pr, h, lane);
+      } else {
+#pragma unroll
+        for (int dt = 0; dt < kCols; ++dt) acc[dt] = mfma(fv[dt], pr, acc[dt]);
+      }
+    }
+  }
+  sum = pair_sum(sum);
+  if (!far) return;
+  const int64_t t = at.start + row;
+  store_rows<DP>(p.out + t * p.ldo + head * p.dim, p.ldo, p.dim, acc, 1.0f / sum, lane);
+  if (lane < 32)
+    p.lse[head * (int64_t)p.tokens + t + lane] = __builtin_fmaf(top, p.scale, __builtin_amdgcn_logf(sum) * (1.0f / kLog2e));
+}
+
 // Forward.  A wavefront holds 32 rows of q and their output transposed (a row per
 // lane), and passes over the keys once with a running maximum and sum.  The output is
 // rescaled only where a maximum has grown by more than 2^8 since the last time: until
@@ -421,7 +521,7 @@ __global__ __launch_bounds__(kThreads, PARTS == 4 ? 1 : 2) void attention_forwar
   f32x16_t acc[DP / 32];
 #pragma unroll
   for (int dt = 0; dt < DP / 32; ++dt) acc[dt] = splat(0.0f);
-  float top = kLowest, sum = 0.0f;   // both times c log2 e; the sum is of this lane's keys
+  float top = -kFar, sum = 0.0f;   // both times c log2 e; the sum is of this lane's keys
   const float c = p.scale * kLog2e;
 
   // N blocks of 32 keys; DIAG: the last is the rows' own.
@@ -476,23 +576,7 @@ __global__ __launch_bounds__(kThreads, PARTS == 4 ? 1 : 2) void attention_forwar
           if (DIAG && b == N - 1) special |= has_special(fv[dt]);
         }
         if (DIAG && b == N - 1 && __any(special)) {
-          // A later row's infinity or NaN times its probability 0 would be a NaN: one
-          // key at a time, and only the rows that see it keep the result.
-#pragma unroll 1
-          for (int e = 0; e < 16; ++e) {
-            // key 16 h + e: half (e / 4) % 2 of the lanes, word and half word
-            const int word = (e >> 3) * 2 + ((e >> 1) & 1);
-            const uint32_t keep = ((e >> 2) & 1) != (lane >> 5) ? 0u : (e & 1) ? 0xffff0000u : 0xffffu;
-            u32x4_t mask;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) mask[w] = w == word ? keep : 0u;
-#pragma unroll
-            for (int dt = 0; dt < DP / 32; ++dt) {
-              const f32x16_t more = mfma(fv[dt] & mask, pr & mask, acc[dt]);
-#pragma unroll
-              for (int r = 0; r < 16; ++r) acc[dt][r] = (lane & 31) >= 16 * h + e ? more[r] : acc[dt][r];
-            }
-          }
+          add_key_by_key(acc, fv, pr, h, lane);
         } else {
 #pragma unroll
           for (int dt = 0; dt < DP / 32; ++dt) acc[dt] = mfma(fv[dt], pr, acc[dt]);
@@ -543,20 +627,23 @@ __global__ __launch_bounds__(kThreads, PARTS == 4 ? 1 : 2) void attention_forwar
       factor[w] = __builtin_amdgcn_exp2f(stats[0][first + w][lane] - most);   // 0 of a wavefront without keys
       total += factor[w] * stats[1][first + w][lane];
     }
-    if (row + (lane & 31) >= at.len) return;
+    const bool live = row + (lane & 31) < at.len, far = live && is_far(most, total);
     const int64_t t = at.start + row;
-    for (int dt = part; dt < kCols; dt += PARTS) {   // the columns over the wavefronts
-      f32x16_t v = splat(0.0f);
+    if (live && !far) {
+      for (int dt = part; dt < kCols; dt += PARTS) {   // the columns over the wavefronts
+        f32x16_t v = splat(0.0f);
 #pragma unroll
-      for (int w = 0; w < PARTS; ++w) {
-        const f32x16_t o = take_sums(place(first + w), dt, lane);
+        for (int w = 0; w < PARTS; ++w) {
+          const f32x16_t o = take_sums(place(first + w), dt, lane);
 #pragma unroll
-        for (int r = 0; r < 16; ++r) v[r] += factor[w] * o[r];
+          for (int r = 0; r < 16; ++r) v[r] += factor[w] * o[r];
+        }
+        store_columns(p.out + t * p.ldo + head * p.dim, p.ldo, p.dim, dt, v, 1.0f / total, lane);
       }
-      store_columns(p.out + t * p.ldo + head * p.dim, p.ldo, p.dim, dt, v, 1.0f / total, lane);
+      if (part == 0 && lane < 32)
+        p.lse[head * (int64_t)p.tokens + t + lane] = (most + __builtin_amdgcn_logf(total)) * (1.0f / kLog2e);
     }
-    if (part == 0 && lane < 32)
-      p.lse[head * (int64_t)p.tokens + t + lane] = (most + __builtin_amdgcn_logf(total)) * (1.0f / kLog2e);
+    if (part == 0) far_rows<DP>(p, q, k, v, at, row, far, head, lane);
     return;
   }
   // The tiles before the workgroup's rows are seen whole by all of them.
@@ -599,10 +686,13 @@ __global__ __launch_bounds__(kThreads, PARTS == 4 ? 1 : 2) void attention_forwar
   }
 
   sum = pair_sum(sum);
-  if (row + (lane & 31) >= at.len) return;
+  const bool live = row + (lane & 31) < at.len, far = live && is_far(top, sum);
   const int64_t t = at.start + row;
-  store_rows<DP>(p.out + t * p.ldo + head * p.dim, p.ldo, p.dim, acc, 1.0f / sum, lane);
-  if (lane < 32) p.lse[head * (int64_t)p.tokens + t + lane] = (top + __builtin_amdgcn_logf(sum)) * (1.0f / kLog2e);
+  if (live && !far) {
+    store_rows<DP>(p.out + t * p.ldo + head * p.dim, p.ldo, p.dim, acc, 1.0f / sum, lane);
+    if (lane < 32) p.lse[head * (int64_t)p.tokens + t + lane] = (top + __builtin_amdgcn_logf(sum)) * (1.0f / kLog2e);
+  }
+  far_rows<DP>(p, q, k, v, at, row, far, head, lane);
 }
 
 // Gradient of q, row by row as in the forward pass: S and dP from k and v, dq from dS and k.

@@ -701,3 +701,60 @@ def test_infinite_keys_by_the_sign_of_their_scores(heads, dim):
                 want, wl, tol, ltol = _seen_softmax(Q[:, h], K[:, h], V[:, h], dim ** -0.5, seen)
                 assert np.all(np.abs(O[some, h] - want[some]) <= tol[some]), (h, "out")
                 assert np.all(np.abs(L[h, some] - wl[some]) <= ltol[some]), (h, "lse")
+
+
+@pytest.mark.parametrize("heads,dim", SPLITS)
+@pytest.mark.parametrize("scale", [0.5, 1.0])
+def test_keys_masked_by_the_least_value(scale, heads, dim):
+    """The first 70 keys have bf16's lowest value as their score, a finite number (with scale 1
+    not so in units of log2 e): rows that see another key have what the formula gives without
+    them."""
+    announce(f"attention lowest scores, scale {scale}, {heads} heads of {dim}")
+    n, masked = 200, 70
+    q, k, v, do, cu = _inputs([n], heads, heads, dim, spread=0.2)
+    q[:, :, -1] = 1.0
+    k[:, :, -1] = 0.0
+    clean = _np(k)
+    k[:masked, :, -1] = torch.finfo(torch.bfloat16).min
+    out, lse = pm.attention_forward(q, k, v, cu, scale=scale)
+    i, j = np.arange(n)[:, None], np.arange(n)[None]
+    seen = (j <= i) & (j >= masked)
+    O, L, Q, V = _np(out), _np(lse), _np(q), _np(v)
+    for h in {0, heads // 2, heads - 1}:
+        want, wl, tol, ltol = _seen_softmax(Q[:, h], clean[:, h], V[:, h], scale, seen)
+        assert np.all(np.abs(O[masked:, h] - want[masked:]) <= tol[masked:]), (h, "out")
+        assert np.all(np.abs(L[h, masked:] - wl[masked:]) <= ltol[masked:]), (h, "lse")
+
+
+@pytest.mark.parametrize("heads,dim", SPLITS)
+def test_rows_of_huge_scores(heads, dim):
+    """Rows whose scores are all equal and far below zero, as those that a mask leaves
+    nothing else, are the keys' mean; of scores that grow by 2^33 every 8 keys the last ones
+    count; other rows of the same wavefronts have what the formula gives."""
+    announce(f"attention huge scores, {heads} heads of {dim}")
+    n = 200
+    q, k, v, do, cu = _inputs([n], heads, heads, dim, spread=0.2)
+    q[:, :, -1] = k[:, :, -1] = 0.0
+    huge = torch.arange(n, device="cuda") % 3 == 1
+    Q, plain, V = _np(q), _np(k), _np(v)
+    for value in (torch.finfo(torch.bfloat16).min, -2.0 ** 30, 2.0 ** 30):
+        bad = k.clone()
+        bad[:, :, -1] = value
+        if value > 0:
+            bad[:, :, -1] *= 1 + torch.arange(n, device="cuda")[:, None] // 8 * 8   # whole in 8 bits
+        mixed = q.clone()
+        mixed[huge] = 0.0
+        mixed[huge, :, -1] = 1.0
+        out, lse = pm.attention_forward(mixed, bad, v, cu, scale=1.0)
+        O, L, K = _np(out), _np(lse), _np(bad)[:, 0, -1]
+        rest = ~_np(huge.float()).astype(bool)
+        for h in {0, heads // 2, heads - 1}:
+            want, wl, tol, ltol = _seen_softmax(Q[:, h], plain[:, h], V[:, h], 1.0, np.tril(np.ones((n, n), dtype=bool)))
+            assert np.all(np.abs(O[rest, h] - want[rest]) <= tol[rest]), (value, h, "out")
+            assert np.all(np.abs(L[h, rest] - wl[rest]) <= ltol[rest]), (value, h, "lse")
+        for i in np.flatnonzero(_np(huge.float())):
+            top = K[:i + 1] == K[:i + 1].max()
+            mean, size = V[:i + 1][top].mean(axis=0), np.abs(V[:i + 1][top]).mean(axis=0)
+            tol = size * 2 * n * U
+            assert np.all(np.abs(O[i] - mean) <= tol + B * (np.abs(mean) + tol)), (value, i)
+            assert np.all(np.abs(L[:, i] - (K[i] + np.log(top.sum()))) <= 2 * U * abs(K[i]) + 8 * U), (value, i)
