@@ -479,10 +479,11 @@ int muonh_norm_backward(const muonh_norm_grad_args* args, void* stream);
  * become zeros, in others they stay as they were.
  *
  * A row all of whose scores are -inf has lse -inf and out NaN, one with a score of +inf NaN in
- * both.  An infinity or a NaN in a token of k or v reaches out and lse of later rows of its
- * sequence (and its own), of no earlier one; one in any operand of the backward pass (lse
- * -inf is one) may reach every gradient of its sequence.  Other sequences' results do not
- * change.
+ * both.  A row whose lse is infinite or beyond 2^24 log 2 in magnitude, where fp32 does not
+ * hold it to a unit, adds nothing to the gradients, and its dq is 0.  An infinity or a NaN in
+ * a token of k or v reaches out and lse of later rows of its sequence (and its own), of no
+ * earlier one; one in any operand of the backward pass but those rows' out and lse may
+ * reach every gradient of its sequence.  Other sequences' results do not change.
  * An output or workspace that overlaps an input or another output is refused, unless
  * they lie side by side in rows of one pitch.                                */
 #define MUONH_ZERO_OUT 1

@@ -732,10 +732,15 @@ __global__ __launch_bounds__(kThreads, PARTS == 4 ? 1 : 2) void attention_dq_ker
   const int64_t t = head * (int64_t)p.tokens + at.start + row + (lane & 31);
   const bool live = row + (lane & 31) < at.len;
   float delta = 0.0f, lse = 0.0f;
+  bool none = false;
   {
     u32x4_t fo[DP / 16];
     load_operand<DP>(fo, o, row, lane);
     if (live) lse = -p.lse[t] * kLog2e;
+    // fp32 does not hold a far lse to a unit, so it says nothing of the row's probabilities,
+    // and -inf is that of no key at all: both are taken as none
+    none = fabsf(lse) > kFar;
+    if (none) lse = -INFINITY;
 #pragma unroll
     for (int s = 0; s < DP / 16; ++s)
 #pragma unroll
@@ -743,7 +748,7 @@ __global__ __launch_bounds__(kThreads, PARTS == 4 ? 1 : 2) void attention_dq_ker
         delta = __builtin_fmaf(__uint_as_float(fo[s][w] << 16), __uint_as_float(fd[s][w] << 16), delta);
         delta = __builtin_fmaf(__uint_as_float(fo[s][w] & 0xffff0000u), __uint_as_float(fd[s][w] & 0xffff0000u), delta);
       }
-    delta = -pair_sum(delta);
+    delta = none ? 0.0f : -pair_sum(delta);
     if (live && lane < 32 && part == 0) {
       g.row_lse[t] = lse;
       g.row_delta[t] = delta;

@@ -758,3 +758,41 @@ def test_rows_of_huge_scores(heads, dim):
             tol = size * 2 * n * U
             assert np.all(np.abs(O[i] - mean) <= tol + B * (np.abs(mean) + tol)), (value, i)
             assert np.all(np.abs(L[:, i] - (K[i] + np.log(top.sum()))) <= 2 * U * abs(K[i]) + 8 * U), (value, i)
+
+
+@pytest.mark.parametrize("heads,dim", SPLITS)
+@pytest.mark.parametrize("flag", [1.0, 8.0])
+def test_gradients_of_rows_that_a_mask_leaves_nothing(flag, heads, dim):
+    """Rows whose keys are all masked by the lowest number (scores finite, or -inf where q
+    has 8) add nothing to the gradients and have none; the others have what the formula
+    gives without the masked keys."""
+    announce(f"attention gradients of masked rows, {flag}, {heads} heads of {dim}")
+    n, masked = 300, 70
+    q, k, v, do, cu = _inputs([n], heads, heads, dim, spread=0.2)
+    q[:, :, -1] = flag
+    k[:, :, -1] = 0.0
+    clean = _np(k)
+    k[:masked, :, -1] = torch.finfo(torch.bfloat16).min
+    out, lse = pm.attention_forward(q, k, v, cu, scale=1.0)
+    dq, dk, dv = (_np(t) for t in pm.attention_backward(do, q, k, v, out, lse, cu, scale=1.0))
+    for t in (dq, dk, dv):
+        assert (t[:masked] == 0).all()
+    seen = np.tril(np.ones((n - masked, n - masked), dtype=bool))
+    Q, V, DO, O, L = (_np(t)[masked:] if t.dim() == 3 else _np(t)[:, masked:] for t in (q, v, do, out, lse))
+    K, m = clean[masked:], n - masked
+    for h in {0, heads // 2, heads - 1}:
+        a, b, vh, d = Q[:, h], K[:, h], V[:, h], DO[:, h]
+        S = a @ b.T
+        P = np.where(seen, np.exp(np.where(seen, S, 0.0) - L[h][:, None]), 0.0)
+        ep = dim * U * (np.abs(a) @ np.abs(b).T) + 8 * U * (np.abs(S) + np.abs(L[h])[:, None] + 1)
+        size = np.abs(d * O[:, h]).sum(axis=1, keepdims=True)
+        delta = (d * O[:, h]).sum(axis=1, keepdims=True)
+        dP = d @ vh.T
+        ds = P * (dP - delta)
+        eds = np.abs(ds) * (B + 2 * ep) + P * (dim * U * (np.abs(d) @ np.abs(vh).T + size) + 2 * U * np.abs(dP - delta))
+        for name, got, want, tol in (
+                ("dq", dq[masked:, h], ds @ b, eds @ np.abs(b) + 2 * m * U * (np.abs(ds) @ np.abs(b))),
+                ("dk", dk[masked:, h], ds.T @ a, eds.T @ np.abs(a) + 2 * m * U * (np.abs(ds).T @ np.abs(a))),
+                ("dv", dv[masked:, h], P.T @ d, (P * (B + 2 * ep + 2 * m * U)).T @ np.abs(d))):
+            tol = tol + B * (np.abs(want) + tol)
+            assert np.all(np.abs(got - want) <= tol), (name, h, float((np.abs(got - want) - tol).max()))
