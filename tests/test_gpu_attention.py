@@ -16,11 +16,14 @@ b = 2^-8: half a step of bf16).  With n rows seen and D columns:
 In the backward pass out and lse are inputs, the same for both sides.
 """
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
 
 import pretraining_optimizer_amd as pm
+from pretraining_optimizer_amd import muonh as mb
 from oracle import attention
 from parity import announce
 
@@ -796,3 +799,54 @@ def test_gradients_of_rows_that_a_mask_leaves_nothing(flag, heads, dim):
                 ("dv", dv[masked:, h], P.T @ d, (P * (B + 2 * ep + 2 * m * U)).T @ np.abs(d))):
             tol = tol + B * (np.abs(want) + tol)
             assert np.all(np.abs(got - want) <= tol), (name, h, float((np.abs(got - want) - tol).max()))
+
+
+@pytest.mark.parametrize("heads,kv,dim", [(4, 2, 40), (4, 1, 104), (64, 32, 40), (120, 60, 104)])
+def test_huge_scores_in_groups_of_heads(heads, kv, dim):
+    """Two sequences and padding, heads that share keys, widths between the tiles': rows of
+    equal scores far below zero are the mean of their own sequence's values up to them, also
+    where a later value is NaN."""
+    announce(f"attention huge scores, {heads}/{kv} heads of {dim}")
+    lens, tail = [150, 71], 9
+    q, k, v, do, cu = _inputs(lens, heads, kv, dim, tail=tail)
+    q[:], k[:] = 0.0, 0.0
+    q[:, :, 0], k[:, :, 0] = 1.0, -2.0 ** 100
+    v[140] = float("nan")
+    out, lse = pm.attention_forward(q, k, v, cu, scale=1.0)
+    O, L, V = _np(out), _np(lse), _np(v)
+    assert np.isnan(O[140:150]).all() and (L[:, :221] == -2.0 ** 100).all() and (L[:, 221:] == 0).all()
+    for start, rows in ((0, 140), (150, 71)):
+        part = np.repeat(V[start:start + rows], heads // kv, axis=1)
+        n = np.arange(1, rows + 1)[:, None, None]
+        mean, size = part.cumsum(axis=0) / n, np.abs(part).cumsum(axis=0) / n
+        tol = 2 * n * U * size
+        assert np.all(np.abs(O[start:start + rows] - mean) <= tol + B * (np.abs(mean) + tol))
+
+
+def test_zeros_into_slices_from_c():
+    """The C entry points' zero_rest: each bit clears its own result's rows, within the
+    heads' columns of a fused buffer."""
+    announce("attention zero_rest into slices")
+    lib, byref = pm.load_library(), ctypes.byref
+    heads, kv, dim, lens, tail = 4, 2, 72, [33, 140], 50
+    q, k, v, do, cu = _inputs(lens, heads, kv, dim, tail=tail)
+    n, live = len(q), sum(lens)
+    want, wl = pm.attention_forward(q, k, v, cu)
+    wants = (want, wl.T) + pm.attention_backward(do, q, k, v, want, wl, cu)
+    stream = torch.cuda.current_stream().cuda_stream
+    for bits in range(32):
+        wide = torch.full((n, (2 * heads + 2 * kv) * dim + 8), 7.0, dtype=torch.bfloat16, device="cuda")
+        parts = [t.unflatten(1, (-1, dim)) for t in wide[:, :-8].split([heads * dim, heads * dim, kv * dim, kv * dim], 1)]
+        lse = torch.full((heads, n), 7.0, device="cuda")
+        ld = wide.stride(0)
+        args = mb.muonh_attention_args(q.data_ptr(), k.data_ptr(), v.data_ptr(), parts[0].data_ptr(), lse.data_ptr(), cu.data_ptr(), n,
+                                       2, heads * dim, kv * dim, kv * dim, ld, heads, kv, dim, dim ** -0.5, bits)
+        assert lib.muonh_attention_forward(byref(args), stream) == 0
+        ws = torch.empty(2 * heads * n + 128, device="cuda")
+        grad = mb.muonh_attention_grad_args(args, do.data_ptr(), *(t.data_ptr() for t in parts[1:]), heads * dim, ld, ld, ld,
+                                            ws.data_ptr(), ws.numel() * 4)
+        assert lib.muonh_attention_backward(byref(grad), stream) == 0
+        for i, (got, clean) in enumerate(zip((parts[0], lse.T, *parts[1:]), wants)):
+            assert torch.equal(got[:live], clean[:live])
+            assert (got[live:] == (0 if bits >> i & 1 else 7)).all(), (bits, i)
+        assert (wide[:, -8:] == 7).all()
