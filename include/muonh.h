@@ -531,7 +531,7 @@ int muonh_attention_backward(const muonh_attention_grad_args* args, void* stream
 /* ---- residual addition, RMS norm and FP8 output ------------------------------
  * What stands between two linear layers of a block:
  *   h = x + residual, rounded to x's type        (residual NULL: h is x)
- *   rstd = 1/sqrt(mean(h^2) + eps),  y = h rstd weight
+ *   rstd = 1/sqrt(mean(h^2) + eps),  y = h rstd weight   (rstd as muonh_norm_forward has it)
  * and y in block-scaled FP8 (blocks of 1 x 128, as muonh_block_quantize gives them): q,
  * its row form, and / or qt, its column form; either may be NULL.  y itself is
  * not stored: it is formed in fp32 from the h that is kept and rounded once, to

@@ -199,7 +199,9 @@ __device__ __forceinline__ void load_operand(u32x4_t (&f)[DP / 16], const Rows& 
 // 8192 tokens, with item_of's order: 349 -> 294 us).  With n_b blocks in sequence b, count(h) = sum_b
 // max(0, n_b - h + 1) blocks see h or more, so the rank's h is the largest with count(h) >
 // rank; a lane per sequence evaluates it.  More than 64 sequences keep their order:
-// blocks are numbered from cu[b] / ROWS + b on, which leaves room for the last, cut one.
+// blocks are numbered from cu[b] / ROWS + b on, which leaves room for the last, cut one
+// (gradients of 8192 tokens in 64 random documents 111 us, in 65 of them 126; the documents above
+// 265, with 57 empty sequences more 328).
 //
 // Ends are taken into [0, tokens], so no cu_seqlens reads or writes outside the tensors; the
 // search among more than 64 needs them not to decrease.
@@ -474,9 +476,9 @@ __device__ __forceinline__ void far_rows(const AttentionArgs& p, const Rows& q, 
 //
 // A workgroup's tiles before its own rows are seen whole, in a loop without branches.
 // Heads up to 64 columns leave room for tiles of 128 keys, whose products cover more of the
-// next one's latency: 1000 + 777 tokens, 12 heads of 64, 17.8 -> 15.7 us (the gradients do
-// not gain by it: dq 19.7, key gradients 17.9 -> 19.5).
-// 2 x 4096 tokens, 16/8 heads of 128: 146 to 175 us as the card's clock allows (940 to 785
+// next one's latency: 1000 + 777 tokens, 12 heads of 64, 17.8 -> 15.7 us in one part (the
+// gradients do not gain by it: dq 19.7, key gradients 17.9 -> 19.5).
+// 2 x 4096 tokens, 16/8 heads of 128: 147 to 177 us as the card's clock allows (935 to 775
 // TFLOP/s; a large library product 1209).  Matrix unit and exponentials bind alike: a tile's
 // 32 products take 1030 cycles of a SIMD, its exponentials, maxima and packing about
 // 900 issue cycles of each of its two wavefronts, which overlap them only in part.  Without
@@ -697,8 +699,8 @@ __global__ __launch_bounds__(kThreads, PARTS == 4 ? 1 : 2) void attention_forwar
 
 // Gradient of q, row by row as in the forward pass: S and dP from k and v, dq from dS and k.
 // It also leaves what the other kernel needs of each row: -lse log2 e and -delta.
-// Packed documents of 8192 tokens, 16/8 heads of 128: 115 us, three products of five (870
-// TFLOP/s); 1000 + 777 tokens, 12 heads of 64: 16 us in two parts, 19 in one, bound by the longest
+// Packed documents of 8192 tokens, 16/8 heads of 128: 117 us, three products of five (855
+// TFLOP/s); 1000 + 777 tokens, 12 heads of 64: 17 us in two parts, 19 in one, bound by the longest
 // workgroup's chain of tiles.
 template <int DP, int PARTS>
 __global__ __launch_bounds__(kThreads, PARTS == 4 ? 1 : 2) void attention_dq_kernel(AttentionGradArgs g) {
@@ -1060,17 +1062,28 @@ __global__ __launch_bounds__(kKeyThreads, 2) void attention_dkv_kernel(Attention
 }  // namespace
 
 // Whether the kernels are to have smaller blocks, by n, the blocks of 128 rows x heads.
-// Measured, in us of the forward pass / of the gradients:
+// Measured, in us of the forward pass / of the gradients (a call is 10 us at least):
 //                                                  n    4 parts        2 parts        1 part
-//   1000 tokens, 8 heads of 128                    64   17.6 / 42.7                   23.0 / 51.9
-//   4000 tokens, 4 heads of 128                   128   71.2 / 134     79.7 / 153     69.1 / 158
-//   8000 tokens, 2 heads of 64                    126   60.8 / 191     67.7 / 207     82.6 / 242
-//   4 x 300 tokens, 8 heads of 128                104   14.5 / 32.8    12.2 / 29.5    11.8 / 28.7
-//   6 x 500 tokens, 4 heads of 64                 116   11.8 / 21.0     8.7 / 20.8     9.3 / 23.0
-//   1000 + 777 tokens, 12 heads of 64             180                  14.8 / 34.5    15.5 / 37.3
-//   1000 + 777 tokens, 16 heads of 128            240                  31.0 / 72.1    25.4 / 68.1
+//   8000 tokens, 1 head of 128                     63   92.4 / 215                   130 / 291
+//   2000 tokens, 6 heads of 128                    96   29.3 / 70.5                  38.7 / 87.7
+//   4 x 300 tokens, 8 heads of 128                104   15.5 / 32.6                  12.1 / 28.9
+//   1100 tokens, 12 heads of 128                  108   24.0 / 52.3                  25.1 / 56.4
+//   1100 tokens, 12 heads of 64                   108   15.2 / 29.1    14.0 / 30.9   14.9 / 35.1
+//   6 x 500 tokens, 4 heads of 64                 116   12.2 / 21.5    10.7 / 21.2   10.6 / 23.6
+//   8000 tokens, 2 heads of 64                    126   61.1 / 125     72.4 / 141    80.5 / 175
+//   4000 tokens, 4 heads of 128                   128   57.4 / 128                   69.9 / 157
+//   4000 tokens, 4 heads of 64                    128   35.1 / 70.0    38.8 / 77.2   42.9 / 94.3
+//   2000 tokens, 10 heads of 64                   160   29.7 / 44.3    22.3 / 47.4   23.8 / 54.2
+//   500 tokens, 40 heads of 64                    160   16.8 / 29.6    10.8 / 25.7   10.7 / 26.8
+//   1000 + 777 tokens, 12 heads of 64             180   22.7 / 35.9    14.7 / 33.5   15.0 / 36.2
+//   1500 tokens, 16 heads of 64                   192   28.3 / 42.4    18.3 / 40.3   18.9 / 44.5
+//   4 x 300 tokens, 16 heads of 64                208   16.4 / 26.5    10.8 / 22.7   10.9 / 22.0
+//   700 + 50 + 900 tokens, 14 heads of 40         210   22.1 / 33.8    13.9 / 31.7   14.5 / 34.2
+//   6 x 500 tokens, 8 heads of 64                 232   19.7 / 32.1    10.8 / 27.3   11.3 / 27.9
 // Four parts up to a quarter of a workgroup of 128 rows per CU, long sequences up to half of
 // one; two up to one of heads up to 64 columns, whose tiles of 128 keys fit a CU twice.
+// n counts the entries of cu_seqlens, of empty sequences as well (the host does not see their
+// lengths): 1000 tokens, 8 heads of 128, with 64 entries 24.0 / 65.0, with one 17.9 / 42.5.
 //   Keys, gradients, smaller and large blocks: 1000 tokens, 8 heads of 128 (64) 42.7 and 63.7;
 //   4000 tokens, 4 heads (128) 134 and 200; 1777 tokens, 12 heads of 64 (180) 38.6 and 43.2.  Worth
 //   it while the large ones are less than one per CU.
